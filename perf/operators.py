@@ -188,7 +188,7 @@ def prepare(case, seed):
         st["w"] = 0.5 + torch.rand(n, device="cuda", generator=g)
         st["w"][torch.rand(n, device="cuda", generator=g) < 0.03] = 0.0  # positions left out of the loss
         st["loss"] = torch.empty(n, dtype=torch.float32, device="cuda")
-        st["stats"] = torch.empty((n, 2), dtype=torch.float32, device="cuda")
+        st["stats"] = torch.empty((n, 4), dtype=torch.float32, device="cuda")
         st["dz"] = None if case["mode"] == "loss" else torch.empty((n, V), dtype=z.dtype, device="cuda")
     return st
 
