@@ -21,7 +21,7 @@ DFLASH_OK = 0
 STATUS_NAMES = {0: "ok", -1: "EINVAL", -2: "EUNSUPPORTED", -3: "ECUDA", -4: "ECAPACITY", -5: "EWORKSPACE"}
 DTYPE_F32, DTYPE_F16, DTYPE_BF16 = 0, 1, 2
 LAYOUT_PLAIN, LAYOUT_GATEUP = 0, 1
-DEV_KV_CAPACITY, DEV_BAD_TOKEN, DEV_BAD_LENGTH, DEV_WAIT_TIMEOUT = 0x1, 0x2, 0x4, 0x100
+DEV_KV_CAPACITY, DEV_BAD_TOKEN, DEV_BAD_LENGTH, DEV_BAD_PARAM, DEV_WAIT_TIMEOUT = 0x1, 0x2, 0x4, 0x8, 0x100
 
 EXPORTS = [
     "dflash_version", "dflash_status_string", "dflash_workspace_size", "dflash_pack_w8a16",
@@ -29,7 +29,9 @@ EXPORTS = [
     "dflash_w8a16_linear_workspace_size", "dflash_w8a16_linear", "dflash_draft_block",
     "dflash_lmhead_workspace_size", "dflash_lmhead_argmax", "dflash_verify_workspace_size",
     "dflash_verify_accept", "dflash_verify_accept_noalloc", "dflash_verify_sample_workspace_size",
-    "dflash_verify_accept_sample", "dflash_kv_commit", "dflash_commit_draft_block", "dflash_set_launch_mode",
+    "dflash_verify_accept_sample", "dflash_sample", "dflash_verify_filtered_workspace_size",
+    "dflash_verify_accept_filtered", "dflash_top_logits", "dflash_distill_loss", "dflash_distill_backward",
+    "dflash_kv_commit", "dflash_commit_draft_block", "dflash_set_launch_mode",
     "dflash_get_launch_mode", "dflash_get_status",
 ]
 LAUNCH_STREAM_ORDER, LAUNCH_EARLY = 0, 1
@@ -98,6 +100,13 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "dflash_verify_sample_workspace_size": ([I32, I32, I64, PSZ], I32),
         "dflash_verify_accept_sample": ([P, P, I32, I32, I32, I64, ctypes.c_float, P, P, P, P, P, P, P, SZ, P],
                                         I32),
+        "dflash_sample": ([P, I32, I64, I64, I64, P, P, P, P, P, I64, P, P, P], I32),
+        "dflash_verify_filtered_workspace_size": ([I32, I32, I64, PSZ], I32),
+        "dflash_verify_accept_filtered": ([P, I32, I64, P, I32, I32, I32, I64, P, P, P, P, P, P, I64, P, P, P, P, P,
+                                           SZ, P], I32),
+        "dflash_top_logits": ([P, I32, I64, I64, I64, I32, ctypes.c_float, P, P, P, P], I32),
+        "dflash_distill_loss": ([P, I32, I64, I64, I64, P, P, I32, P, ctypes.c_float, P, P, P, P, I64, P], I32),
+        "dflash_distill_backward": ([P, I32, I64, I64, I64, P, P, I32, P, ctypes.c_float, P, P, P, I64, P], I32),
         "dflash_kv_commit": ([ctypes.POINTER(Weights), ctypes.POINTER(KV), P, I32, P, P, SZ, P], I32),
         "dflash_commit_draft_block": ([ctypes.POINTER(Weights), ctypes.POINTER(KV), P, I32, P, P, P, P, P, P, SZ, P],
                                       I32),
@@ -291,6 +300,185 @@ def dflash_verify_accept_noalloc(logits, draft, n_out, corr_out, emitted=None, n
     _check("dflash_verify_accept_noalloc", load_library().dflash_verify_accept_noalloc(
         logits.data_ptr(), draft.data_ptr(), b, R, D, V, n_out.data_ptr(), corr_out.data_ptr(), _ptr(emitted),
         _ptr(next_tok), _stream(stream)))
+
+
+# ---------------------------------------------- rows of vocabulary logits ----
+def _row_shape(fn, t, dim):
+    """Row stride of a logits-like tensor whose last dimension is contiguous
+    and whose leading dimensions (if two) form one sequence of rows."""
+    V = t.shape[-1]
+    if t.dim() != dim or t.numel() == 0 or (t.stride(-1) != 1 and V > 1):
+        raise ValueError(f"{fn}: expected a non-empty {dim}-D tensor with contiguous rows, got {tuple(t.shape)}")
+    rows = t.numel() // V
+    if rows == 1:
+        return V
+    if dim == 2:
+        return t.stride(0)
+    b, R, _ = t.shape
+    ld = t.stride(1) if R > 1 else t.stride(0)
+    if b > 1 and t.stride(0) != R * ld:
+        raise ValueError(f"{fn}: the rows of a 3-D tensor must be evenly spaced")
+    return ld
+
+
+def _row_dtype(fn, t):
+    torch = _torch()
+    dt = {torch.float32: DTYPE_F32, torch.float16: DTYPE_F16, torch.bfloat16: DTYPE_BF16}.get(t.dtype)
+    if dt is None or not t.is_cuda:
+        raise ValueError(f"{fn}: logits must be a CUDA tensor of float32, float16 or bfloat16")
+    return dt
+
+
+def _need(fn, dev, dtype, shape, **tensors):
+    """Each given tensor (None: absent) is contiguous, on `dev`, and of this
+    dtype and shape."""
+    for name, t in tensors.items():
+        if t is not None and (t.dtype != dtype or t.device != dev or tuple(t.shape) != tuple(shape)
+                              or not t.is_contiguous()):
+            raise ValueError(f"{fn}: {name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {dev}")
+
+
+def _on(dev, stream, fn, call):
+    """Runs `call(stream handle)` with the tensors' device current, on the
+    given stream or that device's current one."""
+    torch = _torch()
+    if dev.index == torch.cuda.current_device():
+        _check(fn, call(_stream(stream)))
+    else:
+        with torch.cuda.device(dev):
+            _check(fn, call(_stream(stream)))
+
+
+def dflash_sample(logits, temperature, u, tok_out, top_k=None, top_p=None, min_p=None, logprob_out=None, stream=None):
+    """One token per row of logits [rows][V] (fp32/fp16/bf16, contiguous rows),
+    drawn from softmax(z / T) under the row's top-k, top-p and min-p filters.
+    temperature, top_p, min_p fp32 [rows] and top_k int32 [rows] (filters may be
+    None); u fp32 uniforms [rows][V]; tok_out int32 [rows]; logprob_out fp32
+    [rows] (may be None).  T = 0 takes the largest logit."""
+    fn = "dflash_sample"
+    dt = _row_dtype(fn, logits)
+    ld = _row_shape(fn, logits, 2)
+    torch, dev, (n, V) = _torch(), logits.device, logits.shape
+    _need(fn, dev, torch.float32, (n,), temperature=temperature, top_p=top_p, min_p=min_p, logprob_out=logprob_out)
+    _need(fn, dev, torch.int32, (n,), top_k=top_k, tok_out=tok_out)
+    if u.dtype != torch.float32 or u.device != dev or tuple(u.shape) != (n, V):
+        raise ValueError(f"{fn}: u must be float32 [{n}][{V}] on {dev}")
+    lib = load_library()
+    _on(dev, stream, fn, lambda st: lib.dflash_sample(
+        logits.data_ptr(), dt, n, V, ld, temperature.data_ptr(), _ptr(top_k), _ptr(top_p), _ptr(min_p), u.data_ptr(),
+        _row_shape(fn, u, 2), tok_out.data_ptr(), _ptr(logprob_out), st))
+
+
+def dflash_verify_filtered_workspace_size(b: int, R: int, V: int) -> int:
+    n = ctypes.c_size_t(0)
+    _check("dflash_verify_filtered_workspace_size",
+           load_library().dflash_verify_filtered_workspace_size(b, R, V, ctypes.byref(n)))
+    return n.value
+
+
+def dflash_verify_accept_filtered(logits, draft, temperature, u_accept, u_sample, n_out, corr_out, top_k=None,
+                                  top_p=None, min_p=None, emitted=None, next_tok=None, ws=None, stream=None):
+    """Speculative accept under per-sequence filters.  logits [b][R][V]
+    (fp32/fp16/bf16), draft int32 [b][D] (-1: no draft), temperature, top_p,
+    min_p fp32 [b], top_k int32 [b], u_accept fp32 [b][D], u_sample fp32
+    [b][V]; n_out, corr_out, next_tok int32 [b], emitted int32 [b][R].  ws:
+    uint8 workspace of dflash_verify_filtered_workspace_size bytes (allocated
+    here when not given)."""
+    fn = "dflash_verify_accept_filtered"
+    dt = _row_dtype(fn, logits)
+    ld = _row_shape(fn, logits, 3)
+    torch, dev, (b, R, V) = _torch(), logits.device, logits.shape
+    D = draft.shape[-1]
+    _need(fn, dev, torch.int32, (b, D), draft=draft)
+    _need(fn, dev, torch.float32, (b, D), u_accept=u_accept)
+    _need(fn, dev, torch.float32, (b,), temperature=temperature, top_p=top_p, min_p=min_p)
+    _need(fn, dev, torch.int32, (b,), top_k=top_k, n_out=n_out, corr_out=corr_out, next_tok=next_tok)
+    _need(fn, dev, torch.int32, (b, R), emitted=emitted)
+    if u_sample.dtype != torch.float32 or u_sample.device != dev or tuple(u_sample.shape) != (b, V):
+        raise ValueError(f"{fn}: u_sample must be float32 [{b}][{V}] on {dev}")
+    if ws is None:
+        with torch.cuda.stream(stream):  # memory that the call's own stream may reuse (None: the current one)
+            ws = torch.empty(dflash_verify_filtered_workspace_size(b, R, V), dtype=torch.uint8, device=dev)
+    elif ws.device != dev or not ws.is_contiguous():
+        raise ValueError(f"{fn}: ws must be contiguous and on {dev}")
+    lib = load_library()
+    _on(dev, stream, fn, lambda st: lib.dflash_verify_accept_filtered(
+        logits.data_ptr(), dt, ld, draft.data_ptr(), b, R, D, V, temperature.data_ptr(), _ptr(top_k), _ptr(top_p),
+        _ptr(min_p), u_accept.data_ptr(), u_sample.data_ptr(), _row_shape(fn, u_sample, 2), n_out.data_ptr(),
+        corr_out.data_ptr(), _ptr(emitted), _ptr(next_tok), ws.data_ptr(), ws.numel() * ws.element_size(), st))
+
+
+def dflash_top_logits(logits, K: int, val_out, idx_out, lse_out=None, temperature: float = 1.0, stream=None):
+    """The K largest logits of each row [rows][V], falling, lowest index first
+    on ties: val_out fp32 [rows][K], idx_out int32 [rows][K]; lse_out fp32
+    [rows] (may be None) = log sum exp(z / temperature) over the row."""
+    fn = "dflash_top_logits"
+    dt = _row_dtype(fn, logits)
+    ld = _row_shape(fn, logits, 2)
+    torch, dev, (n, V) = _torch(), logits.device, logits.shape
+    _need(fn, dev, torch.float32, (n, K), val_out=val_out)
+    _need(fn, dev, torch.int32, (n, K), idx_out=idx_out)
+    _need(fn, dev, torch.float32, (n,), lse_out=lse_out)
+    lib = load_library()
+    _on(dev, stream, fn, lambda st: lib.dflash_top_logits(
+        logits.data_ptr(), dt, n, V, ld, K, float(temperature), val_out.data_ptr(), idx_out.data_ptr(), _ptr(lse_out),
+        st))
+
+
+def _teacher(fn, logits, t_val, t_idx, t_lse):
+    torch, dev, n = _torch(), logits.device, logits.shape[0]
+    K = t_val.shape[-1]
+    _need(fn, dev, torch.float32, (n, K), t_val=t_val)
+    _need(fn, dev, torch.int32, (n, K), t_idx=t_idx)
+    _need(fn, dev, torch.float32, (n,), t_lse=t_lse)
+    return K
+
+
+def _gradient(fn, logits, dlogits):
+    if dlogits.dtype != logits.dtype or dlogits.device != logits.device or dlogits.shape != logits.shape:
+        raise ValueError(f"{fn}: dlogits must have the logits' dtype, device and shape")
+    return _row_shape(fn, dlogits, 2)
+
+
+def dflash_distill_loss(logits, t_val, t_idx, loss_out, t_lse=None, temperature: float = 1.0, weight=None,
+                        stats_out=None, dlogits=None, stream=None):
+    """KL divergence of the student rows logits [rows][V] from a teacher's top
+    logits t_val fp32 / t_idx int32 [rows][K] (index -1: no entry), and with
+    dlogits (logits' dtype and shape; may be logits itself) its gradient.
+    t_lse fp32 [rows]: the teacher's log-sum-exp over its whole row, so the
+    other tokens count as one entry; weight fp32 [rows] scales a row's loss and
+    gradient (0: the row is left out).  loss_out fp32 [rows]; stats_out fp32
+    [rows][4] for dflash_distill_backward."""
+    fn = "dflash_distill_loss"
+    dt = _row_dtype(fn, logits)
+    ld = _row_shape(fn, logits, 2)
+    K = _teacher(fn, logits, t_val, t_idx, t_lse)
+    torch, dev, (n, V) = _torch(), logits.device, logits.shape
+    _need(fn, dev, torch.float32, (n,), weight=weight, loss_out=loss_out)
+    _need(fn, dev, torch.float32, (n, 4), stats_out=stats_out)
+    ldd = 0 if dlogits is None else _gradient(fn, logits, dlogits)
+    lib = load_library()
+    _on(dev, stream, fn, lambda st: lib.dflash_distill_loss(
+        logits.data_ptr(), dt, n, V, ld, t_val.data_ptr(), t_idx.data_ptr(), K, _ptr(t_lse), float(temperature),
+        _ptr(weight), loss_out.data_ptr(), _ptr(stats_out), _ptr(dlogits), ldd, st))
+
+
+def dflash_distill_backward(logits, t_val, t_idx, stats, grad_loss, dlogits, t_lse=None, temperature: float = 1.0,
+                            stream=None):
+    """dlogits = grad_loss[row] * d loss / d logits of an unweighted
+    dflash_distill_loss call that wrote stats.  dlogits may be logits itself."""
+    fn = "dflash_distill_backward"
+    dt = _row_dtype(fn, logits)
+    ld = _row_shape(fn, logits, 2)
+    K = _teacher(fn, logits, t_val, t_idx, t_lse)
+    torch, dev, (n, V) = _torch(), logits.device, logits.shape
+    _need(fn, dev, torch.float32, (n,), grad_loss=grad_loss)
+    _need(fn, dev, torch.float32, (n, 4), stats=stats)
+    ldd = _gradient(fn, logits, dlogits)
+    lib = load_library()
+    _on(dev, stream, fn, lambda st: lib.dflash_distill_backward(
+        logits.data_ptr(), dt, n, V, ld, t_val.data_ptr(), t_idx.data_ptr(), K, _ptr(t_lse), float(temperature),
+        stats.data_ptr(), grad_loss.data_ptr(), dlogits.data_ptr(), ldd, st))
 
 
 def dflash_draft_block(model: "DeviceDrafter", kv: "KVCache", last_tok, draft_out, ws, hidden=None, logits=None,

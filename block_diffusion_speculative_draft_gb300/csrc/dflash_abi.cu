@@ -496,6 +496,144 @@ int32_t dflash_verify_accept_sample(const float* logits, const int32_t* draft, i
                                emitted_out, next_tok_out, ws, static_cast<cudaStream_t>(stream), true));
 }
 
+// Checks common to the calls on rows of logits.
+static int check_rows(const void* logits, int32_t dtype, int64_t rows, int64_t V, int64_t ld) {
+  if (!logits || dtype < 0 || dtype > 2) return DFLASH_EINVAL;
+  if (rows < 1 || V < 1 || ld < V) return DFLASH_EINVAL;
+  if (rows >= (int64_t)1 << 28 || V > ((int64_t)1 << 31) - 1 || ld > ((int64_t)1 << 62) / rows) return DFLASH_EUNSUPPORTED;
+  if (reinterpret_cast<uintptr_t>(logits) & (dtype == DFLASH_DTYPE_F32 ? 3 : 1)) return DFLASH_EINVAL;
+  return DFLASH_OK;
+}
+static bool row_temperature(float t) { return t >= kFilterMinT && t <= kFilterMaxT; }
+
+int32_t dflash_sample(const void* logits, int32_t dtype, int64_t rows, int64_t V, int64_t ld,
+                      const float* temperature, const int32_t* top_k, const float* top_p, const float* min_p,
+                      const float* u, int64_t ld_u, int32_t* tok_out, float* logprob_out, void* stream) {
+  if (int r = check_rows(logits, dtype, rows, V, ld)) return r;
+  if (!temperature || !u || !tok_out || ld_u < V) return DFLASH_EINVAL;
+  FilterArgs a;
+  memset(&a, 0, sizeof(a));
+  a.logits = logits;
+  a.V = V;
+  a.ld = ld;
+  a.temperature = temperature;
+  a.top_k = top_k;
+  a.top_p = top_p;
+  a.min_p = min_p;
+  a.u = u;
+  a.ld_u = ld_u;
+  a.tok = tok_out;
+  a.logprob = logprob_out;
+  if (!(a.status = status_ptr())) return DFLASH_ECUDA;
+  return map_err(filter_sample(a, dtype, rows, static_cast<cudaStream_t>(stream)));
+}
+
+int32_t dflash_verify_filtered_workspace_size(int32_t b, int32_t R, int64_t V, size_t* bytes) {
+  if (!bytes || b < 1 || R < 1 || R > 64 || V < 1) return DFLASH_EINVAL;
+  *bytes = (size_t)b * R * sizeof(RowCut);
+  return DFLASH_OK;
+}
+
+int32_t dflash_verify_accept_filtered(const void* logits, int32_t dtype, int64_t ld, const int32_t* draft, int32_t b,
+                                      int32_t R, int32_t D, int64_t V, const float* temperature,
+                                      const int32_t* top_k, const float* top_p, const float* min_p,
+                                      const float* u_accept, const float* u_sample, int64_t ld_u, int32_t* n_out,
+                                      int32_t* corr_out, int32_t* emitted_out, int32_t* next_tok_out, void* ws,
+                                      size_t ws_bytes, void* stream) {
+  if (b < 1 || R < 1 || R > 64 || D < 1 || D > R) return DFLASH_EINVAL;
+  if (int r = check_rows(logits, dtype, (int64_t)b * R, V, ld)) return r;
+  if (!draft || !temperature || !u_accept || !u_sample || !n_out || !corr_out || ld_u < V) return DFLASH_EINVAL;
+  if (!ws || ws_bytes < (size_t)b * R * sizeof(RowCut) || !aligned16(ws)) return DFLASH_EWORKSPACE;
+  FilterArgs a;
+  memset(&a, 0, sizeof(a));
+  a.logits = logits;
+  a.V = V;
+  a.ld = ld;
+  a.temperature = temperature;
+  a.top_k = top_k;
+  a.top_p = top_p;
+  a.min_p = min_p;
+  a.u = u_sample;
+  a.ld_u = ld_u;
+  a.R = R;
+  a.D = D;
+  a.draft = draft;
+  a.u_accept = u_accept;
+  a.cuts = static_cast<RowCut*>(ws);
+  a.n_out = n_out;
+  a.corr_out = corr_out;
+  a.emitted = emitted_out;
+  a.next_tok = next_tok_out;
+  if (!(a.status = status_ptr())) return DFLASH_ECUDA;
+  return map_err(filter_accept(a, dtype, b, static_cast<cudaStream_t>(stream)));
+}
+
+int32_t dflash_top_logits(const void* logits, int32_t dtype, int64_t rows, int64_t V, int64_t ld, int32_t K,
+                          float temperature, float* val_out, int32_t* idx_out, float* lse_out, void* stream) {
+  if (int r = check_rows(logits, dtype, rows, V, ld)) return r;
+  if (!val_out || !idx_out || K < 1 || !row_temperature(temperature)) return DFLASH_EINVAL;
+  if (K > kTopLogitsMax) return DFLASH_EUNSUPPORTED;
+  FilterArgs a;
+  memset(&a, 0, sizeof(a));
+  a.logits = logits;
+  a.V = V;
+  a.ld = ld;
+  a.T = temperature;
+  a.K = K;
+  a.val = val_out;
+  a.idx = idx_out;
+  a.lse = lse_out;
+  if (!(a.status = status_ptr())) return DFLASH_ECUDA;
+  return map_err(top_logits(a, dtype, rows, static_cast<cudaStream_t>(stream)));
+}
+
+static int32_t distill_impl(const void* logits, int32_t dtype, int64_t rows, int64_t V, int64_t ld,
+                            const float* t_val, const int32_t* t_idx, int32_t K, const float* t_lse,
+                            float temperature, const float* weight, float* loss, float* stats, void* dlogits,
+                            int64_t ldd, bool backward, void* stream) {
+  if (int r = check_rows(logits, dtype, rows, V, ld)) return r;
+  if (!t_val || !t_idx || K < 1 || !row_temperature(temperature) || !aligned16(stats)) return DFLASH_EINVAL;
+  if (backward ? (!stats || !weight || !dlogits) : !loss) return DFLASH_EINVAL;
+  if (dlogits) {
+    if (int r = check_rows(dlogits, dtype, rows, V, ldd)) return r;
+    if (dlogits == logits && ldd != ld && rows > 1) return DFLASH_EINVAL;
+  }
+  if (K > kDistillMaxK || V > (int64_t)1 << 23) return DFLASH_EUNSUPPORTED;
+  DistillArgs a;
+  memset(&a, 0, sizeof(a));
+  a.logits = logits;
+  a.V = V;
+  a.ld = ld;
+  a.t_val = t_val;
+  a.t_idx = t_idx;
+  a.t_lse = t_lse;
+  a.K = K;
+  a.T = temperature;
+  a.weight = weight;
+  a.loss = loss;
+  a.stats = reinterpret_cast<float4*>(stats);
+  a.dlogits = dlogits;
+  a.ldd = ldd;
+  if (!(a.status = status_ptr())) return DFLASH_ECUDA;
+  return map_err(distill(a, dtype, rows, backward, static_cast<cudaStream_t>(stream)));
+}
+
+int32_t dflash_distill_loss(const void* logits, int32_t dtype, int64_t rows, int64_t V, int64_t ld,
+                            const float* t_val, const int32_t* t_idx, int32_t K, const float* t_lse,
+                            float temperature, const float* weight, float* loss_out, float* stats_out, void* dlogits,
+                            int64_t ldd, void* stream) {
+  return distill_impl(logits, dtype, rows, V, ld, t_val, t_idx, K, t_lse, temperature, weight, loss_out, stats_out,
+                      dlogits, ldd, false, stream);
+}
+
+int32_t dflash_distill_backward(const void* logits, int32_t dtype, int64_t rows, int64_t V, int64_t ld,
+                                const float* t_val, const int32_t* t_idx, int32_t K, const float* t_lse,
+                                float temperature, const float* stats, const float* grad_loss, void* dlogits,
+                                int64_t ldd, void* stream) {
+  return distill_impl(logits, dtype, rows, V, ld, t_val, t_idx, K, t_lse, temperature, grad_loss, nullptr,
+                      const_cast<float*>(stats), dlogits, ldd, true, stream);
+}
+
 int32_t dflash_kv_commit(const dflash_weights* w, const dflash_kv* kv, const uint16_t* hid, int32_t rows_per_seq,
                          const int32_t* n, void* ws, size_t ws_bytes, void* stream) {
   if (int r = check_weights(w)) return r;

@@ -208,6 +208,65 @@ size_t verify_ws_bytes(int b, int R, int64_t V);
 cudaError_t verify_accept(const float* logits, const int* draft, int b, int R, int D, int64_t V, int* n_out,
                           int* corr_out, int* emitted, int* next_tok, void* ws, cudaStream_t st, bool pdl);
 
+// --- filtered sampling, filtered accept, top logits (k_filter.cu) ---
+constexpr float kFilterMinT = 1e-6f, kFilterMaxT = 1e6f;  // sampling temperatures (0: greedy)
+constexpr int kTopLogitsMax = 1024;
+struct RowCut {  // one verified row
+  uint64_t cut;  // an entry is kept iff its place is at or above it
+  float m;       // the row's maximum
+  int accept;    // the row's draft token is accepted
+};
+struct FilterArgs {
+  const void* logits;  // [rows] of V entries, ld apart
+  int64_t V, ld;
+  const float* temperature;  // per row (per sequence in the accept); null: T
+  float T;
+  const int* top_k;  // the filters, each nullable
+  const float* top_p;
+  const float* min_p;
+  const float* u;  // uniforms, ld_u apart
+  int64_t ld_u;
+  int* tok;        // sample
+  float* logprob;
+  int R, D;        // accept
+  const int* draft;
+  const float* u_accept;
+  RowCut* cuts;
+  int* n_out;
+  int* corr_out;
+  int* emitted;
+  int* next_tok;
+  int K;           // top logits
+  float* val;
+  int* idx;
+  float* lse;
+  int* status;
+  int idx_bits;    // set by the launchers: bits of V - 1, scale of the weights
+  float scale;
+};
+cudaError_t filter_sample(FilterArgs a, int dtype, int64_t rows, cudaStream_t st);
+cudaError_t filter_accept(FilterArgs a, int dtype, int64_t b, cudaStream_t st);
+cudaError_t top_logits(FilterArgs a, int dtype, int64_t rows, cudaStream_t st);
+
+// --- distillation from a teacher's top logits (k_distill.cu) ---
+constexpr int kDistillMaxK = 1024;
+struct DistillArgs {
+  const void* logits;  // student [rows] of V entries, ld apart
+  int64_t V, ld;
+  const float* t_val;  // teacher [rows][K]
+  const int* t_idx;
+  const float* t_lse;  // nullable
+  int K;
+  float T;
+  const float* weight;  // nullable; the upstream gradient in the backward call
+  float* loss;          // null in the backward call
+  float4* stats;        // nullable: (m, E, m_rest, E_rest); input of the backward call
+  void* dlogits;        // nullable
+  int64_t ldd;
+  int* status;
+};
+cudaError_t distill(const DistillArgs& a, int dtype, int64_t rows, bool backward, cudaStream_t st);
+
 // Allocation-free variant of verify_accept: scratch lives in a fixed device
 // array of kNoAllocScratchBytes inside the library (k_small.cu).
 constexpr size_t kNoAllocScratchBytes = 64 * 1024;

@@ -67,8 +67,11 @@ typedef enum dflash_status {
 #define DFLASH_DEV_KV_CAPACITY 0x1 /* a commit would pass `cap`: skipped   */
 #define DFLASH_DEV_BAD_TOKEN 0x2   /* a token id outside [0, V): row zeroed */
 #define DFLASH_DEV_BAD_LENGTH 0x4  /* len < 0 or n outside [-1, B]         */
+#define DFLASH_DEV_BAD_PARAM 0x8   /* a row's temperature, top_k, top_p or
+                                      min_p outside its range              */
 
-/* Element types accepted by dflash_pack_w8a16. */
+/* Element types accepted by dflash_pack_w8a16 and by the calls on logits that
+ * take a dtype. */
 #define DFLASH_DTYPE_F32 0
 #define DFLASH_DTYPE_F16 1
 #define DFLASH_DTYPE_BF16 2
@@ -342,6 +345,115 @@ DFLASH_API int32_t dflash_commit_draft_block(const dflash_weights* w, const dfla
                                              int32_t* draft_out, float* hidden_out,
                                              float* logits_out, void* ws, size_t ws_bytes,
                                              void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Operators on rows of vocabulary logits.  Common to the calls below:
+ *  - logits: [rows] of V entries of `dtype` (DFLASH_DTYPE_*), consecutive rows
+ *    ld >= V elements apart, the base aligned to an element; nothing is read
+ *    between V and ld.  1 <= V < 2^31, 1 <= rows < 2^28.
+ *  - An entry that is NaN or -inf is masked: it has probability 0 and is never
+ *    returned (the distillation calls instead propagate a NaN).  Every finite
+ *    value counts, the type's lowest included.
+ *  - The order of a row is by descending logit, equal logits by ascending
+ *    index (-0 equals +0).
+ *  - Results depend on the arguments alone: they repeat bit for bit.
+ * Arguments are checked, and errors returned, as for the other calls.
+ * ------------------------------------------------------------------------- */
+
+/* One token per row, drawn from softmax(z / T) under the row's filters.  With
+ * m = max z and w_v = exp((z_v - m) / T):
+ *   top_k keeps the first top_k entries of the order (0 or >= V: all);
+ *   top_p keeps, of those, each entry whose predecessors' w sum to less than
+ *     top_p times the sum over what top_k kept (the first always; 1: all);
+ *   min_p keeps, of those, the entries with z_v >= m + T ln(min_p) (0: all);
+ *   P(v) = w_v / (sum of the kept w), 0 for the others;
+ *   tok = argmax over the kept v of (z_v - m) / T - log(-log u_v), lowest
+ *     index on ties (Gumbel maximum: an exact draw from P); logprob = ln P(tok).
+ * T = 0 takes the first entry of the order (logprob 0), whatever the filters.
+ * temperature [rows] fp32; top_k [rows] int32, top_p and min_p [rows] fp32,
+ * each nullable (no filter).  T must be 0 or in [1e-6, 1e6], top_k >= 0, top_p
+ * and min_p in [0, 1]; a row outside that gets tok -1 and logprob -inf, and
+ * sets DFLASH_DEV_BAD_PARAM.  u: uniforms in [0, 1), [rows] of V fp32, ld_u >= V
+ * apart; only the entries kept are read.  tok_out [rows] int32, logprob_out
+ * [rows] fp32 (nullable).  A row without an unmasked entry gets tok -1 and
+ * logprob -inf.  No workspace. */
+DFLASH_API int32_t dflash_sample(const void* logits, int32_t dtype, int64_t rows, int64_t V, int64_t ld,
+                                 const float* temperature, const int32_t* top_k, const float* top_p,
+                                 const float* min_p, const float* u, int64_t ld_u, int32_t* tok_out,
+                                 float* logprob_out, void* stream);
+
+/* Workspace bytes for dflash_verify_accept_filtered. */
+DFLASH_API int32_t dflash_verify_filtered_workspace_size(int32_t b, int32_t R, int64_t V, size_t* bytes);
+
+/* dflash_verify_accept_sample with each sequence's own temperature, top_k,
+ * top_p and min_p (as in dflash_sample, [b] each; a sequence at T = 0 is
+ * verified greedily).  With P_r the filtered distribution of row r:
+ *   draft i, in order, is accepted iff u_accept[j][i] < P_i(draft[j][i])
+ *   n    = number of leading accepted drafts
+ *   corr = the draw of dflash_sample at row n without draft[j][n] if n < D,
+ *          at row D if n = D < R, else -1 (-1 too where nothing is left)
+ *   emitted / next_tok as in dflash_verify_accept.
+ * logits: [b][R] rows of V entries, ld apart (sequences R * ld apart).  draft
+ * [b][D] int32; an entry outside [0, V) is rejected, so a sequence with fewer
+ * drafts pads with -1.  u_accept [b][D] and u_sample ([b] of V entries, ld_u
+ * apart) are uniforms in [0, 1).  A sequence with a parameter out of range gets
+ * n = -1 (a commit of which appends nothing), corr and next_tok -1, and sets
+ * DFLASH_DEV_BAD_PARAM.  ws holds dflash_verify_filtered_workspace_size bytes;
+ * it needs no zero fill and keeps nothing between calls. */
+DFLASH_API int32_t dflash_verify_accept_filtered(const void* logits, int32_t dtype, int64_t ld, const int32_t* draft,
+                                                 int32_t b, int32_t R, int32_t D, int64_t V,
+                                                 const float* temperature, const int32_t* top_k, const float* top_p,
+                                                 const float* min_p, const float* u_accept, const float* u_sample,
+                                                 int64_t ld_u, int32_t* n_out, int32_t* corr_out,
+                                                 int32_t* emitted_out, int32_t* next_tok_out, void* ws,
+                                                 size_t ws_bytes, void* stream);
+
+/* The first K entries of each row's order, 1 <= K <= 1024: val_out [rows][K]
+ * fp32 (the logits themselves, falling) and idx_out [rows][K] int32; where a
+ * row has fewer unmasked entries the rest is -inf with index -1.  lse_out
+ * [rows] fp32 (nullable) = log sum_v exp(z_v / T) over the whole row (-inf when
+ * nothing counts), temperature T in [1e-6, 1e6].  A target's rows give the
+ * teacher side of dflash_distill_loss.  No workspace. */
+DFLASH_API int32_t dflash_top_logits(const void* logits, int32_t dtype, int64_t rows, int64_t V, int64_t ld,
+                                     int32_t K, float temperature, float* val_out, int32_t* idx_out, float* lse_out,
+                                     void* stream);
+
+/* Distillation of a student's logits from a teacher's top logits.  Per row,
+ * with q = softmax(z / T), the teacher's entries t_val[k], t_idx[k] (k < K, S
+ * the set of their tokens) and p_k = exp(t_val[k] / T - Lt):
+ *   Lt = log sum_k exp(t_val[k] / T) when t_lse is null, else t_lse[row], the
+ *     log-sum-exp of the teacher's whole row at this T; then the tokens outside
+ *     S count as one entry with p_r = max(0, 1 - sum_k p_k) and q_r = their sum
+ *     of q (without t_lse: p_r = 0)
+ *   loss = weight * [sum_k p_k (ln p_k - ln q_{t_idx[k]}) + p_r (ln p_r - ln q_r)]
+ *   dlogits[j] = weight / T * (P q_j - p_j) for j in S, and
+ *                weight / T * q_j (P - p_r / q_r) outside, P = sum_k p_k + p_r
+ * t_val [rows][K] fp32 (finite or -inf), t_idx [rows][K] int32, 1 <= K <= 1024;
+ * an entry with index -1 is no entry.  t_lse [rows] (nullable), weight [rows]
+ * (nullable: 1) and loss_out [rows] are fp32.  V <= 2^23; T in [1e-6, 1e6].
+ *  - dlogits (nullable): [rows] of V entries of `dtype`, ldd >= V apart, all V
+ *    written; it may be the logits' own buffer with ldd = ld (else the two must
+ *    not overlap).
+ *  - stats_out (nullable): [rows][4] fp32, 16-byte aligned, what
+ *    dflash_distill_backward needs.
+ *  - A row with weight 0, or whose teacher lists nothing above -inf, is left
+ *    out: loss 0, gradient 0, its student logits do not matter.
+ *  - A row with an index listed twice, or outside [-1, V), is refused: loss
+ *    NaN, gradient 0, DFLASH_DEV_BAD_TOKEN set.
+ * No workspace. */
+DFLASH_API int32_t dflash_distill_loss(const void* logits, int32_t dtype, int64_t rows, int64_t V, int64_t ld,
+                                       const float* t_val, const int32_t* t_idx, int32_t K, const float* t_lse,
+                                       float temperature, const float* weight, float* loss_out, float* stats_out,
+                                       void* dlogits, int64_t ldd, void* stream);
+
+/* The gradient of the unweighted loss for a given upstream gradient:
+ * dlogits = grad_loss[row] * dloss/dlogits, with stats [rows][4] of a
+ * dflash_distill_loss call on the same logits, teacher entries and T.
+ * grad_loss: [rows] fp32 (0: a zero row).  The rest as in that call. */
+DFLASH_API int32_t dflash_distill_backward(const void* logits, int32_t dtype, int64_t rows, int64_t V, int64_t ld,
+                                           const float* t_val, const int32_t* t_idx, int32_t K, const float* t_lse,
+                                           float temperature, const float* stats, const float* grad_loss,
+                                           void* dlogits, int64_t ldd, void* stream);
 
 /* Draft-KV commit with rollback of the rejected suffix (mlx-dspark v0.0.3,
  * "Notes": KV rollback; dflash-mlx "What It Does": conditioning on target

@@ -1,0 +1,690 @@
+"""GPU parity of the operators on rows of vocabulary logits against the
+float64 oracle: filtered sampling, the filtered accept, top logits and
+distillation.
+
+Integer outputs are compared exactly wherever the decision has a margin in
+the oracle: 2e-5 between the two best scores (fp32 scores carry about 1e-5 at
+magnitude 30; closer calls are settled in double but a thread's own runner-up
+is not reconsidered), 1e-6 between a uniform and a probability (the weights'
+exponentials are good to 2^-22).  Where an entry's sum is within 1e-6 of
+top-p's border the kept set may differ by entries of that mass: they are one
+in a million to be drawn, and move a log-probability by less than 4e-6.
+
+Tolerances.  A log-probability is (z - m)/T - ln W: three roundings of the
+first term, the relative error of W (2^-22 an exponential) and two of the
+logarithm: (|lp| + |ln W| + 4) 2^-21 covers them.  Distillation: loss terms
+p_k (lp_k - lq_k) carry the same errors, summed with weights that add up to
+at most one, so (1 + largest |lp|, |lq|) 2^-20; gradients are differences of
+probabilities (each good to (4 + |x|) 2^-23 of its value, x its exponent)
+scaled by weight / T (outside the listed tokens the second of them is p_r
+times a share, and p_r is one minus a rounded sum), plus the output type's
+half step and fp16's smallest step.
+"""
+import math
+
+import numpy as np
+import pytest
+
+from oracle import rows_oracle as RO
+from tests.gpu_util import gpu_available
+
+pytestmark = [pytest.mark.gpu, pytest.mark.skipif(not gpu_available(), reason="needs a GPU")]
+
+if gpu_available():
+    import torch
+    from block_diffusion_speculative_draft_gb300 import api
+    DEV = torch.device("cuda:0")
+    DT = {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}
+
+
+def _padded(a, dtype, pad):
+    """Device copy of a [..., V] whose rows are V + pad apart, NaN between."""
+    t = torch.from_numpy(np.ascontiguousarray(a, np.float32)).to(DEV).to(DT[dtype])
+    buf = torch.full(t.shape[:-1] + (t.shape[-1] + pad,), float("nan"), dtype=t.dtype, device=DEV)
+    buf[..., : t.shape[-1]] = t
+    return buf[..., : t.shape[-1]]
+
+
+def _host(t):
+    return t.double().cpu().numpy()
+
+
+def _dev(a, dt):
+    return torch.from_numpy(np.ascontiguousarray(a, dt)).to(DEV)
+
+
+def _uniforms(rng, shape):
+    return ((2 * rng.integers(0, 1 << 23, size=shape) + 1) * 2.0 ** -24).astype(np.float32)
+
+
+def _logits(rng, n, V, kind):
+    z = rng.normal(0, 2.0, size=(n, V))
+    if kind == "peaked":
+        h = min(V, 40)
+        for r in range(n):
+            z[r, rng.choice(V, h, replace=False)] = 14 - 1.3 * np.log1p(np.arange(h)) + rng.normal(0, 0.4, h)
+    elif kind == "ties":  # few distinct values
+        z = np.round(z)
+    elif kind == "equal":
+        z[:] = 3.25
+    elif kind == "masked":
+        z[rng.random((n, V)) < 0.7] = -np.inf
+        z[rng.random((n, V)) < 0.1] = np.nan
+        z[rng.random((n, V)) < 0.05] = -65504.0
+        z[0] = -np.inf
+        z[1 % n, :] = np.nan
+        z[2 % n, :] = -65504.0
+    elif kind == "far":  # exponents far below the weights' resolution
+        z *= 40
+    return z
+
+
+def _ask(rng, n, mode):
+    T = rng.uniform(0.5, 1.5, n).astype(np.float32)
+    k = np.zeros(n, np.int32)
+    p = np.ones(n, np.float32)
+    mp = np.zeros(n, np.float32)
+    for i in range(n):
+        m = ["k", "p", "m", "kp", "kpm", "none", "greedy", "wide"][i % 8] if mode == "mixed" else mode
+        if m == "greedy":
+            T[i] = 0
+        if m in ("k", "kp", "kpm"):
+            k[i] = rng.integers(1, 80)
+        if m in ("p", "kp", "kpm"):
+            p[i] = rng.uniform(0.3, 0.99)
+        if m in ("m", "kpm"):
+            mp[i] = rng.uniform(0.001, 0.3)
+        if m == "wide":
+            k[i] = rng.integers(1000, 6000)
+            p[i] = 0.9995
+    return T, k, p, mp
+
+
+def _top_p_border(z, T, k, p):
+    """How close the sum before any entry comes to top-p's bound (relative)."""
+    ids = RO.row_order(z)
+    if T == 0 or p >= 1 or ids.size == 0:
+        return math.inf
+    if k > 0:
+        ids = ids[:k]
+    w = np.exp((z[ids] - z[ids[0]]) / T)
+    before = np.concatenate([[0.0], np.cumsum(w)])
+    return float(np.abs(before / before[-1] - p).min())
+
+
+def _check_sample(z, u, T, k, p, mp, tok, lp):
+    for r in range(len(tok)):
+        rt, rl, gap = RO.sample(z[r], float(T[r]), u[r], int(k[r]), float(p[r]), float(mp[r]))
+        # entries within 1e-6 of top-p's border may fall on its other side
+        slack = 4e-6 if _top_p_border(z[r], float(T[r]), int(k[r]), float(p[r])) < 1e-6 else 0.0
+        if gap > 2e-5:
+            assert tok[r] == rt, (r, T[r], k[r], p[r], mp[r])
+        if rt < 0:
+            assert tok[r] == -1 and lp[r] == -np.inf
+        elif tok[r] == rt:
+            lnw = math.log(np.sum(np.exp((z[r][RO.row_order(z[r])] - np.nanmax(z[r])) / max(float(T[r]), 1e-6))))
+            assert abs(lp[r] - rl) <= (abs(rl) + lnw + 4) * 2.0 ** -21 + slack, (r, lp[r], rl)
+
+
+def _sample(zt, T, k, p, mp, u, stream=None, filters=True):
+    n = zt.shape[0]
+    tok = torch.full((n,), -7, dtype=torch.int32, device=DEV)
+    lp = torch.full((n,), -7.0, dtype=torch.float32, device=DEV)
+    f = dict(top_k=_dev(k, np.int32), top_p=_dev(p, np.float32), min_p=_dev(mp, np.float32)) if filters else {}
+    api.dflash_sample(zt, _dev(T, np.float32), u, tok, logprob_out=lp, stream=stream, **f)
+    return tok, lp
+
+
+@pytest.mark.parametrize("dtype,n,V,pad,kind,mode", [
+    ("f32", 9, 1, 0, "peaked", "mixed"), ("f16", 9, 2, 1, "peaked", "mixed"), ("bf16", 9, 3, 0, "ties", "mixed"),
+    ("f32", 16, 31, 1, "peaked", "mixed"), ("f32", 16, 33, 0, "ties", "mixed"), ("f16", 16, 257, 3, "equal", "mixed"),
+    ("f32", 24, 2047, 0, "peaked", "mixed"), ("bf16", 24, 2049, 5, "peaked", "mixed"),
+    ("f32", 24, 4096, 0, "masked", "mixed"), ("f16", 24, 4099, 2, "masked", "mixed"),
+    ("bf16", 24, 5003, 0, "masked", "mixed"), ("f32", 24, 9001, 7, "far", "mixed"),
+    ("bf16", 32, 20011, 0, "ties", "mixed"), ("f32", 32, 20000, 0, "flat", "mixed"),
+    ("bf16", 16, 50021, 11, "flat", "mixed"), ("f32", 8, 151936, 0, "flat", "mixed"),
+    ("bf16", 8, 151936, 0, "flat", "p"), ("f16", 8, 151936, 0, "peaked", "kp"), ("f32", 2, 300007, 1, "peaked", "p"),
+    ("bf16", 1, 151936, 0, "peaked", "kpm"), ("f32", 1, 151936, 0, "flat", "none"),
+    ("bf16", 400, 3001, 0, "peaked", "mixed"), ("f32", 3, 1000003, 0, "flat", "kp"), ("bf16", 2, 1200001, 3, "flat", "p"),
+])
+def test_sample(dtype, n, V, pad, kind, mode):
+    rng = np.random.default_rng(V + n)
+    zt = _padded(_logits(rng, n, V, kind), dtype, pad)
+    T, k, p, mp = _ask(rng, n, mode)
+    u = _uniforms(rng, (n, V))
+    ut = _padded(u, "f32", pad)
+    tok, lp = _sample(zt, T, k, p, mp, ut)
+    again = _sample(zt, T, k, p, mp, ut)
+    assert api.dflash_get_status() == 0
+    assert torch.equal(tok, again[0]) and torch.equal(lp, again[1])
+    _check_sample(_host(zt), u, T, k, p, mp, tok.cpu().numpy(), lp.cpu().numpy())
+
+
+def test_sample_takes_every_border_of_a_worked_row():
+    # weights 8, 4, 4, 2, 1 at T = 1 / ln 2; the uniforms make the last kept
+    # entry of the order the winner
+    z = np.array([[1.0, 3.0, 0.0, 2.0, 2.0]] * 9, np.float32)
+    order = [1, 3, 4, 0, 2]
+    k = np.array([1, 2, 3, 4, 5, 0, 0, 0, 0], np.int32)
+    p = np.array([1, 1, 1, 1, 1, 0.40, 0.43, 0.64, 0.95], np.float32)
+    mp = np.zeros(9, np.float32)
+    last = [0, 1, 2, 3, 4, 0, 1, 2, 4]
+    u = np.full((9, 5), 0.5, np.float32)
+    for r in range(9):
+        for i, v in enumerate(order):
+            u[r, v] = 1 - 2.0 ** -(4 + 3 * i)
+    T = np.full(9, 1 / math.log(2), np.float32)
+    tok, _ = _sample(_dev(z, np.float32), T, k, p, mp, _dev(u, np.float32))
+    assert tok.tolist() == [order[i] for i in last]
+    # the same bounds as min-p: exactly the maximum, and a bound between entries
+    mp = np.array([1.0, 0.51, 0.49, 0.26, 0.2, 0.12, 0, 0, 0], np.float32)
+    tok, _ = _sample(_dev(z, np.float32), T, np.zeros(9), np.ones(9), mp, _dev(u, np.float32))
+    assert tok.tolist() == [order[i] for i in [0, 0, 2, 2, 3, 4, 4, 4, 4]]
+
+
+def test_sample_follows_its_distribution():
+    rng = np.random.default_rng(5)
+    n, V = 6000, 40
+    z = rng.normal(0, 1.5, V).astype(np.float32)
+    zt = _dev(np.broadcast_to(z, (n, V)), np.float32)
+    T, k, p, mp = (np.full(n, a) for a in (0.9, 6, 0.95, 0.01))
+    tok, _ = _sample(zt, T, k.astype(np.int32), p, mp, _dev(_uniforms(rng, (n, V)), np.float32))
+    ids, q = RO.filtered(z, 0.9, 6, 0.95, 0.01)
+    got = np.bincount(tok.cpu().numpy(), minlength=V)
+    assert got.sum() == got[ids].sum()
+    assert ids.size <= 6 and float(((got[ids] - n * q) ** 2 / (n * q)).sum()) < 20.52  # <= 5 degrees, 99.9 %
+
+
+def test_sample_near_ties_are_settled_in_double():
+    # scores that fp32 cannot tell apart: equal uniforms, logits one step apart
+    V, n = 4096, 6
+    z = np.zeros((n, V), np.float32)
+    hi = np.float32(2.0 ** -26)
+    at = [3, 700, 1500, 2222, 4000, 4095]
+    for r in range(n):
+        z[r, at[r]] = hi
+    u = np.full((n, V), 0.5, np.float32)
+    tok, _ = _sample(_dev(z, np.float32), np.full(n, 0.9), np.zeros(n), np.ones(n), np.zeros(n), _dev(u, np.float32))
+    # a thread keeps the first of its own equal fp32 scores; the winner is
+    # either the larger logit or, where one thread holds both, an earlier entry
+    for r in range(n):
+        assert tok[r] == at[r] or tok[r] < at[r]
+    z[:] = 1.5
+    tok, _ = _sample(_dev(z, np.float32), np.full(n, 0.9), np.zeros(n), np.ones(n), np.zeros(n), _dev(u, np.float32))
+    assert tok.tolist() == [0] * n
+
+
+def test_sample_without_filters_and_bad_parameters():
+    rng = np.random.default_rng(6)
+    n, V = 10, 777
+    z, u = _logits(rng, n, V, "peaked"), _uniforms(rng, (n, V))
+    zt, ut = _padded(z, "f32", 0), _dev(u, np.float32)
+    T = np.full(n, 0.8, np.float32)
+    tok, lp = _sample(zt, T, None, None, None, ut, filters=False)
+    _check_sample(_host(zt), u, T, np.zeros(n, int), np.ones(n), np.zeros(n), tok.cpu().numpy(), lp.cpu().numpy())
+    assert api.dflash_get_status() == 0
+    k, p, mp = np.zeros(n, np.int32), np.ones(n, np.float32), np.zeros(n, np.float32)
+    T[:6] = [-1.0, np.nan, np.inf, 1e-9, 1e9, 0.8]
+    k[5], p[6], mp[7] = -1, 1.5, np.nan
+    tok, lp = _sample(zt, T, k, p, mp, ut)
+    assert api.dflash_get_status() == api.DEV_BAD_PARAM
+    assert tok.tolist()[:8] == [-1] * 8 and np.isneginf(lp.cpu().numpy()[:8]).all()
+    _check_sample(_host(zt)[8:], u[8:], T[8:], k[8:], p[8:], mp[8:], tok.cpu().numpy()[8:], lp.cpu().numpy()[8:])
+
+
+def test_sample_infinite_logits_win():
+    z = np.zeros((3, 600), np.float32)
+    z[0, 77] = np.inf
+    z[1, [5, 599]] = np.inf
+    z[2, [5, 599]] = np.inf
+    u = np.full((3, 600), 0.5, np.float32)
+    u[1, 599] = 0.9
+    u[2, 5] = 0.9
+    tok, lp = _sample(_dev(z, np.float32), np.ones(3), np.zeros(3), np.array([1, 0.9, 1]), np.zeros(3),
+                      _dev(u, np.float32))
+    assert tok.tolist() == [77, 599, 5]
+    assert np.abs(lp.cpu().numpy() - [0, -math.log(2), -math.log(2)]).max() < 1e-6
+
+
+# --------------------------------------------------------------- accept -----
+def _accept(zt, draft, T, k, p, mp, ua, us, **kw):
+    b, R, _ = zt.shape
+    outs = [torch.full((b,), -7, dtype=torch.int32, device=DEV) for _ in range(3)]
+    em = torch.full((b, R), -7, dtype=torch.int32, device=DEV)
+    api.dflash_verify_accept_filtered(zt, _dev(draft, np.int32), _dev(T, np.float32), _dev(ua, np.float32), us,
+                                      outs[0], outs[1], top_k=_dev(k, np.int32), top_p=_dev(p, np.float32),
+                                      min_p=_dev(mp, np.float32), emitted=em, next_tok=outs[2], **kw)
+    return [o.cpu().numpy() for o in (outs[0], outs[1], em, outs[2])]
+
+
+def _accept_margin(z, draft, T, k, p, mp, ua, us):
+    """Smallest margin of the decisions that lead to the oracle's answer."""
+    m = math.inf
+    for r in range(len(z)):
+        m = min(m, _top_p_border(z[r], T, k, p))
+        ids, q = RO.filtered(z[r], T, k, p, mp)
+        drop = None
+        if r < len(draft):
+            hit = q[ids == draft[r]]
+            if hit.size:
+                m = min(m, abs(float(ua[r]) - hit[0]))
+            if hit.size and ua[r] < hit[0]:
+                continue
+            drop = int(draft[r])
+        if T > 0 and ids.size:
+            m = min(m, RO.gumbel_draw(ids, q, us, drop)[1] / 20)
+        break
+    return m
+
+
+@pytest.mark.parametrize("dtype,b,R,D,V,pad,kind,mode", [
+    ("f32", 16, 4, 3, 50, 0, "peaked", "mixed"), ("f16", 9, 5, 5, 333, 3, "ties", "mixed"),
+    ("bf16", 8, 16, 15, 4096, 0, "peaked", "mixed"), ("f32", 8, 6, 5, 4001, 2, "masked", "mixed"),
+    ("bf16", 3, 32, 31, 20011, 0, "flat", "mixed"), ("f32", 1, 16, 15, 151936, 0, "peaked", "kp"),
+    ("bf16", 2, 64, 63, 9000, 1, "peaked", "p"), ("f16", 24, 1, 1, 1000, 0, "peaked", "mixed"),
+    ("f32", 8, 2, 1, 1, 0, "peaked", "mixed"),
+])
+def test_accept(dtype, b, R, D, V, pad, kind, mode):
+    rng = np.random.default_rng(R * V + b)
+    z = _logits(rng, b * R, V, kind).reshape(b, R, V)
+    best = np.where(np.isnan(z), -np.inf, z).argmax(2)
+    draft = best[:, :D].copy()
+    for j in range(b):
+        for i in range(D):
+            if rng.random() < 0.8:
+                z[j, i, draft[j, i]] = 18.0
+        draft[j, rng.integers(0, D)] = rng.integers(-1, V)
+    zt = _padded(z, dtype, pad)
+    z = _host(zt)
+    T, k, p, mp = _ask(rng, b, mode)
+    ua, us = _uniforms(rng, (b, D)), _uniforms(rng, (b, V))
+    n, c, em, nx = _accept(zt, draft, T, k, p, mp, ua, _padded(us, "f32", pad))
+    assert api.dflash_get_status() == 0
+    same = 0
+    for j in range(b):
+        ask = (float(T[j]), int(k[j]), float(p[j]), float(mp[j]))
+        if _accept_margin(z[j], draft[j], *ask, ua[j], us[j]) < 1e-6:
+            continue
+        rn, rc, rem, rnx = RO.verify_accept_filtered(z[j], draft[j], ask[0], ua[j], us[j], *ask[1:])
+        assert (n[j], c[j], nx[j]) == (rn, rc, rnx) and em[j].tolist() == rem.tolist(), (j, ask)
+        same += 1
+    assert same >= (b + 1) // 2
+
+
+def test_accept_at_zero_temperature_is_the_greedy_kernel():
+    rng = np.random.default_rng(8)
+    b, R, V = 6, 16, 4093
+    z = rng.normal(0, 1, (b, R, V)).astype(np.float32)
+    draft = z.argmax(2)[:, : R - 1].astype(np.int32)
+    for j in range(b):
+        draft[j, rng.integers(0, R - 1)] = 5
+    zt = _dev(z, np.float32)
+    got = _accept(zt, draft, np.zeros(b), np.zeros(b), np.full(b, 0.5), np.full(b, 0.1), _uniforms(rng, (b, R - 1)),
+                  _dev(_uniforms(rng, (b, V)), np.float32))
+    ref = [torch.empty(b, dtype=torch.int32, device=DEV) for _ in range(3)]
+    em = torch.empty((b, R), dtype=torch.int32, device=DEV)
+    api.dflash_verify_accept(zt, _dev(draft, np.int32), ref[0], ref[1], em, ref[2])
+    for g, r in zip(got, (ref[0], ref[1], em, ref[2])):
+        assert np.array_equal(g, r.cpu().numpy())
+
+
+def test_accept_refuses_one_sequence_and_serves_the_others():
+    rng = np.random.default_rng(9)
+    b, R, V = 3, 4, 500
+    z = _logits(rng, b * R, V, "peaked").reshape(b, R, V)
+    draft = z.argmax(2)[:, :3]
+    T, k, p, mp = np.array([0.7, np.nan, 0.7]), np.zeros(b), np.ones(b), np.zeros(b)
+    ua, us = _uniforms(rng, (b, 3)), _uniforms(rng, (b, V))
+    n, c, em, nx = _accept(_padded(z, "f32", 0), draft, T, k, p, mp, ua, _dev(us, np.float32))
+    assert api.dflash_get_status() == api.DEV_BAD_PARAM
+    assert (n[1], c[1], nx[1]) == (-1, -1, -1) and (em[1] == -1).all()
+    for j in (0, 2):
+        assert n[j] == RO.verify_accept_filtered(z[j].astype(np.float32), draft[j], np.float32(0.7), ua[j], us[j])[0]
+
+
+# ------------------------------------------------------------ top logits ----
+@pytest.mark.parametrize("dtype,n,V,pad,K,kind", [
+    ("f32", 3, 1, 0, 1, "peaked"), ("f16", 3, 5, 1, 8, "ties"), ("bf16", 5, 33, 0, 33, "ties"),
+    ("f32", 9, 4097, 0, 64, "masked"), ("f16", 9, 3000, 5, 1024, "masked"), ("bf16", 7, 20011, 0, 1000, "ties"),
+    ("f32", 4, 9000, 0, 1024, "equal"), ("f32", 3, 151936, 0, 64, "peaked"), ("bf16", 5, 151936, 0, 256, "flat"),
+    ("f32", 2, 300001, 3, 1023, "flat"), ("bf16", 300, 2500, 0, 10, "flat"), ("bf16", 2, 1200001, 0, 700, "flat"),
+])
+def test_top_logits(dtype, n, V, pad, K, kind):
+    rng = np.random.default_rng(V + K)
+    zt = _padded(_logits(rng, n, V, kind), dtype, pad)
+    z = _host(zt)
+    T = float(np.float32(rng.choice([1.0, 0.6, 2.5])))
+    val = torch.full((n, K), -7.0, dtype=torch.float32, device=DEV)
+    idx = torch.full((n, K), -7, dtype=torch.int32, device=DEV)
+    lse = torch.full((n,), -7.0, dtype=torch.float32, device=DEV)
+    api.dflash_top_logits(zt, K, val, idx, lse_out=lse, temperature=T)
+    assert api.dflash_get_status() == 0
+    val, idx, lse = val.cpu().numpy(), idx.cpu().numpy(), lse.cpu().numpy()
+    for r in range(n):
+        rv, ri, rl = RO.top_logits(z[r], K, T)
+        assert np.array_equal(idx[r], ri) and np.array_equal(val[r], rv.astype(np.float32))
+        # weights are multiples of 2^-(62 - bits of V - 1) besides their exponentials' error
+        assert lse[r] == rl if rl == -math.inf else abs(lse[r] - rl) <= (abs(rl) + 4) * 2.0 ** -21
+
+
+# ------------------------------------------------------------ distillation ---
+def _teach(rng, n, V, K, spread=1.0):
+    K_real = min(K, V)
+    ti = np.full((n, K), -1, np.int32)
+    tv = rng.normal(5, 2.5 * spread, (n, K)).astype(np.float32)
+    for r in range(n):
+        at = rng.permutation(K)[:K_real]
+        ti[r, at] = rng.choice(V, K_real, replace=False)
+        tv[r, rng.integers(0, K)] = -np.inf if K > 2 and r % 3 == 0 else 5.0
+    return tv, ti
+
+
+def _tolerances(z, tv, ti, T, tl, w, dtype):
+    """Loss and gradient bounds of one row (see the module's docstring)."""
+    eps_out = {"f32": 2.0 ** -24, "f16": 2.0 ** -11, "bf16": 2.0 ** -8}[dtype]
+    zt = z / T
+    L = RO._lse(zt)
+    ids = ti[ti >= 0]
+    t = tv[ti >= 0] / T
+    lt = RO._lse(t) if tl is None else float(tl)
+    fin = t > -np.inf
+    big = max(np.abs(t[fin] - lt).max(), np.abs(zt[ids][fin] - L).max(), abs(lt), 1.0)
+    q = np.exp(zt - L)
+    x = np.where(q > 0, np.abs(zt - zt.max()), 0)
+    err = q * (6 + x) * 2.0 ** -22 + 2.0 ** -80
+    p = np.zeros_like(z)
+    p[ids] = np.exp(t - lt)
+    err += p * (6 + np.abs(lt)) * 2.0 ** -22
+    if tl is not None:  # outside: a difference of P q_j and p_r r_j, r the share of what is outside
+        out = np.ones(z.size, bool)
+        out[ids] = False
+        if out.any() and zt[out].max() > -np.inf:
+            share = np.exp(zt[out] - RO._lse(zt[out]))
+            pr = max(0.0, 1.0 - p.sum())
+            # p_r is one minus a sum whose terms are good to 2^-21 each
+            err[out] += share * (pr * (6 + np.where(share > 0, np.abs(zt[out] - zt[out].max()), 0)) * 2.0 ** -22
+                                 + (p * (1 + np.abs(lt))).sum() * 2.0 ** -22)
+    return abs(w) * (1 + big) * 2.0 ** -20, abs(w) / T * err, eps_out, 2.0 ** -25 if dtype == "f16" else 0.0
+
+
+CASES = [("f32", 4, 1, 0, 1, False), ("f16", 5, 2, 1, 4, True), ("bf16", 6, 33, 0, 5, True),
+         ("f32", 7, 257, 2, 300, False), ("f16", 9, 1000, 7, 37, True), ("bf16", 9, 4099, 0, 64, False),
+         ("f32", 6, 20011, 0, 1024, True), ("f32", 3, 151936, 0, 64, True), ("bf16", 3, 151936, 0, 128, True),
+         ("f16", 3, 50021, 3, 1, False), ("bf16", 320, 2111, 0, 8, True), ("f32", 2, 1000003, 1, 17, True)]
+
+
+def _distill_inputs(dtype, n, V, pad, K, rest):
+    rng = np.random.default_rng(V * 3 + K)
+    z = rng.normal(0, 2.0, (n, V))
+    tv, ti = _teach(rng, n, V, K)
+    for r in range(n):
+        on = ti[r] >= 0
+        z[r, ti[r][on]] = np.where(tv[r][on] > -np.inf, tv[r][on], 0) + rng.normal(0, 1, on.sum()) + 2
+        if V > 40 and r % 4 == 1:
+            z[r, rng.random(V) < 0.3] = -np.inf
+            z[r, ti[r][on]] = 4.0
+    zt = _padded(z, dtype, pad)
+    T = float(np.float32([1.0, 0.7, 2.0][K % 3]))
+    tl = None
+    if rest:
+        tl = np.array([RO._lse(tv[r][ti[r] >= 0] / T) + rng.uniform(0.01, 0.5) for r in range(n)], np.float32)
+    w = rng.uniform(0.2, 2.0, n).astype(np.float32)
+    w[n // 2] = 0.0
+    return zt, tv, ti, T, tl, w
+
+
+def _check_distill(z, tv, ti, T, tl, w, loss, dz, dtype):
+    for r in range(len(z)):
+        tlr = None if tl is None else float(tl[r])
+        rl, rg = RO.distill(z[r], tv[r], ti[r], T, tlr, float(w[r]))
+        if w[r] == 0:
+            assert loss[r] == 0 and not dz[r].any()
+            continue
+        tol_l, tol_g, eps, step = _tolerances(z[r], tv[r], ti[r], T, tlr, float(w[r]), dtype)
+        if loss is not None:
+            assert loss[r] == rl or abs(loss[r] - rl) <= tol_l, (r, loss[r], rl, tol_l)
+        bound = tol_g + (np.abs(rg) + tol_g) * eps + step
+        assert np.all(np.abs(dz[r] - rg) <= bound), (r, np.max(np.abs(dz[r] - rg) - bound))
+
+
+@pytest.mark.parametrize("dtype,n,V,pad,K,rest", CASES)
+def test_distill(dtype, n, V, pad, K, rest):
+    zt, tv, ti, T, tl, w = _distill_inputs(dtype, n, V, pad, K, rest)
+    z = _host(zt)
+    tvd, tid, wd = _dev(tv, np.float32), _dev(ti, np.int32), _dev(w, np.float32)
+    tld = None if tl is None else _dev(tl, np.float32)
+    loss = torch.full((n,), -7.0, device=DEV)
+    dz = _padded(np.full((n, V), 7.0), dtype, pad)
+    api.dflash_distill_loss(zt, tvd, tid, loss, t_lse=tld, temperature=T, weight=wd, dlogits=dz)
+    assert api.dflash_get_status() == 0
+    _check_distill(z, tv, ti, T, tl, w, loss.cpu().numpy(), _host(dz), dtype)
+    if pad:  # what lies between the rows stays
+        buf = torch.as_strided(dz, (n - 1, pad), (V + pad, 1), dz.storage_offset() + V)
+        assert torch.isnan(buf).all()
+    # the loss alone, and its gradient by the second call
+    only, stats = torch.empty_like(loss), torch.empty((n, 4), device=DEV)
+    api.dflash_distill_loss(zt, tvd, tid, only, t_lse=tld, temperature=T, weight=wd)
+    assert torch.equal(only, loss)
+    api.dflash_distill_loss(zt, tvd, tid, only, t_lse=tld, temperature=T, stats_out=stats)
+    back = torch.empty((n, V), dtype=zt.dtype, device=DEV)
+    api.dflash_distill_backward(zt, tvd, tid, stats, wd, back, t_lse=tld, temperature=T)
+    scaled = torch.where(wd == 0, torch.zeros_like(only), only * wd)
+    _check_distill(z, tv, ti, T, tl, w, scaled.cpu().numpy(), _host(back), dtype)
+    # in place of the logits, both ways
+    own = zt.clone() if pad == 0 else _padded(z, dtype, pad)
+    api.dflash_distill_loss(own, tvd, tid, only, t_lse=tld, temperature=T, weight=wd, dlogits=own)
+    assert torch.equal(own, dz) and torch.equal(only, loss)
+    own = _padded(z, dtype, pad)
+    api.dflash_distill_backward(own, tvd, tid, stats, wd, own, t_lse=tld, temperature=T)
+    assert torch.equal(own, back)
+
+
+@pytest.mark.parametrize("rest", [False, True])
+def test_distill_gradient_against_differences(rest):
+    rng = np.random.default_rng(11)
+    V, K, T = 70, 6, 1.3
+    z = rng.normal(0, 1, V)
+    tv, ti = rng.normal(1, 1, (1, K)).astype(np.float32), rng.choice(V, (1, K), replace=False).astype(np.int32)
+    tl = _dev([RO._lse(tv[0] / T) + 0.3], np.float32) if rest else None
+    h = 2.0 ** -6
+    rows = np.stack([z] + [z + s * h * e for e in np.eye(V) for s in (1, -1)])
+    n = len(rows)
+    rows = rows.astype(np.float32)
+    loss = torch.empty(n, device=DEV)
+    grad = torch.empty((n, V), device=DEV)
+    api.dflash_distill_loss(_dev(rows, np.float32), _dev(np.repeat(tv, n, 0), np.float32),
+                            _dev(np.repeat(ti, n, 0), np.int32), loss,
+                            t_lse=None if tl is None else tl.repeat(n), temperature=T, dlogits=grad)
+    l = loss.double().cpu().numpy()
+    num = (l[1::2] - l[2::2]) / (rows[1::2].astype(np.float64) - rows[2::2])[np.arange(V), np.arange(V)]
+    # central differences: h^2 / 6 times a third derivative below 1 / T^3, and
+    # two losses good to 2^-20 of their terms over 2 h
+    assert np.abs(num - _host(grad)[0]).max() < h * h / 6 / T ** 3 + 8 * 2.0 ** -20 / (2 * h)
+
+
+def test_distill_rows_left_out_and_refused():
+    V, K = 3000, 4
+    rng = np.random.default_rng(12)
+    n = 8
+    z = rng.normal(0, 1, (n, V)).astype(np.float32)
+    tv = np.zeros((n, K), np.float32)
+    ti = np.tile(np.array([5, 900, 1700, 2999], np.int32), (n, 1))
+    ti[0] = -1                       # nothing listed
+    tv[1] = -np.inf                  # nothing above -inf
+    z[2] = np.nan                    # left out by its weight
+    ti[3, 2] = 5                     # twice the same token
+    ti[4, 1] = V                     # outside
+    ti[5, 0] = -2                    # outside
+    z[6, 100] = np.nan               # a NaN student
+    w = np.ones(n, np.float32)
+    w[2] = 0
+    loss, dz = torch.full((n,), -7.0, device=DEV), torch.full((n, V), 7.0, device=DEV)
+    stats = torch.empty((n, 4), device=DEV)
+    args = (_dev(z, np.float32), _dev(tv, np.float32), _dev(ti, np.int32))
+    api.dflash_distill_loss(*args, loss, weight=_dev(w, np.float32), dlogits=dz, stats_out=stats)
+    assert api.dflash_get_status() == api.DEV_BAD_TOKEN
+    l, g = loss.cpu().numpy(), dz.cpu().numpy()
+    assert l[:3].tolist() == [0, 0, 0] and np.isnan(l[3:7]).all() and not g[:6].any() and np.isnan(g[6]).any()
+    rl, rg = RO.distill(z[7].astype(np.float64), tv[7], ti[7])
+    assert abs(l[7] - rl) < 1e-5 and np.abs(g[7] - rg).max() < 1e-6
+    # the backward call leaves the same rows out
+    back = torch.full((n, V), 7.0, device=DEV)
+    api.dflash_distill_backward(*args, stats, _dev(w, np.float32), back)
+    assert api.dflash_get_status() == api.DEV_BAD_TOKEN
+    assert not back[:6].any() and np.abs(back[7].cpu().numpy() - rg).max() < 1e-6
+
+
+def test_distill_keeps_the_rest_when_the_student_is_sure():
+    # q outside the listed tokens near 1e-30: far below what 1 - sum of q keeps
+    V = 5000
+    z = np.full((1, V), -70.0, np.float32)
+    z[0, 7], z[0, 9] = 3.0, 2.0
+    tv, ti = np.array([[1.0, 0.5]], np.float32), np.array([[7, 9]], np.int32)
+    tl = np.array([RO._lse(tv[0]) + 0.05], np.float32)
+    loss, dz = torch.empty(1, device=DEV), torch.empty((1, V), device=DEV)
+    api.dflash_distill_loss(_dev(z, np.float32), _dev(tv, np.float32), _dev(ti, np.int32), loss,
+                            t_lse=_dev(tl, np.float32), dlogits=dz)
+    rl, rg = RO.distill(z[0].astype(np.float64), tv[0], ti[0], 1.0, float(tl[0]))
+    # p_r carries the error of sums near one, 2^-23 of 0.05
+    assert abs(float(loss[0]) - rl) < 1e-5 * rl and np.abs(_host(dz)[0] - rg).max() < 1e-6
+    assert np.abs(_host(dz)[0][100] / rg[100] - 1) < 2e-5
+
+
+# ------------------------------------------------------------- as a whole ----
+def test_other_stream_graph_and_early_launch_repeat():
+    rng = np.random.default_rng(13)
+    n, V, K = 12, 20011, 32
+    zt = _padded(_logits(rng, n, V, "peaked"), "bf16", 5)
+    T, k, p, mp = (_dev(a, d) for a, d in zip(_ask(rng, n, "mixed"), (np.float32, np.int32, np.float32, np.float32)))
+    u = _dev(_uniforms(rng, (n, V)), np.float32)
+    ua = _dev(_uniforms(rng, (3, 3)), np.float32)
+    z3 = zt.unflatten(0, (3, 4))
+    draft = torch.nan_to_num(z3.float(), nan=-1e9).argmax(2)[:, :3].to(torch.int32).contiguous()
+    i32 = lambda *s: torch.full(s, -7, dtype=torch.int32, device=DEV)
+    f32 = lambda *s: torch.full(s, -7.0, device=DEV)
+    o = dict(tok=i32(n), lp=f32(n), n=i32(3), c=i32(3), em=i32(3, 4), nx=i32(3), val=f32(n, K), idx=i32(n, K),
+             lse=f32(n), loss=f32(n), st=f32(n, 4), dz=torch.zeros((n, V), dtype=torch.bfloat16, device=DEV),
+             dz2=torch.zeros((n, V), dtype=torch.bfloat16, device=DEV))
+    student = _padded(_logits(rng, n, V, "flat"), "bf16", 0)
+    ones = torch.ones(n, device=DEV)
+    ws = torch.empty(api.dflash_verify_filtered_workspace_size(3, 4, V), dtype=torch.uint8, device=DEV)
+
+    def everything(stream=None):
+        api.dflash_sample(zt, T, u, o["tok"], top_k=k, top_p=p, min_p=mp, logprob_out=o["lp"], stream=stream)
+        api.dflash_verify_accept_filtered(z3, draft, T[:3], ua, u[:3], o["n"], o["c"], top_k=k[:3], top_p=p[:3],
+                                          min_p=mp[:3], emitted=o["em"], next_tok=o["nx"], ws=ws, stream=stream)
+        api.dflash_top_logits(zt, K, o["val"], o["idx"], lse_out=o["lse"], stream=stream)
+        api.dflash_distill_loss(student, o["val"], o["idx"], o["loss"], t_lse=o["lse"], stats_out=o["st"],
+                                dlogits=o["dz"], stream=stream)
+        api.dflash_distill_backward(student, o["val"], o["idx"], o["st"], ones, o["dz2"], t_lse=o["lse"],
+                                    stream=stream)
+
+    def snapshot_and_clear():
+        torch.cuda.synchronize()
+        s = {a: t.clone() for a, t in o.items()}
+        for t in o.values():
+            t.zero_()
+        torch.cuda.synchronize()
+        return s
+
+    everything()
+    ref = snapshot_and_clear()
+    side = torch.cuda.Stream()
+    everything(side)
+    runs = [snapshot_and_clear()]
+    with torch.cuda.stream(side):
+        everything()
+    runs.append(snapshot_and_clear())
+    with api.launch_mode(api.LAUNCH_EARLY):
+        everything()
+    runs.append(snapshot_and_clear())
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        everything()
+    for _ in range(2):
+        g.replay()
+        runs.append(snapshot_and_clear())
+    for s in runs:
+        for a in ref:
+            assert torch.equal(ref[a].view(torch.uint8), s[a].view(torch.uint8)), a
+    assert api.dflash_get_status() == 0
+
+
+def test_a_step_of_the_loop_answers_and_teaches():
+    """Draft a block, score it, accept under filters, commit, and fit the
+    drafter's rows to the target's: the calls as they follow one another."""
+    from block_diffusion_speculative_draft_gb300 import synth
+    from block_diffusion_speculative_draft_gb300 import workload as WL
+    from block_diffusion_speculative_draft_gb300.configs import TINY as cfg
+    model = api.DeviceDrafter(cfg, synth.FloatWeights(synth.drafter_weights(cfg)), DEV)
+    kv = api.KVCache(cfg, 1, cfg.ctx[0] + 4 * cfg.B, DEV)
+    ws = api.workspace(cfg, 1, cfg.B, DEV)
+    WL.commit_contexts(api, torch, cfg, model, kv, ws, WL.contexts(cfg), cfg.B, DEV)
+    B, V, K = cfg.B, cfg.V, 20
+    t0 = torch.tensor([7], dtype=torch.int32, device=DEV)
+    draft = torch.empty((1, B - 1), dtype=torch.int32, device=DEV)
+    rows = torch.empty((1, B - 1, V), device=DEV)
+    api.dflash_draft_block(model, kv, t0, draft, ws, logits=rows)
+    # a target that agrees with the first five drafts
+    rng = np.random.default_rng(14)
+    z = torch.from_numpy(rng.normal(0, 1, (1, B, V)).astype(np.float32)).to(DEV)
+    z[0, torch.arange(5, device=DEV), draft[0, :5].long()] = 30.0
+    T, k, p = (torch.tensor([a], device=DEV, dtype=d) for a, d in
+               ((0.8, torch.float32), (50, torch.int32), (0.95, torch.float32)))
+    ua, us = (torch.from_numpy(_uniforms(rng, s)).to(DEV) for s in ((1, B - 1), (1, V)))
+    n, corr, nxt = (torch.empty(1, dtype=torch.int32, device=DEV) for _ in range(3))
+    em = torch.empty((1, B), dtype=torch.int32, device=DEV)
+    api.dflash_verify_accept_filtered(z, draft, T, ua, us, n, corr, top_k=k, top_p=p, emitted=em, next_tok=nxt)
+    hid = torch.from_numpy(synth.target_hidden(cfg.seed, "blk", B, cfg.k * cfg.H)[None]).to(DEV)
+    before = int(kv.len[0])
+    api.dflash_kv_commit(model, kv, hid, n, ws)
+    zh, dh = z[0].double().cpu().numpy(), draft[0].cpu().numpy()
+    rn, rc, rem, rnx = RO.verify_accept_filtered(zh, dh, float(T[0]), ua[0].cpu().numpy(), us[0].cpu().numpy(), 50,
+                                                 float(p[0]))
+    assert (int(n[0]), int(corr[0]), int(nxt[0])) == (rn, rc, rnx) and em[0].tolist() == rem.tolist() and rn >= 5
+    assert int(kv.len[0]) == before + rn + 1
+    # the target's rows teach the drafter's
+    val, idx = torch.empty((B - 1, K), device=DEV), torch.empty((B - 1, K), dtype=torch.int32, device=DEV)
+    lse, loss = torch.empty(B - 1, device=DEV), torch.empty(B - 1, device=DEV)
+    student = rows[0].clone()
+    api.dflash_top_logits(z[0, : B - 1], K, val, idx, lse_out=lse)
+    api.dflash_distill_loss(student, val, idx, loss, t_lse=lse, dlogits=student)
+    for i in range(B - 1):
+        rl, rg = RO.distill(rows[0, i].double().cpu().numpy(), val[i].cpu().numpy(), idx[i].cpu().numpy(), 1.0,
+                            float(lse[i]))
+        assert abs(float(loss[i]) - rl) < 1e-4 * (1 + abs(rl))
+        assert np.abs(student[i].double().cpu().numpy() - rg).max() < 1e-5
+    assert api.dflash_get_status() == 0
+
+
+def test_binding_refuses_mismatched_tensors():
+    z = torch.zeros((2, 64), device=DEV)
+    f, i, u = torch.ones(2, device=DEV), torch.zeros(2, dtype=torch.int32, device=DEV), torch.zeros((2, 64), device=DEV)
+    for bad in (dict(logits=z.double()), dict(logits=z.cpu()), dict(logits=z.t()), dict(logits=z[0]),
+                dict(temperature=f[:1]), dict(temperature=f.half()), dict(u=u[:, :32]), dict(u=u.half()),
+                dict(tok_out=i.long()), dict(top_k=f), dict(top_p=f.cpu()),
+                dict(logits=z[:1].expand(2, 64), code=-1)):
+        code = bad.pop("code", None)
+        args = dict(logits=z, temperature=f, u=u, tok_out=i)
+        args.update(bad)
+        with pytest.raises(ValueError if code is None else api.DflashError):
+            api.dflash_sample(**args)
+    z3 = torch.zeros((2, 3, 64), device=DEV)
+    with pytest.raises(ValueError):  # uneven rows
+        api.dflash_verify_accept_filtered(torch.zeros((2, 4, 64), device=DEV)[:, :3], torch.zeros((2, 2), dtype=torch.int32, device=DEV),
+                                          f, torch.zeros((2, 2), device=DEV), u, i.clone(), i.clone())
+    with pytest.raises(ValueError):
+        api.dflash_verify_accept_filtered(z3, torch.zeros((2, 2), device=DEV), f, torch.zeros((2, 2), device=DEV), u,
+                                          i.clone(), i.clone())
+    with pytest.raises(api.DflashError) as e:
+        api.dflash_verify_accept_filtered(z3, torch.zeros((2, 2), dtype=torch.int32, device=DEV), f,
+                                          torch.zeros((2, 2), device=DEV), u, i.clone(), i.clone(),
+                                          ws=torch.zeros(8, dtype=torch.uint8, device=DEV))
+    assert e.value.code == -5
+    val, idx = torch.zeros((2, 4), device=DEV), torch.zeros((2, 4), dtype=torch.int32, device=DEV)
+    with pytest.raises(ValueError):
+        api.dflash_top_logits(z, 5, val, idx)
+    with pytest.raises(ValueError):
+        api.dflash_distill_loss(z, val, idx, f.clone(), dlogits=z.half())
+    with pytest.raises(ValueError):
+        api.dflash_distill_backward(z, val, idx, torch.zeros((2, 2), device=DEV), f, z.clone())
