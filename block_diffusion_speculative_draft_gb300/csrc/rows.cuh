@@ -76,6 +76,111 @@ __device__ __forceinline__ float log2_weight(float v, float m, InvT c) {
   return v == m ? 0.f : fmaf(d, c.lo, d * c.hi);
 }
 
+__device__ __forceinline__ float fast_exp2(float x) {  // below 2^-126: 0
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// -------------------------------------------------- 16-byte packs of a row ---
+// Four 32-bit words: one fp32 entry each, or two 16-bit ones.
+template <typename T>
+struct Pack;
+template <>
+struct Pack<float> {
+  static constexpr int kPer = 1;  // entries per word
+  static constexpr uint32_t kNegInf = 0xFF800000u;
+  static __device__ __forceinline__ void open(uint32_t w, float* v) { v[0] = __uint_as_float(w); }
+  static __device__ __forceinline__ uint32_t close(const float* v) { return __float_as_uint(v[0]); }
+  static __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+    return __float_as_uint(fmaxf(__uint_as_float(a), __uint_as_float(b)));
+  }
+};
+template <>
+struct Pack<__half> {
+  static constexpr int kPer = 2;
+  static constexpr uint32_t kNegInf = 0xFC00FC00u;
+  static __device__ __forceinline__ void open(uint32_t w, float* v) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
+    v[0] = f.x;
+    v[1] = f.y;
+  }
+  static __device__ __forceinline__ uint32_t close(const float* v) {
+    const __half2 h = __floats2half2_rn(v[0], v[1]);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+  static __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+    const __half2 h = __hmax2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+};
+template <>
+struct Pack<__nv_bfloat16> {
+  static constexpr int kPer = 2;
+  static constexpr uint32_t kNegInf = 0xFF80FF80u;
+  static __device__ __forceinline__ void open(uint32_t w, float* v) {
+    v[0] = __uint_as_float(w << 16);
+    v[1] = __uint_as_float(w & 0xFFFF0000u);
+  }
+  static __device__ __forceinline__ uint32_t close(const float* v) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(v[0], v[1]);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+  static __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+    const __nv_bfloat162 h =
+        __hmax2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+};
+
+// One part of a row held in shared memory.  A row is cut at 16-byte
+// boundaries of its global addresses, so the part's packs move by one bulk
+// copy and only the row's first and last pack can be partial: their missing
+// entries are -inf in shared memory.  Entry e of the part (row entry first + e)
+// is element off + e of the buffer.
+template <typename T>
+struct Part {
+  static constexpr int kE = 16 / sizeof(T);
+  int64_t first;
+  int n, off, packs;
+
+  __device__ __forceinline__ void cut(const T* row, int64_t V, int part, int parts) {
+    const int o = static_cast<int>((reinterpret_cast<uintptr_t>(row) & 15) / sizeof(T));
+    const int64_t all = (V + o + kE - 1) / kE;
+    const int64_t p0 = all * part / parts, p1 = all * (part + 1) / parts;
+    const int64_t e0 = p0 * kE - o > 0 ? p0 * kE - o : 0;
+    const int64_t e1 = p1 * kE - o < V ? p1 * kE - o : V;
+    first = e0;
+    n = e1 > e0 ? static_cast<int>(e1 - e0) : 0;
+    off = p0 == 0 ? o : 0;
+    packs = static_cast<int>(p1 - p0);
+  }
+  // Starts the copy (thread 0, mbarrier `bar`) and loads the partial packs
+  // (all threads); the part is complete after a wait on `bar` and a barrier.
+  __device__ __forceinline__ void load(const T* row, T* buf, uint64_t* bar) const {
+    const int b0 = off > 0 ? 1 : 0;
+    const int b1 = (off + n) / kE > b0 ? (off + n) / kE : b0;  // full packs [b0, b1)
+    if (threadIdx.x == 0) {
+      const uint32_t bytes = static_cast<uint32_t>(b1 - b0) * 16u;
+      mbar_arrive_expect_tx(bar, bytes);
+      fence_proxy_async_global();  // the logits were written with generic stores
+      if (bytes) bulk_g2s(buf + b0 * kE, row + first + b0 * kE - off, bytes, bar);
+    }
+    if (threadIdx.x < 2 * kE) {  // the first pack, then the one after the full ones
+      const int at = threadIdx.x < kE ? threadIdx.x : b1 * kE + threadIdx.x - kE;
+      const bool partial = threadIdx.x < kE ? b0 == 1 : b1 < packs;
+      if (partial) {
+        const int e = at - off;
+        buf[at] = e >= 0 && e < n ? row[first + e] : from_f32<T>(-INFINITY);
+      }
+    }
+  }
+  static __host__ size_t bytes(int64_t V, int parts) {
+    const int64_t all = (V + 2 * kE - 2) / kE;
+    return static_cast<size_t>((all + parts - 1) / parts) * 16;
+  }
+};
+
 // ------------------------------------------------------------- clusters ----
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
