@@ -215,6 +215,8 @@ struct RowCut {  // one verified row
   uint64_t cut;  // an entry is kept iff its place is at or above it
   float m;       // the row's maximum
   int accept;    // the row's draft token is accepted
+  int tok;       // the token drawn where it is not; -2: still to be drawn
+  int pad;
 };
 struct FilterArgs {
   const void* logits;  // [rows] of V entries, ld apart
@@ -229,6 +231,7 @@ struct FilterArgs {
   int* tok;        // sample
   float* logprob;
   int R, D;        // accept
+  int rows_used;   // rows of a sequence that can matter, set by the launcher
   const int* draft;
   const float* u_accept;
   RowCut* cuts;
