@@ -29,173 +29,245 @@ namespace dfl {
 namespace {
 
 constexpr int kDevBadToken = 0x2;
-constexpr double kMassOne = 1099511627776.0;  // 2^40: probabilities are summed as integers
+constexpr float kMassOne = 1099511627776.f;  // 2^40: probabilities are summed as integers
+constexpr float kLn2 = 0.6931471805599453f;
 
-// Shared memory of one CTA: this header, the teacher's entries (four arrays
+// Shared memory of one CTA: this header, the teacher's entries (three arrays
 // of K), the bitmap of the part's listed entries, then the part itself.
 template <int NW>
-struct Shared {
+struct alignas(16) Shared {
   Exchange<NW> x;
-  float red[NW];
+  float4 warp[2][NW];
+  uint64_t warp_mass[NW];
   float4 part[kMaxCluster];  // (maximum, sum, refused) of each CTA's part
   uint64_t bar;
 };
 
 struct Entries {
-  float* lp;  // the teacher's logits, then log-probabilities
-  float* p;   // its probabilities
+  float* p;   // the teacher's logits, then its probabilities
   float* z;   // the student's logits at its tokens
   int* at;    // the tokens, -1: no entry
 };
 __device__ __forceinline__ Entries entries_at(uint8_t* base, int K) {
   Entries e;
-  e.lp = reinterpret_cast<float*>(base);
-  e.p = e.lp + K;
+  e.p = reinterpret_cast<float*>(base);
   e.z = e.p + K;
   e.at = reinterpret_cast<int*>(e.z + K);
   return e;
 }
-size_t entries_bytes(int K) { return (static_cast<size_t>(K) * 16 + 15) & ~size_t(15); }
+__host__ __device__ inline size_t entries_bytes(int K) { return (static_cast<size_t>(K) * 12 + 15) & ~size_t(15); }
 size_t bitmap_bytes(int64_t n) { return (static_cast<size_t>((n + 31) / 32) * 4 + 15) & ~size_t(15); }
 
 // Sum / maximum of a float over the CTA in a fixed order (every thread gets it).
 template <int NW>
-__device__ __forceinline__ float cta_sum(float v, float* red) {
+__device__ __forceinline__ float cta_sum(float v, float4* red) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5].x = v;
   __syncthreads();
   v = 0.f;
 #pragma unroll
-  for (int w = 0; w < NW; ++w) v += red[w];
-  __syncthreads();
+  for (int w = 0; w < NW; ++w) v += red[w].x;
   return v;
 }
 template <int NW>
-__device__ __forceinline__ float cta_max(float v, float* red) {
+__device__ __forceinline__ float cta_max(float v, float4* red) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5].x = v;
   __syncthreads();
-  v = red[0];
+  v = red[0].x;
 #pragma unroll
-  for (int w = 1; w < NW; ++w) v = fmaxf(v, red[w]);
-  __syncthreads();
+  for (int w = 1; w < NW; ++w) v = fmaxf(v, red[w].x);
   return v;
 }
 
-// exp((v - m) / T) for v <= m
-__device__ __forceinline__ float exp_diff(float v, float m, InvT c) { return exp2f(log2_weight(v, m, c)); }
+// What the teacher's entries contribute, with the student's logits at them.
+// Exponents are in units of log2 (x = z log2(e) / T).
+struct Teacher {
+  float tm;    // largest listed logit (-inf: nothing is listed)
+  bool bad;    // refused by this CTA's view of the row
+  float P;     // sum p + p_r
+  float pr;
+  float ref;   // reference of the listed student logits
+  float es;    // sum of 2^(x_k - ref)
+  float self;  // sum p_k (ln p_k - ln 2 (x_k - ref))
+};
 
-// The teacher's entries of a row.  `bits` (zero) marks the listed entries of
-// [c0, c1); a mark that is there already, or a token out of range, refuses the
-// row.  z is gathered for every entry, or for those in [c0, c1) alone.
-// Returns the largest t of this thread's entries.
+// A reference for exponents whose maximum is m: its own exponent, held within
+// +-kRefMax.  Logits beyond that (the type's lowest value as a mask, infinities
+// aside from -inf) count as the bound, so that rows of nothing else still have
+// a distribution.
+__device__ __forceinline__ float ref_of(float m, float c) {
+  const float r = m * c;
+  return r > kRefMax ? kRefMax : (r > -kRefMax ? r : -kRefMax);
+}
+__device__ __forceinline__ float exponent(float v, float c, float ref) {
+  const float r = v * c;
+  if (fabsf(r) < kRefMax || !(v > -INFINITY)) return fmaf(v, c, -ref);  // -inf and NaN stay
+  return (r > 0.f ? kRefMax : -kRefMax) - ref;
+}
+// Calls f(weight) with weight(v) = 2^(exponent of v): the bare form where the
+// reference, and so every entry below it, is inside the bound.
+template <typename F>
+__device__ __forceinline__ void with_weight(float c, float ref, F f) {
+  if (fabsf(ref) < kRefMax) {
+    f([=](float v) { return fast_exp2(fmaf(v, c, -ref)); });
+  } else {
+    f([=](float v) { return fast_exp2(exponent(v, c, ref)); });
+  }
+}
+
+// Reads the row's entries.  `bits` (zero) marks the listed tokens in [c0, c1);
+// a mark that is there already, or a token out of range, refuses the row.
+// `row_z`: the student's logits are wanted for every entry (read from global
+// memory); else es and self are not formed.
 template <typename T, int NT>
-__device__ __forceinline__ float list_entries(const DistillArgs& a, int64_t row, const T* z, int64_t c0, int64_t c1,
-                                              bool own_only, Entries e, uint32_t* bits, bool& bad) {
-  float tm = -INFINITY;
+__device__ __forceinline__ Teacher read_teacher(const DistillArgs& a, int64_t row, const T* z, int64_t c0, int64_t c1,
+                                                bool row_z, Entries e, uint32_t* bits, Shared<NT / 32>& s) {
+  constexpr int NW = NT / 32;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const bool some = warp * 32 < a.K;  // this warp holds entries
+  Teacher t;
+  bool bad = false;
+  float tm = -INFINITY, zm = -INFINITY;
   for (int k = threadIdx.x; k < a.K; k += NT) {
     const int i = a.t_idx[row * a.K + k];
-    const float t = a.t_val[row * a.K + k];
+    const float v = a.t_val[row * a.K + k];
     const bool in = i >= 0 && i < a.V, own = in && i >= c0 && i < c1;
+    const float zk = own || (in && row_z) ? to_f32(z[i]) : -INFINITY;
     bad |= !in && i != -1;
     if (own) {
       const uint32_t bit = 1u << ((i - c0) & 31);
       bad |= (atomicOr(&bits[(i - c0) >> 5], bit) & bit) != 0;
     }
     e.at[k] = in ? i : -1;
-    e.lp[k] = in ? t : -INFINITY;
-    e.z[k] = own || (in && !own_only) ? to_f32(z[i]) : -INFINITY;
-    tm = fmaxf(tm, in ? t : -INFINITY);
+    e.p[k] = in ? v : -INFINITY;
+    e.z[k] = zk;
+    tm = fmaxf(tm, in ? v : -INFINITY);
+    zm = fmaxf(zm, zk);
   }
-  return tm;
-}
-
-// Turns the entries' logits into log-probabilities and probabilities; tm is
-// the largest logit.  Returns sum p and p_r.
-template <int NT>
-__device__ __forceinline__ float2 teacher_mass(const DistillArgs& a, int64_t row, Entries e, float tm, InvT c,
-                                               Exchange<NT / 32>& x, float* red) {
-  const double inv_t = 1.0 / static_cast<double>(a.T);
+  if (some) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      tm = fmaxf(tm, __shfl_xor_sync(0xffffffffu, tm, o));
+      zm = fmaxf(zm, __shfl_xor_sync(0xffffffffu, zm, o));
+    }
+  }
+  if (lane == 0) s.warp[0][warp] = make_float4(tm, zm, 0.f, 0.f);
+  t.bad = __syncthreads_or(bad);
+#pragma unroll
+  for (int w = 0; w < NW; ++w) {
+    tm = fmaxf(tm, s.warp[0][w].x);
+    zm = fmaxf(zm, s.warp[0][w].y);
+  }
+  t.tm = tm;
+  t.ref = ref_of(zm, a.c);
   double lt;
   if (a.t_lse) {
     lt = static_cast<double>(a.t_lse[row]);
   } else {
     float sp = 0.f;
-    for (int k = threadIdx.x; k < a.K; k += NT) sp += exp_diff(e.lp[k], tm, c);
-    lt = static_cast<double>(tm) * inv_t + static_cast<double>(logf(cta_sum<NT / 32>(sp, red)));
+    for (int k = threadIdx.x; k < a.K; k += NT) sp += exp2f(log2_weight(e.p[k], tm, a.c));
+    lt = static_cast<double>(tm) * a.inv_t + static_cast<double>(logf(cta_sum<NW>(sp, s.warp[1])));
+    __syncthreads();
   }
   // ln p_k = t_k / T - Lt, formed in double: where t_lse is given, p_r is a
   // difference from one.  The probabilities' sum is an integer sum for the
   // same reason.
   uint64_t fixed = 0;
+  float es = 0.f, self = 0.f;
   for (int k = threadIdx.x; k < a.K; k += NT) {
-    const double lp = static_cast<double>(e.lp[k]) * inv_t - lt;
+    const double lp = static_cast<double>(e.p[k]) * a.inv_t - lt;
     const float hi = static_cast<float>(lp);
     float p = expf(hi);
     if (hi > -INFINITY) p = fmaf(p, static_cast<float>(lp - static_cast<double>(hi)), p);
-    e.lp[k] = hi;
     e.p[k] = p;
-    fixed += __float2ull_rn(fminf(p, 256.f) * static_cast<float>(kMassOne));
+    fixed += __float2ull_rn(fminf(p, 256.f) * kMassOne);
+    if (row_z && e.at[k] >= 0) {
+      const float x = exponent(e.z[k], a.c, t.ref);
+      es += exp2f(x);
+      if (p > 0.f) self += p * (hi - x * kLn2);
+    }
   }
-  const double total = static_cast<double>(cta_reduce<NT / 32>(fixed, OpSumU64(), x)) / kMassOne;
-  return make_float2(static_cast<float>(total),
-                     a.t_lse && total < 1.0 ? static_cast<float>(1.0 - total) : 0.f);
+  if (some) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      fixed += __shfl_xor_sync(0xffffffffu, fixed, o);
+      es += __shfl_xor_sync(0xffffffffu, es, o);
+      self += __shfl_xor_sync(0xffffffffu, self, o);
+    }
+  }
+  if (lane == 0) {
+    s.warp_mass[warp] = fixed;
+    s.warp[1][warp] = make_float4(es, self, 0.f, 0.f);
+  }
+  __syncthreads();
+  fixed = 0;
+  t.es = 0.f;
+  t.self = 0.f;
+#pragma unroll
+  for (int w = 0; w < NW; ++w) {
+    fixed += s.warp_mass[w];
+    t.es += s.warp[1][w].x;
+    t.self += s.warp[1][w].y;
+  }
+  // in units of 2^-40: one minus the sum, exactly
+  const int64_t rest = (static_cast<int64_t>(1) << 40) - static_cast<int64_t>(fixed);
+  const float mass = static_cast<float>(fixed) * (1.f / kMassOne);
+  t.pr = a.t_lse && rest > 0 ? static_cast<float>(rest) * (1.f / kMassOne) : 0.f;
+  t.P = mass + t.pr;
+  return t;
 }
 
-// What the row's gradient needs: the maximum and exponential sum over the row
-// (m, E) and outside S (mr, Er).  E = 0 stands for a row without a gradient.
+// What the row's gradient needs: reference and sum of 2^(x - reference) over
+// the row (m, E) and outside S (mr, Er).  E = 0 stands for a row without a
+// gradient.
 struct RowSums {
   float m, E, mr, Er;
 };
 
-// The row's sums from those outside S, and its loss (rank 0's threads).
-template <int NT>
-__device__ __forceinline__ RowSums join_entries(const DistillArgs& a, int64_t row, Entries e, float2 mass, float mr,
-                                                float Er, float w, InvT c, bool first, float* red) {
+// Joins the sums outside S with the listed entries'; thread 0 of the row's
+// first CTA writes the loss.
+__device__ __forceinline__ RowSums join_row(const DistillArgs& a, int64_t row, const Teacher& t, float mr, float Er,
+                                            float w, bool writes) {
   RowSums s;
   s.mr = mr;
   s.Er = Er;
-  float zm = -INFINITY;
-  for (int k = threadIdx.x; k < a.K; k += NT) zm = fmaxf(zm, e.z[k]);
-  s.m = fmaxf(cta_max<NT / 32>(zm, red), mr);
-  float es = 0.f;
-  for (int k = threadIdx.x; k < a.K; k += NT)
-    if (e.at[k] >= 0) es += exp_diff(e.z[k], s.m, c);
+  // a part without a finite logit does not set the reference
+  s.m = t.es > 0.f && Er > 0.f ? fmaxf(t.ref, mr) : (Er > 0.f ? mr : t.ref);
+  s.E = t.es * exp2f(t.ref - s.m) + Er * exp2f(mr - s.m);
   // a row without any finite logit has no distribution
-  es = cta_sum<NT / 32>(es, red);
-  s.E = s.m == -INFINITY ? NAN : es + Er * exp_diff(mr, s.m, c);
-  if (first) {
-    const float log_e = logf(s.E);
-    float l = 0.f;
-    for (int k = threadIdx.x; k < a.K; k += NT) {
-      const float lp = e.lp[k];
-      if (lp > -INFINITY) l += e.p[k] * (lp - ((e.z[k] - s.m) / a.T - log_e));
-    }
-    l = cta_sum<NT / 32>(l, red);
-    if (mass.y > 0.f) l += mass.y * (logf(mass.y) - ((mr - s.m) / a.T + logf(s.Er) - log_e));
-    if (threadIdx.x == 0) {
-      a.loss[row] = w * l;
-      if (a.stats) a.stats[row] = make_float4(s.m, s.E, s.mr, s.Er);
-    }
+  if (s.E == 0.f) s.E = NAN;
+  if (writes) {
+    const float log_e = log2f(s.E);
+    // sum p (ln p - ln q), ln q = ln 2 (x - m - log2 E)
+    float l = t.self + (t.P - t.pr) * (log_e + (s.m - t.ref)) * kLn2;
+    if (t.pr > 0.f) l += t.pr * (logf(t.pr) - (log2f(Er) + (mr - s.m) - log_e) * kLn2);
+    a.loss[row] = w * l;
+    if (a.stats) a.stats[row] = make_float4(s.m, s.E, s.mr, s.Er);
   }
   return s;
 }
 
-// Factor of exp((z_j - mr) / T) outside S.
-__device__ __forceinline__ float outside_factor(const RowSums& s, float2 mass, float g, InvT c) {
-  return s.Er > 0.f ? g * ((mass.x + mass.y) * exp_diff(s.mr, s.m, c) / s.E - mass.y / s.Er) : 0.f;
+__device__ __forceinline__ void leave_out(const DistillArgs& a, int64_t row, bool bad) {
+  a.loss[row] = bad ? NAN : 0.f;
+  if (a.stats) a.stats[row] = make_float4(0.f, 0.f, 0.f, 0.f);
+}
+
+// Factor of 2^(x_j - mr) outside S.
+__device__ __forceinline__ float outside_factor(const RowSums& s, const Teacher& t, float g) {
+  return s.Er > 0.f ? g * (t.P * exp2f(s.mr - s.m) / s.E - t.pr / s.Er) : 0.f;
 }
 
 // Gradients of the listed entries in [c0, c1).
 template <typename T, int NT>
-__device__ __forceinline__ void listed_gradients(T* dz, int K, Entries e, int64_t c0, int64_t c1, const RowSums& s,
-                                                 float2 mass, float g, InvT c) {
-  const float f = (mass.x + mass.y) / s.E;
-  for (int k = threadIdx.x; k < K; k += NT) {
+__device__ __forceinline__ void listed_gradients(const DistillArgs& a, T* dz, Entries e, int64_t c0, int64_t c1,
+                                                 const RowSums& s, const Teacher& t, float g) {
+  const float f = t.P / s.E;
+  for (int k = threadIdx.x; k < a.K; k += NT) {
     const int i = e.at[k];
-    if (i >= c0 && i < c1) dz[i] = from_f32<T>(g * (f * exp_diff(e.z[k], s.m, c) - e.p[k]));
+    if (i >= c0 && i < c1) dz[i] = from_f32<T>(g * (f * exp2f(exponent(e.z[k], a.c, s.m)) - e.p[k]));
   }
 }
 
@@ -273,15 +345,15 @@ __device__ __forceinline__ void write_part(const Part<T>& q, const T* buf, T* dz
 template <typename T, int NT, bool kBackward>
 __global__ void __launch_bounds__(NT, NT == 256 ? 5 : 2) distill_kernel(const DistillArgs a, const int parts,
                                                                        const uint32_t part_bytes) {
-  constexpr int NW = NT / 32;
+  constexpr int NW = NT / 32, kPer = Pack<T>::kPer;
   extern __shared__ __align__(16) uint8_t raw[];
   Shared<NW>& s = *reinterpret_cast<Shared<NW>*>(raw);
   T* buf = reinterpret_cast<T*>(raw + sizeof(Shared<NW>));
   uint8_t* after = raw + sizeof(Shared<NW>) + part_bytes;
   const Entries e = entries_at(after, a.K);
-  uint32_t* bits = reinterpret_cast<uint32_t*>(after + ((static_cast<size_t>(a.K) * 16 + 15) & ~size_t(15)));
-  const int64_t row = blockIdx.x / parts;
-  const int part = static_cast<int>(blockIdx.x % parts);
+  uint32_t* bits = reinterpret_cast<uint32_t*>(after + entries_bytes(a.K));
+  const int64_t row = blockIdx.x >> (31 - __clz(parts));
+  const int part = static_cast<int>(blockIdx.x & (parts - 1));
   const T* z = static_cast<const T*>(a.logits) + row * a.ld;
   T* dz = a.dlogits ? static_cast<T*>(a.dlogits) + row * a.ldd : nullptr;
   Part<T> q;
@@ -297,86 +369,84 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 5 : 2) distill_kernel(const Di
   pdl_wait();
   q.load(z, buf, &s.bar);
   const float w = a.weight ? a.weight[row] : 1.f;
-  const InvT c = inv_temperature(a.T);
-  bool bad = false;
-  float tm = list_entries<T, NT>(a, row, z, c0, c1, kBackward, e, bits, bad);
-  tm = cta_max<NW>(tm, s.red);
-  const float2 mass = teacher_mass<NT>(a, row, e, tm, c, s.x, s.red);
+  const Teacher t = read_teacher<T, NT>(a, row, z, c0, c1, !kBackward, e, bits, s);
   mbar_wait(&s.bar, 0, a.status);
-  bad = __syncthreads_or(bad);
-  T* body = buf + q.off;
+  __syncthreads();
   for (int k = threadIdx.x; k < a.K; k += NT) {
     const int i = e.at[k];
-    if (i >= c0 && i < c1) body[i - c0] = from_f32<T>(-INFINITY);
+    if (i >= c0 && i < c1) buf[q.off + i - c0] = from_f32<T>(-INFINITY);
   }
+  __syncthreads();
   RowSums r;
   if (!kBackward) {
     // maximum and exponential sum of the part, relative to its own maximum
-    __syncthreads();
     const uint4* src = reinterpret_cast<const uint4*>(buf);
     uint32_t mx = Pack<T>::kNegInf;
     for (int j = threadIdx.x; j < q.packs; j += NT) {
       const uint4 v = src[j];
       mx = Pack<T>::max2(mx, Pack<T>::max2(Pack<T>::max2(v.x, v.y), Pack<T>::max2(v.z, v.w)));
     }
-    float t[Pack<T>::kPer];
-    Pack<T>::open(mx, t);
-    float pm = t[0];
+    float v[kPer];
+    Pack<T>::open(mx, v);
+    float pm = v[0];
 #pragma unroll
-    for (int h = 1; h < Pack<T>::kPer; ++h) pm = fmaxf(pm, t[h]);
-    pm = cta_max<NW>(pm, s.red);
-    const float ref = pm == -INFINITY ? 0.f : pm;
+    for (int h = 1; h < kPer; ++h) pm = fmaxf(pm, v[h]);
+    float ref = ref_of(cta_max<NW>(pm, s.warp[0]), a.c);
     float sum = 0.f;
-    for (int j = threadIdx.x; j < q.packs; j += NT) {
-      const uint4 v = src[j];
-      const uint32_t in[4] = {v.x, v.y, v.z, v.w};
+    with_weight(a.c, ref, [&](auto weight) {
+      for (int j = threadIdx.x; j < q.packs; j += NT) {
+        const uint4 y = src[j];
+        const uint32_t in[4] = {y.x, y.y, y.z, y.w};
+        float some = 0.f;
 #pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        Pack<T>::open(in[x], t);
+        for (int x = 0; x < 4; ++x) {
+          Pack<T>::open(in[x], v);
 #pragma unroll
-        for (int h = 0; h < Pack<T>::kPer; ++h) sum += fast_exp2((t[h] - ref) * c.hi);
+          for (int h = 0; h < kPer; ++h) some += weight(v[h]);
+        }
+        sum += some;
       }
-    }
-    sum = cta_sum<NW>(sum, s.red);
+    });
+    sum = cta_sum<NW>(sum, s.warp[1]);
+    bool bad = t.bad;
     if (parts > 1) {
       asm volatile("barrier.cluster.wait.aligned;" ::: "memory");  // the other CTAs have started
-      if (threadIdx.x < parts) *peer(&s.part[part], threadIdx.x) = make_float4(pm, sum, bad ? 1.f : 0.f, 0.f);
+      if (threadIdx.x < parts) *peer(&s.part[part], threadIdx.x) = make_float4(ref, sum, bad ? 1.f : 0.f, 0.f);
       cluster_sync_all(parts);
-      pm = -INFINITY;
+      // references are finite, and below every other where nothing is left
+      ref = -kRefMax;
       for (int o = 0; o < parts; ++o) {
-        pm = fmaxf(pm, s.part[o].x);
+        ref = fmaxf(ref, s.part[o].x);
         bad |= s.part[o].z != 0.f;
       }
       sum = 0.f;
-      for (int o = 0; o < parts; ++o) sum += s.part[o].y * exp_diff(s.part[o].x, pm, c);
+      for (int o = 0; o < parts; ++o) sum += s.part[o].y * exp2f(s.part[o].x - ref);
     }
-    const bool out = bad || w == 0.f || tm == -INFINITY;
-    if (out) {
+    r = RowSums{0.f, 0.f, 0.f, 0.f};
+    if (bad || w == 0.f || t.tm == -INFINITY) {
       if (part == 0 && threadIdx.x == 0) {
-        a.loss[row] = bad ? NAN : 0.f;
-        if (a.stats) a.stats[row] = make_float4(0.f, 0.f, 0.f, 0.f);
+        leave_out(a, row, bad);
         if (bad) atomicOr(a.status, kDevBadToken);
       }
-      r.E = 0.f;
     } else if (dz || part == 0) {
-      r = join_entries<NT>(a, row, e, mass, pm, sum, w, c, part == 0, s.red);
+      r = join_row(a, row, t, ref, sum, w, part == 0 && threadIdx.x == 0);
     }
     if (!dz) return;
   } else {
-    if (bad && threadIdx.x == 0) atomicOr(a.status, kDevBadToken);
+    if (t.bad && threadIdx.x == 0) atomicOr(a.status, kDevBadToken);
     const float4 st = a.stats[row];
-    r = RowSums{st.x, bad || w == 0.f ? 0.f : st.y, st.z, st.w};
-    __syncthreads();
+    r = RowSums{st.x, t.bad || w == 0.f ? 0.f : st.y, st.z, st.w};
   }
   if (r.E == 0.f) {  // left out or refused
     write_part<T, NT>(q, buf, dz, [](float) { return 0.f; });
     return;
   }
-  const float g = w / a.T, f = outside_factor(r, mass, g, c);
-  const float ref = r.mr == -INFINITY ? 0.f : r.mr, ch = c.hi;
-  write_part<T, NT>(q, buf, dz, [=](float v) { return f * fast_exp2((v - ref) * ch); });
+  const float g = w / a.T, f = outside_factor(r, t, g);
+  with_weight(a.c, r.mr, [&](auto weight) {
+    write_part<T, NT>(q, buf, dz, [=](float v) { return f * weight(v); });
+  });
   __syncthreads();
-  listed_gradients<T, NT>(dz, a.K, e, c0, c1, r, mass, g, c);
+  listed_gradients<T, NT>(a, dz, e, c0, c1, r, t, g);
 }
 
 // A row too long for the shared memory of a cluster: the same sums by reading
@@ -390,8 +460,7 @@ __global__ void __launch_bounds__(kLongThr) distill_long_kernel(const DistillArg
   extern __shared__ __align__(16) uint8_t raw[];
   Shared<NW>& s = *reinterpret_cast<Shared<NW>*>(raw);
   const Entries e = entries_at(raw + sizeof(Shared<NW>), a.K);
-  uint32_t* bits = reinterpret_cast<uint32_t*>(raw + sizeof(Shared<NW>) +
-                                               ((static_cast<size_t>(a.K) * 16 + 15) & ~size_t(15)));
+  uint32_t* bits = reinterpret_cast<uint32_t*>(raw + sizeof(Shared<NW>) + entries_bytes(a.K));
   pdl_wait();
   const uint32_t rank = cluster_rank(), size = cluster_size();
   const int64_t row = blockIdx.x / size;
@@ -401,41 +470,33 @@ __global__ void __launch_bounds__(kLongThr) distill_long_kernel(const DistillArg
   const int64_t c0 = chunk * rank < a.V ? chunk * rank : a.V, c1 = c0 + chunk < a.V ? c0 + chunk : a.V;
   int turn = 0;
   const float w = a.weight ? a.weight[row] : 1.f;
-  const InvT c = inv_temperature(a.T);
   for (int64_t i = threadIdx.x; i < (c1 - c0 + 31) / 32; i += NT) bits[i] = 0;
   __syncthreads();
-  bool bad = false;
-  float tm = list_entries<T, NT>(a, row, z, c0, c1, false, e, bits, bad);
-  cluster_sync_all(size);
-  bad = cluster_reduce<NW>(bad, OpMaxU64(), s.x, rank, size, turn) != 0;
-  tm = cta_max<NW>(tm, s.red);
-  const float2 mass = teacher_mass<NT>(a, row, e, tm, c, s.x, s.red);
+  const Teacher t = read_teacher<T, NT>(a, row, z, c0, c1, true, e, bits, s);
+  cluster_sync_all(size);  // the other CTAs have started
+  const bool bad = cluster_reduce<NW>(t.bad, OpMaxU64(), s.x, rank, size, turn) != 0;
   auto outside = [&](int64_t i) { return !(bits[(i - c0) >> 5] >> ((i - c0) & 31) & 1); };
-  RowSums r;
-  if (bad || w == 0.f || tm == -INFINITY) {
+  RowSums r{0.f, 0.f, 0.f, 0.f};
+  if (bad || w == 0.f || t.tm == -INFINITY) {
     if (rank == 0 && threadIdx.x == 0) {
-      if (!backward) a.loss[row] = bad ? NAN : 0.f;
-      if (!backward && a.stats) a.stats[row] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (!backward) leave_out(a, row, bad);
       if (bad) atomicOr(a.status, kDevBadToken);
     }
-    r.E = 0.f;
   } else if (!backward) {
     float v = -INFINITY;
     for (int64_t i = c0 + threadIdx.x; i < c1; i += NT)
       if (outside(i)) v = fmaxf(v, to_f32(z[i]));
-    v = cta_max<NW>(v, s.red);
-    const float mr = key_to_value(static_cast<uint32_t>(
-        cluster_reduce<NW>(max(value_key(v), 0x007FFFFFu), OpMaxU64(), s.x, rank, size, turn)));
-    const float ref = mr == -INFINITY ? 0.f : mr;
+    const uint64_t key = cluster_reduce<NW>(max(value_key(v), 0x007FFFFFu), OpMaxU64(), s.x, rank, size, turn);
+    const float ref = ref_of(key_to_value(static_cast<uint32_t>(key)), a.c);
     float sum = 0.f;
     for (int64_t i = c0 + threadIdx.x; i < c1; i += NT)
-      if (outside(i)) sum += exp_diff(to_f32(z[i]), ref, c);
-    sum = cta_sum<NW>(sum, s.red);
+      if (outside(i)) sum += fast_exp2(exponent(to_f32(z[i]), a.c, ref));
+    sum = cta_sum<NW>(sum, s.warp[0]);
     if (threadIdx.x < size) peer(&s.part[rank], threadIdx.x)->x = sum;
     cluster_sync_all(size);
     sum = 0.f;
     for (uint32_t o = 0; o < size; ++o) sum += s.part[o].x;
-    r = join_entries<NT>(a, row, e, mass, mr, sum, w, c, rank == 0, s.red);
+    r = join_row(a, row, t, ref, sum, w, rank == 0 && threadIdx.x == 0);
   } else {
     const float4 st = a.stats[row];
     r = RowSums{st.x, st.y, st.z, st.w};
@@ -445,10 +506,10 @@ __global__ void __launch_bounds__(kLongThr) distill_long_kernel(const DistillArg
     for (int64_t i = c0 + threadIdx.x; i < c1; i += NT) dz[i] = from_f32<T>(0.f);
     return;
   }
-  const float g = w / a.T, f = outside_factor(r, mass, g, c);
+  const float g = w / a.T, f = outside_factor(r, t, g);
   for (int64_t i = c0 + threadIdx.x; i < c1; i += NT)
-    if (outside(i)) dz[i] = from_f32<T>(f * exp_diff(to_f32(z[i]), r.mr == -INFINITY ? 0.f : r.mr, c));
-  listed_gradients<T, NT>(dz, a.K, e, c0, c1, r, mass, g, c);
+    if (outside(i)) dz[i] = from_f32<T>(f * fast_exp2(exponent(to_f32(z[i]), a.c, r.mr)));
+  listed_gradients<T, NT>(a, dz, e, c0, c1, r, t, g);
 }
 
 template <typename T, int NT, bool kBackward>
@@ -495,7 +556,9 @@ cudaError_t launch(const DistillArgs& a, int64_t rows, bool backward, cudaStream
 
 }  // namespace
 
-cudaError_t distill(const DistillArgs& a, int dtype, int64_t rows, bool backward, cudaStream_t st) {
+cudaError_t distill(DistillArgs a, int dtype, int64_t rows, bool backward, cudaStream_t st) {
+  a.c = static_cast<float>(1.4426950408889634 / static_cast<double>(a.T));
+  a.inv_t = 1.0 / static_cast<double>(a.T);
   if (dtype == 0) return launch<float>(a, rows, backward, st);
   if (dtype == 1) return launch<__half>(a, rows, backward, st);
   return launch<__nv_bfloat16>(a, rows, backward, st);

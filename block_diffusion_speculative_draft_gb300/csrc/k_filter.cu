@@ -95,7 +95,7 @@ struct Row {
   int64_t c0, c1;  // read
   uint32_t rank, size;
   float m;         // the row's maximum
-  InvT c;          // log2(e) / temperature
+  float c;         // log2(e) / temperature
   float scale;     // weights become integers by this power of two
   int turn;
 

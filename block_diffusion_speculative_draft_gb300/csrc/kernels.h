@@ -263,12 +263,14 @@ struct DistillArgs {
   float T;
   const float* weight;  // nullable; the upstream gradient in the backward call
   float* loss;          // null in the backward call
-  float4* stats;        // nullable: (m, E, m_rest, E_rest); input of the backward call
+  float4* stats;        // nullable: the row's sums (RowSums); input of the backward call
   void* dlogits;        // nullable
   int64_t ldd;
   int* status;
+  float c;       // log2(e) / T and 1 / T, set by the launcher
+  double inv_t;
 };
-cudaError_t distill(const DistillArgs& a, int dtype, int64_t rows, bool backward, cudaStream_t st);
+cudaError_t distill(DistillArgs a, int dtype, int64_t rows, bool backward, cudaStream_t st);
 
 // Allocation-free variant of verify_accept: scratch lives in a fixed device
 // array of kNoAllocScratchBytes inside the library (k_small.cu).

@@ -55,26 +55,17 @@ __device__ __forceinline__ uint64_t double_key(double v) {
   return (b >> 63) ? ~b : (b | 0x8000000000000000ull);
 }
 
-// log2(e) / T as a float pair: an exponent formed with both parts carries
-// little more than the rounding of its own last addition.
-struct InvT {
-  float hi, lo;
-};
-__device__ __forceinline__ InvT inv_temperature(float t) {
-  const double c = 1.4426950408889634 / static_cast<double>(t);
-  InvT r;
-  r.hi = static_cast<float>(c);
-  r.lo = static_cast<float>(c - static_cast<double>(r.hi));
-  return r;
-}
+// log2(e) / T.  Exponents are formed in units of log2: x = fma(z, c, -ref) with
+// ref a float near c times a maximum.  The fused product is exact, so x carries
+// one rounding of its own size, c's rounding counts as a temperature 2^-24
+// off, and ref is a known number, not a rounded one, wherever sums with
+// different references meet.
+__device__ __forceinline__ float inv_temperature(float t) { return 1.4426950408889634f / t; }
+// Logits at the type's end (its lowest value as a mask) would overflow z * c;
+// exponents are held within this bound.
+constexpr float kRefMax = 1e30f;
 // log2 of exp((v - m) / T) for v <= m: 0 where both are the same infinity.
-// A difference of -inf is brought to -1e38, which the pair's second part
-// cannot turn into inf - inf; a NaN stays.
-__device__ __forceinline__ float log2_weight(float v, float m, InvT c) {
-  float d;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(v - m), "f"(-1e38f));
-  return v == m ? 0.f : fmaf(d, c.lo, d * c.hi);
-}
+__device__ __forceinline__ float log2_weight(float v, float m, float c) { return v == m ? 0.f : (v - m) * c; }
 
 __device__ __forceinline__ float fast_exp2(float x) {  // below 2^-126: 0
   float y;
@@ -144,10 +135,11 @@ struct Part {
   int64_t first;
   int n, off, packs;
 
-  __device__ __forceinline__ void cut(const T* row, int64_t V, int part, int parts) {
+  __device__ __forceinline__ void cut(const T* row, int64_t V, int part, int parts) {  // parts: a power of two
     const int o = static_cast<int>((reinterpret_cast<uintptr_t>(row) & 15) / sizeof(T));
     const int64_t all = (V + o + kE - 1) / kE;
-    const int64_t p0 = all * part / parts, p1 = all * (part + 1) / parts;
+    const int lg = 31 - __clz(parts);
+    const int64_t p0 = (all * part) >> lg, p1 = (all * (part + 1)) >> lg;
     const int64_t e0 = p0 * kE - o > 0 ? p0 * kE - o : 0;
     const int64_t e1 = p1 * kE - o < V ? p1 * kE - o : V;
     first = e0;

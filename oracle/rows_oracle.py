@@ -120,7 +120,8 @@ def distill(z, t_val, t_idx, T: float = 1.0, t_lse: Optional[float] = None, weig
     t = t_val[listed] / T
     if weight == 0 or not np.any(t > -np.inf):
         return 0.0, np.zeros(V)
-    zt = z / T
+    m = z.max() if np.isfinite(z.max()) else 0.0  # softmax does not see a shift; sums keep their precision
+    zt = (z - m) / T
     L = _lse(zt)
     lp = t - (_lse(t) if t_lse is None else float(t_lse))
     p = np.exp(lp)

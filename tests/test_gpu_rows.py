@@ -534,6 +534,25 @@ def test_distill_rows_left_out_and_refused():
     assert not back[:6].any() and np.abs(back[7].cpu().numpy() - rg).max() < 1e-6
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+def test_distill_with_masks_of_the_lowest_value(dtype):
+    V, K = 3001, 3
+    low = float(torch.finfo(DT[dtype]).min)
+    z = np.full((3, V), low)
+    z[0, :40] = np.linspace(0, 2, 40)         # a masked tail: probability 0
+    z[2, [5, 9, 2000]] = [1.0, 2.0, 0.5]      # all but the listed ones masked
+    tv, ti = np.array([[1.0, 0.5, 0.2]] * 3, np.float32), np.array([[5, 9, 2000], [5, 9, 2000], [5, 9, 2000]], np.int32)
+    ti[0, 2] = 30
+    zt = _padded(z, dtype, 1)
+    loss, dz = torch.empty(3, device=DEV), torch.empty((3, V), dtype=DT[dtype], device=DEV)
+    api.dflash_distill_loss(zt, _dev(tv, np.float32), _dev(ti, np.int32), loss, temperature=0.5, dlogits=dz)
+    eps = {"f32": 2.0 ** -24, "f16": 2.0 ** -11, "bf16": 2.0 ** -8}[dtype]
+    for r in range(3):                        # row 1: nothing but the mask is uniform
+        rl, rg = RO.distill(_host(zt)[r], tv[r], ti[r], 0.5)
+        assert abs(float(loss[r]) - rl) < 1e-5 * (1 + abs(rl)), r
+        assert np.abs(_host(dz)[r] - rg).max() < 1e-5 + 2 * eps, r
+
+
 def test_distill_keeps_the_rest_when_the_student_is_sure():
     # q outside the listed tokens near 1e-30: far below what 1 - sum of q keeps
     V = 5000
