@@ -31,7 +31,8 @@ constexpr int kGroups = 8;            // groups of entries per thread whose maxi
 constexpr int kGroupBins = 256;       // bins of the groups' maxima
 constexpr int kLineBins = 1024;       // bins of the weights, linear in the logit
 constexpr int kDevBadParam = 0x8;
-constexpr int kFewTarget = 128;       // entries the short list aims at where top-k does not say
+constexpr int kFewTarget = 96;        // entries the short list aims at where top-k does not say
+constexpr int kQuick = 128;           // lists up to this length are ranked, longer ones sorted
 constexpr float kLn2 = 0.6931471805599453f;
 
 // What one row asks for.
@@ -75,7 +76,7 @@ struct alignas(16) Shared {
   uint32_t highest[kMaxCluster], lowest[kMaxCluster];  // of each CTA's groups' maxima
   double mass[kMaxCluster];          // each CTA's sum of weights
   uint64_t own_mass;
-  uint32_t own_count, taken;
+  uint32_t own_count, taken, queued;
   uint32_t groups[kGroupBins];
   union {
     uint64_t list[kCap];  // places; complete in rank 0
@@ -85,6 +86,10 @@ struct alignas(16) Shared {
     } bin;
   };
   uint32_t line[kLineBins];
+  ulonglong2 entry[kQuick];          // a quick list's places and weights
+  uint64_t half_before[kQuick];
+  uint32_t half_rank[kQuick];
+  uint64_t join[NT / 32][3];
 };
 
 // One row as a cluster sees it.  Each CTA reads its part of the row from
@@ -425,42 +430,47 @@ __device__ bool join_scan(Row<T, NT>& r, Shared<NT, kCap>& s, const Scan<T, NT>&
   return hi != 0;
 }
 
-// Adds this thread's entries that `take` accepts to rank 0's list and counts
-// them in own_count (own_mass: their weights, if wanted).  Only groups whose
-// maximum reaches t are read again.
-template <typename T, int NT, int kCap, typename F>
+// Puts the places of the entries at or above t on rank 0's list and counts them
+// in own_count (own_mass: their weights, if wanted).  Only groups whose maximum
+// reaches t are read again: their numbers go to a queue, whose packs all
+// threads share, so that one round trip to L2 serves most rows.
+template <typename T, int NT, int kCap>
 __device__ __forceinline__ void list_entries(const Row<T, NT>& r, Shared<NT, kCap>& s, const Scan<T, NT>& sc, float t,
-                                             bool want_mass, F take) {
+                                             bool want_mass) {
   constexpr int kE = Row<T, NT>::kE;
+  static_assert(NT * kGroups * sizeof(uint16_t) <= sizeof(s.line) && NT * kGroups <= 65536, "the queue fits");
+  uint16_t* queue = reinterpret_cast<uint16_t*>(s.line);
+#pragma unroll
+  for (int x = 0; x < kGroups; ++x)
+    if (sc.group[x] >= t && sc.group[x] > -INFINITY)
+      queue[atomicAdd(&s.queued, 1u)] = static_cast<uint16_t>(threadIdx.x + x * NT);
+  __syncthreads();
   const int lane = threadIdx.x & 31;
   uint32_t* taken = peer(&s.taken, 0);
   uint64_t* list = peer(s.list, 0);
-#pragma unroll 1
-  for (int x = 0; x < kGroups; ++x) {
-    float top = sc.group[0];
+  const uint32_t deep = (r.part.packs + kGroups * NT - 1) / (kGroups * NT), units = s.queued * deep;
+  for (uint32_t y = threadIdx.x; y < units; y += NT) {
+    const uint32_t g = y / deep;
+    const int j = queue[g] + static_cast<int>(y - g * deep) * (kGroups * NT);
+    if (j >= r.part.packs) continue;
+    const uint4 w = r.pack(j);
+    if (!(Row<T, NT>::max_of(Row<T, NT>::max_pack(w)) >= t)) continue;
+    float v[kE];
+    Row<T, NT>::open_pack(w, v);
+    const int64_t i = r.index_of(j);
 #pragma unroll
-    for (int y = 1; y < kGroups; ++y) top = y == x ? sc.group[y] : top;
-    if (!(top >= t) || !(top > -INFINITY)) continue;
-    for (int j = threadIdx.x + x * NT; j < r.part.packs; j += kGroups * NT) {
-      const uint4 w = r.pack(j);
-      if (!(Row<T, NT>::max_of(Row<T, NT>::max_pack(w)) >= t)) continue;
-      float v[kE];
-      Row<T, NT>::open_pack(w, v);
-      const int64_t i = r.index_of(j);
-#pragma unroll
-      for (int h = 0; h < kE; ++h) {
-        if (v[h] >= t && v[h] > -INFINITY && take(v[h])) {
-          const unsigned act = __activemask();
-          const int first = __ffs(act) - 1;
-          uint32_t base = 0;
-          if (lane == first) {
-            base = atomicAdd(taken, static_cast<uint32_t>(__popc(act)));
-            atomicAdd(&s.own_count, static_cast<uint32_t>(__popc(act)));
-          }
-          base = __shfl_sync(act, base, first) + __popc(act & ((1u << lane) - 1));
-          if (base < kCap) list[base] = place_of(value_key(v[h]), static_cast<uint32_t>(i + h));
-          if (want_mass) atomicAdd(reinterpret_cast<unsigned long long*>(&s.own_mass), r.weight(v[h]));
+    for (int h = 0; h < kE; ++h) {
+      if (v[h] >= t && v[h] > -INFINITY) {
+        const unsigned act = __activemask();
+        const int first = __ffs(act) - 1;
+        uint32_t base = 0;
+        if (lane == first) {
+          base = atomicAdd(taken, static_cast<uint32_t>(__popc(act)));
+          atomicAdd(&s.own_count, static_cast<uint32_t>(__popc(act)));
         }
+        base = __shfl_sync(act, base, first) + __popc(act & ((1u << lane) - 1));
+        if (base < kCap) list[base] = place_of(value_key(v[h]), static_cast<uint32_t>(i + h));
+        if (want_mass) atomicAdd(reinterpret_cast<unsigned long long*>(&s.own_mass), r.weight(v[h]));
       }
     }
   }
@@ -538,7 +548,7 @@ __device__ bool short_list(Row<T, NT>& r, Shared<NT, kCap>& s, const Scan<T, NT>
       if (V > kCap) return false;
     }
   }
-  list_entries(r, s, sc, t, want_mass, [](float) { return true; });
+  list_entries(r, s, sc, t, want_mass);
   close_list(r, s, count, mass);
   *bound = t;
   return *count <= kCap;
@@ -668,6 +678,119 @@ __device__ int pick_listed(const Row<T, NT>& r, Shared<NT, kCap>& s, const float
   const uint64_t dbest = cta_reduce<NT / 32>(dk, OpMaxU64(), s.x);
   const uint64_t low = close && dk == dbest ? 0xFFFFFFFFull - v : 0ull;
   return static_cast<int>(0xFFFFFFFFull - cta_reduce<NT / 32>(low, OpMaxU64(), s.x));
+}
+
+// What a list says of its row (rank 0's threads).
+struct Verdict {
+  double mass;   // sum of the kept weights
+  uint64_t cut;  // place of the last entry kept
+  int tok;       // Gumbel maximum of the kept entries but `drop` (u given)
+};
+
+// Filters a short list and draws from it.  Up to kQuick entries, each one's
+// rank and the sum of the weights before it come from comparing it with all
+// others (two threads an entry), which needs neither a sort nor a scan; longer
+// lists are sorted.  above, whole: as in filter_list.
+template <typename T, int NT, int kCap>
+__device__ __noinline__ Verdict settle_list(const Row<T, NT>& r, Shared<NT, kCap>& s, const Ask& q, int n, double above,
+                                            double whole, const float* u, int drop) {
+  Verdict out;
+  if (n > kQuick) {
+    sort_list<NT>(s.list, n);
+    const int kept = filter_list(r, s, q, n, above, whole, &out.mass);
+    out.cut = s.list[kept - 1];
+    out.tok = u ? pick_listed(r, s, u, kept, drop, q.T) : -1;
+    return out;
+  }
+  static_assert(NT == 2 * kQuick, "two threads an entry");
+  const int e = threadIdx.x & (kQuick - 1), half = threadIdx.x / kQuick;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint64_t place = e < n ? s.list[e] : 0;
+  const float v = key_to_value(static_cast<uint32_t>(place >> 32));
+  const uint32_t at = place_index(place);
+  uint64_t w = 0;
+  float ue = 0.f;
+  if (half == 0 && e < n) {
+    if (u && !q.greedy) ue = u[at];
+    w = r.weight(v);
+    s.entry[e] = make_ulonglong2(place, w);
+  }
+  __syncthreads();
+  uint32_t rank = 0;
+  uint64_t before = 0;
+  const int i1 = half ? n : (n < kQuick / 2 ? n : kQuick / 2);
+  for (int i = half * (kQuick / 2); i < i1; ++i) {
+    const ulonglong2 o = s.entry[i];
+    if (o.x > place) {
+      ++rank;
+      before += o.y;
+    }
+  }
+  if (half == 1) {
+    s.half_rank[e] = rank;
+    s.half_before[e] = before;
+  }
+  __syncthreads();
+  const bool mine = half == 0 && e < n;
+  if (mine) {
+    rank += s.half_rank[e];
+    before += s.half_before[e];
+  }
+  const bool in_k = mine && rank < static_cast<uint32_t>(q.k);
+  double need = static_cast<double>(q.p) * whole * static_cast<double>(r.scale);
+  if (q.p < 1.f && whole == 0.0) {  // top-p of what top-k keeps
+    uint64_t x = in_k ? w : 0;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    if (lane == 0) s.join[warp][0] = x;
+    __syncthreads();
+    x = 0;
+#pragma unroll
+    for (int y = 0; y < kQuick / 32; ++y) x += s.join[y][0];
+    need = static_cast<double>(q.p) * static_cast<double>(x);
+    __syncthreads();
+  }
+  const double over = above * static_cast<double>(r.scale);
+  const float bound = q.mp > 0.f ? min_p_bound(r.m, q) : -INFINITY;
+  const bool kept =
+      in_k && (rank == 0 || q.p >= 1.f || over + static_cast<double>(before) < need) && v >= bound;
+  const bool runs = kept && u && !q.greedy && static_cast<int>(at) != drop;
+  const float sc = runs ? fmaf(r.log2w(v), kLn2, gumbel(ue)) : -INFINITY;
+  uint64_t sum = kept ? w : 0, last = kept ? ~place : 0, key = runs ? argmax_key(sc, at) : 0;
+  if (q.greedy && kept && static_cast<int>(at) != drop) key = argmax_key(0.f, at);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    const uint64_t y = __shfl_xor_sync(0xffffffffu, last, o), z = __shfl_xor_sync(0xffffffffu, key, o);
+    last = y > last ? y : last;
+    key = z > key ? z : key;
+  }
+  if (lane == 0) {
+    s.join[warp][0] = sum;
+    s.join[warp][1] = last;
+    s.join[warp][2] = key;
+  }
+  __syncthreads();
+  sum = 0;
+  last = 0;
+  key = 0;
+#pragma unroll
+  for (int y = 0; y < kQuick / 32; ++y) {
+    sum += s.join[y][0];
+    last = s.join[y][1] > last ? s.join[y][1] : last;
+    key = s.join[y][2] > key ? s.join[y][2] : key;
+  }
+  out.mass = above + static_cast<double>(sum) / static_cast<double>(r.scale);
+  out.cut = ~last;
+  out.tok = key ? static_cast<int>(key_index(key)) : -1;
+  const bool close = runs && near_best(sc, key_value(key));
+  if (__syncthreads_count(close) > 1) {
+    const uint64_t dk = close ? double_key(score64(v, r.m, q.T, ue)) : 0ull;
+    const uint64_t best = cta_reduce<NT / 32>(dk, OpMaxU64(), s.x);
+    const uint64_t low = close && dk == best ? 0xFFFFFFFFull - at : 0ull;
+    out.tok = static_cast<int>(0xFFFFFFFFull - cta_reduce<NT / 32>(low, OpMaxU64(), s.x));
+  }
+  return out;
 }
 
 // log2 by the special-function unit (2^-22 of the result; -inf at 0)
@@ -947,11 +1070,11 @@ __device__ __noinline__ uint64_t wide_cut(Row<T, NT>& r, Shared<NT, kCap>& s, co
   return cut;
 }
 
-// Tries the short list for a row's filters; true: rank 0 holds the sorted list,
-// of which it keeps *kept entries (rank 0's threads only know).
+// Tries the short list for a row's filters; true: rank 0's threads have the
+// verdict (with a draw from u, if given).
 template <typename T, int NT, int kCap>
 __device__ bool listed_row(Row<T, NT>& r, Shared<NT, kCap>& s, const Scan<T, NT>& sc, const FilterArgs& a,
-                           const Ask& q, float low, double row_mass, int* kept, double* kept_mass) {
+                           const Ask& q, float low, double row_mass, const float* u, int drop, Verdict* out) {
   int target = 0;
   float t = -INFINITY;
   const bool of_row = q.k >= a.V && q.p < 1.f;  // top-p refers to the whole row
@@ -974,9 +1097,7 @@ __device__ bool listed_row(Row<T, NT>& r, Shared<NT, kCap>& s, const Scan<T, NT>
   if (of_row && static_cast<double>(mass) < static_cast<double>(q.p) * row_mass * static_cast<double>(r.scale) &&
       static_cast<int64_t>(count) < a.V && !(q.mp > 0.f && min_p_bound(r.m, q) >= t))
     return false;
-  if (r.rank != 0) return true;
-  sort_list<NT>(s.list, static_cast<int>(count));
-  *kept = filter_list(r, s, q, static_cast<int>(count), 0.0, of_row ? row_mass : 0.0, kept_mass);
+  if (r.rank == 0) *out = settle_list(r, s, q, static_cast<int>(count), 0.0, of_row ? row_mass : 0.0, u, drop);
   return true;
 }
 
@@ -998,6 +1119,7 @@ __device__ __forceinline__ void start(Shared<NT, kCap>& s, uint32_t size) {
     s.own_mass = 0;
     s.own_count = 0;
     s.taken = 0;
+    s.queued = 0;
   }
   for (int b = threadIdx.x; b < kGroupBins; b += NT) s.groups[b] = 0;
   __syncthreads();
@@ -1030,32 +1152,32 @@ __global__ void __launch_bounds__(kThr, 4) sample_rows_kernel(const FilterArgs a
   int tok = -1;
   float lp = -INFINITY;
   if (q.ok && some) {
-    int n = 0;
-    double mass;
+    Verdict v;
     Best best{-INFINITY, 0.f, -1};
-    if (listed_row(r, s, sc, a, q, low, row_mass, &n, &mass)) {
+    int n = 0;
+    if (listed_row(r, s, sc, a, q, low, row_mass, u, -1, &v)) {
       if (r.rank != 0) return;
-      tok = q.greedy ? static_cast<int>(place_index(s.list[0])) : pick_listed(r, s, u, n, -1, q.T);
+      tok = v.tok;
     } else if (q.k >= a.V && q.p < 1.f && q.mp == 0.f &&
-               deep_top_p(r, s, q, a.V, row_mass, u, &n, &mass, &best)) {
+               deep_top_p(r, s, q, a.V, row_mass, u, &n, &v.mass, &best)) {
       if (r.rank == 0) {
         for (int i = threadIdx.x; i < n; i += kThr) {
           const uint32_t x = place_index(s.list[i]);
-          const float v = key_to_value(static_cast<uint32_t>(s.list[i] >> 32));
-          offer(best, v, static_cast<int>(x), r.log2w(v), u[x]);
+          const float z = key_to_value(static_cast<uint32_t>(s.list[i] >> 32));
+          offer(best, z, static_cast<int>(x), r.log2w(z), u[x]);
         }
       }
       tok = join_best(r, s, u, best, q.T);
     } else {
       uint64_t cut = 1ull << 32;
       if (want_mass && q.p >= 1.f) {
-        mass = row_mass;
+        v.mass = row_mass;
       } else {
-        cut = wide_cut(r, s, a, q, &mass);
+        cut = wide_cut(r, s, a, q, &v.mass);
       }
       tok = q.greedy ? static_cast<int>(place_index(cut)) : pick_row(r, s, u, cut, -1, q.T);
     }
-    if (tok >= 0) lp = log_prob(r, tok, mass);
+    if (tok >= 0) lp = log_prob(r, tok, v.mass);
   }
   if (r.rank == 0 && threadIdx.x == 0) {
     a.tok[row] = tok;
@@ -1093,34 +1215,34 @@ __global__ void __launch_bounds__(kThr, 4) accept_rows_kernel(const FilterArgs a
   out.accept = 0;
   out.tok = -1;
   if (q.ok && some) {
+    const int drop = rr < a.D ? a.draft[j * a.D + rr] : -1;
+    Verdict v;
     int n = 0;
-    double kept;
-    const bool listed = listed_row(r, s, sc, a, q, low, row_mass, &n, &kept);
-    if (listed && r.rank != 0) return;
-    if (listed || (q.k >= a.V && q.p < 1.f && q.mp == 0.f &&
-                   deep_top_p(r, s, q, a.V, row_mass, static_cast<const float*>(nullptr), &n, &kept,
-                              static_cast<Best*>(nullptr)))) {
+    if (listed_row(r, s, sc, a, q, low, row_mass, a.u + j * a.ld_u, drop, &v)) {
       if (r.rank != 0) return;
-      out.cut = s.list[n - 1];
-    } else if (want_mass && q.p >= 1.f) {
-      out.cut = 1ull << 32;
-      kept = row_mass;
+      out.cut = v.cut;
+      out.tok = v.tok;
     } else {
-      out.cut = wide_cut(r, s, a, q, &kept);
-    }
-    int drop = -1;
-    if (rr < a.D) {
-      drop = a.draft[j * a.D + rr];
-      if (drop >= 0 && drop < a.V) {
-        const float v = r.at(drop);
-        const uint32_t key = value_key(v);
-        if (key != 0 && place_of(key, static_cast<uint32_t>(drop)) >= out.cut)
-          out.accept = static_cast<double>(a.u_accept[j * a.D + rr]) <
-                       static_cast<double>(r.weight(v)) / static_cast<double>(r.scale) / kept;
+      out.tok = -2;  // not drawn yet
+      if (q.k >= a.V && q.p < 1.f && q.mp == 0.f &&
+          deep_top_p(r, s, q, a.V, row_mass, static_cast<const float*>(nullptr), &n, &v.mass,
+                     static_cast<Best*>(nullptr))) {
+        if (r.rank != 0) return;
+        out.cut = s.list[n - 1];
+      } else if (want_mass && q.p >= 1.f) {
+        out.cut = 1ull << 32;
+        v.mass = row_mass;
+      } else {
+        out.cut = wide_cut(r, s, a, q, &v.mass);
       }
     }
-    out.tok = -2;  // not drawn yet
-    if (listed && !out.accept) out.tok = pick_listed(r, s, a.u + j * a.ld_u, n, drop, q.T);
+    if (drop >= 0 && drop < a.V) {
+      const float z = r.at(drop);
+      const uint32_t key = value_key(z);
+      if (key != 0 && place_of(key, static_cast<uint32_t>(drop)) >= out.cut)
+        out.accept = static_cast<double>(a.u_accept[j * a.D + rr]) <
+                     static_cast<double>(r.weight(z)) / static_cast<double>(r.scale) / v.mass;
+    }
   }
   if (r.rank == 0 && threadIdx.x == 0) a.cuts[row] = out;
 }
