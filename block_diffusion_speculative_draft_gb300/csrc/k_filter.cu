@@ -74,8 +74,10 @@ struct alignas(16) Shared {
   uint64_t list_mass[kMaxCluster];   // what each CTA put on the list, by weight and by count
   uint32_t list_count[kMaxCluster];
   uint32_t highest[kMaxCluster], lowest[kMaxCluster];  // of each CTA's groups' maxima
-  double mass[kMaxCluster];          // each CTA's sum of weights
+  float mass[kMaxCluster];           // each CTA's sum of weights
   uint64_t own_mass;
+  uint64_t need;                     // top-p keeps entries while the sum before them is below this
+  float bound;                       // min-p's bound on a logit
   uint32_t own_count, taken, queued;
   uint32_t groups[kGroupBins];
   union {
@@ -85,11 +87,13 @@ struct alignas(16) Shared {
       uint32_t count[kBins];
     } bin;
   };
-  uint32_t line[kLineBins];
+  alignas(16) uint32_t line[kLineBins];
   ulonglong2 entry[kQuick];          // a quick list's places and weights
   uint64_t half_before[kQuick];
   uint32_t half_rank[kQuick];
   uint64_t join[NT / 32][3];
+  float val;
+  uint32_t bar;                      // key of the best score seen by any thread of the CTA
 };
 
 // One row as a cluster sees it.  Each CTA reads its part of the row from
@@ -106,6 +110,7 @@ struct Row {
   float m;             // the row's maximum
   float c;             // log2(e) / temperature
   float scale;         // weights become integers by this power of two
+  float unit;          // its inverse
   int turn;
 
   __device__ __forceinline__ void open(const FilterArgs& a, int64_t row) {
@@ -114,6 +119,7 @@ struct Row {
     size = cluster_size();
     turn = 0;
     scale = a.scale;
+    unit = a.unit;
     part.cut(p, a.V, static_cast<int>(rank), static_cast<int>(size));
     packs = reinterpret_cast<const uint4*>(p + part.first - part.off);
     cut_head = part.off > 0;
@@ -154,6 +160,38 @@ struct Row {
 #pragma unroll
     for (int h = 1; h < kPer; ++h) r = fmaxf(r, v[h]);
     return r;
+  }
+  // Entry h (not a constant) of a pack.
+  static __device__ __forceinline__ float pick_of(const uint4& w, int h) {
+    const int x = h / kPer;
+    const uint32_t word = x == 0 ? w.x : (x == 1 ? w.y : (x == 2 ? w.z : w.w));
+    float v[kPer];
+    Pack<T>::open(word, v);
+    return h % kPer ? v[kPer - 1] : v[0];
+  }
+  // The uniforms of pack j's entries (0 where it has none); `wide`: u0, those
+  // of pack 0, allows 16-byte loads.
+  __device__ __forceinline__ void uniforms(const float* u, const float* u0, bool wide, int j, float* out) const {
+#pragma unroll
+    for (int h = 0; h < kE; ++h) out[h] = 0.f;
+    if (j >= part.packs) return;
+    if (wide && (j > 0 || !cut_head) && (j + 1 < part.packs || !cut_tail)) {
+      const float4* q = reinterpret_cast<const float4*>(u0 + static_cast<int64_t>(j) * kE);
+#pragma unroll
+      for (int h = 0; h < kE; h += 4) {
+        const float4 y = __ldcs(q + h / 4);
+        out[h] = y.x;
+        out[h + 1] = y.y;
+        out[h + 2] = y.z;
+        out[h + 3] = y.w;
+      }
+      return;
+    }
+#pragma unroll
+    for (int h = 0; h < kE; ++h) {
+      const int e = j * kE + h - part.off;
+      if (e >= 0 && e < part.n) out[h] = __ldcs(u + part.first + e);
+    }
   }
   // f(pack, its number) for this thread's packs, four loads at a time.
   template <typename F>
@@ -295,12 +333,61 @@ __device__ uint64_t mass_from(Row<T, NT>& r, Shared<NT, kCap>& s, uint64_t cut) 
   return cluster_reduce<NT / 32>(w, OpSumU64(), s.x, r.rank, r.size, r.turn);
 }
 
-// Smallest float at or above the bound that min-p puts on a logit.
-__device__ __forceinline__ float min_p_bound(float m, const Ask& q) {
+// The two borders that are formed in double, by one thread (the unit is narrow);
+// seen by all after the next barrier.  min-p: the smallest float at or above
+// its bound.  top-p: sums are integers, so "below p times the whole" is "below
+// the next integer".
+template <int NT, int kCap>
+__device__ __forceinline__ void set_bound(Shared<NT, kCap>& s, float m, const Ask& q) {
+  if (threadIdx.x != 0) return;
   const double t = static_cast<double>(m) + static_cast<double>(q.T) * log(static_cast<double>(q.mp));
   float f = static_cast<float>(t);
   if (static_cast<double>(f) < t) f = nextafterf(f, INFINITY);
-  return f > m ? m : f;
+  s.bound = f > m ? m : f;
+}
+template <int NT, int kCap>
+__device__ __forceinline__ void set_need(Shared<NT, kCap>& s, float p, uint64_t whole) {
+  if (threadIdx.x != 0) return;
+  s.need = p < 1.f ? static_cast<uint64_t>(ceil(static_cast<double>(p) * static_cast<double>(whole))) : ~0ull;
+}
+
+// The score of an entry, (v - m)/T - log(-log u), in fp32 and in double.
+__device__ __forceinline__ float gumbel(float u) { return -logf(-logf(u)); }
+__device__ __forceinline__ double score64(float v, float m, float temp, float u) {
+  return (v == m ? 0.0 : (static_cast<double>(v) - static_cast<double>(m)) / static_cast<double>(temp)) -
+         log(-log(static_cast<double>(u)));
+}
+// fp32 scores this close to the best are compared again in double
+__device__ __forceinline__ bool near_best(float sc, float best) {
+  return sc >= best - (1e-5f + 1e-6f * fabsf(best));
+}
+
+// log2 by the special-function unit (2^-22 of the result; -inf at 0)
+__device__ __forceinline__ float fast_log2(float x) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+template <int N>
+__device__ __forceinline__ float pick_float(const float* v, int h) {
+  float r = v[0];
+#pragma unroll
+  for (int x = 1; x < N; ++x) r = x == h ? v[x] : r;
+  return r;
+}
+
+// A thread's best entry so far.
+struct Best {
+  float score;  // (z - max)/T, or z/T, - log(-log u); starts at -inf
+  float val;
+  int at;       // -1: none yet
+};
+
+// Takes one more entry into account; equal scores keep the lower index.
+__device__ __forceinline__ void offer(Best& b, float v, int i, float log2w, float u) {
+  const float sc = fmaf(log2w, kLn2, gumbel(u));
+  if (b.at < 0 || sc > b.score || (sc == b.score && i < b.at)) b = Best{sc, v, i};
 }
 
 // What one pass over the row leaves in a thread: the maxima of its groups
@@ -373,11 +460,79 @@ __device__ __forceinline__ void scan_row(const Row<T, NT>& r, bool want_mass, Sc
   }
 }
 
+// The scan of a row that nothing filters, and its draw, in one pass over the
+// logits and the uniforms: scores are taken as z/T - log(-log u), before the
+// maximum is known (the caller draws again where z/T is too large for that).
+template <typename T, int NT, int kCap>
+__device__ __forceinline__ void scan_and_draw(const Row<T, NT>& r, Shared<NT, kCap>& s, const float* u,
+                                              Scan<T, NT>& t, Best& best) {
+  constexpr int kE = Row<T, NT>::kE, kB = 16 / kE;
+  const float* u0 = u + (r.part.first - r.part.off);
+  const bool wide = (reinterpret_cast<uintptr_t>(u0) & 15) == 0;
+  uint32_t mx = Pack<T>::kNegInf;
+  t.ref = 0.f;
+  t.sum = 0.f;
+  bool any = false, odd = false;
+  for (int j = threadIdx.x; j < r.part.packs; j += kB * NT) {
+    uint4 w[kB];
+    float uu[kB][kE];
+#pragma unroll
+    for (int x = 0; x < kB; ++x) {
+      w[x] = r.pack(j + x * NT);
+      r.uniforms(u, u0, wide, j + x * NT, uu[x]);
+    }
+#pragma unroll
+    for (int x = 0; x < kB; ++x) {
+      const uint32_t pm = Row<T, NT>::max_pack(w[x]);
+      mx = Pack<T>::max2(mx, pm);
+      const float top = Row<T, NT>::max_of(pm);
+      if (!(top > -INFINITY)) continue;
+      const float ref = top * r.c;
+      if (!any || ref > t.ref) {
+        if (any) t.sum *= fast_exp2(t.ref - ref);
+        t.ref = ref;
+        any = true;
+        odd |= !(fabsf(ref) < kRefMax);
+      }
+      float v[kE], some = 0.f, peak = -INFINITY;
+      Row<T, NT>::open_pack(w[x], v);
+#pragma unroll
+      for (int h = 0; h < kE; ++h) {
+        some += fast_exp2(fmaf(v[h], r.c, -t.ref));
+        peak = fmaxf(peak, fmaf(v[h], r.c, -fast_log2(1.f - uu[x][h])));
+      }
+      t.sum += some;
+      const float seen = key_to_value(*reinterpret_cast<volatile uint32_t*>(&s.bar));
+      const float bar = seen * 1.4426950408889634f - 0.0009765625f - fabsf(seen) * 1e-5f;
+      if (!(peak < bar)) {
+        const int i = static_cast<int>(r.index_of(j + x * NT));
+#pragma unroll 1
+        for (int h = 0; h < kE; ++h) {
+          const float z = Row<T, NT>::pick_of(w[x], h), y = pick_float<kE>(uu[x], h);
+          if (z > -INFINITY && !(fmaf(z, r.c, -fast_log2(1.f - y)) < bar)) offer(best, z, i + h, z * r.c, y);
+        }
+        const uint32_t key = value_key(best.score);
+        if (key > *reinterpret_cast<volatile uint32_t*>(&s.bar)) atomicMax(&s.bar, key);
+      }
+    }
+  }
+  t.top = Row<T, NT>::max_of(mx);
+#pragma unroll
+  for (int x = 0; x < kGroups; ++x) t.group[x] = t.top;
+  t.careful = odd || !(t.sum < INFINITY);
+  if (t.careful) {  // NaN entries, or logits at the type's end: again, with care
+    t.sum = 0.f;
+    r.each([&](float v, int64_t) {
+      if (v > -INFINITY) t.sum += fast_exp2(log2_weight(v, t.top, r.c));
+    });
+  }
+}
+
 // The row's maximum (false: no entry counts), the lowest of the groups' maxima
 // that are not -inf, and where wanted the row's sum of weights.
 template <typename T, int NT, int kCap>
 __device__ bool join_scan(Row<T, NT>& r, Shared<NT, kCap>& s, const Scan<T, NT>& t, bool want_mass, float* low,
-                          double* row_mass) {
+                          float* row_mass) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   uint32_t lo = 0xFFFFFFFFu;
 #pragma unroll
@@ -411,8 +566,9 @@ __device__ bool join_scan(Row<T, NT>& r, Shared<NT, kCap>& s, const Scan<T, NT>&
     *peer(&s.highest[r.rank], threadIdx.x) = hi;
     *peer(&s.lowest[r.rank], threadIdx.x) = lo;
     if (want_mass) {
-      double w = 0.0;
-      for (int x = 0; x < NT / 32; ++x) w += static_cast<double>(__uint_as_float(static_cast<uint32_t>(s.warp_sum[x])));
+      float w = 0.f;
+#pragma unroll
+      for (int x = 0; x < NT / 32; ++x) w += __uint_as_float(static_cast<uint32_t>(s.warp_sum[x]));
       *peer(&s.mass[r.rank], threadIdx.x) = w;
     }
   }
@@ -423,10 +579,10 @@ __device__ bool join_scan(Row<T, NT>& r, Shared<NT, kCap>& s, const Scan<T, NT>&
   }
   r.m = key_to_value(hi);
   *low = key_to_value(lo);
-  *row_mass = 0.0;
+  *row_mass = 0.f;
   if (want_mass && hi != 0)
     for (uint32_t o = 0; o < r.size; ++o)
-      if (s.highest[o]) *row_mass += s.mass[o] * static_cast<double>(fast_exp2(r.log2w(key_to_value(s.highest[o]))));
+      if (s.highest[o]) *row_mass += s.mass[o] * fast_exp2(r.log2w(key_to_value(s.highest[o])));
   return hi != 0;
 }
 
@@ -595,19 +751,19 @@ __device__ void sort_list(uint64_t* list, int n) {
 // and the sum of their weights.  `above` is the weight of the entries before
 // the list; whole > 0 is the weight that top-p refers to, else what top-k keeps.
 template <typename T, int NT, int kCap>
-__device__ int filter_list(const Row<T, NT>& r, Shared<NT, kCap>& s, const Ask& q, int n, double above, double whole,
-                           double* kept_mass) {
+__device__ int filter_list(const Row<T, NT>& r, Shared<NT, kCap>& s, const Ask& q, int n, uint64_t above,
+                           uint64_t whole, uint64_t* kept_mass) {
   constexpr int kMost = (kCap + NT - 1) / NT;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int kk = q.k < n ? q.k : n;
   const int per = (kk + NT - 1) / NT;
   uint64_t w[kMost];
   uint64_t sum = 0;
-  for (int x = 0; x < per; ++x) {
+#pragma unroll
+  for (int x = 0; x < kMost; ++x) {
     const int i = threadIdx.x * per + x;
-    const uint64_t v = i < kk ? r.weight(key_to_value(static_cast<uint32_t>(s.list[i] >> 32))) : 0ull;
-    if (x < kMost) w[x] = v;
-    sum += v;
+    w[x] = x < per && i < kk ? r.weight(key_to_value(static_cast<uint32_t>(s.list[i] >> 32))) : 0ull;
+    sum += w[x];
   }
   uint64_t inc = sum;
 #pragma unroll
@@ -617,39 +773,29 @@ __device__ int filter_list(const Row<T, NT>& r, Shared<NT, kCap>& s, const Ask& 
   }
   if (lane == 31) s.warp_sum[warp] = inc;
   __syncthreads();
-  uint64_t before = inc - sum, all = 0;
+  uint64_t before = above + inc - sum, all = 0;
+#pragma unroll
   for (int x = 0; x < NT / 32; ++x) {
     if (x < warp) before += s.warp_sum[x];
     all += s.warp_sum[x];
   }
-  const double scale = static_cast<double>(r.scale);
-  const double need = static_cast<double>(q.p) * (whole > 0.0 ? whole * scale : static_cast<double>(all));
-  above *= scale;
-  const float bound = q.mp > 0.f ? min_p_bound(r.m, q) : -INFINITY;
-  int kept = 0;
-  uint64_t mass = 0;
-  for (int x = 0; x < per; ++x) {
+  set_need(s, q.p, whole ? whole : all);
+  __syncthreads();
+  const float bound = q.mp > 0.f ? s.bound : -INFINITY;
+  const uint64_t need = s.need;
+  uint64_t mass = 0, kept = 0;
+#pragma unroll
+  for (int x = 0; x < kMost; ++x) {
     const int i = threadIdx.x * per + x;
-    if (i < kk && (i == 0 || q.p >= 1.f || above + static_cast<double>(before) < need) &&
+    if (x < per && i < kk && (i == 0 || before < need) &&
         key_to_value(static_cast<uint32_t>(s.list[i] >> 32)) >= bound) {
       ++kept;
       mass += w[x];
     }
     before += w[x];
   }
-  *kept_mass = (above + static_cast<double>(cta_reduce<NT / 32>(mass, OpSumU64(), s.x))) / scale;
-  return static_cast<int>(cta_reduce<NT / 32>(static_cast<uint64_t>(kept), OpSumU64(), s.x));
-}
-
-// The score of an entry, (v - m)/T - log(-log u), in fp32 and in double.
-__device__ __forceinline__ float gumbel(float u) { return -logf(-logf(u)); }
-__device__ __forceinline__ double score64(float v, float m, float temp, float u) {
-  return (v == m ? 0.0 : (static_cast<double>(v) - static_cast<double>(m)) / static_cast<double>(temp)) -
-         log(-log(static_cast<double>(u)));
-}
-// fp32 scores this close to the best are compared again in double
-__device__ __forceinline__ bool near_best(float sc, float best) {
-  return sc >= best - (1e-5f + 1e-6f * fabsf(best));
+  *kept_mass = above + cta_reduce<NT / 32>(mass, OpSumU64(), s.x);
+  return static_cast<int>(cta_reduce<NT / 32>(kept, OpSumU64(), s.x));
 }
 
 // Gumbel maximum over the first `kept` entries of the sorted list but `drop`
@@ -682,9 +828,10 @@ __device__ int pick_listed(const Row<T, NT>& r, Shared<NT, kCap>& s, const float
 
 // What a list says of its row (rank 0's threads).
 struct Verdict {
-  double mass;   // sum of the kept weights
+  uint64_t mass;  // sum of the kept weights
   uint64_t cut;  // place of the last entry kept
   int tok;       // Gumbel maximum of the kept entries but `drop` (u given)
+  float val;     // its logit
 };
 
 // Filters a short list and draws from it.  Up to kQuick entries, each one's
@@ -692,14 +839,15 @@ struct Verdict {
 // others (two threads an entry), which needs neither a sort nor a scan; longer
 // lists are sorted.  above, whole: as in filter_list.
 template <typename T, int NT, int kCap>
-__device__ __noinline__ Verdict settle_list(const Row<T, NT>& r, Shared<NT, kCap>& s, const Ask& q, int n, double above,
-                                            double whole, const float* u, int drop) {
+__device__ __noinline__ Verdict settle_list(const Row<T, NT>& r, Shared<NT, kCap>& s, const Ask& q, int n, uint64_t above,
+                                            uint64_t whole, const float* u, int drop) {
   Verdict out;
   if (n > kQuick) {
     sort_list<NT>(s.list, n);
     const int kept = filter_list(r, s, q, n, above, whole, &out.mass);
     out.cut = s.list[kept - 1];
     out.tok = u ? pick_listed(r, s, u, kept, drop, q.T) : -1;
+    out.val = out.tok >= 0 ? r.at(out.tok) : 0.f;
     return out;
   }
   static_assert(NT == 2 * kQuick, "two threads an entry");
@@ -737,23 +885,23 @@ __device__ __noinline__ Verdict settle_list(const Row<T, NT>& r, Shared<NT, kCap
     before += s.half_before[e];
   }
   const bool in_k = mine && rank < static_cast<uint32_t>(q.k);
-  double need = static_cast<double>(q.p) * whole * static_cast<double>(r.scale);
-  if (q.p < 1.f && whole == 0.0) {  // top-p of what top-k keeps
-    uint64_t x = in_k ? w : 0;
+  uint64_t need = ~0ull;
+  if (q.p < 1.f) {
+    if (whole == 0) {  // top-p of what top-k keeps
+      uint64_t x = in_k ? w : 0;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-    if (lane == 0) s.join[warp][0] = x;
-    __syncthreads();
-    x = 0;
+      for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+      if (lane == 0) s.join[warp][0] = x;
+      __syncthreads();
 #pragma unroll
-    for (int y = 0; y < kQuick / 32; ++y) x += s.join[y][0];
-    need = static_cast<double>(q.p) * static_cast<double>(x);
+      for (int y = 0; y < kQuick / 32; ++y) whole += s.join[y][0];
+    }
+    set_need(s, q.p, whole);
     __syncthreads();
+    need = s.need;
   }
-  const double over = above * static_cast<double>(r.scale);
-  const float bound = q.mp > 0.f ? min_p_bound(r.m, q) : -INFINITY;
-  const bool kept =
-      in_k && (rank == 0 || q.p >= 1.f || over + static_cast<double>(before) < need) && v >= bound;
+  const float bound = q.mp > 0.f ? s.bound : -INFINITY;
+  const bool kept = in_k && (rank == 0 || above + before < need) && v >= bound;
   const bool runs = kept && u && !q.greedy && static_cast<int>(at) != drop;
   const float sc = runs ? fmaf(r.log2w(v), kLn2, gumbel(ue)) : -INFINITY;
   uint64_t sum = kept ? w : 0, last = kept ? ~place : 0, key = runs ? argmax_key(sc, at) : 0;
@@ -780,7 +928,7 @@ __device__ __noinline__ Verdict settle_list(const Row<T, NT>& r, Shared<NT, kCap
     last = s.join[y][1] > last ? s.join[y][1] : last;
     key = s.join[y][2] > key ? s.join[y][2] : key;
   }
-  out.mass = above + static_cast<double>(sum) / static_cast<double>(r.scale);
+  out.mass = above + sum;
   out.cut = ~last;
   out.tok = key ? static_cast<int>(key_index(key)) : -1;
   const bool close = runs && near_best(sc, key_value(key));
@@ -790,36 +938,20 @@ __device__ __noinline__ Verdict settle_list(const Row<T, NT>& r, Shared<NT, kCap
     const uint64_t low = close && dk == best ? 0xFFFFFFFFull - at : 0ull;
     out.tok = static_cast<int>(0xFFFFFFFFull - cta_reduce<NT / 32>(low, OpMaxU64(), s.x));
   }
+  if (kept && static_cast<int>(at) == out.tok) s.val = v;
+  __syncthreads();
+  out.val = s.val;
   return out;
-}
-
-// log2 by the special-function unit (2^-22 of the result; -inf at 0)
-__device__ __forceinline__ float fast_log2(float x) {
-  float y;
-  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-// A thread's best entry so far.
-struct Best {
-  float score;  // (z - max)/T - log(-log u); starts at -inf
-  float val;
-  int at;       // -1: none yet
-};
-
-// Takes one more entry into account; equal scores keep the lower index.
-__device__ __forceinline__ void offer(Best& b, float v, int i, float log2w, float u) {
-  const float sc = fmaf(log2w, kLn2, gumbel(u));
-  if (b.at < 0 || sc > b.score || (sc == b.score && i < b.at)) b = Best{sc, v, i};
 }
 
 // One pass over this thread's entries with v >= low: f(v, i) for each, and the
 // best of those for which it returns true.  A score needs two logarithms; as
-// -log u >= 1 - u, (z - max)/T - log(1 - u) bounds it, and few entries pass the best
-// score so far by that.  Uniforms are loaded for the packs that hold such an
-// entry.
-template <typename T, int NT, typename F>
-__device__ __forceinline__ void draw_pass(const Row<T, NT>& r, const float* u, float low, Best& best, F f) {
+// -log u >= 1 - u, (z - max)/T - log(1 - u) bounds it, and few entries pass the CTA's
+// best score so far by that.  Uniforms are loaded for the packs that hold such an
+// entry, or with kDense for all, without waiting for the logits.
+template <bool kDense, int kCap, typename T, int NT, typename F>
+__device__ __forceinline__ void draw_pass(const Row<T, NT>& r, Shared<NT, kCap>& s, const float* u, float low,
+                                          Best& best, F f) {
   constexpr int kE = Row<T, NT>::kE, kB = 16 / kE;  // packs in flight
   const float* u0 = u + (r.part.first - r.part.off);
   const bool wide = (reinterpret_cast<uintptr_t>(u0) & 15) == 0;
@@ -834,26 +966,7 @@ __device__ __forceinline__ void draw_pass(const Row<T, NT>& r, const float* u, f
       const int k = j + x * NT;
       const float top = Row<T, NT>::max_of(Row<T, NT>::max_pack(w[x]));
       some[x] = top >= low && top > -INFINITY;
-#pragma unroll
-      for (int h = 0; h < kE; ++h) uu[x][h] = 0.f;
-      if (!some[x]) continue;
-      if (wide && (k > 0 || !r.cut_head) && (k + 1 < r.part.packs || !r.cut_tail)) {
-        const float4* q = reinterpret_cast<const float4*>(u0 + static_cast<int64_t>(k) * kE);
-#pragma unroll
-        for (int h = 0; h < kE; h += 4) {
-          const float4 y = __ldcs(q + h / 4);
-          uu[x][h] = y.x;
-          uu[x][h + 1] = y.y;
-          uu[x][h + 2] = y.z;
-          uu[x][h + 3] = y.w;
-        }
-      } else {
-#pragma unroll
-        for (int h = 0; h < kE; ++h) {
-          const int e = k * kE + h - r.part.off;
-          if (e >= 0 && e < r.part.n) uu[x][h] = __ldcs(u + r.part.first + e);
-        }
-      }
+      if (kDense || some[x]) r.uniforms(u, u0, wide, k, uu[x]);
     }
 #pragma unroll
     for (int x = 0; x < kB; ++x) {
@@ -861,14 +974,20 @@ __device__ __forceinline__ void draw_pass(const Row<T, NT>& r, const float* u, f
       float v[kE];
       Row<T, NT>::open_pack(w[x], v);
       const int i = static_cast<int>(r.index_of(j + x * NT));
-      // bounds in units of log2, and 2^-10 to be safe
-      const float bar = best.score * 1.4426950408889634f - 0.0009765625f - fabsf(best.score) * 1e-5f;
+      // the CTA's best so far in units of log2, less 2^-10 to be safe: whatever
+      // comes near the final best is scored
+      const float seen = key_to_value(*reinterpret_cast<volatile uint32_t*>(&s.bar));
+      const float bar = seen * 1.4426950408889634f - 0.0009765625f - fabsf(seen) * 1e-5f;
 #pragma unroll
       for (int h = 0; h < kE; ++h) {
         if (!(v[h] >= low) || !(v[h] > -INFINITY)) continue;
         const bool counts = f(v[h], i + h);
         const float x2 = (v[h] - r.m) * r.c;
-        if (counts && !(x2 - fast_log2(1.f - uu[x][h]) < bar)) offer(best, v[h], i + h, x2, uu[x][h]);
+        if (counts && !(x2 - fast_log2(1.f - uu[x][h]) < bar)) {
+          offer(best, v[h], i + h, x2, uu[x][h]);
+          const uint32_t key = value_key(best.score);
+          if (best.at == i + h && key > *reinterpret_cast<volatile uint32_t*>(&s.bar)) atomicMax(&s.bar, key);
+        }
       }
     }
   }
@@ -896,10 +1015,17 @@ template <typename T, int NT, int kCap>
 __device__ __noinline__ int pick_row(Row<T, NT>& r, Shared<NT, kCap>& s, const float* u, uint64_t cut, int drop,
                                      float temp) {
   Best b{-INFINITY, 0.f, -1};
+  if (threadIdx.x == 0) s.bar = 0x007FFFFFu;  // -inf
+  __syncthreads();
   if (r.m < INFINITY) {
     const float low = cut_value(cut);
     const int last = static_cast<int>(place_index(cut) < 0x7FFFFFFFu ? place_index(cut) : 0x7FFFFFFFu);
-    draw_pass(r, u, low, b, [=](float v, int i) { return i != drop && (v > low || i <= last); });
+    const auto takes = [=](float v, int i) { return i != drop && (v > low || i <= last); };
+    if (low == -INFINITY) {
+      draw_pass<true>(r, s, u, low, b, takes);
+    } else {
+      draw_pass<false>(r, s, u, low, b, takes);
+    }
   } else {  // only the infinite entries have weight
     r.each([&](float v, int64_t i) {
       if (v == r.m && place_of(value_key(v), static_cast<uint32_t>(i)) >= cut && i != drop)
@@ -909,9 +1035,9 @@ __device__ __noinline__ int pick_row(Row<T, NT>& r, Shared<NT, kCap>& s, const f
   return join_best(r, s, u, b, temp);
 }
 
-// Cluster sum of a double, CTAs in rank order.
+// Cluster sum of a float, CTAs in rank order.
 template <typename T, int NT, int kCap>
-__device__ __forceinline__ double cluster_mass(Row<T, NT>& r, Shared<NT, kCap>& s, float w) {
+__device__ __forceinline__ float cluster_mass(Row<T, NT>& r, Shared<NT, kCap>& s, float w) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) w += __shfl_xor_sync(0xffffffffu, w, o);
@@ -919,12 +1045,13 @@ __device__ __forceinline__ double cluster_mass(Row<T, NT>& r, Shared<NT, kCap>& 
   if (lane == 0) s.warp_sum[warp] = __float_as_uint(w);
   __syncthreads();
   if (threadIdx.x < r.size) {
-    double d = 0.0;
-    for (int x = 0; x < NT / 32; ++x) d += static_cast<double>(__uint_as_float(static_cast<uint32_t>(s.warp_sum[x])));
+    float d = 0.f;
+#pragma unroll
+    for (int x = 0; x < NT / 32; ++x) d += __uint_as_float(static_cast<uint32_t>(s.warp_sum[x]));
     *peer(&s.mass[r.rank], threadIdx.x) = d;
   }
   cluster_sync_all(r.size);
-  double d = 0.0;
+  float d = 0.f;
   for (uint32_t o = 0; o < r.size; ++o) d += s.mass[o];
   return d;
 }
@@ -937,13 +1064,13 @@ __device__ __forceinline__ double cluster_mass(Row<T, NT>& r, Shared<NT, kCap>& 
 // False: the border fell too close to a bin's edge, or the bin does not fit the
 // list.  Else rank 0 holds the list, of which it keeps *kept.
 template <typename T, int NT, int kCap>
-__device__ __noinline__ bool deep_top_p(Row<T, NT>& r, Shared<NT, kCap>& s, const Ask& q, int64_t V, double row_mass,
-                                        const float* u, int* kept, double* kept_mass, Best* best) {
+__device__ __noinline__ bool deep_top_p(Row<T, NT>& r, Shared<NT, kCap>& s, const Ask& q, int64_t V, float row_mass,
+                                        const float* u, int* kept, uint64_t* kept_mass, Best* best) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const double need = static_cast<double>(q.p) * row_mass;
+  const uint64_t whole = __float2ull_rn(row_mass * r.scale);
   // entries this far below the maximum sum to less than (1 - p) / 2 of the row
-  const float span = logf(2.f * static_cast<float>(V) / ((1.f - q.p) * static_cast<float>(row_mass))) * q.T;
-  if (!(r.m < INFINITY) || !(span > 1e-20f) || !(span < 1e30f)) return false;
+  const float span = logf(2.f * static_cast<float>(V) / ((1.f - q.p) * row_mass)) * q.T;
+  if (!(fabsf(r.m) < 1e20f) || !(span > 1e-6f * fabsf(r.m)) || !(span < 1e20f)) return false;
   const float per = kLineBins / span, step = r.c / per;  // log2 of a bin's fall
   // the unit of the bins' integers: 2^31 holds every entry of the longest part
   const int most = static_cast<int>(V / r.size) + 2 * Part<T>::kE;
@@ -954,11 +1081,14 @@ __device__ __noinline__ bool deep_top_p(Row<T, NT>& r, Shared<NT, kCap>& s, cons
     s.own_mass = 0;
     s.taken = 0;
     s.pick[0] = kLineBins;
+    s.bar = 0x007FFFFFu;  // -inf
   }
+  set_need(s, q.p, whole);
   __syncthreads();
-  const float m = r.m;
+  const float m = r.m, from = m * per;
+  const auto line = [=](float v) { return fmaf(v, -per, from); };  // bins below the maximum
   r.each([&](float v, int64_t) {
-    const float d = (m - v) * per;
+    const float d = line(v);
     if (d < static_cast<float>(kLineBins)) {
       const int b = static_cast<int>(d);
       atomicAdd(&s.line[b], __float2uint_rn(fast_exp2((static_cast<float>(b) - d) * step) * one));
@@ -966,29 +1096,37 @@ __device__ __noinline__ bool deep_top_p(Row<T, NT>& r, Shared<NT, kCap>& s, cons
   });
   cluster_sync_all(r.size);
   constexpr int kMine = kLineBins / NT;
-  double mine[kMine], sum = 0.0;
+  static_assert(kMine == 4, "a thread's bins are one 16-byte load");
+  const uint64_t need = s.need;
+  uint4 c[kMaxCluster];
+#pragma unroll
+  for (uint32_t o = 0; o < kMaxCluster; ++o)
+    c[o] = o < r.size ? *peer(reinterpret_cast<const uint4*>(s.line) + threadIdx.x, o) : make_uint4(0, 0, 0, 0);
+  float h[kMine] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (uint32_t o = 0; o < kMaxCluster; ++o) {
+    h[0] += static_cast<float>(c[o].x);
+    h[1] += static_cast<float>(c[o].y);
+    h[2] += static_cast<float>(c[o].z);
+    h[3] += static_cast<float>(c[o].w);
+  }
+  uint64_t mine[kMine], sum = 0;
 #pragma unroll
   for (int x = 0; x < kMine; ++x) {
-    const int b = threadIdx.x * kMine + x;
-    float h = 0.f;
-    uint32_t c[kMaxCluster];
-#pragma unroll
-    for (uint32_t o = 0; o < kMaxCluster; ++o) c[o] = o < r.size ? *peer(&s.line[b], o) : 0u;
-#pragma unroll
-    for (uint32_t o = 0; o < kMaxCluster; ++o) h += static_cast<float>(c[o]);
-    mine[x] = static_cast<double>(h / one * fast_exp2(-static_cast<float>(b) * step));
+    const float b = static_cast<float>(threadIdx.x * kMine + x);
+    mine[x] = __float2ull_rn(h[x] / one * fast_exp2(-b * step) * r.scale);
     sum += mine[x];
   }
-  double inc = sum;
+  uint64_t inc = sum;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const double y = __shfl_up_sync(0xffffffffu, inc, o);
+    const uint64_t y = __shfl_up_sync(0xffffffffu, inc, o);
     if (lane >= o) inc += y;
   }
-  if (lane == 31) s.warp_sum[warp] = __double_as_longlong(inc);
+  if (lane == 31) s.warp_sum[warp] = inc;
   __syncthreads();
-  double before = inc - sum;
-  for (int w = 0; w < warp; ++w) before += __longlong_as_double(s.warp_sum[w]);
+  uint64_t before = inc - sum;
+  for (int w = 0; w < warp; ++w) before += s.warp_sum[w];
 #pragma unroll
   for (int x = 0; x < kMine; ++x) {
     if (before < need && before + mine[x] >= need) s.pick[0] = threadIdx.x * kMine + x;
@@ -997,43 +1135,47 @@ __device__ __noinline__ bool deep_top_p(Row<T, NT>& r, Shared<NT, kCap>& s, cons
   __syncthreads();
   const int bin = static_cast<int>(s.pick[0]);
   if (bin == kLineBins) return false;
-  // second pass
+  // second pass; each CTA lists its entries of the bin in its own memory
   const float edge = static_cast<float>(bin), end = edge + 1.f;
   float w = 0.f;
-  uint32_t* taken = peer(&s.taken, 0);
-  uint64_t* list = peer(s.list, 0);
+  uint64_t listed = 0;
   const float low = m - end / per * 1.0001f - fabsf(m) * 1e-6f;  // no entry of the bin lies below
   auto visit = [&](float v, int i) {
-    const float d = (m - v) * per;
+    const float d = line(v);
     if (d < edge) {
       w += fast_exp2((v - m) * r.c);
       return true;
     }
     if (d < end) {
-      const uint32_t at = atomicAdd(taken, 1u);
-      if (at < kCap) list[at] = place_of(value_key(v), static_cast<uint32_t>(i));
-      atomicAdd(&s.own_count, 1u);
-      atomicAdd(reinterpret_cast<unsigned long long*>(&s.own_mass), r.weight(v));
+      const uint32_t at = atomicAdd(&s.own_count, 1u);
+      if (at < kCap) s.list[at] = place_of(value_key(v), static_cast<uint32_t>(i));
+      listed += r.weight(v);
     }
     return false;
   };
   if (u) {
-    draw_pass(r, u, low, *best, visit);
+    draw_pass<true>(r, s, u, low, *best, visit);
   } else {
     r.each([&](float v, int64_t i) {
       if (v >= low) visit(v, static_cast<int>(i));
     });
   }
-  const double above = cluster_mass(r, s, w);
+  if (listed) atomicAdd(reinterpret_cast<unsigned long long*>(&s.own_mass), listed);
+  const uint64_t above = __float2ull_rn(cluster_mass(r, s, w) * r.scale);
   uint32_t count;
   uint64_t mass;
   close_list(r, s, &count, &mass);
-  if (count > kCap || !(above < need) ||
-      above + static_cast<double>(mass) / static_cast<double>(r.scale) < need)
-    return false;
+  if (r.rank != 0 && count <= kCap) {  // behind the entries of the CTAs before
+    uint32_t at = 0;
+    for (uint32_t o = 0; o < r.rank; ++o) at += s.list_count[o];
+    uint64_t* list = peer(s.list, 0);
+    for (uint32_t i = threadIdx.x; i < s.own_count; i += NT) list[at + i] = s.list[i];
+  }
+  cluster_sync_all(r.size);
+  if (count > kCap || above >= need || above + mass < need) return false;
   if (r.rank == 0) {
     sort_list<NT>(s.list, static_cast<int>(count));
-    *kept = filter_list(r, s, q, static_cast<int>(count), above, row_mass, kept_mass);
+    *kept = filter_list(r, s, q, static_cast<int>(count), above, whole, kept_mass);
   }
   return true;
 }
@@ -1041,7 +1183,7 @@ __device__ __noinline__ bool deep_top_p(Row<T, NT>& r, Shared<NT, kCap>& s, cons
 // The cut and the kept mass of any row, by radix descents.
 template <typename T, int NT, int kCap>
 __device__ __noinline__ uint64_t wide_cut(Row<T, NT>& r, Shared<NT, kCap>& s, const FilterArgs& a, const Ask& q,
-                                          double* kept_mass) {
+                                          uint64_t* kept_mass) {
   uint64_t cut = 1ull << 32;  // every unmasked entry
   if (q.k < a.V) {
     uint64_t valid = 0;
@@ -1052,12 +1194,15 @@ __device__ __noinline__ uint64_t wide_cut(Row<T, NT>& r, Shared<NT, kCap>& s, co
   if (q.p < 1.f) {
     // entries are taken while the sum before them is below p times w
     const uint64_t w = mass_from(r, s, cut);
-    uint64_t need = static_cast<uint64_t>(ceil(static_cast<double>(q.p) * static_cast<double>(w)));
-    if (need < 1) need = 1;
+    set_need(s, q.p, w);
+    __syncthreads();
+    const uint64_t need = s.need < 1 ? 1 : s.need;
     if (need < w) cut = find_cut<T, NT, kCap, true>(r, s, cut, need, a.idx_bits);
   }
   if (q.mp > 0.f) {
-    const uint64_t c = place_of(value_key(min_p_bound(r.m, q)), 0xFFFFFFFFu);
+    set_bound(s, r.m, q);
+    __syncthreads();
+    const uint64_t c = place_of(value_key(s.bound), 0xFFFFFFFFu);
     if (c > cut) cut = c;
   }
   const float low = cut_value(cut);
@@ -1066,7 +1211,7 @@ __device__ __noinline__ uint64_t wide_cut(Row<T, NT>& r, Shared<NT, kCap>& s, co
   r.each([&](float v, int64_t i) {
     if (v > -INFINITY && (v > low || (v == low && i <= last))) w += fast_exp2(r.log2w(v));
   });
-  *kept_mass = cluster_mass(r, s, w);
+  *kept_mass = __float2ull_rn(cluster_mass(r, s, w) * r.scale);
   return cut;
 }
 
@@ -1074,9 +1219,13 @@ __device__ __noinline__ uint64_t wide_cut(Row<T, NT>& r, Shared<NT, kCap>& s, co
 // verdict (with a draw from u, if given).
 template <typename T, int NT, int kCap>
 __device__ bool listed_row(Row<T, NT>& r, Shared<NT, kCap>& s, const Scan<T, NT>& sc, const FilterArgs& a,
-                           const Ask& q, float low, double row_mass, const float* u, int drop, Verdict* out) {
+                           const Ask& q, float low, float row_mass, const float* u, int drop, Verdict* out) {
   int target = 0;
   float t = -INFINITY;
+  if (q.mp > 0.f) {
+    set_bound(s, r.m, q);
+    __syncthreads();
+  }
   const bool of_row = q.k >= a.V && q.p < 1.f;  // top-p refers to the whole row
   if (q.k == 1) {
     t = r.m;
@@ -1085,7 +1234,7 @@ __device__ bool listed_row(Row<T, NT>& r, Shared<NT, kCap>& s, const Scan<T, NT>
   } else if (of_row) {
     target = kFewTarget;
   } else if (q.mp > 0.f) {
-    t = min_p_bound(r.m, q);
+    t = s.bound;
   } else {
     return false;
   }
@@ -1093,17 +1242,19 @@ __device__ bool listed_row(Row<T, NT>& r, Shared<NT, kCap>& s, const Scan<T, NT>
   uint32_t count;
   uint64_t mass;
   if (!short_list(r, s, sc, a.V, low, target, &t, of_row, &count, &mass)) return false;
-  // the list has to hold top-p's border, or all that min-p leaves
-  if (of_row && static_cast<double>(mass) < static_cast<double>(q.p) * row_mass * static_cast<double>(r.scale) &&
-      static_cast<int64_t>(count) < a.V && !(q.mp > 0.f && min_p_bound(r.m, q) >= t))
+  // the list has to hold top-p's border (with a margin for these roundings), or
+  // all that min-p leaves
+  const uint64_t whole = of_row ? __float2ull_rn(row_mass * r.scale) : 0;
+  if (of_row && __ull2float_rz(mass) < q.p * __ull2float_ru(whole) * 1.000001f && static_cast<int64_t>(count) < a.V &&
+      !(q.mp > 0.f && s.bound >= t))
     return false;
-  if (r.rank == 0) *out = settle_list(r, s, q, static_cast<int>(count), 0.0, of_row ? row_mass : 0.0, u, drop);
+  if (r.rank == 0) *out = settle_list(r, s, q, static_cast<int>(count), 0, whole, u, drop);
   return true;
 }
 
 template <typename T, int NT>
-__device__ __forceinline__ float log_prob(const Row<T, NT>& r, int tok, double kept) {
-  return r.log2w(r.at(tok)) * kLn2 - logf(static_cast<float>(kept));
+__device__ __forceinline__ float log_prob(const Row<T, NT>& r, float v, uint64_t kept) {
+  return r.log2w(v) * kLn2 - logf(__ull2float_rn(kept) * r.unit);
 }
 
 // A row whose sum of weights the scan has to form: nothing filters it, or
@@ -1120,6 +1271,7 @@ __device__ __forceinline__ void start(Shared<NT, kCap>& s, uint32_t size) {
     s.own_count = 0;
     s.taken = 0;
     s.queued = 0;
+    s.bar = 0x007FFFFFu;  // -inf
   }
   for (int b = threadIdx.x; b < kGroupBins; b += NT) s.groups[b] = 0;
   __syncthreads();
@@ -1130,34 +1282,44 @@ __device__ __forceinline__ void start(Shared<NT, kCap>& s, uint32_t size) {
 constexpr int kShortCap = 1024;
 constexpr int kThr = 256;
 
-template <typename T>
-__global__ void __launch_bounds__(kThr, 4) sample_rows_kernel(const FilterArgs a) {
-  extern __shared__ __align__(16) uint8_t raw[];
-  using S = Shared<kThr, kShortCap>;
-  S& s = *reinterpret_cast<S*>(raw);
+constexpr int kDeferred = -2;  // tok of a row that is left to the wide kernel, or whose draw is
+
+// The lists' kernels run few CTAs a row; a row that needs more passes is left
+// to a second launch, whose clusters of eight share out such rows, unless the
+// first has as many CTAs a row already.
+template <typename T, bool kWide>
+__device__ __forceinline__ void sample_row(const FilterArgs& a, Shared<kThr, kShortCap>& s, int64_t row) {
   const uint32_t size = cluster_size();
-  const int64_t row = blockIdx.x / size;
   start(s, size);
   const Ask q = read_ask(a, row);
   Row<T, kThr> r;
   r.c = inv_temperature(q.T);
   r.open(a, row);
-  const bool want_mass = wants_mass(a, q);
-  Scan<T, kThr> sc;
-  scan_row(r, want_mass, sc);
-  float low;
-  double row_mass;
-  const bool some = join_scan(r, s, sc, want_mass, &low, &row_mass);
+  const bool want_mass = wants_mass(a, q), unfiltered = want_mass && q.p >= 1.f && q.ok;
   const float* u = a.u + row * a.ld_u;
+  Scan<T, kThr> sc;
+  Best best{-INFINITY, 0.f, -1};
+  if (!kWide && unfiltered) {
+    scan_and_draw(r, s, u, sc, best);
+  } else {
+    scan_row(r, want_mass, sc);
+  }
+  float low;
+  float row_mass;
+  const bool some = join_scan(r, s, sc, want_mass, &low, &row_mass);
   int tok = -1;
   float lp = -INFINITY;
   if (q.ok && some) {
-    Verdict v;
-    Best best{-INFINITY, 0.f, -1};
+    Verdict v{0, 0, -1, 0.f};
     int n = 0;
-    if (listed_row(r, s, sc, a, q, low, row_mass, u, -1, &v)) {
+    if (!kWide && unfiltered && fabsf(r.m * r.c) < 1e3f) {
+      v.mass = __float2ull_rn(row_mass * r.scale);
+      tok = join_best(r, s, u, best, q.T);
+    } else if (!kWide && listed_row(r, s, sc, a, q, low, row_mass, u, -1, &v)) {
       if (r.rank != 0) return;
       tok = v.tok;
+    } else if (a.defer) {
+      tok = kDeferred;
     } else if (q.k >= a.V && q.p < 1.f && q.mp == 0.f &&
                deep_top_p(r, s, q, a.V, row_mass, u, &n, &v.mass, &best)) {
       if (r.rank == 0) {
@@ -1170,14 +1332,14 @@ __global__ void __launch_bounds__(kThr, 4) sample_rows_kernel(const FilterArgs a
       tok = join_best(r, s, u, best, q.T);
     } else {
       uint64_t cut = 1ull << 32;
-      if (want_mass && q.p >= 1.f) {
-        v.mass = row_mass;
+      if (unfiltered) {
+        v.mass = __float2ull_rn(row_mass * r.scale);
       } else {
         cut = wide_cut(r, s, a, q, &v.mass);
       }
       tok = q.greedy ? static_cast<int>(place_index(cut)) : pick_row(r, s, u, cut, -1, q.T);
     }
-    if (tok >= 0) lp = log_prob(r, tok, v.mass);
+    if (tok >= 0 && threadIdx.x == 0) lp = log_prob(r, tok == v.tok ? v.val : r.at(tok), v.mass);
   }
   if (r.rank == 0 && threadIdx.x == 0) {
     a.tok[row] = tok;
@@ -1186,17 +1348,30 @@ __global__ void __launch_bounds__(kThr, 4) sample_rows_kernel(const FilterArgs a
   }
 }
 
+template <typename T>
+__global__ void __launch_bounds__(kThr, 4) sample_rows_kernel(const FilterArgs a) {
+  extern __shared__ __align__(16) uint8_t raw[];
+  sample_row<T, false>(a, *reinterpret_cast<Shared<kThr, kShortCap>*>(raw), blockIdx.x / cluster_size());
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThr, 4) sample_wide_kernel(const FilterArgs a, const int64_t rows) {
+  extern __shared__ __align__(16) uint8_t raw[];
+  pdl_wait();
+  const uint32_t size = cluster_size();
+  for (int64_t row = blockIdx.x / size; row < rows; row += gridDim.x / size) {
+    if (a.tok[row] != kDeferred) continue;  // the cluster's CTAs all read it before one can write it
+    sample_row<T, true>(a, *reinterpret_cast<Shared<kThr, kShortCap>*>(raw), row);
+    cluster_sync_all(size);
+  }
+}
+
 // Verified row rr of sequence j: whether its draft is accepted, and the token
 // drawn here if it is not (or if rr = D).  A row without a short list leaves
-// the draw, which few rows need, to the second kernel.
-template <typename T>
-__global__ void __launch_bounds__(kThr, 4) accept_rows_kernel(const FilterArgs a) {
-  extern __shared__ __align__(16) uint8_t raw[];
-  using S = Shared<kThr, kShortCap>;
-  S& s = *reinterpret_cast<S*>(raw);
+// the draw, which few rows need, to the last kernel.
+template <typename T, bool kWide>
+__device__ __forceinline__ void accept_row(const FilterArgs& a, Shared<kThr, kShortCap>& s, int64_t j, int rr) {
   const uint32_t size = cluster_size();
-  const int64_t j = blockIdx.x / size / a.rows_used;
-  const int rr = static_cast<int>(blockIdx.x / size - j * a.rows_used);
   const int64_t row = j * a.R + rr;
   start(s, size);
   const Ask q = read_ask(a, j);
@@ -1207,44 +1382,69 @@ __global__ void __launch_bounds__(kThr, 4) accept_rows_kernel(const FilterArgs a
   Scan<T, kThr> sc;
   scan_row(r, want_mass, sc);
   float low;
-  double row_mass;
+  float row_mass;
   const bool some = join_scan(r, s, sc, want_mass, &low, &row_mass);
   RowCut out;
   out.cut = ~0ull;
   out.m = r.m;
   out.accept = 0;
   out.tok = -1;
+  out.deferred = 0;
   if (q.ok && some) {
     const int drop = rr < a.D ? a.draft[j * a.D + rr] : -1;
-    Verdict v;
+    Verdict v{0, 0, -1, 0.f};
     int n = 0;
-    if (listed_row(r, s, sc, a, q, low, row_mass, a.u + j * a.ld_u, drop, &v)) {
+    if (!kWide && listed_row(r, s, sc, a, q, low, row_mass, a.u + j * a.ld_u, drop, &v)) {
       if (r.rank != 0) return;
       out.cut = v.cut;
       out.tok = v.tok;
     } else {
-      out.tok = -2;  // not drawn yet
-      if (q.k >= a.V && q.p < 1.f && q.mp == 0.f &&
-          deep_top_p(r, s, q, a.V, row_mass, static_cast<const float*>(nullptr), &n, &v.mass,
-                     static_cast<Best*>(nullptr))) {
-        if (r.rank != 0) return;
-        out.cut = s.list[n - 1];
-      } else if (want_mass && q.p >= 1.f) {
+      out.tok = kDeferred;
+      if (want_mass && q.p >= 1.f) {
         out.cut = 1ull << 32;
-        v.mass = row_mass;
+        v.mass = __float2ull_rn(row_mass * r.scale);
+      } else if (a.defer) {
+        out.deferred = 1;
+      } else if (q.k >= a.V && q.p < 1.f && q.mp == 0.f &&
+                 deep_top_p(r, s, q, a.V, row_mass, static_cast<const float*>(nullptr), &n, &v.mass,
+                            static_cast<Best*>(nullptr))) {
+        if (r.rank == 0) out.cut = s.list[n - 1];
       } else {
         out.cut = wide_cut(r, s, a, q, &v.mass);
       }
     }
-    if (drop >= 0 && drop < a.V) {
+    if (r.rank == 0 && threadIdx.x == 0 && !out.deferred && drop >= 0 && drop < a.V) {
       const float z = r.at(drop);
       const uint32_t key = value_key(z);
       if (key != 0 && place_of(key, static_cast<uint32_t>(drop)) >= out.cut)
-        out.accept = static_cast<double>(a.u_accept[j * a.D + rr]) <
-                     static_cast<double>(r.weight(z)) / static_cast<double>(r.scale) / v.mass;
+        out.accept = static_cast<double>(a.u_accept[j * a.D + rr]) * static_cast<double>(v.mass) <
+                     static_cast<double>(r.weight(z));
     }
   }
   if (r.rank == 0 && threadIdx.x == 0) a.cuts[row] = out;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThr, 4) accept_rows_kernel(const FilterArgs a) {
+  extern __shared__ __align__(16) uint8_t raw[];
+  const uint32_t at = blockIdx.x / cluster_size();
+  const int64_t j = at / a.rows_used;
+  accept_row<T, false>(a, *reinterpret_cast<Shared<kThr, kShortCap>*>(raw), j,
+                       static_cast<int>(at - j * a.rows_used));
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThr, 4) accept_wide_kernel(const FilterArgs a, const int64_t rows) {
+  extern __shared__ __align__(16) uint8_t raw[];
+  pdl_wait();
+  const uint32_t size = cluster_size();
+  for (int64_t at = blockIdx.x / size; at < rows; at += gridDim.x / size) {
+    const int64_t j = at / a.rows_used;
+    const int rr = static_cast<int>(at - j * a.rows_used);
+    if (!a.cuts[j * a.R + rr].deferred) continue;
+    accept_row<T, true>(a, *reinterpret_cast<Shared<kThr, kShortCap>*>(raw), j, rr);
+    cluster_sync_all(size);
+  }
 }
 
 // One cluster per sequence: leading accepts, the draw at the row after them if
@@ -1266,7 +1466,7 @@ __global__ void __launch_bounds__(kThr) accept_pick_kernel(const FilterArgs a) {
     const int64_t row = j * a.R + n;
     const RowCut c = a.cuts[row];
     corr = c.tok;
-    if (corr == -2) {
+    if (corr == kDeferred) {
       Row<T, kThr> r;
       r.c = inv_temperature(q.T);
       r.open(a, row);
@@ -1307,7 +1507,7 @@ __global__ void __launch_bounds__(kThr, 4) top_rows_kernel(const FilterArgs a) {
   const bool want_mass = a.lse != nullptr;
   scan_row(r, want_mass, sc);
   float low, t = -INFINITY;
-  double row_mass;
+  float row_mass;
   const bool some = join_scan(r, s, sc, want_mass, &low, &row_mass);
   uint32_t n = 0;
   uint64_t mass;
@@ -1343,7 +1543,7 @@ __global__ void __launch_bounds__(kThr, 4) top_rows_kernel(const FilterArgs a) {
   if (a.lse && threadIdx.x == 0) {
     // an infinite maximum is the sum
     const float l = r.m < INFINITY ? static_cast<float>(static_cast<double>(r.m) / static_cast<double>(a.T) +
-                                                        static_cast<double>(logf(static_cast<float>(row_mass))))
+                                                        static_cast<double>(logf(row_mass)))
                                    : r.m;
     a.lse[row] = some ? l : -INFINITY;
   }
@@ -1358,24 +1558,50 @@ cudaError_t launch_rows(const void* kern, int64_t rows, int parts, size_t smem, 
   return launch_kc(kern, dim3((unsigned)(rows * parts)), dim3(kThr), smem, st, true, dim3(parts), args);
 }
 
-// CTAs per row: enough to occupy the GPU, at least 4 KB each.
+// CTAs per row: as many as the GPU holds at once (four an SM), at least 4 KB
+// each.
 int pick_parts(int64_t V, int64_t rows, size_t esize) {
   int parts = 1;
-  while (parts < kMaxCluster && rows * parts < 4 * num_sms() && V * (int64_t)esize / (2 * parts) >= 4096) parts *= 2;
+  while (parts < kMaxCluster && rows * parts * 2 <= 4 * num_sms() && V * (int64_t)esize / (2 * parts) >= 4096)
+    parts *= 2;
   return parts;
+}
+// Whether wide rows are left to a second launch: its clusters have to be
+// larger, and cost a launch that short rows do without.
+bool defers(int64_t V, size_t esize, int parts) {
+  return parts < kMaxCluster && V * (int64_t)esize / parts > 64 * 1024;
+}
+
+// The second launch: clusters of eight that fill the GPU share out the rows.
+cudaError_t launch_wide(const void* kern, int64_t rows, size_t smem, const FilterArgs& a, cudaStream_t st) {
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  FilterArgs b = a;
+  b.defer = 0;
+  void* args[] = {&b, &rows};
+  int64_t clusters = 4 * num_sms() / kMaxCluster;
+  if (clusters > rows) clusters = rows;
+  return launch_kc(kern, dim3((unsigned)(clusters * kMaxCluster)), dim3(kThr), smem, st, true, dim3(kMaxCluster), args);
 }
 
 template <typename T>
-cudaError_t launch_sample(const FilterArgs& a, int64_t rows, cudaStream_t st) {
-  return launch_rows((const void*)sample_rows_kernel<T>, rows, pick_parts(a.V, rows, sizeof(T)),
-                     sizeof(Shared<kThr, kShortCap>), a, st);
+cudaError_t launch_sample(FilterArgs a, int64_t rows, cudaStream_t st) {
+  const size_t smem = sizeof(Shared<kThr, kShortCap>);
+  const int parts = pick_parts(a.V, rows, sizeof(T));
+  a.defer = defers(a.V, sizeof(T), parts);
+  cudaError_t e = launch_rows((const void*)sample_rows_kernel<T>, rows, parts, smem, a, st);
+  if (e != cudaSuccess || !a.defer) return e;
+  return launch_wide((const void*)sample_wide_kernel<T>, rows, smem, a, st);
 }
 template <typename T>
-cudaError_t launch_accept(const FilterArgs& a, int64_t b, cudaStream_t st) {
+cudaError_t launch_accept(FilterArgs a, int64_t b, cudaStream_t st) {
   const int64_t rows = b * a.rows_used;
   const size_t smem = sizeof(Shared<kThr, kShortCap>);
-  cudaError_t e = launch_rows((const void*)accept_rows_kernel<T>, rows, pick_parts(a.V, rows, sizeof(T)), smem, a, st);
+  const int parts = pick_parts(a.V, rows, sizeof(T));
+  a.defer = defers(a.V, sizeof(T), parts);
+  cudaError_t e = launch_rows((const void*)accept_rows_kernel<T>, rows, parts, smem, a, st);
   if (e != cudaSuccess) return e;
+  if (a.defer && (e = launch_wide((const void*)accept_wide_kernel<T>, rows, smem, a, st)) != cudaSuccess) return e;
   return launch_rows((const void*)accept_pick_kernel<T>, b, pick_parts(a.V, b, sizeof(T)), smem, a, st);
 }
 template <typename T>
@@ -1388,6 +1614,7 @@ void finish(FilterArgs& a) {
   a.idx_bits = 0;
   while (((int64_t)1 << a.idx_bits) < a.V) ++a.idx_bits;
   a.scale = ldexpf(1.f, 62 - a.idx_bits);
+  a.unit = ldexpf(1.f, a.idx_bits - 62);
 }
 
 }  // namespace

@@ -216,7 +216,7 @@ struct RowCut {  // one verified row
   float m;       // the row's maximum
   int accept;    // the row's draft token is accepted
   int tok;       // the token drawn where it is not; -2: still to be drawn
-  int pad;
+  int deferred;  // the row is left to the wide kernel
 };
 struct FilterArgs {
   const void* logits;  // [rows] of V entries, ld apart
@@ -246,6 +246,8 @@ struct FilterArgs {
   int* status;
   int idx_bits;    // set by the launchers: bits of V - 1, scale of the weights
   float scale;
+  float unit;      // 1 / scale
+  int defer;       // rows without a short list are left to a second launch
 };
 cudaError_t filter_sample(FilterArgs a, int dtype, int64_t rows, cudaStream_t st);
 cudaError_t filter_accept(FilterArgs a, int dtype, int64_t b, cudaStream_t st);
