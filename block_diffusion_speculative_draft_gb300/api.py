@@ -29,7 +29,8 @@ EXPORTS = [
     "dflash_w8a16_linear_workspace_size", "dflash_w8a16_linear", "dflash_draft_block",
     "dflash_lmhead_workspace_size", "dflash_lmhead_argmax", "dflash_verify_workspace_size",
     "dflash_verify_accept", "dflash_verify_accept_noalloc", "dflash_verify_sample_workspace_size",
-    "dflash_verify_accept_sample", "dflash_sample", "dflash_verify_filtered_workspace_size",
+    "dflash_verify_accept_sample", "dflash_sample_workspace_size", "dflash_sample",
+    "dflash_verify_filtered_workspace_size",
     "dflash_verify_accept_filtered", "dflash_top_logits", "dflash_distill_loss", "dflash_distill_backward",
     "dflash_kv_commit", "dflash_commit_draft_block", "dflash_set_launch_mode",
     "dflash_get_launch_mode", "dflash_get_status",
@@ -100,7 +101,8 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "dflash_verify_sample_workspace_size": ([I32, I32, I64, PSZ], I32),
         "dflash_verify_accept_sample": ([P, P, I32, I32, I32, I64, ctypes.c_float, P, P, P, P, P, P, P, SZ, P],
                                         I32),
-        "dflash_sample": ([P, I32, I64, I64, I64, P, P, P, P, P, I64, P, P, P], I32),
+        "dflash_sample_workspace_size": ([I64, I64, PSZ], I32),
+        "dflash_sample": ([P, I32, I64, I64, I64, P, P, P, P, P, I64, P, P, P, SZ, P], I32),
         "dflash_verify_filtered_workspace_size": ([I32, I32, I64, PSZ], I32),
         "dflash_verify_accept_filtered": ([P, I32, I64, P, I32, I32, I32, I64, P, P, P, P, P, P, I64, P, P, P, P, P,
                                            SZ, P], I32),
@@ -349,12 +351,34 @@ def _on(dev, stream, fn, call):
             _check(fn, call(_stream(stream)))
 
 
-def dflash_sample(logits, temperature, u, tok_out, top_k=None, top_p=None, min_p=None, logprob_out=None, stream=None):
+def _workspace(fn, ws, nbytes, dev, stream):
+    """The given workspace, or one in memory that the call's own stream may
+    reuse (stream None: the current one)."""
+    torch = _torch()
+    if ws is None:
+        if stream is None:
+            return torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        with torch.cuda.stream(stream):
+            return torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    if ws.device != dev or not ws.is_contiguous():
+        raise ValueError(f"{fn}: ws must be contiguous and on {dev}")
+    return ws
+
+
+def dflash_sample_workspace_size(rows: int, V: int) -> int:
+    n = ctypes.c_size_t(0)
+    _check("dflash_sample_workspace_size", load_library().dflash_sample_workspace_size(rows, V, ctypes.byref(n)))
+    return n.value
+
+
+def dflash_sample(logits, temperature, u, tok_out, top_k=None, top_p=None, min_p=None, logprob_out=None, ws=None,
+                  stream=None):
     """One token per row of logits [rows][V] (fp32/fp16/bf16, contiguous rows),
     drawn from softmax(z / T) under the row's top-k, top-p and min-p filters.
     temperature, top_p, min_p fp32 [rows] and top_k int32 [rows] (filters may be
     None); u fp32 uniforms [rows][V]; tok_out int32 [rows]; logprob_out fp32
-    [rows] (may be None).  T = 0 takes the largest logit."""
+    [rows] (may be None).  T = 0 takes the largest logit.  ws: uint8 workspace
+    of dflash_sample_workspace_size bytes (allocated here when not given)."""
     fn = "dflash_sample"
     dt = _row_dtype(fn, logits)
     ld = _row_shape(fn, logits, 2)
@@ -364,9 +388,10 @@ def dflash_sample(logits, temperature, u, tok_out, top_k=None, top_p=None, min_p
     if u.dtype != torch.float32 or u.device != dev or tuple(u.shape) != (n, V):
         raise ValueError(f"{fn}: u must be float32 [{n}][{V}] on {dev}")
     lib = load_library()
+    ws = _workspace(fn, ws, 0 if ws is not None else dflash_sample_workspace_size(n, V), dev, stream)
     _on(dev, stream, fn, lambda st: lib.dflash_sample(
         logits.data_ptr(), dt, n, V, ld, temperature.data_ptr(), _ptr(top_k), _ptr(top_p), _ptr(min_p), u.data_ptr(),
-        _row_shape(fn, u, 2), tok_out.data_ptr(), _ptr(logprob_out), st))
+        _row_shape(fn, u, 2), tok_out.data_ptr(), _ptr(logprob_out), ws.data_ptr(), ws.numel() * ws.element_size(), st))
 
 
 def dflash_verify_filtered_workspace_size(b: int, R: int, V: int) -> int:
@@ -396,11 +421,7 @@ def dflash_verify_accept_filtered(logits, draft, temperature, u_accept, u_sample
     _need(fn, dev, torch.int32, (b, R), emitted=emitted)
     if u_sample.dtype != torch.float32 or u_sample.device != dev or tuple(u_sample.shape) != (b, V):
         raise ValueError(f"{fn}: u_sample must be float32 [{b}][{V}] on {dev}")
-    if ws is None:
-        with torch.cuda.stream(stream):  # memory that the call's own stream may reuse (None: the current one)
-            ws = torch.empty(dflash_verify_filtered_workspace_size(b, R, V), dtype=torch.uint8, device=dev)
-    elif ws.device != dev or not ws.is_contiguous():
-        raise ValueError(f"{fn}: ws must be contiguous and on {dev}")
+    ws = _workspace(fn, ws, 0 if ws is not None else dflash_verify_filtered_workspace_size(b, R, V), dev, stream)
     lib = load_library()
     _on(dev, stream, fn, lambda st: lib.dflash_verify_accept_filtered(
         logits.data_ptr(), dt, ld, draft.data_ptr(), b, R, D, V, temperature.data_ptr(), _ptr(top_k), _ptr(top_p),

@@ -506,11 +506,19 @@ static int check_rows(const void* logits, int32_t dtype, int64_t rows, int64_t V
 }
 static bool row_temperature(float t) { return t >= kFilterMinT && t <= kFilterMaxT; }
 
+int32_t dflash_sample_workspace_size(int64_t rows, int64_t V, size_t* bytes) {
+  if (!bytes || rows < 1 || rows >= (int64_t)1 << 28 || V < 1) return DFLASH_EINVAL;
+  *bytes = (size_t)rows * sizeof(RowState);
+  return DFLASH_OK;
+}
+
 int32_t dflash_sample(const void* logits, int32_t dtype, int64_t rows, int64_t V, int64_t ld,
                       const float* temperature, const int32_t* top_k, const float* top_p, const float* min_p,
-                      const float* u, int64_t ld_u, int32_t* tok_out, float* logprob_out, void* stream) {
+                      const float* u, int64_t ld_u, int32_t* tok_out, float* logprob_out, void* ws, size_t ws_bytes,
+                      void* stream) {
   if (int r = check_rows(logits, dtype, rows, V, ld)) return r;
   if (!temperature || !u || !tok_out || ld_u < V) return DFLASH_EINVAL;
+  if (!ws || ws_bytes < (size_t)rows * sizeof(RowState) || !aligned16(ws)) return DFLASH_EWORKSPACE;
   FilterArgs a;
   memset(&a, 0, sizeof(a));
   a.logits = logits;
@@ -523,6 +531,7 @@ int32_t dflash_sample(const void* logits, int32_t dtype, int64_t rows, int64_t V
   a.u = u;
   a.ld_u = ld_u;
   a.tok = tok_out;
+  a.states = static_cast<RowState*>(ws);
   a.logprob = logprob_out;
   if (!(a.status = status_ptr())) return DFLASH_ECUDA;
   return map_err(filter_sample(a, dtype, rows, static_cast<cudaStream_t>(stream)));

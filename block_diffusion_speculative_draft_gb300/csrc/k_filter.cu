@@ -70,6 +70,7 @@ struct alignas(16) Shared {
   Exchange<NT / 32> x;
   uint64_t total[kMaxCluster];       // a level's sum over each CTA's share of the bins
   uint64_t pick[3];                  // a level's choice: bin, sum before it, its count
+  int beside[2];                     // the bins before and after it that hold entries
   uint64_t warp_sum[NT / 32];
   uint64_t list_mass[kMaxCluster];   // what each CTA put on the list, by weight and by count
   uint32_t list_count[kMaxCluster];
@@ -94,6 +95,7 @@ struct alignas(16) Shared {
   uint64_t join[NT / 32][3];
   float val;
   uint32_t bar;                      // key of the best score seen by any thread of the CTA
+  int64_t rows[64];                  // a cluster's rows of a second launch
 };
 
 // One row as a cluster sees it.  Each CTA reads its part of the row from
@@ -494,17 +496,19 @@ __device__ __forceinline__ void scan_and_draw(const Row<T, NT>& r, Shared<NT, kC
         any = true;
         odd |= !(fabsf(ref) < kRefMax);
       }
+      const float seen = key_to_value(*reinterpret_cast<volatile uint32_t*>(&s.bar));
+      const float bar = seen * 1.4426950408889634f - 0.0009765625f - fabsf(seen) * 1e-5f;
+      const float reach = fminf(fast_exp2(bar - t.ref), 1e30f);
       float v[kE], some = 0.f, peak = -INFINITY;
       Row<T, NT>::open_pack(w[x], v);
 #pragma unroll
       for (int h = 0; h < kE; ++h) {
-        some += fast_exp2(fmaf(v[h], r.c, -t.ref));
-        peak = fmaxf(peak, fmaf(v[h], r.c, -fast_log2(1.f - uu[x][h])));
+        const float e = fast_exp2(fmaf(v[h], r.c, -t.ref));
+        some += e;
+        peak = fmaxf(peak, fmaf(uu[x][h], reach, e));  // w >= 2^bar (1 - u)
       }
       t.sum += some;
-      const float seen = key_to_value(*reinterpret_cast<volatile uint32_t*>(&s.bar));
-      const float bar = seen * 1.4426950408889634f - 0.0009765625f - fabsf(seen) * 1e-5f;
-      if (!(peak < bar)) {
+      if (peak >= reach) {
         const int i = static_cast<int>(r.index_of(j + x * NT));
 #pragma unroll 1
         for (int h = 0; h < kE; ++h) {
@@ -601,32 +605,40 @@ __device__ __forceinline__ void list_entries(const Row<T, NT>& r, Shared<NT, kCa
     if (sc.group[x] >= t && sc.group[x] > -INFINITY)
       queue[atomicAdd(&s.queued, 1u)] = static_cast<uint16_t>(threadIdx.x + x * NT);
   __syncthreads();
-  const int lane = threadIdx.x & 31;
+  if (s.queued > kCap) {  // more groups than the list holds entries
+    if (threadIdx.x == 0) s.own_count = kCap + 1;
+    return;
+  }
   uint32_t* taken = peer(&s.taken, 0);
   uint64_t* list = peer(s.list, 0);
   const uint32_t deep = (r.part.packs + kGroups * NT - 1) / (kGroups * NT), units = s.queued * deep;
-  for (uint32_t y = threadIdx.x; y < units; y += NT) {
-    const uint32_t g = y / deep;
-    const int j = queue[g] + static_cast<int>(y - g * deep) * (kGroups * NT);
-    if (j >= r.part.packs) continue;
-    const uint4 w = r.pack(j);
-    if (!(Row<T, NT>::max_of(Row<T, NT>::max_pack(w)) >= t)) continue;
-    float v[kE];
-    Row<T, NT>::open_pack(w, v);
-    const int64_t i = r.index_of(j);
+  for (uint32_t y0 = threadIdx.x; y0 < units; y0 += 4 * NT) {
+    uint4 w[4];
+    int at[4];
 #pragma unroll
-    for (int h = 0; h < kE; ++h) {
-      if (v[h] >= t && v[h] > -INFINITY) {
-        const unsigned act = __activemask();
-        const int first = __ffs(act) - 1;
-        uint32_t base = 0;
-        if (lane == first) {
-          base = atomicAdd(taken, static_cast<uint32_t>(__popc(act)));
-          atomicAdd(&s.own_count, static_cast<uint32_t>(__popc(act)));
-        }
-        base = __shfl_sync(act, base, first) + __popc(act & ((1u << lane) - 1));
-        if (base < kCap) list[base] = place_of(value_key(v[h]), static_cast<uint32_t>(i + h));
-        if (want_mass) atomicAdd(reinterpret_cast<unsigned long long*>(&s.own_mass), r.weight(v[h]));
+    for (int x = 0; x < 4; ++x) {
+      const uint32_t y = y0 + x * NT, g = y / deep;
+      at[x] = y < units ? queue[g] + static_cast<int>(y - g * deep) * (kGroups * NT) : r.part.packs;
+      w[x] = r.pack(at[x]);
+    }
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      float v[kE];
+      Row<T, NT>::open_pack(w[x], v);
+      uint32_t hits = 0;
+#pragma unroll
+      for (int h = 0; h < kE; ++h) hits |= (v[h] >= t && v[h] > -INFINITY ? 1u : 0u) << h;
+      if (hits == 0) continue;
+      uint32_t base = atomicAdd(taken, static_cast<uint32_t>(__popc(hits)));
+      atomicAdd(&s.own_count, static_cast<uint32_t>(__popc(hits)));
+      const int64_t i = r.index_of(at[x]);
+      while (hits) {
+        const int h = __ffs(hits) - 1;
+        hits &= hits - 1;
+        const float z = Row<T, NT>::pick_of(w[x], h);
+        if (base < kCap) list[base] = place_of(value_key(z), static_cast<uint32_t>(i + h));
+        ++base;
+        if (want_mass) atomicAdd(reinterpret_cast<unsigned long long*>(&s.own_mass), r.weight(z));
       }
     }
   }
@@ -834,22 +846,14 @@ struct Verdict {
   float val;     // its logit
 };
 
-// Filters a short list and draws from it.  Up to kQuick entries, each one's
-// rank and the sum of the weights before it come from comparing it with all
-// others (two threads an entry), which needs neither a sort nor a scan; longer
-// lists are sorted.  above, whole: as in filter_list.
+// Filters a list of at most kQuick entries and draws from it: each one's rank
+// and the sum of the weights before it come from comparing it with all others
+// (two threads an entry), which needs neither a sort nor a scan.  above, whole:
+// as in filter_list.
 template <typename T, int NT, int kCap>
-__device__ __noinline__ Verdict settle_list(const Row<T, NT>& r, Shared<NT, kCap>& s, const Ask& q, int n, uint64_t above,
-                                            uint64_t whole, const float* u, int drop) {
+__device__ __noinline__ Verdict quick_list(const Row<T, NT>& r, Shared<NT, kCap>& s, const Ask& q, int n,
+                                           uint64_t above, uint64_t whole, const float* u, int drop) {
   Verdict out;
-  if (n > kQuick) {
-    sort_list<NT>(s.list, n);
-    const int kept = filter_list(r, s, q, n, above, whole, &out.mass);
-    out.cut = s.list[kept - 1];
-    out.tok = u ? pick_listed(r, s, u, kept, drop, q.T) : -1;
-    out.val = out.tok >= 0 ? r.at(out.tok) : 0.f;
-    return out;
-  }
   static_assert(NT == 2 * kQuick, "two threads an entry");
   const int e = threadIdx.x & (kQuick - 1), half = threadIdx.x / kQuick;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -1056,59 +1060,268 @@ __device__ __forceinline__ float cluster_mass(Row<T, NT>& r, Shared<NT, kCap>& s
   return d;
 }
 
+// One pass over a row of which many entries may be kept: those with v > over (or
+// v >= over, kFrom).  Their weights are summed, and with kDraw the best of them
+// found; entries with under < v that are not kept go to the CTA's own list.
+// Decisions are taken per pack, so that a warp leaves the straight path for the
+// few packs that hold a candidate.
+template <bool kDraw, bool kFrom, int kCap, typename T, int NT>
+__device__ __forceinline__ float deep_pass(const Row<T, NT>& r, Shared<NT, kCap>& s, const float* u, float over,
+                                           float under, Best* best) {
+  constexpr int kE = Row<T, NT>::kE, kB = 16 / kE;  // packs in flight
+  const float* u0 = u + (r.part.first - r.part.off);
+  const bool wide = (reinterpret_cast<uintptr_t>(u0) & 15) == 0;
+  const float m = r.m, c = r.c;
+  float sum = 0.f;
+  uint64_t listed = 0;
+  for (int j = threadIdx.x; j < r.part.packs; j += kB * NT) {
+    uint4 w[kB];
+    float uu[kB][kE];
+#pragma unroll
+    for (int x = 0; x < kB; ++x) {
+      w[x] = r.pack(j + x * NT);
+      if (kDraw) r.uniforms(u, u0, wide, j + x * NT, uu[x]);
+    }
+    // the CTA's best so far in units of log2, less 2^-10 to be safe: whatever
+    // comes near the final best is scored
+    const float seen = key_to_value(*reinterpret_cast<volatile uint32_t*>(&s.bar));
+    const float bar = seen * 1.4426950408889634f - 0.0009765625f - fabsf(seen) * 1e-5f;
+    const float reach = fminf(fast_exp2(bar), 1e30f);
+#pragma unroll
+    for (int x = 0; x < kB; ++x) {
+      if (!(Row<T, NT>::max_of(Row<T, NT>::max_pack(w[x])) >= under)) continue;
+      float v[kE], some = 0.f, peak = -INFINITY;
+      bool edge = false;
+      Row<T, NT>::open_pack(w[x], v);
+#pragma unroll
+      for (int h = 0; h < kE; ++h) {
+        const bool k = kFrom ? v[h] >= over : v[h] > over;
+        const float e = fast_exp2((v[h] - m) * c);
+        if (k) some += e;
+        // the bound in the weights' own terms: w >= 2^bar (1 - u)
+        if (kDraw && k) peak = fmaxf(peak, fmaf(uu[x][h], reach, e));
+        if (!kFrom) edge |= !k && v[h] > under;
+      }
+      sum += some;
+      const int i = static_cast<int>(r.index_of(j + x * NT));
+      if (kDraw && peak >= reach) {
+#pragma unroll 1
+        for (int h = 0; h < kE; ++h) {
+          const float z = Row<T, NT>::pick_of(w[x], h), t = pick_float<kE>(uu[x], h), y = (z - m) * c;
+          if ((kFrom ? z >= over : z > over) && !(y - fast_log2(1.f - t) < bar)) offer(*best, z, i + h, y, t);
+        }
+        const uint32_t key = value_key(best->score);
+        if (key > *reinterpret_cast<volatile uint32_t*>(&s.bar)) atomicMax(&s.bar, key);
+      }
+      if (!kFrom && edge) {
+        uint32_t hits = 0;
+#pragma unroll
+        for (int h = 0; h < kE; ++h) hits |= (v[h] > under && !(v[h] > over) ? 1u : 0u) << h;
+        uint32_t at = atomicAdd(&s.own_count, static_cast<uint32_t>(__popc(hits)));
+        while (hits) {
+          const int h = __ffs(hits) - 1;
+          hits &= hits - 1;
+          const float z = Row<T, NT>::pick_of(w[x], h);
+          if (at < kCap) s.list[at] = place_of(value_key(z), static_cast<uint32_t>(i + h));
+          ++at;
+          listed += r.weight(z);
+        }
+      }
+    }
+  }
+  if (!kFrom && listed) atomicAdd(reinterpret_cast<unsigned long long*>(&s.own_mass), listed);
+  return sum;
+}
+
+// Best entry of rank 0's threads (see join_best).
+template <typename T, int NT, int kCap>
+__device__ int join_best_cta(const Row<T, NT>& r, Shared<NT, kCap>& s, const float* u, const Best& b, float temp) {
+  const uint64_t win = cta_reduce<NT / 32>(b.at >= 0 ? argmax_key(b.score, static_cast<uint32_t>(b.at)) : 0ull,
+                                           OpMaxU64(), s.x);
+  if (win == 0) return -1;
+  const bool close = b.at >= 0 && near_best(b.score, key_value(win));
+  if (__syncthreads_count(close) <= 1) return static_cast<int>(key_index(win));
+  const uint64_t dk = close ? double_key(score64(b.val, r.m, temp, u[b.at])) : 0ull;
+  const uint64_t dbest = cta_reduce<NT / 32>(dk, OpMaxU64(), s.x);
+  const uint64_t low = close && dk == dbest ? 0xFFFFFFFFull - static_cast<uint32_t>(b.at) : 0ull;
+  return static_cast<int>(0xFFFFFFFFull - cta_reduce<NT / 32>(low, OpMaxU64(), s.x));
+}
+
+// A long list that top-k does not cut (rank 0's threads).  Top-p's border is
+// found by 256 bins, linear in the value over the list, of exact weights; the
+// border's bin leaves a few entries to rank.  `above` is the weight before the
+// list, `whole` what top-p refers to.  With u the kept entries but `drop` are
+// offered to `best`.
+template <typename T, int NT, int kCap>
+__device__ Verdict long_list(const Row<T, NT>& r, Shared<NT, kCap>& s, const Ask& q, int n, uint64_t above,
+                             uint64_t whole, const float* u, int drop, Best* best) {
+  static_assert(NT == 256 && kCap % NT == 0 && sizeof(s.line) >= 256 * sizeof(uint64_t), "one thread a bin");
+  constexpr int kMine = kCap / NT;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const float bound = q.mp > 0.f ? s.bound : -INFINITY;
+  unsigned long long* sub = reinterpret_cast<unsigned long long*>(s.line);
+  uint64_t place[kMine], all = 0, low = ~0ull, high = 0;
+  sub[threadIdx.x] = 0;
+#pragma unroll
+  for (int x = 0; x < kMine; ++x) {
+    const int i = threadIdx.x + x * NT;
+    place[x] = i < n ? s.list[i] : 0;
+    if (i < n && key_to_value(static_cast<uint32_t>(place[x] >> 32)) < bound) place[x] = 0;  // min-p drops it
+    if (place[x]) {
+      all += r.weight(key_to_value(static_cast<uint32_t>(place[x] >> 32)));
+      low = place[x] < low ? place[x] : low;
+      high = place[x] > high ? place[x] : high;
+    }
+  }
+  Verdict out{0, 0, -1, 0.f};
+  all = cta_reduce<NT / 32>(all, OpSumU64(), s.x);
+  low = ~cta_reduce<NT / 32>(~low, OpMaxU64(), s.x);
+  out.mass = above + all;
+  out.cut = low;
+  if (q.p < 1.f) {
+    set_need(s, q.p, whole);
+    if (threadIdx.x == 0) s.taken = 0;
+    high = cta_reduce<NT / 32>(high, OpMaxU64(), s.x);
+    if (out.mass > s.need) {  // the border is among these entries
+      const float from = key_to_value(static_cast<uint32_t>(high >> 32)),
+                  range = from - key_to_value(static_cast<uint32_t>(low >> 32));
+      const float per = range > 1e-30f ? 255.99f / range : 0.f;
+      int bin[kMine];
+#pragma unroll
+      for (int x = 0; x < kMine; ++x) {
+        const float v = key_to_value(static_cast<uint32_t>(place[x] >> 32));
+        const int b = place[x] ? static_cast<int>((from - v) * per) : 256;
+        bin[x] = b < 0 ? 0 : (place[x] && b > 255 ? 255 : b);
+        if (place[x]) atomicAdd(&sub[bin[x]], r.weight(v));
+      }
+      __syncthreads();
+      const uint64_t mine = sub[threadIdx.x], need = s.need;
+      uint64_t inc = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint64_t y = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += y;
+      }
+      if (lane == 31) s.warp_sum[warp] = inc;
+      __syncthreads();
+      uint64_t before = above + inc - mine;
+      for (int w = 0; w < warp; ++w) before += s.warp_sum[w];
+      if (before < need && before + mine >= need) {
+        s.pick[0] = threadIdx.x;
+        s.pick[1] = before;
+      }
+      __syncthreads();
+      const int at = static_cast<int>(s.pick[0]);
+#pragma unroll
+      for (int x = 0; x < kMine; ++x)
+        if (bin[x] == at) s.list[atomicAdd(&s.taken, 1u)] = place[x];
+      __syncthreads();
+      const int few = static_cast<int>(s.taken);
+      const uint64_t over = s.pick[1];
+      if (few <= kQuick) {
+        out = quick_list(r, s, q, few, over, whole, static_cast<const float*>(nullptr), -1);
+      } else {  // ties
+        sort_list<NT>(s.list, few);
+        const int kept = filter_list(r, s, q, few, over, whole, &out.mass);
+        out.cut = s.list[kept - 1];
+      }
+    }
+  }
+  out.tok = -1;
+  if (u) {
+#pragma unroll
+    for (int x = 0; x < kMine; ++x) {
+      if (place[x] && place[x] >= out.cut) {
+        const float v = key_to_value(static_cast<uint32_t>(place[x] >> 32));
+        const int i = static_cast<int>(place_index(place[x]));
+        if (i != drop) offer(*best, v, i, r.log2w(v), u[i]);
+      }
+    }
+  }
+  return out;
+}
+
+// Filters a list and draws from it (rank 0's threads).
+template <typename T, int NT, int kCap>
+__device__ __forceinline__ Verdict settle_list(const Row<T, NT>& r, Shared<NT, kCap>& s, const Ask& q, int n,
+                                               uint64_t whole, const float* u, int drop) {
+  if (n <= kQuick) return quick_list(r, s, q, n, 0, whole, u, drop);
+  Verdict out;
+  if (q.k >= n && (q.p >= 1.f || whole > 0)) {
+    Best best{-INFINITY, 0.f, -1};
+    out = long_list(r, s, q, n, 0, whole, u, drop, &best);
+    if (u) out.tok = join_best_cta(r, s, u, best, q.T);
+  } else {
+    sort_list<NT>(s.list, n);
+    const int kept = filter_list(r, s, q, n, 0, whole, &out.mass);
+    out.cut = s.list[kept - 1];
+    out.tok = u ? pick_listed(r, s, u, kept, drop, q.T) : -1;
+  }
+  out.val = out.tok >= 0 ? r.at(out.tok) : 0.f;
+  return out;
+}
+
 // Top-p over the whole row where its border lies deep in the row.  A histogram
-// linear in the logit, of weights relative to their bin's upper edge (integers:
+// linear in the logit, of weights relative to their bin's middle (integers:
 // nearly equal within a bin, exact sums), finds the bin of the border; a second
 // pass sums the weights above that bin, draws among them (`u` given) and lists
-// the bin's own entries, which are sorted and filtered as a short list is.
-// False: the border fell too close to a bin's edge, or the bin does not fit the
-// list.  Else rank 0 holds the list, of which it keeps *kept.
+// the bin's own entries.  False: the border fell too close to a bin's edge, or
+// the bin does not fit the list.  Else rank 0 has the verdict, and the draw is
+// left in `best` of the cluster's threads.
 template <typename T, int NT, int kCap>
 __device__ __noinline__ bool deep_top_p(Row<T, NT>& r, Shared<NT, kCap>& s, const Ask& q, int64_t V, float row_mass,
-                                        const float* u, int* kept, uint64_t* kept_mass, Best* best) {
+                                        const float* u, Best* best, Verdict* out) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint64_t whole = __float2ull_rn(row_mass * r.scale);
-  // entries this far below the maximum sum to less than (1 - p) / 2 of the row
-  const float span = logf(2.f * static_cast<float>(V) / ((1.f - q.p) * row_mass)) * q.T;
-  if (!(fabsf(r.m) < 1e20f) || !(span > 1e-6f * fabsf(r.m)) || !(span < 1e20f)) return false;
-  const float per = kLineBins / span, step = r.c / per;  // log2 of a bin's fall
+  // entries this far below the maximum, in units of log2, sum to less than
+  // (1 - p) / 2 of the row
+  const float span = log2f(2.f * static_cast<float>(V) / ((1.f - q.p) * row_mass));
+  if (!(fabsf(r.m) < 1e30f) || !(span > 0.f) || !(span < 1e6f)) return false;
+  const float per = kLineBins / span, step = span / kLineBins;
   // the unit of the bins' integers: 2^31 holds every entry of the longest part
   const int most = static_cast<int>(V / r.size) + 2 * Part<T>::kE;
-  const float one = static_cast<float>(0x80000000u >> (32 - __clz(most - 1)));
+  const float one = fminf(static_cast<float>(0x80000000u >> (32 - __clz(most - 1))), 2097152.f);
   for (int b = threadIdx.x; b < kLineBins; b += NT) s.line[b] = 0;
   if (threadIdx.x == 0) {
     s.own_count = 0;
     s.own_mass = 0;
-    s.taken = 0;
     s.pick[0] = kLineBins;
+    s.beside[0] = -1;
+    s.beside[1] = kLineBins;
     s.bar = 0x007FFFFFu;  // -inf
   }
   set_need(s, q.p, whole);
   __syncthreads();
-  const float m = r.m, from = m * per;
-  const auto line = [=](float v) { return fmaf(v, -per, from); };  // bins below the maximum
+  const float m = r.m, c = r.c;
+  // bin and weight without conversions or exponentials: adding 1.5 2^23 rounds a
+  // float to an integer in its low bits, and within half a bin 2^(-f step) is a
+  // parabola to (step ln 2)^3 / 48
+  const float magic = 12582912.f, t1 = -step * kLn2 * one, t2 = 0.5f * step * kLn2 * step * kLn2 * one;
+  const float slope = -c * per;
   r.each([&](float v, int64_t) {
-    const float d = line(v);
-    if (d < static_cast<float>(kLineBins)) {
-      const int b = static_cast<int>(d);
-      atomicAdd(&s.line[b], __float2uint_rn(fast_exp2((static_cast<float>(b) - d) * step) * one));
+    const float d = (v - m) * slope;
+    if (d < static_cast<float>(kLineBins) - 0.5f) {
+      const float near = d + magic, f = d - (near - magic);
+      const float part = fmaf(fmaf(t2, f, t1), f, one) + magic;
+      atomicAdd(&s.line[__float_as_int(near) & (kLineBins - 1)],
+                static_cast<uint32_t>(__float_as_int(part) - __float_as_int(magic)));
     }
   });
   cluster_sync_all(r.size);
   constexpr int kMine = kLineBins / NT;
   static_assert(kMine == 4, "a thread's bins are one 16-byte load");
   const uint64_t need = s.need;
-  uint4 c[kMaxCluster];
+  uint4 bins[kMaxCluster];
 #pragma unroll
   for (uint32_t o = 0; o < kMaxCluster; ++o)
-    c[o] = o < r.size ? *peer(reinterpret_cast<const uint4*>(s.line) + threadIdx.x, o) : make_uint4(0, 0, 0, 0);
+    bins[o] = o < r.size ? *peer(reinterpret_cast<const uint4*>(s.line) + threadIdx.x, o) : make_uint4(0, 0, 0, 0);
   float h[kMine] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
   for (uint32_t o = 0; o < kMaxCluster; ++o) {
-    h[0] += static_cast<float>(c[o].x);
-    h[1] += static_cast<float>(c[o].y);
-    h[2] += static_cast<float>(c[o].z);
-    h[3] += static_cast<float>(c[o].w);
+    h[0] += static_cast<float>(bins[o].x);
+    h[1] += static_cast<float>(bins[o].y);
+    h[2] += static_cast<float>(bins[o].z);
+    h[3] += static_cast<float>(bins[o].w);
   }
   uint64_t mine[kMine], sum = 0;
 #pragma unroll
@@ -1133,51 +1346,70 @@ __device__ __noinline__ bool deep_top_p(Row<T, NT>& r, Shared<NT, kCap>& s, cons
     before += mine[x];
   }
   __syncthreads();
-  const int bin = static_cast<int>(s.pick[0]);
+  int bin = static_cast<int>(s.pick[0]);
   if (bin == kLineBins) return false;
-  // second pass; each CTA lists its entries of the bin in its own memory
-  const float edge = static_cast<float>(bin), end = edge + 1.f;
-  float w = 0.f;
-  uint64_t listed = 0;
-  const float low = m - end / per * 1.0001f - fabsf(m) * 1e-6f;  // no entry of the bin lies below
-  auto visit = [&](float v, int i) {
-    const float d = line(v);
-    if (d < edge) {
-      w += fast_exp2((v - m) * r.c);
-      return true;
-    }
-    if (d < end) {
-      const uint32_t at = atomicAdd(&s.own_count, 1u);
-      if (at < kCap) s.list[at] = place_of(value_key(v), static_cast<uint32_t>(i));
-      listed += r.weight(v);
-    }
-    return false;
-  };
-  if (u) {
-    draw_pass<true>(r, s, u, low, *best, visit);
-  } else {
-    r.each([&](float v, int64_t i) {
-      if (v >= low) visit(v, static_cast<int>(i));
-    });
+#pragma unroll
+  for (int x = 0; x < kMine; ++x) {
+    const int b = threadIdx.x * kMine + x;
+    if (mine[x] && b < bin) atomicMax(&s.beside[0], b);
+    if (mine[x] && b > bin) atomicMin(&s.beside[1], b);
   }
-  if (listed) atomicAdd(reinterpret_cast<unsigned long long*>(&s.own_mass), listed);
-  const uint64_t above = __float2ull_rn(cluster_mass(r, s, w) * r.scale);
+  // second pass: exact sums, by values in place of bins.  Where rounding put the
+  // border into a neighbour of its bin they tell, and the next bin that holds
+  // entries is taken.
+  uint64_t above;
   uint32_t count;
-  uint64_t mass;
-  close_list(r, s, &count, &mass);
-  if (r.rank != 0 && count <= kCap) {  // behind the entries of the CTAs before
+  for (int attempt = 0;; ++attempt) {
+    const float over = m - (static_cast<float>(bin) - 0.5f) * step / c;
+    const float under = m - (static_cast<float>(bin) + 0.5f) * step / c;
+    const float w = u ? deep_pass<true, false>(r, s, u, over, under, best)
+                      : deep_pass<false, false>(r, s, u, over, under, best);
+    above = __float2ull_rn(cluster_mass(r, s, w) * r.scale);
+    uint64_t mass;
+    close_list(r, s, &count, &mass);
+    if (count <= kCap && above < need && above + mass >= need) break;
+    bin = s.beside[above >= need ? 0 : 1];
+    if (attempt == 1 || count > kCap || bin < 0 || bin >= kLineBins) return false;
+    if (best) *best = Best{-INFINITY, 0.f, -1};
+    if (threadIdx.x == 0) {
+      s.own_count = 0;
+      s.own_mass = 0;
+      s.bar = 0x007FFFFFu;  // -inf
+    }
+    __syncthreads();
+  }
+  if (r.rank != 0) {  // behind the entries of the CTAs before
     uint32_t at = 0;
     for (uint32_t o = 0; o < r.rank; ++o) at += s.list_count[o];
     uint64_t* list = peer(s.list, 0);
     for (uint32_t i = threadIdx.x; i < s.own_count; i += NT) list[at + i] = s.list[i];
   }
   cluster_sync_all(r.size);
-  if (count > kCap || above >= need || above + mass < need) return false;
   if (r.rank == 0) {
-    sort_list<NT>(s.list, static_cast<int>(count));
-    *kept = filter_list(r, s, q, static_cast<int>(count), above, whole, kept_mass);
+    if (count <= kQuick) {
+      *out = quick_list(r, s, q, static_cast<int>(count), above, whole, static_cast<const float*>(nullptr), -1);
+      if (u && threadIdx.x < count && s.list[threadIdx.x] >= out->cut) {
+        const uint32_t i = place_index(s.list[threadIdx.x]);
+        const float v = key_to_value(static_cast<uint32_t>(s.list[threadIdx.x] >> 32));
+        offer(*best, v, static_cast<int>(i), r.log2w(v), u[i]);
+      }
+    } else {
+      *out = long_list(r, s, q, static_cast<int>(count), above, whole, u, -1, best);
+    }
   }
   return true;
+}
+
+// Min-p alone over a row of which it keeps many entries: their mass, and the
+// draw left in `best`.
+template <typename T, int NT, int kCap>
+__device__ __noinline__ uint64_t deep_min_p(Row<T, NT>& r, Shared<NT, kCap>& s, const float* u, Best* best) {
+  const float low = s.bound;
+  if (threadIdx.x == 0) s.bar = 0x007FFFFFu;  // -inf
+  __syncthreads();
+  const float w =
+      u ? deep_pass<true, true>(r, s, u, low, low, best) : deep_pass<false, true>(r, s, u, low, low, best);
+  return __float2ull_rn(cluster_mass(r, s, w) * r.scale);
 }
 
 // The cut and the kept mass of any row, by radix descents.
@@ -1248,7 +1480,7 @@ __device__ bool listed_row(Row<T, NT>& r, Shared<NT, kCap>& s, const Scan<T, NT>
   if (of_row && __ull2float_rz(mass) < q.p * __ull2float_ru(whole) * 1.000001f && static_cast<int64_t>(count) < a.V &&
       !(q.mp > 0.f && s.bound >= t))
     return false;
-  if (r.rank == 0) *out = settle_list(r, s, q, static_cast<int>(count), 0, whole, u, drop);
+  if (r.rank == 0) *out = settle_list(r, s, q, static_cast<int>(count), whole, u, drop);
   return true;
 }
 
@@ -1283,13 +1515,54 @@ constexpr int kShortCap = 1024;
 constexpr int kThr = 256;
 
 constexpr int kDeferred = -2;  // tok of a row that is left to the wide kernel, or whose draw is
+using Short = Shared<kThr, kShortCap>;
 
-// The lists' kernels run few CTAs a row; a row that needs more passes is left
-// to a second launch, whose clusters of eight share out such rows, unless the
-// first has as many CTAs a row already.
-template <typename T, bool kWide>
-__device__ __forceinline__ void sample_row(const FilterArgs& a, Shared<kThr, kShortCap>& s, int64_t row) {
+// A row without a short list: its mass and cut, and with u the token drawn.
+// mass and cut are known to rank 0's threads, the token to all.
+template <typename T>
+__device__ __forceinline__ int wide_row(Row<T, kThr>& r, Short& s, const FilterArgs& a, const Ask& q, float row_mass,
+                                        const float* u, Verdict* v) {
+  Best best{-INFINITY, 0.f, -1};
+  const bool ordinary = q.k >= a.V && fabsf(r.m) < 1e30f;
+  if (q.mp > 0.f) {
+    set_bound(s, r.m, q);
+    __syncthreads();
+  }
+  if (ordinary && q.p < 1.f && q.mp == 0.f && deep_top_p(r, s, q, a.V, row_mass, u, &best, v))
+    return u ? join_best(r, s, u, best, q.T) : -1;
+  if (ordinary && q.p >= 1.f && q.mp > 0.f) {
+    v->mass = deep_min_p(r, s, u, &best);
+    v->cut = place_of(value_key(s.bound), 0xFFFFFFFFu);
+    return u ? join_best(r, s, u, best, q.T) : -1;
+  }
+  if (q.k >= a.V && q.p >= 1.f && q.mp == 0.f) {  // nothing filters
+    v->mass = __float2ull_rn(row_mass * r.scale);
+    v->cut = 1ull << 32;
+  } else {
+    v->cut = wide_cut(r, s, a, q, &v->mass);
+  }
+  if (!u) return -1;
+  return q.greedy ? static_cast<int>(place_index(v->cut)) : pick_row(r, s, u, v->cut, -1, q.T);
+}
+
+template <typename T>
+__device__ __forceinline__ void write_sample(const FilterArgs& a, const Row<T, kThr>& r, int64_t row, int tok,
+                                             const Verdict& v, bool ok) {
+  if (r.rank != 0 || threadIdx.x != 0) return;
+  a.tok[row] = tok;
+  if (a.logprob) a.logprob[row] = tok >= 0 ? log_prob(r, tok == v.tok ? v.val : r.at(tok), v.mass) : -INFINITY;
+  if (!ok) atomicOr(a.status, kDevBadParam);
+}
+
+// Few CTAs serve a row whose filters leave a short list.  A row that needs more
+// passes is left to a second launch, whose clusters share out such rows, unless
+// this one has many CTAs a row already.
+template <typename T>
+__global__ void __launch_bounds__(kThr, 4) sample_rows_kernel(const FilterArgs a) {
+  extern __shared__ __align__(16) uint8_t raw[];
+  Short& s = *reinterpret_cast<Short*>(raw);
   const uint32_t size = cluster_size();
+  const int64_t row = blockIdx.x / size;
   start(s, size);
   const Ask q = read_ask(a, row);
   Row<T, kThr> r;
@@ -1299,79 +1572,122 @@ __device__ __forceinline__ void sample_row(const FilterArgs& a, Shared<kThr, kSh
   const float* u = a.u + row * a.ld_u;
   Scan<T, kThr> sc;
   Best best{-INFINITY, 0.f, -1};
-  if (!kWide && unfiltered) {
+  if (unfiltered) {
     scan_and_draw(r, s, u, sc, best);
   } else {
     scan_row(r, want_mass, sc);
   }
-  float low;
-  float row_mass;
+  float low, row_mass;
   const bool some = join_scan(r, s, sc, want_mass, &low, &row_mass);
-  int tok = -1;
-  float lp = -INFINITY;
+  int tok = -1, left = 0;
+  Verdict v{0, 0, -1, 0.f};
   if (q.ok && some) {
-    Verdict v{0, 0, -1, 0.f};
-    int n = 0;
-    if (!kWide && unfiltered && fabsf(r.m * r.c) < 1e3f) {
+    if (unfiltered && fabsf(r.m * r.c) < 1e3f) {
       v.mass = __float2ull_rn(row_mass * r.scale);
       tok = join_best(r, s, u, best, q.T);
-    } else if (!kWide && listed_row(r, s, sc, a, q, low, row_mass, u, -1, &v)) {
+    } else if (listed_row(r, s, sc, a, q, low, row_mass, u, -1, &v)) {
       if (r.rank != 0) return;
       tok = v.tok;
     } else if (a.defer) {
-      tok = kDeferred;
-    } else if (q.k >= a.V && q.p < 1.f && q.mp == 0.f &&
-               deep_top_p(r, s, q, a.V, row_mass, u, &n, &v.mass, &best)) {
-      if (r.rank == 0) {
-        for (int i = threadIdx.x; i < n; i += kThr) {
-          const uint32_t x = place_index(s.list[i]);
-          const float z = key_to_value(static_cast<uint32_t>(s.list[i] >> 32));
-          offer(best, z, static_cast<int>(x), r.log2w(z), u[x]);
-        }
-      }
-      tok = join_best(r, s, u, best, q.T);
+      left = 1;
     } else {
-      uint64_t cut = 1ull << 32;
-      if (unfiltered) {
-        v.mass = __float2ull_rn(row_mass * r.scale);
-      } else {
-        cut = wide_cut(r, s, a, q, &v.mass);
-      }
-      tok = q.greedy ? static_cast<int>(place_index(cut)) : pick_row(r, s, u, cut, -1, q.T);
+      tok = wide_row(r, s, a, q, row_mass, u, &v);
     }
-    if (tok >= 0 && threadIdx.x == 0) lp = log_prob(r, tok == v.tok ? v.val : r.at(tok), v.mass);
   }
-  if (r.rank == 0 && threadIdx.x == 0) {
-    a.tok[row] = tok;
-    if (a.logprob) a.logprob[row] = lp;
-    if (!q.ok) atomicOr(a.status, kDevBadParam);
-  }
+  if (a.defer && r.rank == 0 && threadIdx.x == 0) a.states[row] = RowState{r.m, row_mass, left};
+  if (!left) write_sample(a, r, row, tok, v, q.ok);
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kThr, 4) sample_rows_kernel(const FilterArgs a) {
-  extern __shared__ __align__(16) uint8_t raw[];
-  sample_row<T, false>(a, *reinterpret_cast<Shared<kThr, kShortCap>*>(raw), blockIdx.x / cluster_size());
+// Visits, in all CTAs of cluster `id` alike, its share of the rows that
+// left(row) tells: the id-th such row, and every `clusters`-th after it.
+template <typename L, typename F>
+__device__ __forceinline__ void share_rows(Short& s, int64_t rows, uint32_t id, uint32_t clusters, L left, F visit) {
+  constexpr int kEach = 8;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int64_t carry = 0;
+  for (int64_t base = 0; base < rows; base += kThr * kEach) {
+    uint32_t bits = 0;
+#pragma unroll
+    for (int x = 0; x < kEach; ++x) {
+      const int64_t i = base + threadIdx.x * kEach + x;
+      if (i < rows && left(i)) bits |= 1u << x;
+    }
+    const uint32_t n = __popc(bits);
+    uint32_t inc = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t y = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += y;
+    }
+    if (lane == 31) s.warp_sum[warp] = inc;
+    __syncthreads();
+    uint32_t before = inc - n, all = 0;
+    for (int w = 0; w < kThr / 32; ++w) {
+      if (w < warp) before += static_cast<uint32_t>(s.warp_sum[w]);
+      all += static_cast<uint32_t>(s.warp_sum[w]);
+    }
+    // ordinals id + t clusters, t >= first, are this cluster's
+    const int64_t first = carry > id ? (carry - id + clusters - 1) / clusters : 0;
+#pragma unroll
+    for (int x = 0; x < kEach; ++x) {
+      if (!(bits >> x & 1)) continue;
+      const int64_t ord = carry + before++;
+      if (ord % clusters == id) s.rows[ord / clusters - first] = base + threadIdx.x * kEach + x;
+    }
+    carry += all;
+    const int64_t end = carry > id ? (carry - id + clusters - 1) / clusters : 0;
+    __syncthreads();
+    for (int64_t t = first; t < end; ++t) visit(s.rows[t - first]);
+    __syncthreads();
+  }
 }
 
 template <typename T>
 __global__ void __launch_bounds__(kThr, 4) sample_wide_kernel(const FilterArgs a, const int64_t rows) {
   extern __shared__ __align__(16) uint8_t raw[];
+  Short& s = *reinterpret_cast<Short*>(raw);
   pdl_wait();
   const uint32_t size = cluster_size();
-  for (int64_t row = blockIdx.x / size; row < rows; row += gridDim.x / size) {
-    if (a.tok[row] != kDeferred) continue;  // the cluster's CTAs all read it before one can write it
-    sample_row<T, true>(a, *reinterpret_cast<Shared<kThr, kShortCap>*>(raw), row);
-    cluster_sync_all(size);
-  }
+  cluster_sync_all(size);  // the other CTAs have started
+  share_rows(
+      s, rows, blockIdx.x / size, gridDim.x / size, [&](int64_t i) { return a.states[i].left != 0; },
+      [&](int64_t row) {
+        const Ask q = read_ask(a, row);
+        const RowState st = a.states[row];
+        Row<T, kThr> r;
+        r.c = inv_temperature(q.T);
+        r.open(a, row);
+        r.m = st.m;
+        Verdict v{0, 0, -1, 0.f};
+        const int tok = wide_row(r, s, a, q, st.mass, a.u + row * a.ld_u, &v);
+        write_sample(a, r, row, tok, v, true);
+        cluster_sync_all(size);
+      });
+}
+
+// Whether the draft of verified row rr of sequence j is accepted (one thread).
+template <typename T>
+__device__ __forceinline__ int accepts(const FilterArgs& a, const Row<T, kThr>& r, int64_t j, int rr, uint64_t cut,
+                                       uint64_t mass) {
+  const int x = rr < a.D ? a.draft[j * a.D + rr] : -1;
+  if (x < 0 || x >= a.V) return 0;
+  const float z = r.at(x);
+  const uint32_t key = value_key(z);
+  return key != 0 && place_of(key, static_cast<uint32_t>(x)) >= cut &&
+         static_cast<double>(a.u_accept[j * a.D + rr]) * static_cast<double>(mass) <
+             static_cast<double>(r.weight(z));
 }
 
 // Verified row rr of sequence j: whether its draft is accepted, and the token
 // drawn here if it is not (or if rr = D).  A row without a short list leaves
 // the draw, which few rows need, to the last kernel.
-template <typename T, bool kWide>
-__device__ __forceinline__ void accept_row(const FilterArgs& a, Shared<kThr, kShortCap>& s, int64_t j, int rr) {
-  const uint32_t size = cluster_size();
+template <typename T>
+__global__ void __launch_bounds__(kThr, 4) accept_rows_kernel(const FilterArgs a) {
+  extern __shared__ __align__(16) uint8_t raw[];
+  Short& s = *reinterpret_cast<Short*>(raw);
+  const uint32_t size = cluster_size(), at = blockIdx.x / size;
+  const int64_t j = at / a.rows_used;
+  const int rr = static_cast<int>(at - j * a.rows_used);
   const int64_t row = j * a.R + rr;
   start(s, size);
   const Ask q = read_ask(a, j);
@@ -1381,70 +1697,56 @@ __device__ __forceinline__ void accept_row(const FilterArgs& a, Shared<kThr, kSh
   const bool want_mass = wants_mass(a, q);
   Scan<T, kThr> sc;
   scan_row(r, want_mass, sc);
-  float low;
-  float row_mass;
+  float low, row_mass;
   const bool some = join_scan(r, s, sc, want_mass, &low, &row_mass);
-  RowCut out;
-  out.cut = ~0ull;
-  out.m = r.m;
-  out.accept = 0;
-  out.tok = -1;
-  out.deferred = 0;
+  RowCut out{~0ull, r.m, 0, -1, 0, row_mass, 0};
   if (q.ok && some) {
     const int drop = rr < a.D ? a.draft[j * a.D + rr] : -1;
     Verdict v{0, 0, -1, 0.f};
-    int n = 0;
-    if (!kWide && listed_row(r, s, sc, a, q, low, row_mass, a.u + j * a.ld_u, drop, &v)) {
+    if (listed_row(r, s, sc, a, q, low, row_mass, a.u + j * a.ld_u, drop, &v)) {
       if (r.rank != 0) return;
-      out.cut = v.cut;
       out.tok = v.tok;
     } else {
       out.tok = kDeferred;
-      if (want_mass && q.p >= 1.f) {
-        out.cut = 1ull << 32;
-        v.mass = __float2ull_rn(row_mass * r.scale);
-      } else if (a.defer) {
-        out.deferred = 1;
-      } else if (q.k >= a.V && q.p < 1.f && q.mp == 0.f &&
-                 deep_top_p(r, s, q, a.V, row_mass, static_cast<const float*>(nullptr), &n, &v.mass,
-                            static_cast<Best*>(nullptr))) {
-        if (r.rank == 0) out.cut = s.list[n - 1];
+      if (a.defer && !(want_mass && q.p >= 1.f)) {
+        out.left = 1;
       } else {
-        out.cut = wide_cut(r, s, a, q, &v.mass);
+        wide_row(r, s, a, q, row_mass, static_cast<const float*>(nullptr), &v);
       }
     }
-    if (r.rank == 0 && threadIdx.x == 0 && !out.deferred && drop >= 0 && drop < a.V) {
-      const float z = r.at(drop);
-      const uint32_t key = value_key(z);
-      if (key != 0 && place_of(key, static_cast<uint32_t>(drop)) >= out.cut)
-        out.accept = static_cast<double>(a.u_accept[j * a.D + rr]) * static_cast<double>(v.mass) <
-                     static_cast<double>(r.weight(z));
-    }
+    out.cut = v.cut;
+    if (r.rank == 0 && threadIdx.x == 0 && !out.left) out.accept = accepts(a, r, j, rr, v.cut, v.mass);
   }
   if (r.rank == 0 && threadIdx.x == 0) a.cuts[row] = out;
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kThr, 4) accept_rows_kernel(const FilterArgs a) {
-  extern __shared__ __align__(16) uint8_t raw[];
-  const uint32_t at = blockIdx.x / cluster_size();
-  const int64_t j = at / a.rows_used;
-  accept_row<T, false>(a, *reinterpret_cast<Shared<kThr, kShortCap>*>(raw), j,
-                       static_cast<int>(at - j * a.rows_used));
-}
-
-template <typename T>
 __global__ void __launch_bounds__(kThr, 4) accept_wide_kernel(const FilterArgs a, const int64_t rows) {
   extern __shared__ __align__(16) uint8_t raw[];
+  Short& s = *reinterpret_cast<Short*>(raw);
   pdl_wait();
   const uint32_t size = cluster_size();
-  for (int64_t at = blockIdx.x / size; at < rows; at += gridDim.x / size) {
-    const int64_t j = at / a.rows_used;
-    const int rr = static_cast<int>(at - j * a.rows_used);
-    if (!a.cuts[j * a.R + rr].deferred) continue;
-    accept_row<T, true>(a, *reinterpret_cast<Shared<kThr, kShortCap>*>(raw), j, rr);
-    cluster_sync_all(size);
-  }
+  cluster_sync_all(size);  // the other CTAs have started
+  const auto row_of = [&](int64_t at) { return at / a.rows_used * a.R + at % a.rows_used; };
+  share_rows(
+      s, rows, blockIdx.x / size, gridDim.x / size, [&](int64_t at) { return a.cuts[row_of(at)].left != 0; },
+      [&](int64_t at) {
+        const int64_t j = at / a.rows_used;
+        const int rr = static_cast<int>(at - j * a.rows_used);
+        const Ask q = read_ask(a, j);
+        RowCut* c = a.cuts + row_of(at);
+        Row<T, kThr> r;
+        r.c = inv_temperature(q.T);
+        r.open(a, row_of(at));
+        r.m = c->m;
+        Verdict v{0, 0, -1, 0.f};
+        wide_row(r, s, a, q, c->mass, static_cast<const float*>(nullptr), &v);
+        if (r.rank == 0 && threadIdx.x == 0) {  // `left` stays: other clusters read it
+          c->cut = v.cut;
+          c->accept = accepts(a, r, j, rr, v.cut, v.mass);
+        }
+        cluster_sync_all(size);
+      });
 }
 
 // One cluster per sequence: leading accepts, the draw at the row after them if
@@ -1566,43 +1868,44 @@ int pick_parts(int64_t V, int64_t rows, size_t esize) {
     parts *= 2;
   return parts;
 }
-// Whether wide rows are left to a second launch: its clusters have to be
-// larger, and cost a launch that short rows do without.
+// Whether wide rows are left to a second launch: worth it where the first gives
+// a row few CTAs.
 bool defers(int64_t V, size_t esize, int parts) {
   return parts < kMaxCluster && V * (int64_t)esize / parts > 64 * 1024;
 }
 
-// The second launch: clusters of eight that fill the GPU share out the rows.
+// The second launch: clusters that fill the GPU share out the rows, of eight
+// CTAs, or of four where many rows may come.
 cudaError_t launch_wide(const void* kern, int64_t rows, size_t smem, const FilterArgs& a, cudaStream_t st) {
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   FilterArgs b = a;
   b.defer = 0;
   void* args[] = {&b, &rows};
-  int64_t clusters = 4 * num_sms() / kMaxCluster;
+  const int parts = rows > 2 * num_sms() ? 4 : 8;
+  int64_t clusters = 4 * num_sms() / parts;
   if (clusters > rows) clusters = rows;
-  return launch_kc(kern, dim3((unsigned)(clusters * kMaxCluster)), dim3(kThr), smem, st, true, dim3(kMaxCluster), args);
+  return launch_kc(kern, dim3((unsigned)(clusters * parts)), dim3(kThr), smem, st, true, dim3(parts), args);
 }
 
 template <typename T>
 cudaError_t launch_sample(FilterArgs a, int64_t rows, cudaStream_t st) {
-  const size_t smem = sizeof(Shared<kThr, kShortCap>);
   const int parts = pick_parts(a.V, rows, sizeof(T));
   a.defer = defers(a.V, sizeof(T), parts);
-  cudaError_t e = launch_rows((const void*)sample_rows_kernel<T>, rows, parts, smem, a, st);
+  cudaError_t e = launch_rows((const void*)sample_rows_kernel<T>, rows, parts, sizeof(Short), a, st);
   if (e != cudaSuccess || !a.defer) return e;
-  return launch_wide((const void*)sample_wide_kernel<T>, rows, smem, a, st);
+  return launch_wide((const void*)sample_wide_kernel<T>, rows, sizeof(Short), a, st);
 }
 template <typename T>
 cudaError_t launch_accept(FilterArgs a, int64_t b, cudaStream_t st) {
   const int64_t rows = b * a.rows_used;
-  const size_t smem = sizeof(Shared<kThr, kShortCap>);
   const int parts = pick_parts(a.V, rows, sizeof(T));
   a.defer = defers(a.V, sizeof(T), parts);
-  cudaError_t e = launch_rows((const void*)accept_rows_kernel<T>, rows, parts, smem, a, st);
+  cudaError_t e = launch_rows((const void*)accept_rows_kernel<T>, rows, parts, sizeof(Short), a, st);
   if (e != cudaSuccess) return e;
-  if (a.defer && (e = launch_wide((const void*)accept_wide_kernel<T>, rows, smem, a, st)) != cudaSuccess) return e;
-  return launch_rows((const void*)accept_pick_kernel<T>, b, pick_parts(a.V, b, sizeof(T)), smem, a, st);
+  if (a.defer && (e = launch_wide((const void*)accept_wide_kernel<T>, rows, sizeof(Short), a, st)) != cudaSuccess)
+    return e;
+  return launch_rows((const void*)accept_pick_kernel<T>, b, pick_parts(a.V, b, sizeof(T)), sizeof(Short), a, st);
 }
 template <typename T>
 cudaError_t launch_top(const FilterArgs& a, int64_t rows, cudaStream_t st) {

@@ -216,7 +216,13 @@ struct RowCut {  // one verified row
   float m;       // the row's maximum
   int accept;    // the row's draft token is accepted
   int tok;       // the token drawn where it is not; -2: still to be drawn
-  int deferred;  // the row is left to the wide kernel
+  int left;      // the row is left to the second launch
+  float mass;    // its sum of weights, for that
+  int pad;
+};
+struct RowState {  // one sampled row between its launches
+  float m, mass;   // the row's maximum and sum of weights
+  int left;        // it is left to the second launch
 };
 struct FilterArgs {
   const void* logits;  // [rows] of V entries, ld apart
@@ -229,6 +235,7 @@ struct FilterArgs {
   const float* u;  // uniforms, ld_u apart
   int64_t ld_u;
   int* tok;        // sample
+  RowState* states;
   float* logprob;
   int R, D;        // accept
   int rows_used;   // rows of a sequence that can matter, set by the launcher

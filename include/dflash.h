@@ -360,6 +360,9 @@ DFLASH_API int32_t dflash_commit_draft_block(const dflash_weights* w, const dfla
  * Arguments are checked, and errors returned, as for the other calls.
  * ------------------------------------------------------------------------- */
 
+/* Workspace bytes for dflash_sample. */
+DFLASH_API int32_t dflash_sample_workspace_size(int64_t rows, int64_t V, size_t* bytes);
+
 /* One token per row, drawn from softmax(z / T) under the row's filters.  With
  * m = max z and w_v = exp((z_v - m) / T):
  *   top_k keeps the first top_k entries of the order (0 or >= V: all);
@@ -376,11 +379,12 @@ DFLASH_API int32_t dflash_commit_draft_block(const dflash_weights* w, const dfla
  * sets DFLASH_DEV_BAD_PARAM.  u: uniforms in [0, 1), [rows] of V fp32, ld_u >= V
  * apart; only the entries kept are read.  tok_out [rows] int32, logprob_out
  * [rows] fp32 (nullable).  A row without an unmasked entry gets tok -1 and
- * logprob -inf.  No workspace. */
+ * logprob -inf.  ws holds dflash_sample_workspace_size bytes, 16-byte aligned;
+ * it needs no zero fill and keeps nothing between calls. */
 DFLASH_API int32_t dflash_sample(const void* logits, int32_t dtype, int64_t rows, int64_t V, int64_t ld,
                                  const float* temperature, const int32_t* top_k, const float* top_p,
                                  const float* min_p, const float* u, int64_t ld_u, int32_t* tok_out,
-                                 float* logprob_out, void* stream);
+                                 float* logprob_out, void* ws, size_t ws_bytes, void* stream);
 
 /* Workspace bytes for dflash_verify_accept_filtered. */
 DFLASH_API int32_t dflash_verify_filtered_workspace_size(int32_t b, int32_t R, int64_t V, size_t* bytes);
