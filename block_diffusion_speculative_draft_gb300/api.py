@@ -9,6 +9,7 @@ library is missing or no GPU is present, the first call raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Dict, List, Optional
 
@@ -141,11 +142,17 @@ def _stream(stream=None) -> int:
     return s.cuda_stream
 
 
+_torch_module = None
+
+
 def _torch():
-    import torch
-    if not torch.cuda.is_available():
-        raise RuntimeError("dflash needs a CUDA GPU; no CPU path exists")
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        if not torch.cuda.is_available():
+            raise RuntimeError("dflash needs a CUDA GPU; no CPU path exists")
+        _torch_module = torch
+    return _torch_module
 
 
 # ---------------------------------------------------------- entry points ----
@@ -308,47 +315,59 @@ def dflash_verify_accept_noalloc(logits, draft, n_out, corr_out, emitted=None, n
 def _row_shape(fn, t, dim):
     """Row stride of a logits-like tensor whose last dimension is contiguous
     and whose leading dimensions (if two) form one sequence of rows."""
-    V = t.shape[-1]
-    if t.dim() != dim or t.numel() == 0 or (t.stride(-1) != 1 and V > 1):
-        raise ValueError(f"{fn}: expected a non-empty {dim}-D tensor with contiguous rows, got {tuple(t.shape)}")
-    rows = t.numel() // V
-    if rows == 1:
-        return V
+    shape, strides = t.shape, t.stride()
+    if len(shape) != dim or 0 in shape or (strides[-1] != 1 and shape[-1] > 1):
+        raise ValueError(f"{fn}: expected a non-empty {dim}-D tensor with contiguous rows, got {tuple(shape)}")
     if dim == 2:
-        return t.stride(0)
-    b, R, _ = t.shape
-    ld = t.stride(1) if R > 1 else t.stride(0)
-    if b > 1 and t.stride(0) != R * ld:
+        return strides[0] if shape[0] > 1 else shape[1]
+    b, R, V = shape
+    if b == R == 1:
+        return V
+    ld = strides[1] if R > 1 else strides[0]
+    if b > 1 and strides[0] != R * ld:
         raise ValueError(f"{fn}: the rows of a 3-D tensor must be evenly spaced")
     return ld
 
 
 def _row_dtype(fn, t):
     torch = _torch()
-    dt = {torch.float32: DTYPE_F32, torch.float16: DTYPE_F16, torch.bfloat16: DTYPE_BF16}.get(t.dtype)
+    dt = t.dtype
+    dt = DTYPE_F32 if dt == torch.float32 else DTYPE_F16 if dt == torch.float16 else \
+        DTYPE_BF16 if dt == torch.bfloat16 else None
     if dt is None or not t.is_cuda:
         raise ValueError(f"{fn}: logits must be a CUDA tensor of float32, float16 or bfloat16")
     return dt
 
 
 def _need(fn, dev, dtype, shape, **tensors):
-    """Each given tensor (None: absent) is contiguous, on `dev`, and of this
-    dtype and shape."""
+    """Data pointers of the given tensors (None: absent), each contiguous, on
+    device number `dev`, and of this dtype and shape."""
+    out = []
     for name, t in tensors.items():
-        if t is not None and (t.dtype != dtype or t.device != dev or tuple(t.shape) != tuple(shape)
-                              or not t.is_contiguous()):
-            raise ValueError(f"{fn}: {name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {dev}")
+        if t is None:
+            out.append(None)
+            continue
+        if t.dtype != dtype or t.get_device() != dev or t.shape != shape or not t.is_contiguous():
+            raise ValueError(f"{fn}: {name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on cuda:{dev}")
+        out.append(t.data_ptr())
+    return out
 
 
-def _on(dev, stream, fn, call):
-    """Runs `call(stream handle)` with the tensors' device current, on the
+def _uniforms(fn, name, u, dev, shape):
+    if u.dtype != _torch().float32 or u.get_device() != dev or u.shape != shape:
+        raise ValueError(f"{fn}: {name} must be a float32 tensor of shape {tuple(shape)} on cuda:{dev}")
+    return _row_shape(fn, u, 2)
+
+
+def _on(dev, stream, fn, call, *args):
+    """call(*args, stream handle) with the tensors' device current, on the
     given stream or that device's current one."""
-    torch = _torch()
-    if dev.index == torch.cuda.current_device():
-        _check(fn, call(_stream(stream)))
+    cuda = _torch().cuda
+    if dev == cuda.current_device():
+        _check(fn, call(*args, (stream if stream is not None else cuda.current_stream()).cuda_stream))
     else:
-        with torch.cuda.device(dev):
-            _check(fn, call(_stream(stream)))
+        with cuda.device(dev):
+            _check(fn, call(*args, (stream if stream is not None else cuda.current_stream()).cuda_stream))
 
 
 def _workspace(fn, ws, nbytes, dev, stream):
@@ -357,14 +376,15 @@ def _workspace(fn, ws, nbytes, dev, stream):
     torch = _torch()
     if ws is None:
         if stream is None:
-            return torch.empty(nbytes, dtype=torch.uint8, device=dev)
+            return torch.empty(nbytes, dtype=torch.uint8, device=torch.device("cuda", dev))
         with torch.cuda.stream(stream):
-            return torch.empty(nbytes, dtype=torch.uint8, device=dev)
-    if ws.device != dev or not ws.is_contiguous():
-        raise ValueError(f"{fn}: ws must be contiguous and on {dev}")
+            return torch.empty(nbytes, dtype=torch.uint8, device=torch.device("cuda", dev))
+    if ws.get_device() != dev or not ws.is_contiguous():
+        raise ValueError(f"{fn}: ws must be contiguous and on cuda:{dev}")
     return ws
 
 
+@functools.lru_cache(maxsize=256)
 def dflash_sample_workspace_size(rows: int, V: int) -> int:
     n = ctypes.c_size_t(0)
     _check("dflash_sample_workspace_size", load_library().dflash_sample_workspace_size(rows, V, ctypes.byref(n)))
@@ -382,18 +402,18 @@ def dflash_sample(logits, temperature, u, tok_out, top_k=None, top_p=None, min_p
     fn = "dflash_sample"
     dt = _row_dtype(fn, logits)
     ld = _row_shape(fn, logits, 2)
-    torch, dev, (n, V) = _torch(), logits.device, logits.shape
-    _need(fn, dev, torch.float32, (n,), temperature=temperature, top_p=top_p, min_p=min_p, logprob_out=logprob_out)
-    _need(fn, dev, torch.int32, (n,), top_k=top_k, tok_out=tok_out)
-    if u.dtype != torch.float32 or u.device != dev or tuple(u.shape) != (n, V):
-        raise ValueError(f"{fn}: u must be float32 [{n}][{V}] on {dev}")
-    lib = load_library()
+    torch, dev, shape = _torch(), logits.get_device(), logits.shape
+    n, V = shape
+    T, p, m, lp = _need(fn, dev, torch.float32, shape[:1], temperature=temperature, top_p=top_p, min_p=min_p,
+                        logprob_out=logprob_out)
+    k, tok = _need(fn, dev, torch.int32, shape[:1], top_k=top_k, tok_out=tok_out)
+    ld_u = _uniforms(fn, "u", u, dev, shape)
     ws = _workspace(fn, ws, 0 if ws is not None else dflash_sample_workspace_size(n, V), dev, stream)
-    _on(dev, stream, fn, lambda st: lib.dflash_sample(
-        logits.data_ptr(), dt, n, V, ld, temperature.data_ptr(), _ptr(top_k), _ptr(top_p), _ptr(min_p), u.data_ptr(),
-        _row_shape(fn, u, 2), tok_out.data_ptr(), _ptr(logprob_out), ws.data_ptr(), ws.numel() * ws.element_size(), st))
+    _on(dev, stream, fn, load_library().dflash_sample, logits.data_ptr(), dt, n, V, ld, T, k, p, m, u.data_ptr(), ld_u,
+        tok, lp, ws.data_ptr(), ws.numel() * ws.element_size())
 
 
+@functools.lru_cache(maxsize=256)
 def dflash_verify_filtered_workspace_size(b: int, R: int, V: int) -> int:
     n = ctypes.c_size_t(0)
     _check("dflash_verify_filtered_workspace_size",
@@ -412,21 +432,19 @@ def dflash_verify_accept_filtered(logits, draft, temperature, u_accept, u_sample
     fn = "dflash_verify_accept_filtered"
     dt = _row_dtype(fn, logits)
     ld = _row_shape(fn, logits, 3)
-    torch, dev, (b, R, V) = _torch(), logits.device, logits.shape
+    torch, dev, shape = _torch(), logits.get_device(), logits.shape
+    b, R, V = shape
     D = draft.shape[-1]
-    _need(fn, dev, torch.int32, (b, D), draft=draft)
-    _need(fn, dev, torch.float32, (b, D), u_accept=u_accept)
-    _need(fn, dev, torch.float32, (b,), temperature=temperature, top_p=top_p, min_p=min_p)
-    _need(fn, dev, torch.int32, (b,), top_k=top_k, n_out=n_out, corr_out=corr_out, next_tok=next_tok)
-    _need(fn, dev, torch.int32, (b, R), emitted=emitted)
-    if u_sample.dtype != torch.float32 or u_sample.device != dev or tuple(u_sample.shape) != (b, V):
-        raise ValueError(f"{fn}: u_sample must be float32 [{b}][{V}] on {dev}")
+    dr, = _need(fn, dev, torch.int32, (b, D), draft=draft)
+    ua, = _need(fn, dev, torch.float32, (b, D), u_accept=u_accept)
+    T, p, m = _need(fn, dev, torch.float32, shape[:1], temperature=temperature, top_p=top_p, min_p=min_p)
+    k, no, co, nx = _need(fn, dev, torch.int32, shape[:1], top_k=top_k, n_out=n_out, corr_out=corr_out,
+                          next_tok=next_tok)
+    em, = _need(fn, dev, torch.int32, shape[:2], emitted=emitted)
+    ld_u = _uniforms(fn, "u_sample", u_sample, dev, (b, V))
     ws = _workspace(fn, ws, 0 if ws is not None else dflash_verify_filtered_workspace_size(b, R, V), dev, stream)
-    lib = load_library()
-    _on(dev, stream, fn, lambda st: lib.dflash_verify_accept_filtered(
-        logits.data_ptr(), dt, ld, draft.data_ptr(), b, R, D, V, temperature.data_ptr(), _ptr(top_k), _ptr(top_p),
-        _ptr(min_p), u_accept.data_ptr(), u_sample.data_ptr(), _row_shape(fn, u_sample, 2), n_out.data_ptr(),
-        corr_out.data_ptr(), _ptr(emitted), _ptr(next_tok), ws.data_ptr(), ws.numel() * ws.element_size(), st))
+    _on(dev, stream, fn, load_library().dflash_verify_accept_filtered, logits.data_ptr(), dt, ld, dr, b, R, D, V, T, k,
+        p, m, ua, u_sample.data_ptr(), ld_u, no, co, em, nx, ws.data_ptr(), ws.numel() * ws.element_size())
 
 
 def dflash_top_logits(logits, K: int, val_out, idx_out, lse_out=None, temperature: float = 1.0, stream=None):
@@ -436,29 +454,29 @@ def dflash_top_logits(logits, K: int, val_out, idx_out, lse_out=None, temperatur
     fn = "dflash_top_logits"
     dt = _row_dtype(fn, logits)
     ld = _row_shape(fn, logits, 2)
-    torch, dev, (n, V) = _torch(), logits.device, logits.shape
-    _need(fn, dev, torch.float32, (n, K), val_out=val_out)
-    _need(fn, dev, torch.int32, (n, K), idx_out=idx_out)
-    _need(fn, dev, torch.float32, (n,), lse_out=lse_out)
-    lib = load_library()
-    _on(dev, stream, fn, lambda st: lib.dflash_top_logits(
-        logits.data_ptr(), dt, n, V, ld, K, float(temperature), val_out.data_ptr(), idx_out.data_ptr(), _ptr(lse_out),
-        st))
+    torch, dev, (n, V) = _torch(), logits.get_device(), logits.shape
+    val, = _need(fn, dev, torch.float32, (n, K), val_out=val_out)
+    idx, = _need(fn, dev, torch.int32, (n, K), idx_out=idx_out)
+    lse, = _need(fn, dev, torch.float32, (n,), lse_out=lse_out)
+    _on(dev, stream, fn, load_library().dflash_top_logits, logits.data_ptr(), dt, n, V, ld, K, float(temperature), val,
+        idx, lse)
 
 
-def _teacher(fn, logits, t_val, t_idx, t_lse):
-    torch, dev, n = _torch(), logits.device, logits.shape[0]
+def _student(fn, logits, t_val, t_idx, t_lse, dlogits):
+    """Arguments common to the distillation calls."""
+    dt = _row_dtype(fn, logits)
+    ld = _row_shape(fn, logits, 2)
+    torch, dev, (n, V) = _torch(), logits.get_device(), logits.shape
     K = t_val.shape[-1]
-    _need(fn, dev, torch.float32, (n, K), t_val=t_val)
-    _need(fn, dev, torch.int32, (n, K), t_idx=t_idx)
-    _need(fn, dev, torch.float32, (n,), t_lse=t_lse)
-    return K
-
-
-def _gradient(fn, logits, dlogits):
-    if dlogits.dtype != logits.dtype or dlogits.device != logits.device or dlogits.shape != logits.shape:
-        raise ValueError(f"{fn}: dlogits must have the logits' dtype, device and shape")
-    return _row_shape(fn, dlogits, 2)
+    tv, = _need(fn, dev, torch.float32, (n, K), t_val=t_val)
+    ti, = _need(fn, dev, torch.int32, (n, K), t_idx=t_idx)
+    tl, = _need(fn, dev, torch.float32, (n,), t_lse=t_lse)
+    dz, ldd = None, 0
+    if dlogits is not None:
+        if dlogits.dtype != logits.dtype or dlogits.get_device() != dev or dlogits.shape != logits.shape:
+            raise ValueError(f"{fn}: dlogits must have the logits' dtype, device and shape")
+        dz, ldd = dlogits.data_ptr(), _row_shape(fn, dlogits, 2)
+    return dev, n, (logits.data_ptr(), dt, n, V, ld, tv, ti, K, tl), dz, ldd
 
 
 def dflash_distill_loss(logits, t_val, t_idx, loss_out, t_lse=None, temperature: float = 1.0, weight=None,
@@ -471,17 +489,11 @@ def dflash_distill_loss(logits, t_val, t_idx, loss_out, t_lse=None, temperature:
     gradient (0: the row is left out).  loss_out fp32 [rows]; stats_out fp32
     [rows][4] for dflash_distill_backward."""
     fn = "dflash_distill_loss"
-    dt = _row_dtype(fn, logits)
-    ld = _row_shape(fn, logits, 2)
-    K = _teacher(fn, logits, t_val, t_idx, t_lse)
-    torch, dev, (n, V) = _torch(), logits.device, logits.shape
-    _need(fn, dev, torch.float32, (n,), weight=weight, loss_out=loss_out)
-    _need(fn, dev, torch.float32, (n, 4), stats_out=stats_out)
-    ldd = 0 if dlogits is None else _gradient(fn, logits, dlogits)
-    lib = load_library()
-    _on(dev, stream, fn, lambda st: lib.dflash_distill_loss(
-        logits.data_ptr(), dt, n, V, ld, t_val.data_ptr(), t_idx.data_ptr(), K, _ptr(t_lse), float(temperature),
-        _ptr(weight), loss_out.data_ptr(), _ptr(stats_out), _ptr(dlogits), ldd, st))
+    dev, n, args, dz, ldd = _student(fn, logits, t_val, t_idx, t_lse, dlogits)
+    f32 = _torch().float32
+    w, loss = _need(fn, dev, f32, (n,), weight=weight, loss_out=loss_out)
+    st, = _need(fn, dev, f32, (n, 4), stats_out=stats_out)
+    _on(dev, stream, fn, load_library().dflash_distill_loss, *args, float(temperature), w, loss, st, dz, ldd)
 
 
 def dflash_distill_backward(logits, t_val, t_idx, stats, grad_loss, dlogits, t_lse=None, temperature: float = 1.0,
@@ -489,17 +501,11 @@ def dflash_distill_backward(logits, t_val, t_idx, stats, grad_loss, dlogits, t_l
     """dlogits = grad_loss[row] * d loss / d logits of an unweighted
     dflash_distill_loss call that wrote stats.  dlogits may be logits itself."""
     fn = "dflash_distill_backward"
-    dt = _row_dtype(fn, logits)
-    ld = _row_shape(fn, logits, 2)
-    K = _teacher(fn, logits, t_val, t_idx, t_lse)
-    torch, dev, (n, V) = _torch(), logits.device, logits.shape
-    _need(fn, dev, torch.float32, (n,), grad_loss=grad_loss)
-    _need(fn, dev, torch.float32, (n, 4), stats=stats)
-    ldd = _gradient(fn, logits, dlogits)
-    lib = load_library()
-    _on(dev, stream, fn, lambda st: lib.dflash_distill_backward(
-        logits.data_ptr(), dt, n, V, ld, t_val.data_ptr(), t_idx.data_ptr(), K, _ptr(t_lse), float(temperature),
-        stats.data_ptr(), grad_loss.data_ptr(), dlogits.data_ptr(), ldd, st))
+    dev, n, args, dz, ldd = _student(fn, logits, t_val, t_idx, t_lse, dlogits)
+    f32 = _torch().float32
+    g, = _need(fn, dev, f32, (n,), grad_loss=grad_loss)
+    st, = _need(fn, dev, f32, (n, 4), stats=stats)
+    _on(dev, stream, fn, load_library().dflash_distill_backward, *args, float(temperature), st, g, dz, ldd)
 
 
 def dflash_draft_block(model: "DeviceDrafter", kv: "KVCache", last_tok, draft_out, ws, hidden=None, logits=None,
