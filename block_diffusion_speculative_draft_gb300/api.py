@@ -362,26 +362,30 @@ def _uniforms(fn, name, u, dev, shape):
 def _on(dev, stream, fn, call, *args):
     """call(*args, stream handle) with the tensors' device current, on the
     given stream or that device's current one."""
-    cuda = _torch().cuda
-    if dev == cuda.current_device():
-        _check(fn, call(*args, (stream if stream is not None else cuda.current_stream()).cuda_stream))
+    torch = _torch()
+    # the current stream's handle without making a Stream object
+    handle = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+    if dev == torch.cuda.current_device():
+        rc = call(*args, handle)
     else:
-        with cuda.device(dev):
-            _check(fn, call(*args, (stream if stream is not None else cuda.current_stream()).cuda_stream))
+        with torch.cuda.device(dev):
+            rc = call(*args, handle)
+    if rc != DFLASH_OK:
+        raise DflashError(fn, rc)
 
 
 def _workspace(fn, ws, nbytes, dev, stream):
-    """The given workspace, or one in memory that the call's own stream may
-    reuse (stream None: the current one)."""
+    """(pointer, bytes, tensor) of the given workspace, or of one in memory that
+    the call's own stream may reuse (stream None: the current one)."""
     torch = _torch()
     if ws is None:
-        if stream is None:
-            return torch.empty(nbytes, dtype=torch.uint8, device=torch.device("cuda", dev))
-        with torch.cuda.stream(stream):
-            return torch.empty(nbytes, dtype=torch.uint8, device=torch.device("cuda", dev))
-    if ws.get_device() != dev or not ws.is_contiguous():
+        if nbytes == 0:
+            return None, 0, None
+        with torch.cuda.stream(stream):  # None: no change
+            ws = torch.empty(nbytes, dtype=torch.uint8, device=torch.device("cuda", dev))
+    elif ws.get_device() != dev or not ws.is_contiguous():
         raise ValueError(f"{fn}: ws must be contiguous and on cuda:{dev}")
-    return ws
+    return ws.data_ptr(), ws.numel() * ws.element_size(), ws
 
 
 @functools.lru_cache(maxsize=256)
@@ -408,9 +412,9 @@ def dflash_sample(logits, temperature, u, tok_out, top_k=None, top_p=None, min_p
                         logprob_out=logprob_out)
     k, tok = _need(fn, dev, torch.int32, shape[:1], top_k=top_k, tok_out=tok_out)
     ld_u = _uniforms(fn, "u", u, dev, shape)
-    ws = _workspace(fn, ws, 0 if ws is not None else dflash_sample_workspace_size(n, V), dev, stream)
+    wp, wn, ws = _workspace(fn, ws, dflash_sample_workspace_size(n, V), dev, stream)
     _on(dev, stream, fn, load_library().dflash_sample, logits.data_ptr(), dt, n, V, ld, T, k, p, m, u.data_ptr(), ld_u,
-        tok, lp, ws.data_ptr(), ws.numel() * ws.element_size())
+        tok, lp, wp, wn)
 
 
 @functools.lru_cache(maxsize=256)
@@ -442,9 +446,9 @@ def dflash_verify_accept_filtered(logits, draft, temperature, u_accept, u_sample
                           next_tok=next_tok)
     em, = _need(fn, dev, torch.int32, shape[:2], emitted=emitted)
     ld_u = _uniforms(fn, "u_sample", u_sample, dev, (b, V))
-    ws = _workspace(fn, ws, 0 if ws is not None else dflash_verify_filtered_workspace_size(b, R, V), dev, stream)
+    wp, wn, ws = _workspace(fn, ws, dflash_verify_filtered_workspace_size(b, R, V), dev, stream)
     _on(dev, stream, fn, load_library().dflash_verify_accept_filtered, logits.data_ptr(), dt, ld, dr, b, R, D, V, T, k,
-        p, m, ua, u_sample.data_ptr(), ld_u, no, co, em, nx, ws.data_ptr(), ws.numel() * ws.element_size())
+        p, m, ua, u_sample.data_ptr(), ld_u, no, co, em, nx, wp, wn)
 
 
 def dflash_top_logits(logits, K: int, val_out, idx_out, lse_out=None, temperature: float = 1.0, stream=None):

@@ -506,9 +506,13 @@ static int check_rows(const void* logits, int32_t dtype, int64_t rows, int64_t V
 }
 static bool row_temperature(float t) { return t >= kFilterMinT && t <= kFilterMaxT; }
 
+static size_t sample_state_bytes(int64_t rows) {
+  return rows > kInlineRows ? (size_t)rows * sizeof(RowState) : 0;
+}
+
 int32_t dflash_sample_workspace_size(int64_t rows, int64_t V, size_t* bytes) {
   if (!bytes || rows < 1 || rows >= (int64_t)1 << 28 || V < 1) return DFLASH_EINVAL;
-  *bytes = (size_t)rows * sizeof(RowState);
+  *bytes = sample_state_bytes(rows);
   return DFLASH_OK;
 }
 
@@ -518,7 +522,8 @@ int32_t dflash_sample(const void* logits, int32_t dtype, int64_t rows, int64_t V
                       void* stream) {
   if (int r = check_rows(logits, dtype, rows, V, ld)) return r;
   if (!temperature || !u || !tok_out || ld_u < V) return DFLASH_EINVAL;
-  if (!ws || ws_bytes < (size_t)rows * sizeof(RowState) || !aligned16(ws)) return DFLASH_EWORKSPACE;
+  const size_t need = sample_state_bytes(rows);
+  if (need && (!ws || ws_bytes < need || !aligned16(ws))) return DFLASH_EWORKSPACE;
   FilterArgs a;
   memset(&a, 0, sizeof(a));
   a.logits = logits;

@@ -462,6 +462,28 @@ __device__ __forceinline__ void scan_row(const Row<T, NT>& r, bool want_mass, Sc
   }
 }
 
+// A first bar for a drawing pass, below the best score among the entries of the
+// threads' first packs with v >= from: -log u <= (1 - u) / u bounds a score from
+// below without a logarithm of a number next to one.  Without a bar every thread
+// would score its first entries in full.
+template <typename T, int NT, int kCap>
+__device__ __forceinline__ void first_bar(const Row<T, NT>& r, Shared<NT, kCap>& s, const float* u, const float* u0,
+                                          bool wide, float from, float m) {
+  constexpr int kE = Row<T, NT>::kE;
+  const int j = threadIdx.x;
+  float uu[kE], v[kE], best = -INFINITY;
+  Row<T, NT>::open_pack(r.pack(j), v);
+  r.uniforms(u, u0, wide, j, uu);
+#pragma unroll
+  for (int h = 0; h < kE; ++h) {
+    const float g = (v[h] - m) * r.c - fast_log2(1.f - uu[h]) + fast_log2(uu[h]);  // u = 0: -inf
+    if (v[h] >= from && v[h] > -INFINITY) best = fmaxf(best, g);
+  }
+  const uint32_t key = __reduce_max_sync(0xffffffffu, value_key(best * kLn2 - 0.00390625f - fabsf(best) * 1e-5f));
+  if ((threadIdx.x & 31) == 0) atomicMax(&s.bar, key);
+  __syncthreads();
+}
+
 // The scan of a row that nothing filters, and its draw, in one pass over the
 // logits and the uniforms: scores are taken as z/T - log(-log u), before the
 // maximum is known (the caller draws again where z/T is too large for that).
@@ -475,6 +497,7 @@ __device__ __forceinline__ void scan_and_draw(const Row<T, NT>& r, Shared<NT, kC
   t.ref = 0.f;
   t.sum = 0.f;
   bool any = false, odd = false;
+  first_bar(r, s, u, u0, wide, -INFINITY, 0.f);
   for (int j = threadIdx.x; j < r.part.packs; j += kB * NT) {
     uint4 w[kB];
     float uu[kB][kE];
@@ -612,6 +635,7 @@ __device__ __forceinline__ void list_entries(const Row<T, NT>& r, Shared<NT, kCa
   uint32_t* taken = peer(&s.taken, 0);
   uint64_t* list = peer(s.list, 0);
   const uint32_t deep = (r.part.packs + kGroups * NT - 1) / (kGroups * NT), units = s.queued * deep;
+  float listed = 0.f;
   for (uint32_t y0 = threadIdx.x; y0 < units; y0 += 4 * NT) {
     uint4 w[4];
     int at[4];
@@ -638,10 +662,12 @@ __device__ __forceinline__ void list_entries(const Row<T, NT>& r, Shared<NT, kCa
         const float z = Row<T, NT>::pick_of(w[x], h);
         if (base < kCap) list[base] = place_of(value_key(z), static_cast<uint32_t>(i + h));
         ++base;
-        if (want_mass) atomicAdd(reinterpret_cast<unsigned long long*>(&s.own_mass), r.weight(z));
+        listed += fast_exp2(r.log2w(z));
       }
     }
   }
+  if (want_mass && listed > 0.f)
+    atomicAdd(reinterpret_cast<unsigned long long*>(&s.own_mass), __float2ull_rn(listed * r.scale));
 }
 
 // Sum of the CTAs' own counts and masses; complete lists are seen after it.
@@ -1073,7 +1099,8 @@ __device__ __forceinline__ float deep_pass(const Row<T, NT>& r, Shared<NT, kCap>
   const bool wide = (reinterpret_cast<uintptr_t>(u0) & 15) == 0;
   const float m = r.m, c = r.c;
   float sum = 0.f;
-  uint64_t listed = 0;
+  if (kDraw) first_bar(r, s, u, u0, wide, kFrom ? over : nextafterf(over, INFINITY), m);
+  float listed = 0.f;
   for (int j = threadIdx.x; j < r.part.packs; j += kB * NT) {
     uint4 w[kB];
     float uu[kB][kE];
@@ -1124,12 +1151,13 @@ __device__ __forceinline__ float deep_pass(const Row<T, NT>& r, Shared<NT, kCap>
           const float z = Row<T, NT>::pick_of(w[x], h);
           if (at < kCap) s.list[at] = place_of(value_key(z), static_cast<uint32_t>(i + h));
           ++at;
-          listed += r.weight(z);
+          listed += fast_exp2((z - m) * c);
         }
       }
     }
   }
-  if (!kFrom && listed) atomicAdd(reinterpret_cast<unsigned long long*>(&s.own_mass), listed);
+  if (!kFrom && listed > 0.f)
+    atomicAdd(reinterpret_cast<unsigned long long*>(&s.own_mass), __float2ull_rn(listed * r.scale));
   return sum;
 }
 
@@ -1148,8 +1176,9 @@ __device__ int join_best_cta(const Row<T, NT>& r, Shared<NT, kCap>& s, const flo
 }
 
 // A long list that top-k does not cut (rank 0's threads).  Top-p's border is
-// found by 256 bins, linear in the value over the list, of exact weights; the
-// border's bin leaves a few entries to rank.  `above` is the weight before the
+// found by 256 bins of exact weights, linear in the place over the list's range
+// (so that equal values are told apart by their indices); the border's bin is
+// cut again until it leaves a few entries to rank.  `above` is the weight before the
 // list, `whole` what top-p refers to.  With u the kept entries but `drop` are
 // offered to `best`.
 template <typename T, int NT, int kCap>
@@ -1183,48 +1212,49 @@ __device__ Verdict long_list(const Row<T, NT>& r, Shared<NT, kCap>& s, const Ask
     if (threadIdx.x == 0) s.taken = 0;
     high = cta_reduce<NT / 32>(high, OpMaxU64(), s.x);
     if (out.mass > s.need) {  // the border is among these entries
-      const float from = key_to_value(static_cast<uint32_t>(high >> 32)),
-                  range = from - key_to_value(static_cast<uint32_t>(low >> 32));
-      const float per = range > 1e-30f ? 255.99f / range : 0.f;
-      int bin[kMine];
+      const uint64_t need = s.need;
+      uint64_t over = above;
+      int few;
+      do {
+        const int bits = 64 - __clzll(static_cast<long long>(high - low)), shift = bits > 8 ? bits - 8 : 0;
+        sub[threadIdx.x] = 0;
+        __syncthreads();
 #pragma unroll
-      for (int x = 0; x < kMine; ++x) {
-        const float v = key_to_value(static_cast<uint32_t>(place[x] >> 32));
-        const int b = place[x] ? static_cast<int>((from - v) * per) : 256;
-        bin[x] = b < 0 ? 0 : (place[x] && b > 255 ? 255 : b);
-        if (place[x]) atomicAdd(&sub[bin[x]], r.weight(v));
-      }
-      __syncthreads();
-      const uint64_t mine = sub[threadIdx.x], need = s.need;
-      uint64_t inc = mine;
+        for (int x = 0; x < kMine; ++x)
+          if (place[x] >= low && place[x] <= high)
+            atomicAdd(&sub[(high - place[x]) >> shift], r.weight(key_to_value(static_cast<uint32_t>(place[x] >> 32))));
+        __syncthreads();
+        const uint64_t mine = sub[threadIdx.x];
+        uint64_t inc = mine;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const uint64_t y = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += y;
-      }
-      if (lane == 31) s.warp_sum[warp] = inc;
-      __syncthreads();
-      uint64_t before = above + inc - mine;
-      for (int w = 0; w < warp; ++w) before += s.warp_sum[w];
-      if (before < need && before + mine >= need) {
-        s.pick[0] = threadIdx.x;
-        s.pick[1] = before;
-      }
-      __syncthreads();
-      const int at = static_cast<int>(s.pick[0]);
+        for (int o = 1; o < 32; o <<= 1) {
+          const uint64_t y = __shfl_up_sync(0xffffffffu, inc, o);
+          if (lane >= o) inc += y;
+        }
+        if (lane == 31) s.warp_sum[warp] = inc;
+        __syncthreads();
+        uint64_t before = over + inc - mine;
+        for (int w = 0; w < warp; ++w) before += s.warp_sum[w];
+        if (before < need && before + mine >= need) {
+          s.pick[0] = threadIdx.x;
+          s.pick[1] = before;
+        }
+        __syncthreads();
+        const uint64_t at = s.pick[0];
+        over = s.pick[1];
+        high -= at << shift;
+        const uint64_t end = high - ((1ull << shift) - 1);
+        if (end > low) low = end;
+        few = 0;
+#pragma unroll
+        for (int x = 0; x < kMine; ++x) few += place[x] >= low && place[x] <= high;
+        few = static_cast<int>(cta_reduce<NT / 32>(static_cast<uint64_t>(few), OpSumU64(), s.x));
+      } while (few > kQuick);
 #pragma unroll
       for (int x = 0; x < kMine; ++x)
-        if (bin[x] == at) s.list[atomicAdd(&s.taken, 1u)] = place[x];
+        if (place[x] >= low && place[x] <= high) s.list[atomicAdd(&s.taken, 1u)] = place[x];
       __syncthreads();
-      const int few = static_cast<int>(s.taken);
-      const uint64_t over = s.pick[1];
-      if (few <= kQuick) {
-        out = quick_list(r, s, q, few, over, whole, static_cast<const float*>(nullptr), -1);
-      } else {  // ties
-        sort_list<NT>(s.list, few);
-        const int kept = filter_list(r, s, q, few, over, whole, &out.mass);
-        out.cut = s.list[kept - 1];
-      }
+      out = quick_list(r, s, q, few, over, whole, static_cast<const float*>(nullptr), -1);
     }
   }
   out.tok = -1;
@@ -1637,7 +1667,10 @@ __device__ __forceinline__ void share_rows(Short& s, int64_t rows, uint32_t id, 
     carry += all;
     const int64_t end = carry > id ? (carry - id + clusters - 1) / clusters : 0;
     __syncthreads();
-    for (int64_t t = first; t < end; ++t) visit(s.rows[t - first]);
+    for (int64_t t = first; t < end; ++t) {
+      cluster_sync_all(cluster_size());  // the other CTAs have started, or are done with the last row
+      visit(s.rows[t - first]);
+    }
     __syncthreads();
   }
 }
@@ -1648,7 +1681,6 @@ __global__ void __launch_bounds__(kThr, 4) sample_wide_kernel(const FilterArgs a
   Short& s = *reinterpret_cast<Short*>(raw);
   pdl_wait();
   const uint32_t size = cluster_size();
-  cluster_sync_all(size);  // the other CTAs have started
   share_rows(
       s, rows, blockIdx.x / size, gridDim.x / size, [&](int64_t i) { return a.states[i].left != 0; },
       [&](int64_t row) {
@@ -1661,7 +1693,6 @@ __global__ void __launch_bounds__(kThr, 4) sample_wide_kernel(const FilterArgs a
         Verdict v{0, 0, -1, 0.f};
         const int tok = wide_row(r, s, a, q, st.mass, a.u + row * a.ld_u, &v);
         write_sample(a, r, row, tok, v, true);
-        cluster_sync_all(size);
       });
 }
 
@@ -1726,7 +1757,6 @@ __global__ void __launch_bounds__(kThr, 4) accept_wide_kernel(const FilterArgs a
   Short& s = *reinterpret_cast<Short*>(raw);
   pdl_wait();
   const uint32_t size = cluster_size();
-  cluster_sync_all(size);  // the other CTAs have started
   const auto row_of = [&](int64_t at) { return at / a.rows_used * a.R + at % a.rows_used; };
   share_rows(
       s, rows, blockIdx.x / size, gridDim.x / size, [&](int64_t at) { return a.cuts[row_of(at)].left != 0; },
@@ -1745,7 +1775,6 @@ __global__ void __launch_bounds__(kThr, 4) accept_wide_kernel(const FilterArgs a
           c->cut = v.cut;
           c->accept = accepts(a, r, j, rr, v.cut, v.mass);
         }
-        cluster_sync_all(size);
       });
 }
 
@@ -1851,10 +1880,9 @@ __global__ void __launch_bounds__(kThr, 4) top_rows_kernel(const FilterArgs a) {
   }
 }
 
+static_assert(sizeof(Shared<kThr, kTopCap>) <= 48 * 1024, "more would have to be asked for");
 cudaError_t launch_rows(const void* kern, int64_t rows, int parts, size_t smem, const FilterArgs& a,
                         cudaStream_t st) {
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (e != cudaSuccess) return e;
   FilterArgs b = a;
   void* args[] = {&b};
   return launch_kc(kern, dim3((unsigned)(rows * parts)), dim3(kThr), smem, st, true, dim3(parts), args);
@@ -1870,15 +1898,13 @@ int pick_parts(int64_t V, int64_t rows, size_t esize) {
 }
 // Whether wide rows are left to a second launch: worth it where the first gives
 // a row few CTAs.
-bool defers(int64_t V, size_t esize, int parts) {
-  return parts < kMaxCluster && V * (int64_t)esize / parts > 64 * 1024;
+bool defers(int64_t V, int64_t rows, size_t esize, int parts) {
+  return rows > kInlineRows && parts < kMaxCluster && V * (int64_t)esize / parts > 64 * 1024;
 }
 
 // The second launch: clusters that fill the GPU share out the rows, of eight
 // CTAs, or of four where many rows may come.
 cudaError_t launch_wide(const void* kern, int64_t rows, size_t smem, const FilterArgs& a, cudaStream_t st) {
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (e != cudaSuccess) return e;
   FilterArgs b = a;
   b.defer = 0;
   void* args[] = {&b, &rows};
@@ -1891,7 +1917,7 @@ cudaError_t launch_wide(const void* kern, int64_t rows, size_t smem, const Filte
 template <typename T>
 cudaError_t launch_sample(FilterArgs a, int64_t rows, cudaStream_t st) {
   const int parts = pick_parts(a.V, rows, sizeof(T));
-  a.defer = defers(a.V, sizeof(T), parts);
+  a.defer = defers(a.V, rows, sizeof(T), parts);
   cudaError_t e = launch_rows((const void*)sample_rows_kernel<T>, rows, parts, sizeof(Short), a, st);
   if (e != cudaSuccess || !a.defer) return e;
   return launch_wide((const void*)sample_wide_kernel<T>, rows, sizeof(Short), a, st);
@@ -1900,7 +1926,7 @@ template <typename T>
 cudaError_t launch_accept(FilterArgs a, int64_t b, cudaStream_t st) {
   const int64_t rows = b * a.rows_used;
   const int parts = pick_parts(a.V, rows, sizeof(T));
-  a.defer = defers(a.V, sizeof(T), parts);
+  a.defer = defers(a.V, rows, sizeof(T), parts);
   cudaError_t e = launch_rows((const void*)accept_rows_kernel<T>, rows, parts, sizeof(Short), a, st);
   if (e != cudaSuccess) return e;
   if (a.defer && (e = launch_wide((const void*)accept_wide_kernel<T>, rows, sizeof(Short), a, st)) != cudaSuccess)

@@ -211,6 +211,7 @@ cudaError_t verify_accept(const float* logits, const int* draft, int b, int R, i
 // --- filtered sampling, filtered accept, top logits (k_filter.cu) ---
 constexpr float kFilterMinT = 1e-6f, kFilterMaxT = 1e6f;  // sampling temperatures (0: greedy)
 constexpr int kTopLogitsMax = 1024;
+constexpr int kInlineRows = 64;  // up to so many sampled rows need no state between launches
 struct RowCut {  // one verified row
   uint64_t cut;  // an entry is kept iff its place is at or above it
   float m;       // the row's maximum

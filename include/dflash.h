@@ -360,7 +360,7 @@ DFLASH_API int32_t dflash_commit_draft_block(const dflash_weights* w, const dfla
  * Arguments are checked, and errors returned, as for the other calls.
  * ------------------------------------------------------------------------- */
 
-/* Workspace bytes for dflash_sample. */
+/* Workspace bytes for dflash_sample (0 for up to 64 rows: ws may be NULL). */
 DFLASH_API int32_t dflash_sample_workspace_size(int64_t rows, int64_t V, size_t* bytes);
 
 /* One token per row, drawn from softmax(z / T) under the row's filters.  With

@@ -35,12 +35,13 @@ ROWS = [(EINVAL, dict(logits=N)), (EINVAL, dict(dtype=3)), (EINVAL, dict(dtype=-
 
 def test_sample(lib):
     from block_diffusion_speculative_draft_gb300 import api
-    need = api.dflash_sample_workspace_size(2, 100)
+    need = api.dflash_sample_workspace_size(200, 100)
+    assert api.dflash_sample_workspace_size(64, 100) == 0
     n = ctypes.c_size_t(0)
     for bad in ((0, 100), (1 << 28, 100), (1, 0)):
         assert need > 0 and lib.dflash_sample_workspace_size(*bad, ctypes.byref(n)) == EINVAL
     assert lib.dflash_sample_workspace_size(2, 100, None) == EINVAL
-    args = dict(logits=X, dtype=0, rows=2, V=100, ld=100, temperature=X, k=N, p=N, mp=N, u=X, ld_u=100, tok=X, lp=N,
+    args = dict(logits=X, dtype=0, rows=200, V=100, ld=100, temperature=X, k=N, p=N, mp=N, u=X, ld_u=100, tok=X, lp=N,
                 ws=X, ws_bytes=need, stream=N)
     _refused(lib.dflash_sample, args, [c for c in ROWS if "V" not in c[1] or c[1]["V"] == 0]
              + [(EINVAL, dict(rows=0)), (EINVAL, dict(temperature=N)), (EINVAL, dict(u=N)), (EINVAL, dict(tok=N)),
