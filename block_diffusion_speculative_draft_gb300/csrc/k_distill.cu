@@ -32,67 +32,47 @@ constexpr int kDevBadToken = 0x2;
 constexpr float kMassOne = 1099511627776.f;  // 2^40: probabilities are summed as integers
 constexpr float kLn2 = 0.6931471805599453f;
 
-// Shared memory of one CTA: this header, the teacher's entries (three arrays
-// of K), the bitmap of the part's listed entries, then the part itself.
+// What a part of a row contributes: the entries outside S (reference and sum of
+// 2^(x - reference)), those listed in it (the same, sum p_k (ln p_k - ln 2 (x_k -
+// reference)) and sum p_k), and whether it refuses the row.
+struct PartSums {
+  float ref, sum, lref, lsum, self, p;
+  int bad;
+};
+
+// Shared memory of one CTA: this header, the part of the row, the teacher's
+// entries (four arrays of K), and the bitmap of the part's listed tokens.
 template <int NW>
 struct alignas(16) Shared {
   Exchange<NW> x;
-  float4 warp[2][NW];
-  uint64_t warp_mass[NW];
-  float4 part[kMaxCluster];  // (maximum, sum, refused) of each CTA's part
+  float4 warp[NW];
+  float2 top[NW];
+  uint64_t mass[NW];
+  PartSums part[kMaxCluster];
+  struct {
+    float f, ref, g, in, m;  // factor and reference outside S, weight / T, P / E and reference in S
+    int zero;                // no gradient
+  } plan;
   uint64_t bar;
+  int flags;  // 1: refused, 2: an entry above -inf
 };
 
 struct Entries {
-  float* p;   // the teacher's logits, then its probabilities
-  float* z;   // the student's logits at its tokens
-  int* at;    // the tokens, -1: no entry
+  float* lp;  // the teacher's logits, then log-probabilities
+  float* p;   // its probabilities
+  float* z;   // the student's logits at the tokens of this part
+  int* at;    // place of the token in this part, -1: not here
 };
 __device__ __forceinline__ Entries entries_at(uint8_t* base, int K) {
   Entries e;
-  e.p = reinterpret_cast<float*>(base);
+  e.lp = reinterpret_cast<float*>(base);
+  e.p = e.lp + K;
   e.z = e.p + K;
   e.at = reinterpret_cast<int*>(e.z + K);
   return e;
 }
-__host__ __device__ inline size_t entries_bytes(int K) { return (static_cast<size_t>(K) * 12 + 15) & ~size_t(15); }
+__host__ __device__ inline size_t entries_bytes(int K) { return (static_cast<size_t>(K) * 16 + 15) & ~size_t(15); }
 size_t bitmap_bytes(int64_t n) { return (static_cast<size_t>((n + 31) / 32) * 4 + 15) & ~size_t(15); }
-
-// Sum / maximum of a float over the CTA in a fixed order (every thread gets it).
-template <int NW>
-__device__ __forceinline__ float cta_sum(float v, float4* red) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5].x = v;
-  __syncthreads();
-  v = 0.f;
-#pragma unroll
-  for (int w = 0; w < NW; ++w) v += red[w].x;
-  return v;
-}
-template <int NW>
-__device__ __forceinline__ float cta_max(float v, float4* red) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5].x = v;
-  __syncthreads();
-  v = red[0].x;
-#pragma unroll
-  for (int w = 1; w < NW; ++w) v = fmaxf(v, red[w].x);
-  return v;
-}
-
-// What the teacher's entries contribute, with the student's logits at them.
-// Exponents are in units of log2 (x = z log2(e) / T).
-struct Teacher {
-  float tm;    // largest listed logit (-inf: nothing is listed)
-  bool bad;    // refused by this CTA's view of the row
-  float P;     // sum p + p_r
-  float pr;
-  float ref;   // reference of the listed student logits
-  float es;    // sum of 2^(x_k - ref)
-  float self;  // sum p_k (ln p_k - ln 2 (x_k - ref))
-};
 
 // A reference for exponents whose maximum is m: its own exponent, held within
 // +-kRefMax.  Logits beyond that (the type's lowest value as a mask, infinities
@@ -118,106 +98,169 @@ __device__ __forceinline__ void with_weight(float c, float ref, F f) {
   }
 }
 
-// Reads the row's entries.  `bits` (zero) marks the listed tokens in [c0, c1);
-// a mark that is there already, or a token out of range, refuses the row.
-// `row_z`: the student's logits are wanted for every entry (read from global
-// memory); else es and self are not formed.
-template <typename T, int NT>
-__device__ __forceinline__ Teacher read_teacher(const DistillArgs& a, int64_t row, const T* z, int64_t c0, int64_t c1,
-                                                bool row_z, Entries e, uint32_t* bits, Shared<NT / 32>& s) {
+// A sum of two floats that carries twice their digits.
+struct Pair {
+  float hi, lo;
+};
+__device__ __forceinline__ Pair two_sum(float a, float b) {  // a + b exactly
+  const float s = a + b, t = s - a;
+  return Pair{s, (a - (s - t)) + (b - t)};
+}
+// v / T, from the launcher's pair of 1 / T
+__device__ __forceinline__ Pair over_t(const DistillArgs& a, float v) {
+  const float h = v * a.inv_hi;
+  return Pair{h, fmaf(v, a.inv_hi, -h) + v * a.inv_lo};
+}
+
+struct Teacher {
+  bool some;   // an entry above -inf is listed
+  bool bad;    // refused by this CTA's view of the row
+  float P;     // sum p + p_r
+  float pr;
+};
+
+// Reads the row's entries and forms the teacher's probabilities.  `bits` (zero)
+// marks the listed tokens in [c0, c1); a mark that is there already, or a token
+// out of range, refuses the row.
+template <int NT>
+__device__ __forceinline__ Teacher read_teacher(const DistillArgs& a, int64_t row, int64_t c0, int64_t c1, Entries e,
+                                                uint32_t* bits, Shared<NT / 32>& s) {
   constexpr int NW = NT / 32;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const bool some = warp * 32 < a.K;  // this warp holds entries
-  Teacher t;
+  const bool holds = warp * 32 < a.K;  // this warp holds entries
+  const int used = a.K < NT ? (a.K + 31) / 32 : NW;
   bool bad = false;
-  float tm = -INFINITY, zm = -INFINITY;
+  float tm = -INFINITY;
+  Pair lt{a.t_lse ? a.t_lse[row] : 0.f, 0.f};
   for (int k = threadIdx.x; k < a.K; k += NT) {
     const int i = a.t_idx[row * a.K + k];
     const float v = a.t_val[row * a.K + k];
     const bool in = i >= 0 && i < a.V, own = in && i >= c0 && i < c1;
-    const float zk = own || (in && row_z) ? to_f32(z[i]) : -INFINITY;
     bad |= !in && i != -1;
     if (own) {
       const uint32_t bit = 1u << ((i - c0) & 31);
       bad |= (atomicOr(&bits[(i - c0) >> 5], bit) & bit) != 0;
     }
-    e.at[k] = in ? i : -1;
-    e.p[k] = in ? v : -INFINITY;
-    e.z[k] = zk;
+    e.at[k] = own ? static_cast<int>(i - c0) : -1;
+    e.lp[k] = in ? v : -INFINITY;
     tm = fmaxf(tm, in ? v : -INFINITY);
-    zm = fmaxf(zm, zk);
   }
-  if (some) {
+  if (!a.t_lse) {  // log of the sum over the listed entries
+    if (holds) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      tm = fmaxf(tm, __shfl_xor_sync(0xffffffffu, tm, o));
-      zm = fmaxf(zm, __shfl_xor_sync(0xffffffffu, zm, o));
+      for (int o = 16; o > 0; o >>= 1) tm = fmaxf(tm, __shfl_xor_sync(0xffffffffu, tm, o));
     }
-  }
-  if (lane == 0) s.warp[0][warp] = make_float4(tm, zm, 0.f, 0.f);
-  t.bad = __syncthreads_or(bad);
-#pragma unroll
-  for (int w = 0; w < NW; ++w) {
-    tm = fmaxf(tm, s.warp[0][w].x);
-    zm = fmaxf(zm, s.warp[0][w].y);
-  }
-  t.tm = tm;
-  t.ref = ref_of(zm, a.c);
-  double lt;
-  if (a.t_lse) {
-    lt = static_cast<double>(a.t_lse[row]);
-  } else {
-    float sp = 0.f;
-    for (int k = threadIdx.x; k < a.K; k += NT) sp += exp2f(log2_weight(e.p[k], tm, a.c));
-    lt = static_cast<double>(tm) * a.inv_t + static_cast<double>(logf(cta_sum<NW>(sp, s.warp[1])));
+    if (lane == 0) s.top[warp].x = tm;
     __syncthreads();
+    for (int w = 0; w < used; ++w) tm = fmaxf(tm, s.top[w].x);
+    float sp = 0.f;
+    for (int k = threadIdx.x; k < a.K; k += NT) sp += exp2f(log2_weight(e.lp[k], tm, a.c));
+    if (holds) {
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) sp += __shfl_xor_sync(0xffffffffu, sp, o);
+    }
+    if (lane == 0) s.warp[warp].x = sp;
+    __syncthreads();
+    sp = 0.f;
+    for (int w = 0; w < used; ++w) sp += s.warp[w].x;
+    lt = over_t(a, tm);
+    const Pair sum = two_sum(lt.hi, logf(sp));
+    lt = Pair{sum.hi, sum.lo + lt.lo};
   }
-  // ln p_k = t_k / T - Lt, formed in double: where t_lse is given, p_r is a
-  // difference from one.  The probabilities' sum is an integer sum for the
+  // ln p_k = t_k / T - Lt, to twice a float's digits: where t_lse is given, p_r is
+  // a difference from one.  The probabilities' sum is an integer sum for the
   // same reason.
   uint64_t fixed = 0;
-  float es = 0.f, self = 0.f;
   for (int k = threadIdx.x; k < a.K; k += NT) {
-    const double lp = static_cast<double>(e.p[k]) * a.inv_t - lt;
-    const float hi = static_cast<float>(lp);
+    const float v = e.lp[k];
+    const Pair x = over_t(a, v), d = two_sum(x.hi, -lt.hi);
+    const float hi = v > -INFINITY ? d.hi : v;
     float p = expf(hi);
-    if (hi > -INFINITY) p = fmaf(p, static_cast<float>(lp - static_cast<double>(hi)), p);
+    if (hi > -INFINITY) p = fmaf(p, d.lo + (x.lo - lt.lo), p);
+    e.lp[k] = hi;
     e.p[k] = p;
     fixed += __float2ull_rn(fminf(p, 256.f) * kMassOne);
-    if (row_z && e.at[k] >= 0) {
-      const float x = exponent(e.z[k], a.c, t.ref);
-      es += exp2f(x);
-      if (p > 0.f) self += p * (hi - x * kLn2);
-    }
   }
-  if (some) {
+  if (holds) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      fixed += __shfl_xor_sync(0xffffffffu, fixed, o);
-      es += __shfl_xor_sync(0xffffffffu, es, o);
-      self += __shfl_xor_sync(0xffffffffu, self, o);
-    }
+    for (int o = 16; o > 0; o >>= 1) fixed += __shfl_xor_sync(0xffffffffu, fixed, o);
   }
-  if (lane == 0) {
-    s.warp_mass[warp] = fixed;
-    s.warp[1][warp] = make_float4(es, self, 0.f, 0.f);
-  }
+  if (lane == 0) s.mass[warp] = fixed;
+  if (bad || tm > -INFINITY) atomicOr(&s.flags, (bad ? 1 : 0) | (tm > -INFINITY ? 2 : 0));
   __syncthreads();
+  Teacher t;
+  t.bad = s.flags & 1;
+  t.some = s.flags & 2;
   fixed = 0;
-  t.es = 0.f;
-  t.self = 0.f;
-#pragma unroll
-  for (int w = 0; w < NW; ++w) {
-    fixed += s.warp_mass[w];
-    t.es += s.warp[1][w].x;
-    t.self += s.warp[1][w].y;
-  }
+  for (int w = 0; w < used; ++w) fixed += s.mass[w];
   // in units of 2^-40: one minus the sum, exactly
   const int64_t rest = (static_cast<int64_t>(1) << 40) - static_cast<int64_t>(fixed);
   const float mass = static_cast<float>(fixed) * (1.f / kMassOne);
   t.pr = a.t_lse && rest > 0 ? static_cast<float>(rest) * (1.f / kMassOne) : 0.f;
   t.P = mass + t.pr;
   return t;
+}
+
+// The references of a part: of its entries outside S, whose maximum over this
+// thread's is `top`, and of its listed ones.
+template <int NW>
+__device__ __forceinline__ float2 part_refs(const DistillArgs& a, float top, Entries e, Shared<NW>& s) {
+  float l = -INFINITY;
+  for (int k = threadIdx.x; k < a.K; k += NW * 32)
+    if (e.at[k] >= 0) l = fmaxf(l, e.z[k]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    l = fmaxf(l, __shfl_xor_sync(0xffffffffu, l, o));
+  }
+  if ((threadIdx.x & 31) == 0) s.top[threadIdx.x >> 5] = make_float2(top, l);
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < NW; ++w) {
+    const float2 v = s.top[w];
+    top = fmaxf(top, v.x);
+    l = fmaxf(l, v.y);
+  }
+  return make_float2(ref_of(top, a.c), ref_of(l, a.c));
+}
+
+// Adds up a part (`sum`: this thread's outside S) and sends it to every CTA of
+// the cluster; complete after a cluster barrier.
+template <int NW>
+__device__ __forceinline__ void send_part(const DistillArgs& a, float2 ref, float sum, bool bad, Entries e,
+                                          Shared<NW>& s, int part, int parts) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  float4 v = make_float4(sum, 0.f, 0.f, 0.f);  // sum, lsum, self, p
+  for (int k = threadIdx.x; k < a.K; k += NW * 32) {
+    if (e.at[k] < 0) continue;
+    const float x = exponent(e.z[k], a.c, ref.y), p = e.p[k];
+    v.y += exp2f(x);
+    if (p > 0.f) v.z += p * (e.lp[k] - x * kLn2);
+    v.w += p;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
+  if (warp * 32 < a.K) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
+      v.z += __shfl_xor_sync(0xffffffffu, v.z, o);
+      v.w += __shfl_xor_sync(0xffffffffu, v.w, o);
+    }
+  }
+  if (lane == 0) s.warp[warp] = v;
+  __syncthreads();
+  if (warp == 0) {
+    v = lane < NW ? s.warp[lane] : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
+      v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
+      v.z += __shfl_xor_sync(0xffffffffu, v.z, o);
+      v.w += __shfl_xor_sync(0xffffffffu, v.w, o);
+    }
+    if (lane < parts) *peer(&s.part[part], lane) = PartSums{ref.x, v.x, ref.y, v.y, v.z, v.w, bad};
+  }
 }
 
 // What the row's gradient needs: reference and sum of 2^(x - reference) over
@@ -227,114 +270,133 @@ struct RowSums {
   float m, E, mr, Er;
 };
 
-// Joins the sums outside S with the listed entries'; thread 0 of the row's
-// first CTA writes the loss.
-__device__ __forceinline__ RowSums join_row(const DistillArgs& a, int64_t row, const Teacher& t, float mr, float Er,
-                                            float w, bool writes) {
-  RowSums s;
-  s.mr = mr;
-  s.Er = Er;
-  // a part without a finite logit does not set the reference
-  s.m = t.es > 0.f && Er > 0.f ? fmaxf(t.ref, mr) : (Er > 0.f ? mr : t.ref);
-  s.E = t.es * exp2f(t.ref - s.m) + Er * exp2f(mr - s.m);
-  // a row without any finite logit has no distribution
-  if (s.E == 0.f) s.E = NAN;
-  if (writes) {
-    const float log_e = log2f(s.E);
-    // sum p (ln p - ln q), ln q = ln 2 (x - m - log2 E)
-    float l = t.self + (t.P - t.pr) * (log_e + (s.m - t.ref)) * kLn2;
-    if (t.pr > 0.f) l += t.pr * (logf(t.pr) - (log2f(Er) + (mr - s.m) - log_e) * kLn2);
-    a.loss[row] = w * l;
-    if (a.stats) a.stats[row] = make_float4(s.m, s.E, s.mr, s.Er);
+// What the gradient pass needs of a row, worked out once per CTA.
+template <int NW>
+__device__ __forceinline__ void make_plan(Shared<NW>& s, const RowSums& r, const Teacher& t, float w, float inv_t) {
+  const float g = w * inv_t;
+  s.plan.zero = r.E == 0.f;
+  s.plan.g = g;
+  s.plan.ref = r.mr;
+  s.plan.m = r.m;
+  s.plan.in = t.P / r.E;
+  // factor of 2^(x_j - mr) outside S
+  s.plan.f = r.Er > 0.f ? g * (t.P * exp2f(r.mr - r.m) / r.E - t.pr / r.Er) : 0.f;
+}
+
+// Joins the parts, in rank order, makes the plan and, in the row's first CTA,
+// writes the loss (the first warp).  A part without a finite logit has the
+// lowest reference and no sum.
+template <int NW>
+__device__ __forceinline__ void join_parts(const DistillArgs& a, int64_t row, const Teacher& t, float w,
+                                           Shared<NW>& s, int part, int parts) {
+  const int lane = threadIdx.x & 31;
+  const PartSums q = lane < parts ? s.part[lane] : PartSums{-kRefMax, 0.f, -kRefMax, 0.f, 0.f, 0.f, 0};
+  const bool bad = __any_sync(0xffffffffu, q.bad != 0);
+  RowSums r;
+  r.mr = q.ref;
+  r.m = fmaxf(q.sum > 0.f ? q.ref : -kRefMax, q.lsum > 0.f ? q.lref : -kRefMax);
+#pragma unroll
+  for (int o = kMaxCluster / 2; o > 0; o >>= 1) {
+    r.mr = fmaxf(r.mr, __shfl_xor_sync(0xffffffffu, r.mr, o));
+    r.m = fmaxf(r.m, __shfl_xor_sync(0xffffffffu, r.m, o));
   }
-  return s;
+  r.Er = q.sum * exp2f(q.ref - r.mr);
+  r.E = q.sum * exp2f(q.ref - r.m) + q.lsum * exp2f(q.lref - r.m);
+#pragma unroll
+  for (int o = kMaxCluster / 2; o > 0; o >>= 1) {
+    r.Er += __shfl_xor_sync(0xffffffffu, r.Er, o);
+    r.E += __shfl_xor_sync(0xffffffffu, r.E, o);
+  }
+  if (r.E == 0.f) r.E = NAN;  // a row without any finite logit has no distribution
+  const float log_e = log2f(r.E);
+  // sum p (ln p - ln q), ln q = ln 2 (x - m - log2 E)
+  float l = q.p > 0.f ? q.self + q.p * (log_e + (r.m - q.lref)) * kLn2 : 0.f;
+#pragma unroll
+  for (int o = kMaxCluster / 2; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+  if (lane != 0) return;
+  const bool out = bad || w == 0.f || !t.some;
+  if (part == 0) {
+    if (t.pr > 0.f) l += t.pr * (logf(t.pr) - (log2f(r.Er) + (r.mr - r.m) - log_e) * kLn2);
+    a.loss[row] = out ? (bad ? NAN : 0.f) : w * l;
+    if (a.stats) a.stats[row] = out ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(r.m, r.E, r.mr, r.Er);
+    if (bad) atomicOr(a.status, kDevBadToken);
+  }
+  if (out) r.E = 0.f;
+  make_plan(s, r, t, w, a.inv_hi);
 }
 
-__device__ __forceinline__ void leave_out(const DistillArgs& a, int64_t row, bool bad) {
-  a.loss[row] = bad ? NAN : 0.f;
-  if (a.stats) a.stats[row] = make_float4(0.f, 0.f, 0.f, 0.f);
-}
-
-// Factor of 2^(x_j - mr) outside S.
-__device__ __forceinline__ float outside_factor(const RowSums& s, const Teacher& t, float g) {
-  return s.Er > 0.f ? g * (t.P * exp2f(s.mr - s.m) / s.E - t.pr / s.Er) : 0.f;
-}
-
-// Gradients of the listed entries in [c0, c1).
+// Gradients of the part's listed entries; out: its first entry's.
 template <typename T, int NT>
-__device__ __forceinline__ void listed_gradients(const DistillArgs& a, T* dz, Entries e, int64_t c0, int64_t c1,
-                                                 const RowSums& s, const Teacher& t, float g) {
-  const float f = t.P / s.E;
+__device__ __forceinline__ void listed_gradients(const DistillArgs& a, const Shared<NT / 32>& s, T* out, Entries e) {
+  const float f = s.plan.in, g = s.plan.g, m = s.plan.m;
   for (int k = threadIdx.x; k < a.K; k += NT) {
     const int i = e.at[k];
-    if (i >= c0 && i < c1) dz[i] = from_f32<T>(g * (f * exp2f(exponent(e.z[k], a.c, s.m)) - e.p[k]));
+    if (i >= 0) out[i] = from_f32<T>(g * (f * exp2f(exponent(e.z[k], a.c, m)) - e.p[k]));
   }
 }
 
-// Writes f(entry) of a part to dz: whole packs where source and destination
-// share their alignment, else 32-bit words of the destination, each from the
-// one or two words of the buffer that hold its entries.
+// Writes f(entry) of a part to dz, in 16-byte packs of the destination.  Where
+// those do not line up with the buffer's, each is cut out of two of them: the
+// distance is the same for the whole part.
 template <typename T, int NT, typename F>
 __device__ __forceinline__ void write_part(const Part<T>& q, const T* buf, T* dz, F f) {
-  constexpr int kPer = Pack<T>::kPer;
+  constexpr int kPer = Pack<T>::kPer, kE = Part<T>::kE;
   T* out = dz + q.first;  // entry 0 of the part
-  const uint32_t* words = reinterpret_cast<const uint32_t*>(buf);
   const int phase = static_cast<int>((reinterpret_cast<uintptr_t>(out) & 15) / sizeof(T));
-  if (phase == q.off) {
-    const uint4* src = reinterpret_cast<const uint4*>(buf);
-    T* dst = out - q.off;
-    const bool cut_tail = (q.off + q.n) % Part<T>::kE != 0;
-    for (int j = threadIdx.x; j < q.packs; j += NT) {
-      const uint4 v = src[j];
-      const uint32_t in[4] = {v.x, v.y, v.z, v.w};
-      uint32_t o[4];
+  // destination pack j holds entries j kE - phase ..., which start `shift`
+  // elements into the buffer's pack j + back
+  const int delta = q.off - phase, back = delta < 0 ? -1 : 0, shift = delta < 0 ? delta + kE : delta;
+  const int packs = (phase + q.n + kE - 1) / kE;
+  const uint4* src = reinterpret_cast<const uint4*>(buf);
+  T* dst = out - phase;
+  for (int j = threadIdx.x; j < packs; j += NT) {
+    const int p = j + back;
+    uint4 v = p >= 0 ? src[p] : make_uint4(0, 0, 0, 0);
+    uint32_t in[8] = {v.x, v.y, v.z, v.w, 0, 0, 0, 0};
+    if (shift) {
+      if (p + 1 < q.packs) v = src[p + 1];
+      in[4] = v.x;
+      in[5] = v.y;
+      in[6] = v.z;
+      in[7] = v.w;
+      const int words = shift / kPer;
+      if (words & 2) {
 #pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        float t[kPer];
-        Pack<T>::open(in[w], t);
-#pragma unroll
-        for (int h = 0; h < kPer; ++h) t[h] = f(t[h]);
-        o[w] = Pack<T>::close(t);
+        for (int w = 0; w < 6; ++w) in[w] = in[w + 2];
       }
-      if ((j > 0 || q.off == 0) && (j + 1 < q.packs || !cut_tail)) {
-        reinterpret_cast<uint4*>(dst)[j] = make_uint4(o[0], o[1], o[2], o[3]);
-      } else {
-        const T* t = reinterpret_cast<const T*>(o);
+      if (words & 1) {
 #pragma unroll
-        for (int h = 0; h < Part<T>::kE; ++h) {
-          const int e = j * Part<T>::kE + h - q.off;
-          if (e >= 0 && e < q.n) out[e] = t[h];
+        for (int w = 0; w < 5; ++w) in[w] = in[w + 1];
+      }
+      if (kPer == 2 && (shift & 1)) {
+#pragma unroll
+        for (int w = 0; w < 4; ++w) in[w] = __byte_perm(in[w], in[w + 1], 0x5432);
+      }
+    }
+    uint32_t o[4];
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      float t[kPer];
+      Pack<T>::open(in[w], t);
+#pragma unroll
+      for (int h = 0; h < kPer; ++h) t[h] = f(t[h]);
+      o[w] = Pack<T>::close(t);
+    }
+    const int e0 = j * kE - phase;
+    if (e0 >= 0 && e0 + kE <= q.n) {
+      reinterpret_cast<uint4*>(dst)[j] = make_uint4(o[0], o[1], o[2], o[3]);
+    } else {
+#pragma unroll
+      for (int h = 0; h < kE; ++h) {
+        const uint32_t word = o[h / kPer];
+        const uint32_t bits = kPer == 1 ? word : (h & 1 ? word >> 16 : word & 0xFFFFu);
+        if (e0 + h >= 0 && e0 + h < q.n) {
+          if (kPer == 1)
+            reinterpret_cast<uint32_t*>(out)[e0 + h] = bits;
+          else
+            reinterpret_cast<uint16_t*>(out)[e0 + h] = static_cast<uint16_t>(bits);
         }
       }
-    }
-    return;
-  }
-  // words of the destination: entry e = kPer * j - shift is the first of word j
-  const int shift = kPer == 2 ? phase & 1 : 0;
-  uint32_t* dst = reinterpret_cast<uint32_t*>(out - shift);
-  const int count = (q.n + shift + kPer - 1) / kPer;
-  for (int j = threadIdx.x; j < count; j += NT) {
-    const int e = kPer * j - shift, b = q.off + e;
-    uint32_t w;
-    if (kPer == 1) {
-      w = words[b];
-    } else {
-      // b + 1 may pass the part's last pack only where e + 1 is no entry
-      const uint32_t lo = b >= 0 ? words[b >> 1] : 0u;
-      const uint32_t hi = (b & 1) && e + 1 < q.n ? words[(b + 1) >> 1] : 0u;
-      w = (b & 1) ? __byte_perm(lo, hi, 0x5432) : lo;
-    }
-    float t[kPer];
-    Pack<T>::open(w, t);
-#pragma unroll
-    for (int h = 0; h < kPer; ++h) t[h] = f(t[h]);
-    w = Pack<T>::close(t);
-    if (kPer == 1 || (e >= 0 && e + 1 < q.n)) {
-      dst[j] = w;
-    } else {
-      const T* h = reinterpret_cast<const T*>(&w);
-      if (e >= 0 && e < q.n) out[e] = h[0];
-      if (e + 1 >= 0 && e + 1 < q.n) out[e + 1] = h[1];
     }
   }
 }
@@ -358,45 +420,47 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 5 : 2) distill_kernel(const Di
   T* dz = a.dlogits ? static_cast<T*>(a.dlogits) + row * a.ldd : nullptr;
   Part<T> q;
   q.cut(z, a.V, part, parts);
-  const int64_t c0 = q.first, c1 = q.first + q.n;
   if (threadIdx.x == 0) {
+    s.flags = 0;
     mbar_init(&s.bar, 1);
     fence_mbar_init();
   }
-  for (int i = threadIdx.x; i < (q.n + 31) / 32; i += NT) bits[i] = 0;
-  __syncthreads();
-  if (!kBackward && parts > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
   pdl_wait();
   q.load(z, buf, &s.bar);
+  for (int i = threadIdx.x; i < (q.n + 31) / 32; i += NT) bits[i] = 0;
   const float w = a.weight ? a.weight[row] : 1.f;
-  const Teacher t = read_teacher<T, NT>(a, row, z, c0, c1, !kBackward, e, bits, s);
-  mbar_wait(&s.bar, 0, a.status);
   __syncthreads();
+  if (!kBackward && parts > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+  const Teacher t = read_teacher<NT>(a, row, q.first, q.first + q.n, e, bits, s);
+  mbar_wait(&s.bar, 0, a.status);
+  // the listed entries leave the part
   for (int k = threadIdx.x; k < a.K; k += NT) {
     const int i = e.at[k];
-    if (i >= c0 && i < c1) buf[q.off + i - c0] = from_f32<T>(-INFINITY);
+    if (i < 0) continue;
+    e.z[k] = to_f32(buf[q.off + i]);
+    buf[q.off + i] = from_f32<T>(-INFINITY);
   }
   __syncthreads();
-  RowSums r;
   if (!kBackward) {
-    // maximum and exponential sum of the part, relative to its own maximum
+    // one pass: the sum relative to a reference that follows this thread's
+    // maximum, then brought to the part's
     const uint4* src = reinterpret_cast<const uint4*>(buf);
-    uint32_t mx = Pack<T>::kNegInf;
+    float top = -INFINITY, own = -kRefMax, sum = 0.f;
     for (int j = threadIdx.x; j < q.packs; j += NT) {
-      const uint4 v = src[j];
-      mx = Pack<T>::max2(mx, Pack<T>::max2(Pack<T>::max2(v.x, v.y), Pack<T>::max2(v.z, v.w)));
-    }
-    float v[kPer];
-    Pack<T>::open(mx, v);
-    float pm = v[0];
+      const uint4 y = src[j];
+      const uint32_t in[4] = {y.x, y.y, y.z, y.w};
+      float v[kPer];
+      Pack<T>::open(Pack<T>::max2(Pack<T>::max2(y.x, y.y), Pack<T>::max2(y.z, y.w)), v);
+      float m = v[0];
 #pragma unroll
-    for (int h = 1; h < kPer; ++h) pm = fmaxf(pm, v[h]);
-    float ref = ref_of(cta_max<NW>(pm, s.warp[0]), a.c);
-    float sum = 0.f;
-    with_weight(a.c, ref, [&](auto weight) {
-      for (int j = threadIdx.x; j < q.packs; j += NT) {
-        const uint4 y = src[j];
-        const uint32_t in[4] = {y.x, y.y, y.z, y.w};
+      for (int h = 1; h < kPer; ++h) m = fmaxf(m, v[h]);
+      if (m > top) {
+        const float ref = ref_of(m, a.c);
+        sum *= fast_exp2(own - ref);
+        own = ref;
+        top = m;
+      }
+      with_weight(a.c, own, [&](auto weight) {
         float some = 0.f;
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
@@ -405,48 +469,31 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 5 : 2) distill_kernel(const Di
           for (int h = 0; h < kPer; ++h) some += weight(v[h]);
         }
         sum += some;
-      }
-    });
-    sum = cta_sum<NW>(sum, s.warp[1]);
-    bool bad = t.bad;
-    if (parts > 1) {
-      asm volatile("barrier.cluster.wait.aligned;" ::: "memory");  // the other CTAs have started
-      if (threadIdx.x < parts) *peer(&s.part[part], threadIdx.x) = make_float4(ref, sum, bad ? 1.f : 0.f, 0.f);
-      cluster_sync_all(parts);
-      // references are finite, and below every other where nothing is left
-      ref = -kRefMax;
-      for (int o = 0; o < parts; ++o) {
-        ref = fmaxf(ref, s.part[o].x);
-        bad |= s.part[o].z != 0.f;
-      }
-      sum = 0.f;
-      for (int o = 0; o < parts; ++o) sum += s.part[o].y * exp2f(s.part[o].x - ref);
+      });
     }
-    r = RowSums{0.f, 0.f, 0.f, 0.f};
-    if (bad || w == 0.f || t.tm == -INFINITY) {
-      if (part == 0 && threadIdx.x == 0) {
-        leave_out(a, row, bad);
-        if (bad) atomicOr(a.status, kDevBadToken);
-      }
-    } else if (dz || part == 0) {
-      r = join_row(a, row, t, ref, sum, w, part == 0 && threadIdx.x == 0);
-    }
+    const float2 ref = part_refs<NW>(a, top, e, s);
+    sum *= fast_exp2(own - ref.x);
+    if (parts > 1) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");  // the other CTAs have started
+    send_part<NW>(a, ref, sum, t.bad, e, s, part, parts);
+    cluster_sync_all(parts);
+    if (threadIdx.x < 32) join_parts<NW>(a, row, t, w, s, part, parts);
     if (!dz) return;
-  } else {
-    if (t.bad && threadIdx.x == 0) atomicOr(a.status, kDevBadToken);
+  } else if (threadIdx.x == 0) {
+    if (t.bad) atomicOr(a.status, kDevBadToken);
     const float4 st = a.stats[row];
-    r = RowSums{st.x, t.bad || w == 0.f ? 0.f : st.y, st.z, st.w};
+    make_plan(s, RowSums{st.x, t.bad || w == 0.f ? 0.f : st.y, st.z, st.w}, t, w, a.inv_hi);
   }
-  if (r.E == 0.f) {  // left out or refused
+  __syncthreads();
+  if (s.plan.zero) {  // left out or refused
     write_part<T, NT>(q, buf, dz, [](float) { return 0.f; });
     return;
   }
-  const float g = w / a.T, f = outside_factor(r, t, g);
-  with_weight(a.c, r.mr, [&](auto weight) {
+  const float f = s.plan.f;
+  with_weight(a.c, s.plan.ref, [&](auto weight) {
     write_part<T, NT>(q, buf, dz, [=](float v) { return f * weight(v); });
   });
   __syncthreads();
-  listed_gradients<T, NT>(a, dz, e, c0, c1, r, t, g);
+  listed_gradients<T, NT>(a, s, dz + q.first, e);
 }
 
 // A row too long for the shared memory of a cluster: the same sums by reading
@@ -468,48 +515,41 @@ __global__ void __launch_bounds__(kLongThr) distill_long_kernel(const DistillArg
   T* dz = a.dlogits ? static_cast<T*>(a.dlogits) + row * a.ldd : nullptr;
   const int64_t chunk = (a.V + size - 1) / size;
   const int64_t c0 = chunk * rank < a.V ? chunk * rank : a.V, c1 = c0 + chunk < a.V ? c0 + chunk : a.V;
-  int turn = 0;
   const float w = a.weight ? a.weight[row] : 1.f;
   for (int64_t i = threadIdx.x; i < (c1 - c0 + 31) / 32; i += NT) bits[i] = 0;
+  if (threadIdx.x == 0) s.flags = 0;
   __syncthreads();
-  const Teacher t = read_teacher<T, NT>(a, row, z, c0, c1, true, e, bits, s);
-  cluster_sync_all(size);  // the other CTAs have started
-  const bool bad = cluster_reduce<NW>(t.bad, OpMaxU64(), s.x, rank, size, turn) != 0;
+  const Teacher t = read_teacher<NT>(a, row, c0, c1, e, bits, s);
+  for (int k = threadIdx.x; k < a.K; k += NT)
+    if (e.at[k] >= 0) e.z[k] = to_f32(z[c0 + e.at[k]]);
   auto outside = [&](int64_t i) { return !(bits[(i - c0) >> 5] >> ((i - c0) & 31) & 1); };
-  RowSums r{0.f, 0.f, 0.f, 0.f};
-  if (bad || w == 0.f || t.tm == -INFINITY) {
-    if (rank == 0 && threadIdx.x == 0) {
-      if (!backward) leave_out(a, row, bad);
-      if (bad) atomicOr(a.status, kDevBadToken);
-    }
-  } else if (!backward) {
-    float v = -INFINITY;
+  if (!backward) {
+    float top = -INFINITY;
     for (int64_t i = c0 + threadIdx.x; i < c1; i += NT)
-      if (outside(i)) v = fmaxf(v, to_f32(z[i]));
-    const uint64_t key = cluster_reduce<NW>(max(value_key(v), 0x007FFFFFu), OpMaxU64(), s.x, rank, size, turn);
-    const float ref = ref_of(key_to_value(static_cast<uint32_t>(key)), a.c);
+      if (outside(i)) top = fmaxf(top, to_f32(z[i]));
+    const float2 ref = part_refs<NW>(a, top, e, s);
     float sum = 0.f;
     for (int64_t i = c0 + threadIdx.x; i < c1; i += NT)
-      if (outside(i)) sum += fast_exp2(exponent(to_f32(z[i]), a.c, ref));
-    sum = cta_sum<NW>(sum, s.warp[0]);
-    if (threadIdx.x < size) peer(&s.part[rank], threadIdx.x)->x = sum;
+      if (outside(i)) sum += fast_exp2(exponent(to_f32(z[i]), a.c, ref.x));
+    cluster_sync_all(size);  // the other CTAs have started
+    send_part<NW>(a, ref, sum, t.bad, e, s, rank, size);
     cluster_sync_all(size);
-    sum = 0.f;
-    for (uint32_t o = 0; o < size; ++o) sum += s.part[o].x;
-    r = join_row(a, row, t, ref, sum, w, rank == 0 && threadIdx.x == 0);
-  } else {
+    if (threadIdx.x < 32) join_parts<NW>(a, row, t, w, s, rank, size);
+    if (!dz) return;
+  } else if (threadIdx.x == 0) {
+    if (t.bad) atomicOr(a.status, kDevBadToken);
     const float4 st = a.stats[row];
-    r = RowSums{st.x, st.y, st.z, st.w};
+    make_plan(s, RowSums{st.x, t.bad || w == 0.f ? 0.f : st.y, st.z, st.w}, t, w, a.inv_hi);
   }
-  if (!dz) return;
-  if (r.E == 0.f) {
+  __syncthreads();
+  if (s.plan.zero) {
     for (int64_t i = c0 + threadIdx.x; i < c1; i += NT) dz[i] = from_f32<T>(0.f);
     return;
   }
-  const float g = w / a.T, f = outside_factor(r, t, g);
+  const float f = s.plan.f, ref = s.plan.ref;
   for (int64_t i = c0 + threadIdx.x; i < c1; i += NT)
-    if (outside(i)) dz[i] = from_f32<T>(f * fast_exp2(exponent(to_f32(z[i]), a.c, r.mr)));
-  listed_gradients<T, NT>(a, dz, e, c0, c1, r, t, g);
+    if (outside(i)) dz[i] = from_f32<T>(f * fast_exp2(exponent(to_f32(z[i]), a.c, ref)));
+  listed_gradients<T, NT>(a, s, dz + c0, e);
 }
 
 template <typename T, int NT, bool kBackward>
@@ -558,7 +598,9 @@ cudaError_t launch(const DistillArgs& a, int64_t rows, bool backward, cudaStream
 
 cudaError_t distill(DistillArgs a, int dtype, int64_t rows, bool backward, cudaStream_t st) {
   a.c = static_cast<float>(1.4426950408889634 / static_cast<double>(a.T));
-  a.inv_t = 1.0 / static_cast<double>(a.T);
+  const double inv = 1.0 / static_cast<double>(a.T);
+  a.inv_hi = static_cast<float>(inv);
+  a.inv_lo = static_cast<float>(inv - static_cast<double>(a.inv_hi));
   if (dtype == 0) return launch<float>(a, rows, backward, st);
   if (dtype == 1) return launch<__half>(a, rows, backward, st);
   return launch<__nv_bfloat16>(a, rows, backward, st);

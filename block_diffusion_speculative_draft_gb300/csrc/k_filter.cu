@@ -896,12 +896,16 @@ __device__ __noinline__ Verdict quick_list(const Row<T, NT>& r, Shared<NT, kCap>
   __syncthreads();
   uint32_t rank = 0;
   uint64_t before = 0;
-  const int i1 = half ? n : (n < kQuick / 2 ? n : kQuick / 2);
-  for (int i = half * (kQuick / 2); i < i1; ++i) {
-    const ulonglong2 o = s.entry[i];
-    if (o.x > place) {
-      ++rank;
-      before += o.y;
+  // each of an entry's two threads looks at every other entry; whole warps
+  // without entries of their own pass by
+  if ((e & ~31) < n) {
+#pragma unroll 4
+    for (int i = half; i < n; i += 2) {
+      const ulonglong2 o = s.entry[i];
+      if (o.x > place) {
+        ++rank;
+        before += o.y;
+      }
     }
   }
   if (half == 1) {

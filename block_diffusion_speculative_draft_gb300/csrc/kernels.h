@@ -277,8 +277,8 @@ struct DistillArgs {
   void* dlogits;        // nullable
   int64_t ldd;
   int* status;
-  float c;       // log2(e) / T and 1 / T, set by the launcher
-  double inv_t;
+  float c;               // log2(e) / T and 1 / T as a float pair, set by the launcher
+  float inv_hi, inv_lo;
 };
 cudaError_t distill(DistillArgs a, int dtype, int64_t rows, bool backward, cudaStream_t st);
 
