@@ -15,12 +15,13 @@
 // scaled by their own maximum, so q_r keeps its precision when the student
 // puts nearly everything on S.
 //
-// Bound by HBM: the row is read, and its gradient written.  A row belongs to
-// a cluster of up to eight CTAs whose shared memory holds it (one bulk copy
-// each), so maximum, sum and gradient take one read of HBM; one exchange of
-// (maximum, sum, refusal) joins the parts.  The listed entries become -inf in
-// shared memory: the loops over the part then need no membership test, and
-// the listed gradients are written after them.
+// Bound by HBM: the row is read, and its gradient written.  A cluster of CTAs
+// takes a row, each a part of it: one pass for the sums, one exchange of them,
+// and a second pass for the gradient, which finds the part in L2 (the CTAs on
+// the GPU hold some 70 MB of parts of its 129 MB).  Nothing but the entries'
+// bookkeeping is kept on chip, so enough loads are in flight to fill HBM while
+// other CTAs exchange.  Entries of S are told by a bitmap of the part, which
+// also shows a token listed twice; the listed gradients are written last.
 #include "kernels.h"
 #include "rows.cuh"
 
@@ -40,11 +41,10 @@ struct PartSums {
   int bad;
 };
 
-// Shared memory of one CTA: this header, the part of the row, the teacher's
-// entries (four arrays of K), and the bitmap of the part's listed tokens.
+// Shared memory of one CTA: this header, the teacher's entries (four arrays of
+// K), and the bitmap of the part's listed tokens.
 template <int NW>
 struct alignas(16) Shared {
-  Exchange<NW> x;
   float4 warp[NW];
   float2 top[NW];
   uint64_t mass[NW];
@@ -53,7 +53,6 @@ struct alignas(16) Shared {
     float f, ref, g, in, m;  // factor and reference outside S, weight / T, P / E and reference in S
     int zero;                // no gradient
   } plan;
-  uint64_t bar;
   int flags;  // 1: refused, 2: an entry above -inf
 };
 
@@ -119,11 +118,12 @@ struct Teacher {
   float pr;
 };
 
-// Reads the row's entries and forms the teacher's probabilities.  `bits` (zero)
-// marks the listed tokens in [c0, c1); a mark that is there already, or a token
-// out of range, refuses the row.
-template <int NT>
-__device__ __forceinline__ Teacher read_teacher(const DistillArgs& a, int64_t row, int64_t c0, int64_t c1, Entries e,
+// Reads the row's entries, with the student's logits at those of this part, and
+// forms the teacher's probabilities.  `bits` (zero) marks the part's listed
+// elements; a mark that is there already, or a token out of range, refuses the
+// row.
+template <typename T, int NT>
+__device__ __forceinline__ Teacher read_teacher(const DistillArgs& a, int64_t row, const Part<T>& q, Entries e,
                                                 uint32_t* bits, Shared<NT / 32>& s) {
   constexpr int NW = NT / 32;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -135,13 +135,15 @@ __device__ __forceinline__ Teacher read_teacher(const DistillArgs& a, int64_t ro
   for (int k = threadIdx.x; k < a.K; k += NT) {
     const int i = a.t_idx[row * a.K + k];
     const float v = a.t_val[row * a.K + k];
-    const bool in = i >= 0 && i < a.V, own = in && i >= c0 && i < c1;
+    const int64_t at = i - q.first;
+    const bool in = i >= 0 && i < a.V, own = in && at >= 0 && at < q.n;
     bad |= !in && i != -1;
     if (own) {
-      const uint32_t bit = 1u << ((i - c0) & 31);
-      bad |= (atomicOr(&bits[(i - c0) >> 5], bit) & bit) != 0;
+      const uint32_t x = static_cast<uint32_t>(q.off + at), bit = 1u << (x & 31);
+      bad |= (atomicOr(&bits[x >> 5], bit) & bit) != 0;
+      e.z[k] = to_f32(q.row[i]);
     }
-    e.at[k] = own ? static_cast<int>(i - c0) : -1;
+    e.at[k] = own ? static_cast<int>(at) : -1;
     e.lp[k] = in ? v : -INFINITY;
     tm = fmaxf(tm, in ? v : -INFINITY);
   }
@@ -335,31 +337,87 @@ __device__ __forceinline__ void listed_gradients(const DistillArgs& a, const Sha
   }
 }
 
+constexpr int kFlight = 4;  // packs a thread loads at a time
+
+// The listed elements of pack j become -inf.
+template <typename T>
+__device__ __forceinline__ void mask_listed(const uint32_t* bits, int j, uint4& w) {
+  constexpr int kE = Part<T>::kE;
+  const uint32_t m = bits[(j * kE) >> 5] >> ((j * kE) & 31) & ((1u << kE) - 1);
+  if (m == 0) return;
+  uint32_t in[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int h = 0; h < kE; ++h) {
+    constexpr int kPer = Pack<T>::kPer;
+    if (!(m >> h & 1)) continue;
+    const uint32_t lane = kPer == 1 ? 0xFFFFFFFFu : (h & 1 ? 0xFFFF0000u : 0xFFFFu);
+    in[h / kPer] = (in[h / kPer] & ~lane) | (Pack<T>::kNegInf & lane);
+  }
+  w = make_uint4(in[0], in[1], in[2], in[3]);
+}
+
 // Writes f(entry) of a part to dz, in 16-byte packs of the destination.  Where
-// those do not line up with the buffer's, each is cut out of two of them: the
+// those do not line up with the row's, each is cut out of two of them: the
 // distance is the same for the whole part.
 template <typename T, int NT, typename F>
-__device__ __forceinline__ void write_part(const Part<T>& q, const T* buf, T* dz, F f) {
+__device__ __forceinline__ void write_part(const Part<T>& q, T* dz, F f) {
   constexpr int kPer = Pack<T>::kPer, kE = Part<T>::kE;
   T* out = dz + q.first;  // entry 0 of the part
   const int phase = static_cast<int>((reinterpret_cast<uintptr_t>(out) & 15) / sizeof(T));
   // destination pack j holds entries j kE - phase ..., which start `shift`
-  // elements into the buffer's pack j + back
+  // elements into the row's pack j + back
   const int delta = q.off - phase, back = delta < 0 ? -1 : 0, shift = delta < 0 ? delta + kE : delta;
   const int packs = (phase + q.n + kE - 1) / kE;
-  const uint4* src = reinterpret_cast<const uint4*>(buf);
   T* dst = out - phase;
-  for (int j = threadIdx.x; j < packs; j += NT) {
-    const int p = j + back;
-    uint4 v = p >= 0 ? src[p] : make_uint4(0, 0, 0, 0);
-    uint32_t in[8] = {v.x, v.y, v.z, v.w, 0, 0, 0, 0};
-    if (shift) {
-      if (p + 1 < q.packs) v = src[p + 1];
-      in[4] = v.x;
-      in[5] = v.y;
-      in[6] = v.z;
-      in[7] = v.w;
-      const int words = shift / kPer;
+  auto put = [&](int j, const uint32_t* in) {
+    uint32_t o[4];
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      float t[kPer];
+      Pack<T>::open(in[w], t);
+#pragma unroll
+      for (int h = 0; h < kPer; ++h) t[h] = f(t[h]);
+      o[w] = Pack<T>::close(t);
+    }
+    const int e0 = j * kE - phase;
+    if (e0 >= 0 && e0 + kE <= q.n) {
+      __stcs(reinterpret_cast<uint4*>(dst) + j, make_uint4(o[0], o[1], o[2], o[3]));
+      return;
+    }
+#pragma unroll
+    for (int h = 0; h < kE; ++h) {
+      const uint32_t word = o[h / kPer];
+      if (e0 + h < 0 || e0 + h >= q.n) continue;
+      if (kPer == 1)
+        reinterpret_cast<uint32_t*>(out)[e0 + h] = word;
+      else
+        reinterpret_cast<uint16_t*>(out)[e0 + h] = static_cast<uint16_t>(h & 1 ? word >> 16 : word);
+    }
+  };
+  if (shift == 0) {
+    for (int j = threadIdx.x; j < packs; j += kFlight * NT) {
+      uint4 v[kFlight];
+#pragma unroll
+      for (int x = 0; x < kFlight; ++x) v[x] = q.template pack<true>(j + x * NT);
+#pragma unroll
+      for (int x = 0; x < kFlight; ++x) {
+        const uint32_t in[4] = {v[x].x, v[x].y, v[x].z, v[x].w};
+        if (j + x * NT < packs) put(j + x * NT, in);
+      }
+    }
+    return;
+  }
+  const int words = shift / kPer;
+  for (int j = threadIdx.x; j < packs; j += 2 * NT) {
+    uint4 v[2][2];
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      v[x][0] = q.pack(j + x * NT + back);
+      v[x][1] = q.pack(j + x * NT + back + 1);
+    }
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      uint32_t in[8] = {v[x][0].x, v[x][0].y, v[x][0].z, v[x][0].w, v[x][1].x, v[x][1].y, v[x][1].z, v[x][1].w};
       if (words & 2) {
 #pragma unroll
         for (int w = 0; w < 6; ++w) in[w] = in[w + 2];
@@ -372,88 +430,49 @@ __device__ __forceinline__ void write_part(const Part<T>& q, const T* buf, T* dz
 #pragma unroll
         for (int w = 0; w < 4; ++w) in[w] = __byte_perm(in[w], in[w + 1], 0x5432);
       }
-    }
-    uint32_t o[4];
-#pragma unroll
-    for (int w = 0; w < 4; ++w) {
-      float t[kPer];
-      Pack<T>::open(in[w], t);
-#pragma unroll
-      for (int h = 0; h < kPer; ++h) t[h] = f(t[h]);
-      o[w] = Pack<T>::close(t);
-    }
-    const int e0 = j * kE - phase;
-    if (e0 >= 0 && e0 + kE <= q.n) {
-      reinterpret_cast<uint4*>(dst)[j] = make_uint4(o[0], o[1], o[2], o[3]);
-    } else {
-#pragma unroll
-      for (int h = 0; h < kE; ++h) {
-        const uint32_t word = o[h / kPer];
-        const uint32_t bits = kPer == 1 ? word : (h & 1 ? word >> 16 : word & 0xFFFFu);
-        if (e0 + h >= 0 && e0 + h < q.n) {
-          if (kPer == 1)
-            reinterpret_cast<uint32_t*>(out)[e0 + h] = bits;
-          else
-            reinterpret_cast<uint16_t*>(out)[e0 + h] = static_cast<uint16_t>(bits);
-        }
-      }
+      if (j + x * NT < packs) put(j + x * NT, in);
     }
   }
 }
 
-// A row held in the shared memory of its cluster (`parts` CTAs), or in the
-// backward call one part of it per CTA: the statistics are given, so the parts
-// need nothing of one another.
+// A row by a cluster of `parts` CTAs, or in the backward call, where the sums
+// are given, by `parts` CTAs that need nothing of one another.
 template <typename T, int NT, bool kBackward>
-__global__ void __launch_bounds__(NT, NT == 256 ? 5 : 2) distill_kernel(const DistillArgs a, const int parts,
-                                                                       const uint32_t part_bytes) {
-  constexpr int NW = NT / 32, kPer = Pack<T>::kPer;
+__global__ void __launch_bounds__(NT, NT == 256 ? 5 : 1) distill_kernel(const DistillArgs a, const int parts) {
+  constexpr int NW = NT / 32, kE = Part<T>::kE;
   extern __shared__ __align__(16) uint8_t raw[];
   Shared<NW>& s = *reinterpret_cast<Shared<NW>*>(raw);
-  T* buf = reinterpret_cast<T*>(raw + sizeof(Shared<NW>));
-  uint8_t* after = raw + sizeof(Shared<NW>) + part_bytes;
-  const Entries e = entries_at(after, a.K);
-  uint32_t* bits = reinterpret_cast<uint32_t*>(after + entries_bytes(a.K));
+  const Entries e = entries_at(raw + sizeof(Shared<NW>), a.K);
+  uint32_t* bits = reinterpret_cast<uint32_t*>(raw + sizeof(Shared<NW>) + entries_bytes(a.K));
   const int64_t row = blockIdx.x >> (31 - __clz(parts));
   const int part = static_cast<int>(blockIdx.x & (parts - 1));
-  const T* z = static_cast<const T*>(a.logits) + row * a.ld;
   T* dz = a.dlogits ? static_cast<T*>(a.dlogits) + row * a.ldd : nullptr;
   Part<T> q;
-  q.cut(z, a.V, part, parts);
-  if (threadIdx.x == 0) {
-    s.flags = 0;
-    mbar_init(&s.bar, 1);
-    fence_mbar_init();
-  }
+  q.cut(static_cast<const T*>(a.logits) + row * a.ld, a.V, part, parts);
   pdl_wait();
-  q.load(z, buf, &s.bar);
-  for (int i = threadIdx.x; i < (q.n + 31) / 32; i += NT) bits[i] = 0;
+  uint4 v[kFlight];  // the first packs are on their way while the entries are read
+  if (!kBackward) {
+#pragma unroll
+    for (int x = 0; x < kFlight; ++x) v[x] = q.pack(threadIdx.x + x * NT);
+  }
+  for (int i = threadIdx.x; i < (q.off + q.n + 31) / 32; i += NT) bits[i] = 0;
+  if (threadIdx.x == 0) s.flags = 0;
   const float w = a.weight ? a.weight[row] : 1.f;
   __syncthreads();
   if (!kBackward && parts > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
-  const Teacher t = read_teacher<NT>(a, row, q.first, q.first + q.n, e, bits, s);
-  mbar_wait(&s.bar, 0, a.status);
-  // the listed entries leave the part
-  for (int k = threadIdx.x; k < a.K; k += NT) {
-    const int i = e.at[k];
-    if (i < 0) continue;
-    e.z[k] = to_f32(buf[q.off + i]);
-    buf[q.off + i] = from_f32<T>(-INFINITY);
-  }
-  __syncthreads();
+  const Teacher t = read_teacher<T, NT>(a, row, q, e, bits, s);
   if (!kBackward) {
-    // one pass: the sum relative to a reference that follows this thread's
-    // maximum, then brought to the part's
-    const uint4* src = reinterpret_cast<const uint4*>(buf);
+    // the sum relative to a reference that follows this thread's maximum, then
+    // brought to the part's
     float top = -INFINITY, own = -kRefMax, sum = 0.f;
-    for (int j = threadIdx.x; j < q.packs; j += NT) {
-      const uint4 y = src[j];
-      const uint32_t in[4] = {y.x, y.y, y.z, y.w};
-      float v[kPer];
-      Pack<T>::open(Pack<T>::max2(Pack<T>::max2(y.x, y.y), Pack<T>::max2(y.z, y.w)), v);
-      float m = v[0];
+    for (int j = threadIdx.x; j < q.packs; j += kFlight * NT) {
 #pragma unroll
-      for (int h = 1; h < kPer; ++h) m = fmaxf(m, v[h]);
+      for (int x = 0; x < kFlight; ++x)
+        if (j + x * NT < q.packs) mask_listed<T>(bits, j + x * NT, v[x]);
+      uint32_t mx = Part<T>::max_words(v[0]);
+#pragma unroll
+      for (int x = 1; x < kFlight; ++x) mx = Pack<T>::max2(mx, Part<T>::max_words(v[x]));
+      const float m = Part<T>::max_of(mx);
       if (m > top) {
         const float ref = ref_of(m, a.c);
         sum *= fast_exp2(own - ref);
@@ -461,15 +480,17 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 5 : 2) distill_kernel(const Di
         top = m;
       }
       with_weight(a.c, own, [&](auto weight) {
-        float some = 0.f;
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          Pack<T>::open(in[x], v);
+        for (int x = 0; x < kFlight; ++x) {
+          float z[kE], some = 0.f;
+          Part<T>::open(v[x], z);
 #pragma unroll
-          for (int h = 0; h < kPer; ++h) some += weight(v[h]);
+          for (int h = 0; h < kE; ++h) some += weight(z[h]);
+          sum += some;
         }
-        sum += some;
       });
+#pragma unroll
+      for (int x = 0; x < kFlight; ++x) v[x] = q.pack(j + (kFlight + x) * NT);
     }
     const float2 ref = part_refs<NW>(a, top, e, s);
     sum *= fast_exp2(own - ref.x);
@@ -485,113 +506,49 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 5 : 2) distill_kernel(const Di
   }
   __syncthreads();
   if (s.plan.zero) {  // left out or refused
-    write_part<T, NT>(q, buf, dz, [](float) { return 0.f; });
+    write_part<T, NT>(q, dz, [](float) { return 0.f; });
     return;
   }
   const float f = s.plan.f;
   with_weight(a.c, s.plan.ref, [&](auto weight) {
-    write_part<T, NT>(q, buf, dz, [=](float v) { return f * weight(v); });
+    write_part<T, NT>(q, dz, [=](float z) { return f * weight(z); });
   });
   __syncthreads();
   listed_gradients<T, NT>(a, s, dz + q.first, e);
 }
 
-// A row too long for the shared memory of a cluster: the same sums by reading
-// the row from global memory for each of them, with the listed entries told by
-// the bitmap.
-constexpr int kLongThr = 512;
-
-template <typename T>
-__global__ void __launch_bounds__(kLongThr) distill_long_kernel(const DistillArgs a, const bool backward) {
-  constexpr int NT = kLongThr, NW = NT / 32;
-  extern __shared__ __align__(16) uint8_t raw[];
-  Shared<NW>& s = *reinterpret_cast<Shared<NW>*>(raw);
-  const Entries e = entries_at(raw + sizeof(Shared<NW>), a.K);
-  uint32_t* bits = reinterpret_cast<uint32_t*>(raw + sizeof(Shared<NW>) + entries_bytes(a.K));
-  pdl_wait();
-  const uint32_t rank = cluster_rank(), size = cluster_size();
-  const int64_t row = blockIdx.x / size;
-  const T* z = static_cast<const T*>(a.logits) + row * a.ld;
-  T* dz = a.dlogits ? static_cast<T*>(a.dlogits) + row * a.ldd : nullptr;
-  const int64_t chunk = (a.V + size - 1) / size;
-  const int64_t c0 = chunk * rank < a.V ? chunk * rank : a.V, c1 = c0 + chunk < a.V ? c0 + chunk : a.V;
-  const float w = a.weight ? a.weight[row] : 1.f;
-  for (int64_t i = threadIdx.x; i < (c1 - c0 + 31) / 32; i += NT) bits[i] = 0;
-  if (threadIdx.x == 0) s.flags = 0;
-  __syncthreads();
-  const Teacher t = read_teacher<NT>(a, row, c0, c1, e, bits, s);
-  for (int k = threadIdx.x; k < a.K; k += NT)
-    if (e.at[k] >= 0) e.z[k] = to_f32(z[c0 + e.at[k]]);
-  auto outside = [&](int64_t i) { return !(bits[(i - c0) >> 5] >> ((i - c0) & 31) & 1); };
-  if (!backward) {
-    float top = -INFINITY;
-    for (int64_t i = c0 + threadIdx.x; i < c1; i += NT)
-      if (outside(i)) top = fmaxf(top, to_f32(z[i]));
-    const float2 ref = part_refs<NW>(a, top, e, s);
-    float sum = 0.f;
-    for (int64_t i = c0 + threadIdx.x; i < c1; i += NT)
-      if (outside(i)) sum += fast_exp2(exponent(to_f32(z[i]), a.c, ref.x));
-    cluster_sync_all(size);  // the other CTAs have started
-    send_part<NW>(a, ref, sum, t.bad, e, s, rank, size);
-    cluster_sync_all(size);
-    if (threadIdx.x < 32) join_parts<NW>(a, row, t, w, s, rank, size);
-    if (!dz) return;
-  } else if (threadIdx.x == 0) {
-    if (t.bad) atomicOr(a.status, kDevBadToken);
-    const float4 st = a.stats[row];
-    make_plan(s, RowSums{st.x, t.bad || w == 0.f ? 0.f : st.y, st.z, st.w}, t, w, a.inv_hi);
-  }
-  __syncthreads();
-  if (s.plan.zero) {
-    for (int64_t i = c0 + threadIdx.x; i < c1; i += NT) dz[i] = from_f32<T>(0.f);
-    return;
-  }
-  const float f = s.plan.f, ref = s.plan.ref;
-  for (int64_t i = c0 + threadIdx.x; i < c1; i += NT)
-    if (outside(i)) dz[i] = from_f32<T>(f * fast_exp2(exponent(to_f32(z[i]), a.c, ref)));
-  listed_gradients<T, NT>(a, s, dz + c0, e);
-}
-
 template <typename T, int NT, bool kBackward>
-cudaError_t launch_resident(const DistillArgs& a, int64_t rows, int parts, cudaStream_t st) {
-  const uint32_t pb = static_cast<uint32_t>(Part<T>::bytes(a.V, parts));
-  const size_t smem = sizeof(Shared<NT / 32>) + pb + entries_bytes(a.K) + bitmap_bytes(pb / sizeof(T));
+cudaError_t launch_kernel(const DistillArgs& a, int64_t rows, int parts, cudaStream_t st) {
+  const int64_t most = a.V / parts + 2 * Part<T>::kE;
+  const size_t smem = sizeof(Shared<NT / 32>) + entries_bytes(a.K) + bitmap_bytes(most);
   const void* kern = (const void*)distill_kernel<T, NT, kBackward>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (e != cudaSuccess) return e;
+  if (smem > 48 * 1024) {
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+  }
   DistillArgs b = a;
-  void* args[] = {&b, &parts, const_cast<uint32_t*>(&pb)};
+  void* args[] = {&b, &parts};
   return launch_kc(kern, dim3((unsigned)(rows * parts)), dim3(NT), smem, st, true, dim3(kBackward ? 1 : parts), args);
 }
 
-// Largest part a CTA keeps beside the entries and the bitmap.
-constexpr size_t kPartMax = 180 * 1024;
-
 template <typename T>
 cudaError_t launch(const DistillArgs& a, int64_t rows, bool backward, cudaStream_t st) {
-  // parts of at most 40 KB let five CTAs share an SM; rows that do not fill the
-  // GPU are cut further
+  // Loss with gradient: parts of at most 80 KB keep what the GPU's CTAs read
+  // twice well inside L2 (2048 x 151936 bf16: 347 / 264 / 270 / 293 us at 40 / 80 /
+  // 160 / 320 KB).  One pass alone wants few CTAs a row (loss: 231 / 159 / 131 / 120
+  // us).  Rows that do not fill the GPU are cut further.
+  const int64_t most = (backward || !a.dlogits ? 320 : 80) * 1024;
   int parts = 1;
-  while (parts < kMaxCluster && (Part<T>::bytes(a.V, parts) > 40 * 1024 ||
-                                 (rows * parts < 2 * num_sms() && Part<T>::bytes(a.V, 2 * parts) >= 4096)))
+  while (parts < kMaxCluster && (a.V * (int64_t)sizeof(T) / parts > most ||
+                                 (rows * parts < 2 * num_sms() && a.V * (int64_t)sizeof(T) / (2 * parts) >= 4096)))
     parts *= 2;
-  const size_t pb = Part<T>::bytes(a.V, parts);
-  if (pb <= kPartMax) {
-    if (pb <= 40 * 1024)
-      return backward ? launch_resident<T, 256, true>(a, rows, parts, st)
-                      : launch_resident<T, 256, false>(a, rows, parts, st);
-    return backward ? launch_resident<T, 512, true>(a, rows, parts, st)
-                    : launch_resident<T, 512, false>(a, rows, parts, st);
-  }
-  const size_t smem = sizeof(Shared<kLongThr / 32>) + entries_bytes(a.K) +
-                      bitmap_bytes((a.V + kMaxCluster - 1) / kMaxCluster);
-  const void* kern = (const void*)distill_long_kernel<T>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (e != cudaSuccess) return e;
-  DistillArgs b = a;
-  void* args[] = {&b, &backward};
-  return launch_kc(kern, dim3((unsigned)(rows * kMaxCluster)), dim3(kLongThr), smem, st, true, dim3(kMaxCluster),
-                   args);
+  // few rows: one large CTA an SM, whose threads have little to do one after
+  // another
+  if (rows * parts <= num_sms())
+    return backward ? launch_kernel<T, 1024, true>(a, rows, parts, st)
+                    : launch_kernel<T, 1024, false>(a, rows, parts, st);
+  return backward ? launch_kernel<T, 256, true>(a, rows, parts, st)
+                  : launch_kernel<T, 256, false>(a, rows, parts, st);
 }
 
 }  // namespace

@@ -106,8 +106,6 @@ struct Row {
   static constexpr int kPer = Pack<T>::kPer, kE = Part<T>::kE;
   const T* p;
   Part<T> part;
-  const uint4* packs;  // pack 0 (its first `off` entries lie before the part)
-  bool cut_head, cut_tail;
   uint32_t rank, size;
   float m;             // the row's maximum
   float c;             // log2(e) / temperature
@@ -123,46 +121,17 @@ struct Row {
     scale = a.scale;
     unit = a.unit;
     part.cut(p, a.V, static_cast<int>(rank), static_cast<int>(size));
-    packs = reinterpret_cast<const uint4*>(p + part.first - part.off);
-    cut_head = part.off > 0;
-    cut_tail = (part.off + part.n) % kE != 0;
   }
   __device__ __forceinline__ float at(int64_t i) const { return to_f32(p[i]); }
-  __device__ __forceinline__ int64_t index_of(int j) const { return part.first + j * kE - part.off; }
+  __device__ __forceinline__ int64_t index_of(int j) const { return part.index_of(j); }
   __device__ __forceinline__ float log2w(float v) const { return log2_weight(v, m, c); }
   __device__ __forceinline__ unsigned long long weight(float v) const {
     return __float2ull_rn(exp2f(log2w(v)) * scale);
   }
-  // Pack j; entries that are not the row's come as -inf, and a pack past the
-  // part as nothing else.
-  __device__ __forceinline__ uint4 pack(int j) const {
-    uint4 v = make_uint4(Pack<T>::kNegInf, Pack<T>::kNegInf, Pack<T>::kNegInf, Pack<T>::kNegInf);
-    if (j >= part.packs) return v;
-    if ((j > 0 || !cut_head) && (j + 1 < part.packs || !cut_tail)) return packs[j];
-    T* e = reinterpret_cast<T*>(&v);
-#pragma unroll
-    for (int h = 0; h < kE; ++h) {
-      const int i = j * kE + h - part.off;
-      if (i >= 0 && i < part.n) e[h] = p[part.first + i];
-    }
-    return v;
-  }
-  static __device__ __forceinline__ void open_pack(const uint4& w, float* v) {  // kE values
-    const uint32_t in[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-    for (int x = 0; x < 4; ++x) Pack<T>::open(in[x], v + x * kPer);
-  }
-  static __device__ __forceinline__ uint32_t max_pack(const uint4& w) {
-    return Pack<T>::max2(Pack<T>::max2(w.x, w.y), Pack<T>::max2(w.z, w.w));
-  }
-  static __device__ __forceinline__ float max_of(uint32_t w) {
-    float v[kPer];
-    Pack<T>::open(w, v);
-    float r = v[0];
-#pragma unroll
-    for (int h = 1; h < kPer; ++h) r = fmaxf(r, v[h]);
-    return r;
-  }
+  __device__ __forceinline__ uint4 pack(int j) const { return part.pack(j); }
+  static __device__ __forceinline__ void open_pack(const uint4& w, float* v) { Part<T>::open(w, v); }
+  static __device__ __forceinline__ uint32_t max_pack(const uint4& w) { return Part<T>::max_words(w); }
+  static __device__ __forceinline__ float max_of(uint32_t w) { return Part<T>::max_of(w); }
   // Entry h (not a constant) of a pack.
   static __device__ __forceinline__ float pick_of(const uint4& w, int h) {
     const int x = h / kPer;
@@ -177,7 +146,7 @@ struct Row {
 #pragma unroll
     for (int h = 0; h < kE; ++h) out[h] = 0.f;
     if (j >= part.packs) return;
-    if (wide && (j > 0 || !cut_head) && (j + 1 < part.packs || !cut_tail)) {
+    if (wide && part.whole(j)) {
       const float4* q = reinterpret_cast<const float4*>(u0 + static_cast<int64_t>(j) * kE);
 #pragma unroll
       for (int h = 0; h < kE; h += 4) {

@@ -124,52 +124,68 @@ struct Pack<__nv_bfloat16> {
   }
 };
 
-// One part of a row held in shared memory.  A row is cut at 16-byte
-// boundaries of its global addresses, so the part's packs move by one bulk
-// copy and only the row's first and last pack can be partial: their missing
-// entries are -inf in shared memory.  Entry e of the part (row entry first + e)
-// is element off + e of the buffer.
+// One part of a row, read in 16-byte packs.  A row is cut at 16-byte boundaries
+// of its addresses, so only its first and last pack can be partial.  Entry e of
+// the part (row entry first + e) is element off + e of its packs.
 template <typename T>
 struct Part {
-  static constexpr int kE = 16 / sizeof(T);
+  static constexpr int kPer = Pack<T>::kPer, kE = 16 / sizeof(T);
+  const T* row;
+  const uint4* base;  // pack 0
   int64_t first;
   int n, off, packs;
+  bool cut_head, cut_tail;
 
-  __device__ __forceinline__ void cut(const T* row, int64_t V, int part, int parts) {  // parts: a power of two
-    const int o = static_cast<int>((reinterpret_cast<uintptr_t>(row) & 15) / sizeof(T));
+  __device__ __forceinline__ void cut(const T* p, int64_t V, int part, int parts) {  // parts: a power of two
+    const int o = static_cast<int>((reinterpret_cast<uintptr_t>(p) & 15) / sizeof(T));
     const int64_t all = (V + o + kE - 1) / kE;
     const int lg = 31 - __clz(parts);
     const int64_t p0 = (all * part) >> lg, p1 = (all * (part + 1)) >> lg;
     const int64_t e0 = p0 * kE - o > 0 ? p0 * kE - o : 0;
     const int64_t e1 = p1 * kE - o < V ? p1 * kE - o : V;
+    row = p;
     first = e0;
     n = e1 > e0 ? static_cast<int>(e1 - e0) : 0;
     off = p0 == 0 ? o : 0;
     packs = static_cast<int>(p1 - p0);
+    base = reinterpret_cast<const uint4*>(p + first - off);
+    cut_head = off > 0;
+    cut_tail = (off + n) % kE != 0;
   }
-  // Starts the copy (thread 0, mbarrier `bar`) and loads the partial packs
-  // (all threads); the part is complete after a wait on `bar` and a barrier.
-  __device__ __forceinline__ void load(const T* row, T* buf, uint64_t* bar) const {
-    const int b0 = off > 0 ? 1 : 0;
-    const int b1 = (off + n) / kE > b0 ? (off + n) / kE : b0;  // full packs [b0, b1)
-    if (threadIdx.x == 0) {
-      const uint32_t bytes = static_cast<uint32_t>(b1 - b0) * 16u;
-      mbar_arrive_expect_tx(bar, bytes);
-      fence_proxy_async_global();  // the logits were written with generic stores
-      if (bytes) bulk_g2s(buf + b0 * kE, row + first + b0 * kE - off, bytes, bar);
-    }
-    if (threadIdx.x < 2 * kE) {  // the first pack, then the one after the full ones
-      const int at = threadIdx.x < kE ? threadIdx.x : b1 * kE + threadIdx.x - kE;
-      const bool partial = threadIdx.x < kE ? b0 == 1 : b1 < packs;
-      if (partial) {
-        const int e = at - off;
-        buf[at] = e >= 0 && e < n ? row[first + e] : from_f32<T>(-INFINITY);
-      }
-    }
+  __device__ __forceinline__ int64_t index_of(int j) const { return first + j * kE - off; }
+  __device__ __forceinline__ bool whole(int j) const {
+    return (j > 0 || !cut_head) && (j + 1 < packs || !cut_tail);
   }
-  static __host__ size_t bytes(int64_t V, int parts) {
-    const int64_t all = (V + 2 * kE - 2) / kE;
-    return static_cast<size_t>((all + parts - 1) / parts) * 16;
+  // Pack j; elements that are no entries of the part come as -inf, and a pack
+  // outside it as nothing else.  kLast: it is not read again.
+  template <bool kLast = false>
+  __device__ __forceinline__ uint4 pack(int j) const {
+    uint4 v = make_uint4(Pack<T>::kNegInf, Pack<T>::kNegInf, Pack<T>::kNegInf, Pack<T>::kNegInf);
+    if (j < 0 || j >= packs) return v;
+    if (whole(j)) return kLast ? __ldcs(base + j) : base[j];
+    T* e = reinterpret_cast<T*>(&v);
+#pragma unroll
+    for (int h = 0; h < kE; ++h) {
+      const int i = j * kE + h - off;
+      if (i >= 0 && i < n) e[h] = row[first + i];
+    }
+    return v;
+  }
+  static __device__ __forceinline__ void open(const uint4& w, float* v) {  // kE values
+    const uint32_t in[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int x = 0; x < 4; ++x) Pack<T>::open(in[x], v + x * kPer);
+  }
+  static __device__ __forceinline__ uint32_t max_words(const uint4& w) {
+    return Pack<T>::max2(Pack<T>::max2(w.x, w.y), Pack<T>::max2(w.z, w.w));
+  }
+  static __device__ __forceinline__ float max_of(uint32_t w) {
+    float v[kPer];
+    Pack<T>::open(w, v);
+    float r = v[0];
+#pragma unroll
+    for (int h = 1; h < kPer; ++h) r = fmaxf(r, v[h]);
+    return r;
   }
 };
 
