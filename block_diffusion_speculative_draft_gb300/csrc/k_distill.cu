@@ -71,7 +71,10 @@ __device__ __forceinline__ Entries entries_at(uint8_t* base, int K) {
   return e;
 }
 __host__ __device__ inline size_t entries_bytes(int K) { return (static_cast<size_t>(K) * 16 + 15) & ~size_t(15); }
-size_t bitmap_bytes(int64_t n) { return (static_cast<size_t>((n + 31) / 32) * 4 + 15) & ~size_t(15); }
+// (with room for the packs that a loop's last round passes the part by)
+size_t bitmap_bytes(int64_t n, int slack) {
+  return (static_cast<size_t>((n + 31) / 32) * 4 + slack + 15) & ~size_t(15);
+}
 
 // A reference for exponents whose maximum is m: its own exponent, held within
 // +-kRefMax.  Logits beyond that (the type's lowest value as a mask, infinities
@@ -337,13 +340,14 @@ __device__ __forceinline__ void listed_gradients(const DistillArgs& a, const Sha
   }
 }
 
-constexpr int kFlight = 4;  // packs a thread loads at a time
+constexpr int kFlight = 3;  // packs a thread loads at a time
 
 // The listed elements of pack j become -inf.
 template <typename T>
 __device__ __forceinline__ void mask_listed(const uint32_t* bits, int j, uint4& w) {
   constexpr int kE = Part<T>::kE;
-  const uint32_t m = bits[(j * kE) >> 5] >> ((j * kE) & 31) & ((1u << kE) - 1);
+  const uint32_t byte = reinterpret_cast<const uint8_t*>(bits)[kE == 8 ? j : j >> 1];
+  const uint32_t m = kE == 8 ? byte : byte >> (4 * (j & 1)) & 15;
   if (m == 0) return;
   uint32_t in[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
@@ -369,7 +373,7 @@ __device__ __forceinline__ void write_part(const Part<T>& q, T* dz, F f) {
   const int delta = q.off - phase, back = delta < 0 ? -1 : 0, shift = delta < 0 ? delta + kE : delta;
   const int packs = (phase + q.n + kE - 1) / kE;
   T* dst = out - phase;
-  auto put = [&](int j, const uint32_t* in) {
+  auto put = [&](int j, const uint32_t* in, bool inside) {
     uint32_t o[4];
 #pragma unroll
     for (int w = 0; w < 4; ++w) {
@@ -379,11 +383,11 @@ __device__ __forceinline__ void write_part(const Part<T>& q, T* dz, F f) {
       for (int h = 0; h < kPer; ++h) t[h] = f(t[h]);
       o[w] = Pack<T>::close(t);
     }
-    const int e0 = j * kE - phase;
-    if (e0 >= 0 && e0 + kE <= q.n) {
+    if (inside) {
       __stcs(reinterpret_cast<uint4*>(dst) + j, make_uint4(o[0], o[1], o[2], o[3]));
       return;
     }
+    const int e0 = j * kE - phase;
 #pragma unroll
     for (int h = 0; h < kE; ++h) {
       const uint32_t word = o[h / kPer];
@@ -397,12 +401,21 @@ __device__ __forceinline__ void write_part(const Part<T>& q, T* dz, F f) {
   if (shift == 0) {
     for (int j = threadIdx.x; j < packs; j += kFlight * NT) {
       uint4 v[kFlight];
+      q.template load<kFlight, true>(j, NT, v);
+      if (j + (kFlight - 1) * NT + 1 < packs && (j > 0 || phase == 0)) {
 #pragma unroll
-      for (int x = 0; x < kFlight; ++x) v[x] = q.template pack<true>(j + x * NT);
-#pragma unroll
-      for (int x = 0; x < kFlight; ++x) {
-        const uint32_t in[4] = {v[x].x, v[x].y, v[x].z, v[x].w};
-        if (j + x * NT < packs) put(j + x * NT, in);
+        for (int x = 0; x < kFlight; ++x) {
+          const uint32_t in[4] = {v[x].x, v[x].y, v[x].z, v[x].w};
+          put(j + x * NT, in, true);
+        }
+      } else {
+#pragma unroll 1
+        for (int x = 0; x < kFlight; ++x) {
+          const uint4 y = q.template pack<true>(j + x * NT);
+          const uint32_t in[4] = {y.x, y.y, y.z, y.w};
+          const int e0 = (j + x * NT) * kE - phase;
+          if (j + x * NT < packs) put(j + x * NT, in, e0 >= 0 && e0 + kE <= q.n);
+        }
       }
     }
     return;
@@ -411,10 +424,7 @@ __device__ __forceinline__ void write_part(const Part<T>& q, T* dz, F f) {
   for (int j = threadIdx.x; j < packs; j += 2 * NT) {
     uint4 v[2][2];
 #pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      v[x][0] = q.pack(j + x * NT + back);
-      v[x][1] = q.pack(j + x * NT + back + 1);
-    }
+    for (int x = 0; x < 2; ++x) q.template load<2>(j + x * NT + back, 1, v[x]);
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
       uint32_t in[8] = {v[x][0].x, v[x][0].y, v[x][0].z, v[x][0].w, v[x][1].x, v[x][1].y, v[x][1].z, v[x][1].w};
@@ -430,7 +440,8 @@ __device__ __forceinline__ void write_part(const Part<T>& q, T* dz, F f) {
 #pragma unroll
         for (int w = 0; w < 4; ++w) in[w] = __byte_perm(in[w], in[w + 1], 0x5432);
       }
-      if (j + x * NT < packs) put(j + x * NT, in);
+      const int e0 = (j + x * NT) * kE - phase;
+      if (j + x * NT < packs) put(j + x * NT, in, e0 >= 0 && e0 + kE <= q.n);
     }
   }
 }
@@ -451,11 +462,9 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 5 : 1) distill_kernel(const Di
   q.cut(static_cast<const T*>(a.logits) + row * a.ld, a.V, part, parts);
   pdl_wait();
   uint4 v[kFlight];  // the first packs are on their way while the entries are read
-  if (!kBackward) {
-#pragma unroll
-    for (int x = 0; x < kFlight; ++x) v[x] = q.pack(threadIdx.x + x * NT);
-  }
-  for (int i = threadIdx.x; i < (q.off + q.n + 31) / 32; i += NT) bits[i] = 0;
+  if (!kBackward) q.template load<kFlight>(threadIdx.x, NT, v);
+  constexpr int kSlack = kFlight * NT * kE / 8;  // bytes
+  for (int i = threadIdx.x; i < (q.off + q.n + 31) / 32 + kSlack / 4; i += NT) bits[i] = 0;
   if (threadIdx.x == 0) s.flags = 0;
   const float w = a.weight ? a.weight[row] : 1.f;
   __syncthreads();
@@ -467,8 +476,7 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 5 : 1) distill_kernel(const Di
     float top = -INFINITY, own = -kRefMax, sum = 0.f;
     for (int j = threadIdx.x; j < q.packs; j += kFlight * NT) {
 #pragma unroll
-      for (int x = 0; x < kFlight; ++x)
-        if (j + x * NT < q.packs) mask_listed<T>(bits, j + x * NT, v[x]);
+      for (int x = 0; x < kFlight; ++x) mask_listed<T>(bits, j + x * NT, v[x]);
       uint32_t mx = Part<T>::max_words(v[0]);
 #pragma unroll
       for (int x = 1; x < kFlight; ++x) mx = Pack<T>::max2(mx, Part<T>::max_words(v[x]));
@@ -489,8 +497,7 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 5 : 1) distill_kernel(const Di
           sum += some;
         }
       });
-#pragma unroll
-      for (int x = 0; x < kFlight; ++x) v[x] = q.pack(j + (kFlight + x) * NT);
+      q.template load<kFlight>(j + kFlight * NT, NT, v);
     }
     const float2 ref = part_refs<NW>(a, top, e, s);
     sum *= fast_exp2(own - ref.x);
@@ -520,7 +527,7 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 5 : 1) distill_kernel(const Di
 template <typename T, int NT, bool kBackward>
 cudaError_t launch_kernel(const DistillArgs& a, int64_t rows, int parts, cudaStream_t st) {
   const int64_t most = a.V / parts + 2 * Part<T>::kE;
-  const size_t smem = sizeof(Shared<NT / 32>) + entries_bytes(a.K) + bitmap_bytes(most);
+  const size_t smem = sizeof(Shared<NT / 32>) + entries_bytes(a.K) + bitmap_bytes(most, kFlight * NT * Part<T>::kE / 8);
   const void* kern = (const void*)distill_kernel<T, NT, kBackward>;
   if (smem > 48 * 1024) {
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);

@@ -171,6 +171,18 @@ struct Part {
     }
     return v;
   }
+  // Packs j, j + step, ... into v[kN], with one test where all lie inside.
+  template <int kN, bool kLast = false>
+  __device__ __forceinline__ void load(int j, int step, uint4* v) const {
+    if (j + (kN - 1) * step + 1 < packs && (j > 0 || (j == 0 && !cut_head))) {
+      const uint4* p = base + j;
+#pragma unroll
+      for (int x = 0; x < kN; ++x) v[x] = kLast ? __ldcs(p + x * step) : p[x * step];
+    } else {
+#pragma unroll
+      for (int x = 0; x < kN; ++x) v[x] = pack<kLast>(j + x * step);
+    }
+  }
   static __device__ __forceinline__ void open(const uint4& w, float* v) {  // kE values
     const uint32_t in[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
