@@ -375,14 +375,15 @@ def _on(dev, stream, fn, call, *args):
 
 
 def _workspace(fn, ws, nbytes, dev, stream):
-    """(pointer, bytes, tensor) of the given workspace, or of one in memory that
-    the call's own stream may reuse (stream None: the current one)."""
+    """(pointer, bytes, tensor) of the given workspace, or of a zero-filled one
+    in memory that the call's own stream may reuse (stream None: the current
+    one)."""
     torch = _torch()
     if ws is None:
         if nbytes == 0:
             return None, 0, None
         with torch.cuda.stream(stream):  # None: no change
-            ws = torch.empty(nbytes, dtype=torch.uint8, device=torch.device("cuda", dev))
+            ws = torch.zeros(nbytes, dtype=torch.uint8, device=torch.device("cuda", dev))
     elif ws.get_device() != dev or not ws.is_contiguous():
         raise ValueError(f"{fn}: ws must be contiguous and on cuda:{dev}")
     return ws.data_ptr(), ws.numel() * ws.element_size(), ws
@@ -431,8 +432,8 @@ def dflash_verify_accept_filtered(logits, draft, temperature, u_accept, u_sample
     (fp32/fp16/bf16), draft int32 [b][D] (-1: no draft), temperature, top_p,
     min_p fp32 [b], top_k int32 [b], u_accept fp32 [b][D], u_sample fp32
     [b][V]; n_out, corr_out, next_tok int32 [b], emitted int32 [b][R].  ws:
-    uint8 workspace of dflash_verify_filtered_workspace_size bytes (allocated
-    here when not given)."""
+    zero-filled uint8 workspace of dflash_verify_filtered_workspace_size bytes
+    (allocated here when not given)."""
     fn = "dflash_verify_accept_filtered"
     dt = _row_dtype(fn, logits)
     ld = _row_shape(fn, logits, 3)

@@ -544,7 +544,7 @@ int32_t dflash_sample(const void* logits, int32_t dtype, int64_t rows, int64_t V
 
 int32_t dflash_verify_filtered_workspace_size(int32_t b, int32_t R, int64_t V, size_t* bytes) {
   if (!bytes || b < 1 || R < 1 || R > 64 || V < 1) return DFLASH_EINVAL;
-  *bytes = (size_t)b * R * sizeof(RowCut);
+  *bytes = accept_ws_bytes(b, R);
   return DFLASH_OK;
 }
 
@@ -557,7 +557,7 @@ int32_t dflash_verify_accept_filtered(const void* logits, int32_t dtype, int64_t
   if (b < 1 || R < 1 || R > 64 || D < 1 || D > R) return DFLASH_EINVAL;
   if (int r = check_rows(logits, dtype, (int64_t)b * R, V, ld)) return r;
   if (!draft || !temperature || !u_accept || !u_sample || !n_out || !corr_out || ld_u < V) return DFLASH_EINVAL;
-  if (!ws || ws_bytes < (size_t)b * R * sizeof(RowCut) || !aligned16(ws)) return DFLASH_EWORKSPACE;
+  if (!ws || ws_bytes < accept_ws_bytes(b, R) || !aligned16(ws)) return DFLASH_EWORKSPACE;
   FilterArgs a;
   memset(&a, 0, sizeof(a));
   a.logits = logits;
@@ -574,6 +574,7 @@ int32_t dflash_verify_accept_filtered(const void* logits, int32_t dtype, int64_t
   a.draft = draft;
   a.u_accept = u_accept;
   a.cuts = static_cast<RowCut*>(ws);
+  a.tickets = reinterpret_cast<int*>(static_cast<uint8_t*>(ws) + accept_cuts_bytes(b, R));
   a.n_out = n_out;
   a.corr_out = corr_out;
   a.emitted = emitted_out;

@@ -1682,9 +1682,43 @@ __device__ __forceinline__ int accepts(const FilterArgs& a, const Row<T, kThr>& 
              static_cast<double>(r.weight(z));
 }
 
+// A sequence's outputs from its rows (one warp): leading accepts, and the token
+// drawn at the row after them, or `drawn` where that is still to be drawn.
+__device__ __forceinline__ int leading_accepts(const FilterArgs& a, int64_t j) {
+  const int lane = threadIdx.x & 31;
+  for (int base = 0; base < a.D; base += 32) {
+    const int i = base + lane;
+    const bool ok = i < a.D && __ldcg(&a.cuts[j * a.R + i].accept);
+    const uint32_t no = ~__ballot_sync(0xffffffffu, ok);
+    if (no) {
+      const int n = base + __ffs(no) - 1;
+      return n < a.D ? n : a.D;
+    }
+  }
+  return a.D;
+}
+__device__ __forceinline__ void write_sequence(const FilterArgs& a, int64_t j, int n, int corr, bool ok) {
+  const int lane = threadIdx.x & 31;
+  const int* dr = a.draft + j * a.D;
+  if (!ok) {
+    n = -1;  // a commit of this length appends nothing
+    corr = -1;
+  }
+  if (lane == 0) {
+    if (!ok) atomicOr(a.status, kDevBadParam);
+    a.n_out[j] = n;
+    a.corr_out[j] = corr;
+    if (a.next_tok) a.next_tok[j] = corr >= 0 ? corr : (n > 0 ? dr[n - 1] : -1);
+  }
+  if (a.emitted)
+    for (int i = lane; i < a.R; i += 32) a.emitted[j * a.R + i] = i < n ? dr[i] : (i == n ? corr : -1);
+}
+
 // Verified row rr of sequence j: whether its draft is accepted, and the token
-// drawn here if it is not (or if rr = D).  A row without a short list leaves
-// the draw, which few rows need, to the last kernel.
+// drawn here if it is not (or if rr = D).  The CTA that finishes a sequence's
+// last row (a ticket) writes the outputs.  With a.defer, rows without a short
+// list are left to two more launches: their cuts, then the one draw that a
+// sequence needs and its outputs.
 template <typename T>
 __global__ void __launch_bounds__(kThr, 4) accept_rows_kernel(const FilterArgs a) {
   extern __shared__ __align__(16) uint8_t raw[];
@@ -1706,22 +1740,49 @@ __global__ void __launch_bounds__(kThr, 4) accept_rows_kernel(const FilterArgs a
   RowCut out{~0ull, r.m, 0, -1, 0, row_mass, 0};
   if (q.ok && some) {
     const int drop = rr < a.D ? a.draft[j * a.D + rr] : -1;
+    const float* u = a.u + j * a.ld_u;
+    const bool unfiltered = want_mass && q.p >= 1.f;
     Verdict v{0, 0, -1, 0.f};
-    if (listed_row(r, s, sc, a, q, low, row_mass, a.u + j * a.ld_u, drop, &v)) {
-      if (r.rank != 0) return;
+    const bool listed = listed_row(r, s, sc, a, q, low, row_mass, u, drop, &v);
+    if (listed && r.rank != 0) return;
+    if (listed) {
       out.tok = v.tok;
     } else {
       out.tok = kDeferred;
-      if (a.defer && !(want_mass && q.p >= 1.f)) {
+      if (a.defer && !unfiltered)
         out.left = 1;
-      } else {
+      else
         wide_row(r, s, a, q, row_mass, static_cast<const float*>(nullptr), &v);
-      }
     }
     out.cut = v.cut;
     if (r.rank == 0 && threadIdx.x == 0 && !out.left) out.accept = accepts(a, r, j, rr, v.cut, v.mass);
+    if (!listed && !a.defer) {  // a wide row draws where it has to
+      if (r.rank == 0 && threadIdx.x == 0) {
+        for (uint32_t o = 0; o < size; ++o) {
+          uint64_t* p = peer(s.pick, o);
+          p[0] = out.cut;
+          p[1] = static_cast<uint64_t>(out.accept);
+        }
+      }
+      cluster_sync_all(size);
+      if (s.pick[1] == 0) out.tok = pick_row(r, s, u, s.pick[0], drop, q.T);
+    }
   }
-  if (r.rank == 0 && threadIdx.x == 0) a.cuts[row] = out;
+  if (r.rank != 0) return;
+  if (threadIdx.x == 0) {
+    a.cuts[row] = out;
+    s.taken = 0;
+    if (!a.defer) {
+      __threadfence();
+      s.taken = atomicAdd(&a.tickets[j], 1) == a.rows_used - 1;
+    }
+  }
+  __syncthreads();
+  if (!s.taken || threadIdx.x >= 32) return;
+  __threadfence();
+  if (threadIdx.x == 0) a.tickets[j] = 0;
+  const int n = leading_accepts(a, j);
+  write_sequence(a, j, n, n < a.R ? __ldcg(&a.cuts[j * a.R + n].tok) : -1, q.ok);
 }
 
 template <typename T>
@@ -1751,20 +1812,16 @@ __global__ void __launch_bounds__(kThr, 4) accept_wide_kernel(const FilterArgs a
       });
 }
 
-// One cluster per sequence: leading accepts, the draw at the row after them if
-// it is still to be made, and the outputs.
+// One cluster per sequence, after rows that were left to a second launch.
 template <typename T>
 __global__ void __launch_bounds__(kThr) accept_pick_kernel(const FilterArgs a) {
   extern __shared__ __align__(16) uint8_t raw[];
-  using S = Shared<kThr, kShortCap>;
-  S& s = *reinterpret_cast<S*>(raw);
+  Short& s = *reinterpret_cast<Short*>(raw);
   pdl_wait();
-  const int64_t j = blockIdx.x / cluster_size();
-  const uint32_t rank = cluster_rank(), size = cluster_size();
+  const uint32_t size = cluster_size();
+  const int64_t j = blockIdx.x / size;
   const Ask q = read_ask(a, j);
-  int n = 0;
-  while (n < a.D && a.cuts[j * a.R + n].accept) ++n;
-  const int* dr = a.draft + j * a.D;
+  const int n = leading_accepts(a, j);
   int corr = -1;
   if (q.ok && n < a.R) {
     const int64_t row = j * a.R + n;
@@ -1776,20 +1833,10 @@ __global__ void __launch_bounds__(kThr) accept_pick_kernel(const FilterArgs a) {
       r.open(a, row);
       r.m = c.m;
       cluster_sync_all(size);
-      corr = pick_row(r, s, a.u + j * a.ld_u, c.cut, n < a.D ? dr[n] : -1, q.T);
+      corr = pick_row(r, s, a.u + j * a.ld_u, c.cut, n < a.D ? a.draft[j * a.D + n] : -1, q.T);
     }
   }
-  if (rank == 0 && threadIdx.x == 0) {
-    if (!q.ok) {
-      n = -1;  // a commit of this length appends nothing
-      atomicOr(a.status, kDevBadParam);
-    }
-    a.n_out[j] = n;
-    a.corr_out[j] = corr;
-    if (a.next_tok) a.next_tok[j] = corr >= 0 ? corr : (n > 0 ? dr[n - 1] : -1);
-    if (a.emitted)
-      for (int i = 0; i < a.R; ++i) a.emitted[j * a.R + i] = i < n ? dr[i] : (i == n ? corr : -1);
-  }
+  if (cluster_rank() == 0 && threadIdx.x < 32) write_sequence(a, j, n, corr, q.ok);
 }
 
 constexpr int kTopCap = 2048;
@@ -1872,7 +1919,7 @@ int pick_parts(int64_t V, int64_t rows, size_t esize) {
 // Whether wide rows are left to a second launch: worth it where the first gives
 // a row few CTAs.
 bool defers(int64_t V, int64_t rows, size_t esize, int parts) {
-  return rows > kInlineRows && parts < kMaxCluster && V * (int64_t)esize / parts > 64 * 1024;
+  return rows > kInlineRows && parts < kMaxCluster && V * (int64_t)esize / parts > 80 * 1024;
 }
 
 // The second launch: clusters that fill the GPU share out the rows, of eight
@@ -1902,8 +1949,8 @@ cudaError_t launch_accept(FilterArgs a, int64_t b, cudaStream_t st) {
   a.defer = defers(a.V, rows, sizeof(T), parts);
   cudaError_t e = launch_rows((const void*)accept_rows_kernel<T>, rows, parts, sizeof(Short), a, st);
   if (e != cudaSuccess) return e;
-  if (a.defer && (e = launch_wide((const void*)accept_wide_kernel<T>, rows, sizeof(Short), a, st)) != cudaSuccess)
-    return e;
+  if (!a.defer) return cudaSuccess;
+  if ((e = launch_wide((const void*)accept_wide_kernel<T>, rows, sizeof(Short), a, st)) != cudaSuccess) return e;
   return launch_rows((const void*)accept_pick_kernel<T>, b, pick_parts(a.V, b, sizeof(T)), sizeof(Short), a, st);
 }
 template <typename T>

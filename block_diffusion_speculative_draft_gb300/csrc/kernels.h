@@ -243,6 +243,7 @@ struct FilterArgs {
   const int* draft;
   const float* u_accept;
   RowCut* cuts;
+  int* tickets;    // [b], zero between calls
   int* n_out;
   int* corr_out;
   int* emitted;
@@ -258,6 +259,8 @@ struct FilterArgs {
   int defer;       // rows without a short list are left to a second launch
 };
 cudaError_t filter_sample(FilterArgs a, int dtype, int64_t rows, cudaStream_t st);
+inline size_t accept_cuts_bytes(int64_t b, int R) { return (size_t)b * R * sizeof(RowCut); }
+inline size_t accept_ws_bytes(int64_t b, int R) { return accept_cuts_bytes(b, R) + (size_t)b * sizeof(int); }
 cudaError_t filter_accept(FilterArgs a, int dtype, int64_t b, cudaStream_t st);
 cudaError_t top_logits(FilterArgs a, int dtype, int64_t rows, cudaStream_t st);
 

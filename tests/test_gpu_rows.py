@@ -586,7 +586,7 @@ def test_other_stream_graph_and_early_launch_repeat():
              dz2=torch.zeros((n, V), dtype=torch.bfloat16, device=DEV))
     student = _padded(_logits(rng, n, V, "flat"), "bf16", 0)
     ones = torch.ones(n, device=DEV)
-    ws = torch.empty(api.dflash_verify_filtered_workspace_size(3, 4, V), dtype=torch.uint8, device=DEV)
+    ws = torch.zeros(api.dflash_verify_filtered_workspace_size(3, 4, V), dtype=torch.uint8, device=DEV)
 
     def everything(stream=None):
         api.dflash_sample(zt, T, u, o["tok"], top_k=k, top_p=p, min_p=mp, logprob_out=o["lp"], stream=stream)
