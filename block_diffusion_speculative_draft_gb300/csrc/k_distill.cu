@@ -33,11 +33,12 @@ constexpr int kDevBadToken = 0x2;
 constexpr float kMassOne = 1099511627776.f;  // 2^40: probabilities are summed as integers
 constexpr float kLn2 = 0.6931471805599453f;
 
-// What a part of a row contributes: the entries outside S (reference and sum of
-// 2^(x - reference)), those listed in it (the same, sum p_k (ln p_k - ln 2 (x_k -
-// reference)) and sum p_k), and whether it refuses the row.
+// What a part of a row contributes: the entries outside S (maximum and sum of
+// 2^((z - maximum) c)), those listed in it (the same, sum p_k (ln p_k - (z_k -
+// maximum) / T) and sum p_k), and whether it refuses the row.  Without an entry
+// above -inf the maximum is -inf and the sum 0.
 struct PartSums {
-  float ref, sum, lref, lsum, self, p;
+  float top, sum, ltop, lsum, self, p;
   int bad;
 };
 
@@ -50,7 +51,7 @@ struct alignas(16) Shared {
   uint64_t mass[NW];
   PartSums part[kMaxCluster];
   struct {
-    float f, ref, g, in, m;  // factor and reference outside S, weight / T, P / E and reference in S
+    float f, mr, g, in, m;  // factor and maximum outside S, weight / T, P / E and the row's maximum
     int zero;                // no gradient
   } plan;
   int flags;  // 1: refused, 2: an entry above -inf
@@ -76,27 +77,19 @@ size_t bitmap_bytes(int64_t n, int slack) {
   return (static_cast<size_t>((n + 31) / 32) * 4 + slack + 15) & ~size_t(15);
 }
 
-// A reference for exponents whose maximum is m: its own exponent, held within
-// +-kRefMax.  Logits beyond that (the type's lowest value as a mask, infinities
-// aside from -inf) count as the bound, so that rows of nothing else still have
-// a distribution.
-__device__ __forceinline__ float ref_of(float m, float c) {
-  const float r = m * c;
-  return r > kRefMax ? kRefMax : (r > -kRefMax ? r : -kRefMax);
-}
-__device__ __forceinline__ float exponent(float v, float c, float ref) {
-  const float r = v * c;
-  if (fabsf(r) < kRefMax || !(v > -INFINITY)) return fmaf(v, c, -ref);  // -inf and NaN stay
-  return (r > 0.f ? kRefMax : -kRefMax) - ref;
-}
-// Calls f(weight) with weight(v) = 2^(exponent of v): the bare form where the
-// reference, and so every entry below it, is inside the bound.
+// Sums of 2^(v c) are kept relative to a maximum m of theirs.  In a pass over
+// the entries the exponent is fma(v, c, -ref) with ref = m c rounded, while that
+// rounding is small (is_near); lead() tells how far it is off.  Past that (the
+// type's lowest value as a mask, say) it is (v - m) c.
+__device__ __forceinline__ bool is_near(float ref) { return fabsf(ref) < kRefMax; }
+__device__ __forceinline__ float lead(float m, float c) { return is_near(m * c) ? fmaf(-m, c, m * c) : 0.f; }
+// Calls f(weight) with weight(v) = 2^(exponent of v) in the form that m asks for.
 template <typename F>
-__device__ __forceinline__ void with_weight(float c, float ref, F f) {
-  if (fabsf(ref) < kRefMax) {
+__device__ __forceinline__ void with_weight(float c, float ref, float m, F f) {
+  if (is_near(ref)) {
     f([=](float v) { return fast_exp2(fmaf(v, c, -ref)); });
   } else {
-    f([=](float v) { return fast_exp2(exponent(v, c, ref)); });
+    f([=](float v) { return fast_exp2(log2_weight(v, m, c)); });
   }
 }
 
@@ -134,7 +127,7 @@ __device__ __forceinline__ Teacher read_teacher(const DistillArgs& a, int64_t ro
   const int used = a.K < NT ? (a.K + 31) / 32 : NW;
   bool bad = false;
   float tm = -INFINITY;
-  Pair lt{a.t_lse ? a.t_lse[row] : 0.f, 0.f};
+  float lt = a.t_lse ? a.t_lse[row] : 0.f;
   for (int k = threadIdx.x; k < a.K; k += NT) {
     const int i = a.t_idx[row * a.K + k];
     const float v = a.t_val[row * a.K + k];
@@ -168,20 +161,19 @@ __device__ __forceinline__ Teacher read_teacher(const DistillArgs& a, int64_t ro
     __syncthreads();
     sp = 0.f;
     for (int w = 0; w < used; ++w) sp += s.warp[w].x;
-    lt = over_t(a, tm);
-    const Pair sum = two_sum(lt.hi, logf(sp));
-    lt = Pair{sum.hi, sum.lo + lt.lo};
+    lt = logf(sp);
   }
   // ln p_k = t_k / T - Lt, to twice a float's digits: where t_lse is given, p_r is
   // a difference from one.  The probabilities' sum is an integer sum for the
-  // same reason.
+  // same reason.  Without t_lse both are taken relative to the largest t_k.
+  const float base = a.t_lse ? 0.f : tm;
   uint64_t fixed = 0;
   for (int k = threadIdx.x; k < a.K; k += NT) {
     const float v = e.lp[k];
-    const Pair x = over_t(a, v), d = two_sum(x.hi, -lt.hi);
+    const Pair y = two_sum(v, -base), x = over_t(a, y.hi), d = two_sum(x.hi, -lt);
     const float hi = v > -INFINITY ? d.hi : v;
     float p = expf(hi);
-    if (hi > -INFINITY) p = fmaf(p, d.lo + (x.lo - lt.lo), p);
+    if (hi > -INFINITY) p = fmaf(p, d.lo + fmaf(y.lo, a.inv_hi, x.lo), p);
     e.lp[k] = hi;
     e.p[k] = p;
     fixed += __float2ull_rn(fminf(p, 256.f) * kMassOne);
@@ -206,12 +198,12 @@ __device__ __forceinline__ Teacher read_teacher(const DistillArgs& a, int64_t ro
   return t;
 }
 
-// The references of a part: of its entries outside S, whose maximum over this
+// The maxima of a part: of its entries outside S, whose maximum over this
 // thread's is `top`, and of its listed ones.
 template <int NW>
-__device__ __forceinline__ float2 part_refs(const DistillArgs& a, float top, Entries e, Shared<NW>& s) {
+__device__ __forceinline__ float2 part_tops(int K, float top, Entries e, Shared<NW>& s) {
   float l = -INFINITY;
-  for (int k = threadIdx.x; k < a.K; k += NW * 32)
+  for (int k = threadIdx.x; k < K; k += NW * 32)
     if (e.at[k] >= 0) l = fmaxf(l, e.z[k]);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
@@ -226,19 +218,20 @@ __device__ __forceinline__ float2 part_refs(const DistillArgs& a, float top, Ent
     top = fmaxf(top, v.x);
     l = fmaxf(l, v.y);
   }
-  return make_float2(ref_of(top, a.c), ref_of(l, a.c));
+  return make_float2(top, l);
 }
 
 // Adds up a part (`sum`: this thread's outside S) and sends it to every CTA of
 // the cluster; complete after a cluster barrier.
 template <int NW>
-__device__ __forceinline__ void send_part(const DistillArgs& a, float2 ref, float sum, bool bad, Entries e,
+__device__ __forceinline__ void send_part(const DistillArgs& a, float2 tops, float sum, bool bad, Entries e,
                                           Shared<NW>& s, int part, int parts) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   float4 v = make_float4(sum, 0.f, 0.f, 0.f);  // sum, lsum, self, p
   for (int k = threadIdx.x; k < a.K; k += NW * 32) {
     if (e.at[k] < 0) continue;
-    const float x = exponent(e.z[k], a.c, ref.y), p = e.p[k];
+    const float z = e.z[k], p = e.p[k];
+    const float x = z == -INFINITY ? z : log2_weight(z, tops.y, a.c);
     v.y += exp2f(x);
     if (p > 0.f) v.z += p * (e.lp[k] - x * kLn2);
     v.w += p;
@@ -264,49 +257,48 @@ __device__ __forceinline__ void send_part(const DistillArgs& a, float2 ref, floa
       v.z += __shfl_xor_sync(0xffffffffu, v.z, o);
       v.w += __shfl_xor_sync(0xffffffffu, v.w, o);
     }
-    if (lane < parts) *peer(&s.part[part], lane) = PartSums{ref.x, v.x, ref.y, v.y, v.z, v.w, bad};
+    if (lane < parts) *peer(&s.part[part], lane) = PartSums{tops.x, v.x, tops.y, v.y, v.z, v.w, bad};
   }
 }
 
-// What the row's gradient needs: reference and sum of 2^(x - reference) over
-// the row (m, E) and outside S (mr, Er).  E = 0 stands for a row without a
-// gradient.
+// What the row's gradient needs: maximum and sum of 2^((z - maximum) c) over the
+// row (m, E) and outside S (mr, Er).  E = 0 stands for a row without a gradient.
 struct RowSums {
   float m, E, mr, Er;
 };
 
 // What the gradient pass needs of a row, worked out once per CTA.
 template <int NW>
-__device__ __forceinline__ void make_plan(Shared<NW>& s, const RowSums& r, const Teacher& t, float w, float inv_t) {
-  const float g = w * inv_t;
+__device__ __forceinline__ void make_plan(const DistillArgs& a, Shared<NW>& s, const RowSums& r, const Teacher& t, float w) {
+  const float g = w * a.inv_hi;
   s.plan.zero = r.E == 0.f;
   s.plan.g = g;
-  s.plan.ref = r.mr;
+  s.plan.mr = r.mr;
   s.plan.m = r.m;
   s.plan.in = t.P / r.E;
-  // factor of 2^(x_j - mr) outside S
-  s.plan.f = r.Er > 0.f ? g * (t.P * exp2f(r.mr - r.m) / r.E - t.pr / r.Er) : 0.f;
+  // factor of the weights outside S, in the form of with_weight
+  const float f = r.Er > 0.f ? g * (t.P * exp2f(log2_weight(r.mr, r.m, a.c)) / r.E - t.pr / r.Er) : 0.f;
+  s.plan.f = f * exp2f(lead(r.mr, a.c));
 }
 
 // Joins the parts, in rank order, makes the plan and, in the row's first CTA,
-// writes the loss (the first warp).  A part without a finite logit has the
-// lowest reference and no sum.
+// writes the loss (the first warp).
 template <int NW>
 __device__ __forceinline__ void join_parts(const DistillArgs& a, int64_t row, const Teacher& t, float w,
                                            Shared<NW>& s, int part, int parts) {
   const int lane = threadIdx.x & 31;
-  const PartSums q = lane < parts ? s.part[lane] : PartSums{-kRefMax, 0.f, -kRefMax, 0.f, 0.f, 0.f, 0};
+  const PartSums q = lane < parts ? s.part[lane] : PartSums{-INFINITY, 0.f, -INFINITY, 0.f, 0.f, 0.f, 0};
   const bool bad = __any_sync(0xffffffffu, q.bad != 0);
   RowSums r;
-  r.mr = q.ref;
-  r.m = fmaxf(q.sum > 0.f ? q.ref : -kRefMax, q.lsum > 0.f ? q.lref : -kRefMax);
+  r.mr = q.top;
+  r.m = fmaxf(q.top, q.ltop);
 #pragma unroll
   for (int o = kMaxCluster / 2; o > 0; o >>= 1) {
     r.mr = fmaxf(r.mr, __shfl_xor_sync(0xffffffffu, r.mr, o));
     r.m = fmaxf(r.m, __shfl_xor_sync(0xffffffffu, r.m, o));
   }
-  r.Er = q.sum * exp2f(q.ref - r.mr);
-  r.E = q.sum * exp2f(q.ref - r.m) + q.lsum * exp2f(q.lref - r.m);
+  r.Er = q.sum * exp2f(log2_weight(q.top, r.mr, a.c));
+  r.E = q.sum * exp2f(log2_weight(q.top, r.m, a.c)) + q.lsum * exp2f(log2_weight(q.ltop, r.m, a.c));
 #pragma unroll
   for (int o = kMaxCluster / 2; o > 0; o >>= 1) {
     r.Er += __shfl_xor_sync(0xffffffffu, r.Er, o);
@@ -314,20 +306,20 @@ __device__ __forceinline__ void join_parts(const DistillArgs& a, int64_t row, co
   }
   if (r.E == 0.f) r.E = NAN;  // a row without any finite logit has no distribution
   const float log_e = log2f(r.E);
-  // sum p (ln p - ln q), ln q = ln 2 (x - m - log2 E)
-  float l = q.p > 0.f ? q.self + q.p * (log_e + (r.m - q.lref)) * kLn2 : 0.f;
+  // sum p (ln p - ln q), ln q = (z - m) / T - ln E
+  float l = q.p > 0.f ? q.self + q.p * (log_e - log2_weight(q.ltop, r.m, a.c)) * kLn2 : 0.f;
 #pragma unroll
   for (int o = kMaxCluster / 2; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
   if (lane != 0) return;
   const bool out = bad || w == 0.f || !t.some;
   if (part == 0) {
-    if (t.pr > 0.f) l += t.pr * (logf(t.pr) - (log2f(r.Er) + (r.mr - r.m) - log_e) * kLn2);
+    if (t.pr > 0.f) l += t.pr * (logf(t.pr) - (log2f(r.Er) + log2_weight(r.mr, r.m, a.c) - log_e) * kLn2);
     a.loss[row] = out ? (bad ? NAN : 0.f) : w * l;
     if (a.stats) a.stats[row] = out ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(r.m, r.E, r.mr, r.Er);
     if (bad) atomicOr(a.status, kDevBadToken);
   }
   if (out) r.E = 0.f;
-  make_plan(s, r, t, w, a.inv_hi);
+  make_plan(a, s, r, t, w);
 }
 
 // Gradients of the part's listed entries; out: its first entry's.
@@ -336,7 +328,7 @@ __device__ __forceinline__ void listed_gradients(const DistillArgs& a, const Sha
   const float f = s.plan.in, g = s.plan.g, m = s.plan.m;
   for (int k = threadIdx.x; k < a.K; k += NT) {
     const int i = e.at[k];
-    if (i >= 0) out[i] = from_f32<T>(g * (f * exp2f(exponent(e.z[k], a.c, m)) - e.p[k]));
+    if (i >= 0) out[i] = from_f32<T>(g * (f * exp2f(log2_weight(e.z[k], m, a.c)) - e.p[k]));
   }
 }
 
@@ -471,9 +463,9 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 5 : 1) distill_kernel(const Di
   if (!kBackward && parts > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
   const Teacher t = read_teacher<T, NT>(a, row, q, e, bits, s);
   if (!kBackward) {
-    // the sum relative to a reference that follows this thread's maximum, then
-    // brought to the part's
-    float top = -INFINITY, own = -kRefMax, sum = 0.f;
+    // the sum relative to this thread's maximum, which it follows, then to the
+    // part's
+    float top = -INFINITY, ref = 0.f, sum = 0.f;
     for (int j = threadIdx.x; j < q.packs; j += kFlight * NT) {
 #pragma unroll
       for (int x = 0; x < kFlight; ++x) mask_listed<T>(bits, j + x * NT, v[x]);
@@ -482,12 +474,15 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 5 : 1) distill_kernel(const Di
       for (int x = 1; x < kFlight; ++x) mx = Pack<T>::max2(mx, Part<T>::max_words(v[x]));
       const float m = Part<T>::max_of(mx);
       if (m > top) {
-        const float ref = ref_of(m, a.c);
-        sum *= fast_exp2(own - ref);
-        own = ref;
+        const float next = m * a.c;
+        if (top > -INFINITY)
+          sum *= fast_exp2(is_near(ref) && is_near(next)
+                               ? ref - next
+                               : log2_weight(top, m, a.c) + (lead(top, a.c) - lead(m, a.c)));
+        ref = next;
         top = m;
       }
-      with_weight(a.c, own, [&](auto weight) {
+      with_weight(a.c, ref, top, [&](auto weight) {
 #pragma unroll
         for (int x = 0; x < kFlight; ++x) {
           float z[kE], some = 0.f;
@@ -499,17 +494,17 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 5 : 1) distill_kernel(const Di
       });
       q.template load<kFlight>(j + kFlight * NT, NT, v);
     }
-    const float2 ref = part_refs<NW>(a, top, e, s);
-    sum *= fast_exp2(own - ref.x);
+    const float2 tops = part_tops<NW>(a.K, top, e, s);
+    if (top > -INFINITY) sum *= fast_exp2(log2_weight(top, tops.x, a.c) + lead(top, a.c));
     if (parts > 1) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");  // the other CTAs have started
-    send_part<NW>(a, ref, sum, t.bad, e, s, part, parts);
+    send_part<NW>(a, tops, sum, t.bad, e, s, part, parts);
     cluster_sync_all(parts);
     if (threadIdx.x < 32) join_parts<NW>(a, row, t, w, s, part, parts);
     if (!dz) return;
   } else if (threadIdx.x == 0) {
     if (t.bad) atomicOr(a.status, kDevBadToken);
     const float4 st = a.stats[row];
-    make_plan(s, RowSums{st.x, t.bad || w == 0.f ? 0.f : st.y, st.z, st.w}, t, w, a.inv_hi);
+    make_plan(a, s, RowSums{st.x, t.bad || w == 0.f ? 0.f : st.y, st.z, st.w}, t, w);
   }
   __syncthreads();
   if (s.plan.zero) {  // left out or refused
@@ -517,7 +512,7 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 5 : 1) distill_kernel(const Di
     return;
   }
   const float f = s.plan.f;
-  with_weight(a.c, s.plan.ref, [&](auto weight) {
+  with_weight(a.c, s.plan.mr * a.c, s.plan.mr, [&](auto weight) {
     write_part<T, NT>(q, dz, [=](float z) { return f * weight(z); });
   });
   __syncthreads();

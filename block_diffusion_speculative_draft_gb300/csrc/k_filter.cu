@@ -13,11 +13,22 @@
 // place is at or above the cut.  The token is the Gumbel maximum
 // argmax (z_v - max z)/T - log(-log u_v) over the kept entries.
 //
-// Weights are summed as 64-bit integers (w scaled by a power of two that
-// keeps V of them below 2^62): the sums do not depend on the order of the
-// additions, so the cut and every result repeat bit for bit; the rounding of
-// one weight, 2^-45 of the largest at V = 152 k, is far below the 2^-23 of
-// its exponential.
+// A row is one cluster's: one pass from HBM takes the row's maximum, the maxima
+// of its groups of entries and, where top-p refers to the whole row, its sum of
+// weights.  Rows whose answer is among a few hundred entries (top-k, a peaked
+// top-p, min-p) list the entries above a bound read off the groups' maxima, and
+// rank 0 settles them.  Others take a histogram of the weights and one more pass
+// (deep top-p), one more pass (min-p), the scan's own draw (no filter), or, for
+// what none of these can hold (top-k above 1024, thousands of equal values), radix
+// descents over the places.  All passes after the first read from L2.
+//
+// Sums that decide which entries are kept are of integers wherever their order
+// is not fixed (w scaled by a power of two that keeps V of them below 2^62; the
+// rounding of one weight, 2^-45 of the largest at V = 152 k, is far below the
+// 2^-23 of its exponential), and floats in a fixed order elsewhere, so every
+// result repeats bit for bit.
+//
+// FIGURES
 #include "kernels.h"
 #include "rows.cuh"
 
@@ -32,6 +43,8 @@ constexpr int kGroupBins = 256;       // bins of the groups' maxima
 constexpr int kLineBins = 1024;       // bins of the weights, linear in the logit
 constexpr int kDevBadParam = 0x8;
 constexpr int kFewTarget = 96;        // entries the short list aims at where top-k does not say
+constexpr int kShareRows = 2048;      // rows looked through at a time by a second launch
+constexpr int kShareMost = 64;        // of which a cluster takes at most so many
 constexpr int kQuick = 128;           // lists up to this length are ranked, longer ones sorted
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -75,7 +88,8 @@ struct alignas(16) Shared {
   uint64_t list_mass[kMaxCluster];   // what each CTA put on the list, by weight and by count
   uint32_t list_count[kMaxCluster];
   uint32_t highest[kMaxCluster], lowest[kMaxCluster];  // of each CTA's groups' maxima
-  float mass[kMaxCluster];           // each CTA's sum of weights
+  float mass[kMaxCluster];           // each CTA's sum of weights, from the scan
+  float sums[kMaxCluster];           // and from a pass over the entries kept
   uint64_t own_mass;
   uint64_t need;                     // top-p keeps entries while the sum before them is below this
   float bound;                       // min-p's bound on a logit
@@ -95,7 +109,7 @@ struct alignas(16) Shared {
   uint64_t join[NT / 32][3];
   float val;
   uint32_t bar;                      // key of the best score seen by any thread of the CTA
-  int64_t rows[64];                  // a cluster's rows of a second launch
+  int64_t rows[kShareMost];          // a cluster's rows of a second launch
 };
 
 // One row as a cluster sees it.  Each CTA reads its part of the row from
@@ -604,7 +618,7 @@ __device__ __forceinline__ void list_entries(const Row<T, NT>& r, Shared<NT, kCa
   uint32_t* taken = peer(&s.taken, 0);
   uint64_t* list = peer(s.list, 0);
   const uint32_t deep = (r.part.packs + kGroups * NT - 1) / (kGroups * NT), units = s.queued * deep;
-  float listed = 0.f;
+  uint64_t listed = 0;  // as integers: which thread takes which pack is not fixed
   for (uint32_t y0 = threadIdx.x; y0 < units; y0 += 4 * NT) {
     uint4 w[4];
     int at[4];
@@ -631,12 +645,11 @@ __device__ __forceinline__ void list_entries(const Row<T, NT>& r, Shared<NT, kCa
         const float z = Row<T, NT>::pick_of(w[x], h);
         if (base < kCap) list[base] = place_of(value_key(z), static_cast<uint32_t>(i + h));
         ++base;
-        listed += fast_exp2(r.log2w(z));
+        if (want_mass) listed += r.weight(z);
       }
     }
   }
-  if (want_mass && listed > 0.f)
-    atomicAdd(reinterpret_cast<unsigned long long*>(&s.own_mass), __float2ull_rn(listed * r.scale));
+  if (listed > 0) atomicAdd(reinterpret_cast<unsigned long long*>(&s.own_mass), static_cast<unsigned long long>(listed));
 }
 
 // Sum of the CTAs' own counts and masses; complete lists are seen after it.
@@ -1051,11 +1064,11 @@ __device__ __forceinline__ float cluster_mass(Row<T, NT>& r, Shared<NT, kCap>& s
     float d = 0.f;
 #pragma unroll
     for (int x = 0; x < NT / 32; ++x) d += __uint_as_float(static_cast<uint32_t>(s.warp_sum[x]));
-    *peer(&s.mass[r.rank], threadIdx.x) = d;
+    *peer(&s.sums[r.rank], threadIdx.x) = d;
   }
   cluster_sync_all(r.size);
   float d = 0.f;
-  for (uint32_t o = 0; o < r.size; ++o) d += s.mass[o];
+  for (uint32_t o = 0; o < r.size; ++o) d += s.sums[o];
   return d;
 }
 
@@ -1605,7 +1618,7 @@ __global__ void __launch_bounds__(kThr, 4) sample_rows_kernel(const FilterArgs a
 // left(row) tells: the id-th such row, and every `clusters`-th after it.
 template <typename L, typename F>
 __device__ __forceinline__ void share_rows(Short& s, int64_t rows, uint32_t id, uint32_t clusters, L left, F visit) {
-  constexpr int kEach = 8;
+  constexpr int kEach = kShareRows / kThr;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int64_t carry = 0;
   for (int64_t base = 0; base < rows; base += kThr * kEach) {
@@ -1930,6 +1943,7 @@ cudaError_t launch_wide(const void* kern, int64_t rows, size_t smem, const Filte
   void* args[] = {&b, &rows};
   const int parts = rows > 2 * num_sms() ? 4 : 8;
   int64_t clusters = 4 * num_sms() / parts;
+  if (clusters < kShareRows / kShareMost) clusters = kShareRows / kShareMost;
   if (clusters > rows) clusters = rows;
   return launch_kc(kern, dim3((unsigned)(clusters * parts)), dim3(kThr), smem, st, true, dim3(parts), args);
 }

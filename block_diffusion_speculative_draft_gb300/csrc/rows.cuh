@@ -55,15 +55,16 @@ __device__ __forceinline__ uint64_t double_key(double v) {
   return (b >> 63) ? ~b : (b | 0x8000000000000000ull);
 }
 
-// log2(e) / T.  Exponents are formed in units of log2: x = fma(z, c, -ref) with
-// ref a float near c times a maximum.  The fused product is exact, so x carries
-// one rounding of its own size, c's rounding counts as a temperature 2^-24
-// off, and ref is a known number, not a rounded one, wherever sums with
-// different references meet.
+// log2(e) / T.  Passes over a row form exponents of 2 as x = fma(z, c, -ref) with
+// ref = c m rounded, m a maximum.  The fused product is exact, so x carries one
+// rounding of its own size, c's rounding counts as a temperature 2^-24 off, and
+// ref is a known number, not a rounded one, wherever sums with different
+// references meet.
 __device__ __forceinline__ float inv_temperature(float t) { return 1.4426950408889634f / t; }
-// Logits at the type's end (its lowest value as a mask) would overflow z * c;
-// exponents are held within this bound.
-constexpr float kRefMax = 1e30f;
+// Up to here ref is within 1/4 of c m, so the weights of entries at m are near 1;
+// further out (logits of 1e38 as a mask) 2^x could overflow, and (v - m) c is
+// taken.
+constexpr float kRefMax = 4194304.f;
 // log2 of exp((v - m) / T) for v <= m: 0 where both are the same infinity.
 __device__ __forceinline__ float log2_weight(float v, float m, float c) { return v == m ? 0.f : (v - m) * c; }
 

@@ -123,6 +123,8 @@ def distill(z, t_val, t_idx, T: float = 1.0, t_lse: Optional[float] = None, weig
     m = z.max() if np.isfinite(z.max()) else 0.0  # softmax does not see a shift; sums keep their precision
     zt = (z - m) / T
     L = _lse(zt)
+    if t_lse is None:
+        t = (t_val[listed] - t_val[listed].max()) / T
     lp = t - (_lse(t) if t_lse is None else float(t_lse))
     p = np.exp(lp)
     on = p > 0
@@ -137,5 +139,6 @@ def distill(z, t_val, t_idx, T: float = 1.0, t_lse: Optional[float] = None, weig
     grad = P * np.exp(zt - L)
     grad[ids] -= p
     if pr > 0 and Lr > -np.inf:
-        grad[outside] -= pr * np.exp(zt[outside] - Lr)
+        w = np.exp(zt[outside] - zt[outside].max())
+        grad[outside] -= pr * w / w.sum()
     return weight * loss, grad * (weight / T)

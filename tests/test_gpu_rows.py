@@ -160,6 +160,51 @@ def test_sample(dtype, n, V, pad, kind, mode):
     _check_sample(_host(zt), u, T, k, p, mp, tok.cpu().numpy(), lp.cpu().numpy())
 
 
+@pytest.mark.parametrize("dtype,n,V,pad,kind,mode,rows", [
+    ("bf16", 160, 151936, 0, "flat", "mixed", 24), ("f32", 330, 60001, 3, "flat", "p", 12),
+    ("bf16", 330, 151936, 0, "ties", "p", 8), ("f16", 330, 90001, 1, "flat", "m", 12),
+    ("bf16", 330, 90001, 0, "flat", "wide", 6), ("f16", 310, 90000, 0, "masked", "mixed", 16),
+    ("bf16", 2200, 83000, 0, "flat", "p", 6),
+])
+def test_sample_leaves_wide_rows_to_a_second_launch(dtype, n, V, pad, kind, mode, rows):
+    # batches large enough that a row has few CTAs; some of the rows are checked
+    rng = np.random.default_rng(V + n)
+    base = _logits(rng, 32, V, kind)
+    zt = _padded(np.zeros((n, V), np.float32), dtype, pad)
+    some = _padded(base, dtype, 0)
+    for r in range(n):
+        zt[r] = torch.roll(some[r % 32], 37 * (r // 32))
+    T, k, p, mp = _ask(rng, n, mode)
+    u = torch.rand((n, V + pad), generator=torch.Generator(device=DEV).manual_seed(3), device=DEV)
+    u = (u * (1 << 23)).floor().mul_(2).add_(1).mul_(2.0 ** -24)[:, :V]
+    tok, lp = _sample(zt, T, k, p, mp, u)
+    again = _sample(zt, T, k, p, mp, u)
+    assert api.dflash_get_status() == 0
+    assert torch.equal(tok, again[0]) and torch.equal(lp, again[1])
+    pick = np.sort(rng.choice(n, rows, replace=False))
+    at = torch.from_numpy(pick).to(DEV)
+    _check_sample(_host(zt[at]), u[at].cpu().numpy(), T[pick], k[pick], p[pick], mp[pick], tok[at].cpu().numpy(),
+                  lp[at].cpu().numpy())
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("T", [1e-6, 1e-3, 50.0, 1e6])
+def test_sample_at_the_ends_of_the_temperature(dtype, T):
+    rng = np.random.default_rng(21)
+    n, V = 12, 30011
+    z = _logits(rng, n, V, "flat")
+    z[3] += 3000.0                       # far from zero
+    z[4] = float(torch.finfo(DT[dtype]).min)
+    z[5, 100:] = float(torch.finfo(DT[dtype]).min)
+    zt = _padded(z, dtype, 0)
+    _, k, p, mp = _ask(rng, n, "mixed")
+    t = np.full(n, T, np.float32)
+    u = _uniforms(rng, (n, V))
+    tok, lp = _sample(zt, t, k, p, mp, _dev(u, np.float32))
+    assert api.dflash_get_status() == 0
+    _check_sample(_host(zt), u, t, k, p, mp, tok.cpu().numpy(), lp.cpu().numpy())
+
+
 def test_sample_takes_every_border_of_a_worked_row():
     # weights 8, 4, 4, 2, 1 at T = 1 / ln 2; the uniforms make the last kept
     # entry of the order the winner
@@ -309,6 +354,43 @@ def test_accept(dtype, b, R, D, V, pad, kind, mode):
         assert (n[j], c[j], nx[j]) == (rn, rc, rnx) and em[j].tolist() == rem.tolist(), (j, ask)
         same += 1
     assert same >= (b + 1) // 2
+
+
+@pytest.mark.parametrize("dtype,b,R,D,V,kind,mode", [
+    ("bf16", 12, 16, 15, 151936, "flat", "mixed"), ("f32", 20, 16, 16, 60001, "flat", "p"),
+    ("bf16", 24, 16, 15, 90001, "flat", "mixed"),
+])
+def test_accept_leaves_wide_rows_to_more_launches(dtype, b, R, D, V, kind, mode):
+    rng = np.random.default_rng(R * V + b)
+    base = _logits(rng, 16, V, kind).astype(np.float32)
+    zt = torch.empty((b, R, V), dtype=DT[dtype], device=DEV)
+    some = _padded(base, dtype, 0)
+    for r in range(b * R):
+        zt[r // R, r % R] = torch.roll(some[r % 16], 41 * (r // 16))
+    draft = zt[:, :D].float().argmax(2).to(torch.int32)
+    for j in range(b):
+        for i in range(min(D, j % (D + 1))):  # certain accepts first, then the drawn lots
+            zt[j, i, draft[j, i].long()] = 60.0
+    draft = draft.cpu().numpy()
+    T, k, p, mp = _ask(rng, b, mode)
+    ua, us = _uniforms(rng, (b, D)), _uniforms(rng, (b, V))
+    ws = torch.zeros(api.dflash_verify_filtered_workspace_size(b, R, V), dtype=torch.uint8, device=DEV)
+    got = _accept(zt, draft, T, k, p, mp, ua, _dev(us, np.float32), ws=ws)
+    again = _accept(zt, draft, T, k, p, mp, ua, _dev(us, np.float32), ws=ws)
+    assert api.dflash_get_status() == 0
+    for x, y in zip(got, again):
+        assert np.array_equal(x, y)
+    n, c, em, nx = got
+    same = 0
+    for j in range(b):
+        ask = (float(T[j]), int(k[j]), float(p[j]), float(mp[j]))
+        z = _host(zt[j])
+        if _accept_margin(z, draft[j], *ask, ua[j], us[j]) < 1e-6:
+            continue
+        rn, rc, rem, rnx = RO.verify_accept_filtered(z, draft[j], ask[0], ua[j], us[j], *ask[1:])
+        assert (n[j], c[j], nx[j]) == (rn, rc, rnx) and em[j].tolist() == rem.tolist(), (j, ask)
+        same += 1
+    assert same >= b // 2
 
 
 def test_accept_at_zero_temperature_is_the_greedy_kernel():
@@ -551,6 +633,43 @@ def test_distill_with_masks_of_the_lowest_value(dtype):
         rl, rg = RO.distill(_host(zt)[r], tv[r], ti[r], 0.5)
         assert abs(float(loss[r]) - rl) < 1e-5 * (1 + abs(rl)), r
         assert np.abs(_host(dz)[r] - rg).max() < 1e-5 + 2 * eps, r
+
+
+@pytest.mark.parametrize("mask", [-1e7, -2e9, -1e10, -3e20, -1e30, -3e38])
+@pytest.mark.parametrize("T", [1e-3, 0.5, 20.0])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_distill_with_masks_far_out(dtype, T, mask):
+    # at any distance: a masked tail, rows of nothing but masks, far maxima
+    V, K = 20011, 4
+    rng = np.random.default_rng(5)
+    z = np.full((6, V), mask)
+    z[0, 50:600] = rng.normal(0, 2, 550) * min(T, 1)
+    z[1] = -mask if abs(mask) < 1e38 else mask          # equal, far above zero
+    z[2, :7000] = 0.0
+    z[3, [5, 9, 2000, 20010]] = np.array([1.0, 2.0, 0.5, 1.5]) * min(T, 1)
+    z[5, ::3] = rng.normal(0, 2, z[5, ::3].size) * min(T, 1)
+    ti = np.array([[60, 90, 200, 555], [5, 9, 2000, 20010], [5, 9, 2000, 600], [5, 9, 2000, 20010],
+                   [5, 9, 2000, 20010], [3, 9, 2001, 20010]], np.int32)
+    tv = (np.array([[1.0, 0.5, 0.2, 0.1]] * 6) * T).astype(np.float32)
+    tv[4] += np.float32(mask)                           # the teacher's as well
+    zt = _padded(z, dtype, 1)
+    for lse in (False, True):
+        tl = [RO._lse(t.astype(np.float64) / np.float64(np.float32(T))) + 0.01 for t in tv]
+        rows = [r for r in range(6) if not (lse and r == 4)]   # (a difference from one needs the sum's digits)
+        n = len(rows)
+        loss, dz = torch.empty(n, device=DEV), torch.empty((n, V), dtype=DT[dtype], device=DEV)
+        stats = torch.empty((n, 4), device=DEV)
+        api.dflash_distill_loss(zt[rows].contiguous(), _dev(tv[rows], np.float32), _dev(ti[rows], np.int32), loss,
+                                temperature=T, t_lse=_dev(np.array(tl)[rows], np.float32) if lse else None, dlogits=dz,
+                                stats_out=stats)
+        eps = {"f32": 2.0 ** -24, "bf16": 2.0 ** -8}[dtype]
+        for at, r in enumerate(rows):
+            rl, rg = RO.distill(_host(zt)[r], tv[r], ti[r], float(np.float32(T)), float(np.float32(tl[r])) if lse else None)
+            if rl < 1e34:  # (log-probabilities below fp32's range count as -inf)
+                assert abs(float(loss[at]) - rl) < 1e-5 * (1 + abs(rl)), (r, lse, float(loss[at]), rl)
+            else:
+                assert float(loss[at]) > 0.999 * min(rl, 3e38), (r, lse)
+            assert np.abs(_host(dz)[at] - rg).max() < (1e-5 + 2 * eps) / T, (r, lse)
 
 
 def test_distill_keeps_the_rest_when_the_student_is_sure():
