@@ -42,7 +42,8 @@ constexpr int kGroups = 8;            // groups of entries per thread whose maxi
 constexpr int kGroupBins = 256;       // bins of the groups' maxima
 constexpr int kLineBins = 1024;       // bins of the weights, linear in the logit
 constexpr int kDevBadParam = 0x8;
-constexpr int kFewTarget = 96;        // entries the short list aims at where top-k does not say
+constexpr int kGroupTarget = 192;      // groups the short list takes at most where top-k does not say
+constexpr float kGroupOne = 131072.f;  // 2^17: a weight of one in sums over groups (at most 2^14 of them)
 constexpr int kShareRows = 2048;      // rows looked through at a time by a second launch
 constexpr int kShareMost = 64;        // of which a cluster takes at most so many
 constexpr int kQuick = 128;           // lists up to this length are ranked, longer ones sorted
@@ -94,7 +95,7 @@ struct alignas(16) Shared {
   uint64_t need;                     // top-p keeps entries while the sum before them is below this
   float bound;                       // min-p's bound on a logit
   uint32_t own_count, taken, queued;
-  uint32_t groups[kGroupBins];
+  uint32_t groups[kGroupBins], weights[kGroupBins];  // groups' maxima: their number and weights
   union {
     uint64_t list[kCap];  // places; complete in rank 0
     struct {
@@ -387,6 +388,20 @@ struct Scan {
   bool careful;
 };
 
+// A thread's sum of weights relative to its maximum, whatever its entries are.
+template <typename T, int NT>
+__device__ __noinline__ float careful_sum(const Part<T> part, const float c, const float top) {
+  float sum = 0.f;
+  for (int j = threadIdx.x; j < part.packs; j += NT) {
+    float v[Part<T>::kE];
+    Part<T>::open(part.pack(j), v);
+#pragma unroll
+    for (int h = 0; h < Part<T>::kE; ++h)
+      if (v[h] > -INFINITY) sum += fast_exp2(log2_weight(v[h], top, c));
+  }
+  return sum;
+}
+
 template <typename T, int NT>
 __device__ __forceinline__ void scan_row(const Row<T, NT>& r, bool want_mass, Scan<T, NT>& t) {
   constexpr int kE = Row<T, NT>::kE;
@@ -437,12 +452,7 @@ __device__ __forceinline__ void scan_row(const Row<T, NT>& r, bool want_mass, Sc
   }
   // masked entries that are NaN, or logits at the type's end: again, with care
   t.careful = want_mass && (odd || !(t.sum < INFINITY));
-  if (t.careful) {
-    t.sum = 0.f;
-    r.each([&](float v, int64_t) {
-      if (v > -INFINITY) t.sum += fast_exp2(log2_weight(v, t.top, r.c));
-    });
-  }
+  if (t.careful) t.sum = careful_sum<T, NT>(r.part, r.c, t.top);
 }
 
 // A first bar for a drawing pass, below the best score among the entries of the
@@ -529,13 +539,8 @@ __device__ __forceinline__ void scan_and_draw(const Row<T, NT>& r, Shared<NT, kC
   t.top = Row<T, NT>::max_of(mx);
 #pragma unroll
   for (int x = 0; x < kGroups; ++x) t.group[x] = t.top;
-  t.careful = odd || !(t.sum < INFINITY);
-  if (t.careful) {  // NaN entries, or logits at the type's end: again, with care
-    t.sum = 0.f;
-    r.each([&](float v, int64_t) {
-      if (v > -INFINITY) t.sum += fast_exp2(log2_weight(v, t.top, r.c));
-    });
-  }
+  t.careful = odd || !(t.sum < INFINITY);  // (see scan_row)
+  if (t.careful) t.sum = careful_sum<T, NT>(r.part, r.c, t.top);
 }
 
 // The row's maximum (false: no entry counts), the lowest of the groups' maxima
@@ -615,33 +620,49 @@ __device__ __forceinline__ void list_entries(const Row<T, NT>& r, Shared<NT, kCa
     if (threadIdx.x == 0) s.own_count = kCap + 1;
     return;
   }
-  uint32_t* taken = peer(&s.taken, 0);
   uint64_t* list = peer(s.list, 0);
+  const int lane = threadIdx.x & 31;
   const uint32_t deep = (r.part.packs + kGroups * NT - 1) / (kGroups * NT), units = s.queued * deep;
   uint64_t listed = 0;  // as integers: which thread takes which pack is not fixed
-  for (uint32_t y0 = threadIdx.x; y0 < units; y0 += 4 * NT) {
+  uint32_t count = 0;
+  for (uint32_t y0 = threadIdx.x - lane; y0 < units; y0 += 4 * NT) {
     uint4 w[4];
     int at[4];
 #pragma unroll
     for (int x = 0; x < 4; ++x) {
-      const uint32_t y = y0 + x * NT, g = y / deep;
+      const uint32_t y = y0 + lane + x * NT, g = y / deep;
       at[x] = y < units ? queue[g] + static_cast<int>(y - g * deep) * (kGroups * NT) : r.part.packs;
       w[x] = r.pack(at[x]);
     }
+    uint32_t hits = 0;  // kE bits a pack
 #pragma unroll
     for (int x = 0; x < 4; ++x) {
       float v[kE];
       Row<T, NT>::open_pack(w[x], v);
-      uint32_t hits = 0;
 #pragma unroll
-      for (int h = 0; h < kE; ++h) hits |= (v[h] >= t && v[h] > -INFINITY ? 1u : 0u) << h;
-      if (hits == 0) continue;
-      uint32_t base = atomicAdd(taken, static_cast<uint32_t>(__popc(hits)));
-      atomicAdd(&s.own_count, static_cast<uint32_t>(__popc(hits)));
+      for (int h = 0; h < kE; ++h) hits |= (v[h] >= t && v[h] > -INFINITY ? 1u : 0u) << (x * kE + h);
+    }
+    // one reservation a warp: a round trip to rank 0 for all of its packs
+    const uint32_t n = __popc(hits);
+    uint32_t before = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t y = __shfl_up_sync(0xffffffffu, before, o);
+      if (lane >= o) before += y;
+    }
+    uint32_t base = 0;
+    if (lane == 31 && before > 0) {
+      count += before;
+      base = r.size == 1 ? atomicAdd(&s.taken, before) : atomicAdd(peer(&s.taken, 0), before);
+    }
+    base = __shfl_sync(0xffffffffu, base, 31) + before - n;
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      uint32_t some = hits >> (x * kE) & ((1u << kE) - 1);
       const int64_t i = r.index_of(at[x]);
-      while (hits) {
-        const int h = __ffs(hits) - 1;
-        hits &= hits - 1;
+      while (some) {
+        const int h = __ffs(some) - 1;
+        some &= some - 1;
         const float z = Row<T, NT>::pick_of(w[x], h);
         if (base < kCap) list[base] = place_of(value_key(z), static_cast<uint32_t>(i + h));
         ++base;
@@ -649,6 +670,7 @@ __device__ __forceinline__ void list_entries(const Row<T, NT>& r, Shared<NT, kCa
       }
     }
   }
+  if (count > 0) atomicAdd(&s.own_count, count);
   if (listed > 0) atomicAdd(reinterpret_cast<unsigned long long*>(&s.own_mass), static_cast<unsigned long long>(listed));
 }
 
@@ -672,12 +694,14 @@ __device__ __forceinline__ void close_list(const Row<T, NT>& r, Shared<NT, kCap>
 // The short list.  A value t with at least `target` entries at or above it is
 // read off a histogram of the groups' maxima (each the largest of a few dozen
 // entries, so few entries beyond the target pass), and the places of the
-// entries that reach t go to rank 0's list.  target 0: t is given.  Returns
-// false where the list would not hold them; else count and mass (if wanted)
-// are those of the list.
+// entries that reach t go to rank 0's list.  With want > 0, t may come earlier:
+// where the maxima's own weights, a lower bound of the entries', sum to `want`;
+// a row whose first `target` groups hold less than half of it is not listed
+// (unless `sure`).  target 0: t is given.  Returns false where there is no list;
+// else count and, with want, mass are those of the list.
 template <typename T, int NT, int kCap>
 __device__ bool short_list(Row<T, NT>& r, Shared<NT, kCap>& s, const Scan<T, NT>& sc, int64_t V, float low, int target,
-                           float* bound, bool want_mass, uint32_t* count, uint64_t* mass) {
+                           float* bound, float want, bool sure, uint32_t* count, uint64_t* mass) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const float range = r.m - low;
   float t = *bound;
@@ -689,34 +713,49 @@ __device__ bool short_list(Row<T, NT>& r, Shared<NT, kCap>& s, const Scan<T, NT>
     for (int x = 0; x < kGroups; ++x) {
       if (sc.group[x] > -INFINITY) {
         const int b = static_cast<int>((r.m - sc.group[x]) * per);
-        atomicAdd(&s.groups[b < 0 ? 0 : (b < kGroupBins ? b : kGroupBins - 1)], 1u);
+        const int at = b < 0 ? 0 : (b < kGroupBins ? b : kGroupBins - 1);
+        atomicAdd(&s.groups[at], 1u);
+        if (want > 0.f) atomicAdd(&s.weights[at], __float2uint_rz(fast_exp2(r.log2w(sc.group[x])) * kGroupOne));
       }
     }
     cluster_sync_all(r.size);
-    // the bin in which the maxima, from the highest, reach the target
-    static_assert(kGroupBins <= NT, "one thread per bin");
-    uint32_t n = 0;
-    if (threadIdx.x < kGroupBins) {
-      uint32_t c[kMaxCluster];
+    // the bin in which the maxima, from the highest, reach the target: number
+    // and weight side by side in one word
+    static_assert(kGroupBins == NT, "one thread per bin");
+    uint64_t c[kMaxCluster], n = 0;
 #pragma unroll
-      for (uint32_t o = 0; o < kMaxCluster; ++o) c[o] = o < r.size ? *peer(&s.groups[threadIdx.x], o) : 0u;
-#pragma unroll
-      for (uint32_t o = 0; o < kMaxCluster; ++o) n += c[o];
+    for (uint32_t o = 0; o < kMaxCluster; ++o) {
+      c[o] = 0;
+      if (o < r.size) {
+        c[o] = static_cast<uint64_t>(*peer(&s.groups[threadIdx.x], o)) << 32;
+        if (want > 0.f) c[o] += *peer(&s.weights[threadIdx.x], o);
+      }
     }
-    uint32_t inc = n;
+#pragma unroll
+    for (uint32_t o = 0; o < kMaxCluster; ++o) n += c[o];
+    uint64_t inc = n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const uint32_t u = __shfl_up_sync(0xffffffffu, inc, o);
+      const uint64_t u = __shfl_up_sync(0xffffffffu, inc, o);
       if (lane >= o) inc += u;
     }
     if (lane == 31) s.warp_sum[warp] = inc;
     if (threadIdx.x == 0) s.pick[0] = kGroupBins;
     __syncthreads();
-    for (int w = 0; w < warp; ++w) inc += static_cast<uint32_t>(s.warp_sum[w]);
-    if (inc - n < static_cast<uint32_t>(target) && inc >= static_cast<uint32_t>(target)) s.pick[0] = threadIdx.x;
+    for (int w = 0; w < warp; ++w) inc += s.warp_sum[w];
+    // (a margin of 2^-10: the list's own sum is compared with what is needed)
+    const uint32_t weight = want > 0.f ? __float2uint_ru(want * kGroupOne * 1.0009765625f) : 0xFFFFFFFFu;
+    const auto reached = [=](uint64_t x) {
+      return (x >> 32) >= static_cast<uint32_t>(target) || static_cast<uint32_t>(x) >= weight;
+    };
+    if (reached(inc) && !reached(inc - n)) {
+      s.pick[0] = threadIdx.x;
+      s.pick[1] = static_cast<uint32_t>(inc) < weight / 2 && !sure;
+    }
     __syncthreads();
     const int b = static_cast<int>(s.pick[0]);
     if (b < kGroupBins) {
+      if (want > 0.f && s.pick[1]) return false;
       // its lower edge, less what the bins' arithmetic may round
       t = per > 0.f ? r.m - (static_cast<float>(b) + 1.f) / per * 1.0001f - fabsf(r.m) * 1e-6f : low;
     } else {
@@ -724,7 +763,7 @@ __device__ bool short_list(Row<T, NT>& r, Shared<NT, kCap>& s, const Scan<T, NT>
       if (V > kCap) return false;
     }
   }
-  list_entries(r, s, sc, t, want_mass);
+  list_entries(r, s, sc, t, want > 0.f);
   close_list(r, s, count, mass);
   *bound = t;
   return *count <= kCap;
@@ -1231,10 +1270,38 @@ __device__ Verdict long_list(const Row<T, NT>& r, Shared<NT, kCap>& s, const Ask
         high -= at << shift;
         const uint64_t end = high - ((1ull << shift) - 1);
         if (end > low) low = end;
+        // what is left: their number, and the range that they fill
+        uint64_t first = 0, last = 0;
         few = 0;
 #pragma unroll
-        for (int x = 0; x < kMine; ++x) few += place[x] >= low && place[x] <= high;
-        few = static_cast<int>(cta_reduce<NT / 32>(static_cast<uint64_t>(few), OpSumU64(), s.x));
+        for (int x = 0; x < kMine; ++x) {
+          if (place[x] < low || place[x] > high) continue;
+          ++few;
+          first = place[x] > first ? place[x] : first;
+          last = ~place[x] > last ? ~place[x] : last;
+        }
+        few = __reduce_add_sync(0xffffffffu, few);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+          const uint64_t y = __shfl_xor_sync(0xffffffffu, first, o), z = __shfl_xor_sync(0xffffffffu, last, o);
+          first = y > first ? y : first;
+          last = z > last ? z : last;
+        }
+        if (lane == 0) {
+          s.join[warp][0] = static_cast<uint64_t>(few);
+          s.join[warp][1] = first;
+          s.join[warp][2] = last;
+        }
+        __syncthreads();
+        few = 0;
+#pragma unroll
+        for (int w = 0; w < NT / 32; ++w) {
+          few += static_cast<int>(s.join[w][0]);
+          first = s.join[w][1] > first ? s.join[w][1] : first;
+          last = s.join[w][2] > last ? s.join[w][2] : last;
+        }
+        high = first;
+        low = ~last;
       } while (few > kQuick);
 #pragma unroll
       for (int x = 0; x < kMine; ++x)
@@ -1480,7 +1547,7 @@ __device__ bool listed_row(Row<T, NT>& r, Shared<NT, kCap>& s, const Scan<T, NT>
   } else if (q.k < a.V) {
     target = q.k;
   } else if (of_row) {
-    target = kFewTarget;
+    target = kGroupTarget;
   } else if (q.mp > 0.f) {
     t = s.bound;
   } else {
@@ -1489,14 +1556,18 @@ __device__ bool listed_row(Row<T, NT>& r, Shared<NT, kCap>& s, const Scan<T, NT>
   if (target > kCap) return false;
   uint32_t count;
   uint64_t mass;
-  if (!short_list(r, s, sc, a.V, low, target, &t, of_row, &count, &mass)) return false;
+  const float want = of_row ? fmaxf(q.p * row_mass, 1.f) : 0.f;  // (the first entry is kept whatever p)
+  if (!short_list(r, s, sc, a.V, low, target, &t, want, q.mp > 0.f, &count, &mass)) return false;
   // the list has to hold top-p's border (with a margin for these roundings), or
   // all that min-p leaves
   const uint64_t whole = of_row ? __float2ull_rn(row_mass * r.scale) : 0;
   if (of_row && __ull2float_rz(mass) < q.p * __ull2float_ru(whole) * 1.000001f && static_cast<int64_t>(count) < a.V &&
       !(q.mp > 0.f && s.bound >= t))
     return false;
-  if (r.rank == 0) *out = settle_list(r, s, q, static_cast<int>(count), whole, u, drop);
+  if (r.rank == 0) {
+    const Row<T, NT> far = r;  // (a copy for calls: the row of the hot loops stays in registers)
+    *out = settle_list(far, s, q, static_cast<int>(count), whole, u, drop);
+  }
   return true;
 }
 
@@ -1521,7 +1592,7 @@ __device__ __forceinline__ void start(Shared<NT, kCap>& s, uint32_t size) {
     s.queued = 0;
     s.bar = 0x007FFFFFu;  // -inf
   }
-  for (int b = threadIdx.x; b < kGroupBins; b += NT) s.groups[b] = 0;
+  for (int b = threadIdx.x; b < kGroupBins; b += NT) s.groups[b] = s.weights[b] = 0;
   __syncthreads();
   if (size > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
   pdl_wait();
@@ -1600,14 +1671,16 @@ __global__ void __launch_bounds__(kThr, 4) sample_rows_kernel(const FilterArgs a
   if (q.ok && some) {
     if (unfiltered && fabsf(r.m * r.c) < 1e3f) {
       v.mass = __float2ull_rn(row_mass * r.scale);
-      tok = join_best(r, s, u, best, q.T);
+      Row<T, kThr> far = r;
+      tok = join_best(far, s, u, best, q.T);
     } else if (listed_row(r, s, sc, a, q, low, row_mass, u, -1, &v)) {
       if (r.rank != 0) return;
       tok = v.tok;
     } else if (a.defer) {
       left = 1;
     } else {
-      tok = wide_row(r, s, a, q, row_mass, u, &v);
+      Row<T, kThr> far = r;
+      tok = wide_row(far, s, a, q, row_mass, u, &v);
     }
   }
   if (a.defer && r.rank == 0 && threadIdx.x == 0) a.states[row] = RowState{r.m, row_mass, left};
@@ -1758,6 +1831,7 @@ __global__ void __launch_bounds__(kThr, 4) accept_rows_kernel(const FilterArgs a
     Verdict v{0, 0, -1, 0.f};
     const bool listed = listed_row(r, s, sc, a, q, low, row_mass, u, drop, &v);
     if (listed && r.rank != 0) return;
+    Row<T, kThr> far = r;
     if (listed) {
       out.tok = v.tok;
     } else {
@@ -1765,7 +1839,7 @@ __global__ void __launch_bounds__(kThr, 4) accept_rows_kernel(const FilterArgs a
       if (a.defer && !unfiltered)
         out.left = 1;
       else
-        wide_row(r, s, a, q, row_mass, static_cast<const float*>(nullptr), &v);
+        wide_row(far, s, a, q, row_mass, static_cast<const float*>(nullptr), &v);
     }
     out.cut = v.cut;
     if (r.rank == 0 && threadIdx.x == 0 && !out.left) out.accept = accepts(a, r, j, rr, v.cut, v.mass);
@@ -1778,7 +1852,7 @@ __global__ void __launch_bounds__(kThr, 4) accept_rows_kernel(const FilterArgs a
         }
       }
       cluster_sync_all(size);
-      if (s.pick[1] == 0) out.tok = pick_row(r, s, u, s.pick[0], drop, q.T);
+      if (s.pick[1] == 0) out.tok = pick_row(far, s, u, s.pick[0], drop, q.T);
     }
   }
   if (r.rank != 0) return;
@@ -1875,7 +1949,7 @@ __global__ void __launch_bounds__(kThr, 4) top_rows_kernel(const FilterArgs a) {
   const bool some = join_scan(r, s, sc, want_mass, &low, &row_mass);
   uint32_t n = 0;
   uint64_t mass;
-  if (some && !short_list(r, s, sc, a.V, low, a.K, &t, false, &n, &mass)) {
+  if (some && !short_list(r, s, sc, a.V, low, a.K, &t, 0.f, false, &n, &mass)) {
     // ties or a clustered row: find the exact border, then list
     uint64_t cut = 1ull << 32, valid = 0;
     r.each([&](float v, int64_t) { valid += v > -INFINITY; });
@@ -1941,7 +2015,7 @@ cudaError_t launch_wide(const void* kern, int64_t rows, size_t smem, const Filte
   FilterArgs b = a;
   b.defer = 0;
   void* args[] = {&b, &rows};
-  const int parts = rows > 2 * num_sms() ? 4 : 8;
+  const int parts = 8;
   int64_t clusters = 4 * num_sms() / parts;
   if (clusters < kShareRows / kShareMost) clusters = kShareRows / kShareMost;
   if (clusters > rows) clusters = rows;
