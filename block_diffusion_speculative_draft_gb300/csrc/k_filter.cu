@@ -1067,8 +1067,9 @@ __device__ int join_best(Row<T, NT>& r, Shared<NT, kCap>& s, const float* u, con
 
 // Gumbel maximum over the row's entries at or above the cut but `drop`.
 template <typename T, int NT, int kCap>
-__device__ __noinline__ int pick_row(Row<T, NT>& r, Shared<NT, kCap>& s, const float* u, uint64_t cut, int drop,
-                                     float temp) {
+__device__ __noinline__ int pick_row(const Row<T, NT>& row, Shared<NT, kCap>& s, const float* u, uint64_t cut,
+                                     int drop, float temp) {
+  Row<T, NT> r = row;
   Best b{-INFINITY, 0.f, -1};
   if (threadIdx.x == 0) s.bar = 0x007FFFFFu;  // -inf
   __syncthreads();
@@ -1352,9 +1353,10 @@ __device__ __forceinline__ Verdict settle_list(const Row<T, NT>& r, Shared<NT, k
 // the bin does not fit the list.  Else rank 0 has the verdict, and the draw is
 // left in `best` of the cluster's threads.
 template <typename T, int NT, int kCap>
-__device__ __noinline__ bool deep_top_p(Row<T, NT>& r, Shared<NT, kCap>& s, const Ask& q, int64_t V, float row_mass,
+__device__ __noinline__ bool deep_top_p(const Row<T, NT>& row, Shared<NT, kCap>& s, const Ask& q, int64_t V, float row_mass,
                                         const float* u, Best* best, Verdict* out) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  Row<T, NT> r = row;
   const uint64_t whole = __float2ull_rn(row_mass * r.scale);
   // entries this far below the maximum, in units of log2, sum to less than
   // (1 - p) / 2 of the row
@@ -1470,14 +1472,14 @@ __device__ __noinline__ bool deep_top_p(Row<T, NT>& r, Shared<NT, kCap>& s, cons
   cluster_sync_all(r.size);
   if (r.rank == 0) {
     if (count <= kQuick) {
-      *out = quick_list(r, s, q, static_cast<int>(count), above, whole, static_cast<const float*>(nullptr), -1);
+      *out = quick_list(row, s, q, static_cast<int>(count), above, whole, static_cast<const float*>(nullptr), -1);
       if (u && threadIdx.x < count && s.list[threadIdx.x] >= out->cut) {
         const uint32_t i = place_index(s.list[threadIdx.x]);
         const float v = key_to_value(static_cast<uint32_t>(s.list[threadIdx.x] >> 32));
         offer(*best, v, static_cast<int>(i), r.log2w(v), u[i]);
       }
     } else {
-      *out = long_list(r, s, q, static_cast<int>(count), above, whole, u, -1, best);
+      *out = long_list(row, s, q, static_cast<int>(count), above, whole, u, -1, best);
     }
   }
   return true;
@@ -1486,7 +1488,8 @@ __device__ __noinline__ bool deep_top_p(Row<T, NT>& r, Shared<NT, kCap>& s, cons
 // Min-p alone over a row of which it keeps many entries: their mass, and the
 // draw left in `best`.
 template <typename T, int NT, int kCap>
-__device__ __noinline__ uint64_t deep_min_p(Row<T, NT>& r, Shared<NT, kCap>& s, const float* u, Best* best) {
+__device__ __noinline__ uint64_t deep_min_p(const Row<T, NT>& row, Shared<NT, kCap>& s, const float* u, Best* best) {
+  Row<T, NT> r = row;
   const float low = s.bound;
   if (threadIdx.x == 0) s.bar = 0x007FFFFFu;  // -inf
   __syncthreads();
@@ -1644,7 +1647,7 @@ __device__ __forceinline__ void write_sample(const FilterArgs& a, const Row<T, k
 // Few CTAs serve a row whose filters leave a short list.  A row that needs more
 // passes is left to a second launch, whose clusters share out such rows, unless
 // this one has many CTAs a row already.
-template <typename T>
+template <typename T, bool kDefer>
 __global__ void __launch_bounds__(kThr, 4) sample_rows_kernel(const FilterArgs a) {
   extern __shared__ __align__(16) uint8_t raw[];
   Short& s = *reinterpret_cast<Short*>(raw);
@@ -1676,14 +1679,14 @@ __global__ void __launch_bounds__(kThr, 4) sample_rows_kernel(const FilterArgs a
     } else if (listed_row(r, s, sc, a, q, low, row_mass, u, -1, &v)) {
       if (r.rank != 0) return;
       tok = v.tok;
-    } else if (a.defer) {
+    } else if constexpr (kDefer) {
       left = 1;
     } else {
       Row<T, kThr> far = r;
       tok = wide_row(far, s, a, q, row_mass, u, &v);
     }
   }
-  if (a.defer && r.rank == 0 && threadIdx.x == 0) a.states[row] = RowState{r.m, row_mass, left};
+  if (kDefer && r.rank == 0 && threadIdx.x == 0) a.states[row] = RowState{r.m, row_mass, left};
   if (!left) write_sample(a, r, row, tok, v, q.ok);
 }
 
@@ -1802,10 +1805,10 @@ __device__ __forceinline__ void write_sequence(const FilterArgs& a, int64_t j, i
 
 // Verified row rr of sequence j: whether its draft is accepted, and the token
 // drawn here if it is not (or if rr = D).  The CTA that finishes a sequence's
-// last row (a ticket) writes the outputs.  With a.defer, rows without a short
+// last row (a ticket) writes the outputs.  With kDefer, rows without a short
 // list are left to two more launches: their cuts, then the one draw that a
 // sequence needs and its outputs.
-template <typename T>
+template <typename T, bool kDefer>
 __global__ void __launch_bounds__(kThr, 4) accept_rows_kernel(const FilterArgs a) {
   extern __shared__ __align__(16) uint8_t raw[];
   Short& s = *reinterpret_cast<Short*>(raw);
@@ -1836,30 +1839,36 @@ __global__ void __launch_bounds__(kThr, 4) accept_rows_kernel(const FilterArgs a
       out.tok = v.tok;
     } else {
       out.tok = kDeferred;
-      if (a.defer && !unfiltered)
+      if (unfiltered) {
+        v.mass = __float2ull_rn(row_mass * r.scale);
+        v.cut = 1ull << 32;
+      } else if constexpr (kDefer) {
         out.left = 1;
-      else
+      } else {
         wide_row(far, s, a, q, row_mass, static_cast<const float*>(nullptr), &v);
+      }
     }
     out.cut = v.cut;
     if (r.rank == 0 && threadIdx.x == 0 && !out.left) out.accept = accepts(a, r, j, rr, v.cut, v.mass);
-    if (!listed && !a.defer) {  // a wide row draws where it has to
-      if (r.rank == 0 && threadIdx.x == 0) {
-        for (uint32_t o = 0; o < size; ++o) {
-          uint64_t* p = peer(s.pick, o);
-          p[0] = out.cut;
-          p[1] = static_cast<uint64_t>(out.accept);
+    if constexpr (!kDefer) {
+      if (!listed) {  // a wide row draws where it has to
+        if (r.rank == 0 && threadIdx.x == 0) {
+          for (uint32_t o = 0; o < size; ++o) {
+            uint64_t* p = peer(s.pick, o);
+            p[0] = out.cut;
+            p[1] = static_cast<uint64_t>(out.accept);
+          }
         }
+        cluster_sync_all(size);
+        if (s.pick[1] == 0) out.tok = pick_row(far, s, u, s.pick[0], drop, q.T);
       }
-      cluster_sync_all(size);
-      if (s.pick[1] == 0) out.tok = pick_row(far, s, u, s.pick[0], drop, q.T);
     }
   }
   if (r.rank != 0) return;
   if (threadIdx.x == 0) {
     a.cuts[row] = out;
     s.taken = 0;
-    if (!a.defer) {
+    if (!kDefer) {
       __threadfence();
       s.taken = atomicAdd(&a.tickets[j], 1) == a.rows_used - 1;
     }
@@ -2013,7 +2022,6 @@ bool defers(int64_t V, int64_t rows, size_t esize, int parts) {
 // CTAs, or of four where many rows may come.
 cudaError_t launch_wide(const void* kern, int64_t rows, size_t smem, const FilterArgs& a, cudaStream_t st) {
   FilterArgs b = a;
-  b.defer = 0;
   void* args[] = {&b, &rows};
   const int parts = 8;
   int64_t clusters = 4 * num_sms() / parts;
@@ -2025,19 +2033,21 @@ cudaError_t launch_wide(const void* kern, int64_t rows, size_t smem, const Filte
 template <typename T>
 cudaError_t launch_sample(FilterArgs a, int64_t rows, cudaStream_t st) {
   const int parts = pick_parts(a.V, rows, sizeof(T));
-  a.defer = defers(a.V, rows, sizeof(T), parts);
-  cudaError_t e = launch_rows((const void*)sample_rows_kernel<T>, rows, parts, sizeof(Short), a, st);
-  if (e != cudaSuccess || !a.defer) return e;
+  const bool defer = defers(a.V, rows, sizeof(T), parts);
+  const void* kern = defer ? (const void*)sample_rows_kernel<T, true> : (const void*)sample_rows_kernel<T, false>;
+  cudaError_t e = launch_rows(kern, rows, parts, sizeof(Short), a, st);
+  if (e != cudaSuccess || !defer) return e;
   return launch_wide((const void*)sample_wide_kernel<T>, rows, sizeof(Short), a, st);
 }
 template <typename T>
 cudaError_t launch_accept(FilterArgs a, int64_t b, cudaStream_t st) {
   const int64_t rows = b * a.rows_used;
   const int parts = pick_parts(a.V, rows, sizeof(T));
-  a.defer = defers(a.V, rows, sizeof(T), parts);
-  cudaError_t e = launch_rows((const void*)accept_rows_kernel<T>, rows, parts, sizeof(Short), a, st);
+  const bool defer = defers(a.V, rows, sizeof(T), parts);
+  const void* kern = defer ? (const void*)accept_rows_kernel<T, true> : (const void*)accept_rows_kernel<T, false>;
+  cudaError_t e = launch_rows(kern, rows, parts, sizeof(Short), a, st);
   if (e != cudaSuccess) return e;
-  if (!a.defer) return cudaSuccess;
+  if (!defer) return cudaSuccess;
   if ((e = launch_wide((const void*)accept_wide_kernel<T>, rows, sizeof(Short), a, st)) != cudaSuccess) return e;
   return launch_rows((const void*)accept_pick_kernel<T>, b, pick_parts(a.V, b, sizeof(T)), sizeof(Short), a, st);
 }

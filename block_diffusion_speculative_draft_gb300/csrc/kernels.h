@@ -256,7 +256,6 @@ struct FilterArgs {
   int idx_bits;    // set by the launchers: bits of V - 1, scale of the weights
   float scale;
   float unit;      // 1 / scale
-  int defer;       // rows without a short list are left to a second launch
 };
 cudaError_t filter_sample(FilterArgs a, int dtype, int64_t rows, cudaStream_t st);
 inline size_t accept_cuts_bytes(int64_t b, int R) { return (size_t)b * R * sizeof(RowCut); }
