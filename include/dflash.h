@@ -353,7 +353,8 @@ DFLASH_API int32_t dflash_commit_draft_block(const dflash_weights* w, const dfla
  *    between V and ld.  1 <= V < 2^31, 1 <= rows < 2^28.
  *  - An entry that is NaN or -inf is masked: it has probability 0 and is never
  *    returned (the distillation calls instead propagate a NaN).  Every finite
- *    value counts, the type's lowest included.
+ *    value counts, the type's lowest included; where the largest is +inf, the
+ *    entries that are +inf share the probability.
  *  - The order of a row is by descending logit, equal logits by ascending
  *    index (-0 equals +0).
  *  - Results depend on the arguments alone: they repeat bit for bit.
@@ -444,6 +445,10 @@ DFLASH_API int32_t dflash_top_logits(const void* logits, int32_t dtype, int64_t 
  *    out: loss 0, gradient 0, its student logits do not matter.
  *  - A row with an index listed twice, or outside [-1, V), is refused: loss
  *    NaN, gradient 0, DFLASH_DEV_BAD_TOKEN set.
+ *  - A student row without a logit above -inf has no distribution: loss NaN,
+ *    gradient undefined.  The loss is +inf where p_k > 0 meets a q below fp32's
+ *    range of logarithms (a -inf logit, or one 3e38 T below the others).
+ *  - t_lse has to be finite in rows that are not left out.
  * No workspace. */
 DFLASH_API int32_t dflash_distill_loss(const void* logits, int32_t dtype, int64_t rows, int64_t V, int64_t ld,
                                        const float* t_val, const int32_t* t_idx, int32_t K, const float* t_lse,
