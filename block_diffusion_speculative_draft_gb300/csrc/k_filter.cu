@@ -1811,11 +1811,20 @@ __device__ __forceinline__ void write_sequence(const FilterArgs& a, int64_t j, i
     for (int i = lane; i < a.R; i += 32) a.emitted[j * a.R + i] = i < n ? dr[i] : (i == n ? corr : -1);
 }
 
+// One thread, after its row's result is written: whether it was the sequence's
+// last (then the ticket starts anew).
+__device__ __forceinline__ bool finishes(const FilterArgs& a, int64_t j) {
+  __threadfence();
+  if (atomicAdd(&a.tickets[j], 1) != a.rows_used - 1) return false;
+  a.tickets[j] = 0;
+  __threadfence();
+  return true;
+}
+
 // Verified row rr of sequence j: whether its draft is accepted, and the token
 // drawn here if it is not (or if rr = D).  The CTA that finishes a sequence's
 // last row (a ticket) writes the outputs.  With kDefer, rows without a short
-// list are left to two more launches: their cuts, then the one draw that a
-// sequence needs and its outputs.
+// list are left to a second launch.
 template <typename T, bool kDefer>
 __global__ void __launch_bounds__(kThr, 4) accept_rows_kernel(const FilterArgs a) {
   extern __shared__ __align__(16) uint8_t raw[];
@@ -1838,7 +1847,6 @@ __global__ void __launch_bounds__(kThr, 4) accept_rows_kernel(const FilterArgs a
   if (q.ok && some) {
     const int drop = rr < a.D ? a.draft[j * a.D + rr] : -1;
     const float* u = a.u + j * a.ld_u;
-    const bool unfiltered = want_mass && q.p >= 1.f;
     Verdict v{0, 0, -1, 0.f};
     const bool listed = listed_row(r, s, sc, a, q, low, row_mass, u, drop, &v);
     if (listed && r.rank != 0) return;
@@ -1847,10 +1855,7 @@ __global__ void __launch_bounds__(kThr, 4) accept_rows_kernel(const FilterArgs a
       out.tok = v.tok;
     } else {
       out.tok = kDeferred;
-      if (unfiltered) {
-        v.mass = __float2ull_rn(row_mass * r.scale);
-        v.cut = 1ull << 32;
-      } else if constexpr (kDefer) {
+      if constexpr (kDefer) {
         out.left = 1;
       } else {
         wide_row(far, s, a, q, row_mass, static_cast<const float*>(nullptr), &v);
@@ -1875,20 +1880,16 @@ __global__ void __launch_bounds__(kThr, 4) accept_rows_kernel(const FilterArgs a
   if (r.rank != 0) return;
   if (threadIdx.x == 0) {
     a.cuts[row] = out;
-    s.taken = 0;
-    if (!kDefer) {
-      __threadfence();
-      s.taken = atomicAdd(&a.tickets[j], 1) == a.rows_used - 1;
-    }
+    s.taken = !out.left && finishes(a, j);
   }
   __syncthreads();
   if (!s.taken || threadIdx.x >= 32) return;
-  __threadfence();
-  if (threadIdx.x == 0) a.tickets[j] = 0;
   const int n = leading_accepts(a, j);
   write_sequence(a, j, n, n < a.R ? __ldcg(&a.cuts[j * a.R + n].tok) : -1, q.ok);
 }
 
+// The rows left by it; the cluster that finishes a sequence's last row makes the one
+// draw that it needs, if that row was left too, and writes the outputs.
 template <typename T>
 __global__ void __launch_bounds__(kThr, 4) accept_wide_kernel(const FilterArgs a, const int64_t rows) {
   extern __shared__ __align__(16) uint8_t raw[];
@@ -1912,35 +1913,24 @@ __global__ void __launch_bounds__(kThr, 4) accept_wide_kernel(const FilterArgs a
         if (r.rank == 0 && threadIdx.x == 0) {  // `left` stays: other clusters read it
           c->cut = v.cut;
           c->accept = accepts(a, r, j, rr, v.cut, v.mass);
+          const bool last = finishes(a, j);
+          for (uint32_t o = 0; o < size; ++o) *peer(s.pick, o) = last;
         }
+        cluster_sync_all(size);
+        if (s.pick[0] == 0) return;
+        const int n = leading_accepts(a, j);
+        int corr = -1;
+        if (n < a.R) {
+          const RowCut* e = a.cuts + j * a.R + n;
+          corr = __ldcg(&e->tok);
+          if (corr == kDeferred) {
+            r.open(a, j * a.R + n);
+            r.m = __ldcg(&e->m);
+            corr = pick_row(r, s, a.u + j * a.ld_u, __ldcg(&e->cut), n < a.D ? a.draft[j * a.D + n] : -1, q.T);
+          }
+        }
+        if (r.rank == 0 && threadIdx.x < 32) write_sequence(a, j, n, corr, true);
       });
-}
-
-// One cluster per sequence, after rows that were left to a second launch.
-template <typename T>
-__global__ void __launch_bounds__(kThr) accept_pick_kernel(const FilterArgs a) {
-  extern __shared__ __align__(16) uint8_t raw[];
-  Short& s = *reinterpret_cast<Short*>(raw);
-  pdl_wait();
-  const uint32_t size = cluster_size();
-  const int64_t j = blockIdx.x / size;
-  const Ask q = read_ask(a, j);
-  const int n = leading_accepts(a, j);
-  int corr = -1;
-  if (q.ok && n < a.R) {
-    const int64_t row = j * a.R + n;
-    const RowCut c = a.cuts[row];
-    corr = c.tok;
-    if (corr == kDeferred) {
-      Row<T, kThr> r;
-      r.c = inv_temperature(q.T);
-      r.open(a, row);
-      r.m = c.m;
-      cluster_sync_all(size);
-      corr = pick_row(r, s, a.u + j * a.ld_u, c.cut, n < a.D ? a.draft[j * a.D + n] : -1, q.T);
-    }
-  }
-  if (cluster_rank() == 0 && threadIdx.x < 32) write_sequence(a, j, n, corr, q.ok);
 }
 
 constexpr int kTopCap = 2048;
@@ -2061,10 +2051,8 @@ cudaError_t launch_accept(FilterArgs a, int64_t b, cudaStream_t st) {
   const bool defer = defers(a.V, rows, sizeof(T), parts);
   const void* kern = defer ? (const void*)accept_rows_kernel<T, true> : (const void*)accept_rows_kernel<T, false>;
   cudaError_t e = launch_rows(kern, rows, parts, sizeof(Short), a, st);
-  if (e != cudaSuccess) return e;
-  if (!defer) return cudaSuccess;
-  if ((e = launch_wide((const void*)accept_wide_kernel<T>, rows, sizeof(Short), a, st)) != cudaSuccess) return e;
-  return launch_rows((const void*)accept_pick_kernel<T>, b, pick_parts(a.V, b, sizeof(T)), sizeof(Short), a, st);
+  if (e != cudaSuccess || !defer) return e;
+  return launch_wide((const void*)accept_wide_kernel<T>, rows, sizeof(Short), a, st);
 }
 template <typename T>
 cudaError_t launch_top(const FilterArgs& a, int64_t rows, cudaStream_t st) {
