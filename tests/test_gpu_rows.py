@@ -748,6 +748,49 @@ def test_other_stream_graph_and_early_launch_repeat():
     assert api.dflash_get_status() == 0
 
 
+def test_two_graphs_of_wide_rows_at_once():
+    # batches whose wide rows take a second launch, on two streams with a workspace
+    # each, replayed side by side
+    rng = np.random.default_rng(17)
+    n, b, R, V = 330, 24, 16, 90001
+    base = _padded(_logits(rng, 8, V, "flat"), "bf16", 0)
+    z = torch.stack([torch.roll(base[r % 8], 29 * r) for r in range(b * R)]).unflatten(0, (b, R))
+    zs = z.flatten(0, 1)[:n]
+    draft = z[:, :R - 1].float().argmax(2).to(torch.int32).contiguous()
+    T, k, p, mp = (_dev(a, d) for a, d in zip(_ask(rng, n, "mixed"), (np.float32, np.int32, np.float32, np.float32)))
+    u = torch.rand((n, V), generator=torch.Generator(device=DEV).manual_seed(5), device=DEV)
+    ua = _dev(_uniforms(rng, (b, R - 1)), np.float32)
+    i32 = lambda *s: torch.full(s, -7, dtype=torch.int32, device=DEV)
+    out = [dict(tok=i32(n), lp=torch.zeros(n, device=DEV), n=i32(b), c=i32(b), em=i32(b, R), nx=i32(b)) for _ in range(3)]
+    ws = [(torch.empty(api.dflash_sample_workspace_size(n, V), dtype=torch.uint8, device=DEV),
+           torch.zeros(api.dflash_verify_filtered_workspace_size(b, R, V), dtype=torch.uint8, device=DEV))
+          for _ in range(3)]
+
+    def both(x):
+        o = out[x]
+        api.dflash_sample(zs, T, u, o["tok"], top_k=k, top_p=p, min_p=mp, logprob_out=o["lp"], ws=ws[x][0])
+        api.dflash_verify_accept_filtered(z, draft, T[:b], ua, u[:b], o["n"], o["c"], top_k=k[:b], top_p=p[:b],
+                                          min_p=mp[:b], emitted=o["em"], next_tok=o["nx"], ws=ws[x][1])
+
+    both(0)
+    torch.cuda.synchronize()
+    graphs, streams = [], [torch.cuda.Stream(), torch.cuda.Stream()]
+    for x in (1, 2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            both(x)
+        graphs.append(g)
+    for _ in range(4):
+        for g, st in zip(graphs, streams):
+            with torch.cuda.stream(st):
+                g.replay()
+    torch.cuda.synchronize()
+    for x in (1, 2):
+        for a in out[0]:
+            assert torch.equal(out[0][a], out[x][a]), a
+    assert api.dflash_get_status() == 0
+
+
 def test_a_step_of_the_loop_answers_and_teaches():
     """Draft a block, score it, accept under filters, commit, and fit the
     drafter's rows to the target's: the calls as they follow one another."""
