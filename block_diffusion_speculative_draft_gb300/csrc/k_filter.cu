@@ -759,14 +759,17 @@ __device__ bool short_list(Row<T, NT>& r, Shared<NT, kCap>& s, const Scan<T, NT>
     }
     __syncthreads();
     const int b = static_cast<int>(s.pick[0]);
-    if (b < kGroupBins) {
-      if (want > 0.f && s.pick[1]) return false;
-      // its lower edge, less what the bins' arithmetic may round
-      t = per > 0.f ? r.m - (static_cast<float>(b) + 1.f) / per * 1.0001f - fabsf(r.m) * 1e-6f : low;
-    } else {
-      t = -INFINITY;  // fewer groups hold entries than the target
-      if (V > kCap) return false;
+    // the first groups hold too little, or fewer groups hold entries than the target
+    if (b < kGroupBins ? want > 0.f && s.pick[1] : V > kCap) {
+      // Peers may still be reading this CTA's bins, and its own threads its pick:
+      // nothing is written anew, and no CTA ends, before all of them are done
+      cluster_sync_all(r.size);
+      return false;
     }
+    // the bin's lower edge, less what the bins' arithmetic may round
+    t = b >= kGroupBins ? -INFINITY
+        : per > 0.f     ? r.m - (static_cast<float>(b) + 1.f) / per * 1.0001f - fabsf(r.m) * 1e-6f
+                        : low;
   }
   list_entries(r, s, sc, t, want > 0.f);
   close_list(r, s, count, mass);

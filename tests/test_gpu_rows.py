@@ -76,6 +76,8 @@ def _logits(rng, n, V, kind):
         z[2 % n, :] = -65504.0
     elif kind == "far":  # exponents far below the weights' resolution
         z *= 40
+    elif kind == "sparse":  # fewer entries than top-k asks for
+        z[rng.random((n, V)) > 20 / V] = -np.inf
     return z
 
 
@@ -185,6 +187,25 @@ def test_sample_leaves_wide_rows_to_a_second_launch(dtype, n, V, pad, kind, mode
     at = torch.from_numpy(pick).to(DEV)
     _check_sample(_host(zt[at]), u[at].cpu().numpy(), T[pick], k[pick], p[pick], mp[pick], tok[at].cpu().numpy(),
                   lp[at].cpu().numpy())
+
+
+@pytest.mark.parametrize("dtype,n,V,kind,mode,rows", [
+    ("f32", 200, 100003, "flat", "p", 12), ("f32", 200, 100003, "flat", "mixed", 16),
+    ("f32", 200, 100003, "sparse", "k", 12), ("f32", 100, 200003, "flat", "p", 8),
+    ("f32", 100, 200003, "ties", "mixed", 16), ("f32", 100, 200003, "sparse", "mixed", 16),
+    ("bf16", 160, 200003, "flat", "p", 8), ("f16", 160, 200003, "sparse", "kp", 12),
+])
+def test_sample_leaves_rows_of_clusters_to_a_second_launch(dtype, n, V, kind, mode, rows):
+    # two or four CTAs a row in the first launch, each with more than 160 KB: a CTA
+    # that gives a row up must not end while its peers read its groups
+    test_sample_leaves_wide_rows_to_a_second_launch(dtype, n, V, 0, kind, mode, rows)
+
+
+@pytest.mark.parametrize("V", [769, 900, 1024])
+@pytest.mark.parametrize("kind,mode", [("flat", "p"), ("ties", "mixed")])
+def test_sample_under_top_p_where_a_whole_row_fits_the_list(V, kind, mode):
+    # a row whose groups hold too little is given up by all of its threads or none
+    test_sample("f32", 64, V, 0, kind, mode)
 
 
 @pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
@@ -391,6 +412,16 @@ def test_accept_leaves_wide_rows_to_more_launches(dtype, b, R, D, V, kind, mode)
         assert (n[j], c[j], nx[j]) == (rn, rc, rnx) and em[j].tolist() == rem.tolist(), (j, ask)
         same += 1
     assert same >= b // 2
+
+
+@pytest.mark.parametrize("dtype,b,R,D,V,kind,mode", [
+    ("f32", 13, 16, 15, 100003, "flat", "p"), ("f32", 13, 16, 16, 100003, "sparse", "mixed"),
+    ("f32", 6, 16, 15, 200003, "flat", "mixed"), ("f32", 25, 4, 3, 200003, "sparse", "k"),
+    ("bf16", 10, 16, 15, 200003, "flat", "p"),
+])
+def test_accept_leaves_rows_of_clusters_to_more_launches(dtype, b, R, D, V, kind, mode):
+    # (as for sample: two or four CTAs a row)
+    test_accept_leaves_wide_rows_to_more_launches(dtype, b, R, D, V, kind, mode)
 
 
 def test_accept_at_zero_temperature_is_the_greedy_kernel():
