@@ -209,8 +209,9 @@ struct Row {
   }
 };
 
-// The place of the last entry kept when entries at or above `lo` are taken in
-// order until the taken ones reach `need` (by count, or by weight): a radix
+// A cut after the last entry kept when entries at or above `lo` are taken in
+// order until the taken ones reach `need` (by count, or by weight): no entry lies
+// between the two, but the cut's low bits need not be the entry's.  A radix
 // descent over the places, kDigit bits of the value key at a time and, where
 // equal values straddle the border, over the index bits.  Each level is one
 // pass over the row that adds every entry with the prefix found so far to its
@@ -311,6 +312,17 @@ __device__ __noinline__ uint64_t find_cut(Row<T, NT>& r, Shared<NT, kCap>& s, ui
 __device__ __forceinline__ float cut_value(uint64_t cut) {
   const uint32_t k = static_cast<uint32_t>(cut >> 32);
   return k > 0x007FFFFFu ? key_to_value(k) : -INFINITY;
+}
+
+// Place of the row's first entry.
+template <typename T, int NT, int kCap>
+__device__ uint64_t first_place(Row<T, NT>& r, Shared<NT, kCap>& s) {
+  uint64_t best = 0;
+  r.each([&](float v, int64_t i) {
+    const uint64_t c = place_of(value_key(v), static_cast<uint32_t>(i));
+    if (v == r.m && c > best) best = c;
+  });
+  return cluster_reduce<NT / 32>(best, OpMaxU64(), s.x, r.rank, r.size, r.turn);
 }
 
 // Sum of the weights at or above a cut.
@@ -896,7 +908,7 @@ __device__ int pick_listed(const Row<T, NT>& r, Shared<NT, kCap>& s, const float
 // What a list says of its row (rank 0's threads).
 struct Verdict {
   uint64_t mass;  // sum of the kept weights
-  uint64_t cut;  // place of the last entry kept
+  uint64_t cut;  // entries at or above it are kept
   int tok;       // Gumbel maximum of the kept entries but `drop` (u given)
   float val;     // its logit
 };
@@ -1634,14 +1646,18 @@ __device__ __forceinline__ int wide_row(Row<T, kThr>& r, Short& s, const FilterA
     v->cut = place_of(value_key(s.bound), 0xFFFFFFFFu);
     return u ? join_best(r, s, u, best, q.T) : -1;
   }
+  if (q.greedy) {  // the first entry of the order
+    v->cut = first_place(r, s);
+    v->mass = r.weight(r.m);
+    return u ? static_cast<int>(place_index(v->cut)) : -1;
+  }
   if (q.k >= a.V && q.p >= 1.f && q.mp == 0.f) {  // nothing filters
     v->mass = __float2ull_rn(row_mass * r.scale);
     v->cut = 1ull << 32;
   } else {
     v->cut = wide_cut(r, s, a, q, &v->mass);
   }
-  if (!u) return -1;
-  return q.greedy ? static_cast<int>(place_index(v->cut)) : pick_row(r, s, u, v->cut, -1, q.T);
+  return u ? pick_row(r, s, u, v->cut, -1, q.T) : -1;
 }
 
 template <typename T>

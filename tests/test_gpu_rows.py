@@ -312,6 +312,49 @@ def test_sample_infinite_logits_win():
     assert np.abs(lp.cpu().numpy() - [0, -math.log(2), -math.log(2)]).max() < 1e-6
 
 
+def _greedy_rows(rng, n, V, dtype):
+    """Rows whose largest entry no short list of the row's groups gives, in turn:
+    all but a few entries at the type's lowest value, one and several infinities,
+    more equal maxima than the list holds, nothing but the lowest value, a NaN and
+    infinities below the maximum; and a plain row."""
+    low = float(torch.finfo(DT[dtype]).min)
+    z = rng.normal(0, 2.0, (n, V))
+    for r in range(n):
+        some = V // 3 + rng.choice(V // 3, 5, replace=False)
+        if r % 7 == 0:
+            keep = z[r, some]
+            z[r] = low
+            z[r, some] = keep
+        elif r % 7 == 1:
+            z[r, some[0]] = np.inf
+        elif r % 7 == 2:
+            z[r, some] = np.inf
+        elif r % 7 == 3:
+            z[r, rng.integers(0, 5)::7] = 11.0
+        elif r % 7 == 4:
+            z[r] = low
+        elif r % 7 == 5:
+            z[r, some] = [np.nan, -np.inf, low, np.nan, -np.inf]
+    return z
+
+
+def _first(z):
+    return np.where(np.isnan(z), -np.inf, z).argmax(-1)
+
+
+@pytest.mark.parametrize("dtype,n,V", [("f32", 14, 20011), ("bf16", 14, 20011), ("f16", 14, 20011), ("f32", 70, 9001),
+                                       ("f32", 7, 151936), ("f32", 200, 100003), ("bf16", 330, 90001)])
+def test_sample_at_zero_temperature_takes_the_first_entry_of_any_row(dtype, n, V):
+    rng = np.random.default_rng(n)
+    base = _padded(_greedy_rows(rng, 14, V, dtype), dtype, 0)
+    zt = base[torch.arange(n, device=DEV) % 14].contiguous()
+    _, k, p, mp = _ask(rng, n, "mixed")
+    # (a row's uniforms do not matter)
+    tok, lp = _sample(zt, np.zeros(n), k, p, mp, torch.full((n, V), float("nan"), device=DEV))
+    assert api.dflash_get_status() == 0
+    assert np.array_equal(tok.cpu().numpy(), _first(_host(base))[np.arange(n) % 14]) and not lp.any()
+
+
 # --------------------------------------------------------------- accept -----
 def _accept(zt, draft, T, k, p, mp, ua, us, **kw):
     b, R, _ = zt.shape
@@ -439,6 +482,28 @@ def test_accept_at_zero_temperature_is_the_greedy_kernel():
     api.dflash_verify_accept(zt, _dev(draft, np.int32), ref[0], ref[1], em, ref[2])
     for g, r in zip(got, (ref[0], ref[1], em, ref[2])):
         assert np.array_equal(g, r.cpu().numpy())
+
+
+@pytest.mark.parametrize("dtype,b,R,V", [("f32", 7, 4, 20011), ("bf16", 7, 2, 20011), ("f32", 50, 4, 100003)])
+def test_accept_at_zero_temperature_over_any_row(dtype, b, R, V):
+    rng = np.random.default_rng(b + R)
+    base = _padded(_greedy_rows(rng, 7, V, dtype), dtype, 0)
+    at = (np.arange(b * R) % 7).reshape(b, R)
+    zt = base[torch.from_numpy(at).to(DEV)].contiguous()
+    first = _first(_host(base))[at]
+    draft = first[:, :R - 1].copy()
+    stop = np.arange(b) % R
+    for j in range(b):
+        if stop[j] < R - 1:
+            draft[j, stop[j]] = (draft[j, stop[j]] + 1) % V
+    _, k, p, mp = _ask(rng, b, "mixed")
+    n, c, em, nx = _accept(zt, draft, np.zeros(b), k, p, mp, _uniforms(rng, (b, R - 1)),
+                           _dev(_uniforms(rng, (b, V)), np.float32))
+    assert api.dflash_get_status() == 0
+    for j in range(b):
+        rest = first[j, stop[j]]
+        assert (n[j], c[j], nx[j]) == (stop[j], rest, rest)
+        assert em[j].tolist() == first[j, :stop[j]].tolist() + [rest] + [-1] * (R - 1 - stop[j])
 
 
 def test_accept_refuses_one_sequence_and_serves_the_others():
