@@ -433,7 +433,8 @@ def dflash_verify_accept_filtered(logits, draft, temperature, u_accept, u_sample
     min_p fp32 [b], top_k int32 [b], u_accept fp32 [b][D], u_sample fp32
     [b][V]; n_out, corr_out, next_tok int32 [b], emitted int32 [b][R].  ws:
     zero-filled uint8 workspace of dflash_verify_filtered_workspace_size bytes
-    (allocated here when not given)."""
+    or more, which may serve batches of any shape one after another (allocated
+    here when not given)."""
     fn = "dflash_verify_accept_filtered"
     dt = _row_dtype(fn, logits)
     ld = _row_shape(fn, logits, 3)

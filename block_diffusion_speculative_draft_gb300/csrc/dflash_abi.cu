@@ -574,7 +574,6 @@ int32_t dflash_verify_accept_filtered(const void* logits, int32_t dtype, int64_t
   a.draft = draft;
   a.u_accept = u_accept;
   a.cuts = static_cast<RowCut*>(ws);
-  a.tickets = reinterpret_cast<int*>(static_cast<uint8_t*>(ws) + accept_cuts_bytes(b, R));
   a.n_out = n_out;
   a.corr_out = corr_out;
   a.emitted = emitted_out;

@@ -1831,11 +1831,14 @@ __device__ __forceinline__ void write_sequence(const FilterArgs& a, int64_t j, i
 }
 
 // One thread, after its row's result is written: whether it was the sequence's
-// last (then the ticket starts anew).
+// last (then the ticket starts anew).  A ticket lies in the record of its
+// sequence's first row, where no batch of another shape over the same workspace
+// writes anything else.
 __device__ __forceinline__ bool finishes(const FilterArgs& a, int64_t j) {
   __threadfence();
-  if (atomicAdd(&a.tickets[j], 1) != a.rows_used - 1) return false;
-  a.tickets[j] = 0;
+  int* ticket = &a.cuts[j * a.R].ticket;
+  if (atomicAdd(ticket, 1) != a.rows_used - 1) return false;
+  *ticket = 0;
   __threadfence();
   return true;
 }
@@ -1862,7 +1865,13 @@ __global__ void __launch_bounds__(kThr, 4) accept_rows_kernel(const FilterArgs a
   scan_row(r, want_mass, sc);
   float low, row_mass;
   const bool some = join_scan(r, s, sc, want_mass, &low, &row_mass);
-  RowCut out{~0ull, r.m, 0, -1, 0, row_mass, 0};
+  RowCut out;
+  out.cut = ~0ull;
+  out.m = r.m;
+  out.accept = 0;
+  out.tok = -1;
+  out.left = 0;
+  out.mass = row_mass;
   if (q.ok && some) {
     const int drop = rr < a.D ? a.draft[j * a.D + rr] : -1;
     const float* u = a.u + j * a.ld_u;
@@ -1898,7 +1907,13 @@ __global__ void __launch_bounds__(kThr, 4) accept_rows_kernel(const FilterArgs a
   }
   if (r.rank != 0) return;
   if (threadIdx.x == 0) {
-    a.cuts[row] = out;
+    RowCut& c = a.cuts[row];  // (all but the ticket)
+    c.cut = out.cut;
+    c.m = out.m;
+    c.accept = out.accept;
+    c.tok = out.tok;
+    c.left = out.left;
+    c.mass = out.mass;
     s.taken = !out.left && finishes(a, j);
   }
   __syncthreads();

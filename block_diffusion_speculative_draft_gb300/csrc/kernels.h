@@ -212,14 +212,14 @@ cudaError_t verify_accept(const float* logits, const int* draft, int b, int R, i
 constexpr float kFilterMinT = 1e-6f, kFilterMaxT = 1e6f;  // sampling temperatures (0: greedy)
 constexpr int kTopLogitsMax = 1024;
 constexpr int kInlineRows = 64;  // up to so many sampled rows need no state between launches
-struct RowCut {  // one verified row
+struct RowCut {  // one verified row; the workspace of every call is a run of these
   uint64_t cut;  // an entry is kept iff its place is at or above it
   float m;       // the row's maximum
   int accept;    // the row's draft token is accepted
   int tok;       // the token drawn where it is not; -2: still to be drawn
   int left;      // the row is left to the second launch
   float mass;    // its sum of weights, for that
-  int pad;
+  int ticket;    // rows done of the sequence that starts here; zero between calls
 };
 struct RowState {  // one sampled row between its launches
   float m, mass;   // the row's maximum and sum of weights
@@ -243,7 +243,6 @@ struct FilterArgs {
   const int* draft;
   const float* u_accept;
   RowCut* cuts;
-  int* tickets;    // [b], zero between calls
   int* n_out;
   int* corr_out;
   int* emitted;
@@ -258,8 +257,7 @@ struct FilterArgs {
   float unit;      // 1 / scale
 };
 cudaError_t filter_sample(FilterArgs a, int dtype, int64_t rows, cudaStream_t st);
-inline size_t accept_cuts_bytes(int64_t b, int R) { return (size_t)b * R * sizeof(RowCut); }
-inline size_t accept_ws_bytes(int64_t b, int R) { return accept_cuts_bytes(b, R) + (size_t)b * sizeof(int); }
+inline size_t accept_ws_bytes(int64_t b, int R) { return (size_t)b * R * sizeof(RowCut); }
 cudaError_t filter_accept(FilterArgs a, int dtype, int64_t b, cudaStream_t st);
 cudaError_t top_logits(FilterArgs a, int dtype, int64_t rows, cudaStream_t st);
 

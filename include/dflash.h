@@ -404,7 +404,9 @@ DFLASH_API int32_t dflash_verify_filtered_workspace_size(int32_t b, int32_t R, i
  * apart) are uniforms in [0, 1).  A sequence with a parameter out of range gets
  * n = -1 (a commit of which appends nothing), corr and next_tok -1, and sets
  * DFLASH_DEV_BAD_PARAM.  ws holds dflash_verify_filtered_workspace_size bytes,
- * 16-byte aligned, zero-filled once (every call leaves its counters zero). */
+ * 16-byte aligned, zero-filled once (every call leaves its counters zero).  It
+ * may be larger, and serve batches of other b, R and D, one call at a time; no
+ * other function may write to it in between. */
 DFLASH_API int32_t dflash_verify_accept_filtered(const void* logits, int32_t dtype, int64_t ld, const int32_t* draft,
                                                  int32_t b, int32_t R, int32_t D, int64_t V,
                                                  const float* temperature, const int32_t* top_k, const float* top_p,

@@ -520,6 +520,31 @@ def test_accept_refuses_one_sequence_and_serves_the_others():
         assert n[j] == RO.verify_accept_filtered(z[j].astype(np.float32), draft[j], np.float32(0.7), ua[j], us[j])[0]
 
 
+@pytest.mark.parametrize("V", [3001, 40001])
+def test_accept_reuses_one_workspace_for_batches_of_any_shape(V):
+    # sequences come and go, blocks grow and shrink: one workspace of the largest
+    # size, against a fresh one each; what lies behind it stays
+    rng = np.random.default_rng(V)
+    shapes = [(8, 16, 15), (4, 16, 15), (8, 16, 16), (1, 64, 63), (64, 2, 1), (3, 5, 5), (128, 1, 1), (5, 7, 3),
+              (16, 8, 7), (2, 64, 40), (8, 16, 15)]
+    size = max(api.dflash_verify_filtered_workspace_size(b, R, V) for b, R, _ in shapes)
+    ws = torch.zeros(size + 64, dtype=torch.uint8, device=DEV)
+    ws[size:] = 0x5A
+    for b, R, D in shapes:
+        z = _logits(rng, b * R, V, "peaked" if R % 2 else "flat").reshape(b, R, V)
+        zt = _padded(z, "bf16", 0)
+        draft = zt[:, :D].float().argmax(2).cpu().numpy()
+        for j in range(b):
+            draft[j, rng.integers(0, D)] = rng.integers(-1, V)
+        T, k, p, mp = _ask(rng, b, "mixed")
+        ua, us = _uniforms(rng, (b, D)) * np.float32(0.25), _dev(_uniforms(rng, (b, V)), np.float32)
+        got = _accept(zt, draft, T, k, p, mp, ua, us, ws=ws)
+        fresh = _accept(zt, draft, T, k, p, mp, ua, us)
+        for x, y in zip(got, fresh):
+            assert np.array_equal(x, y) and not (x == -7).any(), (b, R, D)
+    assert api.dflash_get_status() == 0 and bool((ws[size:] == 0x5A).all())
+
+
 # ------------------------------------------------------------ top logits ----
 @pytest.mark.parametrize("dtype,n,V,pad,K,kind", [
     ("f32", 3, 1, 0, 1, "peaked"), ("f16", 3, 5, 1, 8, "ties"), ("bf16", 5, 33, 0, 33, "ties"),
