@@ -6,7 +6,8 @@
 //   q = softmax(z / T);   p_k = exp(t_k / T - Lt)
 //   Lt = log sum_k exp(t_k / T), or the caller's log-sum-exp over the whole
 //   vocabulary; then p_r = max(0, 1 - sum_k p_k) is the teacher's probability
-//   of every other token together, and q_r = sum of q outside S
+//   of every other token together, and q_r = sum of q outside S; a p_r that the
+//   rounding of the log-sum-exp explains counts as 0 where q_r does (rest_of)
 //   KL = sum_k p_k (ln p_k - ln q_{i_k}) + p_r (ln p_r - ln q_r)
 //   dKL/dz_j = (P q_j - p_j) / T                     j in S, P = sum p + p_r
 //            = exp(z_j / T) (P / E' - p_r / E'_r) / T  outside, E' and E'_r
@@ -34,6 +35,10 @@ namespace {
 constexpr int kDevBadToken = 0x2;
 constexpr float kMassOne = 1099511627776.f;  // 2^40: probabilities are summed as integers
 constexpr float kLn2 = 0.6931471805599453f;
+// A log-sum-exp in fp32 is off by its rounding, 2^-24 of its size, and by its
+// sum's, some 12 2^-24 (exponentials to 2^-22, the scaled logits' own rounding): a
+// p_r up to 2^-20 (1 + |t_lse|) may be nothing else.
+constexpr float kFaintRest = 9.5367431640625e-07f;
 
 // What a part of a row contributes: the entries outside S (maximum and sum of
 // 2^((z - maximum) c)), those listed in it (the same, sum p_k (ln p_k - (z_k -
@@ -112,7 +117,8 @@ __device__ __forceinline__ Pair over_t(const DistillArgs& a, float v) {
 struct Teacher {
   bool some;   // an entry above -inf is listed
   bool bad;    // refused by this CTA's view of the row
-  float P;     // sum p + p_r
+  bool faint;  // p_r is within the rounding of t_lse
+  float mass;  // sum p
   float pr;
 };
 
@@ -194,9 +200,9 @@ __device__ __forceinline__ Teacher read_teacher(const DistillArgs& a, int64_t ro
   for (int w = 0; w < used; ++w) fixed += s.mass[w];
   // in units of 2^-40: one minus the sum, exactly
   const int64_t rest = (static_cast<int64_t>(1) << 40) - static_cast<int64_t>(fixed);
-  const float mass = static_cast<float>(fixed) * (1.f / kMassOne);
+  t.mass = static_cast<float>(fixed) * (1.f / kMassOne);
   t.pr = a.t_lse && rest > 0 ? static_cast<float>(rest) * (1.f / kMassOne) : 0.f;
-  t.P = mass + t.pr;
+  t.faint = t.pr <= kFaintRest * (1.f + fabsf(lt));
   return t;
 }
 
@@ -269,6 +275,14 @@ struct RowSums {
   float m, E, mr, Er;
 };
 
+// p_r where it counts: a faint one meets no q_r below fp32's range, of a row whose
+// unmasked tokens are all listed, say.  It would weigh ln q_r, as large as
+// the mask is low, or infinite, by a rounding.
+__device__ __forceinline__ float rest_of(const DistillArgs& a, const RowSums& r, const Teacher& t) {
+  if (!t.faint) return t.pr;
+  return log2f(r.Er) + log2_weight(r.mr, r.m, a.c) - log2f(r.E) < -126.f ? 0.f : t.pr;
+}
+
 // What the gradient pass needs of a row, worked out once per CTA.
 template <int NW>
 __device__ __forceinline__ void make_plan(const DistillArgs& a, Shared<NW>& s, const RowSums& r, const Teacher& t, float w) {
@@ -277,9 +291,10 @@ __device__ __forceinline__ void make_plan(const DistillArgs& a, Shared<NW>& s, c
   s.plan.g = g;
   s.plan.mr = r.mr;
   s.plan.m = r.m;
-  s.plan.in = t.P / r.E;
+  const float pr = rest_of(a, r, t), P = t.mass + pr;
+  s.plan.in = P / r.E;
   // factor of the weights outside S, in the form of with_weight
-  const float f = r.Er > 0.f ? g * (t.P * exp2f(log2_weight(r.mr, r.m, a.c)) / r.E - t.pr / r.Er) : 0.f;
+  const float f = r.Er > 0.f ? g * (P * exp2f(log2_weight(r.mr, r.m, a.c)) / r.E - pr / r.Er) : 0.f;
   s.plan.f = f * exp2f(lead(r.mr, a.c));
 }
 
@@ -315,7 +330,8 @@ __device__ __forceinline__ void join_parts(const DistillArgs& a, int64_t row, co
   if (lane != 0) return;
   const bool out = bad || w == 0.f || !t.some;
   if (part == 0) {
-    if (t.pr > 0.f) l += t.pr * (logf(t.pr) - (log2f(r.Er) + log2_weight(r.mr, r.m, a.c) - log_e) * kLn2);
+    const float pr = rest_of(a, r, t);
+    if (pr > 0.f) l += pr * (logf(pr) - (log2f(r.Er) + log2_weight(r.mr, r.m, a.c) - log_e) * kLn2);
     a.loss[row] = out ? (bad ? NAN : 0.f) : w * l;
     if (a.stats) a.stats[row] = out ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(r.m, r.E, r.mr, r.Er);
     if (bad) atomicOr(a.status, kDevBadToken);

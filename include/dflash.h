@@ -431,7 +431,9 @@ DFLASH_API int32_t dflash_top_logits(const void* logits, int32_t dtype, int64_t 
  *   Lt = log sum_k exp(t_val[k] / T) when t_lse is null, else t_lse[row], the
  *     log-sum-exp of the teacher's whole row at this T; then the tokens outside
  *     S count as one entry with p_r = max(0, 1 - sum_k p_k) and q_r = their sum
- *     of q (without t_lse: p_r = 0)
+ *     of q (without t_lse: p_r = 0).  Where q_r is below 2^-126 (S holds every
+ *     token, or the student masks the others) a p_r up to 2^-20 (1 + |t_lse|),
+ *     which the rounding of t_lse explains, counts as 0
  *   loss = weight * [sum_k p_k (ln p_k - ln q_{t_idx[k]}) + p_r (ln p_r - ln q_r)]
  *   dlogits[j] = weight / T * (P q_j - p_j) for j in S, and
  *                weight / T * q_j (P - p_r / q_r) outside, P = sum_k p_k + p_r
@@ -448,8 +450,8 @@ DFLASH_API int32_t dflash_top_logits(const void* logits, int32_t dtype, int64_t 
  *  - A row with an index listed twice, or outside [-1, V), is refused: loss
  *    NaN, gradient 0, DFLASH_DEV_BAD_TOKEN set.
  *  - A student row without a logit above -inf has no distribution: loss NaN,
- *    gradient undefined.  The loss is +inf where p_k > 0 meets a q below fp32's
- *    range of logarithms (a -inf logit, or one 3e38 T below the others).
+ *    gradient undefined.  The loss is +inf where a p_k or p_r above 0 meets a q
+ *    below fp32's range of logarithms (a -inf logit, or one 3e38 T below the others).
  *  - t_lse has to be finite in rows that are not left out.
  * No workspace. */
 DFLASH_API int32_t dflash_distill_loss(const void* logits, int32_t dtype, int64_t rows, int64_t V, int64_t ld,

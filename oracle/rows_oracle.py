@@ -133,6 +133,8 @@ def distill(z, t_val, t_idx, T: float = 1.0, t_lse: Optional[float] = None, weig
     outside[ids] = False
     pr = 0.0 if t_lse is None else max(0.0, 1.0 - p.sum())
     Lr = _lse(zt[outside])
+    if t_lse is not None and pr <= 2.0 ** -20 * (1 + abs(t_lse)) and Lr - L < -126 * math.log(2):
+        pr = 0.0  # no more than t_lse's rounding, over tokens that the student leaves out
     if pr > 0:
         loss += pr * (math.log(pr) - (Lr - L))
     P = p.sum() + pr

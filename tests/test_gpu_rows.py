@@ -809,6 +809,57 @@ def test_distill_keeps_the_rest_when_the_student_is_sure():
     assert np.abs(_host(dz)[0][100] / rg[100] - 1) < 2e-5
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("V,K,mask", [(5003, 64, -np.inf), (151936, 64, -np.inf), (5003, 64, -1e9), (5003, 64, None),
+                                      (50, 50, -np.inf), (30, 64, 0.0), (5003, 64, -60.0)])
+def test_distill_from_a_teacher_whose_tokens_are_all_listed(dtype, V, K, mask):
+    """30 allowed tokens a row, K no less, the others masked in teacher and
+    student alike (None: the type's lowest value; -60: not quite): p_r is nothing
+    but the rounding of the log-sum-exp."""
+    if mask is None or (dtype == "f16" and np.isfinite(mask) and mask < -65504):
+        mask = float(torch.finfo(DT[dtype]).min)
+    rng = np.random.default_rng(V)
+    n, T = 48, float(np.float32(0.8))
+    teacher, z = np.full((n, V), mask), np.full((n, V), mask)
+    for r in range(n):
+        at = rng.choice(V, 30, replace=False)
+        teacher[r, at] = 15 + rng.normal(0, 3, 30)
+        z[r, at] = 8 + rng.normal(0, 2, 30)
+    tt, zt = _padded(teacher, dtype, 0), _padded(z, dtype, 1)
+    val, idx, lse = torch.empty((n, K), device=DEV), torch.empty((n, K), dtype=torch.int32, device=DEV), torch.empty(n, device=DEV)
+    loss, stats = torch.empty(n, device=DEV), torch.empty((n, 4), device=DEV)
+    dz, back = (torch.empty((n, V), dtype=DT[dtype], device=DEV) for _ in range(2))
+    api.dflash_top_logits(tt, K, val, idx, lse_out=lse, temperature=T)
+    api.dflash_distill_loss(zt, val, idx, loss, t_lse=lse, temperature=T, dlogits=dz, stats_out=stats)
+    api.dflash_distill_backward(zt, val, idx, stats, torch.ones(n, device=DEV), back, t_lse=lse, temperature=T)
+    assert api.dflash_get_status() == 0
+    tv, ti, tl, zh = val.cpu().numpy(), idx.cpu().numpy(), lse.cpu().numpy(), _host(zt)
+    l, g, positive = loss.cpu().numpy(), _host(dz), 0
+    assert torch.equal(dz, back) and np.isfinite(l).all() and np.isfinite(g).all()
+    for r in range(n):
+        rl, rg = RO.distill(zh[r], tv[r], ti[r], T, float(tl[r]))
+        on = ti[r] >= 0
+        lp = tv[r][on].astype(np.float64) / T - float(tl[r])
+        positive += np.exp(lp).sum() < 1
+        some = lp > -80  # (those below weigh nothing)
+        lq = zh[r][ti[r][on]][some] / T - RO._lse(zh[r] / T)
+        # (the docstring's bound; a p_r of up to 2^-20 (1 + |t_lse|) carries some 2^-22
+        # of error, which ln q_r, -60 / T or so where it counts, scales)
+        tol = (1 + max(np.abs(lp[some]).max(), np.abs(lq).max())) * 2.0 ** -20 + (100 * 2.0 ** -22 if mask == -60.0 else 0)
+        assert abs(l[r] - rl) <= tol, (r, l[r], rl)
+        _, tol_g, eps, step = _tolerances(zh[r], tv[r], ti[r], T, float(tl[r]), 1.0, dtype)
+        assert np.all(np.abs(g[r] - rg) <= tol_g + (np.abs(rg) + tol_g) * eps + step), r
+    assert positive > 0
+    # a p_r above the rounding still meets what the student leaves out
+    api.dflash_distill_loss(zt, val, idx, loss, t_lse=lse + 0.01, temperature=T)
+    for r in range(n):
+        rl = RO.distill(zh[r], tv[r], ti[r], T, float((lse + 0.01)[r]))[0]
+        if rl < 1e34:  # (p_r, a difference from one, is good to 2^-22 of 0.01)
+            assert abs(float(loss[r]) - rl) <= 1e-4 * (1 + abs(rl)), (r, float(loss[r]), rl)
+        else:  # (log-probabilities below fp32's range count as -inf)
+            assert float(loss[r]) > 0.999 * min(rl, 3e38), r
+
+
 # ------------------------------------------------------------- as a whole ----
 def test_other_stream_graph_and_early_launch_repeat():
     rng = np.random.default_rng(13)

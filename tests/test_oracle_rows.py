@@ -133,3 +133,26 @@ def test_distill_rows_left_out_and_refused():
     for ids in ([1, 1], [4, 0], [-2, 0]):
         loss, g = RO.distill(z, [1.0, 2.0], ids)
         assert math.isnan(loss) and not g.any()
+
+
+def test_distill_ignores_a_rest_that_rounding_explains():
+    # 30 allowed tokens, all listed, log-sum-exp in fp32: about half of the rows
+    # leave a p_r above 0 that meets a student without the other tokens
+    rng = np.random.default_rng(5)
+    positive = 0
+    for _ in range(50):
+        t, z = np.full(100, -np.inf), np.full(100, -np.inf)
+        at = rng.choice(100, 30, replace=False)
+        t[at], z[at] = rng.normal(15, 3, 30), rng.normal(0, 1, 30)
+        val, idx, lse = RO.top_logits(t, 64)
+        lse = float(np.float32(lse))
+        positive += np.exp(val - lse).sum() < 1
+        whole, gw = RO.distill(z, val, idx)
+        loss, g = RO.distill(z, val, idx, t_lse=lse)
+        # sum p differs from 1 by 2^-19 at most, and ln p by as much
+        assert abs(loss - whole) < 2.0 ** -19 * (2 + abs(whole)) and np.abs(g - gw).max() < 2.0 ** -18
+        z[np.isinf(z)] = -1e9
+        assert abs(RO.distill(z, val, idx, t_lse=lse)[0] - loss) < 1e-12
+        z[np.abs(z) > 1e8] = -np.inf
+        assert RO.distill(z, val, idx, t_lse=lse + 0.01)[0] == math.inf
+    assert 5 < positive < 45
