@@ -32,7 +32,8 @@ namespace dfl {
 
 namespace {
 
-constexpr int kDevBadToken = 0x2;
+constexpr int kDevBadToken = 0x2, kDevBadParam = 0x8;  // why a row is refused
+constexpr int kSome = 0x1;  // beside them: an entry above -inf is listed
 constexpr float kMassOne = 1099511627776.f;  // 2^40: probabilities are summed as integers
 constexpr float kLn2 = 0.6931471805599453f;
 // A log-sum-exp in fp32 is off by its rounding, 2^-24 of its size, and by its
@@ -42,11 +43,11 @@ constexpr float kFaintRest = 9.5367431640625e-07f;
 
 // What a part of a row contributes: the entries outside S (maximum and sum of
 // 2^((z - maximum) c)), those listed in it (the same, sum p_k (ln p_k - (z_k -
-// maximum) / T) and sum p_k), and whether it refuses the row.  Without an entry
-// above -inf the maximum is -inf and the sum 0.
+// maximum) / T) and sum p_k), and its CTA's flags.  Without an entry above -inf the
+// maximum is -inf and the sum 0.
 struct PartSums {
   float top, sum, ltop, lsum, self, p;
-  int bad;
+  int flags;
 };
 
 // Shared memory of one CTA: this header, the teacher's entries (four arrays of
@@ -61,7 +62,7 @@ struct alignas(16) Shared {
     float f, mr, g, in, m;  // factor and maximum outside S, weight / T, P / E and the row's maximum
     int zero;                // no gradient
   } plan;
-  int flags;  // 1: refused, 2: an entry above -inf
+  int flags;  // reasons to refuse the row, and kSome
 };
 
 struct Entries {
@@ -115,17 +116,22 @@ __device__ __forceinline__ Pair over_t(const DistillArgs& a, float v) {
 }
 
 struct Teacher {
-  bool some;   // an entry above -inf is listed
-  bool bad;    // refused by this CTA's view of the row
+  int flags;   // this CTA's view of the row: reasons to refuse it, and kSome
   bool faint;  // p_r is within the rounding of t_lse
   float mass;  // sum p
   float pr;
 };
 
+// Why a row of weight w is refused (0: it is not).
+__device__ __forceinline__ int reasons(int flags, float w) {
+  return flags & (w != 0.f ? kDevBadToken | kDevBadParam : kDevBadToken);
+}
+
 // Reads the row's entries, with the student's logits at those of this part, and
 // forms the teacher's probabilities.  `bits` (zero) marks the part's listed
 // elements; a mark that is there already, or a token out of range, refuses the
-// row.
+// row; a logit that is NaN or +inf, or a t_lse that is not finite, does so unless
+// the row's weight leaves it out (reasons).
 template <typename T, int NT>
 __device__ __forceinline__ Teacher read_teacher(const DistillArgs& a, int64_t row, const Part<T>& q, Entries e,
                                                 uint32_t* bits, Shared<NT / 32>& s) {
@@ -133,7 +139,7 @@ __device__ __forceinline__ Teacher read_teacher(const DistillArgs& a, int64_t ro
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const bool holds = warp * 32 < a.K;  // this warp holds entries
   const int used = a.K < NT ? (a.K + 31) / 32 : NW;
-  bool bad = false;
+  int flags = 0;
   float tm = -INFINITY;
   float lt = a.t_lse ? a.t_lse[row] : 0.f;
   for (int k = threadIdx.x; k < a.K; k += NT) {
@@ -141,10 +147,11 @@ __device__ __forceinline__ Teacher read_teacher(const DistillArgs& a, int64_t ro
     const float v = a.t_val[row * a.K + k];
     const int64_t at = i - q.first;
     const bool in = i >= 0 && i < a.V, own = in && at >= 0 && at < q.n;
-    bad |= !in && i != -1;
+    if (!in && i != -1) flags |= kDevBadToken;
+    if (in && !(v < INFINITY)) flags |= kDevBadParam;
     if (own) {
       const uint32_t x = static_cast<uint32_t>(q.off + at), bit = 1u << (x & 31);
-      bad |= (atomicOr(&bits[x >> 5], bit) & bit) != 0;
+      if (atomicOr(&bits[x >> 5], bit) & bit) flags |= kDevBadToken;
       e.z[k] = to_f32(q.row[i]);
     }
     e.at[k] = own ? static_cast<int>(at) : -1;
@@ -191,11 +198,11 @@ __device__ __forceinline__ Teacher read_teacher(const DistillArgs& a, int64_t ro
     for (int o = 16; o > 0; o >>= 1) fixed += __shfl_xor_sync(0xffffffffu, fixed, o);
   }
   if (lane == 0) s.mass[warp] = fixed;
-  if (bad || tm > -INFINITY) atomicOr(&s.flags, (bad ? 1 : 0) | (tm > -INFINITY ? 2 : 0));
+  if (tm > -INFINITY) flags |= kSome | (fabsf(lt) < INFINITY ? 0 : kDevBadParam);
+  if (flags) atomicOr(&s.flags, flags);
   __syncthreads();
   Teacher t;
-  t.bad = s.flags & 1;
-  t.some = s.flags & 2;
+  t.flags = s.flags;
   fixed = 0;
   for (int w = 0; w < used; ++w) fixed += s.mass[w];
   // in units of 2^-40: one minus the sum, exactly
@@ -232,7 +239,7 @@ __device__ __forceinline__ float2 part_tops(int K, float top, Entries e, Shared<
 // Adds up a part (`sum`: this thread's outside S) and sends it to every CTA of
 // the cluster; complete after a cluster barrier.
 template <int NW>
-__device__ __forceinline__ void send_part(const DistillArgs& a, float2 tops, float sum, bool bad, Entries e,
+__device__ __forceinline__ void send_part(const DistillArgs& a, float2 tops, float sum, int flags, Entries e,
                                           Shared<NW>& s, int part, int parts) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   float4 v = make_float4(sum, 0.f, 0.f, 0.f);  // sum, lsum, self, p
@@ -265,7 +272,7 @@ __device__ __forceinline__ void send_part(const DistillArgs& a, float2 tops, flo
       v.z += __shfl_xor_sync(0xffffffffu, v.z, o);
       v.w += __shfl_xor_sync(0xffffffffu, v.w, o);
     }
-    if (lane < parts) *peer(&s.part[part], lane) = PartSums{tops.x, v.x, tops.y, v.y, v.z, v.w, bad};
+    if (lane < parts) *peer(&s.part[part], lane) = PartSums{tops.x, v.x, tops.y, v.y, v.z, v.w, flags};
   }
 }
 
@@ -283,15 +290,16 @@ __device__ __forceinline__ float rest_of(const DistillArgs& a, const RowSums& r,
   return log2f(r.Er) + log2_weight(r.mr, r.m, a.c) - log2f(r.E) < -126.f ? 0.f : t.pr;
 }
 
-// What the gradient pass needs of a row, worked out once per CTA.
+// What the gradient pass needs of a row of weight w whose rest counts pr, worked
+// out once per CTA.
 template <int NW>
-__device__ __forceinline__ void make_plan(const DistillArgs& a, Shared<NW>& s, const RowSums& r, const Teacher& t, float w) {
+__device__ __forceinline__ void make_plan(const DistillArgs& a, Shared<NW>& s, const RowSums& r, const Teacher& t, float w, float pr) {
   const float g = w * a.inv_hi;
   s.plan.zero = r.E == 0.f;
   s.plan.g = g;
   s.plan.mr = r.mr;
   s.plan.m = r.m;
-  const float pr = rest_of(a, r, t), P = t.mass + pr;
+  const float P = t.mass + pr;
   s.plan.in = P / r.E;
   // factor of the weights outside S, in the form of with_weight
   const float f = r.Er > 0.f ? g * (P * exp2f(log2_weight(r.mr, r.m, a.c)) / r.E - pr / r.Er) : 0.f;
@@ -305,7 +313,7 @@ __device__ __forceinline__ void join_parts(const DistillArgs& a, int64_t row, co
                                            Shared<NW>& s, int part, int parts) {
   const int lane = threadIdx.x & 31;
   const PartSums q = lane < parts ? s.part[lane] : PartSums{-INFINITY, 0.f, -INFINITY, 0.f, 0.f, 0.f, 0};
-  const bool bad = __any_sync(0xffffffffu, q.bad != 0);
+  const int bad = reasons(__reduce_or_sync(0xffffffffu, q.flags), w);
   RowSums r;
   r.mr = q.top;
   r.m = fmaxf(q.top, q.ltop);
@@ -328,16 +336,16 @@ __device__ __forceinline__ void join_parts(const DistillArgs& a, int64_t row, co
 #pragma unroll
   for (int o = kMaxCluster / 2; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
   if (lane != 0) return;
-  const bool out = bad || w == 0.f || !t.some;
+  const float pr = rest_of(a, r, t);
+  const bool out = bad || w == 0.f || !(t.flags & kSome);
   if (part == 0) {
-    const float pr = rest_of(a, r, t);
     if (pr > 0.f) l += pr * (logf(pr) - (log2f(r.Er) + log2_weight(r.mr, r.m, a.c) - log_e) * kLn2);
     a.loss[row] = out ? (bad ? NAN : 0.f) : w * l;
     if (a.stats) a.stats[row] = out ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(r.m, r.E, r.mr, r.Er);
-    if (bad) atomicOr(a.status, kDevBadToken);
+    if (bad) atomicOr(a.status, bad);
   }
   if (out) r.E = 0.f;
-  make_plan(a, s, r, t, w);
+  make_plan(a, s, r, t, w, pr);
 }
 
 // Gradients of the part's listed entries; out: its first entry's.
@@ -515,14 +523,16 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 5 : 1) distill_kernel(const Di
     const float2 tops = part_tops<NW>(a.K, top, e, s);
     if (top > -INFINITY) sum *= fast_exp2(log2_weight(top, tops.x, a.c) + lead(top, a.c));
     if (parts > 1) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");  // the other CTAs have started
-    send_part<NW>(a, tops, sum, t.bad, e, s, part, parts);
+    send_part<NW>(a, tops, sum, t.flags, e, s, part, parts);
     cluster_sync_all(parts);
     if (threadIdx.x < 32) join_parts<NW>(a, row, t, w, s, part, parts);
     if (!dz) return;
   } else if (threadIdx.x == 0) {
-    if (t.bad) atomicOr(a.status, kDevBadToken);
+    const int bad = reasons(t.flags, w);
+    if (bad) atomicOr(a.status, bad);
     const float4 st = a.stats[row];
-    make_plan(a, s, RowSums{st.x, t.bad || w == 0.f ? 0.f : st.y, st.z, st.w}, t, w);
+    const RowSums r{st.x, bad || w == 0.f ? 0.f : st.y, st.z, st.w};
+    make_plan(a, s, r, t, w, rest_of(a, r, t));
   }
   __syncthreads();
   if (s.plan.zero) {  // left out or refused

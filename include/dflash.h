@@ -67,8 +67,8 @@ typedef enum dflash_status {
 #define DFLASH_DEV_KV_CAPACITY 0x1 /* a commit would pass `cap`: skipped   */
 #define DFLASH_DEV_BAD_TOKEN 0x2   /* a token id outside [0, V): row zeroed */
 #define DFLASH_DEV_BAD_LENGTH 0x4  /* len < 0 or n outside [-1, B]         */
-#define DFLASH_DEV_BAD_PARAM 0x8   /* a row's temperature, top_k, top_p or
-                                      min_p outside its range              */
+#define DFLASH_DEV_BAD_PARAM 0x8   /* a row's temperature, top_k, top_p, min_p
+                                      or teacher's value outside its range  */
 
 /* Element types accepted by dflash_pack_w8a16 and by the calls on logits that
  * take a dtype. */
@@ -448,11 +448,12 @@ DFLASH_API int32_t dflash_top_logits(const void* logits, int32_t dtype, int64_t 
  *  - A row with weight 0, or whose teacher lists nothing above -inf, is left
  *    out: loss 0, gradient 0, its student logits do not matter.
  *  - A row with an index listed twice, or outside [-1, V), is refused: loss
- *    NaN, gradient 0, DFLASH_DEV_BAD_TOKEN set.
+ *    NaN, gradient 0, DFLASH_DEV_BAD_TOKEN set.  So is one that is not left out
+ *    and has a listed t_val that is NaN or +inf, or a t_lse that is not finite
+ *    (of a teacher's row with a +inf logit, say): DFLASH_DEV_BAD_PARAM set.
  *  - A student row without a logit above -inf has no distribution: loss NaN,
  *    gradient undefined.  The loss is +inf where a p_k or p_r above 0 meets a q
  *    below fp32's range of logarithms (a -inf logit, or one 3e38 T below the others).
- *  - t_lse has to be finite in rows that are not left out.
  * No workspace. */
 DFLASH_API int32_t dflash_distill_loss(const void* logits, int32_t dtype, int64_t rows, int64_t V, int64_t ld,
                                        const float* t_val, const int32_t* t_idx, int32_t K, const float* t_lse,

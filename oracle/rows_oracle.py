@@ -118,8 +118,14 @@ def distill(z, t_val, t_idx, T: float = 1.0, t_lse: Optional[float] = None, weig
     if np.any((ids < 0) | (ids >= V)) or np.unique(ids).size != ids.size:
         return math.nan, np.zeros(V)
     t = t_val[listed] / T
-    if weight == 0 or not np.any(t > -np.inf):
+    if weight == 0:
         return 0.0, np.zeros(V)
+    if np.any(np.isnan(t) | (t == np.inf)):
+        return math.nan, np.zeros(V)
+    if not np.any(t > -np.inf):
+        return 0.0, np.zeros(V)
+    if t_lse is not None and not math.isfinite(t_lse):
+        return math.nan, np.zeros(V)
     m = z.max() if np.isfinite(z.max()) else 0.0  # softmax does not see a shift; sums keep their precision
     zt = (z - m) / T
     L = _lse(zt)

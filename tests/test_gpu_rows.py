@@ -737,6 +737,52 @@ def test_distill_rows_left_out_and_refused():
     assert not back[:6].any() and np.abs(back[7].cpu().numpy() - rg).max() < 1e-6
 
 
+@pytest.mark.parametrize("V", [1000, 40011])
+def test_distill_refuses_a_teacher_that_is_no_number(V):
+    K, n = 3, 12
+    rng = np.random.default_rng(V)
+    z = rng.normal(0, 1, (n, V)).astype(np.float32)
+    tv, ti = rng.normal(0, 1, (n, K)).astype(np.float32), np.tile(np.array([5, 900, V - 1], np.int32), (n, 1))
+    tl = np.array([RO._lse(tv[r]) + 0.2 for r in range(n)], np.float32)
+    w = np.full(n, 0.5, np.float32)
+    tv[0, 1] = tv[1] = tv[2, 0] = np.nan
+    tv[3, 2] = np.inf
+    tl[4:7] = [np.nan, np.inf, -np.inf]
+    refused = range(7)
+    # left out: by its weight, by its list; an index of -1 is no entry
+    tv[7], tl[7], w[7] = np.nan, np.nan, 0
+    tv[8], tl[8] = -np.inf, -np.inf
+    ti[9], tv[9], tl[9] = -1, np.nan, np.nan
+    tv[10, 1], ti[10, 1] = np.nan, -1
+    args = (_dev(z, np.float32), _dev(tv, np.float32), _dev(ti, np.int32))
+    loss, dz = torch.full((n,), -7.0, device=DEV), torch.full((n, V), 7.0, device=DEV)
+    back, stats = torch.full((n, V), 7.0, device=DEV), torch.empty((n, 4), device=DEV)
+    tld, wd = _dev(tl, np.float32), _dev(w, np.float32)
+    api.dflash_distill_loss(*args, loss, t_lse=tld, weight=wd, dlogits=dz, stats_out=stats)
+    assert api.dflash_get_status() == api.DEV_BAD_PARAM
+    api.dflash_distill_backward(*args, stats, wd, back, t_lse=tld)
+    assert api.dflash_get_status() == api.DEV_BAD_PARAM and torch.equal(dz, back)
+    l, g = loss.cpu().numpy(), _host(dz)
+    assert np.isnan(l[:7]).all() and not g[:10].any() and l[7:10].tolist() == [0, 0, 0]
+    for r in range(n):
+        rl, rg = RO.distill(z[r].astype(np.float64), tv[r], ti[r], 1.0, float(tl[r]), float(w[r]))
+        assert math.isnan(rl) == (r in refused) and np.abs(g[r] - rg).max() < 1e-6
+        assert r in refused or abs(l[r] - rl) < 1e-5
+    # without a log-sum-exp
+    api.dflash_distill_loss(*args, loss, weight=wd, dlogits=dz)
+    assert api.dflash_get_status() == api.DEV_BAD_PARAM
+    l = loss.cpu().numpy()
+    assert np.isnan(l[:4]).all() and np.isfinite(l[4:]).all() and not dz[:4].any()
+    # a teacher's row with an infinite logit, as it comes from dflash_top_logits
+    teacher = _dev(z[:2], np.float32)
+    teacher[0, 77] = np.inf
+    val, idx, lse = torch.empty((2, K), device=DEV), torch.empty((2, K), dtype=torch.int32, device=DEV), torch.empty(2, device=DEV)
+    api.dflash_top_logits(teacher, K, val, idx, lse_out=lse)
+    api.dflash_distill_loss(args[0][:2], val, idx, loss[:2], t_lse=lse, dlogits=dz[:2])
+    assert api.dflash_get_status() == api.DEV_BAD_PARAM
+    assert np.isnan(float(loss[0])) and np.isfinite(float(loss[1])) and not dz[0].any() and torch.isfinite(dz[1]).all()
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
 def test_distill_with_masks_of_the_lowest_value(dtype):
     V, K = 3001, 3

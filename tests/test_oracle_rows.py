@@ -156,3 +156,12 @@ def test_distill_ignores_a_rest_that_rounding_explains():
         z[np.abs(z) > 1e8] = -np.inf
         assert RO.distill(z, val, idx, t_lse=lse + 0.01)[0] == math.inf
     assert 5 < positive < 45
+
+
+def test_distill_refuses_a_teacher_that_is_no_number():
+    z = np.arange(4.0)
+    for t, lse in (([1.0, math.nan], None), ([math.inf, 1.0], None), ([1.0, 2.0], math.nan), ([1.0, 2.0], math.inf)):
+        loss, g = RO.distill(z, t, [1, 2], t_lse=lse)
+        assert math.isnan(loss) and not g.any()
+        assert RO.distill(z, t, [1, 2], t_lse=lse, weight=0.0)[0] == 0
+    assert RO.distill(z, [1.0, math.nan], [1, -1])[0] > 0 and RO.distill(z, [math.nan], [-1], t_lse=math.nan)[0] == 0
