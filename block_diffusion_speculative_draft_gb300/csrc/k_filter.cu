@@ -380,17 +380,39 @@ __device__ __forceinline__ float pick_float(const float* v, int h) {
   return r;
 }
 
-// A thread's best entry so far.
+// A thread's best entry so far.  Scores are formed in fp32, and those that it cannot
+// tell apart again in double: at once where a few threads hold the listed entries
+// (offer<true>); a pass over a row has no registers for that, and keeps the score of
+// the next best.  Where that comes as near as the row's best, one more pass settles
+// the row (settle_row: some 1e-5 apart, so not once in 10^5 rows).
 struct Best {
   float score;  // (z - max)/T, or z/T, - log(-log u); starts at -inf
+  float next;   // the highest of the thread's others
   float val;
   int at;       // -1: none yet
 };
+__device__ __forceinline__ Best no_best() { return Best{-INFINITY, -INFINITY, 0.f, -1}; }
 
-// Takes one more entry into account; equal scores keep the lower index.
-__device__ __forceinline__ void offer(Best& b, float v, int i, float log2w, float u) {
-  const float sc = fmaf(log2w, kLn2, gumbel(u));
-  if (b.at < 0 || sc > b.score || (sc == b.score && i < b.at)) b = Best{sc, v, i};
+// Whether an entry comes before another by its score in double, equal ones by
+// index.
+__device__ __noinline__ bool beats64(const float* u, float v, int i, float bv, int bi, float m, float temp) {
+  const double x = score64(v, m, temp, u[i]), y = score64(bv, m, temp, u[bi]);
+  return x > y || (x == y && i < bi);
+}
+
+// Takes one more entry into account, whose uniform is ui; equal scores keep the lower
+// index.  With kExact: u, the row's uniforms, its maximum and temperature.
+template <bool kExact = false>
+__device__ __forceinline__ void offer(Best& b, float v, int i, float log2w, float ui, const float* u = nullptr,
+                                      float m = 0.f, float temp = 1.f) {
+  const float sc = fmaf(log2w, kLn2, gumbel(ui));
+  bool better = b.at < 0 || sc > b.score || (sc == b.score && i < b.at);
+  if (kExact) {
+    if (b.at >= 0 && near_best(sc, b.score) && near_best(b.score, sc)) better = beats64(u, v, i, b.val, b.at, m, temp);
+  } else {
+    b.next = fmaxf(b.next, fminf(sc, b.score));
+  }
+  if (better) b = Best{sc, b.next, v, i};
 }
 
 // What one pass over the row leaves in a thread: the maxima of its groups
@@ -877,34 +899,6 @@ __device__ int filter_list(const Row<T, NT>& r, Shared<NT, kCap>& s, const Ask& 
   return static_cast<int>(cta_reduce<NT / 32>(kept, OpSumU64(), s.x));
 }
 
-// Gumbel maximum over the first `kept` entries of the sorted list but `drop`
-// (rank 0's threads); -1 when nothing is left.
-template <typename T, int NT, int kCap>
-__device__ int pick_listed(const Row<T, NT>& r, Shared<NT, kCap>& s, const float* u, int kept, int drop,
-                           float temp) {
-  float best = 0.f;
-  int at = -1;
-  for (int i = threadIdx.x; i < kept; i += NT) {
-    const uint32_t v = place_index(s.list[i]);
-    if (static_cast<int>(v) == drop) continue;
-    const float sc = r.log2w(key_to_value(static_cast<uint32_t>(s.list[i] >> 32))) * kLn2 + gumbel(u[v]);
-    if (at < 0 || argmax_key(sc, v) > argmax_key(best, place_index(s.list[at]))) {
-      best = sc;
-      at = i;
-    }
-  }
-  const uint32_t v = at >= 0 ? place_index(s.list[at]) : 0;
-  const uint64_t win = cta_reduce<NT / 32>(at >= 0 ? argmax_key(best, v) : 0ull, OpMaxU64(), s.x);
-  if (win == 0) return -1;
-  const bool close = at >= 0 && near_best(best, key_value(win));
-  if (__syncthreads_count(close) <= 1) return static_cast<int>(key_index(win));
-  const uint64_t dk =
-      close ? double_key(score64(key_to_value(static_cast<uint32_t>(s.list[at] >> 32)), r.m, temp, u[v])) : 0ull;
-  const uint64_t dbest = cta_reduce<NT / 32>(dk, OpMaxU64(), s.x);
-  const uint64_t low = close && dk == dbest ? 0xFFFFFFFFull - v : 0ull;
-  return static_cast<int>(0xFFFFFFFFull - cta_reduce<NT / 32>(low, OpMaxU64(), s.x));
-}
-
 // What a list says of its row (rank 0's threads).
 struct Verdict {
   uint64_t mass;  // sum of the kept weights
@@ -1069,17 +1063,58 @@ __device__ __forceinline__ void draw_pass(const Row<T, NT>& r, Shared<NT, kCap>&
   }
 }
 
-// The best entry over the cluster; scores that fp32 cannot tell apart are
-// formed again in double (a thread's own runner-up aside).
+// Gumbel maximum over the row's entries at or above the cut (as rank 0 has it) but
+// `drop`, by scores in double; `win` is the entry with the best score in fp32.  (The
+// row comes in pieces: where its own record were passed, the loops would lose it to
+// memory.)
 template <typename T, int NT, int kCap>
-__device__ int join_best(Row<T, NT>& r, Shared<NT, kCap>& s, const float* u, const Best& b, float temp) {
+__device__ __noinline__ int settle_row(Shared<NT, kCap>& s, const T* p, int64_t V, float m, float c, const float* u,
+                                       uint64_t cut, int drop, int win, float temp, int turn) {
+  constexpr int NW = NT / 32;
+  Row<T, NT> r;
+  r.rank = cluster_rank();
+  r.size = cluster_size();
+  r.m = m;
+  r.c = c;
+  r.part.cut(p, V, static_cast<int>(r.rank), static_cast<int>(r.size));
+  if (r.rank == 0 && threadIdx.x < r.size) *peer(&s.pick[0], threadIdx.x) = cut;
+  cluster_sync_all(r.size);
+  cut = s.pick[0];
+  const float best = static_cast<float>(score64(to_f32(p[win]), m, temp, u[win]));
+  uint64_t mine = 0;
+  uint32_t at = 0;
+  r.each([&](float v, int64_t i) {
+    const uint32_t key = value_key(v), x = static_cast<uint32_t>(i);
+    if (key == 0 || place_of(key, x) < cut || static_cast<int>(x) == drop) return;
+    const float ui = u[i];
+    if (!near_best(fmaf(r.log2w(v), kLn2, gumbel(ui)), best)) return;
+    const uint64_t k = double_key(score64(v, m, temp, ui));
+    if (k > mine || (k == mine && x < at)) {
+      mine = k;
+      at = x;
+    }
+  });
+  const uint64_t top = cluster_reduce<NW>(mine, OpMaxU64(), s.x, r.rank, r.size, turn);
+  const uint64_t low = mine == top ? 0xFFFFFFFFull - at : 0ull;
+  return static_cast<int>(0xFFFFFFFFull - cluster_reduce<NW>(low, OpMaxU64(), s.x, r.rank, r.size, turn));
+}
+
+// The best entry over the cluster, of a draw among the row's entries at or above the
+// cut (as rank 0 has it) but `drop`.
+template <typename T, int NT, int kCap>
+__device__ int join_best(Row<T, NT>& r, Shared<NT, kCap>& s, const float* u, const Best& b, int64_t V, uint64_t cut,
+                         int drop, float temp) {
   constexpr int NW = NT / 32;
   const uint64_t k = b.at >= 0 ? argmax_key(b.score, static_cast<uint32_t>(b.at)) : 0ull;
   const uint64_t win = cluster_reduce<NW>(k, OpMaxU64(), s.x, r.rank, r.size, r.turn);
   if (win == 0) return -1;
+  // threads near the best, and above bit 32 those of them with more than one entry there
   const bool close = b.at >= 0 && near_best(b.score, key_value(win));
-  const uint64_t n = cluster_reduce<NW>(close, OpSumU64(), s.x, r.rank, r.size, r.turn);
+  const uint64_t more = close && near_best(b.next, key_value(win)) ? 1ull << 32 : 0ull;
+  const uint64_t n = cluster_reduce<NW>(more + close, OpSumU64(), s.x, r.rank, r.size, r.turn);
   if (n <= 1) return static_cast<int>(key_index(win));
+  if (n >> 32)
+    return settle_row(s, r.p, V, r.m, r.c, u, cut, drop, static_cast<int>(key_index(win)), temp, r.turn);
   const uint64_t dk = close ? double_key(score64(b.val, r.m, temp, u[b.at])) : 0ull;
   const uint64_t dbest = cluster_reduce<NW>(dk, OpMaxU64(), s.x, r.rank, r.size, r.turn);
   const uint64_t low = close && dk == dbest ? 0xFFFFFFFFull - static_cast<uint32_t>(b.at) : 0ull;
@@ -1088,10 +1123,10 @@ __device__ int join_best(Row<T, NT>& r, Shared<NT, kCap>& s, const float* u, con
 
 // Gumbel maximum over the row's entries at or above the cut but `drop`.
 template <typename T, int NT, int kCap>
-__device__ __noinline__ int pick_row(const Row<T, NT>& row, Shared<NT, kCap>& s, const float* u, uint64_t cut,
-                                     int drop, float temp) {
+__device__ __noinline__ int pick_row(const Row<T, NT>& row, Shared<NT, kCap>& s, const float* u, int64_t V,
+                                     uint64_t cut, int drop, float temp) {
   Row<T, NT> r = row;
-  Best b{-INFINITY, 0.f, -1};
+  Best b = no_best();
   if (threadIdx.x == 0) s.bar = 0x007FFFFFu;  // -inf
   __syncthreads();
   if (r.m < INFINITY) {
@@ -1109,7 +1144,7 @@ __device__ __noinline__ int pick_row(const Row<T, NT>& row, Shared<NT, kCap>& s,
         offer(b, v, static_cast<int>(i), 0.f, u[i]);
     });
   }
-  return join_best(r, s, u, b, temp);
+  return join_best(r, s, u, b, V, cut, drop, temp);
 }
 
 // Cluster sum of a float, CTAs in rank order.
@@ -1208,7 +1243,7 @@ __device__ __forceinline__ float deep_pass(const Row<T, NT>& r, Shared<NT, kCap>
   return sum;
 }
 
-// Best entry of rank 0's threads (see join_best).
+// Best of the entries that rank 0's threads hold, each the best of its own in double.
 template <typename T, int NT, int kCap>
 __device__ int join_best_cta(const Row<T, NT>& r, Shared<NT, kCap>& s, const float* u, const Best& b, float temp) {
   const uint64_t win = cta_reduce<NT / 32>(b.at >= 0 ? argmax_key(b.score, static_cast<uint32_t>(b.at)) : 0ull,
@@ -1220,6 +1255,20 @@ __device__ int join_best_cta(const Row<T, NT>& r, Shared<NT, kCap>& s, const flo
   const uint64_t dbest = cta_reduce<NT / 32>(dk, OpMaxU64(), s.x);
   const uint64_t low = close && dk == dbest ? 0xFFFFFFFFull - static_cast<uint32_t>(b.at) : 0ull;
   return static_cast<int>(0xFFFFFFFFull - cta_reduce<NT / 32>(low, OpMaxU64(), s.x));
+}
+
+// Gumbel maximum over the first `kept` entries of the sorted list but `drop`
+// (rank 0's threads); -1 when nothing is left.
+template <typename T, int NT, int kCap>
+__device__ int pick_listed(const Row<T, NT>& r, Shared<NT, kCap>& s, const float* u, int kept, int drop,
+                           float temp) {
+  Best best = no_best();
+  for (int x = threadIdx.x; x < kept; x += NT) {
+    const float v = key_to_value(static_cast<uint32_t>(s.list[x] >> 32));
+    const int i = static_cast<int>(place_index(s.list[x]));
+    if (i != drop) offer<true>(best, v, i, r.log2w(v), u[i], u, r.m, temp);
+  }
+  return join_best_cta(r, s, u, best, temp);
 }
 
 // A long list that top-k does not cut (rank 0's threads).  Top-p's border is
@@ -1339,7 +1388,7 @@ __device__ Verdict long_list(const Row<T, NT>& r, Shared<NT, kCap>& s, const Ask
       if (place[x] && place[x] >= out.cut) {
         const float v = key_to_value(static_cast<uint32_t>(place[x] >> 32));
         const int i = static_cast<int>(place_index(place[x]));
-        if (i != drop) offer(*best, v, i, r.log2w(v), u[i]);
+        if (i != drop) offer<true>(*best, v, i, r.log2w(v), u[i], u, r.m, q.T);
       }
     }
   }
@@ -1353,7 +1402,7 @@ __device__ __forceinline__ Verdict settle_list(const Row<T, NT>& r, Shared<NT, k
   if (n <= kQuick) return quick_list(r, s, q, n, 0, whole, u, drop);
   Verdict out;
   if (q.k >= n && (q.p >= 1.f || whole > 0)) {
-    Best best{-INFINITY, 0.f, -1};
+    Best best = no_best();
     out = long_list(r, s, q, n, 0, whole, u, drop, &best);
     if (u) out.tok = join_best_cta(r, s, u, best, q.T);
   } else {
@@ -1476,7 +1525,7 @@ __device__ __noinline__ bool deep_top_p(const Row<T, NT>& row, Shared<NT, kCap>&
     if (count <= kCap && above < need && above + mass >= need) break;
     bin = s.beside[above >= need ? 0 : 1];
     if (attempt == 1 || count > kCap || bin < 0 || bin >= kLineBins) return false;
-    if (best) *best = Best{-INFINITY, 0.f, -1};
+    if (best) *best = no_best();
     if (threadIdx.x == 0) {
       s.own_count = 0;
       s.own_mass = 0;
@@ -1497,7 +1546,7 @@ __device__ __noinline__ bool deep_top_p(const Row<T, NT>& row, Shared<NT, kCap>&
       if (u && threadIdx.x < count && s.list[threadIdx.x] >= out->cut) {
         const uint32_t i = place_index(s.list[threadIdx.x]);
         const float v = key_to_value(static_cast<uint32_t>(s.list[threadIdx.x] >> 32));
-        offer(*best, v, static_cast<int>(i), r.log2w(v), u[i]);
+        offer<true>(*best, v, static_cast<int>(i), r.log2w(v), u[i], u, r.m, q.T);
       }
     } else {
       *out = long_list(row, s, q, static_cast<int>(count), above, whole, u, -1, best);
@@ -1633,18 +1682,18 @@ using Short = Shared<kThr, kShortCap>;
 template <typename T>
 __device__ __forceinline__ int wide_row(Row<T, kThr>& r, Short& s, const FilterArgs& a, const Ask& q, float row_mass,
                                         const float* u, Verdict* v) {
-  Best best{-INFINITY, 0.f, -1};
+  Best best = no_best();
   const bool ordinary = q.k >= a.V && fabsf(r.m) < 1e30f;
   if (q.mp > 0.f) {
     set_bound(s, r.m, q);
     __syncthreads();
   }
   if (ordinary && q.p < 1.f && q.mp == 0.f && deep_top_p(r, s, q, a.V, row_mass, u, &best, v))
-    return u ? join_best(r, s, u, best, q.T) : -1;
+    return u ? join_best(r, s, u, best, a.V, v->cut, -1, q.T) : -1;
   if (ordinary && q.p >= 1.f && q.mp > 0.f) {
     v->mass = deep_min_p(r, s, u, &best);
     v->cut = place_of(value_key(s.bound), 0xFFFFFFFFu);
-    return u ? join_best(r, s, u, best, q.T) : -1;
+    return u ? join_best(r, s, u, best, a.V, v->cut, -1, q.T) : -1;
   }
   if (q.greedy) {  // the first entry of the order
     v->cut = first_place(r, s);
@@ -1657,7 +1706,7 @@ __device__ __forceinline__ int wide_row(Row<T, kThr>& r, Short& s, const FilterA
   } else {
     v->cut = wide_cut(r, s, a, q, &v->mass);
   }
-  return u ? pick_row(r, s, u, v->cut, -1, q.T) : -1;
+  return u ? pick_row(r, s, u, a.V, v->cut, -1, q.T) : -1;
 }
 
 template <typename T>
@@ -1688,7 +1737,7 @@ __global__ void __launch_bounds__(kThr, 4) sample_rows_kernel(const FilterArgs a
   const bool want_mass = wants_mass(a, q), unfiltered = want_mass && q.p >= 1.f && q.ok;
   const float* u = a.u + row * a.ld_u;
   Scan<T, kThr> sc;
-  Best best{-INFINITY, 0.f, -1};
+  Best best = no_best();
   if (unfiltered) {
     scan_and_draw(r, s, u, sc, best);
   } else {
@@ -1702,7 +1751,7 @@ __global__ void __launch_bounds__(kThr, 4) sample_rows_kernel(const FilterArgs a
     if (unfiltered && fabsf(r.m * r.c) < 1e3f) {
       v.mass = __float2ull_rn(row_mass * r.scale);
       Row<T, kThr> far = r;
-      tok = join_best(far, s, u, best, q.T);
+      tok = join_best(far, s, u, best, a.V, 1ull << 32, -1, q.T);
     } else if (listed_row(r, s, sc, a, q, low, row_mass, u, -1, &v)) {
       if (r.rank != 0) return;
       tok = v.tok;
@@ -1901,7 +1950,7 @@ __global__ void __launch_bounds__(kThr, 4) accept_rows_kernel(const FilterArgs a
           }
         }
         cluster_sync_all(size);
-        if (s.pick[1] == 0) out.tok = pick_row(far, s, u, s.pick[0], drop, q.T);
+        if (s.pick[1] == 0) out.tok = pick_row(far, s, u, a.V, s.pick[0], drop, q.T);
       }
     }
   }
@@ -1960,7 +2009,7 @@ __global__ void __launch_bounds__(kThr, 4) accept_wide_kernel(const FilterArgs a
           if (corr == kDeferred) {
             r.open(a, j * a.R + n);
             r.m = __ldcg(&e->m);
-            corr = pick_row(r, s, a.u + j * a.ld_u, __ldcg(&e->cut), n < a.D ? a.draft[j * a.D + n] : -1, q.T);
+            corr = pick_row(r, s, a.u + j * a.ld_u, a.V, __ldcg(&e->cut), n < a.D ? a.draft[j * a.D + n] : -1, q.T);
           }
         }
         if (r.rank == 0 && threadIdx.x < 32) write_sequence(a, j, n, corr, true);

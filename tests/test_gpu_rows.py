@@ -4,8 +4,8 @@ distillation.
 
 Integer outputs are compared exactly wherever the decision has a margin in
 the oracle: 2e-5 between the two best scores (fp32 scores carry about 1e-5 at
-magnitude 30; closer calls are settled in double but a thread's own runner-up
-is not reconsidered), 1e-6 between a uniform and a probability (the weights'
+magnitude 30; closer calls are settled in double, which has tests of its own),
+1e-6 between a uniform and a probability (the weights'
 exponentials are good to 2^-22).  Where an entry's sum is within 1e-6 of
 top-p's border the kept set may differ by entries of that mass: they are one
 in a million to be drawn, and move a log-probability by less than 4e-6.
@@ -278,6 +278,74 @@ def test_sample_near_ties_are_settled_in_double():
     z[:] = 1.5
     tok, _ = _sample(_dev(z, np.float32), np.full(n, 0.9), np.zeros(n), np.ones(n), np.zeros(n), _dev(u, np.float32))
     assert tok.tolist() == [0] * n
+
+
+def _near_tied(rng, n, V, dtype):
+    """Rows with two entries whose scores lie within 1e-6 of each other, far above
+    the others' but not the same in double: next to each other (one thread's), a few
+    packs apart, or anywhere; in either order.  (logits, uniforms, temperatures)"""
+    z = rng.normal(0, 1, (n, V))
+    T = np.full(n, np.float32(0.9))
+    zt = _padded(z, dtype, 0)
+    u = (_uniforms(rng, (n, V)) * np.float32(0.01)).astype(np.float32)
+    h = _host(zt)
+    for r in range(n):
+        i = int(rng.integers(0, V - 1)) & ~3
+        j = [i + 1, (i + 4096) % V, int(rng.integers(0, V)), i + 2][r % 4]
+        if r % 3 == 0:
+            i, j = j, i
+        while True:
+            zt[r, i] = h[r].max() + 0.5
+            zt[r, j] = h[r].max() + 0.5 - rng.uniform(0.05, 0.3)
+            a, b = float(zt[r, i]) / float(T[r]), float(zt[r, j]) / float(T[r])
+            u[r, i] = np.float32(rng.uniform(0.4, 0.7))
+            u[r, j] = np.float32(math.exp(-math.exp(-(a - math.log(-math.log(float(u[r, i]))) - b))))
+            gap = abs(a - math.log(-math.log(float(u[r, i]))) - b + math.log(-math.log(float(u[r, j]))))
+            if i != j and 1e-9 < gap < 1e-6:
+                break
+            j = (i + 1 + int(rng.integers(0, V - 1))) % V if i == j else j
+    return zt, u, T
+
+
+# nothing; deep top-p; min-p over many, and over some hundred entries; top-k by the
+# sorted list, by its short form and beyond it; all together
+NEAR = [(0, 1, 0), (0, 0.97, 0), (0, 1, 1e-3), (0, 1, 0.08), (600, 1, 0), (40, 0.99, 0), (3000, 1, 0), (2000, 0.999, 1e-3)]
+
+
+@pytest.mark.parametrize("k,p,mp", NEAR)
+@pytest.mark.parametrize("dtype,n,V", [("f32", 24, 20000), ("bf16", 24, 20001), ("f16", 1, 151936), ("f32", 330, 60000),
+                                       ("f32", 130, 9000)])
+def test_sample_tells_scores_apart_that_fp32_cannot(dtype, n, V, k, p, mp):
+    rng = np.random.default_rng(n + k)
+    some = min(n, 24)
+    zt, u, T = _near_tied(rng, some, V, dtype)
+    at = torch.arange(n, device=DEV) % some
+    big, ub = zt[at].contiguous(), _dev(u, np.float32)[at].contiguous()
+    ask = np.full(n, T[0]), np.full(n, k), np.full(n, p), np.full(n, mp)
+    tok, _ = _sample(big, *ask, ub)
+    assert torch.equal(tok, _sample(big, *ask, ub)[0]) and api.dflash_get_status() == 0
+    z, tok = _host(zt), tok.cpu().numpy()
+    for r in range(some):
+        want = RO.sample(z[r], float(T[r]), u[r], k, float(np.float32(p)), float(np.float32(mp)))[0]
+        assert (tok[r::some] == want).all(), (r, want)
+
+
+@pytest.mark.parametrize("k,p,mp", NEAR)
+@pytest.mark.parametrize("dtype,b,V", [("f32", 12, 20000), ("bf16", 3, 151936), ("f32", 170, 60000)])
+def test_accept_tells_scores_apart_that_fp32_cannot(dtype, b, V, k, p, mp):
+    # sequences without a draft: the draw at their first row
+    rng = np.random.default_rng(b + k)
+    some = min(b, 12)
+    zt, u, T = _near_tied(rng, some, V, dtype)
+    at = torch.arange(b, device=DEV) % some
+    z3 = zt[at].unsqueeze(1).expand(b, 2, V).contiguous()
+    n, c, _, _ = _accept(z3, np.full((b, 1), -1), np.full(b, T[0]), np.full(b, k), np.full(b, p), np.full(b, mp),
+                         np.zeros((b, 1)), _dev(u, np.float32)[at].contiguous())
+    assert api.dflash_get_status() == 0 and not n.any()
+    z = _host(zt)
+    for r in range(some):
+        want = RO.sample(z[r], float(T[r]), u[r], k, float(np.float32(p)), float(np.float32(mp)))[0]
+        assert (c[r::some] == want).all(), (r, want)
 
 
 def test_sample_without_filters_and_bad_parameters():
