@@ -339,7 +339,7 @@ __device__ uint64_t mass_from(Row<T, NT>& r, Shared<NT, kCap>& s, uint64_t cut) 
 // The two borders that are formed in double, by one thread (the unit is narrow);
 // seen by all after the next barrier.  min-p: the smallest float at or above
 // its bound.  top-p: sums are integers, so "below p times the whole" is "below
-// the next integer".
+// the next integer", and as the first entry is kept whatever p, 1 stands for 0.
 template <int NT, int kCap>
 __device__ __forceinline__ void set_bound(Shared<NT, kCap>& s, float m, const Ask& q) {
   if (threadIdx.x != 0) return;
@@ -351,7 +351,8 @@ __device__ __forceinline__ void set_bound(Shared<NT, kCap>& s, float m, const As
 template <int NT, int kCap>
 __device__ __forceinline__ void set_need(Shared<NT, kCap>& s, float p, uint64_t whole) {
   if (threadIdx.x != 0) return;
-  s.need = p < 1.f ? static_cast<uint64_t>(ceil(static_cast<double>(p) * static_cast<double>(whole))) : ~0ull;
+  const uint64_t sum = static_cast<uint64_t>(ceil(static_cast<double>(p) * static_cast<double>(whole)));
+  s.need = p >= 1.f ? ~0ull : sum > 0 ? sum : 1;
 }
 
 // The score of an entry, (v - m)/T - log(-log u), in fp32 and in double.
@@ -1584,7 +1585,7 @@ __device__ __noinline__ uint64_t wide_cut(Row<T, NT>& r, Shared<NT, kCap>& s, co
     const uint64_t w = mass_from(r, s, cut);
     set_need(s, q.p, w);
     __syncthreads();
-    const uint64_t need = s.need < 1 ? 1 : s.need;
+    const uint64_t need = s.need;
     if (need < w) cut = find_cut<T, NT, kCap, true>(r, s, cut, need, a.idx_bits);
   }
   if (q.mp > 0.f) {

@@ -248,6 +248,29 @@ def test_sample_takes_every_border_of_a_worked_row():
     assert tok.tolist() == [order[i] for i in [0, 0, 2, 2, 3, 4, 4, 4, 4]]
 
 
+@pytest.mark.parametrize("dtype,n,V", [("f32", 20, 40000), ("bf16", 20, 151936), ("f16", 330, 90000), ("f32", 5, 900)])
+@pytest.mark.parametrize("p", [0.0, 2.0 ** -149, 1e-9])
+def test_sample_under_a_top_p_of_next_to_nothing(dtype, n, V, p):
+    # the first entry alone, wherever the others lie: far below it, some hundred just
+    # below it (a long list whose first bin holds one entry), all at its height
+    rng = np.random.default_rng(V)
+    z = np.full((5, V), -10.0) + rng.normal(0, 0.5, (5, V))
+    for r, height in enumerate((0.0, 9.5, 9.9, 9.99)):
+        at = rng.choice(V, 400, replace=False)
+        z[r, at] = height - 0.05 * rng.random(400)
+        z[r, at[rng.integers(0, 400)]] = 10.0
+    z[4] = 1.0
+    some = _padded(z, dtype, 0)
+    zt = some[torch.arange(n, device=DEV) % 5].contiguous()
+    u = _dev(_uniforms(rng, (5, V)), np.float32)[torch.arange(n, device=DEV) % 5].contiguous()
+    first = _first(_host(some))[np.arange(n) % 5]
+    for T, mp in ((1.0, 0.0), (30.0, 0.0), (1.0, 1e-4)):
+        tok, lp = _sample(zt, np.full(n, T), np.zeros(n), np.full(n, p), np.full(n, mp), u)
+        assert api.dflash_get_status() == 0
+        assert np.array_equal(tok.cpu().numpy(), first), (T, mp)
+        assert float(lp.abs().max()) < 1e-6
+
+
 def test_sample_follows_its_distribution():
     rng = np.random.default_rng(5)
     n, V = 6000, 40
