@@ -303,8 +303,9 @@ __device__ __noinline__ uint64_t find_cut(Row<T, NT>& r, Shared<NT, kCap>& s, ui
     const uint64_t in_bin = s.pick[2];
     pre = (top < 64 ? pre << bits : 0) | b;
     top = shift;
-    // the whole bin is taken, or it holds only the border entry
-    if (top == 0 || in_bin == 1 || (!kMass && in_bin == need)) return pre << top;
+    // the whole bin is taken, or it holds only the border entry; entries below `lo`
+    // may lie in it too
+    if (top == 0 || in_bin == 1 || (!kMass && in_bin == need)) return pre << top > lo ? pre << top : lo;
   }
 }
 

@@ -248,6 +248,33 @@ def test_sample_takes_every_border_of_a_worked_row():
     assert tok.tolist() == [order[i] for i in [0, 0, 2, 2, 3, 4, 4, 4, 4]]
 
 
+@pytest.mark.parametrize("dtype,n,V", [("f32", 6, 20000), ("bf16", 6, 20001), ("f16", 40, 40000), ("bf16", 330, 90001)])
+def test_sample_keeps_top_k_s_border_under_top_p(dtype, n, V):
+    # rows beyond the short list whose last entry under top-k is also top-p's, alone
+    # of its kind above many that top-k drops; those have the higher uniforms
+    rng = np.random.default_rng(V)
+    z = np.full((3, V), 3.0)
+    z[0] = 2.5                                                  # equal: k = 1
+    at = [rng.choice(V, 1101, replace=False) for _ in range(3)]
+    for r in (1, 2):
+        z[r, at[r]] = 5 + rng.random(1101)
+        z[r, at[r][7]] = 3.875 if r == 1 else 3.0               # the last of 1101, or the first of many at 3
+    k, p = np.array([1, 1101, 1101]), np.array([0.999, 0.999995, 0.999995])
+    some = _padded(z, dtype, 0)
+    h = _host(some)
+    u = np.full((3, V), 0.25, np.float32)
+    for r in range(3):
+        ids = RO.filtered(h[r], 1.0, int(k[r]), float(np.float32(p[r])))[0]
+        assert ids.size == k[r]
+        u[r, np.setdiff1d(np.arange(V), ids)] = 1 - 2.0 ** -20
+    zt, ut = some[torch.arange(n, device=DEV) % 3].contiguous(), _dev(u, np.float32)[torch.arange(n, device=DEV) % 3].contiguous()
+    row = np.arange(n) % 3
+    tok, _ = _sample(zt, np.ones(n), k[row], p[row], np.zeros(n), ut)
+    assert api.dflash_get_status() == 0
+    for r in range(3):
+        assert (tok.cpu().numpy()[r::3] == RO.sample(h[r], 1.0, u[r], int(k[r]), float(np.float32(p[r])))[0]).all(), r
+
+
 @pytest.mark.parametrize("dtype,n,V", [("f32", 20, 40000), ("bf16", 20, 151936), ("f16", 330, 90000), ("f32", 5, 900)])
 @pytest.mark.parametrize("p", [0.0, 2.0 ** -149, 1e-9])
 def test_sample_under_a_top_p_of_next_to_nothing(dtype, n, V, p):
