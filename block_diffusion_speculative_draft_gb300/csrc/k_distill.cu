@@ -35,6 +35,7 @@ namespace {
 constexpr int kDevBadToken = 0x2, kDevBadParam = 0x8;  // why a row is refused
 constexpr int kSome = 0x1;  // beside them: an entry above -inf is listed
 constexpr float kMassOne = 1099511627776.f;  // 2^40: probabilities are summed as integers
+constexpr float kMostP = 256.f;               // up to here: 1024 of them stay below 2^58
 constexpr float kLn2 = 0.6931471805599453f;
 // A log-sum-exp in fp32 is off by its rounding, 2^-24 of its size, and by its
 // sum's, some 12 2^-24 (exponentials to 2^-22, the scaled logits' own rounding): a
@@ -130,8 +131,8 @@ __device__ __forceinline__ int reasons(int flags, float w) {
 // Reads the row's entries, with the student's logits at those of this part, and
 // forms the teacher's probabilities.  `bits` (zero) marks the part's listed
 // elements; a mark that is there already, or a token out of range, refuses the
-// row; a logit that is NaN or +inf, or a t_lse that is not finite, does so unless
-// the row's weight leaves it out (reasons).
+// row; a logit that is NaN or +inf, or a t_lse that is not finite or so low that a p
+// is above kMostP, does so unless the row's weight leaves it out (reasons).
 template <typename T, int NT>
 __device__ __forceinline__ Teacher read_teacher(const DistillArgs& a, int64_t row, const Part<T>& q, Entries e,
                                                 uint32_t* bits, Shared<NT / 32>& s) {
@@ -148,7 +149,6 @@ __device__ __forceinline__ Teacher read_teacher(const DistillArgs& a, int64_t ro
     const int64_t at = i - q.first;
     const bool in = i >= 0 && i < a.V, own = in && at >= 0 && at < q.n;
     if (!in && i != -1) flags |= kDevBadToken;
-    if (in && !(v < INFINITY)) flags |= kDevBadParam;
     if (own) {
       const uint32_t x = static_cast<uint32_t>(q.off + at), bit = 1u << (x & 31);
       if (atomicOr(&bits[x >> 5], bit) & bit) flags |= kDevBadToken;
@@ -186,12 +186,15 @@ __device__ __forceinline__ Teacher read_teacher(const DistillArgs& a, int64_t ro
   for (int k = threadIdx.x; k < a.K; k += NT) {
     const float v = e.lp[k];
     const Pair y = two_sum(v, -base), x = over_t(a, y.hi), d = two_sum(x.hi, -lt);
-    const float hi = v > -INFINITY ? d.hi : v;
-    float p = expf(hi);
-    if (hi > -INFINITY) p = fmaf(p, d.lo + fmaf(y.lo, a.inv_hi, x.lo), p);
-    e.lp[k] = hi;
+    Pair lp{v > -INFINITY ? d.hi : v, 0.f};
+    // (the low parts are as large as the difference where t / T and t_lse are far out)
+    if (lp.hi > -INFINITY) lp = two_sum(d.hi, d.lo + fmaf(y.lo, a.inv_hi, x.lo));
+    float p = expf(lp.hi);
+    p = fmaf(p, lp.lo, p);
+    if (!(p <= kMostP)) flags |= kDevBadParam;
+    e.lp[k] = lp.hi;
     e.p[k] = p;
-    fixed += __float2ull_rn(fminf(p, 256.f) * kMassOne);
+    fixed += __float2ull_rn(p * kMassOne);
   }
   if (holds) {
 #pragma unroll

@@ -450,7 +450,9 @@ DFLASH_API int32_t dflash_top_logits(const void* logits, int32_t dtype, int64_t 
  *  - A row with an index listed twice, or outside [-1, V), is refused: loss
  *    NaN, gradient 0, DFLASH_DEV_BAD_TOKEN set.  So is one that is not left out
  *    and has a listed t_val that is NaN or +inf, or a t_lse that is not finite
- *    (of a teacher's row with a +inf logit, say): DFLASH_DEV_BAD_PARAM set.
+ *    (of a teacher's row with a +inf logit, say) or so far below a t_val / T that
+ *    p_k > 256: DFLASH_DEV_BAD_PARAM set.  (In fp32 t_lse is off by up to 2^-24 of
+ *    its size, which p_k shows: teacher logits far from 0 are better shifted.)
  *  - A student row without a logit above -inf has no distribution: loss NaN,
  *    gradient undefined.  The loss is +inf where a p_k or p_r above 0 meets a q
  *    below fp32's range of logarithms (a -inf logit, or one 3e38 T below the others).

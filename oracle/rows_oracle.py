@@ -133,6 +133,8 @@ def distill(z, t_val, t_idx, T: float = 1.0, t_lse: Optional[float] = None, weig
         t = (t_val[listed] - t_val[listed].max()) / T
     lp = t - (_lse(t) if t_lse is None else float(t_lse))
     p = np.exp(lp)
+    if np.any(p > 256):
+        return math.nan, np.zeros(V)
     on = p > 0
     loss = float((p[on] * (lp[on] - (zt[ids][on] - L))).sum())
     outside = np.ones(V, bool)

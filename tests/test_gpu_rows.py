@@ -957,6 +957,38 @@ def test_distill_with_masks_far_out(dtype, T, mask):
             assert np.abs(_host(dz)[at] - rg).max() < (1e-5 + 2 * eps) / T, (r, lse)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("far", [3e3, 1e5, -1e6, 2e6])
+def test_distill_from_a_teacher_far_from_zero(dtype, far):
+    # t / T and t_lse agree in all but their last digits; the next fp32 above the
+    # log-sum-exp leaves the rest its share of what rounding takes
+    rng = np.random.default_rng(7)
+    n, V, K, T = 24, 9001, 12, float(np.float32(0.7))
+    z = rng.normal(0, 2, (n, V))
+    ti = np.stack([rng.choice(V, K, replace=False) for _ in range(n)]).astype(np.int32)
+    tv = (far + rng.normal(0, 2, (n, K))).astype(np.float32)
+    tl = np.array([RO._lse(tv[r].astype(np.float64) / T) + 0.05 for r in range(n)])
+    tl = np.nextafter(tl.astype(np.float32), np.float32(np.inf))
+    zt = _padded(z, dtype, 0)
+    loss, stats = torch.empty(n, device=DEV), torch.empty((n, 4), device=DEV)
+    dz, back = (torch.empty((n, V), dtype=DT[dtype], device=DEV) for _ in range(2))
+    args = zt, _dev(tv, np.float32), _dev(ti, np.int32)
+    api.dflash_distill_loss(*args, loss, t_lse=_dev(tl, np.float32), temperature=T, dlogits=dz, stats_out=stats)
+    api.dflash_distill_backward(*args, stats, torch.ones(n, device=DEV), back, t_lse=_dev(tl, np.float32), temperature=T)
+    assert api.dflash_get_status() == 0 and torch.equal(dz, back)
+    eps = {"f32": 2.0 ** -24, "bf16": 2.0 ** -8}[dtype]
+    h, g = _host(zt), _host(dz)
+    for r in range(n):
+        rl, rg = RO.distill(h[r], tv[r], ti[r], T, float(tl[r]))
+        # a p is off by 2^-46 of t / T (1 / T as a pair) besides its own rounding, a
+        # loss by the sum of their logarithms' as well; the gradients are over T
+        e = 2.0 ** -46 * abs(far) / T + 2.0 ** -21
+        assert abs(float(loss[r]) - rl) <= 32 * e and np.abs(g[r] - rg).max() <= (12 * e + 2 * eps) / T, r
+    # as far below a t / T as no log-sum-exp is
+    api.dflash_distill_loss(*args, loss, t_lse=_dev(tl - 20 - np.abs(tl) / 1e5, np.float32), temperature=T, dlogits=dz)
+    assert api.dflash_get_status() == api.DEV_BAD_PARAM and torch.isnan(loss).all() and not dz.any()
+
+
 def test_distill_keeps_the_rest_when_the_student_is_sure():
     # q outside the listed tokens near 1e-30: far below what 1 - sum of q keeps
     V = 5000
