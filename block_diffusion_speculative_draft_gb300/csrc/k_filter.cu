@@ -1088,6 +1088,7 @@ __device__ __noinline__ int settle_row(Shared<NT, kCap>& s, const T* p, int64_t 
   r.each([&](float v, int64_t i) {
     const uint32_t key = value_key(v), x = static_cast<uint32_t>(i);
     if (key == 0 || place_of(key, x) < cut || static_cast<int>(x) == drop) return;
+    if (m == INFINITY && v != m) return;  // probability 0: not even where u = 0 leaves no score above -inf
     const float ui = u[i];
     if (!near_best(fmaf(r.log2w(v), kLn2, gumbel(ui)), best)) return;
     const uint64_t k = double_key(score64(v, m, temp, ui));

@@ -473,6 +473,20 @@ def test_sample_at_zero_temperature_takes_the_first_entry_of_any_row(dtype, n, V
     assert np.array_equal(tok.cpu().numpy(), _first(_host(base))[np.arange(n) % 14]) and not lp.any()
 
 
+def test_sample_infinite_logits_win_whatever_their_uniforms():
+    # u = 0 scores -inf, as every finite logit beside an infinite one does
+    n, V = 6, 5000
+    z = np.zeros((n, V), np.float32)
+    z[:, 77], z[3:, 4000] = np.inf, np.inf
+    u = np.full((n, V), 0.5, np.float32)
+    u[:, 77] = 0
+    u[4:, 4000] = 0
+    k, p, mp = np.array([0, 0, 300, 0, 0, 300]), np.array([1, 0.9, 1, 1, 1, 0.5]), np.array([0, 0, 0, 0, 0.1, 0])
+    tok, lp = _sample(_dev(z, np.float32), np.ones(n), k, p, mp, _dev(u, np.float32))
+    assert tok.tolist() == [77, 77, 77, 4000, 77, 77]
+    assert np.abs(lp.cpu().numpy() - [0, 0, 0, -math.log(2), -math.log(2), 0]).max() < 1e-6
+
+
 # --------------------------------------------------------------- accept -----
 def _accept(zt, draft, T, k, p, mp, ua, us, **kw):
     b, R, _ = zt.shape
