@@ -368,17 +368,20 @@ DFLASH_API int32_t dflash_sample_workspace_size(int64_t rows, int64_t V, size_t*
  * m = max z and w_v = exp((z_v - m) / T):
  *   top_k keeps the first top_k entries of the order (0 or >= V: all);
  *   top_p keeps, of those, each entry whose predecessors' w sum to less than
- *     top_p times the sum over what top_k kept (the first always; 1: all);
+ *     top_p times the sum over what top_k kept (the first always; 1: all).
+ *     The sums are of fp32 exponentials: an entry within 1e-6 of the whole from
+ *     that border may fall on its other side;
  *   min_p keeps, of those, the entries with z_v >= m + T ln(min_p) (0: all);
  *   P(v) = w_v / (sum of the kept w), 0 for the others;
  *   tok = argmax over the kept v of (z_v - m) / T - log(-log u_v), lowest
- *     index on ties (Gumbel maximum: an exact draw from P); logprob = ln P(tok).
+ *     index on ties (Gumbel maximum: an exact draw from P), formed in 64 bits
+ *     where 32 cannot tell entries apart; logprob = ln P(tok).
  * T = 0 takes the first entry of the order (logprob 0), whatever the filters.
  * temperature [rows] fp32; top_k [rows] int32, top_p and min_p [rows] fp32,
  * each nullable (no filter).  T must be 0 or in [1e-6, 1e6], top_k >= 0, top_p
  * and min_p in [0, 1]; a row outside that gets tok -1 and logprob -inf, and
  * sets DFLASH_DEV_BAD_PARAM.  u: uniforms in [0, 1), [rows] of V fp32, ld_u >= V
- * apart; only the entries kept are read.  tok_out [rows] int32, logprob_out
+ * apart; those of entries that are not kept do not matter.  tok_out [rows] int32, logprob_out
  * [rows] fp32 (nullable).  A row without an unmasked entry gets tok -1 and
  * logprob -inf.  ws holds dflash_sample_workspace_size bytes, 16-byte aligned;
  * it needs no zero fill and keeps nothing between calls. */
@@ -465,7 +468,8 @@ DFLASH_API int32_t dflash_distill_loss(const void* logits, int32_t dtype, int64_
 /* The gradient of the unweighted loss for a given upstream gradient:
  * dlogits = grad_loss[row] * dloss/dlogits, with stats [rows][4] of a
  * dflash_distill_loss call on the same logits, teacher entries and T.
- * grad_loss: [rows] fp32 (0: a zero row).  The rest as in that call. */
+ * grad_loss: [rows] fp32 (0: a zero row).  A row that call left out or refused
+ * stays so.  The rest as in that call. */
 DFLASH_API int32_t dflash_distill_backward(const void* logits, int32_t dtype, int64_t rows, int64_t V, int64_t ld,
                                            const float* t_val, const int32_t* t_idx, int32_t K, const float* t_lse,
                                            float temperature, const float* stats, const float* grad_loss,
