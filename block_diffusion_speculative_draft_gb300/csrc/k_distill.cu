@@ -91,7 +91,10 @@ size_t bitmap_bytes(int64_t n, int slack) {
 // rounding is small (is_near); lead() tells how far it is off.  Past that (the
 // type's lowest value as a mask, say) it is (v - m) c.
 __device__ __forceinline__ bool is_near(float ref) { return fabsf(ref) < kRefMax; }
-__device__ __forceinline__ float lead(float m, float c) { return is_near(m * c) ? fmaf(-m, c, m * c) : 0.f; }
+__device__ __forceinline__ float lead(float m, float c) {
+  const float ref = reference(m, c);
+  return is_near(ref) ? fmaf(-m, c, ref) : 0.f;
+}
 // Calls f(weight) with weight(v) = 2^(exponent of v) in the form that m asks for.
 template <typename F>
 __device__ __forceinline__ void with_weight(float c, float ref, float m, F f) {
@@ -112,7 +115,7 @@ __device__ __forceinline__ Pair two_sum(float a, float b) {  // a + b exactly
 }
 // v / T, from the launcher's pair of 1 / T
 __device__ __forceinline__ Pair over_t(const DistillArgs& a, float v) {
-  const float h = v * a.inv_hi;
+  const float h = __fmul_rn(v, a.inv_hi);  // (not to be fused into the sums it goes to)
   return Pair{h, fmaf(v, a.inv_hi, -h) + v * a.inv_lo};
 }
 
@@ -503,7 +506,7 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 5 : 1) distill_kernel(const Di
       for (int x = 1; x < kFlight; ++x) mx = Pack<T>::max2(mx, Part<T>::max_words(v[x]));
       const float m = Part<T>::max_of(mx);
       if (m > top) {
-        const float next = m * a.c;
+        const float next = reference(m, a.c);
         if (top > -INFINITY)
           sum *= fast_exp2(is_near(ref) && is_near(next)
                                ? ref - next
@@ -543,7 +546,7 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 5 : 1) distill_kernel(const Di
     return;
   }
   const float f = s.plan.f;
-  with_weight(a.c, s.plan.mr * a.c, s.plan.mr, [&](auto weight) {
+  with_weight(a.c, reference(s.plan.mr, a.c), s.plan.mr, [&](auto weight) {
     write_part<T, NT>(q, dz, [=](float z) { return f * weight(z); });
   });
   __syncthreads();

@@ -466,7 +466,7 @@ __device__ __forceinline__ void scan_row(const Row<T, NT>& r, bool want_mass, Sc
     if (want_mass) {
       const float top = Row<T, NT>::max_of(all);
       if (top > -INFINITY) {
-        const float ref = top * r.c;
+        const float ref = reference(top, r.c);
         if (!any || ref > t.ref) {
           if (any) t.sum *= fast_exp2(t.ref - ref);
           t.ref = ref;
@@ -546,7 +546,7 @@ __device__ __forceinline__ void scan_and_draw(const Row<T, NT>& r, Shared<NT, kC
       mx = Pack<T>::max2(mx, pm);
       const float top = Row<T, NT>::max_of(pm);
       if (!(top > -INFINITY)) continue;
-      const float ref = top * r.c;
+      const float ref = reference(top, r.c);
       if (!any || ref > t.ref) {
         if (any) t.sum *= fast_exp2(t.ref - ref);
         t.ref = ref;

@@ -61,6 +61,9 @@ __device__ __forceinline__ uint64_t double_key(double v) {
 // ref is a known number, not a rounded one, wherever sums with different
 // references meet.
 __device__ __forceinline__ float inv_temperature(float t) { return 1.4426950408889634f / t; }
+// (a plain product would be fused into the difference of two references, which then is
+// not that of the numbers: off by half a unit of c m in its last place)
+__device__ __forceinline__ float reference(float m, float c) { return __fmul_rn(m, c); }
 // Up to here ref is within 1/4 of c m, so the weights of entries at m are near 1;
 // further out (logits of 1e38 as a mask) 2^x could overflow, and (v - m) c is
 // taken.

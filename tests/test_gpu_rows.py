@@ -226,6 +226,21 @@ def test_sample_at_the_ends_of_the_temperature(dtype, T):
     _check_sample(_host(zt), u, t, k, p, mp, tok.cpu().numpy(), lp.cpu().numpy())
 
 
+@pytest.mark.parametrize("far", [300.0, 5000.0, -20000.0, 40000.0])
+@pytest.mark.parametrize("T,mode", [(0.7, "mixed"), (0.7, "none"), (0.05, "p"), (0.05, "none")])
+def test_sample_far_from_zero(T, mode, far):
+    # T apart from the logits' size: sums whose references differ meet without a trace of it
+    rng = np.random.default_rng(31)
+    n, V = 16, 30011
+    zt = _padded(far + _logits(rng, n, V, "flat") * T, "f32", 0)
+    _, k, p, mp = _ask(rng, n, mode)
+    t = np.full(n, T, np.float32)
+    u = _uniforms(rng, (n, V))
+    tok, lp = _sample(zt, t, k, p, mp, _dev(u, np.float32))
+    assert api.dflash_get_status() == 0
+    _check_sample(_host(zt), u, t, k, p, mp, tok.cpu().numpy(), lp.cpu().numpy())
+
+
 def test_sample_takes_every_border_of_a_worked_row():
     # weights 8, 4, 4, 2, 1 at T = 1 / ln 2; the uniforms make the last kept
     # entry of the order the winner
@@ -969,6 +984,30 @@ def test_distill_with_masks_far_out(dtype, T, mask):
             else:
                 assert float(loss[at]) > 0.999 * min(rl, 3e38), (r, lse)
             assert np.abs(_host(dz)[at] - rg).max() < (1e-5 + 2 * eps) / T, (r, lse)
+
+
+@pytest.mark.parametrize("far", [300.0, 5000.0, -20000.0, 40000.0])
+@pytest.mark.parametrize("T", [0.7, 0.05])
+@pytest.mark.parametrize("n,rest", [(3, True), (700, False)])
+def test_distill_of_a_student_far_from_zero(far, T, n, rest):
+    rng = np.random.default_rng(33)
+    V, K, T = 20011, 24, float(np.float32(T))
+    tv, ti = _teach(rng, 6, V, K)
+    tv = (tv * T).astype(np.float32)
+    z = rng.normal(0, 2, (6, V))
+    z[np.arange(6)[:, None], ti] = 4 + rng.normal(0, 1, (6, K))
+    some = _padded(far + z * T, "f32", 0)
+    at = np.arange(n) % 6
+    tl = np.array([RO._lse(t.astype(np.float64) / T) + 0.2 for t in tv], np.float32) if rest else None
+    loss, dz = torch.empty(n, device=DEV), torch.empty((n, V), device=DEV)
+    api.dflash_distill_loss(some[torch.from_numpy(at).to(DEV)].contiguous(), _dev(tv[at], np.float32),
+                            _dev(ti[at], np.int32), loss, t_lse=_dev(tl[at], np.float32) if rest else None,
+                            temperature=T, dlogits=dz)
+    assert api.dflash_get_status() == 0
+    h = _host(some) - far                # (exact: the same rows, whose oracle keeps more digits)
+    few = range(0, n, max(1, n // 6))
+    _check_distill(h[at][few], tv[at][few], ti[at][few], T, None if tl is None else tl[at][few], np.ones(len(few)),
+                   loss.cpu().numpy()[few], _host(dz[list(few)]), "f32")
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
