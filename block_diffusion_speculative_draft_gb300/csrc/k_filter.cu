@@ -29,7 +29,7 @@
 // result repeats bit for bit.
 //
 // Large batches are bound by HBM while they stream, and then by random re-reads
-// and one CTA's ranking (512 x 151936 bf16, top-k with top-p: 54 us, 32 of them at
+// and one CTA's ranking (512 x 151936 bf16, top-k with top-p: 52 us, 32 of them at
 // 4.9 TB/s; unfiltered, where every uniform counts too, 86 us, 5.4 TB/s); small
 // ones by the chain of launch, cluster barriers and L2 round trips (one row 12 us).
 #include "kernels.h"
