@@ -23,6 +23,7 @@ STATUS_NAMES = {0: "ok", -1: "EINVAL", -2: "EUNSUPPORTED", -3: "ECUDA", -4: "ECA
 DTYPE_F32, DTYPE_F16, DTYPE_BF16 = 0, 1, 2
 LAYOUT_PLAIN, LAYOUT_GATEUP = 0, 1
 DEV_KV_CAPACITY, DEV_BAD_TOKEN, DEV_BAD_LENGTH, DEV_BAD_PARAM, DEV_WAIT_TIMEOUT = 0x1, 0x2, 0x4, 0x8, 0x100
+DEV_BAD_TREE = 0x10
 
 EXPORTS = [
     "dflash_version", "dflash_status_string", "dflash_workspace_size", "dflash_pack_w8a16",
@@ -33,6 +34,8 @@ EXPORTS = [
     "dflash_verify_accept_sample", "dflash_sample_workspace_size", "dflash_sample",
     "dflash_verify_filtered_workspace_size",
     "dflash_verify_accept_filtered", "dflash_top_logits", "dflash_distill_loss", "dflash_distill_backward",
+    "dflash_adjust_logits", "dflash_tree_mask", "dflash_tree_attention_workspace_size", "dflash_tree_attention",
+    "dflash_tree_accept", "dflash_tree_commit_workspace_size", "dflash_tree_commit",
     "dflash_kv_commit", "dflash_commit_draft_block", "dflash_set_launch_mode",
     "dflash_get_launch_mode", "dflash_get_status",
 ]
@@ -110,6 +113,16 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "dflash_top_logits": ([P, I32, I64, I64, I64, I32, ctypes.c_float, P, P, P, P], I32),
         "dflash_distill_loss": ([P, I32, I64, I64, I64, P, P, I32, P, ctypes.c_float, P, P, P, P, I64, P], I32),
         "dflash_distill_backward": ([P, I32, I64, I64, I64, P, P, I32, P, ctypes.c_float, P, P, P, I64, P], I32),
+        "dflash_adjust_logits": ([P, I32, I64, I32, I64, I64, P, I64, P, I64, I32, P, P, P, I32, P, P, P, P, P, P, I32, P,
+                                  I64, I64, P, P], I32),
+        "dflash_tree_mask": ([P, P, I32, I32, P, P, P], I32),
+        "dflash_tree_attention_workspace_size": ([I32, I32, I32, I32, I32, PSZ], I32),
+        "dflash_tree_attention": ([P, I64, I64, I32, ctypes.POINTER(KV), I32, I32, I32, I32, I32, P, P, I64, I64, P, P,
+                                   ctypes.c_float, P, P, P, SZ, P], I32),
+        "dflash_tree_accept": ([P, P, P, P, I32, I32, I32, P, P, P, P, P, P], I32),
+        "dflash_tree_commit_workspace_size": ([I32, PSZ], I32),
+        "dflash_tree_commit": ([ctypes.POINTER(KV), I32, I32, I32, I32, P, P, I64, I64, I64, P, P, I32, P, I64, P, P, P,
+                                SZ, P], I32),
         "dflash_kv_commit": ([ctypes.POINTER(Weights), ctypes.POINTER(KV), P, I32, P, P, SZ, P], I32),
         "dflash_commit_draft_block": ([ctypes.POINTER(Weights), ctypes.POINTER(KV), P, I32, P, P, P, P, P, P, SZ, P],
                                       I32),
@@ -514,8 +527,196 @@ def dflash_distill_backward(logits, t_val, t_idx, stats, grad_loss, dlogits, t_l
     _on(dev, stream, fn, load_library().dflash_distill_backward, *args, float(temperature), st, g, dz, ldd)
 
 
+def dflash_adjust_logits(logits, out, hist=None, n_hist=None, n_prompt=None, draft=None, path=None, repetition=None,
+                         frequency=None, presence=None, bias_idx=None, bias_val=None, allow=None, allow_row=None,
+                         stream=None):
+    """Penalties for repeated tokens, biases and grammar masks on rows of logits
+    [b][R][V] (fp32/fp16/bf16; [rows][V]: one row a sequence), written to out
+    (same dtype and shape; may be logits itself).  hist int32 [b][H] (rows may
+    be apart), n_hist and n_prompt int32 [b]; draft int32 [b][D] with path int32
+    [b][R][(D + 31) // 32] bits (None: row r follows drafts 0..r-1); repetition,
+    frequency, presence fp32 [b]; bias_idx int32 / bias_val fp32 [b][K]; allow
+    int32 [masks][words] bits (rows may be apart), allow_row int32 [b][R] (-1:
+    no grammar; None: row r of sequence j has mask j R + r)."""
+    fn = "dflash_adjust_logits"
+    if logits.dim() == 2:
+        logits, out = logits.unsqueeze(1), out.unsqueeze(1) if out.dim() == 2 else out
+        allow_row = allow_row.unsqueeze(1) if allow_row is not None and allow_row.dim() == 1 else allow_row
+    dt = _row_dtype(fn, logits)
+    ld = _row_shape(fn, logits, 3)
+    torch, dev, shape = _torch(), logits.get_device(), logits.shape
+    b, R, V = shape
+    if out.dtype != logits.dtype or out.get_device() != dev or out.shape != shape:
+        raise ValueError(f"{fn}: out must have the logits' dtype, device and shape")
+    ld_out = _row_shape(fn, out, 3)
+    i32, f32 = torch.int32, torch.float32
+    hp, H, ld_h = None, 0, 0
+    if hist is not None:
+        if hist.dtype != i32 or hist.get_device() != dev or hist.dim() != 2 or hist.shape[0] != b:
+            raise ValueError(f"{fn}: hist must be an int32 tensor [b][H] on cuda:{dev}")
+        ld_h, H = _row_shape(fn, hist, 2), hist.shape[1]
+        hp = hist.data_ptr()
+    elif n_hist is not None or n_prompt is not None:
+        raise ValueError(f"{fn}: n_hist and n_prompt need hist")
+    nh, np_ = _need(fn, dev, i32, (b,), n_hist=n_hist, n_prompt=n_prompt)
+    D = 0 if draft is None else draft.shape[-1]
+    if path is not None and D == 0:
+        raise ValueError(f"{fn}: path needs draft")
+    dr, = _need(fn, dev, i32, (b, D), draft=draft)
+    pt, = _need(fn, dev, i32, (b, R, (D + 31) // 32), path=path)
+    rho, fr, pr = _need(fn, dev, f32, (b,), repetition=repetition, frequency=frequency, presence=presence)
+    K = 0 if bias_idx is None else bias_idx.shape[-1]
+    bi, = _need(fn, dev, i32, (b, K), bias_idx=bias_idx)
+    bv, = _need(fn, dev, f32, (b, K), bias_val=bias_val)
+    ap, n_allow, ld_a = None, 0, 0
+    if allow is not None:
+        if allow.dtype != i32 or allow.get_device() != dev or allow.dim() != 2 or allow.shape[1] < (V + 31) // 32:
+            raise ValueError(f"{fn}: allow must be an int32 tensor [masks][at least {(V + 31) // 32} words] on cuda:{dev}")
+        ld_a, n_allow = _row_shape(fn, allow, 2), allow.shape[0]
+        if allow_row is None and n_allow < b * R:
+            raise ValueError(f"{fn}: without allow_row, allow needs a mask a row")
+        ap = allow.data_ptr()
+    ar, = _need(fn, dev, i32, (b, R), allow_row=allow_row)
+    _on(dev, stream, fn, load_library().dflash_adjust_logits, logits.data_ptr(), dt, b, R, V, ld, out.data_ptr(), ld_out,
+        hp, ld_h, H, nh, np_, dr, D, pt, rho, fr, pr, bi, bv, K, ap, n_allow, ld_a, ar)
+
+
+# ---------------------------------------------------------- a tree of drafts ----
+def _tree_shape(fn, parent):
+    if parent.dim() != 2 or not parent.is_cuda or 0 in parent.shape:
+        raise ValueError(f"{fn}: expected a non-empty 2-D CUDA tensor [b][N]")
+    _torch()
+    return parent.get_device(), *parent.shape
+
+
+def dflash_tree_mask(parent, mask_out, n_nodes=None, depth_out=None, stream=None):
+    """Ancestor bits mask_out int32 [b][N][(N + 31) // 32] and depths depth_out
+    int32 [b][N] (may be None) of trees given by parent int32 [b][N] (-1: a
+    root); n_nodes int32 [b] (None: all N)."""
+    fn = "dflash_tree_mask"
+    dev, b, N = _tree_shape(fn, parent)
+    i32 = _torch().int32
+    pa, de = _need(fn, dev, i32, (b, N), parent=parent, depth_out=depth_out)
+    ma, = _need(fn, dev, i32, (b, N, (N + 31) // 32), mask_out=mask_out)
+    nn, = _need(fn, dev, i32, (b,), n_nodes=n_nodes)
+    _on(dev, stream, fn, load_library().dflash_tree_mask, pa, nn, b, N, ma, de)
+
+
+@functools.lru_cache(maxsize=256)
+def dflash_tree_attention_workspace_size(b: int, N: int, nq: int, nkv: int, d: int) -> int:
+    n = ctypes.c_size_t(0)
+    _check("dflash_tree_attention_workspace_size", load_library().dflash_tree_attention_workspace_size(
+        b, N, nq, nkv, d, ctypes.byref(n)))
+    return n.value
+
+
+def _heads(fn, name, t, dev, dtype, shape):
+    """Pointer and strides (all but the last two dimensions') of a tensor whose
+    heads lie side by side: [..., heads, d]."""
+    if t.dtype != dtype or t.get_device() != dev or t.shape != shape or t.stride(-1) != 1 or \
+            (shape[-2] > 1 and t.stride(-2) != shape[-1]):
+        raise ValueError(f"{fn}: {name} must be a {dtype} tensor of shape {tuple(shape)} on cuda:{dev} with a token's "
+                         "heads side by side")
+    return t.data_ptr(), [0 if n == 1 else s for n, s in zip(shape[:-2], t.stride())]
+
+
+def dflash_tree_attention(q, kv: "KVCache", layer: int, k_tree, v_tree, mask, out, n_nodes=None, lse_out=None,
+                          scale: Optional[float] = None, ws=None, stream=None):
+    """Attention of the nodes q [b][N][nq][d] (fp16/bf16, the cache's dtype) over
+    layer `layer` of kv and the nodes' own k_tree, v_tree [b][N][nkv][d] (views of
+    one projection's output will do) as mask int32 [b][N][(N + 31) // 32] says
+    (None: node i sees nodes 0..i).  out [b][N][nq][d]; lse_out fp32 [b][N][nq];
+    scale: 1 / sqrt(d).  ws: uint8 workspace of
+    dflash_tree_attention_workspace_size bytes (allocated here when not given)."""
+    fn = "dflash_tree_attention"
+    torch = _torch()
+    if q.dim() != 4 or not q.is_cuda or 0 in q.shape or q.dtype not in (torch.float16, torch.bfloat16):
+        raise ValueError(f"{fn}: q must be a non-empty float16 or bfloat16 CUDA tensor [b][N][nq][d]")
+    dev, dt = q.get_device(), q.dtype
+    b, N, nq, d = q.shape
+    L, kb, nkv, cap, kd = kv.k.shape
+    if kv.k.dtype != dt or kv.k.get_device() != dev or kb != b or kd != d or not 0 <= layer < L:
+        raise ValueError(f"{fn}: kv must be a {dt} cache of {b} sequences and {d} dimensions on cuda:{dev}, with a layer "
+                         f"{layer}")
+    qp, (qs, qt) = _heads(fn, "q", q, dev, dt, (b, N, nq, d))
+    kp, ks = _heads(fn, "k_tree", k_tree, dev, dt, (b, N, nkv, d))
+    vp, vs = _heads(fn, "v_tree", v_tree, dev, dt, (b, N, nkv, d))
+    if ks != vs:
+        raise ValueError(f"{fn}: k_tree and v_tree must have the same strides")
+    op, = _need(fn, dev, dt, (b, N, nq, d), out=out)
+    lp, = _need(fn, dev, torch.float32, (b, N, nq), lse_out=lse_out)
+    mp, = _need(fn, dev, torch.int32, (b, N, (N + 31) // 32), mask=mask)
+    nn, = _need(fn, dev, torch.int32, (b,), n_nodes=n_nodes)
+    wp, wn, ws = _workspace(fn, ws, dflash_tree_attention_workspace_size(b, N, nq, nkv, d), dev, stream)
+    _on(dev, stream, fn, load_library().dflash_tree_attention, qp, qs, qt,
+        DTYPE_F16 if dt == torch.float16 else DTYPE_BF16, ctypes.byref(kv.c), layer, N, nq, nkv, d, kp, vp, *ks, mp, nn,
+        d ** -0.5 if scale is None else scale, op, lp, wp, wn)
+
+
+def dflash_tree_accept(tok, tree_tok, parent, n_out, corr_out, path_out, n_nodes=None, emitted=None, next_tok=None,
+                       stream=None):
+    """The accepted path of each tree: tok int32 [b][N] the target's token at each
+    node, tree_tok and parent int32 [b][N]; n_out, corr_out, next_tok int32 [b],
+    path_out and emitted int32 [b][R], R <= N."""
+    fn = "dflash_tree_accept"
+    dev, b, N = _tree_shape(fn, parent)
+    i32 = _torch().int32
+    tk, tt, pa = _need(fn, dev, i32, (b, N), tok=tok, tree_tok=tree_tok, parent=parent)
+    nn, no, co, nx = _need(fn, dev, i32, (b,), n_nodes=n_nodes, n_out=n_out, corr_out=corr_out, next_tok=next_tok)
+    R = path_out.shape[-1]
+    po, em = _need(fn, dev, i32, (b, R), path_out=path_out, emitted=emitted)
+    _on(dev, stream, fn, load_library().dflash_tree_accept, tk, tt, pa, nn, b, N, R, no, co, po, em, nx)
+
+
+def dflash_tree_commit_workspace_size(b: int) -> int:
+    n = ctypes.c_size_t(0)
+    _check("dflash_tree_commit_workspace_size", load_library().dflash_tree_commit_workspace_size(b, ctypes.byref(n)))
+    return n.value
+
+
+def dflash_tree_commit(kv: "KVCache", k_tree, v_tree, path, n, hid=None, hid_out=None, len_out=None, ws=None,
+                       stream=None):
+    """Append the accepted nodes' k_tree, v_tree [L][b][N][nkv][d] to every layer
+    of kv: path int32 [b][R], n int32 [b] of dflash_tree_accept.  hid [b][N][cols]
+    (16-bit, contiguous): its accepted rows go to hid_out [b][R][cols].  len_out
+    int32 [b]: the new lengths (None: kv.len itself advances).  ws: zero-filled
+    uint8 workspace of dflash_tree_commit_workspace_size bytes (allocated here
+    when not given)."""
+    fn = "dflash_tree_commit"
+    torch = _torch()
+    L, b, nkv, cap, d = kv.k.shape
+    dev, dt = kv.k.get_device(), kv.k.dtype
+    if path.dim() != 2 or k_tree.dim() != 5:
+        raise ValueError(f"{fn}: expected path [b][R] and k_tree [L][b][N][nkv][d]")
+    N, R = k_tree.shape[2], path.shape[1]
+    kp, ks = _heads(fn, "k_tree", k_tree, dev, dt, (L, b, N, nkv, d))
+    vp, vs = _heads(fn, "v_tree", v_tree, dev, dt, (L, b, N, nkv, d))
+    if ks != vs:
+        raise ValueError(f"{fn}: k_tree and v_tree must have the same strides")
+    pa, = _need(fn, dev, torch.int32, (b, R), path=path)
+    nn, lo = _need(fn, dev, torch.int32, (b,), n=n, len_out=len_out)
+    hp = ho = None
+    cols = 0
+    if hid is not None or hid_out is not None:
+        if hid is None or hid_out is None or hid.dim() != 3 or hid.element_size() != 2:
+            raise ValueError(f"{fn}: hid [b][N][cols] of a 16-bit dtype and hid_out go together")
+        cols = hid.shape[2]
+        hp, = _need(fn, dev, hid.dtype, (b, N, cols), hid=hid)
+        ho, = _need(fn, dev, hid.dtype, (b, R, cols), hid_out=hid_out)
+    wp, wn, ws = _workspace(fn, ws, dflash_tree_commit_workspace_size(b), dev, stream)
+    _on(dev, stream, fn, load_library().dflash_tree_commit, ctypes.byref(kv.c), L, nkv, d, N, kp, vp, *ks, pa, nn, R, hp,
+        cols, ho, lo, wp, wn)
+
+
+def _drafter_cache(fn, kv):
+    """A drafter's cache is fp16 (a target's may be bf16)."""
+    if kv.k.dtype != _torch().float16:
+        raise ValueError(f"{fn}: a drafter's cache must be float16")
+
+
 def dflash_draft_block(model: "DeviceDrafter", kv: "KVCache", last_tok, draft_out, ws, hidden=None, logits=None,
                        stream=None):
+    _drafter_cache("dflash_draft_block", kv)
     _check("dflash_draft_block", load_library().dflash_draft_block(
         ctypes.byref(model.c), ctypes.byref(kv.c), last_tok.data_ptr(), draft_out.data_ptr(), _ptr(hidden),
         _ptr(logits), ws.data_ptr(), ws.numel(), _stream(stream)))
@@ -523,6 +724,7 @@ def dflash_draft_block(model: "DeviceDrafter", kv: "KVCache", last_tok, draft_ou
 
 def dflash_kv_commit(model: "DeviceDrafter", kv: "KVCache", hid, n, ws, stream=None):
     """hid fp16 [b][rows_per_seq][k*H]; n int32 [b] (device)."""
+    _drafter_cache("dflash_kv_commit", kv)
     rps = hid.shape[1]
     _check("dflash_kv_commit", load_library().dflash_kv_commit(
         ctypes.byref(model.c), ctypes.byref(kv.c), hid.data_ptr(), rps, n.data_ptr(), ws.data_ptr(), ws.numel(),
@@ -533,6 +735,7 @@ def dflash_commit_draft_block(model: "DeviceDrafter", kv: "KVCache", hid, n, las
                               logits=None, stream=None):
     """dflash_kv_commit(hid, n) and dflash_draft_block(last_tok) in one pass.
     hid fp16 [b][rows_per_seq][k*H], n int32 [b], last_tok int32 [b]."""
+    _drafter_cache("dflash_commit_draft_block", kv)
     rps = hid.shape[1]
     _check("dflash_commit_draft_block", load_library().dflash_commit_draft_block(
         ctypes.byref(model.c), ctypes.byref(kv.c), hid.data_ptr(), rps, n.data_ptr(), last_tok.data_ptr(),
@@ -635,15 +838,29 @@ class DeviceDrafter:
 
 
 class KVCache:
-    """Draft KV cache [L][b][nkv][cap][d] fp16 (K after norm + RoPE) and
-    per-sequence lengths (device int32)."""
+    """KV cache [L][b][nkv][cap][d] (K after norm + RoPE) and per-sequence lengths
+    (device int32): a drafter's, fp16 and zero-filled, or that of a target over
+    which trees are verified: fp16 or bf16, and made of the target's own tensors
+    where k, v [L][b][nkv][cap][d] and len int32 [b] are given.  cfg: anything
+    with L, nkv and d."""
 
-    def __init__(self, cfg, b: int, cap: int, device="cuda"):
+    def __init__(self, cfg, b: int, cap: int, device="cuda", dtype=None, k=None, v=None, len=None):
         torch = _torch()
         shape = (cfg.L, b, cfg.nkv, cap, cfg.d)
-        self.k = torch.zeros(shape, dtype=torch.float16, device=device)
-        self.v = torch.zeros(shape, dtype=torch.float16, device=device)
-        self.len = torch.zeros(b, dtype=torch.int32, device=device)
+        if (k is None) != (v is None):
+            raise ValueError("KVCache: k and v go together")
+        if k is not None:
+            dtype, device = k.dtype if dtype is None else dtype, k.device
+        dtype = torch.float16 if dtype is None else dtype
+        if dtype not in (torch.float16, torch.bfloat16):
+            raise ValueError("KVCache: dtype must be float16 or bfloat16")
+        for name, t, dt, want in (("k", k, dtype, shape), ("v", v, dtype, shape), ("len", len, torch.int32, (b,))):
+            if t is not None and (t.dtype != dt or t.shape != want or not t.is_contiguous() or not t.is_cuda
+                                  or (k is not None and t.device != k.device)):
+                raise ValueError(f"KVCache: {name} must be a contiguous {dt} CUDA tensor of shape {tuple(want)}")
+        self.k = torch.zeros(shape, dtype=dtype, device=device) if k is None else k
+        self.v = torch.zeros(shape, dtype=dtype, device=device) if v is None else v
+        self.len = torch.zeros(b, dtype=torch.int32, device=self.k.device) if len is None else len
         self.b, self.cap = b, cap
         self.c = KV(self.k.data_ptr(), self.v.data_ptr(), self.len.data_ptr(), b, cap)
 

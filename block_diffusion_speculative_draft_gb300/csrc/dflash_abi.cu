@@ -648,6 +648,190 @@ int32_t dflash_distill_backward(const void* logits, int32_t dtype, int64_t rows,
                       const_cast<float*>(stats), dlogits, ldd, true, stream);
 }
 
+int32_t dflash_adjust_logits(const void* logits, int32_t dtype, int64_t b, int32_t R, int64_t V, int64_t ld, void* out,
+                             int64_t ld_out, const int32_t* hist, int64_t ld_hist, int32_t H, const int32_t* n_hist,
+                             const int32_t* n_prompt, const int32_t* draft, int32_t D, const uint32_t* path,
+                             const float* repetition, const float* frequency, const float* presence,
+                             const int32_t* bias_idx, const float* bias_val, int32_t K, const uint32_t* allow,
+                             int64_t n_allow, int64_t ld_allow, const int32_t* allow_row, void* stream) {
+  if (b < 1 || R < 1 || R > kTreeMax) return DFLASH_EINVAL;
+  if (b >= (int64_t)1 << 28) return DFLASH_EUNSUPPORTED;
+  if (int r = check_rows(logits, dtype, b * R, V, ld)) return r;
+  if (int r = check_rows(out, dtype, b * R, V, ld_out)) return r;
+  if (out == logits && ld_out != ld && b * R > 1) return DFLASH_EINVAL;
+  if (hist && (!n_hist || H < 1 || ld_hist < H)) return DFLASH_EINVAL;
+  if (hist && (H > kAdjustMaxHist || ld_hist > ((int64_t)1 << 62) / b)) return DFLASH_EUNSUPPORTED;
+  if (draft ? D < 1 || D > kTreeMax : path != nullptr) return DFLASH_EINVAL;
+  if (!bias_idx != !bias_val || (bias_idx && K < 1)) return DFLASH_EINVAL;
+  if (bias_idx && K > kAdjustMaxBias) return DFLASH_EUNSUPPORTED;
+  if (allow ? n_allow < 1 || ld_allow < (V + 31) / 32 : allow_row != nullptr) return DFLASH_EINVAL;
+  if (allow && ld_allow > ((int64_t)1 << 60) / n_allow) return DFLASH_EUNSUPPORTED;
+  AdjustArgs a;
+  memset(&a, 0, sizeof(a));
+  a.logits = logits;
+  a.out = out;
+  a.V = V;
+  a.ld = ld;
+  a.ld_out = ld_out;
+  a.R = R;
+  a.hist = hist;
+  a.ld_hist = ld_hist;
+  a.H = H;
+  a.n_hist = n_hist;
+  a.n_prompt = n_prompt;
+  a.draft = draft;
+  a.D = draft ? D : 0;
+  a.path = path;
+  a.repetition = repetition;
+  a.frequency = frequency;
+  a.presence = presence;
+  a.bias_idx = bias_idx;
+  a.bias_val = bias_val;
+  a.K = bias_idx ? K : 0;
+  a.allow = allow;
+  a.n_allow = n_allow;
+  a.ld_allow = ld_allow;
+  a.allow_row = allow_row;
+  if (!(a.status = status_ptr())) return DFLASH_ECUDA;
+  return map_err(adjust_logits(a, dtype, b, static_cast<cudaStream_t>(stream)));
+}
+
+// Checks common to the calls on trees.
+static int check_tree(int32_t b, int32_t N) {
+  if (b < 1 || N < 1 || N > kTreeMax) return DFLASH_EINVAL;
+  return b > 65535 ? DFLASH_EUNSUPPORTED : DFLASH_OK;
+}
+// A stride of 16-bit elements between 16-byte aligned places.
+static bool tree_stride(int64_t s) { return s >= 0 && s % 8 == 0 && s < (int64_t)1 << 44; }
+
+int32_t dflash_tree_mask(const int32_t* parent, const int32_t* n_nodes, int32_t b, int32_t N, uint32_t* mask,
+                         int32_t* depth_out, void* stream) {
+  if (int r = check_tree(b, N)) return r;
+  if (!parent || !mask) return DFLASH_EINVAL;
+  TreeMaskArgs a{parent, n_nodes, N, mask, depth_out, status_ptr()};
+  if (!a.status) return DFLASH_ECUDA;
+  return map_err(tree_mask(a, b, static_cast<cudaStream_t>(stream)));
+}
+
+static int check_tree_heads(int32_t b, int32_t N, int32_t nq, int32_t nkv, int32_t d) {
+  if (int r = check_tree(b, N)) return r;
+  if (nq < 1 || nkv < 1) return DFLASH_EINVAL;
+  if ((d != 64 && d != 128) || nq % nkv || (int64_t)nq * d > 1 << 24 || (int64_t)nkv * b > 1 << 22)
+    return DFLASH_EUNSUPPORTED;
+  // CTAs of the launch that joins parts: 16 query rows of a kv head each
+  if ((int64_t)b * nkv * (((int64_t)N * (nq / nkv) + 63) / 64) * 4 > 0x7fffffffll) return DFLASH_EUNSUPPORTED;
+  return DFLASH_OK;
+}
+
+int32_t dflash_tree_attention_workspace_size(int32_t b, int32_t N, int32_t nq, int32_t nkv, int32_t d, size_t* bytes) {
+  if (!bytes) return DFLASH_EINVAL;
+  if (int r = check_tree_heads(b, N, nq, nkv, d)) return r;
+  *bytes = tree_attn_ws_bytes(b, N, nq, nkv, d);
+  return DFLASH_OK;
+}
+
+int32_t dflash_tree_attention(const void* q, int64_t q_seq, int64_t q_tok, int32_t dtype, const dflash_kv* kv,
+                              int32_t layer, int32_t N, int32_t nq, int32_t nkv, int32_t d, const void* k_tree,
+                              const void* v_tree, int64_t t_seq, int64_t t_tok, const uint32_t* mask,
+                              const int32_t* n_nodes, float scale, void* out, float* lse_out, void* ws,
+                              size_t ws_bytes, void* stream) {
+  if (int r = check_kv(kv)) return r;
+  if (int r = check_tree_heads(kv->b, N, nq, nkv, d)) return r;
+  if (dtype != DFLASH_DTYPE_F16 && dtype != DFLASH_DTYPE_BF16) return DFLASH_EINVAL;
+  if (!q || !k_tree || !v_tree || !out || layer < 0 || !(scale > 0.f) || !(scale < INFINITY)) return DFLASH_EINVAL;
+  if (!aligned16(q) || !aligned16(k_tree) || !aligned16(v_tree) || !aligned16(out)) return DFLASH_EINVAL;
+  if (!tree_stride(q_seq) || !tree_stride(q_tok) || !tree_stride(t_seq) || !tree_stride(t_tok)) return DFLASH_EINVAL;
+  if (!ws || ws_bytes < tree_attn_ws_bytes(kv->b, N, nq, nkv, d) || !aligned16(ws)) return DFLASH_EWORKSPACE;
+  TreeAttnArgs a;
+  memset(&a, 0, sizeof(a));
+  const size_t off = (size_t)layer * kv->b * nkv * kv->cap * d;
+  a.q = static_cast<const uint16_t*>(q);
+  a.kt = static_cast<const uint16_t*>(k_tree);
+  a.vt = static_cast<const uint16_t*>(v_tree);
+  a.q_seq = q_seq;
+  a.q_tok = q_tok;
+  a.t_seq = t_seq;
+  a.t_tok = t_tok;
+  a.kc = kv->k + off;
+  a.vc = kv->v + off;
+  a.len = kv->len;
+  a.n_nodes = n_nodes;
+  a.mask = mask;
+  a.out = static_cast<uint16_t*>(out);
+  a.lse = lse_out;
+  a.b = kv->b;
+  a.N = N;
+  a.nq = nq;
+  a.nkv = nkv;
+  a.d = d;
+  a.cap = kv->cap;
+  a.scale = scale;
+  a.ws = ws;
+  if (!(a.status = status_ptr())) return DFLASH_ECUDA;
+  return map_err(tree_attention(a, dtype, static_cast<cudaStream_t>(stream)));
+}
+
+int32_t dflash_tree_accept(const int32_t* tok, const int32_t* tree_tok, const int32_t* parent, const int32_t* n_nodes,
+                           int32_t b, int32_t N, int32_t R, int32_t* n_out, int32_t* corr_out, int32_t* path_out,
+                           int32_t* emitted_out, int32_t* next_tok_out, void* stream) {
+  if (int r = check_tree(b, N)) return r;
+  if (!tok || !tree_tok || !parent || !n_out || !corr_out || !path_out || R < 1 || R > N) return DFLASH_EINVAL;
+  TreeAcceptArgs a{tok,   tree_tok, parent,   n_nodes,     N,            R,
+                   n_out, corr_out, path_out, emitted_out, next_tok_out, status_ptr()};
+  if (!a.status) return DFLASH_ECUDA;
+  return map_err(tree_accept(a, b, static_cast<cudaStream_t>(stream)));
+}
+
+int32_t dflash_tree_commit_workspace_size(int32_t b, size_t* bytes) {
+  if (!bytes || b < 1) return DFLASH_EINVAL;
+  if (b > 65535) return DFLASH_EUNSUPPORTED;
+  *bytes = (size_t)b * sizeof(int);
+  return DFLASH_OK;
+}
+
+int32_t dflash_tree_commit(const dflash_kv* kv, int32_t L, int32_t nkv, int32_t d, int32_t N, const void* k_tree,
+                           const void* v_tree, int64_t t_layer, int64_t t_seq, int64_t t_tok, const int32_t* path,
+                           const int32_t* n, int32_t R, const uint16_t* hid, int64_t hid_cols, uint16_t* hid_out,
+                           int32_t* len_out, void* ws, size_t ws_bytes, void* stream) {
+  if (int r = check_kv(kv)) return r;
+  if (int r = check_tree(kv->b, N)) return r;
+  if (L < 1 || nkv < 1 || d < 1 || R < 1 || R > N || !k_tree || !v_tree || !path || !n) return DFLASH_EINVAL;
+  if (d % 8 || (int64_t)nkv * d > 1 << 24 || L > 1 << 16) return DFLASH_EUNSUPPORTED;
+  if (!aligned16(k_tree) || !aligned16(v_tree) || !tree_stride(t_layer) || !tree_stride(t_seq) || !tree_stride(t_tok))
+    return DFLASH_EINVAL;
+  if (!hid != !hid_out) return DFLASH_EINVAL;
+  if (hid && (hid_cols < 8 || hid_cols % 8 || hid_cols > 1 << 24 || !aligned16(hid) || !aligned16(hid_out)))
+    return DFLASH_EINVAL;
+  const bool in_place = !len_out || len_out == kv->len;
+  if (!ws || ws_bytes < (size_t)kv->b * sizeof(int) || (reinterpret_cast<uintptr_t>(ws) & 3)) return DFLASH_EWORKSPACE;
+  TreeCommitArgs a;
+  memset(&a, 0, sizeof(a));
+  a.k = kv->k;
+  a.v = kv->v;
+  a.len = kv->len;
+  a.len_out = in_place ? kv->len : len_out;
+  a.b = kv->b;
+  a.cap = kv->cap;
+  a.L = L;
+  a.nkv = nkv;
+  a.d = d;
+  a.N = N;
+  a.R = R;
+  a.k_tree = static_cast<const uint16_t*>(k_tree);
+  a.v_tree = static_cast<const uint16_t*>(v_tree);
+  a.ld_layer = t_layer;
+  a.ld_seq = t_seq;
+  a.ld_tok = t_tok;
+  a.path = path;
+  a.n = n;
+  a.hid = hid;
+  a.hid_out = hid_out;
+  a.hid_units = hid ? (int)(hid_cols / 8) : 0;
+  a.tickets = in_place ? static_cast<int*>(ws) : nullptr;
+  if (!(a.status = status_ptr())) return DFLASH_ECUDA;
+  return map_err(tree_commit(a, static_cast<cudaStream_t>(stream)));
+}
+
 int32_t dflash_kv_commit(const dflash_weights* w, const dflash_kv* kv, const uint16_t* hid, int32_t rows_per_seq,
                          const int32_t* n, void* ws, size_t ws_bytes, void* stream) {
   if (int r = check_weights(w)) return r;

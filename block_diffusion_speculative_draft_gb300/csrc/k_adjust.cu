@@ -1,0 +1,305 @@
+// k_adjust.cu — what a request's history, biases and grammar do to rows of
+// logits before a token is drawn from them.  For entry v of a row, c the
+// generated tokens equal to v (the row's own path of drafts among them):
+//   x = z;  v in the prompt or c > 0: x = x > 0 ? x / rho : x rho
+//   x -= frequency c + presence [c > 0];  x += bias[v];  not allowed: -inf
+// in fp32, rounded once to the rows' type.
+//
+// Bound by HBM: a row is read and written once.  One CTA takes one segment of
+// the vocabulary for all rows of a sequence, so the history is counted once a
+// segment and not once a row: a scan of the whole history (L2 after the first
+// CTA) into counters in shared memory, and one bit an entry that tells whether
+// anything but the grammar touches it.  Rows then stream by with two tests a
+// 16-byte pack (those bits, the grammar's bits); most packs pass unchanged.
+// A row's path adds to few entries: they are marked in the counters, and the
+// path is walked where a marked entry comes by, so rows need no barrier
+// between them.
+#include "kernels.h"
+#include "rows.cuh"
+
+namespace dfl {
+
+namespace {
+
+constexpr int kDevBadLength = 0x4, kDevBadParam = 0x8;
+constexpr int kThreads = 256;
+constexpr int kFlight = 4;  // packs a thread has in flight
+
+// A counter: generated tokens (bits 0-19), in the prompt, among the drafts,
+// and, in bits 22-31, kAdjustMaxBias less the place of the entry's bias in the
+// request's list (0: none).
+constexpr uint32_t kCount = (1u << 20) - 1, kPrompt = 1u << 20, kDraft = 1u << 21;
+constexpr int kSlotShift = 22;
+
+template <typename T>
+struct Bits;
+template <>
+struct Bits<float> {
+  static constexpr uint32_t ninf = 0xff800000u, nan = 0x7fffffffu;
+};
+template <>
+struct Bits<__half> {
+  static constexpr uint32_t ninf = 0xfc00u, nan = 0x7fffu;
+};
+template <>
+struct Bits<__nv_bfloat16> {
+  static constexpr uint32_t ninf = 0xff80u, nan = 0x7fffu;
+};
+template <typename T>
+__device__ __forceinline__ T of_bits(uint32_t b) {
+  if constexpr (sizeof(T) == 4) {
+    return __uint_as_float(b);
+  } else {
+    T v;
+    *reinterpret_cast<uint16_t*>(&v) = (uint16_t)b;
+    return v;
+  }
+}
+
+// n <= 16 bits of a bit row from bit `at`; words past `words` are not read.
+__device__ __forceinline__ uint32_t bits_at(const uint32_t* w, int64_t at, int n, int64_t words) {
+  const int64_t i = at >> 5;
+  const int s = (int)(at & 31);
+  uint32_t v = w[i] >> s;
+  if (s + n > 32 && i + 1 < words) v |= w[i + 1] << (32 - s);
+  return v & ((1u << n) - 1u);
+}
+
+struct Shared {
+  float rho, freq, pres;
+  int bad;     // nothing of the sequence can be worked
+  int repeat;  // a biased entry is listed twice
+  int D;
+  int bias_idx[kAdjustMaxBias];
+  float bias_val[kAdjustMaxBias];
+  int draft[kTreeMax];
+  int allow_row[kTreeMax];  // -1: no grammar, -2: out of range
+};
+
+// The entries of a pack that something touches (bits of `touch`); at: the
+// pack's first entry in the segment that starts at s0; path: bits of the
+// drafts that the row follows, null: the first `follows`.
+template <typename T>
+__device__ __noinline__ uint4 touched_pack(uint4 raw, uint32_t touch, int at, int s0, const uint32_t* count,
+                                           const Shared* sh, const uint32_t* path, int follows) {
+  constexpr int E = 16 / sizeof(T);
+  T* x = reinterpret_cast<T*>(&raw);
+#pragma unroll
+  for (int i = 0; i < E; ++i) {
+    if (!(touch >> i & 1)) continue;
+    const uint32_t w = count[at + i];
+    uint32_t c = w & kCount;
+    if (w & kDraft) {
+      const int v = s0 + at + i;
+      if (path) {
+        for (int k = 0; k * 32 < sh->D; ++k)
+          for (uint32_t m = path[k]; m; m &= m - 1) {
+            const int d = k * 32 + __ffs(m) - 1;
+            c += d < sh->D && sh->draft[d] == v;
+          }
+      } else {
+        for (int d = 0; d < follows; ++d) c += sh->draft[d] == v;
+      }
+    }
+    float f = to_f32(x[i]);
+    if (c || (w & kPrompt)) f = f > 0.f ? f / sh->rho : f * sh->rho;
+    if (c) f = f - sh->freq * (float)c - sh->pres;
+    const uint32_t slot = w >> kSlotShift;
+    if (slot) f += sh->bias_val[kAdjustMaxBias - slot];
+    x[i] = from_f32<T>(f);
+  }
+  return raw;
+}
+
+template <typename T, bool kAligned>
+__global__ void __launch_bounds__(kThreads) adjust_kernel(const AdjustArgs a) {
+  constexpr int E = 16 / sizeof(T);  // entries of a pack
+  extern __shared__ uint32_t s_dyn[];
+  uint32_t* const s_count = s_dyn;             // [seg]
+  uint32_t* const s_touch = s_dyn + a.seg;     // [seg / 32 + 1]
+  __shared__ Shared sh;
+  pdl_wait();
+  const int tid = threadIdx.x;
+  const int64_t j = blockIdx.x / a.nseg;
+  const int64_t s0 = (int64_t)(blockIdx.x % a.nseg) * a.seg;
+  const int64_t s1 = s0 + a.seg < a.V ? s0 + a.seg : a.V;
+  const uint32_t len = (uint32_t)(s1 - s0);
+
+  // ---- the sequence's request ----
+  const int nh = a.hist ? a.n_hist[j] : 0;
+  const int np = a.hist && a.n_prompt ? a.n_prompt[j] : 0;
+  if (tid == 0) {
+    sh.rho = a.repetition ? a.repetition[j] : 1.f;
+    sh.freq = a.frequency ? a.frequency[j] : 0.f;
+    sh.pres = a.presence ? a.presence[j] : 0.f;
+    int why = 0;
+    if (!(sh.rho > 0.f && sh.rho < INFINITY && fabsf(sh.freq) < INFINITY && fabsf(sh.pres) < INFINITY))
+      why = kDevBadParam;
+    if (np < 0 || np > nh || nh > a.H) why |= kDevBadLength;
+    sh.bad = why;
+    sh.repeat = 0;
+    sh.D = a.D;
+  }
+  for (int i = tid; i < a.seg + a.seg / 32 + 1; i += kThreads) s_dyn[i] = 0;
+  for (int i = tid; i < a.K; i += kThreads) {
+    sh.bias_idx[i] = a.bias_idx[j * a.K + i];
+    sh.bias_val[i] = a.bias_val[j * a.K + i];
+  }
+  for (int i = tid; i < a.D; i += kThreads) sh.draft[i] = a.draft[j * a.D + i];
+  for (int i = tid; i < a.R; i += kThreads) {
+    int64_t r = -1;
+    if (a.allow) {
+      r = a.allow_row ? a.allow_row[j * a.R + i] : j * a.R + i;
+      if (r < -1 || r >= a.n_allow) {
+        r = -2;
+        if (s0 == 0) atomicOr(a.status, kDevBadParam);
+      }
+    }
+    sh.allow_row[i] = (int)r;
+  }
+  __syncthreads();
+  auto mark = [&](uint32_t e) { atomicOr(&s_touch[e >> 5], 1u << (e & 31)); };
+  if (!sh.bad) {
+    const int* h = a.hist + j * a.ld_hist;
+    auto take = [&](int t, bool made) {
+      const uint32_t e = (uint32_t)t - (uint32_t)s0;  // below the segment, or negative: out of range
+      if (t < 0 || e >= len) return;
+      if (made) atomicAdd(&s_count[e], 1u);
+      else atomicOr(&s_count[e], kPrompt);
+      mark(e);
+    };
+    for (int i = tid; i < nh; i += kThreads * kFlight) {
+      int t[kFlight];
+#pragma unroll
+      for (int q = 0; q < kFlight; ++q) t[q] = i + q * kThreads < nh ? h[i + q * kThreads] : -1;
+#pragma unroll
+      for (int q = 0; q < kFlight; ++q) take(t[q], i + q * kThreads >= np);
+    }
+    for (int i = tid; i < a.D; i += kThreads) {
+      const int t = sh.draft[i];
+      const uint32_t e = (uint32_t)t - (uint32_t)s0;
+      if (t < 0 || e >= len) continue;
+      atomicOr(&s_count[e], kDraft);
+      mark(e);
+    }
+    // The counters' low parts are done before slots go above them: the largest
+    // number wins, so an entry belongs to the first that lists it.
+    __syncthreads();
+    for (int i = tid; i < a.K; i += kThreads) {
+      const int t = sh.bias_idx[i];
+      if (t < 0 || t >= a.V) continue;
+      if (!(sh.bias_val[i] < INFINITY)) atomicOr(&sh.bad, kDevBadParam);
+      const uint32_t e = (uint32_t)t - (uint32_t)s0;
+      if ((int64_t)t < s0 || e >= len) continue;
+      const uint32_t slot = (uint32_t)(kAdjustMaxBias - i) << kSlotShift;
+      const uint32_t low = s_count[e] & ((1u << kSlotShift) - 1u);
+      if (atomicMax(&s_count[e], slot | low) >> kSlotShift) sh.repeat = 1;
+      mark(e);
+    }
+    __syncthreads();
+    // an entry listed again adds up, in the list's order: the first of an entry
+    // writes the sum to its own place, which no other sum reads
+    if (sh.repeat)
+      for (int i = tid; i < a.K; i += kThreads) {
+        const int t = sh.bias_idx[i];
+        const uint32_t e = (uint32_t)t - (uint32_t)s0;
+        if (t < 0 || (int64_t)t < s0 || e >= len || s_count[e] >> kSlotShift != (uint32_t)(kAdjustMaxBias - i)) continue;
+        float sum = sh.bias_val[i];
+        for (int k = i + 1; k < a.K; ++k)
+          if (sh.bias_idx[k] == t) sum += sh.bias_val[k];
+        sh.bias_val[i] = sum;
+      }
+    __syncthreads();
+  }
+  const int bad = sh.bad;
+  if (bad && tid == 0 && s0 == 0) atomicOr(a.status, bad);
+
+  // ---- the rows ----
+  const int W = (a.D + 31) / 32;
+  const int64_t aw = (a.V + 31) / 32;
+  // packs of a row; an unaligned one is cut out of one pack more
+  const uint32_t ppr = kAligned ? (len + E - 1) / E : (len + E - 1) / E + 1;
+  const uint32_t packs = ppr * a.R;
+  for (uint32_t p0 = tid; p0 < packs; p0 += kThreads * kFlight) {
+    uint4 raw[kFlight];
+    int at[kFlight], row[kFlight];  // the pack's first entry in the segment (may be negative), its row
+    uint32_t ok[kFlight];
+#pragma unroll
+    for (int q = 0; q < kFlight; ++q) {
+      const uint32_t p = p0 + q * kThreads;
+      row[q] = -1;
+      if (p >= packs) continue;
+      const int r = (int)(p / ppr);
+      const T* in = static_cast<const T*>(a.logits) + (j * a.R + r) * a.ld + s0;
+      at[q] = (int)(p - r * ppr) * E - (kAligned ? 0 : (int)(((uintptr_t)in & 15) / sizeof(T)));
+      const int lo = at[q] < 0 ? -at[q] : 0, hi = at[q] + E > (int)len ? (int)len - at[q] : E;
+      if (lo >= hi) continue;
+      row[q] = r;
+      if (hi - lo == E) {
+        raw[q] = *reinterpret_cast<const uint4*>(in + at[q]);
+      } else {
+        T* x = reinterpret_cast<T*>(&raw[q]);
+#pragma unroll
+        for (int i = 0; i < E; ++i)
+          if (i >= lo && i < hi) x[i] = in[at[q] + i];
+      }
+      const int ar = sh.allow_row[r];
+      ok[q] = ((1u << (hi - lo)) - 1u) << lo;
+      if (ar >= 0) ok[q] = bits_at(a.allow + ar * a.ld_allow, s0 + at[q] + lo, hi - lo, aw) << lo;
+    }
+#pragma unroll
+    for (int q = 0; q < kFlight; ++q) {
+      if (row[q] < 0) continue;
+      const int r = row[q];
+      const int64_t n = j * a.R + r;
+      const int lo = at[q] < 0 ? -at[q] : 0, hi = at[q] + E > (int)len ? (int)len - at[q] : E;
+      T* x = reinterpret_cast<T*>(&raw[q]);
+      if (bad || sh.allow_row[r] == -2) {
+#pragma unroll
+        for (int i = 0; i < E; ++i) x[i] = of_bits<T>(Bits<T>::nan);
+      } else {
+        const uint32_t touch = ok[q] & (bits_at(s_touch, at[q] + lo, hi - lo, a.seg / 32 + 1) << lo);
+        if (touch)
+          raw[q] = touched_pack<T>(raw[q], touch, at[q], (int)s0, s_count, &sh, a.path ? a.path + n * W : nullptr,
+                                   r < a.D ? r : a.D);
+#pragma unroll
+        for (int i = 0; i < E; ++i)
+          if (!(ok[q] >> i & 1)) x[i] = of_bits<T>(Bits<T>::ninf);
+      }
+      T* out = static_cast<T*>(a.out) + n * a.ld_out + s0 + at[q];
+      if (hi - lo == E && (kAligned || ((uintptr_t)out & 15) == 0)) {
+        *reinterpret_cast<uint4*>(out) = raw[q];
+      } else {
+#pragma unroll
+        for (int i = 0; i < E; ++i)
+          if (i >= lo && i < hi) out[i] = x[i];
+      }
+    }
+  }
+}
+
+}  // namespace
+
+cudaError_t adjust_logits(const AdjustArgs& a0, int dtype, int64_t b, cudaStream_t st) {
+  AdjustArgs a = a0;
+  const int es = dtype == 0 ? 4 : 2;
+  // Segments: as long as they go (the history is scanned once a segment), but
+  // two CTAs an SM where the call has so much to share out.
+  a.seg = 8192;
+  while (a.seg > 1024 && b * ((a.V + a.seg - 1) / a.seg) < 2 * num_sms()) a.seg /= 2;
+  a.nseg = (unsigned)((a.V + a.seg - 1) / a.seg);
+  if (b * (int64_t)a.nseg > 0x7fffffffll) return cudaErrorInvalidValue;
+  const bool aligned = ((uintptr_t)a.logits & 15) == 0 && ((uintptr_t)a.out & 15) == 0 && a.ld * es % 16 == 0 &&
+                       a.ld_out * es % 16 == 0;
+  const void* fn;
+  if (dtype == 0) fn = aligned ? (const void*)adjust_kernel<float, true> : (const void*)adjust_kernel<float, false>;
+  else if (dtype == 1)
+    fn = aligned ? (const void*)adjust_kernel<__half, true> : (const void*)adjust_kernel<__half, false>;
+  else
+    fn = aligned ? (const void*)adjust_kernel<__nv_bfloat16, true> : (const void*)adjust_kernel<__nv_bfloat16, false>;
+  const size_t smem = (size_t)(a.seg + a.seg / 32 + 1) * 4;
+  void* args[] = {&a};
+  return launch_k(fn, dim3((unsigned)(b * a.nseg)), dim3(kThreads), smem, st, true, args);
+}
+
+}  // namespace dfl

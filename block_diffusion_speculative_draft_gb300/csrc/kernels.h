@@ -282,6 +282,102 @@ struct DistillArgs {
 };
 cudaError_t distill(DistillArgs a, int dtype, int64_t rows, bool backward, cudaStream_t st);
 
+// --- a tree of drafts: masks, accepted path, commit (k_tree.cu) ---
+constexpr int kTreeMax = 256;  // nodes of a tree
+struct TreeMaskArgs {
+  const int* parent;   // [b][N]
+  const int* n_nodes;  // [b], nullable
+  int N;
+  uint32_t* mask;  // [b][N][(N + 31) / 32]
+  int* depth;      // [b][N], nullable
+  int* status;
+};
+cudaError_t tree_mask(const TreeMaskArgs& a, int b, cudaStream_t st);
+struct TreeAcceptArgs {
+  const int* tok;       // [b][N] the target's token at each node
+  const int* tree_tok;  // [b][N] the nodes' own tokens
+  const int* parent;
+  const int* n_nodes;  // nullable
+  int N, R;
+  int* n_out;
+  int* corr_out;
+  int* path_out;  // [b][R]
+  int* emitted;   // [b][R], nullable
+  int* next_tok;  // nullable
+  int* status;
+};
+cudaError_t tree_accept(const TreeAcceptArgs& a, int b, cudaStream_t st);
+struct TreeCommitArgs {
+  uint16_t* k;  // cache [L][b][nkv][cap][d]
+  uint16_t* v;
+  const int* len;
+  int* len_out;
+  int b, cap, L, nkv, d, N, R;
+  const uint16_t* k_tree;  // layer l, sequence j, node i at l ld_layer + j ld_seq + i ld_tok
+  const uint16_t* v_tree;
+  int64_t ld_layer, ld_seq, ld_tok;
+  const int* path;  // [b][R]
+  const int* n;     // [b]
+  const uint16_t* hid;  // [b][N] rows of hid_units 16-byte units, nullable
+  uint16_t* hid_out;    // [b][R]
+  int hid_units;
+  int* tickets;  // [b], zero between calls; null: len_out is not len
+  int* status;
+};
+cudaError_t tree_commit(const TreeCommitArgs& a, cudaStream_t st);
+
+// --- penalties, biases and grammar masks on rows of logits (k_adjust.cu) ---
+constexpr int kAdjustMaxBias = 512;
+constexpr int kAdjustMaxHist = (1 << 20) - 1 - kTreeMax;  // counts have 20 bits
+struct AdjustArgs {
+  const void* logits;  // sequence j's row r at (j R + r) ld
+  void* out;
+  int64_t V, ld, ld_out;
+  int R;
+  const int* hist;  // [b] rows of H tokens, ld_hist apart; nullable
+  int64_t ld_hist;
+  int H;
+  const int* n_hist;
+  const int* n_prompt;  // nullable: 0
+  const int* draft;     // [b][D], nullable
+  int D;
+  const uint32_t* path;  // [b][R][(D + 31) / 32]; null: row r follows drafts 0..r-1
+  const float* repetition;  // [b] each, nullable
+  const float* frequency;
+  const float* presence;
+  const int* bias_idx;  // [b][K], nullable
+  const float* bias_val;
+  int K;
+  const uint32_t* allow;  // rows of bits, ld_allow words apart; nullable
+  int64_t n_allow, ld_allow;
+  const int* allow_row;  // [b R], nullable: its own number
+  int* status;
+  int seg;        // set by the launcher: entries of a CTA's segment, segments of a row
+  unsigned nseg;
+};
+cudaError_t adjust_logits(const AdjustArgs& a, int dtype, int64_t b, cudaStream_t st);
+
+// --- attention of a tree's nodes over a cache (k_tree_attn.cu) ---
+struct TreeAttnArgs {
+  const uint16_t* q;   // node i, head h of sequence j at j q_seq + i q_tok + h d
+  const uint16_t* kt;  // node i, kv head h at j t_seq + i t_tok + h d
+  const uint16_t* vt;
+  int64_t q_seq, q_tok, t_seq, t_tok;
+  const uint16_t* kc;  // the layer's cache [b][nkv][cap][d]
+  const uint16_t* vc;
+  const int* len;
+  const int* n_nodes;    // nullable
+  const uint32_t* mask;  // [b][N][(N + 31) / 32]; null: node i sees nodes 0..i
+  uint16_t* out;         // [b][N][nq][d]
+  float* lse;            // [b][N][nq], nullable
+  int b, N, nq, nkv, d, cap;
+  float scale;
+  void* ws;
+  int* status;
+};
+size_t tree_attn_ws_bytes(int64_t b, int N, int nq, int nkv, int d);
+cudaError_t tree_attention(const TreeAttnArgs& a, int dtype, cudaStream_t st);
+
 // Allocation-free variant of verify_accept: scratch lives in a fixed device
 // array of kNoAllocScratchBytes inside the library (k_small.cu).
 constexpr size_t kNoAllocScratchBytes = 64 * 1024;

@@ -69,6 +69,8 @@ typedef enum dflash_status {
 #define DFLASH_DEV_BAD_LENGTH 0x4  /* len < 0 or n outside [-1, B]         */
 #define DFLASH_DEV_BAD_PARAM 0x8   /* a row's temperature, top_k, top_p, min_p
                                       or teacher's value outside its range  */
+#define DFLASH_DEV_BAD_TREE 0x10  /* a node's parent outside [-1, node), or a
+                                      path's node outside the tree          */
 
 /* Element types accepted by dflash_pack_w8a16 and by the calls on logits that
  * take a dtype. */
@@ -474,6 +476,146 @@ DFLASH_API int32_t dflash_distill_backward(const void* logits, int32_t dtype, in
                                            const float* t_val, const int32_t* t_idx, int32_t K, const float* t_lse,
                                            float temperature, const float* stats, const float* grad_loss,
                                            void* dlogits, int64_t ldd, void* stream);
+
+/* What a request's history, biases and grammar do to its rows of logits, before
+ * a token is drawn from them (dflash_sample, dflash_verify_accept_filtered) or
+ * they are read otherwise.  Sequence j's row r, of R a sequence, is row j R + r.
+ * With c_v the generated tokens that equal v (those of the history and those
+ * among the row's own drafts):
+ *   x = z_v
+ *   v in the prompt or c_v > 0:  x = x > 0 ? x / repetition : x * repetition
+ *   x = x - frequency * c_v - (c_v > 0 ? presence : 0)
+ *   x = x + the sum of v's biases;   where the grammar does not allow v: -inf
+ * formed in fp32 and rounded once to `dtype` (to an infinity beyond its range).
+ * Entries that nothing changes are copied; a NaN stays one unless disallowed.
+ *  - out: rows ld_out >= V apart; it may be the logits' own buffer with
+ *    ld_out = ld (else the two must not overlap).  Only V entries a row are
+ *    written.  b * R < 2^28, R <= 256.
+ *  - hist (nullable): [b] rows of up to H tokens, ld_hist apart; of sequence j
+ *    the first n_prompt[j] (nullable: 0) are the prompt, those up to n_hist[j]
+ *    were generated.  0 <= n_prompt <= n_hist <= H < 2^20 - 256.
+ *  - draft (nullable): [b][D] tokens, D <= 256, that the rows verify, and path
+ *    (nullable): [b][R][(D + 31) / 32] bits, which of them come before row r's
+ *    token (of a tree: the masks of dflash_tree_mask, D = R).  Without path row
+ *    r follows drafts 0 to r - 1.  They count beside the history, so a token
+ *    that is in it already (a tree's root) is given as -1 in one of the two.
+ *  - repetition, frequency, presence (each nullable: 1, 0, 0): [b] fp32,
+ *    repetition finite and > 0, the others finite.
+ *  - bias_idx, bias_val (both or neither): [b][K], K <= 512; a token listed
+ *    again adds up in the list's order; a value is finite or -inf.
+ *  - allow (nullable): n_allow rows of bits, ld_allow >= (V + 31) / 32 words
+ *    apart, bit v % 32 of word v / 32 set where v is allowed; allow_row
+ *    (nullable: the row's own number) [b][R] names each row's, -1: no grammar.
+ *  - A token outside [0, V) in hist, draft or bias_idx is no token.
+ *  - A sequence with a parameter out of range gets rows of NaN, which the calls
+ *    on rows take as masked, and sets DFLASH_DEV_BAD_PARAM (a length:
+ *    DFLASH_DEV_BAD_LENGTH); so does a row whose allow_row is out of range.
+ * No workspace. */
+DFLASH_API int32_t dflash_adjust_logits(const void* logits, int32_t dtype, int64_t b, int32_t R, int64_t V, int64_t ld,
+                                        void* out, int64_t ld_out, const int32_t* hist, int64_t ld_hist, int32_t H,
+                                        const int32_t* n_hist, const int32_t* n_prompt, const int32_t* draft,
+                                        int32_t D, const uint32_t* path, const float* repetition,
+                                        const float* frequency, const float* presence, const int32_t* bias_idx,
+                                        const float* bias_val, int32_t K, const uint32_t* allow, int64_t n_allow,
+                                        int64_t ld_allow, const int32_t* allow_row, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * A tree of drafts: several continuations verified in one target pass.  Common
+ * to the calls below:
+ *  - A sequence's tree has up to N nodes, 1 <= N <= 256, of which it uses the
+ *    first n_nodes[j] (nullable: all N; 0 <= n_nodes <= N, else it has none and
+ *    DFLASH_DEV_BAD_LENGTH is set).  What belongs to other nodes is neither read
+ *    nor, in outputs, written, unless a call says so.
+ *  - parent: [b][N] int32, parent[i] in [-1, i), -1 for a root.  Node 0 is where
+ *    the walk begins: the last emitted token, whose keys and values are not in
+ *    the cache yet (as slot 0 of a draft block).
+ *  - b <= 65535.
+ * One block of a target: dflash_tree_mask; in each layer dflash_tree_attention;
+ * on the nodes' logits dflash_adjust_logits and dflash_sample (or
+ * dflash_lmhead_argmax); dflash_tree_accept; dflash_tree_commit.
+ * ------------------------------------------------------------------------- */
+
+/* mask [b][N][(N + 31) / 32]: bit t % 32 of word t / 32 of node i's row is set
+ * where t is i or one of its ancestors; depth_out (nullable) [b][N] int32: the
+ * number of ancestors, so node i's position is len + depth.  Nodes that are not
+ * there get no bits and depth -1; so do one whose parent is out of range and
+ * all that hang from it (DFLASH_DEV_BAD_TREE). */
+DFLASH_API int32_t dflash_tree_mask(const int32_t* parent, const int32_t* n_nodes, int32_t b, int32_t N,
+                                    uint32_t* mask, int32_t* depth_out, void* stream);
+
+/* Workspace bytes for dflash_tree_attention. */
+DFLASH_API int32_t dflash_tree_attention_workspace_size(int32_t b, int32_t N, int32_t nq, int32_t nkv, int32_t d,
+                                                        size_t* bytes);
+
+/* Attention of a tree's nodes over a cache and one another.  For node i and head
+ * h of sequence j, over the len[j] cached keys of kv head h nkv / nq and the
+ * nodes that mask has for i:
+ *   o = sum_t exp(s_t) v_t / sum_t exp(s_t),  s_t = scale q . k_t
+ *   lse = ln sum_t exp(s_t)
+ * in fp32 (probabilities enter the product with v rounded to dtype); a node that
+ * sees no key gets o = 0, lse = -inf.  Values of keys that a node does not see
+ * do not matter to it, infinities and NaN included.
+ *  - kv: the cache of any model, k and v [layers][b][nkv][cap][d] of `dtype`
+ *    (DFLASH_DTYPE_F16 or _BF16, as all tensors here); `layer` is read at len.
+ *  - q: node i of sequence j at j q_seq + i q_tok elements, its nq heads of d
+ *    side by side; k_tree, v_tree likewise, nkv heads, at j t_seq + i t_tok (so
+ *    all three may lie in one projection's output).  16-byte aligned, strides
+ *    multiples of 8 elements.
+ *  - mask: as of dflash_tree_mask, any bits (of nodes that are not there they
+ *    count for nothing); null: node i sees nodes 0 to i, a chain (N = 1: one
+ *    token's step).
+ *  - out [b][N][nq][d] of dtype, lse_out (nullable) [b][N][nq] fp32.
+ *  - d is 64 or 128, nq a multiple of nkv, scale finite and > 0.
+ * A len[j] outside [0, cap] leaves the sequence out (DFLASH_DEV_BAD_LENGTH).  ws
+ * holds dflash_tree_attention_workspace_size bytes, 16-byte aligned; it needs no
+ * zero fill and keeps nothing between calls. */
+DFLASH_API int32_t dflash_tree_attention(const void* q, int64_t q_seq, int64_t q_tok, int32_t dtype,
+                                         const dflash_kv* kv, int32_t layer, int32_t N, int32_t nq, int32_t nkv,
+                                         int32_t d, const void* k_tree, const void* v_tree, int64_t t_seq,
+                                         int64_t t_tok, const uint32_t* mask, const int32_t* n_nodes, float scale,
+                                         void* out, float* lse_out, void* ws, size_t ws_bytes, void* stream);
+
+/* The path that the target accepts.  tok [b][N]: the target's token at each node
+ * (its argmax, or a draw: each emitted token is then an exact sample, because the
+ * walk only asks which of a node's children the drawn token is); tree_tok
+ * [b][N]: the nodes' own tokens.  From node 0, while a child's token is the
+ * target's token at the node (the first such child) and the path has less than R
+ * nodes, the walk steps to that child.
+ *   path_out [b][R]: the walk's nodes, then -1;  n_out [b]: its steps (accepted
+ *     drafts; -1 for a sequence without nodes)
+ *   corr_out [b]: the target's token at the last node (-1: none)
+ *   emitted_out (nullable) [b][R]: the accepted drafts' tokens, then corr, then -1
+ *   next_tok_out (nullable) [b]: corr; where that is -1 the last node's token.
+ * 1 <= R <= N.  A tok below 0 equals no child's.  A node whose parent is out of
+ * range is no child (DFLASH_DEV_BAD_TREE). */
+DFLASH_API int32_t dflash_tree_accept(const int32_t* tok, const int32_t* tree_tok, const int32_t* parent,
+                                      const int32_t* n_nodes, int32_t b, int32_t N, int32_t R, int32_t* n_out,
+                                      int32_t* corr_out, int32_t* path_out, int32_t* emitted_out,
+                                      int32_t* next_tok_out, void* stream);
+
+/* Workspace bytes for dflash_tree_commit. */
+DFLASH_API int32_t dflash_tree_commit_workspace_size(int32_t b, size_t* bytes);
+
+/* Commit of an accepted path to the cache.  Of sequence j the nodes
+ * path[j][0..n[j]] (n + 1 of them, none for n = -1; n, path as of
+ * dflash_tree_accept) become rows len[j] + i of all L layers of kv, and its length
+ * grows by as many; hid (nullable): [b][N] rows of hid_cols 16-bit elements, whose
+ * nodes of the path become rows i of hid_out [b][R] (for dflash_kv_commit, which
+ * takes n too).
+ *  - k_tree, v_tree: layer l, sequence j, node i at l t_layer + j t_seq + i t_tok
+ *    elements (16 bits each), nkv heads of d side by side; 16-byte aligned,
+ *    strides, d and hid_cols multiples of 8.
+ *  - len_out (nullable: kv->len itself) [b]: the new lengths.
+ *  - A sequence that would pass cap, whose n is outside [-1, R) or len below 0, or
+ *    whose path has a node outside [0, N) is left as it is, hidden rows included,
+ *    and sets DFLASH_DEV_KV_CAPACITY, _BAD_LENGTH or _BAD_TREE.
+ * ws holds dflash_tree_commit_workspace_size bytes, zero-filled once (every call
+ * leaves them zero). */
+DFLASH_API int32_t dflash_tree_commit(const dflash_kv* kv, int32_t L, int32_t nkv, int32_t d, int32_t N,
+                                      const void* k_tree, const void* v_tree, int64_t t_layer, int64_t t_seq,
+                                      int64_t t_tok, const int32_t* path, const int32_t* n, int32_t R,
+                                      const uint16_t* hid, int64_t hid_cols, uint16_t* hid_out, int32_t* len_out,
+                                      void* ws, size_t ws_bytes, void* stream);
 
 /* Draft-KV commit with rollback of the rejected suffix (mlx-dspark v0.0.3,
  * "Notes": KV rollback; dflash-mlx "What It Does": conditioning on target
