@@ -102,6 +102,9 @@ bool encode_tmap_2d(CUtensorMap* map, CUtensorMapDataType dt, const void* base, 
 // Same for a 3-D tensor: dims innermost first, strides (bytes) of dims 1 and 2.
 bool encode_tmap_3d(CUtensorMap* map, CUtensorMapDataType dt, const void* base, const uint64_t dims[3],
                     const uint64_t strides[2], const uint32_t box[3], CUtensorMapSwizzle swz);
+// Same for `rank` (2 to 5) dimensions: rank - 1 strides.
+bool encode_tmap(CUtensorMap* map, CUtensorMapDataType dt, const void* base, int rank, const uint64_t* dims,
+                 const uint64_t* strides, const uint32_t* box, CUtensorMapSwizzle swz);
 
 // Launch helpers: the programmatic-dependent-launch attribute is set when
 // `pdl` is requested and the library's launch mode allows early launches
