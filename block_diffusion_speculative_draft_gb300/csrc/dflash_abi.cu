@@ -716,7 +716,7 @@ int32_t dflash_tree_mask(const int32_t* parent, const int32_t* n_nodes, int32_t 
 static int check_tree_heads(int32_t b, int32_t N, int32_t nq, int32_t nkv, int32_t d) {
   if (int r = check_tree(b, N)) return r;
   if (nq < 1 || nkv < 1) return DFLASH_EINVAL;
-  if ((d != 64 && d != 128) || nq % nkv || (int64_t)nq * d > 1 << 24 || (int64_t)nkv * b > 1 << 22)
+  if ((d != 64 && d != 128) || nq % nkv || nq / nkv > kTreeMaxGroup || (int64_t)nq * d > 1 << 24 || (int64_t)nkv * b > 1 << 22)
     return DFLASH_EUNSUPPORTED;
   // CTAs of the launch that joins parts: 16 query rows of a kv head each
   if ((int64_t)b * nkv * (((int64_t)N * (nq / nkv) + 63) / 64) * 4 > 0x7fffffffll) return DFLASH_EUNSUPPORTED;
@@ -765,6 +765,8 @@ int32_t dflash_tree_attention(const void* q, int64_t q_seq, int64_t q_tok, int32
   a.nkv = nkv;
   a.d = d;
   a.cap = kv->cap;
+  a.g = nq / nkv;
+  a.g_inv = (uint32_t)((((uint64_t)1 << 32) + a.g - 1) / a.g);
   a.scale = scale;
   a.ws = ws;
   if (!(a.status = status_ptr())) return DFLASH_ECUDA;

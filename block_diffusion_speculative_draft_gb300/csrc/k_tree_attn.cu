@@ -48,7 +48,7 @@ __device__ __forceinline__ Seq seq_of(const TreeAttnArgs& a, int j, int* status 
     s.len = s.n = 0;
   }
   s.tiles = s.n ? P::tiles(s.len, s.n) : 0;
-  s.qtiles = (s.n * (a.nq / a.nkv) + P::ROWS - 1) / P::ROWS;
+  s.qtiles = (s.n * a.g + P::ROWS - 1) / P::ROWS;
   return s;
 }
 
@@ -60,60 +60,102 @@ __device__ __forceinline__ uint32_t node_bits(const TreeAttnArgs& a, int j, int 
   return own < 0 ? 0u : own >= 31 ? ~0u : (2u << own) - 1u;
 }
 
-// Sum over the block of a 64-bit number, and over the threads before this one.
-__device__ __forceinline__ long long block_scan(long long v, long long* s_warp, long long& before) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  long long x = v;
+// Runs: tiles [c all / runs, (c + 1) all / runs) of all items' tiles belong to
+// CTA c < runs; tile u to run ((u + 1) runs - 1) / all.
+struct Runs {
+  long long all, runs;
+  __device__ __forceinline__ long long start(long long c) const { return ratio(c * all, runs); }
+  __device__ __forceinline__ long long of(long long u) const { return ratio((u + 1) * runs - 1, all); }
+  static __device__ __forceinline__ long long ratio(long long x, long long y) {  // (64-bit division is slow)
+    return x >> 32 ? x / y : (long long)((uint32_t)x / (uint32_t)y);
+  }
+};
+
+// Every warp by itself, so without a barrier: the tiles of all sequences, as
+// runs for at most `ctas` CTAs; then the sequence that holds tile u and the
+// tiles before it.
+template <typename P>
+__device__ __forceinline__ Runs count_runs(const TreeAttnArgs& a, int ctas) {
+  const int lane = threadIdx.x & 31;
+  Runs r;
+  r.all = 0;
+  for (int i = lane; i < a.b; i += 32) r.all += seq_of<P>(a, i).units(a.nkv);
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long y = __shfl_up_sync(0xffffffffu, x, o);
-    if (lane >= o) x += y;
+  for (int o = 16; o > 0; o >>= 1) r.all += __shfl_xor_sync(0xffffffffu, r.all, o);
+  const long long most = (r.all + P::MIN_TILES - 1) / P::MIN_TILES;
+  r.runs = most < ctas ? most : ctas;
+  return r;
+}
+template <typename P>
+__device__ __forceinline__ int find_seq(const TreeAttnArgs& a, long long u, long long& before) {
+  const int lane = threadIdx.x & 31;
+  before = 0;
+  for (int c = 0; c < a.b; c += 32) {
+    const long long t = c + lane < a.b ? seq_of<P>(a, c + lane).units(a.nkv) : 0;
+    long long x = t;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    const unsigned in = __ballot_sync(0xffffffffu, before + x > u);  // from the sequence that holds u
+    if (in) {
+      const int l = __ffs(in) - 1;
+      before += __shfl_sync(0xffffffffu, x - t, l);
+      return c + l;
+    }
+    before += __shfl_sync(0xffffffffu, x, 31);
   }
-  __syncthreads();
-  if (lane == 31) s_warp[warp] = x;
-  __syncthreads();
-  before = x - v;
-  long long all = 0;
-  for (int w = 0; w < (int)blockDim.x / 32; ++w) {
-    if (w < warp) before += s_warp[w];
-    all += s_warp[w];
-  }
-  return all;
+  return -1;
 }
 
-// Tiles of all items, and of the sequences before j.
-template <typename P>
-__device__ __forceinline__ long long count_tiles(const TreeAttnArgs& a, int j, long long* s_warp, long long& before) {
-  long long x = 0, y = 0, none;
-  for (int i = threadIdx.x; i < a.b; i += blockDim.x) {
-    const long long t = seq_of<P>(a, i).units(a.nkv);
-    y += t;
-    if (i < j) x += t;
-  }
-  before = j ? block_scan(x, s_warp, none) : 0;
-  return block_scan(y, s_warp, none);
-}
+// What the second launch has to join: a record a run.  An item whose parts lie
+// in several runs belongs to the second of them.
+struct Join {
+  int j, item;      // sequence, item of the sequence; j < 0: nothing
+  int first, last;  // runs
+  int slot;         // of the part in the first run; 0 in the others
+  int pad[3];
+};
 
-// Runs: tiles [run_start(c), run_start(c + 1)) of `all` belong to CTA c < ctas.
-template <typename P>
-__device__ __forceinline__ long long run_count(long long all, int ctas) {
-  const long long most = (all + P::MIN_TILES - 1) / P::MIN_TILES;
-  return most < ctas ? most : ctas;
-}
-__device__ __forceinline__ long long run_start(long long all, long long runs, long long c) { return c * all / runs; }
-__device__ __forceinline__ long long run_of(long long all, long long runs, long long u) {
-  return ((u + 1) * runs - 1) / all;
-}
+// Node and place in the group of a query row: x / g by a product with 2^32 / g
+// rounded up, exact for x g < 2^32 (x is below 256 g, g at most 1024).
+struct Group {
+  uint32_t g, inv;
+  __device__ __forceinline__ explicit Group(const TreeAttnArgs& a) : g(a.g), inv(a.g_inv) {}
+  __device__ __forceinline__ int node(int x) const { return g == 1 ? x : (int)__umulhi((uint32_t)x, inv); }
+  __device__ __forceinline__ int place(int x, int node) const { return x - node * (int)g; }
+};
 
 // A part in the workspace: O of rows x D fp32, then (m, sum) of each row, m in
-// log2 units.  O lies by rows, or, where a thread writes a whole row, in
-// columns of four, so that a warp's 16-byte stores lie side by side.
-template <int D, int ROWS, bool BY_ROW>
+// log2 units.  A run has two: of its first item, and of its last.
+template <int D, int ROWS>
 struct PartOf {
-  float4 o[ROWS * D / 4];
+  float o[ROWS][D];
   float2 ml[ROWS];
-  static __device__ __forceinline__ int at(int r, int c) { return BY_ROW ? r * (D / 4) + c / 4 : (c / 4) * ROWS + r; }
 };
+__device__ __forceinline__ uint8_t* aligned32(void* ws) {
+  return reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(ws) + 31) & ~uintptr_t(31));
+}
+template <int D, int ROWS>
+__device__ __forceinline__ Join* joins_of(const TreeAttnArgs& a) {
+  return reinterpret_cast<Join*>(aligned32(a.ws) + (size_t)kMaxCtas * 2 * sizeof(PartOf<D, ROWS>));
+}
+// CTA c's record; u0 its first tile, which is tile t0 of an item of `tiles`.
+__device__ __forceinline__ void leave_join(Join* joins, const Runs& r, int c, long long u0, int j, int item, int t0,
+                                           int tiles) {
+  Join x;
+  x.j = -1;
+  const long long ub = u0 - t0;
+  if (t0 > 0 && r.of(ub) == c - 1) {
+    x.j = j;
+    x.item = item;
+    x.first = c - 1;
+    x.last = (int)r.of(ub + tiles - 1);
+    x.slot = r.start(c - 1) < ub;
+  }
+  joins[c] = x;
+}
 
 // Byte offset of 16-byte unit ch (of D / 8) of row r in a K, V or Q tile of
 // `rows` rows: [D / 64 column halves][rows][128 bytes], unit c of a row at
@@ -153,7 +195,6 @@ struct Shape {
   static constexpr int KW = RW == 1 ? 4 : 8 / RW;
   static constexpr int THREADS = RW * KW * 32;
   static constexpr int ROWS = RW * 16;  // of a query tile
-  static constexpr bool BY_ROW = true;
   // cached keys and the tree's side by side
   __host__ __device__ static int64_t tiles(int64_t len, int n) { return (len + n + kKT - 1) / kKT; }
   static constexpr int MIN_TILES = 2;  // of a run: fewer cost more in joining parts
@@ -172,40 +213,26 @@ __global__ void __launch_bounds__(Shape<D, RW>::THREADS, Shape<D, RW>::CTAS)
   constexpr int CH = D / 8;       // 16-byte units of a row
   extern __shared__ __align__(128) uint8_t sKV[];                                 // [NST][K, V]
   uint32_t* const sMask = reinterpret_cast<uint32_t*>(sKV + NST * 2 * TILE);  // [ROWS][W] of the rows' nodes
-  __shared__ long long s_warp[THREADS / 32];
   __shared__ float2 s_ml[KW][ROWS];
   __shared__ uint32_t s_odd[kTreeMax / 32];  // tree keys whose V has an infinity or NaN
-  __shared__ int s_j0;
-  __shared__ long long s_base;
 
   pdl_wait();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rw = warp % RW, kg = warp / RW;
-  const int g = a.nq / a.nkv;
+  const int g = a.g;
+  const Group grp(a);
   const int W = (a.N + 31) / 32;
-  long long none;
-  const long long all = count_tiles<S>(a, 0, s_warp, none);
+  const Runs runs = count_runs<S>(a, gridDim.x);
   if (blockIdx.x == 0)
     for (int i = tid; i < a.b; i += THREADS) seq_of<S>(a, i, a.status);  // out of range: told once
-  if (all == 0) return;
-  const long long runs = run_count<S>(all, gridDim.x);
-  if (blockIdx.x >= runs) return;
-  const long long u0 = run_start(all, runs, blockIdx.x), u1 = run_start(all, runs, blockIdx.x + 1);
-
-  // the sequence that holds tile u0, and the tiles before it
-  for (long long c = 0, base = 0; base <= u0; c += THREADS) {
-    const long long i = c + tid;
-    const long long t = i < a.b ? seq_of<S>(a, (int)i).units(a.nkv) : 0;
-    long long before;
-    const long long sum = block_scan(t, s_warp, before);
-    before += base;
-    if (before <= u0 && u0 < before + t) {
-      s_j0 = (int)i;
-      s_base = before;
-    }
-    base += sum;
+  Join* const joins = joins_of<D, ROWS>(a);
+  if (blockIdx.x >= runs.runs) {
+    if (tid == 0) joins[blockIdx.x].j = -1;
+    return;
   }
-  __syncthreads();
+  const long long u0 = runs.start(blockIdx.x), u1 = runs.start(blockIdx.x + 1);
+  long long base;
+  const int j0 = find_seq<S>(a, u0, base);
 
   // A place in the run: sequence, item of the sequence (kv head, query tile), tile.
   struct Place {
@@ -223,10 +250,11 @@ __global__ void __launch_bounds__(Shape<D, RW>::THREADS, Shape<D, RW>::CTAS)
     } while (!p.s.tiles);
   };
   Place cur;
-  cur.j = s_j0;
+  cur.j = j0;
   cur.s = seq_of<S>(a, cur.j);
-  cur.item = (int)((u0 - s_base) / cur.s.tiles);
-  cur.tile = (int)((u0 - s_base) % cur.s.tiles);
+  cur.item = (int)Runs::ratio(u0 - base, cur.s.tiles);
+  cur.tile = (int)(u0 - base - (long long)cur.item * cur.s.tiles);
+  if (tid == 0) leave_join(joins, runs, blockIdx.x, u0, cur.j, cur.item, cur.tile, cur.s.tiles);
   Place pre = cur;  // the tile to copy next
 
   // K and V of a tile: cached keys, then the tree's, then zeros
@@ -279,7 +307,7 @@ __global__ void __launch_bounds__(Shape<D, RW>::THREADS, Shape<D, RW>::CTAS)
       const int r = c / W, w = c % W;
       uint32_t x = 0;
       if (r < rows) {
-        const int node = (row0 + r) / g;
+        const int node = grp.node(row0 + r);
         x = node_bits(a, j, node, w);
         const int left = n - w * 32;  // nodes past the count are not there
         if (left < 32) x &= left <= 0 ? 0u : (1u << left) - 1u;
@@ -293,7 +321,7 @@ __global__ void __launch_bounds__(Shape<D, RW>::THREADS, Shape<D, RW>::CTAS)
     for (int x = 0; x < 2; ++x) {
       const int r = rw * 16 + (lane >> 2) + x * 8;
       const bool there = r < rows;
-      const int node = there ? (row0 + r) / g : 0, hh = there ? (row0 + r) % g : 0;
+      const int node = there ? grp.node(row0 + r) : 0, hh = there ? grp.place(row0 + r, node) : 0;
       const uint16_t* q = a.q + j * a.q_seq + node * a.q_tok + (h * g + hh) * D + (lane & 3) * 2;
 #pragma unroll
       for (int k = 0; k < D / 16; ++k) {
@@ -460,13 +488,13 @@ __global__ void __launch_bounds__(Shape<D, RW>::THREADS, Shape<D, RW>::CTAS)
     }
     if (kg == 0) {
       const bool whole = t_first == 0 && t_last == tiles;
-      using Part = PartOf<D, ROWS, true>;
-      Part* part = static_cast<Part*>(a.ws) + (size_t)blockIdx.x * 2 + (first ? 0 : 1);
+      PartOf<D, ROWS>* part =
+          reinterpret_cast<PartOf<D, ROWS>*>(aligned32(a.ws)) + (size_t)blockIdx.x * 2 + (first ? 0 : 1);
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
         const int r = rw * 16 + (lane >> 2) + x * 8;
         if (r >= rows) continue;
-        const int node = (row0 + r) / g, head = h * g + (row0 + r) % g;
+        const int node = grp.node(row0 + r), head = h * g + grp.place(row0 + r, node);
         for (int w = 0; w < W; ++w)
           for (uint32_t z = s_odd[w] & sMask[r * W + w]; z; z &= z - 1) {
             const uint16_t* v = a.vt + j * a.t_seq + (w * 32 + __ffs(z) - 1) * a.t_tok + h * D;
@@ -490,7 +518,7 @@ __global__ void __launch_bounds__(Shape<D, RW>::THREADS, Shape<D, RW>::CTAS)
         } else {
 #pragma unroll
           for (int i = 0; i < D / 8; ++i)
-            reinterpret_cast<float2*>(&part->o[Part::at(r, i * 8)])[lane & 3] = make_float2(o[i][2 * x], o[i][2 * x + 1]);
+            *reinterpret_cast<float2*>(&part->o[r][i * 8 + (lane & 3) * 2]) = make_float2(o[i][2 * x], o[i][2 * x + 1]);
           if ((lane & 3) == 0) part->ml[r] = make_float2(mt[x], lt[x]);
         }
       }
@@ -502,63 +530,94 @@ __global__ void __launch_bounds__(Shape<D, RW>::THREADS, Shape<D, RW>::CTAS)
   cp_async_wait<0>();
 }
 
-// Joins the parts of one item: 16 query rows a CTA, a thread per row and four
-// columns, the parts in the order of their keys.
-constexpr int kJoinRows = 16, kJoinThreads = 256;
+// Joins the parts of an item, a record of a run: JR query rows a CTA, 8 / JR
+// warps a row that share out its parts (each the same ones every time, in the
+// order of their keys; the shares are added in order too).  Bound by the loads'
+// latency where an item has few rows, by L2 where it has many.
+constexpr int kJoinThreads = 256;
 
-template <typename T, int D, typename S>
-__global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const TreeAttnArgs a, int ctas) {
-  constexpr int ROWS = S::ROWS;
-  using Part = PartOf<D, ROWS, S::BY_ROW>;
-  __shared__ long long s_warp[kJoinThreads / 32];
+template <typename T, int D, int ROWS, int JR>
+__global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const TreeAttnArgs a) {
+  constexpr int LANES = D / 4;                  // of a row: four columns each
+  constexpr int SHARES = 8 / JR * (32 / LANES);  // of a row's parts
+  __shared__ float4 s_o[JR][SHARES][LANES];
   pdl_wait();
-  const int g = a.nq / a.nkv, most = (a.N * g + ROWS - 1) / ROWS;  // query tiles of a kv head
-  constexpr int BLK = ROWS / kJoinRows;
-  const int blk = blockIdx.x % BLK, qt = blockIdx.x / BLK % most;
-  const int h = (int)(blockIdx.x / (BLK * most) % a.nkv), j = (int)(blockIdx.x / (BLK * most) / a.nkv);
-  const Seq s = seq_of<S>(a, j);
-  const int row0 = qt * ROWS, rows = min(ROWS, s.n * g - row0);
-  if (rows <= blk * kJoinRows) return;  // (the same for the whole block)
-  long long before;
-  const long long all = count_tiles<S>(a, j, s_warp, before);
-  const long long runs = run_count<S>(all, ctas);
-  const long long ub = before + (long long)(h * s.qtiles + qt) * s.tiles;
-  const long long c0 = run_of(all, runs, ub), c1 = run_of(all, runs, ub + s.tiles - 1);
-  if (c0 == c1) return;  // written by the run itself
-  const Part* parts = static_cast<const Part*>(a.ws);
-  // the item is its run's first unless the run has tiles before it
-  const Part* p0 = parts + 2 * c0 + (run_start(all, runs, c0) < ub ? 1 : 0);
-  for (int it = threadIdx.x; it < kJoinRows * (D / 4); it += kJoinThreads) {
-    // neighbouring threads read neighbouring places of a part
-    const int r = blk * kJoinRows + (S::BY_ROW ? it / (D / 4) : it % kJoinRows);
-    const int c = (S::BY_ROW ? it % (D / 4) : it / kJoinRows) * 4;
-    if (r >= rows) continue;
-    float m = p0->ml[r].x;
-    for (long long k = c0 + 1; k <= c1; ++k) m = fmaxf(m, parts[2 * k].ml[r].x);
+  const Join x = joins_of<D, ROWS>(a)[blockIdx.y];
+  if (x.j < 0) return;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = a.g;
+  const int len_n = a.n_nodes ? a.n_nodes[x.j] : a.N;  // (in range: the sequence has work)
+  const int qtiles = (len_n * g + ROWS - 1) / ROWS;
+  const int row0 = (x.item % qtiles) * ROWS, rows = min(ROWS, len_n * g - row0);
+  const int lr = warp % JR, r = blockIdx.x * JR + lr;
+  const int share = warp / JR * (32 / LANES) + lane / LANES, c = lane % LANES;
+  if ((int)blockIdx.x * JR >= rows) return;
+  const PartOf<D, ROWS>* parts = reinterpret_cast<const PartOf<D, ROWS>*>(aligned32(a.ws));
+  const int n = x.last - x.first + 1;
+  auto part = [&](int k) { return parts + 2 * (x.first + k) + (k ? 0 : x.slot); };
+  float m = -INFINITY, l = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (r < rows) {
+    for (int k = lane; k < n; k += 32) m = fmaxf(m, part(k)->ml[r].x);
+#pragma unroll
+    for (int q = 16; q > 0; q >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, q));
     const float ref = m == -INFINITY ? 0.f : m;
-    float l = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (long long k = c0; k <= c1; ++k) {
-      const Part* p = k == c0 ? p0 : parts + 2 * k;
-      const float2 ml = p->ml[r];
-      const float4 v = p->o[Part::at(r, c)];
+    for (int k0 = 0; k0 < n; k0 += 32) {
+      const float2 ml = k0 + lane < n ? part(k0 + lane)->ml[r] : make_float2(-INFINITY, 0.f);
       const float w = fast_exp2(ml.x - ref);
       l += ml.y * w;
-      o.x += v.x * w;
-      o.y += v.y * w;
-      o.z += v.z * w;
-      o.w += v.w * w;
+      const int ke = min(32, n - k0);
+      for (int k = share; k - share < ke; k += 8 * SHARES) {
+        float4 v[8];
+        float wk[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int q = k + i * SHARES;
+          wk[i] = __shfl_sync(0xffffffffu, w, q & 31);
+          v[i] = q < ke ? *reinterpret_cast<const float4*>(&part(k0 + q)->o[r][4 * c]) : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          if (k + i * SHARES >= ke) continue;
+          o.x += v[i].x * wk[i];
+          o.y += v[i].y * wk[i];
+          o.z += v[i].z * wk[i];
+          o.w += v[i].w * wk[i];
+        }
+      }
     }
-    const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
-    const int node = (row0 + r) / g, head = h * g + (row0 + r) % g;
-    const size_t row = ((size_t)j * a.N + node) * a.nq + head;
-    uint2 x;
-    x.x = pack2<T>(o.x * inv, o.y * inv);
-    x.y = pack2<T>(o.z * inv, o.w * inv);
-    *reinterpret_cast<uint2*>(a.out + row * D + c) = x;
-    if (a.lse && c == 0) a.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * (1.f / kLog2e);
+#pragma unroll
+    for (int q = 16; q > 0; q >>= 1) l += __shfl_xor_sync(0xffffffffu, l, q);
   }
+  if (SHARES > 1) {
+    s_o[lr][share][c] = o;
+    __syncthreads();
+    if (share) return;
+#pragma unroll
+    for (int k = 1; k < SHARES; ++k) {
+      const float4 v = s_o[lr][k][c];
+      o.x += v.x;
+      o.y += v.y;
+      o.z += v.z;
+      o.w += v.w;
+    }
+  }
+  if (r >= rows) return;
+  const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+  const Group grp(a);
+  const int node = grp.node(row0 + r), head = x.item / qtiles * g + grp.place(row0 + r, node);
+  const size_t row = ((size_t)x.j * a.N + node) * a.nq + head;
+  *reinterpret_cast<uint2*>(a.out + row * D + 4 * c) =
+      make_uint2(pack2<T>(o.x * inv, o.y * inv), pack2<T>(o.z * inv, o.w * inv));
+  if (a.lse && c == 0) a.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * (1.f / kLog2e);
+}
+
+template <typename T, int D, int ROWS>
+cudaError_t launch_join(TreeAttnArgs& a, int ctas, cudaStream_t st) {
+  constexpr int JR = ROWS <= 16 ? 2 : ROWS <= 64 ? 4 : 8;
+  void* args[] = {&a};
+  const int rows = a.N * a.g < ROWS ? a.N * a.g : ROWS;
+  return launch_k((const void*)tree_join_kernel<T, D, ROWS, JR>, dim3((rows + JR - 1) / JR, ctas), dim3(kJoinThreads), 0, st,
+                  true, args);
 }
 
 template <typename T, int D, int RW>
@@ -570,16 +629,14 @@ cudaError_t launch(const TreeAttnArgs& a0, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   int ctas = S::CTAS * num_sms();
   if (ctas > kMaxCtas) ctas = kMaxCtas;
-  const int g = a.nq / a.nkv;
+  const int g = a.g;
   const int64_t items = (int64_t)a.b * a.nkv * ((a.N * g + S::ROWS - 1) / S::ROWS);
   const int64_t most = (items * S::tiles(a.cap, a.N) + S::MIN_TILES - 1) / S::MIN_TILES;  // were every cache full
   if (most < ctas) ctas = (int)most;
   void* args[] = {&a};
   e = launch_k(fn, dim3(ctas), dim3(S::THREADS), S::SMEM, st, true, args);
   if (e != cudaSuccess) return e;
-  void* jargs[] = {&a, &ctas};
-  return launch_k((const void*)tree_join_kernel<T, D, S>, dim3((unsigned)(items * (S::ROWS / kJoinRows))),
-                  dim3(kJoinThreads), 0, st, true, jargs);
+  return launch_join<T, D, S::ROWS>(a, ctas, st);
 }
 
 // ---------------------------------------------------------------------------
@@ -589,19 +646,21 @@ cudaError_t launch(const TreeAttnArgs& a0, cudaStream_t st) {
 // same rows over every other tile, joined at the end.  While one stream's four
 // warps make P of its S (a thread a row, no exchange), the tensor cores work
 // for the other.  One thread copies tiles (TMA, one ring of K and V tiles in
-// the order of their use), one issues the products:
-//   step v: wait for P of v; O += P V; S of step v + 2 = Q K^T
+// the order of their use); a warp a stream issues the products,
+//   wait for P; O += P V; S of the stream's next tile = Q K^T
+// so that one stream's waits (150 to 250 cycles each) pass under the other's
+// products (one warp for both: 3.6 to 3.9 thousand cycles a tile of 256 rows
+// against 2.1 of products).
 // Cached keys fill tiles of their own, the last one padded, and the tree's keys
 // follow in theirs.  Tiles with absent keys have those rows of V zeroed by the
 // threads that mask S, before they hand over P.
 constexpr int kTcKeys = 128;
-constexpr int kTcThreads = 320;  // warps 0-7: rows; 8: tensor memory and products; 9: copies
-constexpr int kTcMma = 8, kTcCopy = 9;
+constexpr int kTcThreads = 352;  // warps 0-7: rows; 8, 9: the streams' products; 10: copies
+constexpr int kTcMma = 8, kTcCopy = 10;
 
 template <int D, bool PAR>
 struct TcShape {
   static constexpr int ROWS = PAR ? 128 : 256;
-  static constexpr bool BY_ROW = false;
   static constexpr int MIN_TILES = 1;
   __host__ __device__ static int64_t tiles(int64_t len, int n) {
     return (len + kTcKeys - 1) / kTcKeys + (n + kTcKeys - 1) / kTcKeys;
@@ -616,9 +675,7 @@ struct TcShape {
 struct TcCtrl {
   float2 ml[2][128];
   uint64_t full[8], empty[8], s_ready[2], p_ready[2], q_ready[2], o_done;
-  long long warp[kTcThreads / 32], base;
   uint32_t odd[2][kTreeMax / 32];
-  int j0;
   uint32_t tmem;
 };
 static_assert(sizeof(TcCtrl) <= 2 * 128 * 8 + 512, "");
@@ -637,6 +694,17 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16
       "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
       : "memory");
 }
+// Whether a phase has completed.  Where it has, this answers some 150 cycles
+// before the try_wait of mbar_wait does.
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
 // One box of a tensor map of four dimensions (the rule of tma_load_2d for x).
 __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, int x, int y, int z, int w, uint64_t* bar) {
   asm volatile(
@@ -644,6 +712,51 @@ __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, i
       "[%6];" ::"r"(smem_u32(dst)),
       "l"(map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
       : "memory");
+}
+// The products and commits of tcgen05.cuh, issued by the lanes where `on` is set.
+__device__ __forceinline__ void mma_ss_if(uint32_t on, uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                          uint32_t accumulate) {
+  asm volatile(
+      "{ .reg .pred p, q; setp.ne.u32 p, %4, 0; setp.ne.u32 q, %5, 0;\n"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p; }" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(on)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts_if(uint32_t on, uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                          uint32_t accumulate) {
+  asm volatile(
+      "{ .reg .pred p, q; setp.ne.u32 p, %4, 0; setp.ne.u32 q, %5, 0;\n"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p; }" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(on)
+      : "memory");
+}
+__device__ __forceinline__ void commit_if(uint32_t on, uint64_t* bar) {
+  asm volatile(
+      "{ .reg .pred q; setp.ne.u32 q, %1, 0;\n"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0]; }" ::"r"(smem_u32(bar)),
+      "r"(on)
+      : "memory");
+}
+// Two fp32 numbers in a register pair, worked on by one instruction.
+__device__ __forceinline__ uint64_t pair(float x, float y) {
+  uint64_t v;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(x), "f"(y));
+  return v;
+}
+__device__ __forceinline__ float2 halves(uint64_t v) {
+  float2 f;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
+  return f;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t x, uint64_t y, uint64_t z) {
+  uint64_t v;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(v) : "l"(x), "l"(y), "l"(z));
+  return v;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t x, uint64_t y) {
+  uint64_t v;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(v) : "l"(x), "l"(y));
+  return v;
 }
 __device__ __forceinline__ void rows_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 
@@ -653,7 +766,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         const __grid_constant__ CUtensorMap ktmap, const __grid_constant__ CUtensorMap vtmap,
                         const TreeAttnArgs a) {
   using S = TcShape<D, PAR>;
-  using Part = PartOf<D, S::ROWS, false>;
+  using Part = PartOf<D, S::ROWS>;
   constexpr int TILE = S::TILE, HALF = S::HALF, SLOTS = S::SLOTS, CH = D / 8;
   extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* const sQ = smem;              // [2 streams][D / 64][128 rows][128 bytes]
@@ -662,52 +775,19 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 
   pdl_wait();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int g = a.nq / a.nkv;
-  long long none;
-  const long long all = count_tiles<S>(a, 0, sh.warp, none);
+  const int g = a.g;
+  const Group grp(a);
+  const Runs runs = count_runs<S>(a, gridDim.x);
   if (blockIdx.x == 0)
     for (int i = tid; i < a.b; i += kTcThreads) seq_of<S>(a, i, a.status);  // out of range: told once
-  if (all == 0) return;
-  const long long runs = run_count<S>(all, gridDim.x);
-  if (blockIdx.x >= runs) return;
-  const long long u0 = run_start(all, runs, blockIdx.x), u1 = run_start(all, runs, blockIdx.x + 1);
-  for (long long c = 0, base = 0; base <= u0; c += kTcThreads) {
-    const long long i = c + tid;
-    const long long t = i < a.b ? seq_of<S>(a, (int)i).units(a.nkv) : 0;
-    long long before;
-    const long long sum = block_scan(t, sh.warp, before);
-    before += base;
-    if (before <= u0 && u0 < before + t) {
-      sh.j0 = (int)i;
-      sh.base = before;
-    }
-    base += sum;
+  Join* const joins = joins_of<D, S::ROWS>(a);
+  if (blockIdx.x >= runs.runs) {
+    if (tid == 0) joins[blockIdx.x].j = -1;
+    return;
   }
-  if (warp == kTcMma) tmem_alloc(&sh.tmem, 512);
-  if (warp == kTcCopy && lane == 0) {
-    for (int i = 0; i < SLOTS; ++i) {
-      mbar_init(&sh.full[i], 1);
-      mbar_init(&sh.empty[i], 1);
-    }
-    for (int m = 0; m < 2; ++m) {
-      mbar_init(&sh.s_ready[m], 1);
-      mbar_init(&sh.p_ready[m], 4);
-      mbar_init(&sh.q_ready[m], 4);
-    }
-    mbar_init(&sh.o_done, 1);
-    fence_mbar_init();
-    prefetch_tmap(&kmap);
-    prefetch_tmap(&vmap);
-    prefetch_tmap(&ktmap);
-    prefetch_tmap(&vtmap);
-  }
-  if (tid < 2 * (kTreeMax / 32)) sh.odd[tid / (kTreeMax / 32)][tid % (kTreeMax / 32)] = 0;
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = sh.tmem;
-  constexpr uint32_t kS = 2 * D;  // columns: O of the two streams, then their S
-
+  const long long u0 = runs.start(blockIdx.x), u1 = runs.start(blockIdx.x + 1);
+  long long base;
+  const int j0 = find_seq<S>(a, u0, base);
   // The run's items, walked by every role by itself.
   struct Item {
     int j, item;   // sequence, its item
@@ -717,10 +797,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   };
   long long u = u0;
   Item it;
-  it.j = sh.j0;
+  it.j = j0;
   it.s = seq_of<S>(a, it.j);
-  it.item = (int)((u0 - sh.base) / it.s.tiles);
-  it.t0 = (int)((u0 - sh.base) % it.s.tiles);
+  it.item = (int)Runs::ratio(u0 - base, it.s.tiles);
+  it.t0 = (int)(u0 - base - (long long)it.item * it.s.tiles);
   auto enter = [&]() {  // the rest of the item's places
     it.t1 = (int)min((long long)it.s.tiles, it.t0 + (u1 - u));
     it.head = it.item / it.s.qtiles;
@@ -740,14 +820,67 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     return true;
   };
   enter();
+  // Q of the stream's rows (zero where there is none), a row by neighbouring threads
+  auto copy_q = [&]() {
+    const int m = warp >> 2, lr = (warp & 3) * 32 + lane;
+    const int rows = min(S::ROWS, it.s.n * g - it.row0);
+    const uint16_t* q = a.q + it.j * a.q_seq + it.head * g * D;
+#pragma unroll 4
+    for (int i = 0; i < CH; ++i) {
+      const int r = i * (128 / CH) + lr / CH, c = lr % CH, qr = PAR ? r : m * 128 + r;
+      const bool ok = qr < rows;
+      const int nd = ok ? grp.node(it.row0 + qr) : 0, hd = ok ? grp.place(it.row0 + qr, nd) : 0;
+      cp_async16(sQ + m * TILE + tile_off(r, c, 128), q + nd * a.q_tok + hd * D + c * 8, ok);
+    }
+    cp_async_commit();
+  };
+  // The first item's Q before any tile: behind the ring's first tiles of all
+  // CTAs it would arrive 4 us later.
+  if (warp < 8) copy_q();
+  if (warp == kTcMma) tmem_alloc(&sh.tmem, 512);
+  if (warp == kTcCopy && lane == 0) {
+    for (int i = 0; i < SLOTS; ++i) {
+      mbar_init(&sh.full[i], 1);
+      mbar_init(&sh.empty[i], PAR ? 1 : 2);  // streams that read a tile
+    }
+    for (int m = 0; m < 2; ++m) {
+      mbar_init(&sh.s_ready[m], 1);
+      mbar_init(&sh.p_ready[m], 4);
+      mbar_init(&sh.q_ready[m], 4);
+    }
+    mbar_init(&sh.o_done, 2);
+    fence_mbar_init();
+    prefetch_tmap(&kmap);
+    prefetch_tmap(&vmap);
+    prefetch_tmap(&ktmap);
+    prefetch_tmap(&vtmap);
+  }
+  if (tid < 2 * (kTreeMax / 32)) sh.odd[tid / (kTreeMax / 32)][tid % (kTreeMax / 32)] = 0;
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sh.tmem;
+  constexpr uint32_t kS = 2 * D;  // columns: O of the two streams, then their S
   bool dead = false;  // a wait gave up: the status is raised, the rest only drains
   auto wait = [&](uint64_t* bar, uint32_t n) {  // for the bar's n-th completion, from 0
-    if (!dead && !mbar_wait(bar, n & 1, a.status)) dead = true;
+    if (!dead && !mbar_test(bar, n & 1) && !mbar_wait(bar, n & 1, a.status)) dead = true;
+  };
+  // For the ring's x-th tile.  A barrier tells a phase from the one before it,
+  // not from the one two before, so the one before has to be over: of the same
+  // rows' earlier tiles it is, but with PAR the slot may have held the other
+  // stream's, which can land after later ones.  Its release is waited for first
+  // (the release before that is over: the tile in between was sent for after
+  // it, and before the stream's last one, which was used; none but this stream
+  // gives the next one).
+  auto landed = [&](uint32_t x) {
+    if (PAR && x >= SLOTS) wait(&sh.empty[x % SLOTS], x / SLOTS - 1);
+    wait(&sh.full[x % SLOTS], x / SLOTS);
   };
 
   if (warp == kTcCopy) {
     if (lane == 0) {
       uint32_t x = 0;  // K and V tiles so far
+      const int j = it.j, item = it.item, t0 = it.t0, tiles = it.s.tiles;  // (the first item's)
       fence_proxy_async_global();  // the inputs were written by generic stores
       do {
         for (int t = it.t0; t < it.t1; ++t)
@@ -768,60 +901,72 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             }
           }
       } while (!dead && leave());
+      leave_join(joins, runs, blockIdx.x, u0, j, item, t0, tiles);
       // nothing is in flight when the CTA ends (in order: each slot's last copy)
       if (dead)
         for (uint32_t i = x > SLOTS ? x - SLOTS : 0; i < x; ++i) mbar_wait(&sh.full[i % SLOTS], i / SLOTS & 1, nullptr);
     }
-  } else if (warp == kTcMma) {
-    if (lane == 0) {
-      constexpr uint32_t idesc_s = __is_same(T, __half) ? tc_idesc_f16(kTcKeys) : tc_idesc_bf16(128, kTcKeys);
-      constexpr uint32_t idesc_o = (__is_same(T, __half) ? tc_idesc_f16(D) : tc_idesc_bf16(128, D)) | (1u << 16);
-      uint32_t x0 = 0;             // K and V tiles before the item
-      uint32_t item = 0, np[2] = {0, 0};
-      do {
-        const int steps = (it.t1 - it.t0) * (PAR ? 1 : 2);
-        auto tile_of = [&](int v) { return x0 + 2 * (uint32_t)(PAR ? v : v >> 1); };
-        auto last_use = [&](int v) { return PAR || (v & 1); };
-        auto qk = [&](int v) {
-          const int m = v & 1;
-          const uint32_t x = tile_of(v), slot = x % SLOTS;
-          wait(&sh.full[slot], x / SLOTS);
-          if (dead) return;
-          tc_fence_after();
-          const uint32_t qa = smem_u32(sQ + m * TILE), kb = smem_u32(sKV + slot * TILE);
+  } else if (warp >= kTcMma) {
+    // All lanes walk along, so that descriptors and addresses are the warp's and
+    // not a thread's; one of them issues.
+    const uint32_t m = __reduce_max_sync(0xffffffffu, (unsigned)(warp - kTcMma)), lead = lane == 0;
+    const uint32_t tmem = __reduce_max_sync(0xffffffffu, sh.tmem);
+    constexpr uint32_t idesc_s = __is_same(T, __half) ? tc_idesc_f16(kTcKeys) : tc_idesc_bf16(128, kTcKeys);
+    constexpr uint32_t idesc_o = (__is_same(T, __half) ? tc_idesc_f16(D) : tc_idesc_bf16(128, D)) | (1u << 16);
+    const uint32_t kv_at = smem_u32(sKV), s_at = tmem + kS + 128 * m, o_at = tmem + D * m;
+    // An operand register that a product still reads cannot be written, so
+    // descriptors are formed before the waits, each in registers of its own.
+    uint64_t qd[D / 16], kd[D / 16], vd[kTcKeys / 16];
 #pragma unroll
-          for (int k = 0; k < D / 16; ++k) {
-            const uint32_t o = (k >> 2) * HALF + (k & 3) * 32;
-            tc_mma_ss(tmem + kS + 128 * m, tc_sdesc_sw128(qa + o), tc_sdesc_sw128(kb + o), idesc_s, k != 0);
-          }
-          tc_commit(&sh.s_ready[m]);
-          if (last_use(v)) tc_commit(&sh.empty[slot]);
-        };
-        wait(&sh.q_ready[0], item);
-        wait(&sh.q_ready[1], item);
-        tc_fence_after();
-        qk(0);
-        if (steps > 1) qk(1);
-        for (int v = 0; v < steps; ++v) {
-          const int m = v & 1;
-          const uint32_t x = tile_of(v) + 1, slot = x % SLOTS;
-          wait(&sh.full[slot], x / SLOTS);
-          wait(&sh.p_ready[m], np[m]++);
-          if (dead) break;
-          tc_fence_after();
-          const uint32_t vb = smem_u32(sKV + slot * TILE);
-#pragma unroll
-          for (int k = 0; k < kTcKeys / 16; ++k)
-            tc_mma_f16_ta(tmem + D * m, tmem + kS + 128 * m + 8 * k, tc_sdesc_mn_sw128(vb + k * 2048, HALF, 1024), idesc_o,
-                          v > 1 || k != 0);
-          if (last_use(v)) tc_commit(&sh.empty[slot]);
-          if (v + 2 < steps) qk(v + 2);
-        }
-        tc_commit(&sh.o_done);
-        x0 += 2 * (it.t1 - it.t0);
-        ++item;
-      } while (leave());
+    for (int k = 0; k < D / 16; ++k) {
+      qd[k] = tc_sdesc_sw128(smem_u32(sQ) + m * TILE) + (((k >> 2) * HALF + (k & 3) * 32) >> 4);  // (the address field)
+      asm volatile("" : "+l"(qd[k]));
     }
+    uint32_t x0 = 0;  // K and V tiles before the item
+    uint32_t item = 0, np = 0;
+    do {
+      const int tiles = (int)__reduce_max_sync(0xffffffffu, (unsigned)(it.t1 - it.t0));
+      auto qk = [&](int t) {  // S of the item's t-th tile
+        const uint32_t x = x0 + 2 * (uint32_t)t, slot = x % SLOTS;
+        const uint64_t d = tc_sdesc_sw128(kv_at + slot * TILE);
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          kd[k] = d + (((k >> 2) * HALF + (k & 3) * 32) >> 4);
+          asm volatile("" : "+l"(kd[k]));
+        }
+        landed(x);
+        if ((dead = __any_sync(0xffffffffu, dead))) return;
+        tc_fence_after();
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) mma_ss_if(lead, s_at, qd[k], kd[k], idesc_s, k != 0);
+        commit_if(lead, &sh.s_ready[m]);
+        commit_if(lead, &sh.empty[slot]);
+      };
+      wait(&sh.q_ready[m], item);
+      constexpr int STEP = PAR ? 2 : 1;
+      const int t0 = PAR ? (int)m : 0;
+      if (t0 < tiles) qk(t0);
+      for (int t = t0; t < tiles; t += STEP) {
+        const uint32_t x = x0 + 2 * (uint32_t)t + 1, slot = x % SLOTS;
+        const uint64_t d = tc_sdesc_mn_sw128(kv_at + slot * TILE, HALF, 1024);
+#pragma unroll
+        for (int k = 0; k < kTcKeys / 16; ++k) {
+          vd[k] = d + k * (2048 >> 4);
+          asm volatile("" : "+l"(vd[k]));
+        }
+        landed(x);
+        wait(&sh.p_ready[m], np++);
+        if ((dead = __any_sync(0xffffffffu, dead))) break;
+        tc_fence_after();
+#pragma unroll
+        for (int k = 0; k < kTcKeys / 16; ++k) mma_ts_if(lead, o_at, s_at + 8 * k, vd[k], idesc_o, t != t0 || k != 0);
+        commit_if(lead, &sh.empty[slot]);
+        if (t + STEP < tiles) qk(t + STEP);
+      }
+      commit_if(lead, &sh.o_done);
+      x0 += 2 * (uint32_t)tiles;
+      ++item;
+    } while (__reduce_max_sync(0xffffffffu, (unsigned)leave()));
   } else if (warp < 8) {
     const int m = warp >> 2, lr = (warp & 3) * 32 + lane;  // stream, row of the stream
     const int rt = PAR ? lr : m * 128 + lr;                 // row of the query tile
@@ -832,13 +977,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     do {
       const int rows = min(S::ROWS, it.s.n * g - it.row0);
       const bool there = rt < rows, some = rt - lane < rows;
-      const int node = there ? (it.row0 + rt) / g : 0, hh = there ? (it.row0 + rt) % g : 0;
-      {  // this row of Q (zero where there is none)
-        const uint16_t* q = a.q + it.j * a.q_seq + node * a.q_tok + (it.head * g + hh) * D;
-#pragma unroll
-        for (int c = 0; c < CH; ++c)
-          *reinterpret_cast<uint4*>(sQ + m * TILE + tile_off(lr, c, 128)) =
-              there ? *reinterpret_cast<const uint4*>(q + c * 8) : make_uint4(0u, 0u, 0u, 0u);
+      const int node = there ? grp.node(it.row0 + rt) : 0, hh = there ? grp.place(it.row0 + rt, node) : 0;
+      {  // Q of the stream's rows
+        if (item) copy_q();
+        cp_async_wait<0>();
         fence_proxy_async_shared();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.q_ready[m]);
@@ -854,38 +996,36 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         wait(&sh.s_ready[m], ns++);
         tc_fence_after();
         if (some) {
+          const uint32_t sa = tmem + lanes + kS + 128 * m;
+          if (tree || here < kTcKeys) {  // keys that the row does not see
+#pragma unroll 1
+            for (int w = 0; w < 4; ++w) {
+              const int left = here - w * 32;
+              uint32_t bits = left >= 32 ? ~0u : left <= 0 ? 0u : (1u << left) - 1u;
+              if (tree) bits &= there ? node_bits(a, it.j, node, (first >> 5) + w) : 0u;
+              uint32_t y[32];
+              tmem_ld32_wait(sa + 32 * w, y);
+#pragma unroll
+              for (int n = 0; n < 32; ++n)
+                if (!(bits >> n & 1)) y[n] = 0xff800000u;
+              tmem_st32(sa + 32 * w, y);
+            }
+            asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+          }
           // Two passes over S, 32 keys at a time (the next ones on their way):
           // the maximum, then the weights.  P of 32 keys takes half the columns
           // of their S, which lie behind all that is still to be read.
-          const uint32_t sa = tmem + lanes + kS + 128 * m;
-          const bool edge = tree || here < kTcKeys;
-          uint32_t bits[4];  // keys that the row sees
-          if (edge) {
-#pragma unroll
-            for (int w = 0; w < 4; ++w) {
-              const int left = here - w * 32;
-              bits[w] = left >= 32 ? ~0u : left <= 0 ? 0u : (1u << left) - 1u;
-              if (tree) bits[w] &= there ? node_bits(a, it.j, node, (first >> 5) + w) : 0u;
-            }
-          }
           float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
           uint32_t x[2][32];
-          auto seen = [&](uint32_t (&y)[32], int w) {
-            if (edge) {
-#pragma unroll
-              for (int n = 0; n < 32; ++n)
-                if (!(bits[w] >> n & 1)) y[n] = 0xff800000u;
-            }
-          };
           tmem_ld32(sa, x[0]);
           tmem_wait_ld(x[0]);
 #pragma unroll
           for (int w = 0; w < 4; ++w) {
             tmem_ld32(sa + 32 * ((w + 1) & 3), x[(w + 1) & 1]);
-            uint32_t(&y)[32] = x[w & 1];
-            seen(y, w);
+            const uint32_t(&y)[32] = x[w & 1];
 #pragma unroll
-            for (int n = 0; n < 32; ++n) mx[n & 3] = fmaxf(mx[n & 3], __uint_as_float(y[n]));
+            for (int n = 0; n < 32; n += 2)
+              mx[n / 2 & 3] = fmaxf(mx[n / 2 & 3], fmaxf(__uint_as_float(y[n]), __uint_as_float(y[n + 1])));
             tmem_wait_ld(x[(w + 1) & 1]);
           }
           const float mnew = fmaxf(mref, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
@@ -906,31 +1046,32 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             }
           }
           const float nb = mref == -INFINITY ? 0.f : -mref * sl2;
-          float sum[4] = {0.f, 0.f, 0.f, 0.f};
+          const uint64_t sl22 = pair(sl2, sl2), nb2 = pair(nb, nb);
+          uint64_t sum[2] = {0, 0};  // pairs of zeros
 #pragma unroll
           for (int w = 0; w < 4; ++w) {  // (the first 32 are in x[0] again)
             if (w < 3) tmem_ld32(sa + 32 * (w + 1), x[(w + 1) & 1]);
-            uint32_t(&y)[32] = x[w & 1];
-            seen(y, w);
+            const uint32_t(&y)[32] = x[w & 1];
             uint32_t p[16];
 #pragma unroll
             for (int c = 0; c < 16; ++c) {
-              const float p0 = fast_exp2(fmaf(__uint_as_float(y[2 * c]), sl2, nb));
-              const float p1 = fast_exp2(fmaf(__uint_as_float(y[2 * c + 1]), sl2, nb));
-              sum[c & 3] += p0 + p1;
+              const float2 e = halves(fma2(pair(__uint_as_float(y[2 * c]), __uint_as_float(y[2 * c + 1])), sl22, nb2));
+              const float p0 = fast_exp2(e.x), p1 = fast_exp2(e.y);
+              sum[c & 1] = add2(sum[c & 1], pair(p0, p1));
               p[c] = pack2<T>(p0, p1);
             }
             if (w < 3) tmem_wait_ld(x[(w + 1) & 1]);
             tmem_st16(sa + 16 * w, p);
           }
-          lsum = lsum * corr + ((sum[0] + sum[1]) + (sum[2] + sum[3]));
+          const float2 total = halves(add2(sum[0], sum[1]));
+          lsum = lsum * corr + (total.x + total.y);
           asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
         }
         if (here < kTcKeys || tree) {
           // rows of V that are not there become zero, and so do a tree's
           // infinities and NaN: they are added to the rows that see them
           const uint32_t x = x0 + 2 * (uint32_t)(t - it.t0) + 1, slot = x % SLOTS;
-          wait(&sh.full[slot], x / SLOTS);
+          landed(x);
           uint8_t* const sV = sKV + slot * TILE;
           bool bad = false;
 #pragma unroll 4
@@ -975,9 +1116,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       }
       const bool whole = it.t0 == 0 && it.t1 == it.s.tiles;
       if (some) {
-        const float inv = lt > 0.f || lt != lt ? 1.f / lt : 0.f;
+        const float keep = !whole ? 1.f : lt > 0.f || lt != lt ? 1.f / lt : 0.f;
         const size_t row = ((size_t)it.j * a.N + node) * a.nq + it.head * g + hh;
-        Part* part = static_cast<Part*>(a.ws) + (size_t)blockIdx.x * 2 + (item ? 1 : 0);
+        Part* part = reinterpret_cast<Part*>(aligned32(a.ws)) + (size_t)blockIdx.x * 2 + (item ? 1 : 0);
         constexpr int COLS = PAR ? D / 2 : D;  // of this thread
 #pragma unroll 1
         for (int c0 = PAR ? m * COLS : 0, ce = c0 + COLS; c0 < ce; c0 += 32) {
@@ -997,9 +1138,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
               }
             }
           }
-          if (there) {
           for (int k = 0; k < W; ++k) {
-            uint32_t z = odd[k];
+            uint32_t z = there ? odd[k] : 0u;
             if (z) z &= node_bits(a, it.j, node, k);
             for (; z; z &= z - 1) {
               const uint16_t* v = a.vt + it.j * a.t_seq + (k * 32 + __ffs(z) - 1) * a.t_tok + it.head * D + c0;
@@ -1010,19 +1150,26 @@ __global__ void __launch_bounds__(kTcThreads, 1)
               }
             }
           }
-          if (whole) {
+          // 32 rows x 32 columns change hands through this warp's share of Q's
+          // room, so that a store covers whole lines of few rows
+          float4* const box = reinterpret_cast<float4*>(sQ + m * TILE) + (warp & 3) * 256;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float* y = o + 8 * e;
-              *reinterpret_cast<uint4*>(a.out + row * D + c0 + 8 * e) =
-                  make_uint4(pack2<T>(y[0] * inv, y[1] * inv), pack2<T>(y[2] * inv, y[3] * inv),
-                             pack2<T>(y[4] * inv, y[5] * inv), pack2<T>(y[6] * inv, y[7] * inv));
+          for (int e = 0; e < 8; ++e)
+            box[lane * 8 + (e ^ (lane & 7))] =
+                make_float4(o[4 * e] * keep, o[4 * e + 1] * keep, o[4 * e + 2] * keep, o[4 * e + 3] * keep);
+          __syncwarp();
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const int r = e * 4 + (lane >> 3), q = lane & 7, qr = rt - lane + r;
+            const float4 y = box[r * 8 + (q ^ (r & 7))];
+            if (qr >= rows) continue;
+            if (whole) {
+              const int nd = grp.node(it.row0 + qr), hd = it.head * g + grp.place(it.row0 + qr, nd);
+              *reinterpret_cast<uint2*>(a.out + (((size_t)it.j * a.N + nd) * a.nq + hd) * D + c0 + 4 * q) =
+                  make_uint2(pack2<T>(y.x, y.y), pack2<T>(y.z, y.w));
+            } else {
+              *reinterpret_cast<float4*>(&part->o[qr][c0 + 4 * q]) = y;
             }
-          } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-              part->o[Part::at(rt, c0 + 4 * e)] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
-          }
           }
           __syncwarp();
         }
@@ -1069,16 +1216,14 @@ cudaError_t launch_tc(const TreeAttnArgs& a0, cudaStream_t st) {
   }
   int ctas = num_sms();
   if (ctas > kMaxCtas) ctas = kMaxCtas;
-  const int g = a.nq / a.nkv;
+  const int g = a.g;
   const int64_t items = (int64_t)a.b * a.nkv * ((a.N * g + S::ROWS - 1) / S::ROWS);
   const int64_t most = (items * S::tiles(a.cap, a.N) + S::MIN_TILES - 1) / S::MIN_TILES;  // were every cache full
   if (most < ctas) ctas = (int)most;
   void* args[] = {&maps[0], &maps[1], &maps[2], &maps[3], &a};
   e = launch_k(fn, dim3(ctas), dim3(kTcThreads), S::SMEM, st, true, args);
   if (e != cudaSuccess) return e;
-  void* jargs[] = {&a, &ctas};
-  return launch_k((const void*)tree_join_kernel<T, D, S>, dim3((unsigned)(items * (S::ROWS / kJoinRows))),
-                  dim3(kJoinThreads), 0, st, true, jargs);
+  return launch_join<T, D, S::ROWS>(a, ctas, st);
 }
 
 // Query tiles of more than kWarpRows rows go to the tensor cores' own memory.
@@ -1093,7 +1238,7 @@ bool maps_fit(const TreeAttnArgs& a) {
 
 template <typename T, int D>
 cudaError_t launch_rows(const TreeAttnArgs& a, cudaStream_t st) {
-  const int rows = a.N * (a.nq / a.nkv);
+  const int rows = a.N * a.g;
   if (rows > kWarpRows && maps_fit(a)) return rows <= 128 ? launch_tc<T, D, true>(a, st) : launch_tc<T, D, false>(a, st);
   return rows <= 16 ? launch<T, D, 1>(a, st) : rows <= 32 ? launch<T, D, 2>(a, st) : launch<T, D, 4>(a, st);
 }
@@ -1109,7 +1254,7 @@ size_t tree_attn_ws_bytes(int64_t b, int N, int nq, int nkv, int d) {
   (void)b;
   const int rows = N * (nq / nkv);
   const int tile = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : rows <= 128 ? 128 : 256;
-  return (size_t)kMaxCtas * 2 * tile * (d + 2) * 4;
+  return (size_t)kMaxCtas * (2 * (size_t)tile * (d + 2) * 4 + sizeof(Join)) + 32;
 }
 
 cudaError_t tree_attention(const TreeAttnArgs& a, int dtype, cudaStream_t st) {

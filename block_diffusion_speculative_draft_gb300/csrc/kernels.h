@@ -374,10 +374,13 @@ struct TreeAttnArgs {
   uint16_t* out;         // [b][N][nq][d]
   float* lse;            // [b][N][nq], nullable
   int b, N, nq, nkv, d, cap;
+  int g;           // nq / nkv, and 2^32 / g rounded up
+  uint32_t g_inv;
   float scale;
   void* ws;
   int* status;
 };
+constexpr int kTreeMaxGroup = 1024;  // query heads of a kv head
 size_t tree_attn_ws_bytes(int64_t b, int N, int nq, int nkv, int d);
 cudaError_t tree_attention(const TreeAttnArgs& a, int dtype, cudaStream_t st);
 

@@ -565,7 +565,8 @@ DFLASH_API int32_t dflash_tree_attention_workspace_size(int32_t b, int32_t N, in
  *    count for nothing); null: node i sees nodes 0 to i, a chain (N = 1: one
  *    token's step).
  *  - out [b][N][nq][d] of dtype, lse_out (nullable) [b][N][nq] fp32.
- *  - d is 64 or 128, nq a multiple of nkv, scale finite and > 0.
+ *  - d is 64 or 128, nq a multiple of nkv (1024 times at most), scale finite and
+ *    > 0.
  * A len[j] outside [0, cap] leaves the sequence out (DFLASH_DEV_BAD_LENGTH).  ws
  * holds dflash_tree_attention_workspace_size bytes, 16-byte aligned; it needs no
  * zero fill and keeps nothing between calls. */

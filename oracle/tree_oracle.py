@@ -38,20 +38,19 @@ def tree_attention(q, k, v, kt, vt, sees, scale):
     n, nq, d = q.shape
     nkv = kt.shape[1]
     o, lse, spread = np.zeros((n, nq, d)), np.full((n, nq), -np.inf), np.zeros((n, nq, d))
-    for i in range(n):
-        at = np.flatnonzero(sees[i])
-        for h in range(nq):
-            g = h * nkv // nq
-            keys = np.concatenate([k[:, g], kt[at, g]]).astype(np.float64)
-            vals = np.concatenate([v[:, g], vt[at, g]]).astype(np.float64)
-            if not len(keys):
-                continue
-            s = scale * (keys @ q[i, h].astype(np.float64))
-            m = s.max()
-            p = np.exp(s - m)
-            o[i, h] = p @ vals / p.sum()
-            spread[i, h] = p @ np.abs(vals) / p.sum()
-            lse[i, h] = m + np.log(p.sum())
+    for h in range(nq):
+        g = h * nkv // nq
+        keys = np.concatenate([k[:, g], kt[:, g]]).astype(np.float64)
+        vals = np.concatenate([v[:, g], vt[:, g]]).astype(np.float64)
+        s = scale * (q[:, h].astype(np.float64) @ keys.T)
+        s[:, len(k):][~sees] = -np.inf
+        m = s.max(1, initial=-np.inf)
+        p = np.exp(s - np.where(np.isneginf(m), 0.0, m)[:, None])
+        total = p.sum(1)
+        some = total > 0
+        o[some, h] = (p @ vals)[some] / total[some, None]
+        spread[some, h] = (p @ np.abs(vals))[some] / total[some, None]
+        lse[some, h] = m[some] + np.log(total[some])
     return o, lse, spread
 
 

@@ -201,6 +201,27 @@ def test_attention_of_many_sequences(b, N, lo, hi):
     _check_attention("f16", kv, 0, q, kt, vt, sees, lens, nodes, 0.125, out, lse, 7.0)
 
 
+@pytest.mark.parametrize("dtype,b,N,nq,nkv,d,cap", [
+    ("f16", 3, 32, 8, 2, 128, 30011),    # 128 rows: both streams walk the tiles of long runs
+    ("bf16", 2, 20, 10, 2, 64, 60000),   # 100 rows
+    ("bf16", 2, 64, 8, 2, 128, 40001),   # 256 rows
+    ("f16", 5, 12, 4, 1, 128, 50000),    # 48 rows
+    ("f16", 6, 1, 16, 4, 128, 30000)])   # one token
+def test_attention_over_long_runs(dtype, b, N, nq, nkv, d, cap):
+    rng = np.random.default_rng(cap)
+    lens, nodes = [cap - 7 * j for j in range(b)], np.array([N - j % 2 * (N // 3) for j in range(b)])
+    kv, q, kt, vt = _attention_case(rng, dtype, b, N, nq, nkv, d, cap, lens, nodes, L=1)
+    sees = np.stack([TO.tree_mask(p)[0] for p in _trees(rng, b, N)])
+    mask = _i32(TO.pack_bits(sees))
+    api.dflash_get_status()
+    out, lse = _attend(kv, 0, q, kt, vt, mask, _i32(nodes))
+    _check_attention(dtype, kv, 0, q, kt, vt, sees, lens, nodes, d ** -0.5, out, lse, 7.0)
+    for _ in range(20):
+        again, lse2 = _attend(kv, 0, q, kt, vt, mask, _i32(nodes))
+        assert torch.equal(out, again) and torch.equal(lse, lse2)
+    assert api.dflash_get_status() == 0
+
+
 @pytest.mark.parametrize("N", [6, 40, 128])
 def test_attention_values_that_a_node_does_not_see_do_not_matter(N):
     rng = np.random.default_rng(N)

@@ -106,3 +106,42 @@ def test_adjust_by_hand():
     assert list(TO.adjust_row(z)[0]) == z
     # the prompt alone asks for no frequency or presence penalty
     assert TO.adjust_row(z, prompt=[5], presence=1.0)[0][5] == 3.0
+
+
+# ---- the ring of K and V tiles that two streams share (a model of its barriers) ----
+def _ring(seed, slots, release_first, tiles=40):
+    """Copies land in any order; stream m uses tiles m, m + 2, ... (K then V of
+    each).  A wait passes where a phase of its parity is the last one over, as
+    the hardware decides it.  'early': it passed before the tile had landed."""
+    r = np.random.default_rng(seed)
+    full, empty, sent, flying = [0] * slots, [0] * slots, 0, []
+    at = [0, 2]  # each stream's next tile, K and V counted
+    passes = lambda over, n: (over - 1) % 2 == n % 2
+    while min(at) < 2 * tiles:
+        who = r.integers(4)
+        if who == 0 and sent < 2 * tiles:
+            if sent < slots or passes(empty[sent % slots], sent // slots - 1):
+                flying.append(sent)
+                sent += 1
+        elif who == 1 and flying:
+            full[flying.pop(r.integers(len(flying))) % slots] += 1
+        elif who >= 2 and at[who - 2] < 2 * tiles:
+            x = at[who - 2]
+            s, n = x % slots, x // slots
+            if release_first and x >= slots and not passes(empty[s], n - 1):
+                continue
+            if passes(full[s], n):
+                if full[s] != n + 1:
+                    return "early"
+                empty[s] += 1
+                at[who - 2] += 3 if x % 2 else 1
+    return "done"
+
+
+@pytest.mark.parametrize("slots", [5, 8])
+def test_two_streams_share_a_ring(slots):
+    assert all(_ring(seed, slots, True) == "done" for seed in range(150))
+
+
+def test_a_ring_of_five_needs_the_release():
+    assert "early" in {_ring(seed, 5, False) for seed in range(30)}
