@@ -640,23 +640,25 @@ cudaError_t launch(const TreeAttnArgs& a0, cudaStream_t st) {
 }
 
 // ---------------------------------------------------------------------------
-// The tensor-memory form.  Two streams of 128 query rows each have S (128 keys,
-// fp32; P over its first half) and O in tensor memory: two blocks of a query
-// tile of 256 rows, each over every tile; or, with up to 128 rows (PAR), the
-// same rows over every other tile, joined at the end.  While one stream's four
-// warps make P of its S (a thread a row, no exchange), the tensor cores work
-// for the other.  One thread copies tiles (TMA, one ring of K and V tiles in
-// the order of their use); a warp a stream issues the products,
-//   wait for P; O += P V; S of the stream's next tile = Q K^T
-// so that one stream's waits (150 to 250 cycles each) pass under the other's
-// products (one warp for both: 3.6 to 3.9 thousand cycles a tile of 256 rows
-// against 2.1 of products).
+// The tensor-memory form.  Two streams of 128 query rows each have O and two
+// buffers of S (64 keys, fp32; P over its first half) in tensor memory: two
+// blocks of a query tile of 256 rows, each over every tile; or, with up to 128
+// rows (PAR), the same rows over every other tile, joined at the end.  One
+// thread copies tiles of 128 keys (TMA, one ring of K and V tiles in the order
+// of their use); a warp a stream issues the products of half a tile after
+// another,
+//   wait for P(i); O += P(i) V;  S(i + 2) = Q K^T, in the buffer of P(i)
+// and four warps a stream make P(i + 1) of the other buffer meanwhile, a thread
+// a row: neither waits for the other while both keep up.  (With one buffer of
+// 128 keys each row's chain, weights then products, took 4.3 thousand cycles a
+// tile of 256 rows; its products take 2.6.)
 // Cached keys fill tiles of their own, the last one padded, and the tree's keys
 // follow in theirs.  Tiles with absent keys have those rows of V zeroed by the
 // threads that mask S, before they hand over P.
 constexpr int kTcKeys = 128;
 constexpr int kTcThreads = 352;  // warps 0-7: rows; 8, 9: the streams' products; 10: copies
 constexpr int kTcMma = 8, kTcCopy = 10;
+constexpr int kTcStep = 64;  // keys of a buffer of S
 
 template <int D, bool PAR>
 struct TcShape {
@@ -674,19 +676,27 @@ struct TcShape {
 
 struct TcCtrl {
   float2 ml[2][128];
-  uint64_t full[8], empty[8], s_ready[2], p_ready[2], q_ready[2], o_done;
+  uint64_t full[8], empty[8], s_ready[2][2], p_ready[2][2], pv_done[2], q_ready[2], o_done;
   uint32_t odd[2][kTreeMax / 32];
   uint32_t tmem;
 };
 static_assert(sizeof(TcCtrl) <= 2 * 128 * 8 + 512, "");
 
-// Waits for this thread's tensor-memory loads; names the registers of one, so
-// that no use of them is scheduled before.
-__device__ __forceinline__ void tmem_wait_ld(uint32_t (&v)[32]) {
-#define R8(i) "+r"(v[i]), "+r"(v[i + 1]), "+r"(v[i + 2]), "+r"(v[i + 3]), "+r"(v[i + 4]), "+r"(v[i + 5]), "+r"(v[i + 6]), "+r"(v[i + 7])
-  asm volatile("tcgen05.wait::ld.sync.aligned;" : R8(0), R8(8), R8(16), R8(24)::"memory");
+// 64 consecutive tensor-memory columns of this warp's 32 lanes to registers.
+__device__ __forceinline__ void tmem_ld64_wait(uint32_t taddr, uint32_t (&v)[64]) {
+#define R8(i) "=r"(v[i]), "=r"(v[i + 1]), "=r"(v[i + 2]), "=r"(v[i + 3]), "=r"(v[i + 4]), "=r"(v[i + 5]), "=r"(v[i + 6]), "=r"(v[i + 7])
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
+      "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%64];\n"
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,%48,%49,"
+      "%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%65];\n"
+      "tcgen05.wait::ld.sync.aligned;"
+      : R8(0), R8(8), R8(16), R8(24), R8(32), R8(40), R8(48), R8(56)
+      : "r"(taddr), "r"(taddr + 32)
+      : "memory");
 #undef R8
 }
+#undef R8
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
@@ -795,21 +805,21 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     Seq s;
     int head, row0, ctx;  // kv head, first query row, tiles of cached keys
   };
-  long long u = u0;
+  int left = (int)(u1 - u0);  // tiles of the run from the item on (a cache that fits the device has fewer than 2^31)
   Item it;
   it.j = j0;
   it.s = seq_of<S>(a, it.j);
   it.item = (int)Runs::ratio(u0 - base, it.s.tiles);
   it.t0 = (int)(u0 - base - (long long)it.item * it.s.tiles);
   auto enter = [&]() {  // the rest of the item's places
-    it.t1 = (int)min((long long)it.s.tiles, it.t0 + (u1 - u));
+    it.t1 = min(it.s.tiles, it.t0 + left);
     it.head = it.item / it.s.qtiles;
     it.row0 = (it.item % it.s.qtiles) * S::ROWS;
     it.ctx = (it.s.len + kTcKeys - 1) / kTcKeys;
   };
   auto leave = [&]() {  // to the next item; false at the run's end
-    u += it.t1 - it.t0;
-    if (u >= u1) return false;
+    left -= it.t1 - it.t0;
+    if (left <= 0) return false;
     it.t0 = 0;
     if (++it.item >= a.nkv * it.s.qtiles) {
       it.item = 0;
@@ -820,6 +830,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     return true;
   };
   enter();
+  // Keys of tile t (of the run's item; 128 or more: all), and its halves that hold any.
+  auto keys_of = [&](int t) { return t < it.ctx ? it.s.len - t * kTcKeys : it.s.n - (t - it.ctx) * kTcKeys; };
+  auto halves_of = [&](int t) { return keys_of(t) > kTcStep ? 2 : 1; };
   // Q of the stream's rows (zero where there is none), a row by neighbouring threads
   auto copy_q = [&]() {
     const int m = warp >> 2, lr = (warp & 3) * 32 + lane;
@@ -844,8 +857,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       mbar_init(&sh.empty[i], PAR ? 1 : 2);  // streams that read a tile
     }
     for (int m = 0; m < 2; ++m) {
-      mbar_init(&sh.s_ready[m], 1);
-      mbar_init(&sh.p_ready[m], 4);
+      for (int i = 0; i < 2; ++i) {
+        mbar_init(&sh.s_ready[m][i], 1);
+        mbar_init(&sh.p_ready[m][i], 4);
+      }
+      mbar_init(&sh.pv_done[m], 1);
       mbar_init(&sh.q_ready[m], 4);
     }
     mbar_init(&sh.o_done, 2);
@@ -860,7 +876,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sh.tmem;
-  constexpr uint32_t kS = 2 * D;  // columns: O of the two streams, then their S
+  constexpr uint32_t kS = 2 * D;  // columns: O of the two streams, then the buffers of S of each
   bool dead = false;  // a wait gave up: the status is raised, the rest only drains
   auto wait = [&](uint64_t* bar, uint32_t n) {  // for the bar's n-th completion, from 0
     if (!dead && !mbar_test(bar, n & 1) && !mbar_wait(bar, n & 1, a.status)) dead = true;
@@ -911,57 +927,59 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     // not a thread's; one of them issues.
     const uint32_t m = __reduce_max_sync(0xffffffffu, (unsigned)(warp - kTcMma)), lead = lane == 0;
     const uint32_t tmem = __reduce_max_sync(0xffffffffu, sh.tmem);
-    constexpr uint32_t idesc_s = __is_same(T, __half) ? tc_idesc_f16(kTcKeys) : tc_idesc_bf16(128, kTcKeys);
+    constexpr uint32_t idesc_s = __is_same(T, __half) ? tc_idesc_f16(kTcStep) : tc_idesc_bf16(128, kTcStep);
     constexpr uint32_t idesc_o = (__is_same(T, __half) ? tc_idesc_f16(D) : tc_idesc_bf16(128, D)) | (1u << 16);
+    constexpr uint32_t kHalfTile = kTcStep * 128;  // bytes from a half's rows to the other's
     const uint32_t kv_at = smem_u32(sKV), s_at = tmem + kS + 128 * m, o_at = tmem + D * m;
-    // An operand register that a product still reads cannot be written, so
-    // descriptors are formed before the waits, each in registers of its own.
-    uint64_t qd[D / 16], kd[D / 16], vd[kTcKeys / 16];
-#pragma unroll
-    for (int k = 0; k < D / 16; ++k) {
-      qd[k] = tc_sdesc_sw128(smem_u32(sQ) + m * TILE) + (((k >> 2) * HALF + (k & 3) * 32) >> 4);  // (the address field)
-      asm volatile("" : "+l"(qd[k]));
-    }
+    const uint64_t qd = tc_sdesc_sw128(smem_u32(sQ) + m * TILE);
     uint32_t x0 = 0;  // K and V tiles before the item
-    uint32_t item = 0, np = 0;
+    uint32_t item = 0, ns = 0, np = 0;  // items, halves sent for and added so far
     do {
       const int tiles = (int)__reduce_max_sync(0xffffffffu, (unsigned)(it.t1 - it.t0));
-      auto qk = [&](int t) {  // S of the item's t-th tile
-        const uint32_t x = x0 + 2 * (uint32_t)t, slot = x % SLOTS;
-        const uint64_t d = tc_sdesc_sw128(kv_at + slot * TILE);
-#pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          kd[k] = d + (((k >> 2) * HALF + (k & 3) * 32) >> 4);
-          asm volatile("" : "+l"(kd[k]));
-        }
-        landed(x);
+      constexpr int STEP = PAR ? 2 : 1;
+      const int k0 = PAR ? (int)m : 0;
+      int kq = k0, hq = 0;  // tile and half that the next S is of
+      auto qk = [&]() {
+        const uint32_t x = x0 + 2 * (uint32_t)kq, slot = x % SLOTS;
+        if (hq == 0) landed(x);
         if ((dead = __any_sync(0xffffffffu, dead))) return;
         tc_fence_after();
+        const uint64_t kd = tc_sdesc_sw128(kv_at + slot * TILE + hq * kHalfTile);
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k) mma_ss_if(lead, s_at, qd[k], kd[k], idesc_s, k != 0);
-        commit_if(lead, &sh.s_ready[m]);
-        commit_if(lead, &sh.empty[slot]);
+        for (int k = 0; k < D / 16; ++k) {
+          const uint32_t o = ((k >> 2) * HALF + (k & 3) * 32) >> 4;  // (of the address field)
+          mma_ss_if(lead, s_at + kTcStep * (ns & 1), qd + o, kd + o, idesc_s, k != 0);
+        }
+        commit_if(lead, &sh.s_ready[m][ns & 1]);
+        ++ns;
+        if (++hq == halves_of(it.t0 + kq)) {
+          commit_if(lead, &sh.empty[slot]);
+          hq = 0;
+          kq += STEP;
+        }
       };
       wait(&sh.q_ready[m], item);
-      constexpr int STEP = PAR ? 2 : 1;
-      const int t0 = PAR ? (int)m : 0;
-      if (t0 < tiles) qk(t0);
-      for (int t = t0; t < tiles; t += STEP) {
-        const uint32_t x = x0 + 2 * (uint32_t)t + 1, slot = x % SLOTS;
-        const uint64_t d = tc_sdesc_mn_sw128(kv_at + slot * TILE, HALF, 1024);
+      if (kq < tiles) qk();
+      if (kq < tiles) qk();
+      bool first = true;
+      for (int k = k0; k < tiles && !dead; k += STEP) {
+        const uint32_t x = x0 + 2 * (uint32_t)k + 1, slot = x % SLOTS;
+        const int halves = halves_of(it.t0 + k);
+        for (int h = 0; h < halves; ++h) {
+          if (h == 0) landed(x);
+          wait(&sh.p_ready[m][np & 1], np >> 1);
+          if ((dead = __any_sync(0xffffffffu, dead))) break;
+          tc_fence_after();
+          const uint64_t vd = tc_sdesc_mn_sw128(kv_at + slot * TILE + h * kHalfTile, HALF, 1024);
 #pragma unroll
-        for (int k = 0; k < kTcKeys / 16; ++k) {
-          vd[k] = d + k * (2048 >> 4);
-          asm volatile("" : "+l"(vd[k]));
+          for (int c = 0; c < kTcStep / 16; ++c)
+            mma_ts_if(lead, o_at, s_at + kTcStep * (np & 1) + 8 * c, vd + c * (2048 >> 4), idesc_o, !first || c != 0);
+          first = false;
+          commit_if(lead, &sh.pv_done[m]);
+          ++np;
+          if (h + 1 == halves) commit_if(lead, &sh.empty[slot]);
+          if (kq < tiles) qk();
         }
-        landed(x);
-        wait(&sh.p_ready[m], np++);
-        if ((dead = __any_sync(0xffffffffu, dead))) break;
-        tc_fence_after();
-#pragma unroll
-        for (int k = 0; k < kTcKeys / 16; ++k) mma_ts_if(lead, o_at, s_at + 8 * k, vd[k], idesc_o, t != t0 || k != 0);
-        commit_if(lead, &sh.empty[slot]);
-        if (t + STEP < tiles) qk(t + STEP);
       }
       commit_if(lead, &sh.o_done);
       x0 += 2 * (uint32_t)tiles;
@@ -986,117 +1004,110 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         if (lane == 0) mbar_arrive(&sh.q_ready[m]);
       }
       float mref = -INFINITY, lsum = 0.f;  // reference maximum (raw scores) and sum of the row
-      const int steps = (it.t1 - it.t0) * (PAR ? 1 : 2);
+      const int tiles = it.t1 - it.t0;
       uint32_t* const odd = sh.odd[item & 1];
-      for (int v = m; v < steps; v += 2) {
-        const int t = it.t0 + (PAR ? v : v >> 1);
+      for (int k = PAR ? m : 0; k < tiles; k += PAR ? 2 : 1) {
+        const int t = it.t0 + k, keys = keys_of(t), halves_t = halves_of(t);
         const bool tree = t >= it.ctx;
-        const int first = (tree ? t - it.ctx : t) * kTcKeys;         // the tile's first key or node
-        const int here = (tree ? it.s.n : it.s.len) - first;  // keys of the tile (128 or more: all)
-        wait(&sh.s_ready[m], ns++);
-        tc_fence_after();
-        if (some) {
-          const uint32_t sa = tmem + lanes + kS + 128 * m;
-          if (tree || here < kTcKeys) {  // keys that the row does not see
-#pragma unroll 1
-            for (int w = 0; w < 4; ++w) {
-              const int left = here - w * 32;
-              uint32_t bits = left >= 32 ? ~0u : left <= 0 ? 0u : (1u << left) - 1u;
-              if (tree) bits &= there ? node_bits(a, it.j, node, (first >> 5) + w) : 0u;
-              uint32_t y[32];
-              tmem_ld32_wait(sa + 32 * w, y);
+        const int first = (tree ? t - it.ctx : t) * kTcKeys;  // the tile's first key or node
+        for (int h = 0; h < halves_t; ++h, ++ns) {
+          const int here = keys - h * kTcStep;  // keys of the half (64 or more: all)
+          const bool edge = tree || here < kTcStep;
+          const uint32_t sa = tmem + lanes + kS + 128 * m + kTcStep * (ns & 1);
+          wait(&sh.s_ready[m][ns & 1], ns >> 1);
+          tc_fence_after();
+          if (some) {
+            uint32_t s[64];
+            tmem_ld64_wait(sa, s);
+            if (edge) {  // keys that the row does not see
 #pragma unroll
-              for (int n = 0; n < 32; ++n)
-                if (!(bits >> n & 1)) y[n] = 0xff800000u;
-              tmem_st32(sa + 32 * w, y);
-            }
-            asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-          }
-          // Two passes over S, 32 keys at a time (the next ones on their way):
-          // the maximum, then the weights.  P of 32 keys takes half the columns
-          // of their S, which lie behind all that is still to be read.
-          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-          uint32_t x[2][32];
-          tmem_ld32(sa, x[0]);
-          tmem_wait_ld(x[0]);
+              for (int w = 0; w < 2; ++w) {
+                const int rest = here - w * 32;
+                uint32_t bits = rest >= 32 ? ~0u : rest <= 0 ? 0u : (1u << rest) - 1u;
+                if (tree) bits &= there ? node_bits(a, it.j, node, (first + h * kTcStep) / 32 + w) : 0u;
 #pragma unroll
-          for (int w = 0; w < 4; ++w) {
-            tmem_ld32(sa + 32 * ((w + 1) & 3), x[(w + 1) & 1]);
-            const uint32_t(&y)[32] = x[w & 1];
-#pragma unroll
-            for (int n = 0; n < 32; n += 2)
-              mx[n / 2 & 3] = fmaxf(mx[n / 2 & 3], fmaxf(__uint_as_float(y[n]), __uint_as_float(y[n + 1])));
-            tmem_wait_ld(x[(w + 1) & 1]);
-          }
-          const float mnew = fmaxf(mref, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
-          // The reference follows the maximum where it lags by more than 8 in
-          // log2 units: weights stay below 2^8, which P and the sums hold, and
-          // O is seldom rescaled.
-          const bool resc = mref != -INFINITY && (mnew - mref) * sl2 > 8.f;
-          const float corr = resc ? fast_exp2((mref - mnew) * sl2) : 1.f;
-          if (mref == -INFINITY || resc) mref = mnew;
-          if (__any_sync(0xffffffffu, resc)) {
-#pragma unroll 1
-            for (int c = 0; c < D; c += 32) {  // (the stream's earlier products were committed before this S)
-              uint32_t o[32];
-              tmem_ld32_wait(tmem + lanes + m * D + c, o);
-#pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * corr);
-              tmem_st32(tmem + lanes + m * D + c, o);
-            }
-          }
-          const float nb = mref == -INFINITY ? 0.f : -mref * sl2;
-          const uint64_t sl22 = pair(sl2, sl2), nb2 = pair(nb, nb);
-          uint64_t sum[2] = {0, 0};  // pairs of zeros
-#pragma unroll
-          for (int w = 0; w < 4; ++w) {  // (the first 32 are in x[0] again)
-            if (w < 3) tmem_ld32(sa + 32 * (w + 1), x[(w + 1) & 1]);
-            const uint32_t(&y)[32] = x[w & 1];
-            uint32_t p[16];
-#pragma unroll
-            for (int c = 0; c < 16; ++c) {
-              const float2 e = halves(fma2(pair(__uint_as_float(y[2 * c]), __uint_as_float(y[2 * c + 1])), sl22, nb2));
-              const float p0 = fast_exp2(e.x), p1 = fast_exp2(e.y);
-              sum[c & 1] = add2(sum[c & 1], pair(p0, p1));
-              p[c] = pack2<T>(p0, p1);
-            }
-            if (w < 3) tmem_wait_ld(x[(w + 1) & 1]);
-            tmem_st16(sa + 16 * w, p);
-          }
-          const float2 total = halves(add2(sum[0], sum[1]));
-          lsum = lsum * corr + (total.x + total.y);
-          asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-        }
-        if (here < kTcKeys || tree) {
-          // rows of V that are not there become zero, and so do a tree's
-          // infinities and NaN: they are added to the rows that see them
-          const uint32_t x = x0 + 2 * (uint32_t)(t - it.t0) + 1, slot = x % SLOTS;
-          landed(x);
-          uint8_t* const sV = sKV + slot * TILE;
-          bool bad = false;
-#pragma unroll 4
-          for (int c = 0; c < CH; ++c) {
-            uint4* e = reinterpret_cast<uint4*>(sV + tile_off(lr, c, 128));
-            if (lr >= here) {
-              *e = make_uint4(0u, 0u, 0u, 0u);
-            } else if (tree) {
-              uint4 y = *e;
-              if (not_finite<T>(y.x) | not_finite<T>(y.y) | not_finite<T>(y.z) | not_finite<T>(y.w)) {
-                uint16_t* z = reinterpret_cast<uint16_t*>(&y);
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                  if (not_finite<T>(z[i])) z[i] = 0;
-                *e = y;
-                bad = true;
+                for (int n = 0; n < 32; ++n)
+                  if (!(bits >> n & 1)) s[w * 32 + n] = 0xff800000u;
               }
             }
+            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+            for (int n = 0; n < 64; n += 2)
+              mx[n / 2 & 3] = fmaxf(mx[n / 2 & 3], fmaxf(__uint_as_float(s[n]), __uint_as_float(s[n + 1])));
+            const float mnew = fmaxf(mref, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
+            // The reference follows the maximum where it lags by more than 8 in
+            // log2 units: weights stay below 2^8, which P and the sums hold, and
+            // O is seldom rescaled.
+            const bool resc = mref != -INFINITY && (mnew - mref) * sl2 > 8.f;
+            if (__any_sync(0xffffffffu, resc)) {
+              const float corr = resc ? fast_exp2((mref - mnew) * sl2) : 1.f;
+              lsum *= corr;
+              // O holds what was added before this half: the last of it has to be
+              // over (the one before it is, S was sent for after it)
+              wait(&sh.pv_done[m], ns - 1);
+              tc_fence_after();
+#pragma unroll 1
+              for (int c = 0; c < D; c += 32) {
+                uint32_t o[32];
+                tmem_ld32_wait(tmem + lanes + m * D + c, o);
+#pragma unroll
+                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * corr);
+                tmem_st32(tmem + lanes + m * D + c, o);
+              }
+            }
+            if (mref == -INFINITY || resc) mref = mnew;
+            const float nb = mref == -INFINITY ? 0.f : -mref * sl2;
+            const uint64_t sl22 = pair(sl2, sl2), nb2 = pair(nb, nb);
+            uint64_t sum[2] = {0, 0};  // pairs of zeros
+#pragma unroll
+            for (int w = 0; w < 2; ++w) {
+              uint32_t p[16];
+#pragma unroll
+              for (int c = 0; c < 16; ++c) {
+                const int n = w * 32 + 2 * c;
+                const float2 e = halves(fma2(pair(__uint_as_float(s[n]), __uint_as_float(s[n + 1])), sl22, nb2));
+                const float p0 = fast_exp2(e.x), p1 = fast_exp2(e.y);
+                sum[c & 1] = add2(sum[c & 1], pair(p0, p1));
+                p[c] = pack2<T>(p0, p1);
+              }
+              tmem_st16(sa + 16 * w, p);
+            }
+            const float2 total = halves(add2(sum[0], sum[1]));
+            lsum += total.x + total.y;
+            asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
           }
-          if (bad) atomicOr(&odd[(first + lr) >> 5], 1u << (lr & 31));
-          fence_proxy_async_shared();
+          if (edge) {
+            // rows of V that are not there become zero, and so do a tree's
+            // infinities and NaN: they are added to the rows that see them
+            const uint32_t x = x0 + 2 * (uint32_t)k + 1;
+            landed(x);
+            const int r = lr % kTcStep;  // two threads a row of the half
+            uint8_t* const sV = sKV + x % SLOTS * TILE;
+            bool bad = false;
+#pragma unroll 4
+            for (int c = lr / kTcStep * (CH / 2), ce = c + CH / 2; c < ce; ++c) {
+              uint4* e = reinterpret_cast<uint4*>(sV + tile_off(h * kTcStep + r, c, 128));
+              if (r >= here) {
+                *e = make_uint4(0u, 0u, 0u, 0u);
+              } else if (tree) {
+                uint4 y = *e;
+                if (not_finite<T>(y.x) | not_finite<T>(y.y) | not_finite<T>(y.z) | not_finite<T>(y.w)) {
+                  uint16_t* z = reinterpret_cast<uint16_t*>(&y);
+#pragma unroll
+                  for (int i = 0; i < 8; ++i)
+                    if (not_finite<T>(z[i])) z[i] = 0;
+                  *e = y;
+                  bad = true;
+                }
+              }
+            }
+            if (bad) atomicOr(&odd[(first + h * kTcStep + r) >> 5], 1u << (r & 31));
+            fence_proxy_async_shared();
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh.p_ready[m][ns & 1]);
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.p_ready[m]);
       }
       // ---------------- the item's rows ----------------
       wait(&sh.o_done, item);
@@ -1131,7 +1142,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             if (PAR) {
 #pragma unroll
               for (int e = 0; e < 32; ++e) o[e] *= w[0];
-              if (steps > 1) {
+              if (tiles > 1) {
                 tmem_ld32_wait(tmem + lanes + D + c0, y);
 #pragma unroll
                 for (int e = 0; e < 32; ++e) o[e] = fmaf(__uint_as_float(y[e]), w[1], o[e]);
@@ -1181,7 +1192,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       if (tid < kTreeMax / 32) sh.odd[(item & 1) ^ 1][tid] = 0;  // (last read before the barrier above)
       tc_fence_before();
       rows_sync();  // O is read, the statistics too
-      x0 += 2 * (uint32_t)(it.t1 - it.t0);
+      x0 += 2 * (uint32_t)tiles;
       ++item;
     } while (leave());
   }
