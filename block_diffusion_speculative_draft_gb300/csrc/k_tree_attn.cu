@@ -723,28 +723,29 @@ __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, i
       "l"(map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
       : "memory");
 }
-// The products and commits of tcgen05.cuh, issued by the lanes where `on` is set.
-__device__ __forceinline__ void mma_ss_if(uint32_t on, uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+// The products and commits of tcgen05.cuh, called by a whole warp and issued by
+// one of its lanes.  The choice stands beside each instruction: with a predicate
+// kept from before, 4 x 64 nodes over 65536 keys took 243 us in place of 228.
+__device__ __forceinline__ void mma_ss_elect(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
                                           uint32_t accumulate) {
   asm volatile(
-      "{ .reg .pred p, q; setp.ne.u32 p, %4, 0; setp.ne.u32 q, %5, 0;\n"
+      "{ .reg .pred p, q; setp.ne.u32 p, %4, 0; elect.sync _|q, 0xffffffff;\n"
       "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p; }" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(on)
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
-__device__ __forceinline__ void mma_ts_if(uint32_t on, uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+__device__ __forceinline__ void mma_ts_elect(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
                                           uint32_t accumulate) {
   asm volatile(
-      "{ .reg .pred p, q; setp.ne.u32 p, %4, 0; setp.ne.u32 q, %5, 0;\n"
+      "{ .reg .pred p, q; setp.ne.u32 p, %4, 0; elect.sync _|q, 0xffffffff;\n"
       "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p; }" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(on)
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
-__device__ __forceinline__ void commit_if(uint32_t on, uint64_t* bar) {
+__device__ __forceinline__ void commit_elect(uint64_t* bar) {
   asm volatile(
-      "{ .reg .pred q; setp.ne.u32 q, %1, 0;\n"
-      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0]; }" ::"r"(smem_u32(bar)),
-      "r"(on)
+      "{ .reg .pred q; elect.sync _|q, 0xffffffff;\n"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0]; }" ::"r"(smem_u32(bar))
       : "memory");
 }
 // Two fp32 numbers in a register pair, worked on by one instruction.
@@ -924,8 +925,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     }
   } else if (warp >= kTcMma) {
     // All lanes walk along, so that descriptors and addresses are the warp's and
-    // not a thread's; one of them issues.
-    const uint32_t m = __reduce_max_sync(0xffffffffu, (unsigned)(warp - kTcMma)), lead = lane == 0;
+    // not a thread's.
+    const uint32_t m = __reduce_max_sync(0xffffffffu, (unsigned)(warp - kTcMma));
     const uint32_t tmem = __reduce_max_sync(0xffffffffu, sh.tmem);
     constexpr uint32_t idesc_s = __is_same(T, __half) ? tc_idesc_f16(kTcStep) : tc_idesc_bf16(128, kTcStep);
     constexpr uint32_t idesc_o = (__is_same(T, __half) ? tc_idesc_f16(D) : tc_idesc_bf16(128, D)) | (1u << 16);
@@ -948,12 +949,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
           const uint32_t o = ((k >> 2) * HALF + (k & 3) * 32) >> 4;  // (of the address field)
-          mma_ss_if(lead, s_at + kTcStep * (ns & 1), qd + o, kd + o, idesc_s, k != 0);
+          mma_ss_elect(s_at + kTcStep * (ns & 1), qd + o, kd + o, idesc_s, k != 0);
         }
-        commit_if(lead, &sh.s_ready[m][ns & 1]);
+        commit_elect(&sh.s_ready[m][ns & 1]);
         ++ns;
         if (++hq == halves_of(it.t0 + kq)) {
-          commit_if(lead, &sh.empty[slot]);
+          commit_elect(&sh.empty[slot]);
           hq = 0;
           kq += STEP;
         }
@@ -973,15 +974,15 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           const uint64_t vd = tc_sdesc_mn_sw128(kv_at + slot * TILE + h * kHalfTile, HALF, 1024);
 #pragma unroll
           for (int c = 0; c < kTcStep / 16; ++c)
-            mma_ts_if(lead, o_at, s_at + kTcStep * (np & 1) + 8 * c, vd + c * (2048 >> 4), idesc_o, !first || c != 0);
+            mma_ts_elect(o_at, s_at + kTcStep * (np & 1) + 8 * c, vd + c * (2048 >> 4), idesc_o, !first || c != 0);
           first = false;
-          commit_if(lead, &sh.pv_done[m]);
+          commit_elect(&sh.pv_done[m]);
           ++np;
-          if (h + 1 == halves) commit_if(lead, &sh.empty[slot]);
+          if (h + 1 == halves) commit_elect(&sh.empty[slot]);
           if (kq < tiles) qk();
         }
       }
-      commit_if(lead, &sh.o_done);
+      commit_elect(&sh.o_done);
       x0 += 2 * (uint32_t)tiles;
       ++item;
     } while (__reduce_max_sync(0xffffffffu, (unsigned)leave()));
@@ -1017,19 +1018,25 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           wait(&sh.s_ready[m][ns & 1], ns >> 1);
           tc_fence_after();
           if (some) {
-            uint32_t s[64];
-            tmem_ld64_wait(sa, s);
             if (edge) {  // keys that the row does not see
-#pragma unroll
+#pragma unroll 1
               for (int w = 0; w < 2; ++w) {
                 const int rest = here - w * 32;
                 uint32_t bits = rest >= 32 ? ~0u : rest <= 0 ? 0u : (1u << rest) - 1u;
                 if (tree) bits &= there ? node_bits(a, it.j, node, (first + h * kTcStep) / 32 + w) : 0u;
+                uint32_t y[32];
+                tmem_ld32_wait(sa + 32 * w, y);
 #pragma unroll
                 for (int n = 0; n < 32; ++n)
-                  if (!(bits >> n & 1)) s[w * 32 + n] = 0xff800000u;
+                  if (!(bits >> n & 1)) y[n] = 0xff800000u;
+                tmem_st32(sa + 32 * w, y);
               }
+              asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
             }
+            // two passes over S: in registers for the maximum, 32 keys at a time for
+            // the weights (a short loop; all 64 at once: 248 us in place of 243)
+            uint32_t s[64];
+            tmem_ld64_wait(sa, s);
             float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
             for (int n = 0; n < 64; n += 2)
@@ -1059,13 +1066,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             const float nb = mref == -INFINITY ? 0.f : -mref * sl2;
             const uint64_t sl22 = pair(sl2, sl2), nb2 = pair(nb, nb);
             uint64_t sum[2] = {0, 0};  // pairs of zeros
-#pragma unroll
+#pragma unroll 1
             for (int w = 0; w < 2; ++w) {
-              uint32_t p[16];
+              uint32_t y[32], p[16];
+              tmem_ld32_wait(sa + 32 * w, y);
 #pragma unroll
               for (int c = 0; c < 16; ++c) {
-                const int n = w * 32 + 2 * c;
-                const float2 e = halves(fma2(pair(__uint_as_float(s[n]), __uint_as_float(s[n + 1])), sl22, nb2));
+                const float2 e = halves(fma2(pair(__uint_as_float(y[2 * c]), __uint_as_float(y[2 * c + 1])), sl22, nb2));
                 const float p0 = fast_exp2(e.x), p1 = fast_exp2(e.y);
                 sum[c & 1] = add2(sum[c & 1], pair(p0, p1));
                 p[c] = pack2<T>(p0, p1);
