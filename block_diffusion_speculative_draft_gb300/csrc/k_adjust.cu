@@ -8,12 +8,13 @@
 // Bound by HBM: a row is read and written once.  One CTA takes one segment of
 // the vocabulary for all rows of a sequence, so the history is counted once a
 // segment and not once a row: a scan of the whole history (L2 after the first
-// CTA) into counters in shared memory, and one bit an entry that tells whether
-// anything but the grammar touches it.  Rows then stream by with two tests a
-// 16-byte pack (those bits, the grammar's bits); most packs pass unchanged.
-// A row's path adds to few entries: they are marked in the counters, and the
-// path is walked where a marked entry comes by, so rows need no barrier
-// between them.
+// CTA) into counters in shared memory, then a list of the entries that it, the
+// drafts or the biases touch.  A few rows at a time then stream by as they are,
+// but for the grammar's bits, and a warp a row goes through the list and writes
+// the touched entries over.  (With the touched entries worked on where they came
+// by, nearly every warp had one, and a batch of 1024 rows took 4.6 times the
+// bytes' time.)  A row's path adds to few entries: they are marked in the
+// counters, and the path is walked for those.
 #include "kernels.h"
 #include "rows.cuh"
 
@@ -24,6 +25,7 @@ namespace {
 constexpr int kDevBadLength = 0x4, kDevBadParam = 0x8;
 constexpr int kThreads = 256;
 constexpr int kFlight = 4;  // packs a thread has in flight
+constexpr int kScan = 8;    // tokens of the history
 
 // A counter: generated tokens (bits 0-19), in the prompt, among the drafts,
 // and, in bits 22-31, kAdjustMaxBias less the place of the entry's bias in the
@@ -56,67 +58,60 @@ __device__ __forceinline__ T of_bits(uint32_t b) {
   }
 }
 
-// n <= 16 bits of a bit row from bit `at`; words past `words` are not read.
+// n <= 16 bits of a bit row from bit `at`, ones above them; words past `words`
+// are not read.
 __device__ __forceinline__ uint32_t bits_at(const uint32_t* w, int64_t at, int n, int64_t words) {
   const int64_t i = at >> 5;
   const int s = (int)(at & 31);
   uint32_t v = w[i] >> s;
   if (s + n > 32 && i + 1 < words) v |= w[i + 1] << (32 - s);
-  return v & ((1u << n) - 1u);
+  return v | ~((1u << n) - 1u);
 }
 
 struct Shared {
   float rho, freq, pres;
   int bad;     // nothing of the sequence can be worked
   int repeat;  // a biased entry is listed twice
-  int D;
+  int listed[kThreads / 32 + 1];  // touched entries of each warp's share, and before it
   int bias_idx[kAdjustMaxBias];
   float bias_val[kAdjustMaxBias];
   int draft[kTreeMax];
   int allow_row[kTreeMax];  // -1: no grammar, -2: out of range
 };
 
-// The entries of a pack that something touches (bits of `touch`); at: the
-// pack's first entry in the segment that starts at s0; path: bits of the
-// drafts that the row follows, null: the first `follows`.
+// Entries before a row's first 16-byte boundary.
 template <typename T>
-__device__ __noinline__ uint4 touched_pack(uint4 raw, uint32_t touch, int at, int s0, const uint32_t* count,
-                                           const Shared* sh, const uint32_t* path, int follows) {
-  constexpr int E = 16 / sizeof(T);
-  T* x = reinterpret_cast<T*>(&raw);
+__device__ __forceinline__ int head_of(const T* p) {
+  return (int)((16 - ((uintptr_t)p & 15)) & 15) / (int)sizeof(T);
+}
+template <typename T>
+__device__ __forceinline__ uint4 fill(uint32_t bits) {
+  const uint32_t w = sizeof(T) == 4 ? bits : bits << 16 | bits;
+  return make_uint4(w, w, w, w);
+}
+// -inf where a bit of `ok` is clear.
+template <typename T>
+__device__ __forceinline__ uint4 allow_pack(uint4 raw, uint32_t ok) {
+  uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
 #pragma unroll
-  for (int i = 0; i < E; ++i) {
-    if (!(touch >> i & 1)) continue;
-    const uint32_t w = count[at + i];
-    uint32_t c = w & kCount;
-    if (w & kDraft) {
-      const int v = s0 + at + i;
-      if (path) {
-        for (int k = 0; k * 32 < sh->D; ++k)
-          for (uint32_t m = path[k]; m; m &= m - 1) {
-            const int d = k * 32 + __ffs(m) - 1;
-            c += d < sh->D && sh->draft[d] == v;
-          }
-      } else {
-        for (int d = 0; d < follows; ++d) c += sh->draft[d] == v;
-      }
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (sizeof(T) == 4) {
+      if (!(ok >> i & 1)) w[i] = Bits<T>::ninf;
+    } else {
+      if (!(ok >> (2 * i) & 1)) w[i] = (w[i] & 0xffff0000u) | Bits<T>::ninf;
+      if (!(ok >> (2 * i + 1) & 1)) w[i] = (w[i] & 0xffffu) | Bits<T>::ninf << 16;
     }
-    float f = to_f32(x[i]);
-    if (c || (w & kPrompt)) f = f > 0.f ? f / sh->rho : f * sh->rho;
-    if (c) f = f - sh->freq * (float)c - sh->pres;
-    const uint32_t slot = w >> kSlotShift;
-    if (slot) f += sh->bias_val[kAdjustMaxBias - slot];
-    x[i] = from_f32<T>(f);
   }
-  return raw;
+  return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 template <typename T, bool kAligned>
 __global__ void __launch_bounds__(kThreads) adjust_kernel(const AdjustArgs a) {
   constexpr int E = 16 / sizeof(T);  // entries of a pack
   extern __shared__ uint32_t s_dyn[];
-  uint32_t* const s_count = s_dyn;             // [seg]
-  uint32_t* const s_touch = s_dyn + a.seg;     // [seg / 32 + 1]
+  uint32_t* const s_count = s_dyn;                                           // [seg]
+  uint32_t* const s_touch = s_dyn + a.seg;                                   // [seg / 32] one bit an entry
+  uint16_t* const s_list = reinterpret_cast<uint16_t*>(s_touch + a.seg / 32);  // [seg] touched entries
   __shared__ Shared sh;
   pdl_wait();
   const int tid = threadIdx.x;
@@ -138,9 +133,8 @@ __global__ void __launch_bounds__(kThreads) adjust_kernel(const AdjustArgs a) {
     if (np < 0 || np > nh || nh > a.H) why |= kDevBadLength;
     sh.bad = why;
     sh.repeat = 0;
-    sh.D = a.D;
   }
-  for (int i = tid; i < a.seg + a.seg / 32 + 1; i += kThreads) s_dyn[i] = 0;
+  for (int i = tid; i < a.seg + a.seg / 32; i += kThreads) s_dyn[i] = 0;
   for (int i = tid; i < a.K; i += kThreads) {
     sh.bias_idx[i] = a.bias_idx[j * a.K + i];
     sh.bias_val[i] = a.bias_val[j * a.K + i];
@@ -168,12 +162,12 @@ __global__ void __launch_bounds__(kThreads) adjust_kernel(const AdjustArgs a) {
       else atomicOr(&s_count[e], kPrompt);
       mark(e);
     };
-    for (int i = tid; i < nh; i += kThreads * kFlight) {
-      int t[kFlight];
+    for (int i = tid; i < nh; i += kThreads * kScan) {
+      int t[kScan];
 #pragma unroll
-      for (int q = 0; q < kFlight; ++q) t[q] = i + q * kThreads < nh ? h[i + q * kThreads] : -1;
+      for (int q = 0; q < kScan; ++q) t[q] = i + q * kThreads < nh ? h[i + q * kThreads] : -1;
 #pragma unroll
-      for (int q = 0; q < kFlight; ++q) take(t[q], i + q * kThreads >= np);
+      for (int q = 0; q < kScan; ++q) take(t[q], i + q * kThreads >= np);
     }
     for (int i = tid; i < a.D; i += kThreads) {
       const int t = sh.draft[i];
@@ -214,66 +208,117 @@ __global__ void __launch_bounds__(kThreads) adjust_kernel(const AdjustArgs a) {
   const int bad = sh.bad;
   if (bad && tid == 0 && s0 == 0) atomicOr(a.status, bad);
 
-  // ---- the rows ----
-  const int W = (a.D + 31) / 32;
-  const int64_t aw = (a.V + 31) / 32;
-  // packs of a row; an unaligned one is cut out of one pack more
-  const uint32_t ppr = kAligned ? (len + E - 1) / E : (len + E - 1) / E + 1;
-  const uint32_t packs = ppr * a.R;
-  for (uint32_t p0 = tid; p0 < packs; p0 += kThreads * kFlight) {
-    uint4 raw[kFlight];
-    int at[kFlight], row[kFlight];  // the pack's first entry in the segment (may be negative), its row
-    uint32_t ok[kFlight];
+  // ---- the touched entries, in order ----
+  const int lane = tid & 31, warp = tid >> 5;
+  int listed = 0;
+  if (!bad) {
+    const int words = a.seg / 32;  // at most a word a thread
+    const uint32_t w = tid < words ? s_touch[tid] : 0u;
+    int n = __popc(w);
 #pragma unroll
-    for (int q = 0; q < kFlight; ++q) {
-      const uint32_t p = p0 + q * kThreads;
-      row[q] = -1;
-      if (p >= packs) continue;
-      const int r = (int)(p / ppr);
-      const T* in = static_cast<const T*>(a.logits) + (j * a.R + r) * a.ld + s0;
-      at[q] = (int)(p - r * ppr) * E - (kAligned ? 0 : (int)(((uintptr_t)in & 15) / sizeof(T)));
-      const int lo = at[q] < 0 ? -at[q] : 0, hi = at[q] + E > (int)len ? (int)len - at[q] : E;
-      if (lo >= hi) continue;
-      row[q] = r;
-      if (hi - lo == E) {
-        raw[q] = *reinterpret_cast<const uint4*>(in + at[q]);
-      } else {
-        T* x = reinterpret_cast<T*>(&raw[q]);
-#pragma unroll
-        for (int i = 0; i < E; ++i)
-          if (i >= lo && i < hi) x[i] = in[at[q] + i];
-      }
-      const int ar = sh.allow_row[r];
-      ok[q] = ((1u << (hi - lo)) - 1u) << lo;
-      if (ar >= 0) ok[q] = bits_at(a.allow + ar * a.ld_allow, s0 + at[q] + lo, hi - lo, aw) << lo;
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, n, o);
+      if (lane >= o) n += y;
     }
+    if (lane == 31) sh.listed[warp] = n;
+    __syncthreads();
+    int at = n - __popc(w);
+    for (int i = 0; i < kThreads / 32; ++i) {
+      if (i < warp) at += sh.listed[i];
+      listed += sh.listed[i];
+    }
+    for (uint32_t m = w; m; m &= m - 1) s_list[at++] = (uint16_t)(tid * 32 + __ffs(m) - 1);
+    __syncthreads();
+  }
+
+  // ---- the rows, up to one a warp at a time ----
+  const int64_t aw = (a.V + 31) / 32;
+  const T* const in0 = static_cast<const T*>(a.logits) + j * a.R * a.ld + s0;
+  T* const out0 = static_cast<T*>(a.out) + j * a.R * a.ld_out + s0;
+  const uint32_t shift = 31 - __clz(a.seg / E);  // packs of a whole segment, a power of two
+  for (int r0 = 0; r0 < a.R; r0 += kThreads / 32) {
+    const int rn = min(kThreads / 32, a.R - r0);
+    // Whole packs on 16-byte boundaries, then (unaligned rows) the entries before
+    // the first and behind the last of them.
+    for (uint32_t p0 = tid; p0 < (uint32_t)rn << shift; p0 += kThreads * kFlight) {
+      uint4 raw[kFlight];
+      uint32_t ok[kFlight];
 #pragma unroll
-    for (int q = 0; q < kFlight; ++q) {
-      if (row[q] < 0) continue;
-      const int r = row[q];
-      const int64_t n = j * a.R + r;
-      const int lo = at[q] < 0 ? -at[q] : 0, hi = at[q] + E > (int)len ? (int)len - at[q] : E;
-      T* x = reinterpret_cast<T*>(&raw[q]);
-      if (bad || sh.allow_row[r] == -2) {
-#pragma unroll
-        for (int i = 0; i < E; ++i) x[i] = of_bits<T>(Bits<T>::nan);
-      } else {
-        const uint32_t touch = ok[q] & (bits_at(s_touch, at[q] + lo, hi - lo, a.seg / 32 + 1) << lo);
-        if (touch)
-          raw[q] = touched_pack<T>(raw[q], touch, at[q], (int)s0, s_count, &sh, a.path ? a.path + n * W : nullptr,
-                                   r < a.D ? r : a.D);
-#pragma unroll
-        for (int i = 0; i < E; ++i)
-          if (!(ok[q] >> i & 1)) x[i] = of_bits<T>(Bits<T>::ninf);
+      for (int q = 0; q < kFlight; ++q) {
+        const uint32_t p = p0 + q * kThreads;
+        const int r = r0 + (int)(p >> shift);
+        ok[q] = ~0u;
+        if (r >= r0 + rn) continue;
+        const T* in = in0 + r * a.ld;
+        const int at = (int)(p & ((1u << shift) - 1u)) * E + (kAligned ? 0 : head_of(in));
+        if (at + E > (int)len) continue;
+        raw[q] = *reinterpret_cast<const uint4*>(in + at);
+        const int ar = sh.allow_row[r];
+        if (ar >= 0) ok[q] = bits_at(a.allow + ar * a.ld_allow, s0 + at, E, aw);
       }
-      T* out = static_cast<T*>(a.out) + n * a.ld_out + s0 + at[q];
-      if (hi - lo == E && (kAligned || ((uintptr_t)out & 15) == 0)) {
-        *reinterpret_cast<uint4*>(out) = raw[q];
-      } else {
 #pragma unroll
-        for (int i = 0; i < E; ++i)
-          if (i >= lo && i < hi) out[i] = x[i];
+      for (int q = 0; q < kFlight; ++q) {
+        const uint32_t p = p0 + q * kThreads;
+        const int r = r0 + (int)(p >> shift);
+        if (r >= r0 + rn) continue;
+        const int at = (int)(p & ((1u << shift) - 1u)) * E + (kAligned ? 0 : head_of(in0 + r * a.ld));
+        if (at + E > (int)len) continue;
+        if (bad || sh.allow_row[r] == -2) raw[q] = fill<T>(Bits<T>::nan);
+        else if (ok[q] != ~0u) raw[q] = allow_pack<T>(raw[q], ok[q]);
+        T* out = out0 + r * a.ld_out + at;
+        if (kAligned || ((uintptr_t)out & 15) == 0) {
+          *reinterpret_cast<uint4*>(out) = raw[q];
+        } else {
+          const T* x = reinterpret_cast<const T*>(&raw[q]);
+#pragma unroll
+          for (int i = 0; i < E; ++i) out[i] = x[i];
+        }
       }
+    }
+    if (!kAligned || len % E) {
+      for (int i = tid; i < rn * 2 * E; i += kThreads) {
+        const int r = r0 + i / (2 * E), e = i % (2 * E);
+        const T* in = in0 + r * a.ld;
+        const int head = kAligned ? 0 : min(head_of(in), (int)len);
+        const int at = e < E ? e : head + ((int)len - head) / E * E + e - E;
+        if (e < E ? e >= head : at >= (int)len) continue;
+        const int ar = sh.allow_row[r];
+        T x = in[at];
+        if (ar >= 0 && !(a.allow[ar * a.ld_allow + ((s0 + at) >> 5)] >> ((s0 + at) & 31) & 1)) x = of_bits<T>(Bits<T>::ninf);
+        if (bad || ar == -2) x = of_bits<T>(Bits<T>::nan);
+        out0[r * a.ld_out + at] = x;
+      }
+    }
+    if (!listed) continue;
+    __syncthreads();  // the rows' entries are written, the touched ones as they were
+    const int share = kThreads / 32 / rn;  // warps a row
+    const int r = r0 + warp % rn;
+    const int ar = sh.allow_row[r];
+    if (warp / rn >= share || ar == -2) continue;
+    const uint32_t* const path = a.path ? a.path + (j * a.R + r) * ((a.D + 31) / 32) : nullptr;
+    for (int i = warp / rn * 32 + lane; i < listed; i += share * 32) {
+      const int e = s_list[i];
+      if (ar >= 0 && !(a.allow[ar * a.ld_allow + ((s0 + e) >> 5)] >> ((s0 + e) & 31) & 1)) continue;
+      const uint32_t w = s_count[e];
+      uint32_t c = w & kCount;
+      if (w & kDraft) {
+        const int v = (int)s0 + e;
+        if (path) {
+          for (int k = 0; k * 32 < a.D; ++k)
+            for (uint32_t m = path[k]; m; m &= m - 1) {
+              const int d = k * 32 + __ffs(m) - 1;
+              c += d < a.D && sh.draft[d] == v;
+            }
+        } else {
+          for (int d = 0; d < min(r, a.D); ++d) c += sh.draft[d] == v;
+        }
+      }
+      float f = to_f32(in0[r * a.ld + e]);
+      if (c || (w & kPrompt)) f = f > 0.f ? f / sh.rho : f * sh.rho;
+      if (c) f = f - sh.freq * (float)c - sh.pres;
+      const uint32_t slot = w >> kSlotShift;
+      if (slot) f += sh.bias_val[kAdjustMaxBias - slot];
+      out0[r * a.ld_out + e] = from_f32<T>(f);
     }
   }
 }
@@ -297,7 +342,8 @@ cudaError_t adjust_logits(const AdjustArgs& a0, int dtype, int64_t b, cudaStream
     fn = aligned ? (const void*)adjust_kernel<__half, true> : (const void*)adjust_kernel<__half, false>;
   else
     fn = aligned ? (const void*)adjust_kernel<__nv_bfloat16, true> : (const void*)adjust_kernel<__nv_bfloat16, false>;
-  const size_t smem = (size_t)(a.seg + a.seg / 32 + 1) * 4;
+  const size_t smem = (size_t)(a.seg + a.seg / 32) * 4 + (size_t)a.seg * 2;
+  if (cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) return e;
   void* args[] = {&a};
   return launch_k(fn, dim3((unsigned)(b * a.nseg)), dim3(kThreads), smem, st, true, args);
 }
