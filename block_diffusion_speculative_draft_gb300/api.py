@@ -366,6 +366,15 @@ def _need(fn, dev, dtype, shape, **tensors):
     return out
 
 
+def _one(fn, name, t, dev, dtype, shape):
+    """_need for one tensor (None: absent)."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.get_device() != dev or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{fn}: {name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on cuda:{dev}")
+    return t.data_ptr()
+
+
 def _uniforms(fn, name, u, dev, shape):
     if u.dtype != _torch().float32 or u.get_device() != dev or u.shape != shape:
         raise ValueError(f"{fn}: {name} must be a float32 tensor of shape {tuple(shape)} on cuda:{dev}")
@@ -542,33 +551,41 @@ def dflash_adjust_logits(logits, out, hist=None, n_hist=None, n_prompt=None, dra
     if logits.dim() == 2:
         logits, out = logits.unsqueeze(1), out.unsqueeze(1) if out.dim() == 2 else out
         allow_row = allow_row.unsqueeze(1) if allow_row is not None and allow_row.dim() == 1 else allow_row
-    dt = _row_dtype(fn, logits)
+    torch = _torch()
+    i32, f32 = torch.int32, torch.float32
+    dt, shape, dev = _row_dtype(fn, logits), logits.shape, logits.get_device()
     ld = _row_shape(fn, logits, 3)
-    torch, dev, shape = _torch(), logits.get_device(), logits.shape
     b, R, V = shape
     if out.dtype != logits.dtype or out.get_device() != dev or out.shape != shape:
         raise ValueError(f"{fn}: out must have the logits' dtype, device and shape")
-    ld_out = _row_shape(fn, out, 3)
-    i32, f32 = torch.int32, torch.float32
-    hp, H, ld_h = None, 0, 0
+    ld_out = ld if out is logits else _row_shape(fn, out, 3)
+    one = shape[:1]
+    hp = nh = np_ = dr = pt = rho = fr = pr = bi = bv = ap = ar = None
+    H = ld_h = D = K = n_allow = ld_a = 0
     if hist is not None:
         if hist.dtype != i32 or hist.get_device() != dev or hist.dim() != 2 or hist.shape[0] != b:
             raise ValueError(f"{fn}: hist must be an int32 tensor [b][H] on cuda:{dev}")
         ld_h, H = _row_shape(fn, hist, 2), hist.shape[1]
         hp = hist.data_ptr()
+        nh, np_ = _one(fn, "n_hist", n_hist, dev, i32, one), _one(fn, "n_prompt", n_prompt, dev, i32, one)
     elif n_hist is not None or n_prompt is not None:
         raise ValueError(f"{fn}: n_hist and n_prompt need hist")
-    nh, np_ = _need(fn, dev, i32, (b,), n_hist=n_hist, n_prompt=n_prompt)
-    D = 0 if draft is None else draft.shape[-1]
-    if path is not None and D == 0:
-        raise ValueError(f"{fn}: path needs draft")
-    dr, = _need(fn, dev, i32, (b, D), draft=draft)
-    pt, = _need(fn, dev, i32, (b, R, (D + 31) // 32), path=path)
-    rho, fr, pr = _need(fn, dev, f32, (b,), repetition=repetition, frequency=frequency, presence=presence)
-    K = 0 if bias_idx is None else bias_idx.shape[-1]
-    bi, = _need(fn, dev, i32, (b, K), bias_idx=bias_idx)
-    bv, = _need(fn, dev, f32, (b, K), bias_val=bias_val)
-    ap, n_allow, ld_a = None, 0, 0
+    if draft is not None:
+        D = draft.shape[-1]
+        dr = _one(fn, "draft", draft, dev, i32, (b, D))
+    if path is not None:
+        if D == 0:
+            raise ValueError(f"{fn}: path needs draft")
+        pt = _one(fn, "path", path, dev, i32, (b, R, (D + 31) // 32))
+    if repetition is not None:
+        rho = _one(fn, "repetition", repetition, dev, f32, one)
+    if frequency is not None:
+        fr = _one(fn, "frequency", frequency, dev, f32, one)
+    if presence is not None:
+        pr = _one(fn, "presence", presence, dev, f32, one)
+    if bias_idx is not None or bias_val is not None:
+        K = 0 if bias_idx is None else bias_idx.shape[-1]
+        bi, bv = _one(fn, "bias_idx", bias_idx, dev, i32, (b, K)), _one(fn, "bias_val", bias_val, dev, f32, (b, K))
     if allow is not None:
         if allow.dtype != i32 or allow.get_device() != dev or allow.dim() != 2 or allow.shape[1] < (V + 31) // 32:
             raise ValueError(f"{fn}: allow must be an int32 tensor [masks][at least {(V + 31) // 32} words] on cuda:{dev}")
@@ -576,7 +593,8 @@ def dflash_adjust_logits(logits, out, hist=None, n_hist=None, n_prompt=None, dra
         if allow_row is None and n_allow < b * R:
             raise ValueError(f"{fn}: without allow_row, allow needs a mask a row")
         ap = allow.data_ptr()
-    ar, = _need(fn, dev, i32, (b, R), allow_row=allow_row)
+    if allow_row is not None:
+        ar = _one(fn, "allow_row", allow_row, dev, i32, shape[:2])
     _on(dev, stream, fn, load_library().dflash_adjust_logits, logits.data_ptr(), dt, b, R, V, ld, out.data_ptr(), ld_out,
         hp, ld_h, H, nh, np_, dr, D, pt, rho, fr, pr, bi, bv, K, ap, n_allow, ld_a, ar)
 
@@ -596,10 +614,10 @@ def dflash_tree_mask(parent, mask_out, n_nodes=None, depth_out=None, stream=None
     fn = "dflash_tree_mask"
     dev, b, N = _tree_shape(fn, parent)
     i32 = _torch().int32
-    pa, de = _need(fn, dev, i32, (b, N), parent=parent, depth_out=depth_out)
-    ma, = _need(fn, dev, i32, (b, N, (N + 31) // 32), mask_out=mask_out)
-    nn, = _need(fn, dev, i32, (b,), n_nodes=n_nodes)
-    _on(dev, stream, fn, load_library().dflash_tree_mask, pa, nn, b, N, ma, de)
+    rows = parent.shape
+    _on(dev, stream, fn, load_library().dflash_tree_mask, _one(fn, "parent", parent, dev, i32, rows),
+        _one(fn, "n_nodes", n_nodes, dev, i32, rows[:1]), b, N,
+        _one(fn, "mask_out", mask_out, dev, i32, (b, N, (N + 31) // 32)), _one(fn, "depth_out", depth_out, dev, i32, rows))
 
 
 @functools.lru_cache(maxsize=256)
@@ -617,7 +635,8 @@ def _heads(fn, name, t, dev, dtype, shape):
             (shape[-2] > 1 and t.stride(-2) != shape[-1]):
         raise ValueError(f"{fn}: {name} must be a {dtype} tensor of shape {tuple(shape)} on cuda:{dev} with a token's "
                          "heads side by side")
-    return t.data_ptr(), [0 if n == 1 else s for n, s in zip(shape[:-2], t.stride())]
+    st = t.stride()
+    return t.data_ptr(), [0 if shape[i] == 1 else st[i] for i in range(len(st) - 2)]
 
 
 def dflash_tree_attention(q, kv: "KVCache", layer: int, k_tree, v_tree, mask, out, n_nodes=None, lse_out=None,
@@ -643,10 +662,10 @@ def dflash_tree_attention(q, kv: "KVCache", layer: int, k_tree, v_tree, mask, ou
     vp, vs = _heads(fn, "v_tree", v_tree, dev, dt, (b, N, nkv, d))
     if ks != vs:
         raise ValueError(f"{fn}: k_tree and v_tree must have the same strides")
-    op, = _need(fn, dev, dt, (b, N, nq, d), out=out)
-    lp, = _need(fn, dev, torch.float32, (b, N, nq), lse_out=lse_out)
-    mp, = _need(fn, dev, torch.int32, (b, N, (N + 31) // 32), mask=mask)
-    nn, = _need(fn, dev, torch.int32, (b,), n_nodes=n_nodes)
+    op = _one(fn, "out", out, dev, dt, q.shape)
+    lp = _one(fn, "lse_out", lse_out, dev, torch.float32, q.shape[:3])
+    mp = _one(fn, "mask", mask, dev, torch.int32, (b, N, (N + 31) // 32))
+    nn = _one(fn, "n_nodes", n_nodes, dev, torch.int32, q.shape[:1])
     wp, wn, ws = _workspace(fn, ws, dflash_tree_attention_workspace_size(b, N, nq, nkv, d), dev, stream)
     _on(dev, stream, fn, load_library().dflash_tree_attention, qp, qs, qt,
         DTYPE_F16 if dt == torch.float16 else DTYPE_BF16, ctypes.byref(kv.c), layer, N, nq, nkv, d, kp, vp, *ks, mp, nn,
@@ -661,13 +680,16 @@ def dflash_tree_accept(tok, tree_tok, parent, n_out, corr_out, path_out, n_nodes
     fn = "dflash_tree_accept"
     dev, b, N = _tree_shape(fn, parent)
     i32 = _torch().int32
-    tk, tt, pa = _need(fn, dev, i32, (b, N), tok=tok, tree_tok=tree_tok, parent=parent)
-    nn, no, co, nx = _need(fn, dev, i32, (b,), n_nodes=n_nodes, n_out=n_out, corr_out=corr_out, next_tok=next_tok)
-    R = path_out.shape[-1]
-    po, em = _need(fn, dev, i32, (b, R), path_out=path_out, emitted=emitted)
-    _on(dev, stream, fn, load_library().dflash_tree_accept, tk, tt, pa, nn, b, N, R, no, co, po, em, nx)
+    rows = parent.shape
+    one, R = rows[:1], path_out.shape[-1]
+    _on(dev, stream, fn, load_library().dflash_tree_accept, _one(fn, "tok", tok, dev, i32, rows),
+        _one(fn, "tree_tok", tree_tok, dev, i32, rows), _one(fn, "parent", parent, dev, i32, rows),
+        _one(fn, "n_nodes", n_nodes, dev, i32, one), b, N, R, _one(fn, "n_out", n_out, dev, i32, one),
+        _one(fn, "corr_out", corr_out, dev, i32, one), _one(fn, "path_out", path_out, dev, i32, (b, R)),
+        _one(fn, "emitted", emitted, dev, i32, (b, R)), _one(fn, "next_tok", next_tok, dev, i32, one))
 
 
+@functools.lru_cache(maxsize=256)
 def dflash_tree_commit_workspace_size(b: int) -> int:
     n = ctypes.c_size_t(0)
     _check("dflash_tree_commit_workspace_size", load_library().dflash_tree_commit_workspace_size(b, ctypes.byref(n)))
@@ -693,16 +715,16 @@ def dflash_tree_commit(kv: "KVCache", k_tree, v_tree, path, n, hid=None, hid_out
     vp, vs = _heads(fn, "v_tree", v_tree, dev, dt, (L, b, N, nkv, d))
     if ks != vs:
         raise ValueError(f"{fn}: k_tree and v_tree must have the same strides")
-    pa, = _need(fn, dev, torch.int32, (b, R), path=path)
-    nn, lo = _need(fn, dev, torch.int32, (b,), n=n, len_out=len_out)
+    pa, nn = _one(fn, "path", path, dev, torch.int32, (b, R)), _one(fn, "n", n, dev, torch.int32, (b,))
+    lo = _one(fn, "len_out", len_out, dev, torch.int32, (b,))
     hp = ho = None
     cols = 0
     if hid is not None or hid_out is not None:
         if hid is None or hid_out is None or hid.dim() != 3 or hid.element_size() != 2:
             raise ValueError(f"{fn}: hid [b][N][cols] of a 16-bit dtype and hid_out go together")
         cols = hid.shape[2]
-        hp, = _need(fn, dev, hid.dtype, (b, N, cols), hid=hid)
-        ho, = _need(fn, dev, hid.dtype, (b, R, cols), hid_out=hid_out)
+        hp = _one(fn, "hid", hid, dev, hid.dtype, (b, N, cols))
+        ho = _one(fn, "hid_out", hid_out, dev, hid.dtype, (b, R, cols))
     wp, wn, ws = _workspace(fn, ws, dflash_tree_commit_workspace_size(b), dev, stream)
     _on(dev, stream, fn, load_library().dflash_tree_commit, ctypes.byref(kv.c), L, nkv, d, N, kp, vp, *ks, pa, nn, R, hp,
         cols, ho, lo, wp, wn)

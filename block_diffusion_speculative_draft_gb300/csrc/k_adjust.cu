@@ -343,7 +343,8 @@ cudaError_t adjust_logits(const AdjustArgs& a0, int dtype, int64_t b, cudaStream
   else
     fn = aligned ? (const void*)adjust_kernel<__nv_bfloat16, true> : (const void*)adjust_kernel<__nv_bfloat16, false>;
   const size_t smem = (size_t)(a.seg + a.seg / 32) * 4 + (size_t)a.seg * 2;
-  if (cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) return e;
+  static unsigned long long done[6];
+  if (cudaError_t e = allow_smem(fn, 8192 * 4 + 8192 / 8 + 8192 * 2, &done[dtype * 2 + aligned])) return e;
   void* args[] = {&a};
   return launch_k(fn, dim3((unsigned)(b * a.nseg)), dim3(kThreads), smem, st, true, args);
 }

@@ -16,7 +16,9 @@
 // sum, O rescaled when the maximum rises); an item that lies within one run is
 // written straight out, the parts of the others go to the workspace as fp32
 // (O, m, sum) and a second launch joins them in the order of the keys, so
-// results repeat bit for bit.
+// results repeat bit for bit.  (Joined by the last of an item's runs instead,
+// one CTA's loads in place of many: 31 us against 18 for one sequence of 8192
+// keys and 16 rows.)
 #include "kernels.h"
 #include "ptx.cuh"
 #include "rows.cuh"
@@ -71,42 +73,67 @@ struct Runs {
   }
 };
 
-// Every warp by itself, so without a barrier: the tiles of all sequences, as
-// runs for at most `ctas` CTAs; then the sequence that holds tile u and the
-// tiles before it.
-template <typename P>
-__device__ __forceinline__ Runs count_runs(const TreeAttnArgs& a, int ctas) {
-  const int lane = threadIdx.x & 31;
-  Runs r;
-  r.all = 0;
-  for (int i = lane; i < a.b; i += 32) r.all += seq_of<P>(a, i).units(a.nkv);
+// A CTA's run: the tiles [u0, u1), and the sequence that holds u0 (base tiles
+// come before it).  Every warp finds it by itself, so without a barrier; up to
+// 32 sequences are one load a lane.  False: there is nothing for this CTA.
+struct Run {
+  Runs all;
+  long long u0, u1, base;
+  int j;
+  Seq s;
+};
+__device__ __forceinline__ long long warp_scan(long long x) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) r.all += __shfl_xor_sync(0xffffffffu, r.all, o);
-  const long long most = (r.all + P::MIN_TILES - 1) / P::MIN_TILES;
-  r.runs = most < ctas ? most : ctas;
-  return r;
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, x, o);
+    if ((int)(threadIdx.x & 31) >= o) x += y;
+  }
+  return x;
 }
 template <typename P>
-__device__ __forceinline__ int find_seq(const TreeAttnArgs& a, long long u, long long& before) {
+__device__ __forceinline__ bool locate(const TreeAttnArgs& a, int cta, int ctas, Run& r) {
   const int lane = threadIdx.x & 31;
-  before = 0;
-  for (int c = 0; c < a.b; c += 32) {
-    const long long t = c + lane < a.b ? seq_of<P>(a, c + lane).units(a.nkv) : 0;
-    long long x = t;
+  auto units = [&](int i, Seq& q) {
+    if (i >= a.b) return 0ll;
+    q = seq_of<P>(a, i, a.status);  // (a length out of range is told wherever it is seen)
+    return q.units(a.nkv);
+  };
+  Seq q = {0, 0, 0, 0};
+  const long long mine = units(lane, q);
+  const long long upto = warp_scan(mine);
+  r.all.all = __shfl_sync(0xffffffffu, upto, 31);
+  if (a.b > 32) {
+    long long more = 0;
+    Seq none;
+    for (int i = 32 + lane; i < a.b; i += 32) more += units(i, none);
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long y = __shfl_up_sync(0xffffffffu, x, o);
-      if (lane >= o) x += y;
-    }
-    const unsigned in = __ballot_sync(0xffffffffu, before + x > u);  // from the sequence that holds u
-    if (in) {
-      const int l = __ffs(in) - 1;
-      before += __shfl_sync(0xffffffffu, x - t, l);
-      return c + l;
-    }
-    before += __shfl_sync(0xffffffffu, x, 31);
+    for (int o = 16; o > 0; o >>= 1) more += __shfl_xor_sync(0xffffffffu, more, o);
+    r.all.all += more;
   }
-  return -1;
+  const long long most = Runs::ratio(r.all.all + P::MIN_TILES - 1, P::MIN_TILES);
+  r.all.runs = most < ctas ? most : ctas;
+  if (cta >= r.all.runs) return false;
+  r.u0 = r.all.start(cta);
+  r.u1 = r.all.start(cta + 1);
+  unsigned in = __ballot_sync(0xffffffffu, upto > r.u0);  // from the sequence that holds u0
+  r.base = 0;
+  r.j = 0;
+  long long x = upto, t = mine;
+  while (!in) {  // (more than 32 sequences)
+    r.base += __shfl_sync(0xffffffffu, x, 31);
+    r.j += 32;
+    t = units(r.j + lane, q);
+    x = warp_scan(t);
+    in = __ballot_sync(0xffffffffu, r.base + x > r.u0);
+  }
+  const int l = __ffs(in) - 1;
+  r.base += __shfl_sync(0xffffffffu, x - t, l);
+  r.j += l;
+  r.s.len = __shfl_sync(0xffffffffu, q.len, l);
+  r.s.n = __shfl_sync(0xffffffffu, q.n, l);
+  r.s.tiles = __shfl_sync(0xffffffffu, q.tiles, l);
+  r.s.qtiles = __shfl_sync(0xffffffffu, q.qtiles, l);
+  return true;
 }
 
 // What the second launch has to join: a record a run.  An item whose parts lie
@@ -134,12 +161,17 @@ struct PartOf {
   float o[ROWS][D];
   float2 ml[ROWS];
 };
-__device__ __forceinline__ uint8_t* aligned32(void* ws) {
-  return reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(ws) + 31) & ~uintptr_t(31));
+// The workspace: the parts, then the records.
+__device__ __forceinline__ uint8_t* aligned32(void* p) {
+  return reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(p) + 31) & ~uintptr_t(31));
+}
+template <int D, int ROWS>
+__device__ __forceinline__ PartOf<D, ROWS>* parts_of(const TreeAttnArgs& a) {
+  return reinterpret_cast<PartOf<D, ROWS>*>(aligned32(a.ws));
 }
 template <int D, int ROWS>
 __device__ __forceinline__ Join* joins_of(const TreeAttnArgs& a) {
-  return reinterpret_cast<Join*>(aligned32(a.ws) + (size_t)kMaxCtas * 2 * sizeof(PartOf<D, ROWS>));
+  return reinterpret_cast<Join*>(parts_of<D, ROWS>(a) + 2 * kMaxCtas);
 }
 // CTA c's record; u0 its first tile, which is tile t0 of an item of `tiles`.
 __device__ __forceinline__ void leave_join(Join* joins, const Runs& r, int c, long long u0, int j, int item, int t0,
@@ -222,17 +254,13 @@ __global__ void __launch_bounds__(Shape<D, RW>::THREADS, Shape<D, RW>::CTAS)
   const int g = a.g;
   const Group grp(a);
   const int W = (a.N + 31) / 32;
-  const Runs runs = count_runs<S>(a, gridDim.x);
-  if (blockIdx.x == 0)
-    for (int i = tid; i < a.b; i += THREADS) seq_of<S>(a, i, a.status);  // out of range: told once
   Join* const joins = joins_of<D, ROWS>(a);
-  if (blockIdx.x >= runs.runs) {
+  Run run;
+  if (!locate<S>(a, blockIdx.x, gridDim.x, run)) {
     if (tid == 0) joins[blockIdx.x].j = -1;
     return;
   }
-  const long long u0 = runs.start(blockIdx.x), u1 = runs.start(blockIdx.x + 1);
-  long long base;
-  const int j0 = find_seq<S>(a, u0, base);
+  const long long u0 = run.u0, u1 = run.u1;
 
   // A place in the run: sequence, item of the sequence (kv head, query tile), tile.
   struct Place {
@@ -250,11 +278,11 @@ __global__ void __launch_bounds__(Shape<D, RW>::THREADS, Shape<D, RW>::CTAS)
     } while (!p.s.tiles);
   };
   Place cur;
-  cur.j = j0;
-  cur.s = seq_of<S>(a, cur.j);
-  cur.item = (int)Runs::ratio(u0 - base, cur.s.tiles);
-  cur.tile = (int)(u0 - base - (long long)cur.item * cur.s.tiles);
-  if (tid == 0) leave_join(joins, runs, blockIdx.x, u0, cur.j, cur.item, cur.tile, cur.s.tiles);
+  cur.j = run.j;
+  cur.s = run.s;
+  cur.item = (int)Runs::ratio(u0 - run.base, cur.s.tiles);
+  cur.tile = (int)(u0 - run.base - (long long)cur.item * cur.s.tiles);
+  const int item0 = cur.item, tile0 = cur.tile;
   Place pre = cur;  // the tile to copy next
 
   // K and V of a tile: cached keys, then the tree's, then zeros
@@ -486,10 +514,9 @@ __global__ void __launch_bounds__(Shape<D, RW>::THREADS, Shape<D, RW>::CTAS)
         __syncthreads();
       }
     }
+    const bool whole = t_first == 0 && t_last == tiles;
     if (kg == 0) {
-      const bool whole = t_first == 0 && t_last == tiles;
-      PartOf<D, ROWS>* part =
-          reinterpret_cast<PartOf<D, ROWS>*>(aligned32(a.ws)) + (size_t)blockIdx.x * 2 + (first ? 0 : 1);
+      PartOf<D, ROWS>* part = parts_of<D, ROWS>(a) + (size_t)blockIdx.x * 2 + (first ? 0 : 1);
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
         const int r = rw * 16 + (lane >> 2) + x * 8;
@@ -528,12 +555,13 @@ __global__ void __launch_bounds__(Shape<D, RW>::THREADS, Shape<D, RW>::CTAS)
     next(cur);
   }
   cp_async_wait<0>();
+  if (tid == 0) leave_join(joins, run.all, blockIdx.x, u0, run.j, item0, tile0, run.s.tiles);
 }
 
 // Joins the parts of an item, a record of a run: JR query rows a CTA, 8 / JR
-// warps a row that share out its parts (each the same ones every time, in the
-// order of their keys; the shares are added in order too).  Bound by the loads'
-// latency where an item has few rows, by L2 where it has many.
+// warps a row that share out its parts (each the same ones every time; the
+// shares are added in order).  Bound by the loads' latency where an item has few
+// rows, by L2 where it has many.
 constexpr int kJoinThreads = 256;
 
 template <typename T, int D, int ROWS, int JR>
@@ -551,7 +579,7 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const TreeAttnA
   const int lr = warp % JR, r = blockIdx.x * JR + lr;
   const int share = warp / JR * (32 / LANES) + lane / LANES, c = lane % LANES;
   if ((int)blockIdx.x * JR >= rows) return;
-  const PartOf<D, ROWS>* parts = reinterpret_cast<const PartOf<D, ROWS>*>(aligned32(a.ws));
+  const PartOf<D, ROWS>* parts = parts_of<D, ROWS>(a);
   const int n = x.last - x.first + 1;
   auto part = [&](int k) { return parts + 2 * (x.first + k) + (k ? 0 : x.slot); };
   float m = -INFINITY, l = 0.f;
@@ -613,7 +641,7 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const TreeAttnA
 
 template <typename T, int D, int ROWS>
 cudaError_t launch_join(TreeAttnArgs& a, int ctas, cudaStream_t st) {
-  constexpr int JR = ROWS <= 16 ? 2 : ROWS <= 64 ? 4 : 8;
+  constexpr int JR = ROWS <= 16 ? 2 : ROWS <= 32 ? 4 : 8;
   void* args[] = {&a};
   const int rows = a.N * a.g < ROWS ? a.N * a.g : ROWS;
   return launch_k((const void*)tree_join_kernel<T, D, ROWS, JR>, dim3((rows + JR - 1) / JR, ctas), dim3(kJoinThreads), 0, st,
@@ -625,7 +653,8 @@ cudaError_t launch(const TreeAttnArgs& a0, cudaStream_t st) {
   using S = Shape<D, RW>;
   TreeAttnArgs a = a0;
   const void* fn = (const void*)tree_attn_kernel<T, D, RW>;
-  cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
+  static unsigned long long done;  // devices that the kernel may use so much shared memory on
+  cudaError_t e = allow_smem(fn, S::SMEM, &done);
   if (e != cudaSuccess) return e;
   int ctas = S::CTAS * num_sms();
   if (ctas > kMaxCtas) ctas = kMaxCtas;
@@ -788,17 +817,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = a.g;
   const Group grp(a);
-  const Runs runs = count_runs<S>(a, gridDim.x);
-  if (blockIdx.x == 0)
-    for (int i = tid; i < a.b; i += kTcThreads) seq_of<S>(a, i, a.status);  // out of range: told once
   Join* const joins = joins_of<D, S::ROWS>(a);
-  if (blockIdx.x >= runs.runs) {
+  Run run;
+  if (!locate<S>(a, blockIdx.x, gridDim.x, run)) {
     if (tid == 0) joins[blockIdx.x].j = -1;
     return;
   }
-  const long long u0 = runs.start(blockIdx.x), u1 = runs.start(blockIdx.x + 1);
-  long long base;
-  const int j0 = find_seq<S>(a, u0, base);
   // The run's items, walked by every role by itself.
   struct Item {
     int j, item;   // sequence, its item
@@ -806,12 +830,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     Seq s;
     int head, row0, ctx;  // kv head, first query row, tiles of cached keys
   };
-  int left = (int)(u1 - u0);  // tiles of the run from the item on (a cache that fits the device has fewer than 2^31)
+  int left = (int)(run.u1 - run.u0);  // tiles of the run from the item on (a cache that fits the device has fewer than 2^31)
   Item it;
-  it.j = j0;
-  it.s = seq_of<S>(a, it.j);
-  it.item = (int)Runs::ratio(u0 - base, it.s.tiles);
-  it.t0 = (int)(u0 - base - (long long)it.item * it.s.tiles);
+  it.j = run.j;
+  it.s = run.s;
+  it.item = (int)Runs::ratio(run.u0 - run.base, it.s.tiles);
+  it.t0 = (int)(run.u0 - run.base - (long long)it.item * it.s.tiles);
   auto enter = [&]() {  // the rest of the item's places
     it.t1 = min(it.s.tiles, it.t0 + left);
     it.head = it.item / it.s.qtiles;
@@ -918,7 +942,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             }
           }
       } while (!dead && leave());
-      leave_join(joins, runs, blockIdx.x, u0, j, item, t0, tiles);
+      leave_join(joins, run.all, blockIdx.x, run.u0, j, item, t0, tiles);
       // nothing is in flight when the CTA ends (in order: each slot's last copy)
       if (dead)
         for (uint32_t i = x > SLOTS ? x - SLOTS : 0; i < x; ++i) mbar_wait(&sh.full[i % SLOTS], i / SLOTS & 1, nullptr);
@@ -1136,7 +1160,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       if (some) {
         const float keep = !whole ? 1.f : lt > 0.f || lt != lt ? 1.f / lt : 0.f;
         const size_t row = ((size_t)it.j * a.N + node) * a.nq + it.head * g + hh;
-        Part* part = reinterpret_cast<Part*>(aligned32(a.ws)) + (size_t)blockIdx.x * 2 + (item ? 1 : 0);
+        Part* part = parts_of<D, S::ROWS>(a) + (size_t)blockIdx.x * 2 + (item ? 1 : 0);
         constexpr int COLS = PAR ? D / 2 : D;  // of this thread
 #pragma unroll 1
         for (int c0 = PAR ? m * COLS : 0, ce = c0 + COLS; c0 < ce; c0 += 32) {
@@ -1216,7 +1240,8 @@ cudaError_t launch_tc(const TreeAttnArgs& a0, cudaStream_t st) {
   using S = TcShape<D, PAR>;
   TreeAttnArgs a = a0;
   const void* fn = (const void*)tree_attn_tc_kernel<T, D, PAR>;
-  cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
+  static unsigned long long done;
+  cudaError_t e = allow_smem(fn, S::SMEM, &done);
   if (e != cudaSuccess) return e;
   const CUtensorMapDataType dt = __is_same(T, __half) ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   CUtensorMap maps[4];
@@ -1245,7 +1270,10 @@ cudaError_t launch_tc(const TreeAttnArgs& a0, cudaStream_t st) {
 }
 
 // Query tiles of more than kWarpRows rows go to the tensor cores' own memory.
-constexpr int kWarpRows = 64;
+// (Device time, us, warp-level / tensor-memory form: 8 sequences of 4096 keys,
+// 64 rows 61 / 45, 32 rows 48 / 43, 16 rows 37 / 41, 4 rows 32 / 40; one of 8192,
+// 64 rows 24 / 25, 32 rows 19 / 24; 64 of 500, 64 rows 85 / 64.)
+constexpr int kWarpRows = 32;
 
 // The tensor maps want the tree's strides to grow: what a cut out of larger
 // tensors has, but not every order of dimensions.
@@ -1258,7 +1286,7 @@ template <typename T, int D>
 cudaError_t launch_rows(const TreeAttnArgs& a, cudaStream_t st) {
   const int rows = a.N * a.g;
   if (rows > kWarpRows && maps_fit(a)) return rows <= 128 ? launch_tc<T, D, true>(a, st) : launch_tc<T, D, false>(a, st);
-  return rows <= 16 ? launch<T, D, 1>(a, st) : rows <= 32 ? launch<T, D, 2>(a, st) : launch<T, D, 4>(a, st);
+  return rows <= 16 ? launch<T, D, 1>(a, st) : launch<T, D, 2>(a, st);
 }
 
 template <typename T>
@@ -1271,7 +1299,7 @@ cudaError_t launch_type(const TreeAttnArgs& a, cudaStream_t st) {
 size_t tree_attn_ws_bytes(int64_t b, int N, int nq, int nkv, int d) {
   (void)b;
   const int rows = N * (nq / nkv);
-  const int tile = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : rows <= 128 ? 128 : 256;
+  const int tile = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 128 ? 128 : 256;
   return (size_t)kMaxCtas * (2 * (size_t)tile * (d + 2) * 4 + sizeof(Join)) + 32;
 }
 

@@ -106,6 +106,10 @@ bool encode_tmap_3d(CUtensorMap* map, CUtensorMapDataType dt, const void* base, 
 bool encode_tmap(CUtensorMap* map, CUtensorMapDataType dt, const void* base, int rank, const uint64_t* dims,
                  const uint64_t* strides, const uint32_t* box, CUtensorMapSwizzle swz);
 
+// Lets a kernel use so much dynamic shared memory, once a device: `done` has a
+// bit for each where that has been asked for.
+cudaError_t allow_smem(const void* fn, int bytes, unsigned long long* done);
+
 // Launch helpers: the programmatic-dependent-launch attribute is set when
 // `pdl` is requested and the library's launch mode allows early launches
 // (launch_early()); launch_kc also groups blocks into thread-block clusters
