@@ -12,8 +12,8 @@
 // drafts or the biases touch.  A few rows at a time then stream by as they are,
 // but for the grammar's bits, and a warp a row goes through the list and writes
 // the touched entries over.  (With the touched entries worked on where they came
-// by, nearly every warp had one, and a batch of 1024 rows took 4.6 times the
-// bytes' time.)  A row's path adds to few entries: they are marked in the
+// by, nearly every warp had one, and 32 x 32 rows of 151936 bf16 took 426 us in
+// place of 144; rows that nothing touches stream at 6.3 TB/s.)  A row's path adds to few entries: they are marked in the
 // counters, and the path is walked for those.
 #include "kernels.h"
 #include "rows.cuh"
@@ -23,8 +23,10 @@ namespace dfl {
 namespace {
 
 constexpr int kDevBadLength = 0x4, kDevBadParam = 0x8;
-constexpr int kThreads = 256;
-constexpr int kFlight = 4;  // packs a thread has in flight
+// 512 threads and 64 registers, two CTAs an SM: 144 us for 32 x 32 rows of 151936 bf16
+// with everything asked for and 31 us for 8 x 16 of fp32 (256 threads: 164 and 32).
+constexpr int kThreads = 512;
+constexpr int kFlight = 4;  // packs a thread has in flight (twice as many without a grammar)
 constexpr int kScan = 8;    // tokens of the history
 
 // A counter: generated tokens (bits 0-19), in the prompt, among the drafts,
@@ -59,12 +61,13 @@ __device__ __forceinline__ T of_bits(uint32_t b) {
 }
 
 // n <= 16 bits of a bit row from bit `at`, ones above them; words past `words`
-// are not read.
+// are not read.  kIn: they lie in one word.
+template <bool kIn>
 __device__ __forceinline__ uint32_t bits_at(const uint32_t* w, int64_t at, int n, int64_t words) {
   const int64_t i = at >> 5;
   const int s = (int)(at & 31);
   uint32_t v = w[i] >> s;
-  if (s + n > 32 && i + 1 < words) v |= w[i + 1] << (32 - s);
+  if (!kIn && s + n > 32 && i + 1 < words) v |= w[i + 1] << (32 - s);
   return v | ~((1u << n) - 1u);
 }
 
@@ -105,9 +108,11 @@ __device__ __forceinline__ uint4 allow_pack(uint4 raw, uint32_t ok) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-template <typename T, bool kAligned>
-__global__ void __launch_bounds__(kThreads) adjust_kernel(const AdjustArgs a) {
+// kMasked: rows may have a grammar.
+template <typename T, bool kAligned, bool kMasked>
+__global__ void __launch_bounds__(kThreads, 2) adjust_kernel(const AdjustArgs a) {
   constexpr int E = 16 / sizeof(T);  // entries of a pack
+  constexpr int FL = kMasked ? kFlight : 2 * kFlight;
   extern __shared__ uint32_t s_dyn[];
   uint32_t* const s_count = s_dyn;                                           // [seg]
   uint32_t* const s_touch = s_dyn + a.seg;                                   // [seg / 32] one bit an entry
@@ -212,7 +217,7 @@ __global__ void __launch_bounds__(kThreads) adjust_kernel(const AdjustArgs a) {
   const int lane = tid & 31, warp = tid >> 5;
   int listed = 0;
   if (!bad) {
-    const int words = a.seg / 32;  // at most a word a thread
+    const int words = a.seg / 32;
     const uint32_t w = tid < words ? s_touch[tid] : 0u;
     int n = __popc(w);
 #pragma unroll
@@ -240,31 +245,32 @@ __global__ void __launch_bounds__(kThreads) adjust_kernel(const AdjustArgs a) {
     const int rn = min(kThreads / 32, a.R - r0);
     // Whole packs on 16-byte boundaries, then (unaligned rows) the entries before
     // the first and behind the last of them.
-    for (uint32_t p0 = tid; p0 < (uint32_t)rn << shift; p0 += kThreads * kFlight) {
-      uint4 raw[kFlight];
-      uint32_t ok[kFlight];
+    for (uint32_t p0 = tid; p0 < (uint32_t)rn << shift; p0 += kThreads * FL) {
+      uint4 raw[FL];
+      uint32_t ok[FL];
 #pragma unroll
-      for (int q = 0; q < kFlight; ++q) {
+      for (int q = 0; q < FL; ++q) {
         const uint32_t p = p0 + q * kThreads;
         const int r = r0 + (int)(p >> shift);
-        ok[q] = ~0u;
         if (r >= r0 + rn) continue;
         const T* in = in0 + r * a.ld;
         const int at = (int)(p & ((1u << shift) - 1u)) * E + (kAligned ? 0 : head_of(in));
         if (at + E > (int)len) continue;
         raw[q] = *reinterpret_cast<const uint4*>(in + at);
+        if (!kMasked) continue;
+        ok[q] = ~0u;
         const int ar = sh.allow_row[r];
-        if (ar >= 0) ok[q] = bits_at(a.allow + ar * a.ld_allow, s0 + at, E, aw);
+        if (ar >= 0) ok[q] = bits_at<kAligned>(a.allow + ar * a.ld_allow, s0 + at, E, aw);
       }
 #pragma unroll
-      for (int q = 0; q < kFlight; ++q) {
+      for (int q = 0; q < FL; ++q) {
         const uint32_t p = p0 + q * kThreads;
         const int r = r0 + (int)(p >> shift);
         if (r >= r0 + rn) continue;
         const int at = (int)(p & ((1u << shift) - 1u)) * E + (kAligned ? 0 : head_of(in0 + r * a.ld));
         if (at + E > (int)len) continue;
-        if (bad || sh.allow_row[r] == -2) raw[q] = fill<T>(Bits<T>::nan);
-        else if (ok[q] != ~0u) raw[q] = allow_pack<T>(raw[q], ok[q]);
+        if (bad || (kMasked && sh.allow_row[r] == -2)) raw[q] = fill<T>(Bits<T>::nan);
+        else if (kMasked && ok[q] != ~0u) raw[q] = allow_pack<T>(raw[q], ok[q]);
         T* out = out0 + r * a.ld_out + at;
         if (kAligned || ((uintptr_t)out & 15) == 0) {
           *reinterpret_cast<uint4*>(out) = raw[q];
@@ -296,31 +302,52 @@ __global__ void __launch_bounds__(kThreads) adjust_kernel(const AdjustArgs a) {
     const int ar = sh.allow_row[r];
     if (warp / rn >= share || ar == -2) continue;
     const uint32_t* const path = a.path ? a.path + (j * a.R + r) * ((a.D + 31) / 32) : nullptr;
-    for (int i = warp / rn * 32 + lane; i < listed; i += share * 32) {
-      const int e = s_list[i];
-      if (ar >= 0 && !(a.allow[ar * a.ld_allow + ((s0 + e) >> 5)] >> ((s0 + e) & 31) & 1)) continue;
-      const uint32_t w = s_count[e];
-      uint32_t c = w & kCount;
-      if (w & kDraft) {
-        const int v = (int)s0 + e;
-        if (path) {
-          for (int k = 0; k * 32 < a.D; ++k)
-            for (uint32_t m = path[k]; m; m &= m - 1) {
-              const int d = k * 32 + __ffs(m) - 1;
-              c += d < a.D && sh.draft[d] == v;
-            }
-        } else {
-          for (int d = 0; d < min(r, a.D); ++d) c += sh.draft[d] == v;
+    for (int i0 = warp / rn * 32 + lane; i0 < listed; i0 += share * 32 * kFlight) {
+      T z[kFlight];
+      int entry[kFlight];  // -1: none, or not allowed
+#pragma unroll
+      for (int q = 0; q < kFlight; ++q) {
+        const int i = i0 + q * share * 32;
+        entry[q] = i < listed ? s_list[i] : -1;
+        if (entry[q] >= 0 && ar >= 0) {
+          const int64_t v = s0 + entry[q];
+          if (!(a.allow[ar * a.ld_allow + (v >> 5)] >> (v & 31) & 1)) entry[q] = -1;
         }
+        if (entry[q] >= 0) z[q] = in0[r * a.ld + entry[q]];
       }
-      float f = to_f32(in0[r * a.ld + e]);
-      if (c || (w & kPrompt)) f = f > 0.f ? f / sh.rho : f * sh.rho;
-      if (c) f = f - sh.freq * (float)c - sh.pres;
-      const uint32_t slot = w >> kSlotShift;
-      if (slot) f += sh.bias_val[kAdjustMaxBias - slot];
-      out0[r * a.ld_out + e] = from_f32<T>(f);
+#pragma unroll
+      for (int q = 0; q < kFlight; ++q) {
+        const int e = entry[q];
+        if (e < 0) continue;
+        const uint32_t w = s_count[e];
+        uint32_t c = w & kCount;
+        if (w & kDraft) {
+          const int v = (int)s0 + e;
+          if (path) {
+            for (int k = 0; k * 32 < a.D; ++k)
+              for (uint32_t m = path[k]; m; m &= m - 1) {
+                const int d = k * 32 + __ffs(m) - 1;
+                c += d < a.D && sh.draft[d] == v;
+              }
+          } else {
+            for (int d = 0; d < min(r, a.D); ++d) c += sh.draft[d] == v;
+          }
+        }
+        float f = to_f32(z[q]);
+        if (c || (w & kPrompt)) f = f > 0.f ? f / sh.rho : f * sh.rho;
+        if (c) f = f - sh.freq * (float)c - sh.pres;
+        const uint32_t slot = w >> kSlotShift;
+        if (slot) f += sh.bias_val[kAdjustMaxBias - slot];
+        out0[r * a.ld_out + e] = from_f32<T>(f);
+      }
     }
   }
+}
+
+template <typename T>
+const void* pick(bool aligned, bool masked) {
+  if (aligned) return masked ? (const void*)adjust_kernel<T, true, true> : (const void*)adjust_kernel<T, true, false>;
+  return masked ? (const void*)adjust_kernel<T, false, true> : (const void*)adjust_kernel<T, false, false>;
 }
 
 }  // namespace
@@ -336,15 +363,12 @@ cudaError_t adjust_logits(const AdjustArgs& a0, int dtype, int64_t b, cudaStream
   if (b * (int64_t)a.nseg > 0x7fffffffll) return cudaErrorInvalidValue;
   const bool aligned = ((uintptr_t)a.logits & 15) == 0 && ((uintptr_t)a.out & 15) == 0 && a.ld * es % 16 == 0 &&
                        a.ld_out * es % 16 == 0;
-  const void* fn;
-  if (dtype == 0) fn = aligned ? (const void*)adjust_kernel<float, true> : (const void*)adjust_kernel<float, false>;
-  else if (dtype == 1)
-    fn = aligned ? (const void*)adjust_kernel<__half, true> : (const void*)adjust_kernel<__half, false>;
-  else
-    fn = aligned ? (const void*)adjust_kernel<__nv_bfloat16, true> : (const void*)adjust_kernel<__nv_bfloat16, false>;
+  const void* fn = dtype == 0   ? pick<float>(aligned, a.allow)
+                   : dtype == 1 ? pick<__half>(aligned, a.allow)
+                                : pick<__nv_bfloat16>(aligned, a.allow);
   const size_t smem = (size_t)(a.seg + a.seg / 32) * 4 + (size_t)a.seg * 2;
-  static unsigned long long done[6];
-  if (cudaError_t e = allow_smem(fn, 8192 * 4 + 8192 / 8 + 8192 * 2, &done[dtype * 2 + aligned])) return e;
+  static unsigned long long done[12];
+  if (cudaError_t e = allow_smem(fn, 8192 * 4 + 8192 / 8 + 8192 * 2, &done[dtype * 4 + aligned * 2 + (a.allow != nullptr)])) return e;
   void* args[] = {&a};
   return launch_k(fn, dim3((unsigned)(b * a.nseg)), dim3(kThreads), smem, st, true, args);
 }

@@ -142,7 +142,8 @@ struct Join {
   int j, item;      // sequence, item of the sequence; j < 0: nothing
   int first, last;  // runs
   int slot;         // of the part in the first run; 0 in the others
-  int pad[3];
+  int n;            // nodes of the sequence
+  int pad[2];
 };
 
 // Node and place in the group of a query row: x / g by a product with 2^32 / g
@@ -175,8 +176,10 @@ __device__ __forceinline__ Join* joins_of(const TreeAttnArgs& a) {
 }
 // CTA c's record; u0 its first tile, which is tile t0 of an item of `tiles`.
 __device__ __forceinline__ void leave_join(Join* joins, const Runs& r, int c, long long u0, int j, int item, int t0,
-                                           int tiles) {
+                                           const Seq& s) {
+  const int tiles = s.tiles;
   Join x;
+  x.n = s.n;
   x.j = -1;
   const long long ub = u0 - t0;
   if (t0 > 0 && r.of(ub) == c - 1) {
@@ -555,97 +558,119 @@ __global__ void __launch_bounds__(Shape<D, RW>::THREADS, Shape<D, RW>::CTAS)
     next(cur);
   }
   cp_async_wait<0>();
-  if (tid == 0) leave_join(joins, run.all, blockIdx.x, u0, run.j, item0, tile0, run.s.tiles);
+  if (tid == 0) leave_join(joins, run.all, blockIdx.x, u0, run.j, item0, tile0, run.s);
 }
 
-// Joins the parts of an item, a record of a run: JR query rows a CTA, 8 / JR
-// warps a row that share out its parts (each the same ones every time; the
-// shares are added in order).  Bound by the loads' latency where an item has few
-// rows, by L2 where it has many.
+// Joins the parts of the items that have several: JR query rows a CTA and turn,
+// 8 / JR warps a row that share out its parts (each the same ones every time; the
+// shares are added in order).  Every CTA lists the records that ask for it, so
+// that none is started for nothing.  Bound by the loads' latency where an item
+// has few rows, by L2 where it has many.
 constexpr int kJoinThreads = 256;
 
 template <typename T, int D, int ROWS, int JR>
-__global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const TreeAttnArgs a) {
+__global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const TreeAttnArgs a, int ctas, int chunks) {
   constexpr int LANES = D / 4;                  // of a row: four columns each
   constexpr int SHARES = 8 / JR * (32 / LANES);  // of a row's parts
   __shared__ float4 s_o[JR][SHARES][LANES];
+  __shared__ int s_count[kJoinThreads / 32], s_run[kMaxCtas];
   pdl_wait();
-  const Join x = joins_of<D, ROWS>(a)[blockIdx.y];
-  if (x.j < 0) return;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = a.g;
-  const int len_n = a.n_nodes ? a.n_nodes[x.j] : a.N;  // (in range: the sequence has work)
-  const int qtiles = (len_n * g + ROWS - 1) / ROWS;
-  const int row0 = (x.item % qtiles) * ROWS, rows = min(ROWS, len_n * g - row0);
-  const int lr = warp % JR, r = blockIdx.x * JR + lr;
-  const int share = warp / JR * (32 / LANES) + lane / LANES, c = lane % LANES;
-  if ((int)blockIdx.x * JR >= rows) return;
-  const PartOf<D, ROWS>* parts = parts_of<D, ROWS>(a);
-  const int n = x.last - x.first + 1;
-  auto part = [&](int k) { return parts + 2 * (x.first + k) + (k ? 0 : x.slot); };
-  float m = -INFINITY, l = 0.f;
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (r < rows) {
-    for (int k = lane; k < n; k += 32) m = fmaxf(m, part(k)->ml[r].x);
+  const Join* const joins = joins_of<D, ROWS>(a);
+  int items = 0;
+  for (int c0 = 0; c0 < ctas; c0 += kJoinThreads) {
+    const int c = c0 + threadIdx.x;
+    const bool some = c < ctas && joins[c].j >= 0;
+    const unsigned in = __ballot_sync(0xffffffffu, some);
+    if (lane == 0) s_count[warp] = __popc(in);
+    __syncthreads();
+    int at = items + __popc(in & ((1u << lane) - 1u));
+    for (int w = 0; w < kJoinThreads / 32; ++w) {
+      if (w < warp) at += s_count[w];
+      items += s_count[w];
+    }
+    if (some) s_run[at] = c;
+    __syncthreads();
+  }
+  for (int work = blockIdx.x; work < items * chunks; work += gridDim.x) {
+    const Join x = joins[s_run[work / chunks]];
+    const int qtiles = (x.n * g + ROWS - 1) / ROWS;
+    const int row0 = (x.item % qtiles) * ROWS, rows = min(ROWS, x.n * g - row0);
+    const int lr = warp % JR, chunk = work % chunks, r = chunk * JR + lr;
+    const int share = warp / JR * (32 / LANES) + lane / LANES, c = lane % LANES;
+    if (chunk * JR >= rows) continue;
+    const PartOf<D, ROWS>* parts = parts_of<D, ROWS>(a);
+    const int n = x.last - x.first + 1;
+    auto part = [&](int k) { return parts + 2 * (x.first + k) + (k ? 0 : x.slot); };
+    float m = -INFINITY, l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (r < rows) {
+      for (int k = lane; k < n; k += 32) m = fmaxf(m, part(k)->ml[r].x);
 #pragma unroll
-    for (int q = 16; q > 0; q >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, q));
-    const float ref = m == -INFINITY ? 0.f : m;
-    for (int k0 = 0; k0 < n; k0 += 32) {
-      const float2 ml = k0 + lane < n ? part(k0 + lane)->ml[r] : make_float2(-INFINITY, 0.f);
-      const float w = fast_exp2(ml.x - ref);
-      l += ml.y * w;
-      const int ke = min(32, n - k0);
-      for (int k = share; k - share < ke; k += 8 * SHARES) {
-        float4 v[8];
-        float wk[8];
+      for (int q = 16; q > 0; q >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, q));
+      const float ref = m == -INFINITY ? 0.f : m;
+      for (int k0 = 0; k0 < n; k0 += 32) {
+        const float2 ml = k0 + lane < n ? part(k0 + lane)->ml[r] : make_float2(-INFINITY, 0.f);
+        const float w = fast_exp2(ml.x - ref);
+        l += ml.y * w;
+        const int ke = min(32, n - k0);
+        for (int k = share; k - share < ke; k += 8 * SHARES) {
+          float4 v[8];
+          float wk[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int q = k + i * SHARES;
-          wk[i] = __shfl_sync(0xffffffffu, w, q & 31);
-          v[i] = q < ke ? *reinterpret_cast<const float4*>(&part(k0 + q)->o[r][4 * c]) : make_float4(0.f, 0.f, 0.f, 0.f);
-        }
+          for (int i = 0; i < 8; ++i) {
+            const int q = k + i * SHARES;
+            wk[i] = __shfl_sync(0xffffffffu, w, q & 31);
+            v[i] = q < ke ? *reinterpret_cast<const float4*>(&part(k0 + q)->o[r][4 * c]) : make_float4(0.f, 0.f, 0.f, 0.f);
+          }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          if (k + i * SHARES >= ke) continue;
-          o.x += v[i].x * wk[i];
-          o.y += v[i].y * wk[i];
-          o.z += v[i].z * wk[i];
-          o.w += v[i].w * wk[i];
+          for (int i = 0; i < 8; ++i) {
+            if (k + i * SHARES >= ke) continue;
+            o.x += v[i].x * wk[i];
+            o.y += v[i].y * wk[i];
+            o.z += v[i].z * wk[i];
+            o.w += v[i].w * wk[i];
+          }
         }
       }
-    }
 #pragma unroll
-    for (int q = 16; q > 0; q >>= 1) l += __shfl_xor_sync(0xffffffffu, l, q);
-  }
-  if (SHARES > 1) {
-    s_o[lr][share][c] = o;
-    __syncthreads();
-    if (share) return;
-#pragma unroll
-    for (int k = 1; k < SHARES; ++k) {
-      const float4 v = s_o[lr][k][c];
-      o.x += v.x;
-      o.y += v.y;
-      o.z += v.z;
-      o.w += v.w;
+      for (int q = 16; q > 0; q >>= 1) l += __shfl_xor_sync(0xffffffffu, l, q);
     }
+    if (SHARES > 1) {
+      __syncthreads();  // (the last turn's are read)
+      s_o[lr][share][c] = o;
+      __syncthreads();
+      if (share) continue;
+#pragma unroll
+      for (int k = 1; k < SHARES; ++k) {
+        const float4 v = s_o[lr][k][c];
+        o.x += v.x;
+        o.y += v.y;
+        o.z += v.z;
+        o.w += v.w;
+      }
+    }
+    if (r >= rows) continue;
+    const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+    const Group grp(a);
+    const int node = grp.node(row0 + r), head = x.item / qtiles * g + grp.place(row0 + r, node);
+    const size_t row = ((size_t)x.j * a.N + node) * a.nq + head;
+    *reinterpret_cast<uint2*>(a.out + row * D + 4 * c) =
+        make_uint2(pack2<T>(o.x * inv, o.y * inv), pack2<T>(o.z * inv, o.w * inv));
+    if (a.lse && c == 0) a.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * (1.f / kLog2e);
   }
-  if (r >= rows) return;
-  const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
-  const Group grp(a);
-  const int node = grp.node(row0 + r), head = x.item / qtiles * g + grp.place(row0 + r, node);
-  const size_t row = ((size_t)x.j * a.N + node) * a.nq + head;
-  *reinterpret_cast<uint2*>(a.out + row * D + 4 * c) =
-      make_uint2(pack2<T>(o.x * inv, o.y * inv), pack2<T>(o.z * inv, o.w * inv));
-  if (a.lse && c == 0) a.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * (1.f / kLog2e);
 }
 
 template <typename T, int D, int ROWS>
 cudaError_t launch_join(TreeAttnArgs& a, int ctas, cudaStream_t st) {
   constexpr int JR = ROWS <= 16 ? 2 : ROWS <= 32 ? 4 : 8;
-  void* args[] = {&a};
   const int rows = a.N * a.g < ROWS ? a.N * a.g : ROWS;
-  return launch_k((const void*)tree_join_kernel<T, D, ROWS, JR>, dim3((rows + JR - 1) / JR, ctas), dim3(kJoinThreads), 0, st,
-                  true, args);
+  int chunks = (rows + JR - 1) / JR;
+  int64_t grid = (int64_t)(ctas - 1) * chunks;  // an item has its second run's record: at most so many
+  if (grid < 1) return cudaSuccess;             // one run: nothing is split
+  if (grid > 4 * num_sms()) grid = 4 * num_sms();
+  void* args[] = {&a, &ctas, &chunks};
+  return launch_k((const void*)tree_join_kernel<T, D, ROWS, JR>, dim3((unsigned)grid), dim3(kJoinThreads), 0, st, true, args);
 }
 
 template <typename T, int D, int RW>
@@ -921,7 +946,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   if (warp == kTcCopy) {
     if (lane == 0) {
       uint32_t x = 0;  // K and V tiles so far
-      const int j = it.j, item = it.item, t0 = it.t0, tiles = it.s.tiles;  // (the first item's)
+      const int j = it.j, item = it.item, t0 = it.t0;  // (the first item's)
       fence_proxy_async_global();  // the inputs were written by generic stores
       do {
         for (int t = it.t0; t < it.t1; ++t)
@@ -942,7 +967,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             }
           }
       } while (!dead && leave());
-      leave_join(joins, run.all, blockIdx.x, run.u0, j, item, t0, tiles);
+      leave_join(joins, run.all, blockIdx.x, run.u0, j, item, t0, run.s);
       // nothing is in flight when the CTA ends (in order: each slot's last copy)
       if (dead)
         for (uint32_t i = x > SLOTS ? x - SLOTS : 0; i < x; ++i) mbar_wait(&sh.full[i % SLOTS], i / SLOTS & 1, nullptr);
