@@ -666,6 +666,7 @@ int32_t dflash_adjust_logits(const void* logits, int32_t dtype, int64_t b, int32
   if (bias_idx && K > kAdjustMaxBias) return DFLASH_EUNSUPPORTED;
   if (allow ? n_allow < 1 || ld_allow < (V + 31) / 32 : allow_row != nullptr) return DFLASH_EINVAL;
   if (allow && ld_allow > ((int64_t)1 << 60) / n_allow) return DFLASH_EUNSUPPORTED;
+  if (b * ((V + 8191) / 8192) > 0x7fffffffll) return DFLASH_EUNSUPPORTED;  // CTAs: a segment of 8192 entries each
   AdjustArgs a;
   memset(&a, 0, sizeof(a));
   a.logits = logits;

@@ -9,8 +9,8 @@
 // row against 4 bytes a key and dimension, and HBM is the bound up to about
 // 280 rows.
 //
-// Work is shared out by keys, not by sequences: the 64-key tiles of all
-// (sequence, kv head, query tile) items, in that order, are cut into as many
+// Work is shared out by keys, not by sequences: the key tiles (64 or 128 keys) of
+// all (sequence, kv head, query tile) items, in that order, are cut into as many
 // equal runs as CTAs are resident, whatever the lengths (which only the device
 // knows).  A CTA walks its run with the online softmax (running maximum and
 // sum, O rescaled when the maximum rises); an item that lies within one run is
@@ -156,11 +156,15 @@ struct Group {
 };
 
 // A part in the workspace: O of rows x D fp32, then (m, sum) of each row, m in
-// log2 units.  A run has two: of its first item, and of its last.
+// log2 units.  A run has two: of its first item, and of its last.  O lies by
+// rows, or (the tensor-memory form, a thread a row) in columns of four, so that
+// a warp's 16-byte stores lie side by side either way.
 template <int D, int ROWS>
 struct PartOf {
-  float o[ROWS][D];
+  float o[ROWS * D];
   float2 ml[ROWS];
+  __device__ __forceinline__ static int by_row(int r, int c) { return r * D + c; }
+  __device__ __forceinline__ static int by_four(int r, int c) { return (c / 4 * ROWS + r) * 4; }
 };
 // The workspace: the parts, then the records.
 __device__ __forceinline__ uint8_t* aligned32(void* p) {
@@ -222,9 +226,11 @@ __device__ __forceinline__ bool not_finite(uint32_t pair) {
 }
 
 // ---------------------------------------------------------------------------
-// RW row warps of 16 query rows, KW groups of warps that share out a tile's
-// keys.  Each warp keeps its own running maximum, sum and O over its keys; the
-// groups are joined when the item or the run ends.
+// The warp-level form, for few rows a key: RW row warps of 16 query rows, KW
+// groups of warps that share out a tile's keys.  Each warp keeps its own running
+// maximum, sum and O over its keys; the groups are joined when the item or the
+// run ends.  Bound by HBM: 64 sequences of 2000 keys with one token each run at
+// 5.7 TB/s; small calls by their two launches (12 us at 1024 keys).
 template <int D, int RW>
 struct Shape {
   static constexpr int KW = RW == 1 ? 4 : 8 / RW;
@@ -548,7 +554,8 @@ __global__ void __launch_bounds__(Shape<D, RW>::THREADS, Shape<D, RW>::CTAS)
         } else {
 #pragma unroll
           for (int i = 0; i < D / 8; ++i)
-            *reinterpret_cast<float2*>(&part->o[r][i * 8 + (lane & 3) * 2]) = make_float2(o[i][2 * x], o[i][2 * x + 1]);
+            *reinterpret_cast<float2*>(&part->o[part->by_row(r, i * 8 + (lane & 3) * 2)]) =
+                make_float2(o[i][2 * x], o[i][2 * x + 1]);
           if ((lane & 3) == 0) part->ml[r] = make_float2(mt[x], lt[x]);
         }
       }
@@ -561,22 +568,15 @@ __global__ void __launch_bounds__(Shape<D, RW>::THREADS, Shape<D, RW>::CTAS)
   if (tid == 0) leave_join(joins, run.all, blockIdx.x, u0, run.j, item0, tile0, run.s);
 }
 
-// Joins the parts of the items that have several: JR query rows a CTA and turn,
-// 8 / JR warps a row that share out its parts (each the same ones every time; the
-// shares are added in order).  Every CTA lists the records that ask for it, so
-// that none is started for nothing.  Bound by the loads' latency where an item
-// has few rows, by L2 where it has many.
+// Joins the parts of the items that have several.  Every CTA lists the records
+// that ask for it, so that none is started for nothing, and takes (item, chunk)
+// pairs in turn.  Bound by the loads' latency where an item has few rows, by L2
+// where it has many.
 constexpr int kJoinThreads = 256;
 
-template <typename T, int D, int ROWS, int JR>
-__global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const TreeAttnArgs a, int ctas, int chunks) {
-  constexpr int LANES = D / 4;                  // of a row: four columns each
-  constexpr int SHARES = 8 / JR * (32 / LANES);  // of a row's parts
-  __shared__ float4 s_o[JR][SHARES][LANES];
-  __shared__ int s_count[kJoinThreads / 32], s_run[kMaxCtas];
-  pdl_wait();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = a.g;
-  const Join* const joins = joins_of<D, ROWS>(a);
+// The runs with a record, in s_run; their number.
+__device__ __forceinline__ int list_joins(const Join* joins, int ctas, int* s_run, int* s_count) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int items = 0;
   for (int c0 = 0; c0 < ctas; c0 += kJoinThreads) {
     const int c = c0 + threadIdx.x;
@@ -592,6 +592,21 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const TreeAttnA
     if (some) s_run[at] = c;
     __syncthreads();
   }
+  return items;
+}
+
+// Parts by rows: JR query rows a chunk, 8 / JR warps a row that share out its
+// parts (each the same ones every time; the shares are added in order).
+template <typename T, int D, int ROWS, int JR>
+__global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const TreeAttnArgs a, int ctas, int chunks) {
+  constexpr int LANES = D / 4;                  // of a row: four columns each
+  constexpr int SHARES = 8 / JR * (32 / LANES);  // of a row's parts
+  __shared__ float4 s_o[JR][SHARES][LANES];
+  __shared__ int s_count[kJoinThreads / 32], s_run[kMaxCtas];
+  pdl_wait();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = a.g;
+  const Join* const joins = joins_of<D, ROWS>(a);
+  const int items = list_joins(joins, ctas, s_run, s_count);
   for (int work = blockIdx.x; work < items * chunks; work += gridDim.x) {
     const Join x = joins[s_run[work / chunks]];
     const int qtiles = (x.n * g + ROWS - 1) / ROWS;
@@ -621,7 +636,7 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const TreeAttnA
           for (int i = 0; i < 8; ++i) {
             const int q = k + i * SHARES;
             wk[i] = __shfl_sync(0xffffffffu, w, q & 31);
-            v[i] = q < ke ? *reinterpret_cast<const float4*>(&part(k0 + q)->o[r][4 * c]) : make_float4(0.f, 0.f, 0.f, 0.f);
+            v[i] = q < ke ? *reinterpret_cast<const float4*>(&part(k0 + q)->o[PartOf<D, ROWS>::by_row(r, 4 * c)]) : make_float4(0.f, 0.f, 0.f, 0.f);
           }
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
@@ -661,16 +676,71 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const TreeAttnA
   }
 }
 
+// Parts by columns of four: 32 rows and 32 columns a chunk, a lane a row and a
+// warp four columns.
 template <typename T, int D, int ROWS>
-cudaError_t launch_join(TreeAttnArgs& a, int ctas, cudaStream_t st) {
-  constexpr int JR = ROWS <= 16 ? 2 : ROWS <= 32 ? 4 : 8;
-  const int rows = a.N * a.g < ROWS ? a.N * a.g : ROWS;
-  int chunks = (rows + JR - 1) / JR;
+__global__ void __launch_bounds__(kJoinThreads) tree_join_cols_kernel(const TreeAttnArgs a, int ctas, int chunks) {
+  using Part = PartOf<D, ROWS>;
+  __shared__ int s_count[kJoinThreads / 32], s_run[kMaxCtas];
+  pdl_wait();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = a.g;
+  const Join* const joins = joins_of<D, ROWS>(a);
+  const int items = list_joins(joins, ctas, s_run, s_count);
+  for (int work = blockIdx.x; work < items * chunks; work += gridDim.x) {
+    const Join x = joins[s_run[work / chunks]];
+    const int qtiles = (x.n * g + ROWS - 1) / ROWS;
+    const int row0 = (x.item % qtiles) * ROWS, rows = min(ROWS, x.n * g - row0);
+    const int chunk = work % chunks, r = chunk / (D / 32) * 32 + lane, c = chunk % (D / 32) * 32 + warp * 4;
+    if (r >= rows) continue;
+    const Part* parts = parts_of<D, ROWS>(a);
+    const int n = x.last - x.first + 1;
+    auto part = [&](int k) { return parts + 2 * (x.first + k) + (k ? 0 : x.slot); };
+    float m = -INFINITY, l = 0.f;
+    for (int k0 = 0; k0 < n; k0 += 8) {
+      float y[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) y[i] = k0 + i < n ? part(k0 + i)->ml[r].x : -INFINITY;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) m = fmaxf(m, y[i]);
+    }
+    const float ref = m == -INFINITY ? 0.f : m;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k0 = 0; k0 < n; k0 += 8) {
+      float4 v[8];
+      float2 ml[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if (k0 + i >= n) continue;
+        ml[i] = part(k0 + i)->ml[r];
+        v[i] = *reinterpret_cast<const float4*>(&part(k0 + i)->o[Part::by_four(r, c)]);
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if (k0 + i >= n) continue;
+        const float w = fast_exp2(ml[i].x - ref);
+        l += ml[i].y * w;
+        o.x += v[i].x * w;
+        o.y += v[i].y * w;
+        o.z += v[i].z * w;
+        o.w += v[i].w * w;
+      }
+    }
+    const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+    const Group grp(a);
+    const int node = grp.node(row0 + r), head = x.item / qtiles * g + grp.place(row0 + r, node);
+    const size_t row = ((size_t)x.j * a.N + node) * a.nq + head;
+    *reinterpret_cast<uint2*>(a.out + row * D + c) = make_uint2(pack2<T>(o.x * inv, o.y * inv), pack2<T>(o.z * inv, o.w * inv));
+    if (a.lse && c == 0) a.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * (1.f / kLog2e);
+  }
+}
+
+// fn: the joining kernel, whose items have `chunks` chunks.
+cudaError_t launch_join(const void* fn, TreeAttnArgs& a, int ctas, int chunks, cudaStream_t st) {
   int64_t grid = (int64_t)(ctas - 1) * chunks;  // an item has its second run's record: at most so many
   if (grid < 1) return cudaSuccess;             // one run: nothing is split
   if (grid > 4 * num_sms()) grid = 4 * num_sms();
   void* args[] = {&a, &ctas, &chunks};
-  return launch_k((const void*)tree_join_kernel<T, D, ROWS, JR>, dim3((unsigned)grid), dim3(kJoinThreads), 0, st, true, args);
+  return launch_k(fn, dim3((unsigned)grid), dim3(kJoinThreads), 0, st, true, args);
 }
 
 template <typename T, int D, int RW>
@@ -690,7 +760,9 @@ cudaError_t launch(const TreeAttnArgs& a0, cudaStream_t st) {
   void* args[] = {&a};
   e = launch_k(fn, dim3(ctas), dim3(S::THREADS), S::SMEM, st, true, args);
   if (e != cudaSuccess) return e;
-  return launch_join<T, D, S::ROWS>(a, ctas, st);
+  constexpr int JR = S::ROWS <= 16 ? 2 : 4;
+  const int rows = a.N * a.g < S::ROWS ? a.N * a.g : S::ROWS;
+  return launch_join((const void*)tree_join_kernel<T, D, S::ROWS, JR>, a, ctas, (rows + JR - 1) / JR, st);
 }
 
 // ---------------------------------------------------------------------------
@@ -1042,12 +1114,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const float sl2 = a.scale * kLog2e;
     const int W = (a.N + 31) / 32;
     uint32_t x0 = 0, item = 0, ns = 0;
-    do {
+    for (;;) {
       const int rows = min(S::ROWS, it.s.n * g - it.row0);
       const bool there = rt < rows, some = rt - lane < rows;
       const int node = there ? grp.node(it.row0 + rt) : 0, hh = there ? grp.place(it.row0 + rt, node) : 0;
       {  // Q of the stream's rows
-        if (item) copy_q();
         cp_async_wait<0>();
         fence_proxy_async_shared();
         __syncwarp();
@@ -1168,6 +1239,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       // ---------------- the item's rows ----------------
       wait(&sh.o_done, item);
       tc_fence_after();
+      const Item at = it;
+      const bool more = leave();
+      if (more) copy_q();  // the next one's Q: no product reads this one's any more
       float mt = mref * sl2, lt = lsum, w[2] = {1.f, 1.f};  // m in log2 units; weights of the streams' O
       if (mref == -INFINITY) mt = -INFINITY;
       if (PAR) sh.ml[m][lr] = make_float2(mt, lt);
@@ -1181,10 +1255,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         lt = m ? o.y * theirs + lt * mine : lt * mine + o.y * theirs;  // the same sum in both streams
         mt = top;
       }
-      const bool whole = it.t0 == 0 && it.t1 == it.s.tiles;
+      const bool whole = at.t0 == 0 && at.t1 == at.s.tiles;
       if (some) {
-        const float keep = !whole ? 1.f : lt > 0.f || lt != lt ? 1.f / lt : 0.f;
-        const size_t row = ((size_t)it.j * a.N + node) * a.nq + it.head * g + hh;
+        const float inv = lt > 0.f || lt != lt ? 1.f / lt : 0.f;
+        const size_t row = ((size_t)at.j * a.N + node) * a.nq + at.head * g + hh;
         Part* part = parts_of<D, S::ROWS>(a) + (size_t)blockIdx.x * 2 + (item ? 1 : 0);
         constexpr int COLS = PAR ? D / 2 : D;  // of this thread
 #pragma unroll 1
@@ -1207,9 +1281,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           }
           for (int k = 0; k < W; ++k) {
             uint32_t z = there ? odd[k] : 0u;
-            if (z) z &= node_bits(a, it.j, node, k);
+            if (z) z &= node_bits(a, at.j, node, k);
             for (; z; z &= z - 1) {
-              const uint16_t* v = a.vt + it.j * a.t_seq + (k * 32 + __ffs(z) - 1) * a.t_tok + it.head * D + c0;
+              const uint16_t* v = a.vt + at.j * a.t_seq + (k * 32 + __ffs(z) - 1) * a.t_tok + at.head * D + c0;
 #pragma unroll
               for (int e = 0; e < 32; ++e) {
                 const uint16_t y = v[e];
@@ -1217,26 +1291,19 @@ __global__ void __launch_bounds__(kTcThreads, 1)
               }
             }
           }
-          // 32 rows x 32 columns change hands through this warp's share of Q's
-          // room, so that a store covers whole lines of few rows
-          float4* const box = reinterpret_cast<float4*>(sQ + m * TILE) + (warp & 3) * 256;
+          if (there && whole) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e)
-            box[lane * 8 + (e ^ (lane & 7))] =
-                make_float4(o[4 * e] * keep, o[4 * e + 1] * keep, o[4 * e + 2] * keep, o[4 * e + 3] * keep);
-          __syncwarp();
+            for (int e = 0; e < 32; ++e) o[e] *= inv;
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const int r = e * 4 + (lane >> 3), q = lane & 7, qr = rt - lane + r;
-            const float4 y = box[r * 8 + (q ^ (r & 7))];
-            if (qr >= rows) continue;
-            if (whole) {
-              const int nd = grp.node(it.row0 + qr), hd = it.head * g + grp.place(it.row0 + qr, nd);
-              *reinterpret_cast<uint2*>(a.out + (((size_t)it.j * a.N + nd) * a.nq + hd) * D + c0 + 4 * q) =
-                  make_uint2(pack2<T>(y.x, y.y), pack2<T>(y.z, y.w));
-            } else {
-              *reinterpret_cast<float4*>(&part->o[qr][c0 + 4 * q]) = y;
-            }
+            for (int e = 0; e < 4; ++e)
+              *reinterpret_cast<uint4*>(a.out + row * D + c0 + 8 * e) =
+                  make_uint4(pack2<T>(o[8 * e], o[8 * e + 1]), pack2<T>(o[8 * e + 2], o[8 * e + 3]),
+                             pack2<T>(o[8 * e + 4], o[8 * e + 5]), pack2<T>(o[8 * e + 6], o[8 * e + 7]));
+          } else if (there) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              *reinterpret_cast<float4*>(&part->o[Part::by_four(rt, c0 + 4 * e)]) =
+                  make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
           }
           __syncwarp();
         }
@@ -1250,7 +1317,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       rows_sync();  // O is read, the statistics too
       x0 += 2 * (uint32_t)tiles;
       ++item;
-    } while (leave());
+      if (!more) break;
+    }
   }
   tc_fence_before();
   __syncthreads();
@@ -1291,7 +1359,8 @@ cudaError_t launch_tc(const TreeAttnArgs& a0, cudaStream_t st) {
   void* args[] = {&maps[0], &maps[1], &maps[2], &maps[3], &a};
   e = launch_k(fn, dim3(ctas), dim3(kTcThreads), S::SMEM, st, true, args);
   if (e != cudaSuccess) return e;
-  return launch_join<T, D, S::ROWS>(a, ctas, st);
+  const int rows = a.N * a.g < S::ROWS ? a.N * a.g : S::ROWS;
+  return launch_join((const void*)tree_join_cols_kernel<T, D, S::ROWS>, a, ctas, (rows + 31) / 32 * (D / 32), st);
 }
 
 // Query tiles of more than kWarpRows rows go to the tensor cores' own memory.
@@ -1300,11 +1369,13 @@ cudaError_t launch_tc(const TreeAttnArgs& a0, cudaStream_t st) {
 // 64 rows 24 / 25, 32 rows 19 / 24; 64 of 500, 64 rows 85 / 64.)
 constexpr int kWarpRows = 32;
 
-// The tensor maps want the tree's strides to grow: what a cut out of larger
-// tensors has, but not every order of dimensions.
+// Tensor maps take strides below 2^40 bytes; that they grow with the dimension is
+// what a cut out of larger tensors has, but not every order of dimensions, and
+// other orders (or a repeated token's 0) are left to the warp-level form.
 bool maps_fit(const TreeAttnArgs& a) {
-  const int64_t tok = (int64_t)a.nkv * a.d;
-  return (a.N == 1 || a.t_tok >= tok) && (a.b == 1 || a.t_seq >= (a.N > 1 ? a.t_tok : tok));
+  const int64_t tok = (int64_t)a.nkv * a.d, most = (int64_t)1 << 39;
+  return (a.N == 1 || (a.t_tok >= tok && a.t_tok < most)) &&
+         (a.b == 1 || (a.t_seq >= (a.N > 1 ? a.t_tok : tok) && a.t_seq < most));
 }
 
 template <typename T, int D>

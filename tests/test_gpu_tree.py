@@ -222,6 +222,43 @@ def test_attention_over_long_runs(dtype, b, N, nq, nkv, d, cap):
     assert api.dflash_get_status() == 0
 
 
+@pytest.mark.parametrize("dtype,N,nq,nkv,d,cap", [
+    ("f16", 9, 2, 1, 64, 100), ("bf16", 40, 4, 2, 128, 333), ("f16", 130, 2, 1, 64, 70), ("bf16", 200, 4, 1, 128, 260)])
+def test_attention_with_any_bits(dtype, N, nq, nkv, d, cap):
+    """Masks that are no tree's: nodes see later ones, not themselves, or bits of
+    nodes that are not there; and no log-sum-exp asked for."""
+    rng = np.random.default_rng(N + 1)
+    lens, nodes = [cap, 0, 65], np.array([N - 3, N, N // 2 + 1])
+    kv, q, kt, vt = _attention_case(rng, dtype, 3, N, nq, nkv, d, cap, lens, nodes, L=1)
+    sees = rng.random((3, N, N)) < 0.3
+    sees[1, 0] = False   # with no cached key either: nothing
+    sees[1, 1] = False
+    sees[1, 1, N - 1] = True
+    mask = _i32(TO.pack_bits(sees))
+    out, lse = _attend(kv, 0, q, kt, vt, mask, _i32(nodes))
+    _check_attention(dtype, kv, 0, q, kt, vt, sees, lens, nodes, d ** -0.5, out, lse, 7.0)
+    alone = torch.full_like(out, 7.0)
+    api.dflash_tree_attention(q, kv, 0, kt, vt, mask, alone, n_nodes=_i32(nodes))
+    assert torch.equal(out, alone)
+
+
+@pytest.mark.parametrize("N,nq,nkv", [(5, 4, 2), (20, 8, 2), (70, 10, 2)])
+def test_attention_in_other_orders(N, nq, nkv):
+    """Trees kept node by node (a sequence's nodes apart), one sequence's keys
+    given to all, and one token's to all nodes."""
+    rng = np.random.default_rng(N + 2)
+    b, d, cap = 3, 64, 90
+    lens, nodes = [90, 31, 0], [N] * 3
+    kv, q, kt, vt = _attention_case(rng, "bf16", b, N, nq, nkv, d, cap, lens, nodes, L=1)
+    sees = np.stack([TO.tree_mask(p)[0] for p in _trees(rng, b, N)])
+    mask = _i32(TO.pack_bits(sees))
+    turned = lambda t: t.transpose(0, 1).contiguous().transpose(0, 1)
+    for kk, vv in ((turned(kt), turned(vt)), (kt[:1].expand(b, -1, -1, -1), vt[:1].expand(b, -1, -1, -1)),
+                   (kt[:, :1].expand(-1, N, -1, -1), vt[:, :1].expand(-1, N, -1, -1))):
+        out, lse = _attend(kv, 0, turned(q), kk, vv, mask, None)
+        _check_attention("bf16", kv, 0, q, kk, vv, sees, lens, nodes, d ** -0.5, out, lse, 7.0)
+
+
 @pytest.mark.parametrize("N", [6, 40, 128])
 def test_attention_values_that_a_node_does_not_see_do_not_matter(N):
     rng = np.random.default_rng(N)

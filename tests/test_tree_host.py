@@ -35,6 +35,7 @@ def test_adjust(lib):
         (EINVAL, dict(b=0)), (EINVAL, dict(R=0)), (EINVAL, dict(R=257)), (EINVAL, dict(V=0)), (EINVAL, dict(ld=99)),
         (EINVAL, dict(ld_out=99)), (EINVAL, dict(ld_out=101)), (EINVAL, dict(logits=ODD)), (EINVAL, dict(out=ODD)),
         (EUNSUPPORTED, dict(b=1 << 28)), (EUNSUPPORTED, dict(b=1 << 27)),
+        (EUNSUPPORTED, dict(b=1 << 20, V=1 << 25, ld=1 << 25, ld_out=1 << 25, n_allow=1 << 22, ld_allow=1 << 20)),
         (EUNSUPPORTED, dict(V=1 << 31, ld=1 << 31, ld_out=1 << 31, ld_allow=1 << 26)),
         (EINVAL, dict(n_hist=N)), (EINVAL, dict(H=0)), (EINVAL, dict(H=51)),
         (EUNSUPPORTED, dict(H=(1 << 20) - 256, ld_hist=1 << 20)), (EUNSUPPORTED, dict(ld_hist=1 << 62)),
