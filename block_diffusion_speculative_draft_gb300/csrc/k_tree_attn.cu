@@ -677,8 +677,8 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const TreeAttnA
 }
 
 // Parts by columns of four: 32 rows and 32 columns a chunk, a lane a row and a
-// warp four columns.
-template <typename T, int D, int ROWS>
+// warp four columns, BATCH parts in flight.
+template <typename T, int D, int ROWS, int BATCH>
 __global__ void __launch_bounds__(kJoinThreads) tree_join_cols_kernel(const TreeAttnArgs a, int ctas, int chunks) {
   using Part = PartOf<D, ROWS>;
   __shared__ int s_count[kJoinThreads / 32], s_run[kMaxCtas];
@@ -696,26 +696,25 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_cols_kernel(const Tree
     const int n = x.last - x.first + 1;
     auto part = [&](int k) { return parts + 2 * (x.first + k) + (k ? 0 : x.slot); };
     float m = -INFINITY, l = 0.f;
-    for (int k0 = 0; k0 < n; k0 += 8) {
-      float y[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) y[i] = k0 + i < n ? part(k0 + i)->ml[r].x : -INFINITY;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) m = fmaxf(m, y[i]);
-    }
-    const float ref = m == -INFINITY ? 0.f : m;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int k0 = 0; k0 < n; k0 += 8) {
-      float4 v[8];
-      float2 ml[8];
+    for (int k0 = 0; k0 < n; k0 += BATCH) {  // (the maximum runs along)
+      float4 v[BATCH];
+      float2 ml[BATCH];
+      float top = m;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        if (k0 + i >= n) continue;
-        ml[i] = part(k0 + i)->ml[r];
-        v[i] = *reinterpret_cast<const float4*>(&part(k0 + i)->o[Part::by_four(r, c)]);
+      for (int i = 0; i < BATCH; ++i) {
+        ml[i] = k0 + i < n ? part(k0 + i)->ml[r] : make_float2(-INFINITY, 0.f);
+        v[i] = k0 + i < n ? *reinterpret_cast<const float4*>(&part(k0 + i)->o[Part::by_four(r, c)])
+                          : make_float4(0.f, 0.f, 0.f, 0.f);
       }
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
+      for (int i = 0; i < BATCH; ++i) top = fmaxf(top, ml[i].x);
+      const float ref = top == -INFINITY ? 0.f : top, old = fast_exp2(m - ref);
+      m = top;
+      l *= old;
+      o = make_float4(o.x * old, o.y * old, o.z * old, o.w * old);
+#pragma unroll
+      for (int i = 0; i < BATCH; ++i) {
         if (k0 + i >= n) continue;
         const float w = fast_exp2(ml[i].x - ref);
         l += ml[i].y * w;
@@ -1360,7 +1359,14 @@ cudaError_t launch_tc(const TreeAttnArgs& a0, cudaStream_t st) {
   e = launch_k(fn, dim3(ctas), dim3(kTcThreads), S::SMEM, st, true, args);
   if (e != cudaSuccess) return e;
   const int rows = a.N * a.g < S::ROWS ? a.N * a.g : S::ROWS;
-  return launch_join((const void*)tree_join_cols_kernel<T, D, S::ROWS>, a, ctas, (rows + 31) / 32 * (D / 32), st);
+  // Items of many parts wait for loads: 16 in flight (39 rows of 3 x 2999 keys, 25
+  // runs an item, 11.7 us in place of 13.7); of few parts or many rows, for the
+  // CTAs that so many registers keep out (8 x 32 nodes over 4096 keys, 52.7 us in
+  // place of 44.9).
+  const bool many = PAR && items * 8 < ctas;
+  const void* join = many ? (const void*)tree_join_cols_kernel<T, D, S::ROWS, 16>
+                          : (const void*)tree_join_cols_kernel<T, D, S::ROWS, 8>;
+  return launch_join(join, a, ctas, (rows + 31) / 32 * (D / 32), st);
 }
 
 // Query tiles of more than kWarpRows rows go to the tensor cores' own memory.
