@@ -794,14 +794,17 @@ struct TcShape {
   }
   static constexpr int TILE = kTcKeys * D * 2;
   static constexpr int HALF = kTcKeys * 128;  // bytes of 64 columns of a tile
-  static constexpr int SLOTS = D == 128 ? 5 : 8;
+  static constexpr int QTILES = PAR ? 1 : 2;  // the streams' own rows of Q, or the same
+  // as many tiles in flight as fit: with 5 in place of 6, 64 sequences of 2000 keys
+  // and 32 rows took 118 us in place of 99
+  static constexpr int SLOTS = D == 64 ? 12 : PAR ? 6 : 5;
   static constexpr int CTRL = 2 * 128 * 8 + 512;  // row statistics, then barriers and small change
-  static constexpr int SMEM = 2 * TILE + SLOTS * TILE + CTRL;
+  static constexpr int SMEM = (QTILES + SLOTS) * TILE + CTRL;
 };
 
 struct TcCtrl {
   float2 ml[2][128];
-  uint64_t full[8], empty[8], s_ready[2][2], p_ready[2][2], pv_done[2], q_ready[2], o_done;
+  uint64_t full[12], empty[12], s_ready[2][2], p_ready[2][2], pv_done[2], q_ready[2], o_done;
   uint32_t odd[2][kTreeMax / 32];
   uint32_t tmem;
 };
@@ -905,8 +908,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   using Part = PartOf<D, S::ROWS>;
   constexpr int TILE = S::TILE, HALF = S::HALF, SLOTS = S::SLOTS, CH = D / 8;
   extern __shared__ __align__(1024) uint8_t smem[];
-  uint8_t* const sQ = smem;              // [2 streams][D / 64][128 rows][128 bytes]
-  uint8_t* const sKV = smem + 2 * TILE;  // the ring
+  uint8_t* const sQ = smem;                      // [QTILES][D / 64][128 rows][128 bytes]
+  uint8_t* const sKV = smem + S::QTILES * TILE;  // the ring
   TcCtrl& sh = *reinterpret_cast<TcCtrl*>(sKV + SLOTS * TILE);
 
   pdl_wait();
@@ -954,17 +957,16 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   // Keys of tile t (of the run's item; 128 or more: all), and its halves that hold any.
   auto keys_of = [&](int t) { return t < it.ctx ? it.s.len - t * kTcKeys : it.s.n - (t - it.ctx) * kTcKeys; };
   auto halves_of = [&](int t) { return keys_of(t) > kTcStep ? 2 : 1; };
-  // Q of the stream's rows (zero where there is none), a row by neighbouring threads
+  // Q of the tile's rows (zero where there is none), a row by neighbouring threads
   auto copy_q = [&]() {
-    const int m = warp >> 2, lr = (warp & 3) * 32 + lane;
     const int rows = min(S::ROWS, it.s.n * g - it.row0);
     const uint16_t* q = a.q + it.j * a.q_seq + it.head * g * D;
 #pragma unroll 4
-    for (int i = 0; i < CH; ++i) {
-      const int r = i * (128 / CH) + lr / CH, c = lr % CH, qr = PAR ? r : m * 128 + r;
-      const bool ok = qr < rows;
-      const int nd = ok ? grp.node(it.row0 + qr) : 0, hd = ok ? grp.place(it.row0 + qr, nd) : 0;
-      cp_async16(sQ + m * TILE + tile_off(r, c, 128), q + nd * a.q_tok + hd * D + c * 8, ok);
+    for (int i = 0; i < S::ROWS * CH / 256; ++i) {
+      const int x = i * 256 + tid, r = x / CH, c = x % CH;
+      const bool ok = r < rows;
+      const int nd = ok ? grp.node(it.row0 + r) : 0, hd = ok ? grp.place(it.row0 + r, nd) : 0;
+      cp_async16(sQ + (r >> 7) * TILE + tile_off(r & 127, c, 128), q + nd * a.q_tok + hd * D + c * 8, ok);
     }
     cp_async_commit();
   };
@@ -983,7 +985,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         mbar_init(&sh.p_ready[m][i], 4);
       }
       mbar_init(&sh.pv_done[m], 1);
-      mbar_init(&sh.q_ready[m], 4);
+      mbar_init(&sh.q_ready[m], 8);
     }
     mbar_init(&sh.o_done, 2);
     fence_mbar_init();
@@ -1052,7 +1054,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     constexpr uint32_t idesc_o = (__is_same(T, __half) ? tc_idesc_f16(D) : tc_idesc_bf16(128, D)) | (1u << 16);
     constexpr uint32_t kHalfTile = kTcStep * 128;  // bytes from a half's rows to the other's
     const uint32_t kv_at = smem_u32(sKV), s_at = tmem + kS + 128 * m, o_at = tmem + D * m;
-    const uint64_t qd = tc_sdesc_sw128(smem_u32(sQ) + m * TILE);
+    const uint64_t qd = tc_sdesc_sw128(smem_u32(sQ) + (PAR ? 0 : m * TILE));
     uint32_t x0 = 0;  // K and V tiles before the item
     uint32_t item = 0, ns = 0, np = 0;  // items, halves sent for and added so far
     do {
@@ -1121,7 +1123,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         cp_async_wait<0>();
         fence_proxy_async_shared();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.q_ready[m]);
+        if (lane < 2) mbar_arrive(&sh.q_ready[lane]);  // (its copies are of rows of either stream)
       }
       float mref = -INFINITY, lsum = 0.f;  // reference maximum (raw scores) and sum of the row
       const int tiles = it.t1 - it.t0;
@@ -1370,10 +1372,11 @@ cudaError_t launch_tc(const TreeAttnArgs& a0, cudaStream_t st) {
 }
 
 // Query tiles of more than kWarpRows rows go to the tensor cores' own memory.
-// (Device time, us, warp-level / tensor-memory form: 8 sequences of 4096 keys,
-// 64 rows 61 / 45, 32 rows 48 / 43, 16 rows 37 / 41, 4 rows 32 / 40; one of 8192,
-// 64 rows 24 / 25, 32 rows 19 / 24; 64 of 500, 64 rows 85 / 64.)
-constexpr int kWarpRows = 32;
+// (Device time, us, warp-level / tensor-memory form, one kv head's rows: 64
+// sequences of 2000 keys, 4 rows 93 / 115, 16 rows 107 / 116, 32 rows 150 / 118; 8
+// of 4096, 4 rows 32 / 39, 16 rows 36 / 39, 32 rows 47 / 39; one of 8192, 16 rows
+// 16.8 / 17.2, 32 rows 18.7 / 17.2.)
+constexpr int kWarpRows = 16;
 
 // Tensor maps take strides below 2^40 bytes; that they grow with the dimension is
 // what a cut out of larger tensors has, but not every order of dimensions, and
@@ -1401,7 +1404,7 @@ cudaError_t launch_type(const TreeAttnArgs& a, cudaStream_t st) {
 size_t tree_attn_ws_bytes(int64_t b, int N, int nq, int nkv, int d) {
   (void)b;
   const int rows = N * (nq / nkv);
-  const int tile = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 128 ? 128 : 256;
+  const int tile = rows <= 16 ? 16 : rows <= 128 ? 128 : 256;
   return (size_t)kMaxCtas * (2 * (size_t)tile * (d + 2) * 4 + sizeof(Join)) + 32;
 }
 

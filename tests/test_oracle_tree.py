@@ -138,10 +138,11 @@ def _ring(seed, slots, release_first, tiles=40):
     return "done"
 
 
-@pytest.mark.parametrize("slots", [5, 8])
+@pytest.mark.parametrize("slots", [5, 6, 12])
 def test_two_streams_share_a_ring(slots):
     assert all(_ring(seed, slots, True) == "done" for seed in range(150))
 
 
-def test_a_ring_of_five_needs_the_release():
-    assert "early" in {_ring(seed, 5, False) for seed in range(30)}
+@pytest.mark.parametrize("slots", [5, 6])
+def test_a_ring_whose_slots_change_hands_needs_the_release(slots):
+    assert "early" in {_ring(seed, slots, False) for seed in range(30)}
