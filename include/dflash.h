@@ -524,8 +524,8 @@ DFLASH_API int32_t dflash_adjust_logits(const void* logits, int32_t dtype, int64
  * to the calls below:
  *  - A sequence's tree has up to N nodes, 1 <= N <= 256, of which it uses the
  *    first n_nodes[j] (nullable: all N; 0 <= n_nodes <= N, else it has none and
- *    DFLASH_DEV_BAD_LENGTH is set).  What belongs to other nodes is neither read
- *    nor, in outputs, written, unless a call says so.
+ *    DFLASH_DEV_BAD_LENGTH is set).  What belongs to other nodes does not matter,
+ *    whatever its bits, and is not written in outputs, unless a call says so.
  *  - parent: [b][N] int32, parent[i] in [-1, i), -1 for a root.  Node 0 is where
  *    the walk begins: the last emitted token, whose keys and values are not in
  *    the cache yet (as slot 0 of a draft block).
