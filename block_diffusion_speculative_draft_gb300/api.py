@@ -876,10 +876,14 @@ class KVCache:
         dtype = torch.float16 if dtype is None else dtype
         if dtype not in (torch.float16, torch.bfloat16):
             raise ValueError("KVCache: dtype must be float16 or bfloat16")
+        device = torch.device(device)
+        if device.type == "cuda" and device.index is None:
+            device = torch.device("cuda", torch.cuda.current_device())
+        # calls look at k's device alone: the others have to share it
         for name, t, dt, want in (("k", k, dtype, shape), ("v", v, dtype, shape), ("len", len, torch.int32, (b,))):
             if t is not None and (t.dtype != dt or t.shape != want or not t.is_contiguous() or not t.is_cuda
-                                  or (k is not None and t.device != k.device)):
-                raise ValueError(f"KVCache: {name} must be a contiguous {dt} CUDA tensor of shape {tuple(want)}")
+                                  or t.device != device):
+                raise ValueError(f"KVCache: {name} must be a contiguous {dt} CUDA tensor of shape {tuple(want)} on {device}")
         self.k = torch.zeros(shape, dtype=dtype, device=device) if k is None else k
         self.v = torch.zeros(shape, dtype=dtype, device=device) if v is None else v
         self.len = torch.zeros(b, dtype=torch.int32, device=self.k.device) if len is None else len
