@@ -22,6 +22,7 @@
 #include "kernels.h"
 #include "ptx.cuh"
 #include "rows.cuh"
+#include "runs.h"
 #include "tcgen05.cuh"
 
 namespace dfl {
@@ -61,17 +62,6 @@ __device__ __forceinline__ uint32_t node_bits(const TreeAttnArgs& a, int j, int 
   const int own = node - w * 32;  // the last node it sees, in this word
   return own < 0 ? 0u : own >= 31 ? ~0u : (2u << own) - 1u;
 }
-
-// Runs: tiles [c all / runs, (c + 1) all / runs) of all items' tiles belong to
-// CTA c < runs; tile u to run ((u + 1) runs - 1) / all.
-struct Runs {
-  long long all, runs;
-  __device__ __forceinline__ long long start(long long c) const { return ratio(c * all, runs); }
-  __device__ __forceinline__ long long of(long long u) const { return ratio((u + 1) * runs - 1, all); }
-  static __device__ __forceinline__ long long ratio(long long x, long long y) {  // (64-bit division is slow)
-    return x >> 32 ? x / y : (long long)((uint32_t)x / (uint32_t)y);
-  }
-};
 
 // A CTA's run: the tiles [u0, u1), and the sequence that holds u0 (base tiles
 // come before it).  Every warp finds it by itself, so without a barrier; up to
