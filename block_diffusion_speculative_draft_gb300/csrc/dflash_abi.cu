@@ -719,8 +719,6 @@ static int check_tree_heads(int32_t b, int32_t N, int32_t nq, int32_t nkv, int32
   if (nq < 1 || nkv < 1) return DFLASH_EINVAL;
   if ((d != 64 && d != 128) || nq % nkv || nq / nkv > kTreeMaxGroup || (int64_t)nq * d > 1 << 24 || (int64_t)nkv * b > 1 << 22)
     return DFLASH_EUNSUPPORTED;
-  // CTAs of the launch that joins parts: 16 query rows of a kv head each
-  if ((int64_t)b * nkv * (((int64_t)N * (nq / nkv) + 63) / 64) * 4 > 0x7fffffffll) return DFLASH_EUNSUPPORTED;
   return DFLASH_OK;
 }
 

@@ -51,3 +51,12 @@ def test_ratio(runs):
     for x in (0, 1, 9, 2 ** 32 - 1, 2 ** 32, 2 ** 40 + 3, 2 ** 62):
         for y in (1, 2, 320, 2 ** 32 - 1, 2 ** 32, 2 ** 32 + 1, 2 ** 45):
             assert runs.ratio(x, y) == x // y, (x, y)
+
+
+@pytest.mark.parametrize("shape", [(4096, 256, 4096, 64, 64), (16384, 256, 65536, 256, 64), (4, 256, 1 << 18, 1 << 8, 64)])
+def test_no_size_is_refused_for_the_joins_sake(shape):
+    """The launch that joins parts has a grid of its own, whatever the rows."""
+    from block_diffusion_speculative_draft_gb300 import api
+    build.build()
+    b, N, nq, nkv, d = shape
+    assert api.dflash_tree_attention_workspace_size(*shape) == api.dflash_tree_attention_workspace_size(1, N, nq, nkv, d)
