@@ -396,16 +396,17 @@ def _on(dev, stream, fn, call, *args):
         raise DflashError(fn, rc)
 
 
-def _workspace(fn, ws, nbytes, dev, stream):
-    """(pointer, bytes, tensor) of the given workspace, or of a zero-filled one
-    in memory that the call's own stream may reuse (stream None: the current
-    one)."""
+def _workspace(fn, ws, nbytes, dev, stream, zero=True):
+    """(pointer, bytes, tensor) of the given workspace, or of one (zero-filled if
+    the call asks for that) in memory that the call's own stream may reuse (stream
+    None: the current one)."""
     torch = _torch()
     if ws is None:
         if nbytes == 0:
             return None, 0, None
         with torch.cuda.stream(stream):  # None: no change
-            ws = torch.zeros(nbytes, dtype=torch.uint8, device=torch.device("cuda", dev))
+            make = torch.zeros if zero else torch.empty
+            ws = make(nbytes, dtype=torch.uint8, device=torch.device("cuda", dev))
     elif ws.get_device() != dev or not ws.is_contiguous():
         raise ValueError(f"{fn}: ws must be contiguous and on cuda:{dev}")
     return ws.data_ptr(), ws.numel() * ws.element_size(), ws
@@ -666,7 +667,8 @@ def dflash_tree_attention(q, kv: "KVCache", layer: int, k_tree, v_tree, mask, ou
     lp = _one(fn, "lse_out", lse_out, dev, torch.float32, q.shape[:3])
     mp = _one(fn, "mask", mask, dev, torch.int32, (b, N, (N + 31) // 32))
     nn = _one(fn, "n_nodes", n_nodes, dev, torch.int32, q.shape[:1])
-    wp, wn, ws = _workspace(fn, ws, dflash_tree_attention_workspace_size(b, N, nq, nkv, d), dev, stream)
+    wp, wn, ws = _workspace(fn, ws, dflash_tree_attention_workspace_size(b, N, nq, nkv, d), dev, stream,
+                            zero=False)
     _on(dev, stream, fn, load_library().dflash_tree_attention, qp, qs, qt,
         DTYPE_F16 if dt == torch.float16 else DTYPE_BF16, ctypes.byref(kv.c), layer, N, nq, nkv, d, kp, vp, *ks, mp, nn,
         d ** -0.5 if scale is None else scale, op, lp, wp, wn)
