@@ -644,7 +644,8 @@ def dflash_tree_attention(q, kv: "KVCache", layer: int, k_tree, v_tree, mask, ou
                           scale: Optional[float] = None, ws=None, stream=None):
     """Attention of the nodes q [b][N][nq][d] (fp16/bf16, the cache's dtype) over
     layer `layer` of kv and the nodes' own k_tree, v_tree [b][N][nkv][d] (views of
-    one projection's output will do) as mask int32 [b][N][(N + 31) // 32] says
+    one projection's output will do; tokens of a sequence apart, or one given to
+    several by a stride of 0, are slow above 16 rows) as mask int32 [b][N][(N + 31) // 32] says
     (None: node i sees nodes 0..i).  out [b][N][nq][d]; lse_out fp32 [b][N][nq];
     scale: 1 / sqrt(d).  ws: uint8 workspace of
     dflash_tree_attention_workspace_size bytes (allocated here when not given)."""

@@ -24,7 +24,9 @@ namespace {
 
 constexpr int kDevBadLength = 0x4, kDevBadParam = 0x8;
 // 512 threads and 64 registers, two CTAs an SM: 144 us for 32 x 32 rows of 151936 bf16
-// with everything asked for and 31 us for 8 x 16 of fp32 (256 threads: 164 and 32).
+// with everything asked for and 31 us for 8 x 16 of fp32, the same rows again and
+// again (256 threads: 164 and 32); with rows that are not in L2, 144 and 35.  The
+// form without a grammar spills 20 to 116 bytes a thread for its packs in flight.
 constexpr int kThreads = 512;
 constexpr int kFlight = 4;  // packs a thread has in flight (twice as many without a grammar)
 constexpr int kScan = 8;    // tokens of the history

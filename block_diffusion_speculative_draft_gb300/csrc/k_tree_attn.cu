@@ -219,11 +219,12 @@ __device__ __forceinline__ bool not_finite(uint32_t pair) {
 // The warp-level form, for few rows a key: RW row warps of 16 query rows, KW
 // groups of warps that share out a tile's keys.  Each warp keeps its own running
 // maximum, sum and O over its keys; the groups are joined when the item or the
-// run ends.  Bound by HBM: 64 sequences of 2000 keys with one token each run at
-// 5.7 TB/s; small calls by their two launches (12 us at 1024 keys).
+// run ends.  Bound by HBM: 64 sequences of 2000 keys with one token each (32 / 8
+// heads) run at 5.6 TB/s; small calls by their two launches (12 us at 1024 keys).
 template <int D, int RW>
 struct Shape {
-  static constexpr int KW = RW == 1 ? 4 : 8 / RW;
+  static_assert(RW == 1 || RW == 2, "");
+  static constexpr int KW = 4;
   static constexpr int THREADS = RW * KW * 32;
   static constexpr int ROWS = RW * 16;  // of a query tile
   // cached keys and the tree's side by side
@@ -1362,10 +1363,17 @@ cudaError_t launch_tc(const TreeAttnArgs& a0, cudaStream_t st) {
 }
 
 // Query tiles of more than kWarpRows rows go to the tensor cores' own memory.
-// (Device time, us, warp-level / tensor-memory form, one kv head's rows: 64
-// sequences of 2000 keys, 4 rows 93 / 115, 16 rows 107 / 116, 32 rows 150 / 118; 8
-// of 4096, 4 rows 32 / 39, 16 rows 36 / 39, 32 rows 47 / 39; one of 8192, 16 rows
-// 16.8 / 17.2, 32 rows 18.7 / 17.2.)
+// Device time, us, warp-level / tensor-memory form, 8 kv heads, by rows of one:
+//                             4          8          16           32
+//   d 128, 64 x 2000 keys   94 / 96    98 / 96   107 / 97    150 / 99
+//           8 x 4096        33 / 35    33 / 35    36 / 35     47 / 36
+//           1 x 8192      17.2/17.4  17.3/17.3  17.7/17.4   19.3/17.2
+//   d  64, 64 x 2000        63 / 79               71 / 79     89 / 79
+//           1 x 8192                            14.3/14.6
+// Sixteen rows are one of the warp-level form's tiles, 17 and more two: it wins
+// at 64 dimensions up to there, and at 128 up to 8 rows; from 9 to 16 rows of 128
+// the tensor-memory form would be up to a tenth faster, for a workspace of eight
+// times the size.
 constexpr int kWarpRows = 16;
 
 // Tensor maps take strides below 2^40 bytes; that they grow with the dimension is
